@@ -340,6 +340,191 @@ int w4a16_swa_attention(const void *q, const void *k_cache, const void *vt_cache
 /* Workspace bytes of w4a16_swa_attention for these sizes (0 for invalid ones). */
 size_t w4a16_swa_workspace_bytes(int nq, int Hq, int Hkv, int head_dim, int L, int window, int block);
 
+/*
+ * Paged serving: the operators of one batched model step around the linear
+ * layers -- the cache's bookkeeping, its writes, the attention over it, and
+ * the choice of the next tokens.  The pages describe serving of one request
+ * (the 16-token draft block verified by one forward of the target); the
+ * interface below is this library's.
+ *
+ * The cache is two arrays of pages, keys and values, addressed as
+ * [page][head][slot][head_dim] with strides of its own in each of the first
+ * three (in elements; head_dim is contiguous), so that head-major and
+ * token-major pages, and key and value pages interleaved in one array, are all
+ * expressible.  page_size (slots of a page) is a power of two, 8 .. 256.
+ * Request b's position j is in slot j % page_size of page
+ * block_table[b][j / page_size]; slot number = page * page_size + slot, below
+ * 2^31.  A table entry outside [0, num_pages) stands for a page that is not
+ * there.
+ *
+ * Lengths live on the GPU (int32), so that a step can be captured once and
+ * replayed with other lengths.  Argument structs are read during the call
+ * only.  flags: 0 or W4A16_FLAG_PDL.  Errors: W4A16_EINVAL for a null pointer,
+ * a bad size, stride or flag, W4A16_EALIGN for a misaligned pointer or stride,
+ * W4A16_EUNSUPPORTED for a type, head width or size outside the stated set,
+ * W4A16_EWORKSPACE for a missing or short workspace.
+ */
+typedef enum { W4A16_BF16 = 0, W4A16_F16 = 1, W4A16_F32 = 2 } w4a16_dtype;
+
+/*
+ * Block tables, slot map and positions of a step, from the requests' lengths:
+ *
+ *     held_b = ceil(past_len[b] / page_size),  need_b = ceil((past_len[b] + new_len[b]) / page_size)
+ *     first_b = sum_{a < b} (need_a - held_a)
+ *     block_table[b][c] = unchanged                       c < held_b
+ *                         free_pages[first_b + c - held_b] held_b <= c < need_b (-1 past the end of free_pages)
+ *                         -1                              need_b <= c < columns
+ *     q_start[b] = sum_{a < b} new_len[a], q_start[requests] the number of new tokens
+ *     kv_len[b] = past_len[b] + new_len[b]
+ *     for new token t = q_start[b] + i:  positions[t] = past_len[b] + i,
+ *         slot_map[t] = page * page_size + positions[t] % page_size,  -1 where the page is not there
+ *     for q_start[requests] <= t < tokens: positions[t] = slot_map[t] = -1
+ *     pages_used[0] = first_requests (the free pages taken; more than num_free if they did not suffice)
+ *
+ * A negative length counts as 0; positions past the table's last column have
+ * no page.  requests <= 16384 (W4A16_EUNSUPPORTED); all arrays int32, 4-byte
+ * aligned, none overlapping another.  One launch.
+ */
+typedef struct {
+    const int32_t *past_len;   /* [requests] tokens in the cache */
+    const int32_t *new_len;    /* [requests] tokens of this step */
+    const int32_t *free_pages; /* [num_free], may be NULL when num_free is 0 */
+    int32_t *block_table;      /* [requests][columns], rows table_stride apart */
+    int32_t *q_start;          /* [requests + 1] */
+    int32_t *kv_len;           /* [requests] */
+    int32_t *positions;        /* [tokens] */
+    int32_t *slot_map;         /* [tokens] */
+    int32_t *pages_used;       /* [1] */
+    int64_t table_stride;
+    int32_t requests, num_free, columns, tokens, page_size;
+    uint32_t flags;
+} w4a16_page_plan_args;
+int w4a16_page_plan(const w4a16_page_plan_args *args, w4a16_stream_t stream);
+
+/*
+ * New keys and values into the cache: for every token t with
+ * 0 <= slot_map[t] < num_pages * page_size and every head h,
+ *
+ *     k_cache[slot / page_size][h][slot % page_size] = k[t][h],  v alike.
+ *
+ * Other tokens (padding) are skipped.  Two tokens of one call must not name
+ * one slot.  16-bit elements (dtype bf16 or fp16, copied bit for bit);
+ * head_dim a multiple of 8; all pointers 16-byte aligned, all strides
+ * multiples of 8 elements.  The cache must not overlap k, v or slot_map.
+ */
+typedef struct {
+    const void *k, *v;        /* [tokens][heads][head_dim] */
+    const int32_t *slot_map;  /* [tokens] */
+    void *k_cache, *v_cache;
+    int64_t k_token, k_head, v_token, v_head;                     /* strides, elements */
+    int64_t kc_page, kc_head, kc_slot, vc_page, vc_head, vc_slot; /* strides, elements */
+    int32_t tokens, heads, head_dim, num_pages, page_size, dtype;
+    uint32_t flags;
+    int32_t reserved;         /* 0 */
+} w4a16_kv_write_args;
+int w4a16_kv_write(const w4a16_kv_write_args *args, w4a16_stream_t stream);
+
+/*
+ * Attention of every request's new tokens over its paged cache.  Request b has
+ * the n_b = q_start[b+1] - q_start[b] query tokens t = q_start[b] + i, and
+ * L_b = kv_len[b] positions in the cache (the new tokens' own among them).
+ * For query head h, key head hk = h / (q_heads / kv_heads):
+ *
+ *     e_i = L_b - n_b + i (block = 0, causal)  or  L_b - 1 (block = 1)
+ *     J_i = { j : max(0, e_i - window + 1) <= j <= e_i, j's page is there }   (window = 0: no lower bound)
+ *     out[t][h] = sum_{j in J_i} softmax_j(scale q[t][h] . k[j][hk]) v[j][hk]
+ *     lse[t][h] = log sum_{j in J_i} exp(scale q[t][h] . k[j][hk])
+ *
+ * One token a request (decode), a draft block, a chunk of a prompt, and any
+ * mixture of them in one call.  Scores, softmax and sums are f32; the softmax
+ * weights are rounded once to the inputs' type for the product with v.  A
+ * token that sees no position (J_i empty, or all its scores -inf) gets out = 0
+ * and lse = -inf.  What lies outside J_i has no effect on out[t], NaN and
+ * infinities included.  Rows t >= q_start[requests] are not written.
+ *
+ *   dtype       bf16 or fp16, one for q, k, v and out
+ *   head_dim    64 or 128;  q_heads % kv_heads == 0, q_heads / kv_heads <= 64
+ *   max_q       at least every n_b (a tighter bound gives a better grid): the
+ *               result is undefined for a request with more new tokens
+ *   strides     elements, multiples of 8; pointers 16-byte aligned (lse and
+ *               the int32 arrays 4-byte)
+ *   lse         may be NULL
+ *   kv_len[b]   counted as at most columns * page_size
+ *   workspace   w4a16_paged_attention_workspace_bytes bytes, 16-byte aligned,
+ *               zero-filled once before its first use (its first 64 KB hold
+ *               arrival counters that every call leaves at zero: the GEMM's
+ *               workspace rules apply, and one buffer serves both)
+ * out and lse must not overlap the inputs.
+ */
+typedef struct {
+    const void *q;              /* [tokens][q_heads][head_dim] */
+    const void *k_cache, *v_cache;
+    const int32_t *block_table; /* [requests][columns], rows table_stride apart */
+    const int32_t *q_start;     /* [requests + 1], not decreasing, from 0 */
+    const int32_t *kv_len;      /* [requests] */
+    void *out;                  /* [tokens][q_heads][head_dim] */
+    float *lse;                 /* [tokens][q_heads] dense, or NULL */
+    void *workspace;
+    uint64_t workspace_bytes;
+    int64_t q_token, q_head, out_token, out_head;                 /* strides, elements */
+    int64_t kc_page, kc_head, kc_slot, vc_page, vc_head, vc_slot; /* strides, elements */
+    int64_t table_stride;
+    int32_t tokens, requests, q_heads, kv_heads, head_dim, num_pages, page_size, columns;
+    int32_t max_q, window, block, dtype;
+    float scale;                /* of the scores; 0 stands for 1 / sqrt(head_dim) */
+    uint32_t flags;
+} w4a16_paged_attention_args;
+int w4a16_paged_attention(const w4a16_paged_attention_args *args, w4a16_stream_t stream);
+/* Workspace that any call with these sizes or fewer tokens and requests needs on the current device. */
+size_t w4a16_paged_attention_workspace_bytes(int tokens, int requests, int q_heads, int kv_heads, int head_dim,
+                                             int max_q);
+
+/*
+ * Sampling of one token a row from logits[rows][vocab], with random numbers
+ * that the caller gives.  With z_i = logits[r][i] / temperature[r] (one f32
+ * division) and the row's tokens in order of falling z, equal ones by rising
+ * index, three filters keep a beginning of that order each, and all three hold:
+ *
+ *     top_k   the first top_k[r] tokens (off: <= 0)
+ *     top_p   the tokens before which less than top_p[r] of the probability of
+ *             what top_k left has gone by (off: >= 1; the first token stays)
+ *     min_p   the tokens at least min_p[r] as probable as the first:
+ *             z_i - z_max >= log(min_p[r]) (off: <= 0; the first token stays)
+ *
+ *     token[r] = argmax over the kept tokens of z_i - log noise[r][i]   (ties: the lowest index)
+ *
+ * For noise drawn from the exponential distribution of rate 1 this is a draw
+ * with the kept tokens' renormalised probabilities (of independent exponential
+ * variables with rates p_i, variable i is the smallest with probability
+ * p_i / sum p).  temperature[r] <= 0 takes the most probable token (lowest
+ * index among equals) and reads no noise.
+ * logprob[r] = z_token - log sum_i exp(z_i) over the whole row, before the
+ * filters (temperature 1 where temperature[r] <= 0).  NaN logits count as
+ * -inf and are never taken, nor are -inf ones; a row without any other gives
+ * token -1 and logprob -inf.  All arithmetic is f32.
+ *
+ *   dtype        of the logits: bf16, fp16 or f32; noise, temperature, top_p,
+ *                min_p, logprob f32; top_k, token int32
+ *   temperature, top_k, top_p, min_p   [rows] or NULL (temperature 1; filter off)
+ *   noise        non-negative; rows noise_row elements apart (0: one row for all)
+ *   logprob      may be NULL
+ * Any alignment of the rows is accepted that the element type has.
+ */
+typedef struct {
+    const void *logits;   /* [rows][vocab], rows logits_row apart */
+    const float *noise;   /* [rows][vocab], rows noise_row apart */
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    int32_t *token;       /* [rows] */
+    float *logprob;       /* [rows] or NULL */
+    int64_t logits_row, noise_row;
+    int32_t rows, vocab, dtype;
+    uint32_t flags;
+} w4a16_sample_args;
+int w4a16_sample(const w4a16_sample_args *args, w4a16_stream_t stream);
+
 /* Number of kernel launches the library has issued in this process (every
  * entry point that launches counts its kernel; w4a16_gemm_noalloc's counter
  * memset is not a kernel launch). */

@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -84,6 +85,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                 ctypes.c_uint, vp]
             lib.w4a16_swa_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci, ci]
             lib.w4a16_swa_workspace_bytes.restype = sz
+            for name in ("w4a16_page_plan", "w4a16_kv_write", "w4a16_paged_attention", "w4a16_sample"):
+                getattr(lib, name).argtypes = [ctypes.c_char_p, vp]  # a packed argument struct, a stream
+            lib.w4a16_paged_attention_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci]
+            lib.w4a16_paged_attention_workspace_bytes.restype = sz
             _lib = lib
     return _lib
 
@@ -364,6 +369,207 @@ def w4a16_swa_attention(q: torch.Tensor, k_cache: torch.Tensor, vt_cache: torch.
                                  workspace.numel() * workspace.element_size(), flags, _stream(stream))
     _raise(st, "w4a16_swa_attention")
     return out
+
+
+# ---------------------------------------------------------------------------
+# serving: paged cache and sampling (see include/w4a16.h)
+# ---------------------------------------------------------------------------
+# The argument structs of the C ABI, packed by position (native sizes, no
+# padding: the fields are ordered by size).
+_PLAN_ARGS = struct.Struct("=9QqiiiiiI")
+_WRITE_ARGS = struct.Struct("=5Q10qiiiiiiIi")
+_ATTN_ARGS = struct.Struct("=9QQ11qiiiiiiiiiiiifI")
+_SAMPLE_ARGS = struct.Struct("=8QqqiiiI")
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _int32(t, name, n=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if n is not None and (t.dim() != 1 or t.shape[0] != n):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
+    return t
+
+
+def _block_table(t, requests):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2:
+        raise ValueError("block_table must be a 2-D int32 CUDA tensor")
+    if t.shape[0] != requests or (t.stride(1) != 1 and t.shape[1] > 1 and requests > 0):
+        raise ValueError(f"block_table must be [{requests}, columns] with contiguous rows")
+    return t
+
+
+def _strided(t, name, dtype, dims):
+    """A CUDA tensor of that many dimensions whose last one is contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be {dims}-D with a contiguous last dimension")
+    return t.shape
+
+
+def w4a16_page_plan(past_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
+                    block_table: torch.Tensor, page_size: int, q_start: torch.Tensor | None = None,
+                    kv_len: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                    slot_map: torch.Tensor | None = None, pages_used: torch.Tensor | None = None,
+                    max_tokens: int | None = None, stream=None, flags: int = FLAG_PDL):
+    """Block tables, slot map and positions of a step, on the GPU, from the
+    requests' cached and new lengths (int32 [B]; see include/w4a16.h).
+
+    block_table [B, columns] int32 is updated in place: the pages a request
+    holds stay, the ones it needs now are taken from free_pages in request
+    order, the rest becomes -1.  Returns (q_start [B+1], kv_len [B], positions
+    [T], slot_map [T], pages_used [1]), all int32; T is slot_map's length, or
+    max_tokens where slot_map is None (entries past the new tokens are -1)."""
+    B = past_len.shape[0]
+    _int32(past_len, "past_len", B)
+    _int32(new_len, "new_len", B)
+    _int32(free_pages, "free_pages")
+    _block_table(block_table, B)
+    dev = past_len.device
+    if slot_map is None:
+        if max_tokens is None:
+            raise ValueError("give slot_map or max_tokens")
+        slot_map = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    T = slot_map.shape[0]
+    _int32(slot_map, "slot_map", T)
+    positions = torch.empty(T, dtype=torch.int32, device=dev) if positions is None else _int32(positions, "positions", T)
+    q_start = torch.empty(B + 1, dtype=torch.int32, device=dev) if q_start is None else _int32(q_start, "q_start", B + 1)
+    kv_len = torch.empty(B, dtype=torch.int32, device=dev) if kv_len is None else _int32(kv_len, "kv_len", B)
+    pages_used = (torch.empty(1, dtype=torch.int32, device=dev) if pages_used is None
+                  else _int32(pages_used, "pages_used", 1))
+    args = _PLAN_ARGS.pack(past_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(), block_table.data_ptr(),
+                           q_start.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), slot_map.data_ptr(),
+                           pages_used.data_ptr(), block_table.stride(0) if B > 1 else block_table.shape[1], B,
+                           free_pages.numel(), block_table.shape[1], T, page_size, flags)
+    _raise(load_library().w4a16_page_plan(args, _stream(stream, dev.index)), "w4a16_page_plan")
+    return q_start, kv_len, positions, slot_map, pages_used
+
+
+def _cache_shape(k_cache, v_cache, dtype):
+    shape = _strided(k_cache, "k_cache", dtype, 4)
+    if _strided(v_cache, "v_cache", dtype, 4) != shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(shape)}")
+    return shape
+
+
+def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, stream=None, flags: int = FLAG_PDL) -> None:
+    """New keys and values [T, heads, head_dim] (bf16 or fp16; strided views
+    such as slices of a fused projection's output) into the caches [pages,
+    heads, page_size, head_dim] at the slots of slot_map [T] (int32; negative
+    or past the cache: skipped)."""
+    dtype = k.dtype
+    T, heads, d = _strided(k, "k", dtype, 3)
+    if _strided(v, "v", dtype, 3) != k.shape:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(k.shape)}")
+    pages, ch, page, cd = _cache_shape(k_cache, v_cache, dtype)
+    if ch != heads or cd != d or dtype not in _DTYPES:
+        raise ValueError(f"caches of {ch} heads of {cd} do not take k of {heads} heads of {d} in {dtype}")
+    _int32(slot_map, "slot_map", T)
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    args = _WRITE_ARGS.pack(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                            kt, kh, vt, vh, *k_cache.stride()[:3], *v_cache.stride()[:3], T, heads, d, pages, page,
+                            _DTYPES[dtype], flags, 0)
+    _raise(load_library().w4a16_kv_write(args, _stream(stream, k.device.index)), "w4a16_kv_write")
+
+
+def w4a16_paged_attention_workspace_bytes(tokens: int, requests: int, q_heads: int, kv_heads: int, head_dim: int,
+                                          max_q: int) -> int:
+    return int(load_library().w4a16_paged_attention_workspace_bytes(tokens, requests, q_heads, kv_heads, head_dim,
+                                                                    max_q))
+
+
+def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                          q_start: torch.Tensor, kv_len: torch.Tensor, max_q: int, window: int = 0,
+                          block: bool = False, scale: float | None = None, out: torch.Tensor | None = None,
+                          lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
+                          flags: int = FLAG_PDL) -> torch.Tensor:
+    """Attention of every request's new tokens over its paged cache (see
+    include/w4a16.h): decode, draft blocks, prompt chunks and mixtures of them.
+
+    q [T, Hq, d] bf16 or fp16, d 64 or 128; caches [pages, Hkv, page_size, d];
+    block_table [B, columns], q_start [B+1], kv_len [B] int32; max_q at least
+    every request's number of new tokens.  window = 0: no window.  lse: [T, Hq]
+    f32, filled if given.  Returns out [T, Hq, d]."""
+    dtype = q.dtype
+    T, Hq, d = _strided(q, "q", dtype, 3)
+    pages, Hkv, page, cd = _cache_shape(k_cache, v_cache, dtype)
+    if cd != d or dtype not in _DTYPES:
+        raise ValueError(f"caches with heads of {cd} do not go with q with heads of {d} in {dtype}")
+    B = kv_len.shape[0]
+    _int32(kv_len, "kv_len", B)
+    _int32(q_start, "q_start", B + 1)
+    _block_table(block_table, B)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
+    elif _strided(out, "out", dtype, 3) != q.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (T, Hq))
+    lib = load_library()
+    if workspace is None:
+        idx = q.device.index
+        key = ("paged_attention", T, B, Hq, Hkv, d, max_q, idx)
+        need = _need_cache.get(key)
+        if need is None:
+            need = int(lib.w4a16_paged_attention_workspace_bytes(T, B, Hq, Hkv, d, max_q))
+            _need_cache[key] = need
+        if need:
+            workspace = _cached_workspace(need, q.device)
+    qt, qh, _ = q.stride()
+    ot, oh, _ = out.stride()
+    args = _ATTN_ARGS.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                           q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
+                           0 if lse is None else lse.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
+                           0 if workspace is None else workspace.numel() * workspace.element_size(), qt, qh, ot, oh,
+                           *k_cache.stride()[:3], *v_cache.stride()[:3],
+                           block_table.stride(0) if B > 1 else block_table.shape[1], T, B, Hq, Hkv, d, pages, page,
+                           block_table.shape[1], max_q, window, int(block), _DTYPES[dtype],
+                           0.0 if scale is None else scale, flags)
+    _raise(lib.w4a16_paged_attention(args, _stream(stream, q.device.index)), "w4a16_paged_attention")
+    return out
+
+
+def _rows_of(t, name, dtype, rows):
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if t.dim() != 1 or t.shape[0] != rows:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows,)}")
+    return t.data_ptr()
+
+
+def w4a16_sample(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.Tensor | None = None,
+                 top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                 min_p: torch.Tensor | None = None, token: torch.Tensor | None = None,
+                 logprob: torch.Tensor | None = None, stream=None, flags: int = FLAG_PDL) -> torch.Tensor:
+    """One token a row of logits [R, V] (bf16, fp16 or f32), filtered by each
+    row's top-k, top-p and min-p at its temperature, drawn with the given
+    exponential random numbers noise [R, V] f32 (see include/w4a16.h).
+
+    temperature, top_p, min_p f32 [R] and top_k int32 [R], or None.  Returns
+    token [R] int32; logprob [R] f32 is filled if given."""
+    dtype = logits.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"logits must be bf16, fp16 or f32, got {dtype}")
+    R, V = _strided(logits, "logits", dtype, 2)
+    if tuple(_strided(noise, "noise", torch.float32, 2)) != (R, V):
+        raise ValueError(f"noise has shape {tuple(noise.shape)}, expected {(R, V)}")
+    if token is None:
+        token = torch.empty(R, dtype=torch.int32, device=logits.device)
+    f32 = torch.float32
+    args = _SAMPLE_ARGS.pack(logits.data_ptr(), noise.data_ptr(), _rows_of(temperature, "temperature", f32, R),
+                             _rows_of(top_k, "top_k", torch.int32, R), _rows_of(top_p, "top_p", f32, R),
+                             _rows_of(min_p, "min_p", f32, R), _rows_of(token, "token", torch.int32, R),
+                             _rows_of(logprob, "logprob", f32, R), logits.stride(0) if R > 1 else V,
+                             noise.stride(0) if R > 1 else V, R, V, _DTYPES[dtype], flags)
+    _raise(load_library().w4a16_sample(args, _stream(stream, logits.device.index)), "w4a16_sample")
+    return token
 
 
 def to_device(problem, device="cuda"):

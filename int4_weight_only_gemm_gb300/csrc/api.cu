@@ -186,6 +186,11 @@ int check_gemm(const void* x, const uint32_t* qd, const void* scales, const uint
     return W4A16_OK;
 }
 
+int current_sms() {
+    const int dev = current_device();
+    return dev < 0 ? -1 : device_sms(dev);
+}
+
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 const DispatchRow* dispatch_row(int M, int K, int N) {

@@ -133,6 +133,16 @@ cudaError_t launch_swa(const uint16_t* q, const uint16_t* kc, const uint16_t* vt
                        bool pdl);
 int swa_read_status();
 
+// serving operators (api_serving.cu checks their arguments)
+constexpr int kPlanMaxRequests = 16384;
+cudaError_t launch_page_plan(const w4a16_page_plan_args& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_write(const w4a16_kv_write_args& a, int sms, cudaStream_t s);
+size_t paged_attn_workspace(int tokens, int requests, int Hq, int Hkv, int d, int max_q, int sms);
+cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cudaStream_t s);
+cudaError_t launch_sample(const w4a16_sample_args& a, int sms, cudaStream_t s);
+// multiprocessors of the current device (api.cu), or <= 0
+int current_sms();
+
 // failure-detection self-test
 cudaError_t launch_selftest_wait(uint64_t limit_ns, cudaStream_t s);
 int selftest_read_status();

@@ -1,0 +1,130 @@
+// Shared pieces of the paged-attention kernels: their parameters, the 16-bit
+// types, and one query row computed from the definition.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace w4a16 {
+
+struct PagedAttnParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const int* table;
+    const int* q_start;
+    const int* kv_len;
+    uint16_t* out;
+    float* lse;  // or null
+    int64_t q_token, q_head, o_token, o_head;
+    int64_t kp, kh, ks, vp, vh, vs;  // strides of pages, heads, slots
+    int64_t table_stride;
+    int T, B, Hq, Hkv, G, pages, shift, columns;
+    int window, block;
+    float scale2;  // scale * log2(e): scores in the base-2 exponent
+};
+
+struct Bf16 {
+    static constexpr uint32_t idesc_type = 1;  // of kind::f16 operands
+    W4A16_DEVICE static float lo(uint32_t v) { return bf16lo(v); }
+    W4A16_DEVICE static float hi(uint32_t v) { return bf16hi(v); }
+    W4A16_DEVICE static uint32_t pack(float a, float b) {  // a in the low half
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
+};
+struct F16 {
+    static constexpr uint32_t idesc_type = 0;
+    W4A16_DEVICE static float lo(uint32_t v) { return f16_bits_to_f32((uint16_t)v); }
+    W4A16_DEVICE static float hi(uint32_t v) { return f16_bits_to_f32((uint16_t)(v >> 16)); }
+    W4A16_DEVICE static uint32_t pack(float a, float b) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
+};
+
+W4A16_DEVICE float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The positions that token i of request b sees: lo <= j <= e.  L and n are the
+// request's lengths, already clamped to the table and to the tokens.
+struct Request {
+    int t0, n, L;
+};
+W4A16_DEVICE Request request_of(const PagedAttnParams& p, int b) {
+    Request r;
+    r.t0 = min(max(p.q_start[b], 0), p.T);
+    r.n = min(max(p.q_start[b + 1], r.t0), p.T) - r.t0;
+    const int64_t room = (int64_t)p.columns << p.shift;
+    r.L = max(p.kv_len[b], 0);
+    if (r.L > room) r.L = (int)room;
+    return r;
+}
+W4A16_DEVICE int last_seen(const PagedAttnParams& p, const Request& r, int i) {
+    return p.block ? r.L - 1 : r.L - r.n + i;
+}
+W4A16_DEVICE int first_seen(const PagedAttnParams& p, int e) {
+    return p.window > 0 && e - p.window + 1 > 0 ? e - p.window + 1 : 0;
+}
+
+// One query row from the definition, by one warp: every lane holds D / 32
+// elements, one key after the other, with the running maximum and sum of the
+// softmax.  Reads only the positions that the row sees.
+template <typename Ty, int D>
+W4A16_DEVICE void attn_row(const PagedAttnParams& p, int b, const Request& r, int i, int h) {
+    constexpr int E = D / 64;  // 32-bit words a lane
+    const int lane = threadIdx.x & 31;
+    const int hk = h / p.G, t = r.t0 + i;
+    const int e = last_seen(p, r, i), lo = first_seen(p, e);
+    uint32_t q[E];
+    const uint32_t* qp = reinterpret_cast<const uint32_t*>(p.q + t * p.q_token + h * p.q_head) + lane * E;
+#pragma unroll
+    for (int u = 0; u < E; ++u) q[u] = qp[u];
+    float m = -INFINITY, l = 0.f, acc[2 * E];
+#pragma unroll
+    for (int u = 0; u < 2 * E; ++u) acc[u] = 0.f;
+    const int* row = p.table + b * p.table_stride;
+    for (int j = lo; j <= e; ++j) {
+        const int pg = row[j >> p.shift], sl = j & ((1 << p.shift) - 1);
+        if (pg < 0 || pg >= p.pages) continue;
+        const uint32_t* kp =
+            reinterpret_cast<const uint32_t*>(p.k + pg * p.kp + hk * p.kh + sl * p.ks) + lane * E;
+        const uint32_t* vp =
+            reinterpret_cast<const uint32_t*>(p.v + pg * p.vp + hk * p.vh + sl * p.vs) + lane * E;
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < E; ++u) {
+            const uint32_t kk = kp[u];
+            s = fmaf(Ty::lo(q[u]), Ty::lo(kk), s);
+            s = fmaf(Ty::hi(q[u]), Ty::hi(kk), s);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        s *= p.scale2;
+        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2_approx(m - base), w = exp2_approx(s - base);
+        l = l * f + w;
+#pragma unroll
+        for (int u = 0; u < E; ++u) {
+            const uint32_t vv = vp[u];
+            acc[2 * u] = acc[2 * u] * f + w * Ty::lo(vv);
+            acc[2 * u + 1] = acc[2 * u + 1] * f + w * Ty::hi(vv);
+        }
+        m = mn;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no position seen: zero
+    uint32_t* op = reinterpret_cast<uint32_t*>(p.out + t * p.o_token + h * p.o_head) + lane * E;
+#pragma unroll
+    for (int u = 0; u < E; ++u)
+        op[u] = l == 0.f ? 0u : Ty::pack(acc[2 * u] * inv, acc[2 * u + 1] * inv);
+    if (p.lse && lane == 0) p.lse[(int64_t)t * p.Hq + h] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+}
+
+}  // namespace w4a16
