@@ -436,8 +436,9 @@ int w4a16_kv_write(const w4a16_kv_write_args *args, w4a16_stream_t stream);
  *     lse[t][h] = log sum_{j in J_i} exp(scale q[t][h] . k[j][hk])
  *
  * One token a request (decode), a draft block, a chunk of a prompt, and any
- * mixture of them in one call.  Scores, softmax and sums are f32; the softmax
- * weights are rounded once to the inputs' type for the product with v.  A
+ * mixture of them in one call.  Scores, softmax and sums are f32.  For the
+ * product with v the softmax weights are split in two numbers of the inputs'
+ * type (16 bits of precision in bf16, 22 in fp16) where rows are few.  A
  * token that sees no position (J_i empty, or all its scores -inf) gets out = 0
  * and lse = -inf.  What lies outside J_i has no effect on out[t], NaN and
  * infinities included.  Rows t >= q_start[requests] are not written.

@@ -2,6 +2,8 @@
 // types, and one query row computed from the definition.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -21,6 +23,9 @@ struct PagedAttnParams {
     int64_t table_stride;
     int T, B, Hq, Hkv, G, pages, shift, columns;
     int window, block;
+    int small_rows;  // requests with up to this many query rows a key head go to the small-row kernel
+    unsigned* counters;  // arrival counters, zero between calls
+    float* part;         // partial results of split work
     float scale2;  // scale * log2(e): scores in the base-2 exponent
 };
 
@@ -44,6 +49,35 @@ struct F16 {
         return r;
     }
 };
+
+// D += A B, 16 x 8 x 16, warp-wide
+template <typename Ty>
+W4A16_DEVICE void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (Ty::idesc_type == 1)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+W4A16_DEVICE void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+W4A16_DEVICE void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 
 W4A16_DEVICE float exp2_approx(float x) {
     float y;
@@ -126,5 +160,14 @@ W4A16_DEVICE void attn_row(const PagedAttnParams& p, int b, const Request& r, in
         op[u] = l == 0.f ? 0u : Ty::pack(acc[2 * u] * inv, acc[2 * u + 1] * inv);
     if (p.lse && lane == 0) p.lse[(int64_t)t * p.Hq + h] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
+
+// Tensor map of the key or value cache, (column, slot, head, page), in boxes of
+// 64 columns by `rows` slots, 128-byte swizzle (paged_attn.cu).
+bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool values, int rows);
+
+// requests of up to 16 query rows a key head (paged_decode.cu)
+constexpr int kSmallRows = 16;
+size_t paged_decode_part_bytes(int d, int sms);
+cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl);
 
 }  // namespace w4a16
