@@ -437,9 +437,10 @@ int w4a16_kv_write(const w4a16_kv_write_args *args, w4a16_stream_t stream);
  *
  * One token a request (decode), a draft block, a chunk of a prompt, and any
  * mixture of them in one call.  Scores, softmax and sums are f32.  For the
- * product with v the softmax weights are split in two numbers of the inputs'
- * type (16 bits of precision in bf16, 22 in fp16) where rows are few.  A
- * token that sees no position (J_i empty, or all its scores -inf) gets out = 0
+ * product with v the softmax weights are rounded to the inputs' type; for
+ * tokens that see fewer than 256 positions, and in requests of few query rows,
+ * they are split in two numbers of that type (16 bits of precision in bf16, 22
+ * in fp16).  A token that sees no position (J_i empty, or all its scores -inf) gets out = 0
  * and lse = -inf.  What lies outside J_i has no effect on out[t], NaN and
  * infinities included.  Rows t >= q_start[requests] are not written.
  *
@@ -472,7 +473,7 @@ typedef struct {
     int64_t table_stride;
     int32_t tokens, requests, q_heads, kv_heads, head_dim, num_pages, page_size, columns;
     int32_t max_q, window, block, dtype;
-    float scale;                /* of the scores; 0 stands for 1 / sqrt(head_dim) */
+    float scale;                /* of the scores, >= 0; 0 stands for 1 / sqrt(head_dim) */
     uint32_t flags;
 } w4a16_paged_attention_args;
 int w4a16_paged_attention(const w4a16_paged_attention_args *args, w4a16_stream_t stream);

@@ -136,7 +136,7 @@ int w4a16_paged_attention(const w4a16_paged_attention_args* a, w4a16_stream_t st
     int st = check_paged_sizes(a->tokens, a->requests, a->q_heads, a->kv_heads, a->head_dim, a->max_q);
     if (st != W4A16_OK) return st;
     if (a->num_pages < 1 || a->columns < 1 || a->table_stride < a->columns || a->window < 0 ||
-        (a->block != 0 && a->block != 1) || !(a->scale == a->scale))
+        (a->block != 0 && a->block != 1) || !(a->scale >= 0.f))
         return W4A16_EINVAL;
     st = check_page_size(a->page_size);
     if (st != W4A16_OK) return st;

@@ -1,27 +1,12 @@
-// Attention of the new tokens over a paged cache: one warp per query row.
+// Attention of the new tokens over a paged cache: tensor maps, workspace, and
+// which kernel takes a request -- the small-row kernel (paged_decode.cu) up to
+// kSmallRows query rows a key head, the chunk kernel (paged_chunk.cu) above.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include "paged_attn.cuh"
 
 namespace w4a16 {
-
-template <typename Ty, int D>
-__global__ void __launch_bounds__(128) paged_attn_rows_kernel(const PagedAttnParams p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int t = (int)(row / p.Hq), h = (int)(row - (int64_t)t * p.Hq);
-    if (t >= p.T || t >= p.q_start[p.B]) return;
-    int lo = 0, hi = p.B;  // the last request that starts at or before t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.q_start[mid] <= t) lo = mid; else hi = mid;
-    }
-    const Request r = request_of(p, lo);
-    if (r.n * p.G <= p.small_rows) return;  // the small-row kernel's
-    attn_row<Ty, D>(p, lo, r, t - r.t0, h);
-}
 
 static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
@@ -53,8 +38,24 @@ bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t paged_attn_workspace(int, int, int, int, int d, int, int sms) {
-    return kCounterBytes + paged_decode_part_bytes(d, sms);
+bool query_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, int tokens) {
+    auto encode = encoder();
+    if (!encode) return false;
+    const uint64_t row = (uint64_t)d * 2;
+    const uint64_t hs = p.Hq == 1 ? row : (uint64_t)p.q_head * 2, ts = p.T == 1 ? row : (uint64_t)p.q_token * 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+    const cuuint64_t strides[2] = {hs, ts};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tokens}, estr[3] = {1, 1, 1};
+    return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<uint16_t*>(p.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The arrival counters, both kernels' partial results (two a CTA, one CTA an SM).
+size_t paged_attn_workspace(int, int, int Hq, int Hkv, int d, int max_q, int sms) {
+    const bool large = (int64_t)max_q * (Hq / Hkv) > kSmallRows;
+    return kCounterBytes + paged_decode_part_bytes(d, sms) + (large ? paged_chunk_part_bytes(d, sms) : 0);
 }
 
 cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cudaStream_t s) {
@@ -90,14 +91,10 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cuda
         note_launch();
     }
     if (!large) return cudaSuccess;
-    const int64_t rows = (int64_t)a.tokens * a.q_heads;
-    const dim3 grid((unsigned)((rows + 3) / 4)), block(128);
-    note_launch();
-    if (bf16)
-        return a.head_dim == 128 ? launch_kernel(paged_attn_rows_kernel<Bf16, 128>, grid, block, 0, s, pdl, p)
-                                 : launch_kernel(paged_attn_rows_kernel<Bf16, 64>, grid, block, 0, s, pdl, p);
-    return a.head_dim == 128 ? launch_kernel(paged_attn_rows_kernel<F16, 128>, grid, block, 0, s, pdl, p)
-                             : launch_kernel(paged_attn_rows_kernel<F16, 64>, grid, block, 0, s, pdl, p);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes + paged_decode_part_bytes(a.head_dim, sms));
+    const cudaError_t e = launch_paged_chunk(p, bf16, a.head_dim, sms, s, pdl);
+    if (e == cudaSuccess) note_launch();
+    return e;
 }
 
 }  // namespace w4a16

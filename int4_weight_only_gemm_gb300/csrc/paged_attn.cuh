@@ -165,9 +165,17 @@ W4A16_DEVICE void attn_row(const PagedAttnParams& p, int b, const Request& r, in
 // 64 columns by `rows` slots, 128-byte swizzle (paged_attn.cu).
 bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool values, int rows);
 
+// Tensor map of the queries, (column, head, token), in boxes of 64 columns by
+// the heads of a group by `tokens` tokens, 128-byte swizzle (paged_attn.cu).
+bool query_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, int tokens);
+
 // requests of up to 16 query rows a key head (paged_decode.cu)
 constexpr int kSmallRows = 16;
 size_t paged_decode_part_bytes(int d, int sms);
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl);
+
+// the other requests (paged_chunk.cu)
+size_t paged_chunk_part_bytes(int d, int sms);
+cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl);
 
 }  // namespace w4a16

@@ -1,0 +1,841 @@
+// Paged attention for many query rows: prompt chunks, draft blocks, and every
+// request whose new tokens make more than 16 rows a key head.  tcgen05 + TMA.
+//
+//     row r = i G + g of 128: token i of the tile, head hk G + g
+//     S = Q K^T,  P = 2^(scale log2(e) S - m),  O = sum over key tiles of P V,  out = O / sum P
+//
+// An item is up to two 128-row tiles of one (request, key head): the two tiles
+// share every key and value tile of 128 positions, and while one tile's softmax
+// runs, the tensor cores work on the other's products.  With at most 128 rows
+// left (a draft block, the end of a chunk) the two softmax warpgroups take
+// turns on the key tiles of the same rows instead, and join their sums.
+//
+//   * warp 9 copies Q and the pages of the key / value tiles into shared memory
+//     (one 128-byte-swizzled box a page and 64 columns), a ring of tiles;
+//   * warp 8 issues the MMAs: S = Q K^T from shared memory (128 x 128 x D, f32
+//     in tensor memory), O += P V with P from tensor memory (over S) and V in
+//     the layout it has in the cache (its columns are contiguous: MN-major);
+//   * warpgroups 0 and 1, a thread a row: mask, row maximum, exponentials, sum,
+//     P back to tensor memory.  O is rescaled only when a row's maximum grew by
+//     more than 2^8 since the last time: weights up to 2^8 lose nothing in f32
+//     sums or in 16-bit floating weights.
+//
+// The key tiles of all items form one line, cut evenly over the CTAs (one an
+// SM); an item whose tiles fall to several CTAs is joined by the last of them
+// to arrive, in CTA order.
+//
+// Precision: weights are rounded to the 16-bit type for the product with V.
+// Over hundreds of positions these roundings average out; rows that see fewer
+// than 256 positions carry them in two parts (hi + lo, two products).
+//
+// Positions that no row of an item sees are cleared in the value tile; where a
+// value that only some rows see is not finite, the item's rows are computed
+// from the definition instead (attn_row), so that a NaN stays with the rows
+// that see it.
+//
+// Every wait is bounded: on a timeout the kernel records W4A16_ETIMEOUT, ends
+// its copies and MMAs, frees its tensor memory and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "paged_attn.cuh"
+
+namespace w4a16 {
+
+static __device__ int g_chunk_status;
+
+constexpr int kChThreads = 320;  // two softmax warpgroups, the MMA warp and the copy warp
+constexpr int kChKeys = 128;
+constexpr int kChTwo = 256;  // rows that see fewer positions carry their weights in two parts
+constexpr int kChCounters = 1024;  // first arrival counter of this kernel (the small-row kernel's lie below)
+
+template <int D>
+struct Ch {
+    static constexpr int kSlabs = D / 64;
+    static constexpr int kTile = kSlabs * 16384;    // bytes of 128 rows of keys, values or queries
+    static constexpr int kSlots = D == 128 ? 5 : 10;
+    static constexpr int kRingOff = 2 * kTile;
+    static constexpr int kMlOff = kRingOff + kSlots * kTile;  // [128] m, l of warpgroup 1
+    static constexpr int kBarOff = kMlOff + 1024;
+    static constexpr int kMissOff = kBarOff + 256;            // [8] pages of a tile that are not there
+    static constexpr int kMiscOff = kMissOff + 64;
+    static constexpr int kSmem = kMiscOff + 128 + 1024;
+    static constexpr int kPartHalf = 128 * (D + 2);           // floats of one row tile's partial result
+    static constexpr uint32_t kTS = 0, kTO = 256;             // tensor memory: S and P of both tiles, then O
+};
+static_assert(Ch<128>::kSmem + 256 <= 232448 && Ch<64>::kSmem + 256 <= 232448, "shared memory");
+
+// ---- instructions ---------------------------------------------------------
+// D[tmem] (+)= A[smem] B[smem], issued by one lane of a converged warp
+W4A16_DEVICE void mma_ss_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// V tile, [128 keys][64 columns] slabs: columns contiguous (MN-major), 128-byte
+// swizzle; slabs 16 KB apart along the columns, 8-key groups 1 KB apart.
+W4A16_DEVICE uint64_t desc_v(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFF) >> 4);
+    d |= (uint64_t)(16384 >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+template <typename Ty>
+__device__ constexpr uint32_t idesc_ch(int N, bool v) {
+    return (1u << 4) | (Ty::idesc_type << 7) | (Ty::idesc_type << 10) | ((v ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+#define W4A16_R32(v, o)                                                                                            \
+    "r"((v)[o]), "r"((v)[o + 1]), "r"((v)[o + 2]), "r"((v)[o + 3]), "r"((v)[o + 4]), "r"((v)[o + 5]),              \
+        "r"((v)[o + 6]), "r"((v)[o + 7]), "r"((v)[o + 8]), "r"((v)[o + 9]), "r"((v)[o + 10]), "r"((v)[o + 11]),    \
+        "r"((v)[o + 12]), "r"((v)[o + 13]), "r"((v)[o + 14]), "r"((v)[o + 15]), "r"((v)[o + 16]),                  \
+        "r"((v)[o + 17]), "r"((v)[o + 18]), "r"((v)[o + 19]), "r"((v)[o + 20]), "r"((v)[o + 21]),                  \
+        "r"((v)[o + 22]), "r"((v)[o + 23]), "r"((v)[o + 24]), "r"((v)[o + 25]), "r"((v)[o + 26]),                  \
+        "r"((v)[o + 27]), "r"((v)[o + 28]), "r"((v)[o + 29]), "r"((v)[o + 30]), "r"((v)[o + 31])
+W4A16_DEVICE void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        W4A16_R32(v, 0)
+        : "memory");
+}
+W4A16_DEVICE void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+W4A16_DEVICE void tmem_ld32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// ---- the line of key tiles --------------------------------------------------
+// sum over i < n of floor((a i + b) / m), by the Euclid-like recursion on (a, m)
+W4A16_DEVICE int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    int64_t s = 0;
+    while (true) {
+        if (a >= m) {
+            s += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2);
+            a %= m;
+        }
+        if (b >= m) {
+            s += (int64_t)(b / m) * n;
+            b %= m;
+        }
+        const uint64_t y = (uint64_t)a * n + b;
+        if (y < m) return s;
+        n = (uint32_t)(y / m);
+        b = (uint32_t)(y - (uint64_t)n * m);
+        const uint32_t t = m;
+        m = a;
+        a = t;
+    }
+}
+
+struct ChunkItem {
+    int i0, tokens;      // first token (of the request) and their number
+    int e0, e1;          // last position that the first and the last token see
+    int lo0, lo1;        // first position that they see
+    int t0, tiles;       // first key tile and their number
+};
+W4A16_DEVICE ChunkItem item_of(const PagedAttnParams& p, const Request& r, int q, int span) {
+    ChunkItem it;
+    it.i0 = q * span;
+    it.tokens = min(span, r.n - it.i0);
+    it.e0 = last_seen(p, r, it.i0);
+    it.e1 = last_seen(p, r, it.i0 + it.tokens - 1);
+    it.lo0 = first_seen(p, it.e0);
+    it.lo1 = first_seen(p, it.e1);
+    it.t0 = it.lo0 / kChKeys;
+    it.tiles = it.e1 < it.lo0 ? 1 : it.e1 / kChKeys + 1 - it.t0;  // nothing seen: one masked tile
+    return it;
+}
+W4A16_DEVICE int items_of(const PagedAttnParams& p, const Request& r, int span) {
+    return r.n * p.G <= p.small_rows ? 0 : (r.n + span - 1) / span;
+}
+// key tiles of the first k items of a request, for one key head
+W4A16_DEVICE int64_t tiles_before(const PagedAttnParams& p, const Request& r, int span, int k) {
+    if (k == 0) return 0;
+    if (p.block || r.L < r.n) {
+        if (p.block) return (int64_t)k * item_of(p, r, 0, span).tiles;
+        int64_t s = 0;
+        for (int q = 0; q < k; ++q) s += item_of(p, r, q, span).tiles;
+        return s;
+    }
+    const int base = r.L - r.n;
+    const int full = min(k, r.n / span);  // items that end before or at a whole span
+    int64_t s = floor_sum(full, kChKeys, span, base + span - 1) + full;
+    if (k > full) s += (r.L - 1) / kChKeys + 1;
+    if (p.window > 0) {
+        const int x = base - p.window + 1;            // item q starts at x + q span where that is positive
+        const int q0 = x > 0 ? 0 : (-x) / span + 1;
+        if (k > q0) s -= floor_sum(k - q0, kChKeys, span, x + q0 * span);
+    }
+    return s;
+}
+
+struct ChunkPiece {
+    Request r;
+    ChunkItem it;
+    int b, hk, q;
+    int off, take;            // key tiles of the item before this piece, and in it
+    int64_t first;            // the item's first tile on the line
+    bool duo;                 // two row tiles (else both warpgroups share the first)
+    bool two;                 // weights in two parts
+};
+// Walks a CTA's part of the line; every warp walks it for itself.
+struct ChunkWalk {
+    int b, hk, q, off, items;
+    int64_t at, left;
+    Request r;
+    W4A16_DEVICE bool next(const PagedAttnParams& p, int span, ChunkPiece& c) {
+        if (left <= 0) return false;
+        c.r = r;
+        c.it = item_of(p, r, q, span);
+        c.b = b;
+        c.hk = hk;
+        c.q = q;
+        c.off = off;
+        c.take = (int)(left < c.it.tiles - off ? left : c.it.tiles - off);
+        c.first = at - off;
+        c.duo = 2 * c.it.tokens > span;
+        c.two = c.it.e0 - c.it.lo0 + 1 < kChTwo;
+        at += c.take;
+        left -= c.take;
+        if (left > 0) {
+            off = 0;
+            if (++q == items) {
+                q = 0;
+                if (++hk == p.Hkv) {
+                    hk = 0;
+                    do {
+                        r = request_of(p, ++b);
+                        items = items_of(p, r, span);
+                    } while (items == 0);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+template <typename Ty, int D>
+W4A16_DEVICE void attn_rows_from_definition(const PagedAttnParams& p, int b, Request r, int i0, int tokens,
+                                                       int hk, int warp) {
+    // a warp takes every fourth row of up to 128
+    for (int x = warp; x < tokens * p.G; x += 4) {
+        const int i = x / p.G;
+        attn_row<Ty, D>(p, b, r, i0 + i, hk * p.G + x - i * p.G);
+    }
+}
+
+template <typename Ty, int D>
+__global__ void __launch_bounds__(kChThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedAttnParams p) {
+    using L = Ch<D>;
+    constexpr int NS = L::kSlots;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    float2* ml1 = reinterpret_cast<float2*>(smem + L::kMlOff);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+    uint64_t* empty = full + NS;
+    uint64_t* s_full = empty + NS;   // [2]
+    uint64_t* p_full = s_full + 2;   // [2]
+    uint64_t* o_full = p_full + 2;   // [2]
+    uint64_t* o_free = o_full + 2;   // [2]
+    uint64_t* q_full = o_free + 2;
+    uint64_t* q_free = q_full + 1;
+    uint64_t* join = q_free + 1;     // warpgroup 1's maxima and sums are in ml1
+    uint64_t* done = join + 1;       // every MMA of the CTA is done
+    static_assert((2 * NS + 12) * 8 <= 256, "barriers");
+    volatile uint32_t* miss = reinterpret_cast<volatile uint32_t*>(smem + L::kMissOff);
+    volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
+    volatile int* abort_flag = misc;  // misc: abort, request, -, item, offset, last arrival (2), -, tensor memory
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff) + 8;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = (int)blockIdx.x;
+    const int toks = 128 / p.G, span = 2 * toks;  // tokens of a row tile and of an item
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(s_full + g, 1);
+            mbar_init(p_full + g, 128);
+            mbar_init(o_full + g, 1);
+            mbar_init(o_free + g, 128);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_free, 1);
+        mbar_init(join, 128);
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    if (warp == 9 && lane == 0) {
+        prefetch_tmap(&tmap_q);
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---- this CTA's part of the line --------------------------------------
+    __shared__ int64_t warp_sum[kChThreads / 32];
+    __shared__ int64_t rest_smem;
+    const int per = (p.B + kChThreads - 1) / kChThreads;
+    const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+    auto units_of = [&](int b) {
+        const Request r = request_of(p, b);
+        return tiles_before(p, r, span, items_of(p, r, span)) * p.Hkv;
+    };
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units_of(b);
+    int64_t before = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += x;
+    }
+    if (lane == 31) warp_sum[warp] = before;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t U = 0;
+    for (int w = 0; w < kChThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        U += warp_sum[w];
+    }
+    before -= mine;
+    const uint32_t tmem = *tmem_holder;
+    const int C = (int)(U < gridDim.x ? U : gridDim.x);
+    ChunkWalk walk;
+    walk.left = 0;
+    if (c < C) {
+        const int64_t u0 = (int64_t)c * U / C, u1 = (int64_t)(c + 1) * U / C;
+        if (u0 >= before && u0 < before + mine) {
+            int64_t at = before;
+            for (int b = b0; b < b1; ++b) {
+                const int64_t n = units_of(b);
+                if (u0 < at + n) {
+                    misc[1] = b;
+                    rest_smem = u0 - at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        walk.b = misc[1];
+        walk.r = request_of(p, walk.b);
+        walk.items = items_of(p, walk.r, span);
+        const int64_t head = tiles_before(p, walk.r, span, walk.items);
+        walk.hk = (int)(rest_smem / head);
+        const int64_t rest = rest_smem - walk.hk * head;
+        for (int q = threadIdx.x; q < walk.items; q += kChThreads) {
+            const int64_t a = tiles_before(p, walk.r, span, q);
+            if (rest >= a && rest < a + item_of(p, walk.r, q, span).tiles) {
+                misc[3] = q;
+                misc[4] = (int)(rest - a);
+            }
+        }
+        __syncthreads();
+        walk.q = misc[3];
+        walk.off = misc[4];
+        walk.at = u0;
+        walk.left = u1 - u0;
+    }
+
+    ChunkPiece pc;
+    if (warp == 9) {
+        // ---------------------------------------------------------- copies
+        const int page = 1 << p.shift, rows = page < kChKeys ? page : kChKeys, boxes = kChKeys / rows;
+        uint32_t e = 0;     // ring entries: keys 2 i, values 2 i + 1 of this CTA's tile i
+        uint32_t items = 0;
+        bool ok = true;
+        while (ok && walk.next(p, span, pc)) {
+            if (items > 0) ok = mbar_wait_warp(q_free, (items - 1) & 1, abort_flag, &g_chunk_status);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, (uint32_t)((pc.duo ? 2 : 1) * L::kSlabs * toks * p.G * 128));
+                for (int g = 0; g < (pc.duo ? 2 : 1); ++g)
+                    for (int s = 0; s < L::kSlabs; ++s)
+                        tma_load_3d(smem + g * L::kTile + s * 16384, &tmap_q, 64 * s, pc.hk * p.G,
+                                    pc.r.t0 + pc.it.i0 + g * toks, q_full);
+            }
+            ++items;
+            const int* row = p.table + (int64_t)pc.b * p.table_stride;
+            auto entry = [&](int t) {  // lane's box of the piece's tile t
+                const int j = (pc.it.t0 + pc.off + t) * kChKeys + lane * rows, col = j >> p.shift;
+                // boxes that no row sees are not read: -2
+                if (lane >= boxes || j > pc.it.e1 || j + rows <= pc.it.lo0) return -2;
+                return col < p.columns ? row[col] : -1;
+            };
+            int ent = entry(0);
+            for (int t = 0; t < pc.take; ++t) {
+                const int j = (pc.it.t0 + pc.off + t) * kChKeys + lane * rows, slot = j & (page - 1);
+                const bool there = ent >= 0 && ent < p.pages;
+                const int pg = there ? ent : p.pages;  // past the tensor: filled with zeros
+                const uint32_t no = __ballot_sync(0xffffffffu, !there && ent != -2);
+                if (t + 1 < pc.take) ent = entry(t + 1);
+                for (int kv = 0; kv < 2; ++kv, ++e) {
+                    const int sl = e % NS;
+                    if (e >= NS) ok = mbar_wait_warp(empty + sl, (e / NS - 1) & 1, abort_flag, &g_chunk_status);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (kv == 0) miss[(e >> 1) & 7] = no;
+                        mbar_arrive_expect_tx(full + sl, (uint32_t)L::kTile);
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        unsigned char* dst = smem + L::kRingOff + sl * L::kTile + lane * rows * 128;
+#pragma unroll
+                        for (int s = 0; s < L::kSlabs; ++s)
+                            tma_load_4d(dst + s * 16384, kv ? &tmap_v : &tmap_k, 64 * s, slot, pc.hk, pg, full + sl);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+        }
+        // the copies in flight land before the CTA ends
+        for (uint32_t i = e > NS ? e - NS : 0; i < e; ++i)
+            (void)mbar_wait_warp(full + i % NS, (i / NS) & 1, nullptr, &g_chunk_status);
+        if (items > 0) (void)mbar_wait_warp(q_full, (items - 1) & 1, nullptr, &g_chunk_status);
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<Ty>(D, true);
+        uint32_t tile0 = 0, items = 0, np[2] = {0, 0};
+        bool ok = true;
+        while (ok && walk.next(p, span, pc)) {
+            const int cnt[2] = {pc.duo ? pc.take : (pc.take + 1) / 2, pc.duo ? pc.take : pc.take / 2};
+            int scores = cnt[0] + cnt[1];
+            auto tile_of = [&](int g, int k) { return tile0 + (pc.duo ? k : 2 * k + g); };
+            auto score = [&](int g, int k) {  // S_g of the warpgroup's k-th tile
+                const uint32_t e = 2 * tile_of(g, k), sl = e % NS;
+                if (!mbar_wait_warp(full + sl, (e / NS) & 1, abort_flag, &g_chunk_status)) return false;
+                tc_fence_after();
+                const uint32_t qa = smem_u32(smem + (pc.duo ? g : 0) * L::kTile);
+                const uint32_t ka = smem_u32(smem + L::kRingOff + sl * L::kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+                    mma_ss_warp(tmem + L::kTS + 128 * g, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), id_s,
+                                kk > 0 ? 1u : 0u);
+                }
+                mma_commit_warp(s_full + g);
+                if (!pc.duo || g == 1) mma_commit_warp(empty + sl);
+                if (--scores == 0) mma_commit_warp(q_free);
+                return true;
+            };
+            ok = mbar_wait_warp(q_full, items & 1, abort_flag, &g_chunk_status);
+            for (int g = 0; g < 2 && ok; ++g)
+                if (cnt[g] > 0) ok = score(g, 0);
+            for (int k = 0; k < cnt[0] && ok; ++k) {
+                for (int g = 0; g < 2 && ok; ++g) {
+                    if (k >= cnt[g]) continue;
+                    const uint32_t e = 2 * tile_of(g, k) + 1, sl = e % NS;
+                    if (k == 0 && items > 0)
+                        ok = mbar_wait_warp(o_free + g, (items - 1) & 1, abort_flag, &g_chunk_status);
+                    ok = ok && mbar_wait_warp(full + sl, (e / NS) & 1, abort_flag, &g_chunk_status) &&
+                         mbar_wait_warp(p_full + g, np[g] & 1, abort_flag, &g_chunk_status);
+                    if (!ok) break;
+                    ++np[g];
+                    tc_fence_after();
+                    const uint32_t va = smem_u32(smem + L::kRingOff + sl * L::kTile);
+                    for (int part = 0; part < (pc.two ? 2 : 1); ++part) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ts_warp(tmem + L::kTO + D * g, tmem + L::kTS + 128 * g + 64 * part + 8 * kk,
+                                             desc_v(va + kk * 2048), id_o, k > 0 || part > 0 || kk > 0 ? 1u : 0u);
+                    }
+                    if (!pc.duo || g == 1) mma_commit_warp(empty + sl);
+                    if (k + 1 < cnt[g])
+                        ok = score(g, k + 1);
+                    else
+                        mma_commit_warp(o_full + g);
+                }
+            }
+            if (ok && cnt[1] == 0) {  // a single tile: warpgroup 1 has nothing to wait for but the count
+                if (items > 0) ok = mbar_wait_warp(o_free + 1, (items - 1) & 1, abort_flag, &g_chunk_status);
+                mma_commit_warp(o_full + 1);
+            }
+            tile0 += pc.take;
+            ++items;
+        }
+        mma_commit_warp(done);
+        (void)mbar_wait_warp(done, 0, nullptr, &g_chunk_status);
+    } else if (warp < 8) {
+        // --------------------------------------------------------- softmax
+        const int g = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + L::kTS + 128 * g, to = tmem + lanes + L::kTO + D * g;
+        const uint32_t to_other = tmem + lanes + L::kTO + D * (1 - g);
+        const int tok = row / p.G, hh = row - tok * p.G;
+        uint32_t tile0 = 0, items = 0, ns = 0, joins = 0;
+        bool ok = true;
+        while (ok && walk.next(p, span, pc)) {
+            const int base_tok = pc.duo ? g * toks : 0;
+            const int mytok = base_tok + tok;  // of the item
+            const bool valid = tok < toks && mytok < pc.it.tokens;
+            const int e = valid ? last_seen(p, pc.r, pc.it.i0 + mytok) : -1, lo = first_seen(p, e);
+            const int cnt = pc.duo ? pc.take : (pc.take + 1 - g) / 2;
+            float m = -INFINITY, l = 0.f;
+            bool odd = false;
+            for (int k = 0; k < cnt; ++k) {
+                const int t = pc.duo ? k : 2 * k + g;
+                const int j0 = (pc.it.t0 + pc.off + t) * kChKeys;
+                ok = mbar_wait_warp(s_full + g, ns & 1, abort_flag, &g_chunk_status);
+                ++ns;
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t no = miss[(tile0 + t) & 7];
+                if (j0 < pc.it.lo1 || j0 + kChKeys - 1 > pc.it.e0 || no) {
+                    // an edge: scores outside the row's positions
+                    const int rl = lo - j0, re = e - j0, sh = p.shift < 7 ? p.shift : 7;
+#pragma unroll 1
+                    for (int x = 0; x < 128; x += 32) {
+                        uint32_t sv[32];
+                        tmem_ld32(ts + x, sv);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (x + i < rl || x + i > re || ((no >> ((x + i) >> sh)) & 1u)) sv[i] = 0xff800000u;  // -inf
+                        tmem_st32(ts + x, sv);
+                    }
+                    tmem_wait_st();
+                    // values: a thread looks at one key's
+                    const int j = j0 + row;
+                    const bool none = j < pc.it.lo0 || j > pc.it.e1;  // seen by no row of the item
+                    const bool some = !none && (j < pc.it.lo1 || j > pc.it.e0);
+                    const uint32_t en = 2 * (tile0 + t) + 1, sl = en % NS;
+                    ok = mbar_wait_warp(full + sl, (en / NS) & 1, abort_flag, &g_chunk_status);
+                    if (!ok) break;
+                    if (none || some) {
+                        const uint32_t va = smem_u32(smem + L::kRingOff + sl * L::kTile) + row * 128;
+                        for (int x = 0; x < 8 * L::kSlabs; ++x) {
+                            const uint32_t a = va + (x >> 3) * 16384 + (((x & 7) ^ (row & 7)) << 4);
+                            if (none) {
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+                            } else {
+                                const uint4 v = lds_v4(a);
+                                for (uint32_t y : {v.x, v.y, v.z, v.w})
+                                    odd |= !(fabsf(Ty::lo(y)) < INFINITY) || !(fabsf(Ty::hi(y)) < INFINITY);
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                // the row's maximum, 32 scores at a time and the next 32 on their way
+                uint32_t sv[2][32];
+                tmem_ld32(ts, sv[0]);
+                float mx = m, mo = m;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    tmem_wait_ld();
+                    if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        mx = fmaxf(mx, __uint_as_float(sv[x & 1][i]));
+                        mo = fmaxf(mo, __uint_as_float(sv[x & 1][i + 1]));
+                    }
+                }
+                mx = fmaxf(mx, mo);
+                const bool grew = (mx - m) * p.scale2 > 8.f;  // also from -inf
+                if (__any_sync(0xffffffffu, grew)) {
+                    const float f = mx == -INFINITY ? 1.f : exp2_approx((m - mx) * p.scale2);
+                    l *= f;
+                    m = mx;
+                    if (k > 0) {
+                        // all MMAs before this tile's scores are done: nothing adds to O now
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t ov[16];
+                            tmem_ld_x16(to + i, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f);
+                            tmem_st_x8(to + i, *reinterpret_cast<const uint32_t(*)[8]>(ov));
+                            tmem_st_x8(to + i + 8, *reinterpret_cast<const uint32_t(*)[8]>(ov + 8));
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m * p.scale2;
+                float l0 = 0.f, l1 = 0.f;
+                // weights: scores 32 x .. become the 16 columns 16 x .., over scores read before
+                auto weights = [&](const uint32_t* v, uint32_t* pk) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = exp2_approx(fmaf(__uint_as_float(v[2 * i]), p.scale2, -base));
+                        const float b = exp2_approx(fmaf(__uint_as_float(v[2 * i + 1]), p.scale2, -base));
+                        l0 += a;
+                        l1 += b;
+                        pk[i] = Ty::pack(a, b);
+                    }
+                };
+                tmem_ld32(ts, sv[0]);
+                if (!pc.two) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        tmem_wait_ld();
+                        if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
+                        uint32_t pk[16];
+                        weights(sv[x & 1], pk);
+                        tmem_st16(ts + 16 * x, pk);
+                    }
+                } else {
+                    // second parts go to columns 64 + 16 x .., once all scores are read
+                    uint32_t pk[4][16], pl[4][16];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        tmem_wait_ld();
+                        weights(sv[x & 1], pk[x]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float a = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i]), p.scale2, -base));
+                            const float b = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i + 1]), p.scale2, -base));
+                            pl[x][i] = Ty::pack(a - Ty::lo(pk[x][i]), b - Ty::hi(pk[x][i]));
+                        }
+                        if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        tmem_st16(ts + 16 * x, pk[x]);
+                        tmem_st16(ts + 64 + 16 * x, pl[x]);
+                    }
+                }
+                l += l0 + l1;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + g);
+            }
+            // ---- the item's (or the piece's) result; the warpgroup goes on or gives up together
+            ok = ok && mbar_wait_warp(o_full + g, items & 1, abort_flag, &g_chunk_status);
+            if (!pc.duo && g == 0) {
+                ok = ok && mbar_wait_warp(join, joins & 1, abort_flag, &g_chunk_status) &&
+                     mbar_wait_warp(o_full + 1, items & 1, abort_flag, &g_chunk_status);
+                ++joins;
+            }
+            ok = bar_and(1 + g, 128, ok);
+            if (!ok) break;
+            odd = !bar_and(1 + g, 128, !odd);
+            if (!pc.duo && g == 1) {
+                ml1[row] = make_float2(odd ? NAN : m, l);  // NaN: this piece asks for the definition
+                mbar_arrive(join);
+                tile0 += pc.take;
+                ++items;
+                continue;  // warpgroup 0 reads both outputs
+            }
+            float f0 = 1.f, f1 = 0.f;
+            const bool other = !pc.duo && pc.take > 1;
+            if (!pc.duo) {
+                const float2 o = ml1[row];
+                odd = odd || o.x != o.x;
+                if (other && !odd) {
+                    const float M = fmaxf(m, o.x), b = M == -INFINITY ? 0.f : M;
+                    f0 = exp2_approx((m - b) * p.scale2);
+                    f1 = exp2_approx((o.x - b) * p.scale2);
+                    // a sum that is not a number stays one
+                    l = (l == 0.f ? 0.f : l * (m == -INFINITY ? 1.f : f0)) + (o.y == 0.f ? 0.f : o.y * (o.x == -INFINITY ? 1.f : f1));
+                    m = M;
+                }
+            }
+            tc_fence_after();
+            const bool whole = pc.off == 0 && pc.take == pc.it.tiles;
+            const int64_t t = pc.r.t0 + pc.it.i0 + mytok;
+            const int h = pc.hk * p.G + hh;
+            uint16_t* out = p.out + t * p.o_token + (int64_t)h * p.o_head;
+            float* part = p.part + ((int64_t)(2 * c + (pc.off == 0 ? 1 : 0)) * 2 + g) * L::kPartHalf;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+                uint32_t ov[32];
+                tmem_ld32(to + i, ov);
+                tmem_wait_ld();
+                if (other) {
+                    uint32_t ow[32];
+                    tmem_ld32(to_other + i, ow);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f0 + __uint_as_float(ow[x]) * f1);
+                }
+                if (whole) {
+                    if (valid && !odd) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8) {
+                            uint4 v;
+                            uint32_t* y = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                y[z] = l == 0.f ? 0u
+                                                : Ty::pack(__uint_as_float(ov[x + 2 * z]) * inv,
+                                                           __uint_as_float(ov[x + 2 * z + 1]) * inv);
+                            *reinterpret_cast<uint4*>(out + i + x) = v;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)  // [column / 4][row]: neighbours write neighbours
+                        *reinterpret_cast<uint4*>(part + 256 + (((i + x) >> 2) * 128 + row) * 4) =
+                            make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
+                }
+            }
+            if (whole && valid && !odd && p.lse)
+                p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : kLn2 * (m * p.scale2 + log2f(l));
+            tc_fence_before();
+            mbar_arrive(o_free + g);
+            if (!pc.duo) mbar_arrive(o_free + 1);
+            bool again = whole && odd;  // rows to compute from the definition
+            if (!whole) {
+                reinterpret_cast<float2*>(part)[row] = make_float2(odd ? NAN : m * p.scale2, l);
+                const int64_t end = pc.first + pc.it.tiles;
+                const int c0 = (int)(((pc.first + 1) * C - 1) / U), c1 = (int)((end * C - 1) / U);
+                __threadfence();
+                named_bar(1 + g, 128);
+                if (row == 0) {
+                    unsigned* counter = p.counters + kChCounters + 2 * c0 + g;
+                    const bool last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+                    if (last) *counter = 0;
+                    misc[5 + g] = last;
+                }
+                named_bar(1 + g, 128);
+                if (misc[5 + g]) {
+                    __threadfence();
+                    auto at = [&](int i) {
+                        return p.part + ((int64_t)(2 * i + (i == c0)) * 2 + g) * L::kPartHalf;
+                    };
+                    float M = -INFINITY, S = 0.f;
+                    bool bad = false;
+                    for (int i = c0; i <= c1; ++i) {
+                        const float x = __ldcg(at(i) + 2 * row);
+                        bad |= x != x;
+                        M = fmaxf(M, x);
+                    }
+                    const float b = M == -INFINITY ? 0.f : M;
+                    again = !bar_and(1 + g, 128, !bad);
+                    if (!again) {
+                        for (int i = c0; i <= c1; ++i) {
+                            const float2 mi = __ldcg(reinterpret_cast<const float2*>(at(i)) + row);
+                            if (mi.y != 0.f) S = fmaf(mi.y, exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - b), S);
+                        }
+                        const float w = S == 0.f ? 0.f : 1.f / S;
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            float acc[32];
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) acc[y] = 0.f;
+                            for (int i = c0; i <= c1; ++i) {
+                                const float* q = at(i);
+                                const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
+                                if (mi.y == 0.f) continue;  // no seen key in this piece
+                                const float f = exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - b);
+#pragma unroll
+                                for (int y = 0; y < 32; y += 4) {
+                                    const float4 v =
+                                        __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x + y) >> 2) * 128 + row);
+                                    acc[y] = fmaf(v.x, f, acc[y]);
+                                    acc[y + 1] = fmaf(v.y, f, acc[y + 1]);
+                                    acc[y + 2] = fmaf(v.z, f, acc[y + 2]);
+                                    acc[y + 3] = fmaf(v.w, f, acc[y + 3]);
+                                }
+                            }
+                            if (!valid) continue;
+#pragma unroll
+                            for (int y = 0; y < 32; y += 8)
+                                *reinterpret_cast<uint4*>(out + x + y) =
+                                    S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                             : make_uint4(Ty::pack(acc[y] * w, acc[y + 1] * w),
+                                                          Ty::pack(acc[y + 2] * w, acc[y + 3] * w),
+                                                          Ty::pack(acc[y + 4] * w, acc[y + 5] * w),
+                                                          Ty::pack(acc[y + 6] * w, acc[y + 7] * w));
+                        }
+                        if (valid) {
+                            if (p.lse) p.lse[t * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
+                        }
+                    }
+                }
+            }
+            if (again) {
+                const int n = min(toks, pc.it.tokens - base_tok);
+                attn_rows_from_definition<Ty, D>(p, pc.b, pc.r, pc.it.i0 + base_tok, n, pc.hk, warp & 3);
+            }
+            tile0 += pc.take;
+            ++items;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename Ty, int D>
+static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnParams& p,
+                          int ctas, cudaStream_t s, bool pdl) {
+    static bool set_for[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set_for[dev]) {
+        e = cudaFuncSetAttribute(paged_chunk_kernel<Ty, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ch<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        set_for[dev] = true;
+    }
+    return launch_kernel(paged_chunk_kernel<Ty, D>, dim3(ctas), dim3(kChThreads), (size_t)Ch<D>::kSmem, s, pdl, tq, tk,
+                         tv, p);
+}
+
+size_t paged_chunk_part_bytes(int d, int sms) {
+    return (size_t)4 * sms * (d == 128 ? Ch<128>::kPartHalf : Ch<64>::kPartHalf) * sizeof(float);
+}
+
+cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl) {
+    CUtensorMap tq, tk, tv;
+    const int box = (1 << p.shift) < kChKeys ? 1 << p.shift : kChKeys;
+    if (!paged_tmap(&tk, p, bf16, d, false, box) || !paged_tmap(&tv, p, bf16, d, true, box) ||
+        !query_tmap(&tq, p, bf16, d, 128 / p.G))
+        return cudaErrorInvalidValue;
+    if (bf16)
+        return d == 128 ? launch<Bf16, 128>(tq, tk, tv, p, sms, s, pdl) : launch<Bf16, 64>(tq, tk, tv, p, sms, s, pdl);
+    return d == 128 ? launch<F16, 128>(tq, tk, tv, p, sms, s, pdl) : launch<F16, 64>(tq, tk, tv, p, sms, s, pdl);
+}
+
+int chunk_read_status() {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_chunk_status, sizeof(int)) != cudaSuccess) return W4A16_ECUDA;
+    if (cudaMemcpyToSymbol(g_chunk_status, &zero, sizeof(int)) != cudaSuccess) return W4A16_ECUDA;
+    return v;
+}
+
+}  // namespace w4a16
