@@ -510,7 +510,10 @@ size_t w4a16_paged_attention_workspace_bytes(int tokens, int requests, int q_hea
  *   temperature, top_k, top_p, min_p   [rows] or NULL (temperature 1; filter off)
  *   noise        non-negative; rows noise_row elements apart (0: one row for all)
  *   logprob      may be NULL
- * Any alignment of the rows is accepted that the element type has.
+ *   workspace    w4a16_sample_workspace_bytes bytes (NULL where that is 0), under the
+ *                GEMM's workspace rules: 16-byte aligned, zero-filled once before its
+ *                first use, its first 64 KB left as they were
+ * One launch, two where a filter is given.  Any alignment of the rows is accepted that the element type has.
  */
 typedef struct {
     const void *logits;   /* [rows][vocab], rows logits_row apart */
@@ -521,11 +524,15 @@ typedef struct {
     const float *min_p;
     int32_t *token;       /* [rows] */
     float *logprob;       /* [rows] or NULL */
+    void *workspace;
+    uint64_t workspace_bytes;
     int64_t logits_row, noise_row;
     int32_t rows, vocab, dtype;
     uint32_t flags;
 } w4a16_sample_args;
 int w4a16_sample(const w4a16_sample_args *args, w4a16_stream_t stream);
+/* Workspace of a call with these sizes on the current device; filters: whether top_k, top_p or min_p is given. */
+size_t w4a16_sample_workspace_bytes(int rows, int vocab, int filters);
 
 /* Number of kernel launches the library has issued in this process (every
  * entry point that launches counts its kernel; w4a16_gemm_noalloc's counter

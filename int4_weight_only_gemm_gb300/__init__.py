@@ -89,6 +89,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                 getattr(lib, name).argtypes = [ctypes.c_char_p, vp]  # a packed argument struct, a stream
             lib.w4a16_paged_attention_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci]
             lib.w4a16_paged_attention_workspace_bytes.restype = sz
+            lib.w4a16_sample_workspace_bytes.argtypes = [ci, ci, ci]
+            lib.w4a16_sample_workspace_bytes.restype = sz
             _lib = lib
     return _lib
 
@@ -379,7 +381,7 @@ def w4a16_swa_attention(q: torch.Tensor, k_cache: torch.Tensor, vt_cache: torch.
 _PLAN_ARGS = struct.Struct("=9QqiiiiiI")
 _WRITE_ARGS = struct.Struct("=5Q10qiiiiiiIi")
 _ATTN_ARGS = struct.Struct("=9QQ11qiiiiiiiiiiiifI")
-_SAMPLE_ARGS = struct.Struct("=8QqqiiiI")
+_SAMPLE_ARGS = struct.Struct("=9QQqqiiiI")
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
@@ -544,10 +546,15 @@ def _rows_of(t, name, dtype, rows):
     return t.data_ptr()
 
 
+def w4a16_sample_workspace_bytes(rows: int, vocab: int, filters: bool = True) -> int:
+    return int(load_library().w4a16_sample_workspace_bytes(rows, vocab, int(filters)))
+
+
 def w4a16_sample(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.Tensor | None = None,
                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
                  min_p: torch.Tensor | None = None, token: torch.Tensor | None = None,
-                 logprob: torch.Tensor | None = None, stream=None, flags: int = FLAG_PDL) -> torch.Tensor:
+                 logprob: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
+                 flags: int = FLAG_PDL) -> torch.Tensor:
     """One token a row of logits [R, V] (bf16, fp16 or f32), filtered by each
     row's top-k, top-p and min-p at its temperature, drawn with the given
     exponential random numbers noise [R, V] f32 (see include/w4a16.h).
@@ -563,12 +570,25 @@ def w4a16_sample(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.T
     if token is None:
         token = torch.empty(R, dtype=torch.int32, device=logits.device)
     f32 = torch.float32
+    lib = load_library()
+    if workspace is None:
+        filters = top_k is not None or top_p is not None or min_p is not None
+        key = ("sample", R, V, filters, logits.device.index)
+        need = _need_cache.get(key)
+        if need is None:
+            need = int(lib.w4a16_sample_workspace_bytes(R, V, int(filters)))
+            _need_cache[key] = need
+        if need:
+            workspace = _cached_workspace(need, logits.device)
     args = _SAMPLE_ARGS.pack(logits.data_ptr(), noise.data_ptr(), _rows_of(temperature, "temperature", f32, R),
                              _rows_of(top_k, "top_k", torch.int32, R), _rows_of(top_p, "top_p", f32, R),
                              _rows_of(min_p, "min_p", f32, R), _rows_of(token, "token", torch.int32, R),
-                             _rows_of(logprob, "logprob", f32, R), logits.stride(0) if R > 1 else V,
+                             _rows_of(logprob, "logprob", f32, R),
+                             0 if workspace is None else workspace.data_ptr(),
+                             0 if workspace is None else workspace.numel() * workspace.element_size(),
+                             logits.stride(0) if R > 1 else V,
                              noise.stride(0) if R > 1 else V, R, V, _DTYPES[dtype], flags)
-    _raise(load_library().w4a16_sample(args, _stream(stream, logits.device.index)), "w4a16_sample")
+    _raise(lib.w4a16_sample(args, _stream(stream, logits.device.index)), "w4a16_sample")
     return token
 
 

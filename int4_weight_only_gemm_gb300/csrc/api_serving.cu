@@ -6,7 +6,7 @@
 
 // the binding packs these structs by position
 static_assert(sizeof(w4a16_page_plan_args) == 104 && sizeof(w4a16_kv_write_args) == 152 &&
-                  sizeof(w4a16_paged_attention_args) == 224 && sizeof(w4a16_sample_args) == 96,
+                  sizeof(w4a16_paged_attention_args) == 224 && sizeof(w4a16_sample_args) == 112,
               "argument structs without padding");
 
 namespace w4a16 {
@@ -173,6 +173,12 @@ int w4a16_paged_attention(const w4a16_paged_attention_args* a, w4a16_stream_t st
     return status_of(launch_paged_attn(*a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t w4a16_sample_workspace_bytes(int rows, int vocab, int filters) {
+    if (rows < 1 || rows > 65535 || vocab < 1 || vocab > (1 << 24)) return 0;
+    const int sms = current_sms();
+    return sms > 0 ? sample_workspace(rows, vocab, filters != 0, sms) : 0;
+}
+
 int w4a16_sample(const w4a16_sample_args* a, w4a16_stream_t stream) {
     if (!a || (a->flags & ~(unsigned)W4A16_FLAG_PDL)) return W4A16_EINVAL;
     if (a->rows < 0 || a->vocab < 1 || a->logits_row < 0 || a->noise_row < 0) return W4A16_EINVAL;
@@ -197,6 +203,8 @@ int w4a16_sample(const w4a16_sample_args* a, w4a16_stream_t stream) {
     if (meet(token, lp)) return W4A16_EINVAL;
     const int sms = current_sms();
     if (sms <= 0) return W4A16_ECUDA;
+    const size_t need = sample_workspace(a->rows, a->vocab, a->top_k || a->top_p || a->min_p, sms);
+    if (need && (!a->workspace || a->workspace_bytes < need || !aligned(a->workspace, 16))) return W4A16_EWORKSPACE;
     return status_of(launch_sample(*a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -139,6 +139,7 @@ cudaError_t launch_page_plan(const w4a16_page_plan_args& a, int sms, cudaStream_
 cudaError_t launch_kv_write(const w4a16_kv_write_args& a, int sms, cudaStream_t s);
 size_t paged_attn_workspace(int tokens, int requests, int Hq, int Hkv, int d, int max_q, int sms);
 cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cudaStream_t s);
+size_t sample_workspace(int rows, int vocab, bool filters, int sms);
 cudaError_t launch_sample(const w4a16_sample_args& a, int sms, cudaStream_t s);
 int decode_read_status();
 int chunk_read_status();

@@ -1,17 +1,62 @@
-// Sampling with temperature, top-k, top-p and min-p from given random numbers:
-// one CTA a row.
+// Sampling with temperature, top-k, top-p and min-p from given random numbers.
 //
-// The three filters keep a beginning of the row's order (falling z, equal ones
-// by rising index), so what they keep together is one cut: the tokens whose
-// order-preserving key is above the cut's, and the first `ties` of those whose
-// key equals it.  Keys and counts are integers, and sums are added in a fixed
-// order, so a row's token does not depend on timing.
+// With z = l / T, the three filters keep a beginning of the row's order each
+// (falling z, equal ones by rising index), so together they keep one beginning,
+// and the token drawn is the kept one with the largest z - log noise.  No row
+// is ever sorted whole:
+//
+//   1. sample_stats_kernel, S CTAs a row: the row's maximum and sum of
+//      exponentials, and, where no filter is on, the race itself: one pass over
+//      logits and noise, joined by the row's last CTA;
+//   2. sample_pick_kernel, S CTAs a row, where filters may be on: what can be
+//      kept is cut down to candidates without knowing the order -- top-k by the
+//      k-th largest of the threads' own maxima (k tokens at least are that
+//      large), top-p by the weight below which all the row's tokens together
+//      are less than (1 - p) of the sum, min-p by its own bound -- and
+//      collected in a list of the row;
+//   3. the row's last CTA sorts up to kList candidates and settles the cuts and
+//      the race there.  Only their random numbers are read;
+//   4. with more candidates (a flat row) it counts them in bins, which bounds
+//      where the cuts fall; tokens above are kept for certain and take part in
+//      the race as they are read, their weights summed; only the tokens around
+//      the cuts are collected and sorted;
+//   5. where even those are more than kList (thousands of equal logits), it
+//      finds the cuts by bisection over order-preserving keys.
+//
+// Bound: HBM for many rows (every logit once; the passes after the first find
+// them in L2), launches and the chain of passes for few.
+//
+// Sums are added in an order that depends on the sizes alone, and the sort
+// makes the order of collection irrelevant, so a row's token and logprob do
+// not depend on timing.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace w4a16 {
 
-constexpr int kSampleThreads = 1024;
+constexpr int kStatThreads = 1024, kPickThreads = 512;
+constexpr int kList = 2048;   // candidates that are sorted
+constexpr int kBins = 4096;   // of the histogram of a flat row
+constexpr int kMaxSplits = 8; // CTAs a row
+constexpr float kBig = 3.402823466e38f;
+constexpr float kLog2E = 1.4426950408889634f;
+// the rows' arrival counters in the workspace's counter area, behind the attention kernels'
+constexpr int kSampleCounters = 4096, kSampleSplitRows = 4096;
+
+// What a CTA leaves of its slice after the first pass, and its part of the race.
+struct SliceStats {
+    float lmax, sum, tau, best;
+    int imax, ibest, pad[2];
+};
+// A row's part of the workspace.
+struct RowSpace {
+    SliceStats stats[kMaxSplits];
+    int found, pad[3];            // candidates collected (may exceed kList)
+    uint32_t key[kList];          // candidates: keys of z, all bits turned (rising key is falling z)
+    int index[kList];
+};
 
 // order-preserving map of f32 to unsigned (no NaN): a < b <=> key(a) < key(b)
 W4A16_DEVICE uint32_t key_of(float z) {
@@ -20,186 +65,717 @@ W4A16_DEVICE uint32_t key_of(float z) {
 }
 W4A16_DEVICE float value_of(uint32_t k) { return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k); }
 
+// a logit as f32: NaN counts as -inf, +inf as the largest finite value, -0 as 0
+W4A16_DEVICE float clean(float x) { return fminf(fmaxf(x, -INFINITY), kBig) + 0.f; }
 template <int DT>
-W4A16_DEVICE float load_logit(const void* row, int i) {
-    if constexpr (DT == W4A16_F32) return __ldg(static_cast<const float*>(row) + i);
-    const uint16_t b = __ldg(static_cast<const uint16_t*>(row) + i);
-    if constexpr (DT == W4A16_BF16) return __uint_as_float((uint32_t)b << 16);
-    return f16_bits_to_f32(b);
+W4A16_DEVICE float decode(uint32_t bits) {
+    if constexpr (DT == W4A16_F32) return clean(__uint_as_float(bits));
+    if constexpr (DT == W4A16_BF16) return clean(__uint_as_float(bits << 16));
+    return clean(f16_bits_to_f32((uint16_t)bits));
+}
+// z of a cleaned logit: the f32 quotient, at most the largest finite value
+W4A16_DEVICE float z_of(float l, float t) { return fminf(__fdiv_rn(l, t), kBig) + 0.f; }
+
+W4A16_DEVICE float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+W4A16_DEVICE float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// z of a logit: NaN counts as -inf, +inf as the largest finite value; -0 as 0
-W4A16_DEVICE float z_of(float x, float t) {
-    const float z = __fdiv_rn(x, t);
-    return z != z ? -INFINITY : fminf(z, 3.402823466e38f) + 0.f;
-}
-
-struct Red {
-    float f[32];
-    int i[32];
-};
-// sum / maximum over the CTA, the same value in every thread, added in a fixed order
-W4A16_DEVICE float cta_sum(float x, Red& r) {
+// ---- reductions over the CTA, in a fixed order --------------------------------
+template <int NT>
+W4A16_DEVICE float cta_sum(float x, float* f) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) r.f[threadIdx.x >> 5] = x;
+    if (lane == 0) f[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = r.f[threadIdx.x & 31];
+    x = lane < NT / 32 ? f[lane] : 0.f;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
-W4A16_DEVICE int cta_sum(int x, Red& r) {
+template <int NT>
+W4A16_DEVICE int cta_count(int x, int* n) {
+    const int lane = threadIdx.x & 31;
     x = __reduce_add_sync(0xffffffffu, x);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) r.i[threadIdx.x >> 5] = x;
+    if (lane == 0) n[threadIdx.x >> 5] = x;
     __syncthreads();
-    return __reduce_add_sync(0xffffffffu, r.i[threadIdx.x & 31]);
+    return __reduce_add_sync(0xffffffffu, lane < NT / 32 ? n[lane] : 0);
 }
-// the largest x, and among equal ones the lowest index
-W4A16_DEVICE void cta_best(float& x, int& i, Red& r) {
-    auto join = [&](float y, int j) {
-        if (y > x || (y == x && j < i)) {
-            x = y;
-            i = j;
-        }
-    };
+// the larger x, and of equal ones the lower index
+W4A16_DEVICE void join_best(float& x, int& i, float y, int j) {
+    if (y > x || (y == x && j < i)) {
+        x = y;
+        i = j;
+    }
+}
+template <int NT>
+W4A16_DEVICE void cta_best(float& x, int& i, float* f, int* n) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) join(__shfl_xor_sync(0xffffffffu, x, d), __shfl_xor_sync(0xffffffffu, i, d));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        r.f[threadIdx.x >> 5] = x;
-        r.i[threadIdx.x >> 5] = i;
+    for (int d = 16; d > 0; d >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, x, d);
+        const int j = __shfl_xor_sync(0xffffffffu, i, d);
+        join_best(x, i, y, j);
     }
     __syncthreads();
-    x = r.f[threadIdx.x & 31];
-    i = r.i[threadIdx.x & 31];
+    if (lane == 0) {
+        f[threadIdx.x >> 5] = x;
+        n[threadIdx.x >> 5] = i;
+    }
+    __syncthreads();
+    x = lane < NT / 32 ? f[lane] : -INFINITY;
+    i = lane < NT / 32 ? n[lane] : 0x7fffffff;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) join(__shfl_xor_sync(0xffffffffu, x, d), __shfl_xor_sync(0xffffffffu, i, d));
+    for (int d = 16; d > 0; d >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, x, d);
+        const int j = __shfl_xor_sync(0xffffffffu, i, d);
+        join_best(x, i, y, j);
+    }
+}
+// sum over the threads before this one
+W4A16_DEVICE float cta_before(float x, float* f) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float s = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) f[warp] = s;
+    __syncthreads();
+    float w = lane < warp ? f[lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+    const float before = __shfl_up_sync(0xffffffffu, s, 1);
+    return w + (lane ? before : 0.f);
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kSampleThreads) sample_kernel(const w4a16_sample_args p) {
-    __shared__ Red red;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int r = blockIdx.x, V = p.vocab;
-    const void* row = DT == W4A16_F32 ? (const void*)(static_cast<const float*>(p.logits) + r * p.logits_row)
-                                      : (const void*)(static_cast<const uint16_t*>(p.logits) + r * p.logits_row);
-    const float* noise = p.noise + r * p.noise_row;
-    const float temp = p.temperature ? p.temperature[r] : 1.f;
-    const bool greedy = !(temp > 0.f);
-    const float t = greedy ? 1.f : temp;
-    auto z_at = [&](int i) { return z_of(load_logit<DT>(row, i), t); };
+// ---- a CTA's slice of a row ----------------------------------------------------
+template <int DT, int NT>
+struct Slice {
+    static constexpr int VE = DT == W4A16_F32 ? 4 : 8;  // logits of a 16-byte load
+    using El = typename std::conditional<DT == W4A16_F32, uint32_t, uint16_t>::type;
+    const El* row;
+    int V, head, v0, v1, tail;  // [0, head) and [tail, V) one by one; 16-byte loads v0 .. v1 behind head
+    bool first, last;
 
-    float zmax = -INFINITY;
-    int imax = V;
-    for (int i = threadIdx.x; i < V; i += kSampleThreads) {
-        const float z = z_at(i);
-        if (z > zmax) {
-            zmax = z;
-            imax = i;
+    W4A16_DEVICE Slice(const void* base, int64_t off, int vocab, int rank, int S) {
+        row = static_cast<const El*>(base) + off;
+        V = vocab;
+        head = (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(El));
+        if (head > V) head = V;
+        const int nv = (V - head) / VE;
+        v0 = (int)((int64_t)nv * rank / S);
+        v1 = (int)((int64_t)nv * (rank + 1) / S);
+        tail = head + nv * VE;
+        first = rank == 0;
+        last = rank == S - 1;
+    }
+    W4A16_DEVICE static void split(const uint4& x, float (&l)[VE]) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == W4A16_F32) {
+                l[i] = decode<DT>(w[i]);
+            } else {
+                l[2 * i] = decode<DT>(w[i] & 0xffffu);
+                l[2 * i + 1] = decode<DT>(w[i] >> 16);
+            }
         }
     }
-    cta_best(zmax, imax, red);
-    if (zmax == -INFINITY) {
-        if (threadIdx.x == 0) {
-            p.token[r] = -1;
-            if (p.logprob) p.logprob[r] = -INFINITY;
+    // one(logit, index) for single tokens, many(logits, index of the first) for VE of them: this thread's
+    // tokens, by rising index
+    template <typename One, typename Many>
+    W4A16_DEVICE void each(One one, Many many) const {
+        constexpr int U = 4;
+        if (first && (int)threadIdx.x < head) one(at((int)threadIdx.x), (int)threadIdx.x);
+        const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+        int v = v0 + (int)threadIdx.x;
+        for (; v + (U - 1) * NT < v1; v += U * NT) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = vec[v + u * NT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float l[VE];
+                split(x[u], l);
+                many(l, head + (v + u * NT) * VE);
+            }
         }
+        for (; v < v1; v += NT) {
+            float l[VE];
+            split(vec[v], l);
+            many(l, head + v * VE);
+        }
+        if (last && tail + (int)threadIdx.x < V) one(at(tail + (int)threadIdx.x), tail + (int)threadIdx.x);
+    }
+    template <typename One>
+    W4A16_DEVICE void each(One one) const {
+        each(one, [&](const float (&l)[VE], int i0) {
+#pragma unroll
+            for (int x = 0; x < VE; ++x) one(l[x], i0 + x);
+        });
+    }
+    W4A16_DEVICE float at(int i) const { return decode<DT>(row[i]); }
+};
+
+// A row's parameters.
+struct RowParams {
+    float T, tp, mp, c2;  // temperature, top-p, min-p, log2(e) / T
+    int k;
+    bool greedy, by_k, by_p, by_m, race;
+    W4A16_DEVICE RowParams(const w4a16_sample_args& p, int r) {
+        const float t = p.temperature ? p.temperature[r] : 1.f;
+        greedy = !(t > 0.f);
+        T = greedy ? 1.f : t;
+        c2 = fminf(kLog2E / T, kBig);
+        k = p.top_k ? p.top_k[r] : 0;
+        tp = p.top_p ? p.top_p[r] : 1.f;
+        mp = p.min_p ? p.min_p[r] : 0.f;
+        by_k = !greedy && k > 0 && k < p.vocab;
+        by_p = !greedy && tp < 1.f;
+        by_m = !greedy && mp > 0.f;
+        race = !greedy && !by_k && !by_p && !by_m;
+    }
+};
+
+// The row's token and its log-probability, by one thread.
+template <int DT, int NT>
+W4A16_DEVICE void write_row(const w4a16_sample_args& p, int r, const Slice<DT, NT>& row, const RowParams& q, int token,
+                            int imax, float lmax, float sum) {
+    if (lmax == -INFINITY) {
+        p.token[r] = -1;
+        if (p.logprob) p.logprob[r] = -INFINITY;
         return;
     }
-    float sum = 0.f;
-    for (int i = threadIdx.x; i < V; i += kSampleThreads) sum += expf(z_at(i) - zmax);
-    sum = cta_sum(sum, red);
+    if (token < 0 || token >= p.vocab) token = imax;  // the noise of every kept token was infinite or NaN
+    p.token[r] = token;
+    if (p.logprob) p.logprob[r] = (z_of(row.at(token), q.T) - z_of(lmax, q.T)) - logf(sum);
+}
 
-    int token = imax;
-    if (!greedy) {
-        // the cut: keys above `cut` are kept, and `ties` of those equal to it
-        uint32_t cut = 0;
-        int ties = V;
-        const int k = p.top_k ? p.top_k[r] : 0;
-        auto count = [&](uint32_t c) {  // tokens with a key >= c
-            int n = 0;
-            for (int i = threadIdx.x; i < V; i += kSampleThreads) n += key_of(z_at(i)) >= c;
-            return cta_sum(n, red);
-        };
-        if (k > 0 && k < V) {
-            for (int b = 31; b >= 0; --b)
-                if (count(cut | (1u << b)) >= k) cut |= 1u << b;
-            ties = k - (cut == 0xffffffffu ? 0 : count(cut + 1));
+// The slices' results as one, in slice order.
+struct RowStats {
+    float lmax, sum, tau, best;
+    int imax, ibest;
+    W4A16_DEVICE RowStats(const SliceStats* s, int S, float c2) {
+        lmax = tau = best = -INFINITY;
+        sum = 0.f;
+        imax = ibest = 0x7fffffff;
+        for (int i = 0; i < S; ++i) {
+            join_best(lmax, imax, __ldcg(&s[i].lmax), __ldcg(&s[i].imax));
+            tau = fmaxf(tau, __ldcg(&s[i].tau));
+            join_best(best, ibest, __ldcg(&s[i].best), __ldcg(&s[i].ibest));
         }
-        const float tp = p.top_p ? p.top_p[r] : 1.f;
-        if (tp < 1.f) {
-            // mass of the kept tokens above a key; the ties of the top-k cut share one value
-            const float wcut = expf(value_of(cut) - zmax);
-            auto mass = [&](uint32_t c) {
-                float s = 0.f;
-                for (int i = threadIdx.x; i < V; i += kSampleThreads) {
-                    const float z = z_at(i);
-                    const uint32_t y = key_of(z);
-                    if (y >= c && y > cut) s += expf(z - zmax);
+        for (int i = 0; i < S; ++i) {
+            const float x = __ldcg(&s[i].lmax);
+            if (x != -INFINITY) sum += __ldcg(&s[i].sum) * ex2((x - lmax) * c2);
+        }
+    }
+};
+
+// ---- 1. maximum, sum, and the race of unfiltered rows ---------------------------
+template <int DT>
+__global__ void __launch_bounds__(kStatThreads) sample_stats_kernel(const w4a16_sample_args p, const int S,
+                                                                    const int filters) {
+    constexpr int NT = kStatThreads;
+    __shared__ float rf[32];
+    __shared__ int ri[32];
+    __shared__ int last;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
+    const Slice<DT, NT> slice(p.logits, r * p.logits_row, V, rank, S);
+    const float* noise = p.noise + r * p.noise_row;
+    const RowParams q(p, r);
+    const bool race = q.race;
+    const float inv_t = fminf(1.f / q.T, kBig);
+
+    float mx = -kBig, sum = 0.f, best = -INFINITY;
+    int imax = V, ibest = 0x7fffffff;
+    const bool noise4 = (reinterpret_cast<uintptr_t>(noise + slice.head) & 15) == 0;
+    auto try_race = [&](float l, float e, int i) {
+        // the approximate score decides whether the exact one is worth computing: its error is below
+        // 2^-21 |z| + 2^-20, and |z| <= |score| + 104 for any finite noise
+        const float s = fmaf(l, inv_t, -0.6931471805599453f * lg2(e));
+        if (fmaf(fabsf(s), 4e-6f, s) + 1e-3f > best || e == 0.f) {
+            const float x = z_of(l, q.T) - logf(e);
+            if (x > best && l > -INFINITY) {
+                best = x;
+                ibest = i;
+            }
+        }
+    };
+    auto maximum = [&](float b) {  // a new one; -kBig itself may be the first
+        if (b > mx || (imax == V && b == -kBig)) {
+            sum *= ex2((mx - b) * q.c2);
+            mx = b;
+            return true;
+        }
+        return false;
+    };
+    constexpr int VE = Slice<DT, NT>::VE;
+    slice.each(
+        [&](float l, int i) {
+            if (maximum(l)) imax = i;
+            sum += ex2((l - mx) * q.c2);
+            if (race) try_race(l, noise[i], i);
+        },
+        [&](const float (&l)[VE], int i0) {
+            float b = l[0];
+#pragma unroll
+            for (int x = 1; x < VE; ++x) b = fmaxf(b, l[x]);
+            if (maximum(b)) {
+#pragma unroll
+                for (int x = VE - 1; x >= 0; --x)
+                    if (l[x] == b) imax = i0 + x;
+            }
+            float s = 0.f;
+#pragma unroll
+            for (int x = 0; x < VE; ++x) s += ex2((l[x] - mx) * q.c2);
+            sum += s;
+            if (race) {
+                if (noise4) {
+#pragma unroll
+                    for (int x = 0; x < VE; x += 4) {
+                        const float4 e = *reinterpret_cast<const float4*>(noise + i0 + x);
+                        try_race(l[x], e.x, i0 + x);
+                        try_race(l[x + 1], e.y, i0 + x + 1);
+                        try_race(l[x + 2], e.z, i0 + x + 2);
+                        try_race(l[x + 3], e.w, i0 + x + 3);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < VE; ++x) try_race(l[x], noise[i0 + x], i0 + x);
                 }
-                return cta_sum(s, red) + (c <= cut && cut != 0 ? ties * wcut : 0.f);
-            };
-            const float want = tp * mass(cut);
-            // the largest key at and above which the kept mass reaches `want`
-            uint32_t lo = cut, hi = key_of(zmax);
+            }
+        });
+    const float mine = imax < V ? mx : -INFINITY;  // this thread's largest logit
+    float lmax = mine;
+    cta_best<NT>(lmax, imax, rf, ri);
+    sum = cta_sum<NT>(mine == -INFINITY ? 0.f : sum * ex2((mine - lmax) * q.c2), rf);
+    if (race) cta_best<NT>(best, ibest, rf, ri);
+    // k tokens of this slice at least are as large as the k-th largest of its threads' maxima
+    float tau = -INFINITY;
+    if (q.by_k && q.k <= NT / 2) {
+        uint32_t lo = key_of(-INFINITY), hi = key_of(lmax);
+        const uint32_t y = key_of(mine);
+        for (int b = 0; b < 16 && lo < hi; ++b) {
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            if (__syncthreads_count(y >= mid) >= q.k) lo = mid; else hi = mid - 1;
+        }
+        tau = value_of(lo);
+    }
+    RowSpace* space = reinterpret_cast<RowSpace*>(static_cast<char*>(p.workspace) + kCounterBytes) + r;
+    const bool settled = race || q.greedy;  // nothing is left for the second kernel
+    if (S == 1 && (settled || !filters)) {
+        if (threadIdx.x == 0) write_row<DT, NT>(p, r, slice, q, q.greedy ? imax : ibest, imax, lmax, sum);
+        if (!filters) return;
+    }
+    if (threadIdx.x == 0) {
+        SliceStats* s = space->stats + rank;
+        s->lmax = lmax;
+        s->sum = sum;
+        s->tau = tau;
+        s->best = best;
+        s->imax = imax;
+        s->ibest = ibest;
+        if (rank == 0) space->found = 0;
+    }
+    if (S == 1 || !settled) return;
+    // the row's last CTA joins the slices
+    __threadfence();
+    if (threadIdx.x == 0) {
+        unsigned* counter = static_cast<unsigned*>(p.workspace) + kSampleCounters + r;
+        last = atomicAdd(counter, 1u) == (unsigned)(S - 1);
+        if (last) *counter = 0;
+    }
+    __syncthreads();
+    if (last && threadIdx.x == 0) {
+        __threadfence();
+        const RowStats a(space->stats, S, q.c2);
+        write_row<DT, NT>(p, r, slice, q, q.greedy ? a.imax : a.ibest, a.imax, a.lmax, a.sum);
+    }
+}
+
+// the candidate list, by rising key and then by rising index: bitonic, n a power of two
+template <int NT>
+W4A16_DEVICE void sort_list(uint32_t* key, int* idx, int n) {
+    for (int k = 2; k <= n; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            __syncthreads();
+            for (int t = threadIdx.x; t < n / 2; t += NT) {
+                const int a = 2 * t - (t & (j - 1)), b = a + j;
+                const uint32_t x = key[a], y = key[b];
+                const int u = idx[a], v = idx[b];
+                if ((x > y || (x == y && u > v)) == ((a & k) == 0)) {
+                    key[a] = y;
+                    key[b] = x;
+                    idx[a] = v;
+                    idx[b] = u;
+                }
+            }
+        }
+    __syncthreads();
+}
+
+// ---- 2. to 5. filtered rows ------------------------------------------------------
+template <int DT>
+__global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a16_sample_args p, const int S) {
+    constexpr int NT = kPickThreads;
+    __shared__ float rf[32];
+    __shared__ int ri[32];
+    __shared__ uint32_t list_z[kList];
+    __shared__ int list_i[kList];
+    __shared__ int hist[kBins];
+    __shared__ int win[8];    // windows of bins (two), tokens above and between, list length, last arrival
+    __shared__ float bound[2];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
+    const RowParams q(p, r);
+    if (q.race || q.greedy) return;
+    RowSpace* space = reinterpret_cast<RowSpace*>(static_cast<char*>(p.workspace) + kCounterBytes) + r;
+    const RowStats st(space->stats, S, q.c2);
+    const float T = q.T, lmax = st.lmax, sum = st.sum;
+    const float* noise = p.noise + r * p.noise_row;
+    const Slice<DT, NT> slice(p.logits, r * p.logits_row, V, rank, S), row(p.logits, r * p.logits_row, V, 0, 1);
+    if (lmax == -INFINITY) {
+        if (rank == 0 && threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, -1, -1, lmax, sum);
+        return;
+    }
+    const float zmax = z_of(lmax, T);
+    const float least = q.by_m ? fminf(logf(q.mp), 0.f) : -INFINITY;  // of z - zmax
+    float best = -INFINITY;
+    int ibest = 0x7fffffff;
+    auto score = [&](float z, int i) {
+        if (!(z - zmax >= least)) return;
+        const float x = z - logf(noise[i]);
+        if (x > best || (x == best && i < ibest)) {
+            best = x;
+            ibest = i;
+        }
+    };
+    auto weight = [&](float z) { return ex2((z - zmax) * kLog2E); };
+    const bool alone = !q.by_k && !q.by_p;  // min-p alone: its bound is known
+
+    // ---- 2. candidates: logits >= low
+    // top-p: tokens with z < zmax - R weigh less than V e^-R = (1 - p) sum e^-0.02 together
+    float R = 40.f;
+    if (q.by_p && !q.by_k) R = fminf(fmaxf(logf((float)V / ((1.f - q.tp) * sum)), 0.f) + 0.02f, 80.f);
+    float low = lmax - R * T * 1.0001f;
+    bool listed = q.by_p && !q.by_k;  // whether the candidates may be few
+    if (q.by_k && st.tau != -INFINITY) {
+        low = st.tau;
+        listed = true;
+    }
+    if (V <= kList) {
+        low = -kBig;
+        listed = true;
+    }
+    if (alone) {
+        const float floor_l = (zmax + least) * T - fabsf(zmax * T) * 1e-5f - 1e-5f;  // no token below it passes
+        slice.each([&](float l, int i) {
+            if (l >= floor_l && l > -INFINITY) score(z_of(l, T), i);
+        });
+        cta_best<NT>(best, ibest, rf, ri);
+        if (threadIdx.x == 0) {
+            space->stats[rank].best = best;
+            space->stats[rank].ibest = ibest;
+        }
+    } else if (listed) {
+        bool full = false;  // a list that has overflowed takes no more from this thread
+        slice.each([&](float l, int i) {
+            if (l >= low && l > -INFINITY && !full) {
+                const int at = atomicAdd(&space->found, 1);
+                if (at < kList) {
+                    space->key[at] = ~key_of(z_of(l, T));
+                    space->index[at] = i;
+                } else {
+                    full = true;
+                }
+            }
+        });
+    }
+    // ---- the row's last CTA goes on
+    if (S > 1) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            unsigned* counter = static_cast<unsigned*>(p.workspace) + kSampleCounters + r;
+            win[7] = atomicAdd(counter, 1u) == (unsigned)(S - 1);
+            if (win[7]) *counter = 0;
+        }
+        __syncthreads();
+        if (!win[7]) return;
+        __threadfence();
+    } else {
+        __syncthreads();
+    }
+    if (alone) {
+        const RowStats a(space->stats, S, q.c2);
+        if (threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, a.ibest, a.imax, lmax, sum);
+        return;
+    }
+    int n = listed ? __ldcg(&space->found) : kList + 1;
+    if (n <= kList) {
+        for (int i = threadIdx.x; i < n; i += NT) {
+            list_z[i] = __ldcg(space->key + i);
+            list_i[i] = __ldcg(space->index + i);
+        }
+    }
+    const int k = q.k;
+    int above = 0, between = 0;        // tokens above the windows around the cuts, and between them
+    float mass_a = 0.f, mass_b = 0.f;  // their weights
+    bool slow = false;
+    if (n > kList) {
+        // ---- 4. too many: bins of equal width in l, from the maximum down
+        for (int i = threadIdx.x; i < kBins; i += NT) hist[i] = 0;
+        if (threadIdx.x == 0) win[6] = 0;
+        const float width = fmaxf((lmax - low) * 1.0001f, 1e-30f);
+        // no bin narrower than 4 units in the last place of a logit: equal z lie in one bin or in two neighbours
+        const float scale = fminf((kBins - 3) / width, 2097152.f / fmaxf(fmaxf(fabsf(lmax), fabsf(low)), 1e-30f));
+        // round((lmax - l) scale), by adding 2^23: never rising with l
+        auto bin_of = [&](float l) {
+            return (int)(__float_as_uint(fminf((lmax - l) * scale, (float)(kBins - 1)) + 8388608.f) & 0x7fffffu);
+        };
+        __syncthreads();
+        row.each([&](float l, int) {
+            if (l >= low && l > -INFINITY) atomicAdd(&hist[bin_of(l)], 1);
+        });
+        __syncthreads();
+        // thread: PB bins; sums of counts, and of least and greatest weights, before them
+        constexpr int PB = kBins / NT;
+        const int base = threadIdx.x * PB;
+        const float step = q.c2 / scale;  // of the exponent, base 2, a bin
+        float cnt[PB], lo[PB], up[PB], ct = 0.f, lt = 0.f, ut = 0.f;
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            cnt[i] = (float)hist[base + i];  // at most 2^24: exact
+            lo[i] = cnt[i] * ex2(-((float)(base + i) + 0.51f) * step);
+            up[i] = cnt[i] * ex2(fminf(-((float)(base + i) - 0.51f) * step, 0.f));
+            ct += cnt[i];
+            lt += lo[i];
+            ut += up[i];
+        }
+        const float cb = cta_before(ct, rf), lb = cta_before(lt, rf), ub = cta_before(ut, rf);
+        if (threadIdx.x == 0) {
+            win[0] = win[1] = win[2] = kBins;
+            bound[0] = bound[1] = 0.f;
+        }
+        __syncthreads();
+        if (q.by_k) {  // the bin in which the k-th token lies
+            float c = cb, a = lb, u = ub;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                if (c < (float)k && c + cnt[i] >= (float)k) {
+                    win[2] = base + i;
+                    bound[0] = a;          // the kept weight is at least this
+                    bound[1] = u + up[i];  // and at most this
+                }
+                c += cnt[i], a += lo[i], u += up[i];
+            }
+        }
+        __syncthreads();
+        const int bk = win[2];
+        if (q.by_p) {
+            const float t_lo = q.tp * (q.by_k ? bound[0] : sum) * 0.9999f;
+            const float t_up = q.tp * (q.by_k ? bound[1] : sum) * 1.0001f;
+            float a = lb, u = ub;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                u += up[i];
+                a += lo[i];
+                if (u >= t_lo) atomicMin(&win[0], base + i);  // the cut is in this bin or below
+                if (a >= t_up) atomicMin(&win[1], base + i);  // in this bin or above
+            }
+        }
+        __syncthreads();
+        int b1 = win[0], b2 = win[1];
+        slow = (q.by_k && bk >= kBins - 1) || (q.by_p && (q.by_k ? b1 : b2) >= kBins - 1);
+        // equal z may have unequal l, one bin apart at most: a bin more on each side
+        if (q.by_k && b2 > bk) b2 = bk;
+        if (!q.by_p) b1 = b2 = bk;
+        b1 = max(b1 - 1, 0);
+        b2 = min(b2 + 1, kBins - 1);
+        int bk1 = q.by_k ? max(bk - 1, 0) : kBins, bk2 = q.by_k ? min(bk + 1, kBins - 1) : kBins - 1;
+        if (q.by_k && bk1 <= b2 + 1) {  // one window
+            b2 = bk2;
+            bk1 = kBins;
+        }
+        const bool apart = bk1 < kBins;
+        if (!slow) {
+            int ca = 0, cc = 0;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int b = base + i;
+                if (b < b1) ca += (int)cnt[i];
+                if (apart && b > b2 && b < bk1) cc += (int)cnt[i];
+            }
+            above = cta_count<NT>(ca, ri);
+            between = cta_count<NT>(cc, ri);
+            row.each([&](float l, int i) {
+                if (!(l >= low && l > -INFINITY)) return;
+                const int b = bin_of(l);
+                if (b < b1) {
+                    const float z = z_of(l, T);
+                    mass_a += weight(z);
+                    score(z, i);
+                } else if (b <= b2 || (apart && b >= bk1 && b <= bk2)) {
+                    const int at = atomicAdd(&win[6], 1);
+                    if (at < kList) {
+                        list_z[at] = ~key_of(z_of(l, T));
+                        list_i[at] = i;
+                    }
+                } else if (apart && b < bk1) {
+                    mass_b += weight(z_of(l, T));
+                }
+            });
+            mass_a = cta_sum<NT>(mass_a, rf);
+            mass_b = cta_sum<NT>(mass_b, rf);
+            n = win[6];
+            slow = n > kList;
+        }
+    }
+    if (!slow) {
+        // ---- 3. the list decides
+        int size = 1;
+        while (size < n) size <<= 1;
+        for (int i = n + (int)threadIdx.x; i < size; i += NT) {
+            list_z[i] = 0xffffffffu;
+            list_i[i] = 0x7fffffff;
+        }
+        sort_list<NT>(list_z, list_i, size);
+        constexpr int PL = kList / NT;
+        const int base = threadIdx.x * PL;
+        // entries that top-k keeps (a second window lies behind `between` tokens)
+        const int kept_k = q.by_k ? min(n, k - above - between) : n;
+        float w[PL], wt = 0.f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            w[i] = base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
+            wt += w[i];
+        }
+        const float before = cta_before(wt, rf);
+        float total = sum;
+        if (q.by_k) total = mass_a + mass_b + cta_sum<NT>(wt, rf);
+        const float want = q.by_p ? q.tp * total : INFINITY;
+        float at = mass_a + before;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            if (base + i < kept_k && (!q.by_p || at < want || (above == 0 && base + i == 0)))
+                score(value_of(~list_z[base + i]), list_i[base + i]);
+            at += w[i];
+        }
+        cta_best<NT>(best, ibest, rf, ri);
+    } else {
+        // ---- 5. bisection
+        best = -INFINITY, ibest = 0x7fffffff;
+        uint32_t cut = 0;  // keys above it are kept, and `ties` of those equal to it
+        int ties = V;
+        auto count = [&](uint32_t c) {
+            int m = 0;
+            row.each([&](float l, int) { m += key_of(z_of(l, T)) >= c; });
+            return cta_count<NT>(m, ri);
+        };
+        if (q.by_k) {
+            uint32_t lo = 0, hi = key_of(zmax);
             while (lo < hi) {
+                const uint32_t mid = lo + (hi - lo + 1) / 2;
+                if (count(mid) >= k) lo = mid; else hi = mid - 1;
+            }
+            cut = lo;
+            ties = k - count(cut + 1);
+        }
+        if (q.by_p) {
+            const float wcut = weight(value_of(cut));
+            const uint32_t top = cut;
+            const int top_ties = ties;
+            auto mass = [&](uint32_t c) {  // weight of the kept tokens with a key >= c
+                float s = 0.f;
+                row.each([&](float l, int) {
+                    const float z = z_of(l, T);
+                    const uint32_t y = key_of(z);
+                    if (y >= c && y > top) s += weight(z);
+                });
+                return cta_sum<NT>(s, rf) + (q.by_k && c <= top ? (float)top_ties * wcut : 0.f);
+            };
+            const float want = q.tp * mass(top);
+            uint32_t lo = top, hi = key_of(zmax);
+            while (lo < hi) {  // the largest key at and above which the weight reaches `want`
                 const uint32_t mid = lo + (hi - lo + 1) / 2;
                 if (mass(mid) >= want) lo = mid; else hi = mid - 1;
             }
-            const uint32_t c = lo;
-            const float above = c == 0xffffffffu ? 0.f : mass(c + 1), w = expf(value_of(c) - zmax);
-            int n = c == cut ? ties : count(c) - count(c + 1);
-            int keep = 1;
-            while (keep < n && above + keep * w < want) ++keep;
-            cut = c;
-            ties = keep;
-        }
-        const float mp = p.min_p ? p.min_p[r] : 0.f;
-        const float least = mp > 0.f ? fminf(logf(mp), 0.f) : -INFINITY;
-        // the index below which the ties of the cut are kept
-        int end = V;
-        {
-            int lo = 0, hi = V;  // the smallest end with at least `ties` ties before it
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                int n = 0;
-                for (int i = threadIdx.x; i < mid; i += kSampleThreads) n += key_of(z_at(i)) == cut;
-                if (cta_sum(n, red) >= ties) hi = mid; else lo = mid + 1;
+            const float over = mass(lo + 1), wt = weight(value_of(lo));
+            const int here = q.by_k && lo == top ? top_ties : count(lo) - count(lo + 1);
+            cut = lo;
+            ties = 1;
+            if (wt > 0.f && over + wt < want) {  // tie i stays while over + i wt < want
+                int a = 1, b = here;
+                while (a < b) {
+                    const int mid = (a + b) / 2;
+                    if (over + (float)mid * wt < want) a = mid + 1; else b = mid;
+                }
+                ties = a;
             }
-            end = lo;
         }
-        float best = -INFINITY;
-        token = V;
-        for (int i = threadIdx.x; i < V; i += kSampleThreads) {
-            const float z = z_at(i);
+        int lo = 0, hi = V;  // the smallest end with `ties` ties before it
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            int m = 0;
+            row.each([&](float l, int i) { m += i < mid && key_of(z_of(l, T)) == cut; });
+            if (cta_count<NT>(m, ri) >= ties) hi = mid; else lo = mid + 1;
+        }
+        row.each([&](float l, int i) {
+            const float z = z_of(l, T);
             const uint32_t y = key_of(z);
-            if (z == -INFINITY || y < cut || (y == cut && i >= end) || !(z - zmax >= least)) continue;
-            const float score = z - logf(noise[i]);
-            if (score > best || (score == best && i < token)) {
-                best = score;
-                token = i;
-            }
-        }
-        cta_best(best, token, red);
-        if (token >= V) token = imax;  // every noise of the kept tokens was infinite or NaN
+            if (l > -INFINITY && (y > cut || (y == cut && i < lo))) score(z, i);
+        });
+        cta_best<NT>(best, ibest, rf, ri);
     }
-    if (threadIdx.x == 0) {
-        p.token[r] = token;
-        if (p.logprob) p.logprob[r] = (z_at(token) - zmax) - logf(sum);
-    }
+    if (threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, ibest, st.imax, lmax, sum);
 }
 
-cudaError_t launch_sample(const w4a16_sample_args& a, int, cudaStream_t s) {
+// CTAs a row: as many as keep the SMs at up to two CTAs each, slices of 4096 tokens at least
+static int splits_of(int rows, int vocab, int sms) {
+    int S = kMaxSplits;
+    while (S > 1 && ((int64_t)rows * S > 2 * sms || vocab / S < 4096)) S >>= 1;
+    return rows > kSampleSplitRows ? 1 : S;
+}
+
+size_t sample_workspace(int rows, int vocab, bool filters, int sms) {
+    if (!filters && splits_of(rows, vocab, sms) == 1) return 0;
+    return kCounterBytes + (size_t)rows * sizeof(RowSpace);
+}
+
+template <int DT>
+static cudaError_t launch(const w4a16_sample_args& a, int S, cudaStream_t s) {
     const bool pdl = (a.flags & W4A16_FLAG_PDL) != 0;
-    const dim3 grid((unsigned)a.rows), block(kSampleThreads);
+    const int filters = a.top_k || a.top_p || a.min_p;
+    const dim3 grid((unsigned)S, (unsigned)a.rows);
+    cudaError_t e = launch_kernel(sample_stats_kernel<DT>, grid, dim3(kStatThreads), 0, s, pdl, a, S, filters);
+    if (e != cudaSuccess) return e;
     note_launch();
-    if (a.dtype == W4A16_F32) return launch_kernel(sample_kernel<W4A16_F32>, grid, block, 0, s, pdl, a);
-    if (a.dtype == W4A16_BF16) return launch_kernel(sample_kernel<W4A16_BF16>, grid, block, 0, s, pdl, a);
-    return launch_kernel(sample_kernel<W4A16_F16>, grid, block, 0, s, pdl, a);
+    if (!filters) return cudaSuccess;
+    e = launch_kernel(sample_pick_kernel<DT>, grid, dim3(kPickThreads), 0, s, pdl, a, S);
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+cudaError_t launch_sample(const w4a16_sample_args& a, int sms, cudaStream_t s) {
+    const int S = splits_of(a.rows, a.vocab, sms);
+    if (a.dtype == W4A16_F32) return launch<W4A16_F32>(a, S, s);
+    if (a.dtype == W4A16_BF16) return launch<W4A16_BF16>(a, S, s);
+    return launch<W4A16_F16>(a, S, s);
 }
 
 }  // namespace w4a16

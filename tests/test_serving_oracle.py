@@ -175,8 +175,8 @@ def test_attention_refusals(w):
 
 
 def test_sample_refusals(w):
-    order = fields("logits noise temperature top_k top_p min_p token logprob lrow nrow R V dtype flags")
-    base = dict(zip(order, PTR[:8] + [1000, 1000, 4, 1000, 0, 1]))
+    order = fields("logits noise temperature top_k top_p min_p token logprob ws ws_bytes lrow nrow R V dtype flags")
+    base = dict(zip(order, PTR[:9] + [1 << 20, 1000, 1000, 4, 1000, 0, 1]))
     do = lambda **c: call(w, "w4a16_sample", w._SAMPLE_ARGS, order, base, **c)  # noqa: E731
     for p in ("logits", "noise", "token"):
         assert do(**{p: 0}) == w.W4A16_EINVAL, p
@@ -189,6 +189,6 @@ def test_sample_refusals(w):
 
 
 def test_argument_structs_have_the_headers_sizes(w):
-    assert [s.size for s in (w._PLAN_ARGS, w._WRITE_ARGS, w._ATTN_ARGS, w._SAMPLE_ARGS)] == [104, 152, 224, 96]
+    assert [s.size for s in (w._PLAN_ARGS, w._WRITE_ARGS, w._ATTN_ARGS, w._SAMPLE_ARGS)] == [104, 152, 224, 112]
     for s in (w._PLAN_ARGS, w._WRITE_ARGS, w._ATTN_ARGS, w._SAMPLE_ARGS):
         assert s.size % ctypes.sizeof(ctypes.c_void_p) == 0
