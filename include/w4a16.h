@@ -445,7 +445,8 @@ int w4a16_kv_write(const w4a16_kv_write_args *args, w4a16_stream_t stream);
  * infinities included.  Rows t >= q_start[requests] are not written.
  *
  *   dtype       bf16 or fp16, one for q, k, v and out
- *   head_dim    64 or 128;  q_heads % kv_heads == 0, q_heads / kv_heads <= 64
+ *   head_dim    64 or 128;  q_heads % kv_heads == 0, q_heads / kv_heads <= 64;
+ *               requests <= 16384
  *   max_q       at least every n_b (a tighter bound gives a better grid): the
  *               result is undefined for a request with more new tokens
  *   strides     elements, multiples of 8; pointers 16-byte aligned (lse and

@@ -119,7 +119,7 @@ int w4a16_kv_write(const w4a16_kv_write_args* a, w4a16_stream_t stream) {
 
 static int check_paged_sizes(int tokens, int requests, int Hq, int Hkv, int d, int max_q) {
     if (tokens < 0 || requests < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 0) return W4A16_EINVAL;
-    if ((d != 64 && d != 128) || Hq / Hkv > 64 || Hq > 65535 || requests > 65535 ||
+    if ((d != 64 && d != 128) || Hq / Hkv > 64 || Hq > 65535 || requests > kPlanMaxRequests ||
         (int64_t)tokens * Hq >= (1ll << 31))
         return W4A16_EUNSUPPORTED;
     return W4A16_OK;

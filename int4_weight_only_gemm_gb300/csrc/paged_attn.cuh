@@ -33,6 +33,8 @@ struct Bf16 {
     static constexpr uint32_t idesc_type = 1;  // of kind::f16 operands
     W4A16_DEVICE static float lo(uint32_t v) { return bf16lo(v); }
     W4A16_DEVICE static float hi(uint32_t v) { return bf16hi(v); }
+    // bit 15 or 31 is set where that half is an infinity or NaN (its exponent bits are all ones)
+    W4A16_DEVICE static uint32_t all_ones(uint32_t v) { return (v & 0x7f807f80u) + 0x00800080u; }
     W4A16_DEVICE static uint32_t pack(float a, float b) {  // a in the low half
         uint32_t r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -43,6 +45,7 @@ struct F16 {
     static constexpr uint32_t idesc_type = 0;
     W4A16_DEVICE static float lo(uint32_t v) { return f16_bits_to_f32((uint16_t)v); }
     W4A16_DEVICE static float hi(uint32_t v) { return f16_bits_to_f32((uint16_t)(v >> 16)); }
+    W4A16_DEVICE static uint32_t all_ones(uint32_t v) { return (v & 0x7c007c00u) + 0x04000400u; }
     W4A16_DEVICE static uint32_t pack(float a, float b) {
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));

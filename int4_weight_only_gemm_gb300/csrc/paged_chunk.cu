@@ -10,8 +10,10 @@
 // left (a draft block, the end of a chunk) the two softmax warpgroups take
 // turns on the key tiles of the same rows instead, and join their sums.
 //
-//   * warp 9 copies Q and the pages of the key / value tiles into shared memory
-//     (one 128-byte-swizzled box a page and 64 columns), a ring of tiles;
+//   * warp 9 copies the pages of the key / value tiles into a ring in shared
+//     memory (one 128-byte-swizzled box a page and 64 columns), warp 10 the Q
+//     tiles, so that an item's first keys are on their way before the last
+//     item's queries are done with;
 //   * warp 8 issues the MMAs: S = Q K^T from shared memory (128 x 128 x D, f32
 //     in tensor memory), O += P V with P from tensor memory (over S) and V in
 //     the layout it has in the cache (its columns are contiguous: MN-major);
@@ -44,7 +46,7 @@ namespace w4a16 {
 
 static __device__ int g_chunk_status;
 
-constexpr int kChThreads = 320;  // two softmax warpgroups, the MMA warp and the copy warp
+constexpr int kChThreads = 352;  // two softmax warpgroups, the MMA warp, the key / value and the query copy warp
 constexpr int kChKeys = 128;
 constexpr int kChTwo = 256;  // rows that see fewer positions carry their weights in two parts
 constexpr int kChCounters = 1024;  // first arrival counter of this kernel (the small-row kernel's lie below)
@@ -126,29 +128,30 @@ W4A16_DEVICE void tmem_ld32(uint32_t taddr, uint32_t* v) {
         : "memory");
 }
 
-// ---- the line of key tiles --------------------------------------------------
-// sum over i < n of floor((a i + b) / m), by the Euclid-like recursion on (a, m)
-W4A16_DEVICE int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    int64_t s = 0;
-    while (true) {
-        if (a >= m) {
-            s += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2);
-            a %= m;
-        }
-        if (b >= m) {
-            s += (int64_t)(b / m) * n;
-            b %= m;
-        }
-        const uint64_t y = (uint64_t)a * n + b;
-        if (y < m) return s;
-        n = (uint32_t)(y / m);
-        b = (uint32_t)(y - (uint64_t)n * m);
-        const uint32_t t = m;
-        m = a;
-        a = t;
-    }
+W4A16_DEVICE float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// two f32 operations in one instruction
+W4A16_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+W4A16_DEVICE float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
+// ---- the line of key tiles --------------------------------------------------
 struct ChunkItem {
     int i0, tokens;      // first token (of the request) and their number
     int e0, e1;          // last position that the first and the last token see
@@ -170,27 +173,6 @@ W4A16_DEVICE ChunkItem item_of(const PagedAttnParams& p, const Request& r, int q
 W4A16_DEVICE int items_of(const PagedAttnParams& p, const Request& r, int span) {
     return r.n * p.G <= p.small_rows ? 0 : (r.n + span - 1) / span;
 }
-// key tiles of the first k items of a request, for one key head
-W4A16_DEVICE int64_t tiles_before(const PagedAttnParams& p, const Request& r, int span, int k) {
-    if (k == 0) return 0;
-    if (p.block || r.L < r.n) {
-        if (p.block) return (int64_t)k * item_of(p, r, 0, span).tiles;
-        int64_t s = 0;
-        for (int q = 0; q < k; ++q) s += item_of(p, r, q, span).tiles;
-        return s;
-    }
-    const int base = r.L - r.n;
-    const int full = min(k, r.n / span);  // items that end before or at a whole span
-    int64_t s = floor_sum(full, kChKeys, span, base + span - 1) + full;
-    if (k > full) s += (r.L - 1) / kChKeys + 1;
-    if (p.window > 0) {
-        const int x = base - p.window + 1;            // item q starts at x + q span where that is positive
-        const int q0 = x > 0 ? 0 : (-x) / span + 1;
-        if (k > q0) s -= floor_sum(k - q0, kChKeys, span, x + q0 * span);
-    }
-    return s;
-}
-
 struct ChunkPiece {
     Request r;
     ChunkItem it;
@@ -221,10 +203,10 @@ struct ChunkWalk {
         left -= c.take;
         if (left > 0) {
             off = 0;
-            if (++q == items) {
-                q = 0;
-                if (++hk == p.Hkv) {
-                    hk = 0;
+            if (++hk == p.Hkv) {
+                hk = 0;
+                if (++q == items) {
+                    q = 0;
                     do {
                         r = request_of(p, ++b);
                         items = items_of(p, r, span);
@@ -269,7 +251,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     static_assert((2 * NS + 12) * 8 <= 256, "barriers");
     volatile uint32_t* miss = reinterpret_cast<volatile uint32_t*>(smem + L::kMissOff);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
-    volatile int* abort_flag = misc;  // misc: abort, request, -, item, offset, last arrival (2), -, tensor memory
+    volatile int* abort_flag = misc;  // misc: abort, request, head, item, offset, last arrival (2), -, tensor memory
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff) + 8;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -307,67 +289,91 @@ __global__ void __launch_bounds__(kChThreads, 1)
     pdl_wait();
 
     // ---- this CTA's part of the line --------------------------------------
-    __shared__ int64_t warp_sum[kChThreads / 32];
-    __shared__ int64_t rest_smem;
-    const int per = (p.B + kChThreads - 1) / kChThreads;
-    const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
-    auto units_of = [&](int b) {
-        const Request r = request_of(p, b);
-        return tiles_before(p, r, span, items_of(p, r, span)) * p.Hkv;
-    };
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units_of(b);
-    int64_t before = mine;
+    // The line runs over the requests, their items, the key heads and the key
+    // tiles.  Pair j = (request, item): start[b] is request b's first pair (in
+    // the ring's memory, not yet in use); a thread takes a pair at a time.
+    __shared__ int warp_sum[kChThreads / 32];
+    constexpr int NT = kChThreads;
+    int* start = reinterpret_cast<int*>(smem);
+    auto scan = [&](int x, int& total) {  // exclusive sum over the threads
+        int y = x;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += x;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += z;
+        }
+        __syncthreads();
+        if (lane == 31) warp_sum[warp] = y;
+        __syncthreads();
+        const int w = lane < NT / 32 ? warp_sum[lane] : 0;
+        total = __reduce_add_sync(0xffffffffu, w);
+        return y - x + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    };
+    int pairs = 0;
+    for (int b = 0; b < p.B; b += NT) {
+        int n = 0, total;
+        if (b + (int)threadIdx.x < p.B) n = items_of(p, request_of(p, b + threadIdx.x), span);
+        const int at = pairs + scan(n, total);
+        if (b + (int)threadIdx.x < p.B) start[b + threadIdx.x] = at;
+        pairs += total;
     }
-    if (lane == 31) warp_sum[warp] = before;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int64_t U = 0;
-    for (int w = 0; w < kChThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        U += warp_sum[w];
-    }
-    before -= mine;
     const uint32_t tmem = *tmem_holder;
+    Request pr{0, 0, 0};
+    int pb = 0, pq = 0;
+    auto tiles_of = [&](int j) {  // key tiles of pair j (0 past the last)
+        if (j >= pairs) return 0;
+        int lo = 0, hi = p.B;  // the last request whose first pair is j or before it and that has a pair
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= j) lo = mid; else hi = mid;
+        }
+        pb = lo;
+        pq = j - start[lo];
+        pr = request_of(p, lo);
+        return item_of(p, pr, pq, span).tiles;
+    };
+    int64_t U = 0;
+    int first_tiles = 0, first_at = 0;  // of this thread's first pair
+    for (int j = 0; j < pairs; j += NT) {
+        int total;
+        const int n = tiles_of(j + threadIdx.x), at = scan(n, total);
+        if (j == 0) first_tiles = n, first_at = at;
+        U += total;
+    }
+    U *= p.Hkv;
     const int C = (int)(U < gridDim.x ? U : gridDim.x);
     ChunkWalk walk;
     walk.left = 0;
     if (c < C) {
         const int64_t u0 = (int64_t)c * U / C, u1 = (int64_t)(c + 1) * U / C;
-        if (u0 >= before && u0 < before + mine) {
-            int64_t at = before;
-            for (int b = b0; b < b1; ++b) {
-                const int64_t n = units_of(b);
-                if (u0 < at + n) {
-                    misc[1] = b;
-                    rest_smem = u0 - at;
-                    break;
-                }
-                at += n;
+        int64_t before = 0;
+        for (int j = 0; j < pairs; j += NT) {
+            int total = 0, n = first_tiles, at = first_at;
+            if (pairs > NT) {
+                n = tiles_of(j + threadIdx.x);
+                at = scan(n, total);
             }
+            const int64_t a = (before + at) * p.Hkv;
+            if (n > 0 && u0 >= a && u0 < a + (int64_t)n * p.Hkv) {
+                const int rest = (int)(u0 - a);
+                misc[1] = pb;
+                misc[2] = rest / n;
+                misc[3] = pq;
+                misc[4] = rest % n;
+            }
+            before += total;
         }
+        fence_proxy_async_smem();  // copies will overwrite `start`
         __syncthreads();
         walk.b = misc[1];
-        walk.r = request_of(p, walk.b);
-        walk.items = items_of(p, walk.r, span);
-        const int64_t head = tiles_before(p, walk.r, span, walk.items);
-        walk.hk = (int)(rest_smem / head);
-        const int64_t rest = rest_smem - walk.hk * head;
-        for (int q = threadIdx.x; q < walk.items; q += kChThreads) {
-            const int64_t a = tiles_before(p, walk.r, span, q);
-            if (rest >= a && rest < a + item_of(p, walk.r, q, span).tiles) {
-                misc[3] = q;
-                misc[4] = (int)(rest - a);
-            }
-        }
-        __syncthreads();
+        walk.hk = misc[2];
         walk.q = misc[3];
         walk.off = misc[4];
+        walk.r = request_of(p, walk.b);
+        walk.items = items_of(p, walk.r, span);
         walk.at = u0;
         walk.left = u1 - u0;
     }
@@ -377,19 +383,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // ---------------------------------------------------------- copies
         const int page = 1 << p.shift, rows = page < kChKeys ? page : kChKeys, boxes = kChKeys / rows;
         uint32_t e = 0;     // ring entries: keys 2 i, values 2 i + 1 of this CTA's tile i
-        uint32_t items = 0;
         bool ok = true;
         while (ok && walk.next(p, span, pc)) {
-            if (items > 0) ok = mbar_wait_warp(q_free, (items - 1) & 1, abort_flag, &g_chunk_status);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, (uint32_t)((pc.duo ? 2 : 1) * L::kSlabs * toks * p.G * 128));
-                for (int g = 0; g < (pc.duo ? 2 : 1); ++g)
-                    for (int s = 0; s < L::kSlabs; ++s)
-                        tma_load_3d(smem + g * L::kTile + s * 16384, &tmap_q, 64 * s, pc.hk * p.G,
-                                    pc.r.t0 + pc.it.i0 + g * toks, q_full);
-            }
-            ++items;
             const int* row = p.table + (int64_t)pc.b * p.table_stride;
             auto entry = [&](int t) {  // lane's box of the piece's tile t
                 const int j = (pc.it.t0 + pc.off + t) * kChKeys + lane * rows, col = j >> p.shift;
@@ -427,6 +422,21 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // the copies in flight land before the CTA ends
         for (uint32_t i = e > NS ? e - NS : 0; i < e; ++i)
             (void)mbar_wait_warp(full + i % NS, (i / NS) & 1, nullptr, &g_chunk_status);
+    } else if (warp == 10) {
+        // --------------------------------------------------------- queries
+        uint32_t items = 0;
+        while (walk.next(p, span, pc)) {
+            if (items > 0 && !mbar_wait_warp(q_free, (items - 1) & 1, abort_flag, &g_chunk_status)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, (uint32_t)((pc.duo ? 2 : 1) * L::kSlabs * toks * p.G * 128));
+                for (int g = 0; g < (pc.duo ? 2 : 1); ++g)
+                    for (int s = 0; s < L::kSlabs; ++s)
+                        tma_load_3d(smem + g * L::kTile + s * 16384, &tmap_q, 64 * s, pc.hk * p.G,
+                                    pc.r.t0 + pc.it.i0 + g * toks, q_full);
+            }
+            __syncwarp();
+            ++items;
+        }
         if (items > 0) (void)mbar_wait_warp(q_full, (items - 1) & 1, nullptr, &g_chunk_status);
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMAs
@@ -491,7 +501,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         mma_commit_warp(done);
         (void)mbar_wait_warp(done, 0, nullptr, &g_chunk_status);
-    } else if (warp < 8) {
+    } else {
         // --------------------------------------------------------- softmax
         const int g = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -517,16 +527,24 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 tc_fence_after();
                 const uint32_t no = miss[(tile0 + t) & 7];
                 if (j0 < pc.it.lo1 || j0 + kChKeys - 1 > pc.it.e0 || no) {
-                    // an edge: scores outside the row's positions
-                    const int rl = lo - j0, re = e - j0, sh = p.shift < 7 ? p.shift : 7;
+                    // an edge: scores outside the row's positions become -inf, 32 at a time
+                    const int rl = lo - j0, re = e - j0;
 #pragma unroll 1
                     for (int x = 0; x < 128; x += 32) {
+                        uint32_t seen = re >= x + 31 ? ~0u : re < x ? 0u : (2u << (re - x)) - 1u;
+                        seen &= rl <= x ? ~0u : rl > x + 31 ? 0u : ~0u << (rl - x);
+                        if (no) {  // pages that are not there: 2^sh keys a bit
+                            const int sh = p.shift < 7 ? p.shift : 7;
+                            for (int i = 0; i < 32; i += 8)
+                                if ((no >> ((x + i) >> sh)) & 1u) seen &= ~(0xffu << i);
+                        }
+                        if (__all_sync(0xffffffffu, seen == ~0u)) continue;
                         uint32_t sv[32];
                         tmem_ld32(ts + x, sv);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (x + i < rl || x + i > re || ((no >> ((x + i) >> sh)) & 1u)) sv[i] = 0xff800000u;  // -inf
+                            if (!((seen >> i) & 1u)) sv[i] = 0xff800000u;
                         tmem_st32(ts + x, sv);
                     }
                     tmem_wait_st();
@@ -539,16 +557,18 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     if (!ok) break;
                     if (none || some) {
                         const uint32_t va = smem_u32(smem + L::kRingOff + sl * L::kTile) + row * 128;
+                        uint32_t top = 0;  // a half's exponent is all ones: its top bit after the addition
+#pragma unroll 4
                         for (int x = 0; x < 8 * L::kSlabs; ++x) {
                             const uint32_t a = va + (x >> 3) * 16384 + (((x & 7) ^ (row & 7)) << 4);
                             if (none) {
                                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
                             } else {
                                 const uint4 v = lds_v4(a);
-                                for (uint32_t y : {v.x, v.y, v.z, v.w})
-                                    odd |= !(fabsf(Ty::lo(y)) < INFINITY) || !(fabsf(Ty::hi(y)) < INFINITY);
+                                top |= Ty::all_ones(v.x) | Ty::all_ones(v.y) | Ty::all_ones(v.z) | Ty::all_ones(v.w);
                             }
                         }
+                        odd |= (top & 0x80008000u) != 0;
                     }
                     fence_proxy_async_smem();
                 }
@@ -561,9 +581,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     tmem_wait_ld();
                     if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        mx = fmaxf(mx, __uint_as_float(sv[x & 1][i]));
-                        mo = fmaxf(mo, __uint_as_float(sv[x & 1][i + 1]));
+                    for (int i = 0; i < 32; i += 4) {
+                        mx = max3(mx, __uint_as_float(sv[x & 1][i]), __uint_as_float(sv[x & 1][i + 1]));
+                        mo = max3(mo, __uint_as_float(sv[x & 1][i + 2]), __uint_as_float(sv[x & 1][i + 3]));
                     }
                 }
                 mx = fmaxf(mx, mo);
@@ -587,16 +607,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     }
                 }
                 const float base = m == -INFINITY ? 0.f : m * p.scale2;
-                float l0 = 0.f, l1 = 0.f;
                 // weights: scores 32 x .. become the 16 columns 16 x .., over scores read before
+                float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+                const float2 sc = make_float2(p.scale2, p.scale2), nb = make_float2(-base, -base);
                 auto weights = [&](const uint32_t* v, uint32_t* pk) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float a = exp2_approx(fmaf(__uint_as_float(v[2 * i]), p.scale2, -base));
-                        const float b = exp2_approx(fmaf(__uint_as_float(v[2 * i + 1]), p.scale2, -base));
-                        l0 += a;
-                        l1 += b;
-                        pk[i] = Ty::pack(a, b);
+                        float2 a = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        a = fma2(a, sc, nb);
+                        a.x = exp2_approx(a.x);
+                        a.y = exp2_approx(a.y);
+                        if (i & 1) l1 = add2(l1, a);
+                        else l0 = add2(l0, a);
+                        pk[i] = Ty::pack(a.x, a.y);
                     }
                 };
                 tmem_ld32(ts, sv[0]);
@@ -630,7 +653,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                         tmem_st16(ts + 64 + 16 * x, pl[x]);
                     }
                 }
-                l += l0 + l1;
+                l += (l0.x + l0.y) + (l1.x + l1.y);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full + g);
@@ -717,17 +740,17 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 reinterpret_cast<float2*>(part)[row] = make_float2(odd ? NAN : m * p.scale2, l);
                 const int64_t end = pc.first + pc.it.tiles;
                 const int c0 = (int)(((pc.first + 1) * C - 1) / U), c1 = (int)((end * C - 1) / U);
-                __threadfence();
                 named_bar(1 + g, 128);
                 if (row == 0) {
+                    __threadfence();  // the warpgroup's stores, ordered before by the barrier
                     unsigned* counter = p.counters + kChCounters + 2 * c0 + g;
                     const bool last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
                     if (last) *counter = 0;
                     misc[5 + g] = last;
+                    __threadfence();
                 }
                 named_bar(1 + g, 128);
                 if (misc[5 + g]) {
-                    __threadfence();
                     auto at = [&](int i) {
                         return p.part + ((int64_t)(2 * i + (i == c0)) * 2 + g) * L::kPartHalf;
                     };
@@ -747,17 +770,17 @@ __global__ void __launch_bounds__(kChThreads, 1)
                         }
                         const float w = S == 0.f ? 0.f : 1.f / S;
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 32) {
-                            float acc[32];
+                        for (int x = 0; x < D; x += 64) {
+                            float acc[64];
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) acc[y] = 0.f;
+                            for (int y = 0; y < 64; ++y) acc[y] = 0.f;
                             for (int i = c0; i <= c1; ++i) {
                                 const float* q = at(i);
                                 const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
                                 if (mi.y == 0.f) continue;  // no seen key in this piece
                                 const float f = exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - b);
 #pragma unroll
-                                for (int y = 0; y < 32; y += 4) {
+                                for (int y = 0; y < 64; y += 4) {
                                     const float4 v =
                                         __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x + y) >> 2) * 128 + row);
                                     acc[y] = fmaf(v.x, f, acc[y]);
@@ -768,7 +791,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                             }
                             if (!valid) continue;
 #pragma unroll
-                            for (int y = 0; y < 32; y += 8)
+                            for (int y = 0; y < 64; y += 8)
                                 *reinterpret_cast<uint4*>(out + x + y) =
                                     S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
                                              : make_uint4(Ty::pack(acc[y] * w, acc[y + 1] * w),
