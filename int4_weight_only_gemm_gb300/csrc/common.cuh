@@ -140,6 +140,40 @@ W4A16_DEVICE bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
     return false;
 }
 
+// Whether the phase with the given parity is complete, without waiting.
+W4A16_DEVICE bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// As mbar_wait_warp for waits of well under a microsecond: polls instead of
+// sleeping (a sleeping thread wakes ~90 ns later); the flag and the clock are
+// looked at every 64 polls.
+W4A16_DEVICE bool mbar_spin_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+    const uint32_t a = smem_u32(bar);
+    bool ok = mbar_try_wait(a, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer();
+        for (uint32_t i = 1; i < kWaitSpins; ++i) {
+            ok = mbar_try_wait(a, parity);
+            if (ok) break;
+            if ((i & 63) == 0 && ((abort && *abort) || globaltimer() - t0 > kWaitNs)) break;
+        }
+        if (!ok) {
+            if (abort) *abort = 1;
+            atomicExch(status, (int)W4A16_ETIMEOUT);
+        }
+    }
+    return __all_sync(0xFFFFFFFFu, ok) != 0;
+}
+
 // Warp-uniform bounded wait: every lane waits (so every lane acquires the
 // phase), then the warp agrees on the outcome, so the warp-collective tcgen05
 // instructions that follow never diverge.

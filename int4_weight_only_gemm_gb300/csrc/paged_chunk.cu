@@ -49,6 +49,7 @@ static __device__ int g_chunk_status;
 constexpr int kChThreads = 352;  // two softmax warpgroups, the MMA warp, the key / value and the query copy warp
 constexpr int kChKeys = 128;
 constexpr int kChTwo = 256;  // rows that see fewer positions carry their weights in two parts
+constexpr int kChSnap = 4, kChJoin = 12;  // key tiles; see the line
 constexpr int kChCounters = 1024;  // first arrival counter of this kernel (the small-row kernel's lie below)
 
 template <int D>
@@ -57,15 +58,15 @@ struct Ch {
     static constexpr int kTile = kSlabs * 16384;    // bytes of 128 rows of keys, values or queries
     static constexpr int kSlots = D == 128 ? 5 : 10;
     static constexpr int kRingOff = 2 * kTile;
-    static constexpr int kMlOff = kRingOff + kSlots * kTile;  // [128] m, l of warpgroup 1
-    static constexpr int kBarOff = kMlOff + 1024;
-    static constexpr int kMissOff = kBarOff + 256;            // [8] pages of a tile that are not there
+    static constexpr int kMlOff = kRingOff + kSlots * kTile;
+    static constexpr int kBarOff = kMlOff + 2048;
+    static constexpr int kMissOff = kBarOff + 384;            // [8] pages of a tile that are not there
     static constexpr int kMiscOff = kMissOff + 64;
-    static constexpr int kSmem = kMiscOff + 128 + 1024;
+    static constexpr int kSmem = kMiscOff + 128;               // no static shared memory: the base is 1024-aligned
     static constexpr int kPartHalf = 128 * (D + 2);           // floats of one row tile's partial result
     static constexpr uint32_t kTS = 0, kTO = 256;             // tensor memory: S and P of both tiles, then O
 };
-static_assert(Ch<128>::kSmem + 256 <= 232448 && Ch<64>::kSmem + 256 <= 232448, "shared memory");
+static_assert(Ch<128>::kSmem <= 232448 && Ch<64>::kSmem <= 232448, "shared memory");
 
 // ---- instructions ---------------------------------------------------------
 // D[tmem] (+)= A[smem] B[smem], issued by one lane of a converged warp
@@ -234,10 +235,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedAttnParams p) {
     using L = Ch<D>;
     constexpr int NS = L::kSlots;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    float2* ml1 = reinterpret_cast<float2*>(smem + L::kMlOff);
+    extern __shared__ __align__(1024) unsigned char smem[];
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
+        if (threadIdx.x == 0) atomicExch(&g_chunk_status, (int)W4A16_ECUDA);
+        return;
+    }
+    float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);  // [2][128] m and l of both warpgroups
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     uint64_t* empty = full + NS;
     uint64_t* s_full = empty + NS;   // [2]
@@ -246,9 +249,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
     uint64_t* o_free = o_full + 2;   // [2]
     uint64_t* q_full = o_free + 2;
     uint64_t* q_free = q_full + 1;
-    uint64_t* join = q_free + 1;     // warpgroup 1's maxima and sums are in ml1
+    uint64_t* join = q_free + 1;     // both warpgroups' maxima and sums are in ml
     uint64_t* done = join + 1;       // every MMA of the CTA is done
-    static_assert((2 * NS + 12) * 8 <= 256, "barriers");
+    static_assert((2 * NS + 12) * 8 <= 384, "barriers");
     volatile uint32_t* miss = reinterpret_cast<volatile uint32_t*>(smem + L::kMissOff);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
     volatile int* abort_flag = misc;  // misc: abort, request, head, item, offset, last arrival (2), -, tensor memory
@@ -265,13 +268,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(s_full + g, 1);
-            mbar_init(p_full + g, 128);
+            mbar_init(p_full + g, 4);  // a lane of each warp arrives
             mbar_init(o_full + g, 1);
-            mbar_init(o_free + g, 128);
+            mbar_init(o_free + g, 8);  // the warps that may read it, or four of them twice
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
-        mbar_init(join, 128);
+        mbar_init(join, 8);
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -292,7 +295,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
     // The line runs over the requests, their items, the key heads and the key
     // tiles.  Pair j = (request, item): start[b] is request b's first pair (in
     // the ring's memory, not yet in use); a thread takes a pair at a time.
-    __shared__ int warp_sum[kChThreads / 32];
+    int* warp_sum = reinterpret_cast<int*>(ml);                        // (not in use before the first item's end)
+    int64_t* cut = reinterpret_cast<int64_t*>(warp_sum + 16);
     constexpr int NT = kChThreads;
     int* start = reinterpret_cast<int*>(smem);
     auto scan = [&](int x, int& total) {  // exclusive sum over the threads
@@ -344,39 +348,89 @@ __global__ void __launch_bounds__(kChThreads, 1)
         U += total;
     }
     U *= p.Hkv;
-    const int C = (int)(U < gridDim.x ? U : gridDim.x);
+    const int most = [&] {  // key tiles of the longest item
+        int m = first_tiles;
+        for (int j = NT; j < pairs; j += NT) m = max(m, tiles_of(j + threadIdx.x));
+        m = __reduce_max_sync(0xffffffffu, m);
+        __syncthreads();
+        if (lane == 0) warp_sum[warp] = m;
+        __syncthreads();
+        return __reduce_max_sync(0xffffffffu, lane < NT / 32 ? warp_sum[lane] : 0);
+    }();
+    // An item split over CTAs costs about kChJoin tiles' time on each side: the
+    // piece written, waited for and joined.  So with no more items than CTAs
+    // every CTA takes one, unless the longest would take that much longer than
+    // an even share; and a cut less than kChSnap tiles from an item's end moves
+    // to the end.
+    const int64_t n_items = (int64_t)pairs * p.Hkv;
+    const bool single = n_items <= gridDim.x && (int64_t)(most - kChJoin) * gridDim.x <= U;
+    const int C = single ? (int)n_items : (int)(U < gridDim.x ? U : gridDim.x);
     ChunkWalk walk;
     walk.left = 0;
     if (c < C) {
-        const int64_t u0 = (int64_t)c * U / C, u1 = (int64_t)(c + 1) * U / C;
-        int64_t before = 0;
-        for (int j = 0; j < pairs; j += NT) {
-            int total = 0, n = first_tiles, at = first_at;
-            if (pairs > NT) {
-                n = tiles_of(j + threadIdx.x);
-                at = scan(n, total);
-            }
-            const int64_t a = (before + at) * p.Hkv;
-            if (n > 0 && u0 >= a && u0 < a + (int64_t)n * p.Hkv) {
-                const int rest = (int)(u0 - a);
+        int64_t u0 = (int64_t)c * U / C, u1 = (int64_t)(c + 1) * U / C;
+        if (single) {
+            if (threadIdx.x == 0) {
+                const int n = tiles_of(c / p.Hkv);
                 misc[1] = pb;
-                misc[2] = rest / n;
+                misc[2] = c % p.Hkv;
                 misc[3] = pq;
-                misc[4] = rest % n;
+                misc[4] = 0;
+                cut[0] = 0;
+                cut[1] = n;
             }
-            before += total;
+            __syncthreads();
+        } else {
+            // the items that hold this CTA's first unit and the next CTA's
+            int64_t before = 0;
+            for (int j = 0; j < pairs; j += NT) {
+                int total = 0, n = first_tiles, at = first_at;
+                if (pairs > NT) {
+                    n = tiles_of(j + threadIdx.x);
+                    at = scan(n, total);
+                }
+                const int64_t a = (before + at) * p.Hkv;
+                auto snapped = [&](int64_t u) {
+                    const int d = (int)(u - a) % n;
+                    return d <= kChSnap && d <= n - d ? u - d : n - d <= kChSnap ? u + n - d : u;
+                };
+                if (n > 0 && u0 >= a && u0 < a + (int64_t)n * p.Hkv) {
+                    cut[0] = snapped(u0);
+                    int rest = (int)(cut[0] - a);
+                    const bool next = rest == n * p.Hkv;  // at the next pair's first item
+                    if (next && j + (int)threadIdx.x + 1 < pairs) {
+                        (void)tiles_of(j + threadIdx.x + 1);
+                        rest = 0;
+                    }
+                    misc[1] = pb;
+                    misc[2] = rest / n;
+                    misc[3] = pq;
+                    misc[4] = rest % n;
+                }
+                if (n > 0 && u1 >= a && u1 < a + (int64_t)n * p.Hkv) cut[1] = snapped(u1);
+                if (u1 == U && threadIdx.x == 0) cut[1] = U;
+                before += total;
+            }
+            __syncthreads();
+        }
+        walk.left = cut[1] - cut[0];
+        if (walk.left > 0) {
+            walk.b = misc[1];
+            walk.hk = misc[2];
+            walk.q = misc[3];
+            walk.off = misc[4];
+            walk.r = request_of(p, walk.b);
+            walk.items = items_of(p, walk.r, span);
+            walk.at = cut[0];
         }
         fence_proxy_async_smem();  // copies will overwrite `start`
         __syncthreads();
-        walk.b = misc[1];
-        walk.hk = misc[2];
-        walk.q = misc[3];
-        walk.off = misc[4];
-        walk.r = request_of(p, walk.b);
-        walk.items = items_of(p, walk.r, span);
-        walk.at = u0;
-        walk.left = u1 - u0;
     }
+    // the CTAs that share an item of `n` tiles whose first unit is `first`
+    auto sharers = [&](int64_t first, int n, int& lo, int& hi) {
+        lo = (int)(((first + kChSnap + 1) * C + U - 1) / U) - 1;
+        hi = (int)(((first + n - kChSnap) * C + U - 1) / U) - 1;
+    };
 
     ChunkPiece pc;
     if (warp == 9) {
@@ -440,6 +494,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (items > 0) (void)mbar_wait_warp(q_full, (items - 1) & 1, nullptr, &g_chunk_status);
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMAs
+        // The warpgroups in turn: P V of a tile and the scores of the next one
+        // go out together.
         constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<Ty>(D, true);
         uint32_t tile0 = 0, items = 0, np[2] = {0, 0};
         bool ok = true;
@@ -474,7 +530,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     if (k == 0 && items > 0)
                         ok = mbar_wait_warp(o_free + g, (items - 1) & 1, abort_flag, &g_chunk_status);
                     ok = ok && mbar_wait_warp(full + sl, (e / NS) & 1, abort_flag, &g_chunk_status) &&
-                         mbar_wait_warp(p_full + g, np[g] & 1, abort_flag, &g_chunk_status);
+                         mbar_spin_warp(p_full + g, np[g] & 1, abort_flag, &g_chunk_status);
                     if (!ok) break;
                     ++np[g];
                     tc_fence_after();
@@ -506,7 +562,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int g = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + L::kTS + 128 * g, to = tmem + lanes + L::kTO + D * g;
-        const uint32_t to_other = tmem + lanes + L::kTO + D * (1 - g);
         const int tok = row / p.G, hh = row - tok * p.G;
         uint32_t tile0 = 0, items = 0, ns = 0, joins = 0;
         bool ok = true;
@@ -521,7 +576,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             for (int k = 0; k < cnt; ++k) {
                 const int t = pc.duo ? k : 2 * k + g;
                 const int j0 = (pc.it.t0 + pc.off + t) * kChKeys;
-                ok = mbar_wait_warp(s_full + g, ns & 1, abort_flag, &g_chunk_status);
+                ok = mbar_spin_warp(s_full + g, ns & 1, abort_flag, &g_chunk_status);
                 ++ns;
                 if (!ok) break;
                 tc_fence_after();
@@ -653,145 +708,183 @@ __global__ void __launch_bounds__(kChThreads, 1)
                         tmem_st16(ts + 64 + 16 * x, pl[x]);
                     }
                 }
-                l += (l0.x + l0.y) + (l1.x + l1.y);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(p_full + g);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + g);
+                l += (l0.x + l0.y) + (l1.x + l1.y);
             }
-            // ---- the item's (or the piece's) result; the warpgroup goes on or gives up together
-            ok = ok && mbar_wait_warp(o_full + g, items & 1, abort_flag, &g_chunk_status);
-            if (!pc.duo && g == 0) {
-                ok = ok && mbar_wait_warp(join, joins & 1, abort_flag, &g_chunk_status) &&
-                     mbar_wait_warp(o_full + 1, items & 1, abort_flag, &g_chunk_status);
+            // ---- the item's (or the piece's) result; the warpgroup goes on or gives up together.
+            // Warpgroups with rows of their own write them; where they share the rows, each
+            // joins both outputs for half of the columns.
+            const int g0 = pc.duo ? g : 0;
+            if (!pc.duo) {
+                // (the last item's are read)
+                if (items > 0) ok = ok && mbar_wait_warp(o_free + g, (items - 1) & 1, abort_flag, &g_chunk_status);
+                ml[g * 128 + row] = make_float2(m, l);
+                if (odd) ml[g * 128 + row].x = NAN;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(join);
+                ok = ok && mbar_wait_warp(join, joins & 1, abort_flag, &g_chunk_status);
                 ++joins;
             }
+            ok = ok && mbar_wait_warp(o_full + g, items & 1, abort_flag, &g_chunk_status) &&
+                 (pc.duo || mbar_wait_warp(o_full + 1 - g, items & 1, abort_flag, &g_chunk_status));
             ok = bar_and(1 + g, 128, ok);
             if (!ok) break;
-            odd = !bar_and(1 + g, 128, !odd);
-            if (!pc.duo && g == 1) {
-                ml1[row] = make_float2(odd ? NAN : m, l);  // NaN: this piece asks for the definition
-                mbar_arrive(join);
-                tile0 += pc.take;
-                ++items;
-                continue;  // warpgroup 0 reads both outputs
-            }
             float f0 = 1.f, f1 = 0.f;
             const bool other = !pc.duo && pc.take > 1;
             if (!pc.duo) {
-                const float2 o = ml1[row];
-                odd = odd || o.x != o.x;
-                if (other && !odd) {
+                for (int x = 0; x < 256; x += 128) odd = odd || ml[x + row].x != ml[x + row].x;
+                const float2 a = ml[row], o = ml[128 + row];
+                m = a.x;
+                l = a.y;
+                if (other) {
                     const float M = fmaxf(m, o.x), b = M == -INFINITY ? 0.f : M;
                     f0 = exp2_approx((m - b) * p.scale2);
                     f1 = exp2_approx((o.x - b) * p.scale2);
                     // a sum that is not a number stays one
-                    l = (l == 0.f ? 0.f : l * (m == -INFINITY ? 1.f : f0)) + (o.y == 0.f ? 0.f : o.y * (o.x == -INFINITY ? 1.f : f1));
+                    l = (l == 0.f ? 0.f : l * (m == -INFINITY ? 1.f : f0)) +
+                        (o.y == 0.f ? 0.f : o.y * (o.x == -INFINITY ? 1.f : f1));
                     m = M;
                 }
             }
+            odd = !bar_and(1 + g, 128, !odd);
+            const uint32_t toa = tmem + lanes + L::kTO + D * g0, tob = toa + D;
+            const int x0 = pc.duo ? 0 : g * (D / 2), x1 = pc.duo ? D : x0 + D / 2;  // columns
             tc_fence_after();
             const bool whole = pc.off == 0 && pc.take == pc.it.tiles;
             const int64_t t = pc.r.t0 + pc.it.i0 + mytok;
             const int h = pc.hk * p.G + hh;
             uint16_t* out = p.out + t * p.o_token + (int64_t)h * p.o_head;
-            float* part = p.part + ((int64_t)(2 * c + (pc.off == 0 ? 1 : 0)) * 2 + g) * L::kPartHalf;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
-                uint32_t ov[32];
-                tmem_ld32(to + i, ov);
-                tmem_wait_ld();
-                if (other) {
-                    uint32_t ow[32];
-                    tmem_ld32(to_other + i, ow);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f0 + __uint_as_float(ow[x]) * f1);
+            // the CTAs that share the item, and where CTA i keeps its piece of this row tile
+            int c0 = c, c1 = c;
+            unsigned* counter = nullptr;
+            if (!whole) {
+                sharers(pc.first, pc.it.tiles, c0, c1);
+                counter = p.counters + kChCounters + 2 * c0 + g;
+            }
+            auto piece = [&](int i) { return p.part + ((int64_t)(2 * i + (i == c0)) * 2 + g) * L::kPartHalf; };
+            const float mine_m = odd ? NAN : m * p.scale2;
+            // Where all other pieces are there already, this one need not be written:
+            // it goes into the sum from tensor memory, in its place of the order.
+            bool last = whole, kept = true;  // kept: this piece's output is still in tensor memory only
+            if (!whole) {
+                bool all = true;
+                if (row == 0) {
+                    unsigned n;
+                    asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(n) : "l"(counter) : "memory");
+                    all = n == (unsigned)(c1 - c0);
+                    if (all) *counter = 0;
                 }
-                if (whole) {
-                    if (valid && !odd) {
+                last = bar_and(1 + g, 128, all);
+                if (!last) {
+                    kept = false;
+                    float* part = piece(c);
+#pragma unroll 1
+                    for (int i = x0; i < x1; i += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(toa + i, ov);
+                        tmem_wait_ld();
+                        if (other) {
+                            uint32_t ow[32];
+                            tmem_ld32(tob + i, ow);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
-                            uint4 v;
-                            uint32_t* y = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                y[z] = l == 0.f ? 0u
-                                                : Ty::pack(__uint_as_float(ov[x + 2 * z]) * inv,
-                                                           __uint_as_float(ov[x + 2 * z + 1]) * inv);
-                            *reinterpret_cast<uint4*>(out + i + x) = v;
+                            for (int x = 0; x < 32; ++x)
+                                ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f0 + __uint_as_float(ow[x]) * f1);
                         }
-                    }
-                } else {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4)  // [column / 4][row]: neighbours write neighbours
-                        *reinterpret_cast<uint4*>(part + 256 + (((i + x) >> 2) * 128 + row) * 4) =
-                            make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
+                        for (int x = 0; x < 32; x += 4)  // [column / 4][row]: neighbours write neighbours
+                            *reinterpret_cast<uint4*>(part + 256 + (((i + x) >> 2) * 128 + row) * 4) =
+                                make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
+                    }
+                    reinterpret_cast<float2*>(part)[row] = make_float2(mine_m, l);
+                    named_bar(1 + g, 128);
+                    bool is_last = true;
+                    if (row == 0) {
+                        __threadfence();  // the warpgroup's stores, ordered before by the barrier
+                        is_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+                        if (is_last) *counter = 0;
+                        __threadfence();
+                    }
+                    last = bar_and(1 + g, 128, is_last);
                 }
             }
-            if (whole && valid && !odd && p.lse)
-                p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : kLn2 * (m * p.scale2 + log2f(l));
-            tc_fence_before();
-            mbar_arrive(o_free + g);
-            if (!pc.duo) mbar_arrive(o_free + 1);
-            bool again = whole && odd;  // rows to compute from the definition
-            if (!whole) {
-                reinterpret_cast<float2*>(part)[row] = make_float2(odd ? NAN : m * p.scale2, l);
-                const int64_t end = pc.first + pc.it.tiles;
-                const int c0 = (int)(((pc.first + 1) * C - 1) / U), c1 = (int)((end * C - 1) / U);
-                named_bar(1 + g, 128);
-                if (row == 0) {
-                    __threadfence();  // the warpgroup's stores, ordered before by the barrier
-                    unsigned* counter = p.counters + kChCounters + 2 * c0 + g;
-                    const bool last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
-                    if (last) *counter = 0;
-                    misc[5 + g] = last;
-                    __threadfence();
-                }
-                named_bar(1 + g, 128);
-                if (misc[5 + g]) {
-                    auto at = [&](int i) {
-                        return p.part + ((int64_t)(2 * i + (i == c0)) * 2 + g) * L::kPartHalf;
-                    };
-                    float M = -INFINITY, S = 0.f;
+            bool again = odd;  // rows to compute from the definition
+            if (last) {
+                float M = m * p.scale2, S = l;
+                if (!whole) {
+                    M = -INFINITY;
                     bool bad = false;
+#pragma unroll 4
                     for (int i = c0; i <= c1; ++i) {
-                        const float x = __ldcg(at(i) + 2 * row);
+                        const float x = i == c && kept ? mine_m : __ldcg(piece(i) + 2 * row);
                         bad |= x != x;
                         M = fmaxf(M, x);
                     }
-                    const float b = M == -INFINITY ? 0.f : M;
                     again = !bar_and(1 + g, 128, !bad);
-                    if (!again) {
-                        for (int i = c0; i <= c1; ++i) {
-                            const float2 mi = __ldcg(reinterpret_cast<const float2*>(at(i)) + row);
-                            if (mi.y != 0.f) S = fmaf(mi.y, exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - b), S);
-                        }
-                        const float w = S == 0.f ? 0.f : 1.f / S;
+                    S = 0.f;
+                }
+                const float b = M == -INFINITY ? 0.f : M;
+                auto factor = [&](float mi) { return exp2_approx(mi == -INFINITY ? 0.f : mi - b); };
+                if (!whole)
+#pragma unroll 4
+                    for (int i = c0; i <= c1; ++i) {
+                        const float2 mi = i == c && kept ? make_float2(mine_m, l)
+                                                         : __ldcg(reinterpret_cast<const float2*>(piece(i)) + row);
+                        if (mi.y != 0.f) S = fmaf(mi.y, factor(mi.x), S);
+                    }
+                const float w = S == 0.f ? 0.f : 1.f / S;
+                if (!again) {
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 64) {
-                            float acc[64];
+                    for (int x = x0; x < x1; x += 32) {
+                        float acc[32];
+                        auto own = [&](float f) {  // this piece's columns, times f, onto acc
+                            uint32_t ov[32];
+                            tmem_ld32(toa + x, ov);
+                            tmem_wait_ld();
+                            if (other) {
+                                uint32_t ow[32];
+                                tmem_ld32(tob + x, ow);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int y = 0; y < 64; ++y) acc[y] = 0.f;
+                                for (int y = 0; y < 32; ++y)
+                                    ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
+                            }
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), f, acc[y]);
+                        };
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) acc[y] = 0.f;
+                        if (whole) {
+                            own(1.f);
+                        } else {
                             for (int i = c0; i <= c1; ++i) {
-                                const float* q = at(i);
+                                if (i == c && kept) {
+                                    // (every lane: tensor-memory loads are the warp's)
+                                    own(l == 0.f ? 0.f : factor(mine_m));
+                                    continue;
+                                }
+                                const float* q = piece(i);
                                 const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
-                                if (mi.y == 0.f) continue;  // no seen key in this piece
-                                const float f = exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - b);
+                                const float f = mi.y == 0.f ? 0.f : factor(mi.x);  // no seen key: zeros
+                                float4 v[8];
 #pragma unroll
-                                for (int y = 0; y < 64; y += 4) {
-                                    const float4 v =
-                                        __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x + y) >> 2) * 128 + row);
-                                    acc[y] = fmaf(v.x, f, acc[y]);
-                                    acc[y + 1] = fmaf(v.y, f, acc[y + 1]);
-                                    acc[y + 2] = fmaf(v.z, f, acc[y + 2]);
-                                    acc[y + 3] = fmaf(v.w, f, acc[y + 3]);
+                                for (int y = 0; y < 8; ++y)
+                                    v[y] = __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row);
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) {
+                                    acc[4 * y] = fmaf(v[y].x, f, acc[4 * y]);
+                                    acc[4 * y + 1] = fmaf(v[y].y, f, acc[4 * y + 1]);
+                                    acc[4 * y + 2] = fmaf(v[y].z, f, acc[4 * y + 2]);
+                                    acc[4 * y + 3] = fmaf(v[y].w, f, acc[4 * y + 3]);
                                 }
                             }
-                            if (!valid) continue;
+                        }
+                        if (valid) {
 #pragma unroll
-                            for (int y = 0; y < 64; y += 8)
+                            for (int y = 0; y < 32; y += 8)
                                 *reinterpret_cast<uint4*>(out + x + y) =
                                     S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
                                              : make_uint4(Ty::pack(acc[y] * w, acc[y + 1] * w),
@@ -799,12 +892,18 @@ __global__ void __launch_bounds__(kChThreads, 1)
                                                           Ty::pack(acc[y + 4] * w, acc[y + 5] * w),
                                                           Ty::pack(acc[y + 6] * w, acc[y + 7] * w));
                         }
-                        if (valid) {
-                            if (p.lse) p.lse[t * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
-                        }
+                        __syncwarp();
                     }
+                    if (valid && p.lse && x0 == 0) p.lse[t * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(o_free + g);
+                mbar_arrive(o_free + (pc.duo ? g : 1 - g));
+            }
+            again = again && last && x0 == 0;
             if (again) {
                 const int n = min(toks, pc.it.tokens - base_tok);
                 attn_rows_from_definition<Ty, D>(p, pc.b, pc.r, pc.it.i0 + base_tok, n, pc.hk, warp & 3);
