@@ -390,15 +390,12 @@ int w4a16_last_device_status(w4a16_stream_t stream) {
     const int b = tc_read_status();
     const int c = selftest_read_status();
     const int d = swa_read_status();
-    const int f = decode_read_status();
     const int g = chunk_read_status();
-    if (a == W4A16_ECUDA || b == W4A16_ECUDA || c == W4A16_ECUDA || d == W4A16_ECUDA || f == W4A16_ECUDA ||
-        g == W4A16_ECUDA)
+    if (a == W4A16_ECUDA || b == W4A16_ECUDA || c == W4A16_ECUDA || d == W4A16_ECUDA || g == W4A16_ECUDA)
         return W4A16_ECUDA;
     if (a != 0) return a;
     if (b != 0) return b;
     if (d != 0) return d;
-    if (f != 0) return f;
     if (g != 0) return g;
     return c;
 }

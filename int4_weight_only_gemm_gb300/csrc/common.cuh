@@ -279,6 +279,11 @@ W4A16_DEVICE void cp_async_8(void* smem_dst, const void* gsrc) {
 W4A16_DEVICE void cp_async_16(void* smem_dst, const void* gsrc) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(gsrc) : "memory");
 }
+// 16 bytes, or 16 zero bytes where `there` is false (nothing is read then)
+W4A16_DEVICE void cp_async_16_or_zero(uint32_t smem_dst, const void* gsrc, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(there ? 16 : 0)
+                 : "memory");
+}
 // Close the group of this thread's cp.async copies issued since the last commit.
 W4A16_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most N of this thread's committed cp.async groups are pending.

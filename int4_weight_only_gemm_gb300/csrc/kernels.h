@@ -141,7 +141,6 @@ size_t paged_attn_workspace(int tokens, int requests, int Hq, int Hkv, int d, in
 cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cudaStream_t s);
 size_t sample_workspace(int rows, int vocab, bool filters, int sms);
 cudaError_t launch_sample(const w4a16_sample_args& a, int sms, cudaStream_t s);
-int decode_read_status();
 int chunk_read_status();
 // multiprocessors of the current device (api.cu), or <= 0
 int current_sms();

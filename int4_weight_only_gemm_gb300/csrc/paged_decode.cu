@@ -12,27 +12,26 @@
 // CTA order, so the result does not depend on timing.
 //
 // Inside a CTA eight warps work without meeting: warp w takes the 16-key tiles
-// w, w + 8, ... of the range through a ring of its own, filled by tensor
-// copies (one 128-byte-swizzled box a page and 64 columns) that its lane 0
-// issues, and keeps the rows' maxima, sums and 16 x head_dim outputs in
-// registers.  The products are warp-wide 16 x 8 x 16 MMAs: with 16 rows the
-// tensor pipe is not what bounds this kernel, and fragments that stay in
-// registers need no tensor-memory round trip between the two products.  The
-// warps' results meet once per pair, in shared memory.
+// w, w + 8, ... of the range through a ring of its own and keeps the rows'
+// maxima, sums and 16 x head_dim outputs in registers.  The products are
+// warp-wide 16 x 8 x 16 MMAs: with 16 rows the tensor pipe is not what bounds
+// this kernel, and fragments that stay in registers need no tensor-memory round
+// trip between the two products.  The warps' results meet once per pair, in
+// shared memory, while the next pair's first tiles are on their way.
+//
+// The ring is filled by 16-byte asynchronous copies, not by tensor copies: one
+// of 16 rows x 128 bytes (all that a 16-slot page gives at once) occupies the
+// copy unit of an SM for ~100 clocks, 20 bytes a clock, below what HBM delivers
+// to an SM; with them 64 requests took 248 us.
 //
 // Positions that a row does not see are masked in the scores; the values of
 // positions that no row of the tile sees (stale slots of the last page, slots
 // before the window) are cleared in shared memory first, and non-finite values
 // that only some rows see are added for those rows alone, so that no row takes
 // a NaN from a position outside its own.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "paged_attn.cuh"
 
 namespace w4a16 {
-
-static __device__ int g_decode_status;
 
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;
@@ -49,12 +48,14 @@ struct Dec {
     static constexpr int kMergeOff = kRing;
     static constexpr int kMerge = 4 * kRegs * 32 * 4;
     static constexpr int kMlOff = kMergeOff + kMerge;        // [warp][16][2]
-    static constexpr int kBarOff = kMlOff + kDecWarps * 16 * 2 * 4;
-    static constexpr int kMiscOff = kBarOff + kDecWarps * kSlots * 8;
-    static constexpr int kSmem = kMiscOff + 64 + 1024;
+    static constexpr int kMiscOff = kMlOff + kDecWarps * 16 * 2 * 4;
+    static constexpr int kSmem = kMiscOff + 128;
     static constexpr int kPart = 16 * (D + 2);               // floats of a partial result
 };
 static_assert(Dec<128>::kSmem <= 232448 && Dec<64>::kSmem <= 232448, "shared memory");
+// What a pair costs beside its units, in units: the rows' first load, the
+// warps' meeting and the output, of which the copies ahead hide a part.
+constexpr int kDecPair = 2;
 
 // Units of a request for one key head, and its first key (a multiple of 16).
 struct DecSpan {
@@ -69,43 +70,35 @@ W4A16_DEVICE DecSpan dec_span(const PagedAttnParams& p, const Request& r) {
     return s;
 }
 
-// CTA that holds unit u of U over C CTAs
+// CTA that holds place u of the line of U places cut over C CTAs
 W4A16_DEVICE int owner_of(int64_t u, int64_t U, int C) { return (int)(((u + 1) * C - 1) / U); }
 
 template <typename Ty, int D>
-__global__ void __launch_bounds__(kDecThreads, 1)
-    paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                        const PagedAttnParams p) {
+__global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __grid_constant__ PagedAttnParams p) {
     using L = Dec<D>;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(128) unsigned char smem[];
     float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
     float* ml = reinterpret_cast<float*>(smem + L::kMlOff);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
-    volatile int* abort_flag = misc;  // misc: abort, request, head, offset, last
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = (int)blockIdx.x;
-
-    uint64_t* wbar = bars + warp * L::kSlots;
-    unsigned char* ring = smem + warp * (L::kSlots * 2 * L::kHalf);
-    if (threadIdx.x == 0) *abort_flag = 0;
-    if (lane == 0) {
-        for (int i = 0; i < L::kSlots; ++i) mbar_init(wbar + i, 1);
-        fence_mbar_init();
-        prefetch_tmap(&tmap_k);
-        prefetch_tmap(&tmap_v);
-    }
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- this CTA's units: sums over the requests, a run of them a thread ----
-    __shared__ int64_t warp_sum[kDecWarps];
+    // ---- this CTA's part of the line ----------------------------------------
+    // A pair (request, key head) takes kDecPair + units places of it.
+    int64_t* warp_sum = reinterpret_cast<int64_t*>(ml);
     const int per = (p.B + kDecThreads - 1) / kDecThreads;
     const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+    Request r{0, 0, 0};
+    DecSpan sp{0, 0};
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (int64_t)dec_span(p, request_of(p, b)).units * p.Hkv;
+    auto places = [&](int b) {  // of a request, r and sp on the way
+        r = request_of(p, b);
+        sp = dec_span(p, r);
+        return sp.units ? (int64_t)(sp.units + kDecPair) * p.Hkv : (int64_t)0;
+    };
+    for (int b = b0; b < b1; ++b) mine += places(b);
     int64_t before = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -115,130 +108,131 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (lane == 31) warp_sum[warp] = before;
     __syncthreads();
     int64_t U = 0;
+#pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
         if (w < warp) before += warp_sum[w];
         U += warp_sum[w];
     }
     before -= mine;
-    const int C = (int)(U < gridDim.x ? U : gridDim.x);  // every CTA of the C has a unit at least
+    const int C = (int)(U < gridDim.x ? U : gridDim.x);  // every CTA of the C has a place at least
     if (c >= C) return;
     const int64_t u0 = (int64_t)c * U / C, u1 = (int64_t)(c + 1) * U / C;
     if (u0 >= before && u0 < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
-            const int64_t n = (int64_t)dec_span(p, request_of(p, b)).units;
-            if (u0 < at + n * p.Hkv) {
-                misc[1] = b;
-                misc[2] = (int)((u0 - at) / n);
-                misc[3] = (int)((u0 - at) % n);
+            const int64_t n = per == 1 ? mine : places(b);
+            if (u0 < at + n) {
+                const int len = sp.units + kDecPair;
+                misc[0] = b;
+                misc[1] = (int)((u0 - at) / len);
+                misc[2] = (int)((u0 - at) % len);
+                misc[3] = r.t0;
+                misc[4] = r.n;
+                misc[5] = r.L;
+                misc[6] = sp.units;
+                misc[7] = sp.j0;
                 break;
             }
-            at += n * p.Hkv;
+            at += n;
         }
     }
     __syncthreads();
-    int b = misc[1], hk = misc[2], off = misc[3];
-    int64_t u = u0;  // the current piece's first unit
+    int b = misc[0], hk = misc[1];
+    int64_t s0 = u0 - misc[2];  // the pair's first place
+    r = Request{misc[3], misc[4], misc[5]};
+    sp = DecSpan{misc[6], misc[7]};
+    if (u1 <= s0 + kDecPair) return;  // a place before the pair's first unit
 
     // ---- the warp's ring -------------------------------------------------
-    int put = 0, get = 0;          // slots to fill and to read next
-    uint32_t parity = 0;           // of `get`
+    const uint32_t ring = smem_u32(smem) + warp * (L::kSlots * 2 * L::kHalf);
     uint32_t gone = 0;             // 2 bits a slot: pages of the tile that are not there
     const int page = 1 << p.shift, box = page < kDecTile ? page : kDecTile;
     const int boxes = kDecTile / box;  // 1, or 2 for 8-slot pages
-
-    struct Piece {
-        Request r;
-        int j0, e_last, tile0, tiles;  // first key, last key seen, this warp's first tile and their number
-    } w;
-    int ent[2];       // table entries of the tiles ent_base + lane
-    int ent_base = 0;
-    auto open_piece = [&](int take) {
-        w.r = request_of(p, b);
-        const DecSpan s = dec_span(p, w.r);
-        w.j0 = s.j0;
-        w.e_last = last_seen(p, w.r, w.r.n - 1);
-        w.tile0 = off * kDecWarps + warp;
-        const int all = w.e_last < w.j0 ? 0 : (w.e_last - w.j0) / kDecTile + 1;  // tiles that hold a seen key
+    constexpr int kRow = D / 8;        // lanes a row
+    const int crow = lane / kRow, cch = lane % kRow;  // this lane's row and 16-byte piece of a copy step
+    int j0, e_last, tile0, tiles;      // of the piece: first key, last key seen, this warp's first tile and their number
+    int off, take;                     // units of the pair before the piece, and in it
+    int ent[2], ent_base;              // table entries of the tiles ent_base + lane
+    auto open_piece = [&] {
+        off = (int)(u0 > s0 + kDecPair ? u0 - s0 - kDecPair : 0);
+        take = (int)(u1 - s0 - kDecPair < sp.units ? u1 - s0 - kDecPair : sp.units) - off;
+        j0 = sp.j0;
+        e_last = last_seen(p, r, r.n - 1);
+        tile0 = off * kDecWarps + warp;
+        const int all = e_last < j0 ? 0 : (e_last - j0) / kDecTile + 1;  // tiles that hold a seen key
         const int end = min((off + take) * kDecWarps, all);
-        w.tiles = w.tile0 < end ? (end - w.tile0 + kDecWarps - 1) / kDecWarps : 0;
+        tiles = tile0 < end ? (end - tile0 + kDecWarps - 1) / kDecWarps : 0;
         ent_base = -32;
     };
-    auto entries = [&](int base) {  // lane i: the pages of tile base + i
-        ent_base = base;
-        const int t = base + lane;
-        ent[0] = ent[1] = -1;
-        if (t < w.tiles) {
-            const int j = w.j0 + (w.tile0 + t * kDecWarps) * kDecTile;
-            const int* row = p.table + (int64_t)b * p.table_stride;
-            for (int i = 0; i < boxes; ++i) {
-                const int col = (j + i * box) >> p.shift;
-                if (col < p.columns) ent[i] = row[col];
+    auto issue = [&](int t, int slot) {  // the copies of the piece's tile t; a group of copies in any case
+        if (t < tiles) {
+            if (t >= ent_base + 32) {  // lane i: the pages of tile t + i
+                ent_base = t;
+                ent[0] = ent[1] = -1;
+                if (t + lane < tiles) {
+                    const int j = j0 + (tile0 + (t + lane) * kDecWarps) * kDecTile;
+                    const int* row = p.table + (int64_t)b * p.table_stride;
+                    for (int i = 0; i < boxes; ++i) {
+                        const int col = (j + i * box) >> p.shift;
+                        if (col < p.columns) ent[i] = row[col];
+                    }
+                }
             }
+            uint32_t no = 0;
+            const int j = j0 + (tile0 + t * kDecWarps) * kDecTile;
+            const uint32_t dst = ring + slot * 2 * L::kHalf + (cch >> 3) * (kDecTile * 128);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // rows 0 .. 7 and 8 .. 15
+                const int i = boxes == 2 ? h : 0;
+                int pg = __shfl_sync(0xffffffffu, ent[i], t - ent_base);
+                const bool there = pg >= 0 && pg < p.pages;
+                if (!there) {
+                    no |= 1u << i;
+                    pg = 0;
+                }
+                const int slot0 = (j + 8 * h) & (page - 1);
+                const uint16_t* kp = p.k + pg * p.kp + hk * p.kh + (int64_t)(slot0 + crow) * p.ks + cch * 8;
+                const uint16_t* vp = p.v + pg * p.vp + hk * p.vh + (int64_t)(slot0 + crow) * p.vs + cch * 8;
+#pragma unroll
+                for (int x = 0; x < 8 * kRow / 32; ++x) {
+                    const int row = 8 * h + x * (32 / kRow) + crow;
+                    const uint32_t a = dst + row * 128 + (((cch & 7) ^ (row & 7)) << 4);
+                    cp_async_16_or_zero(a, kp + (int64_t)(x * (32 / kRow)) * p.ks, there);
+                    cp_async_16_or_zero(a + L::kHalf, vp + (int64_t)(x * (32 / kRow)) * p.vs, there);
+                }
+            }
+            gone = (gone & ~(3u << (2 * slot))) | no << (2 * slot);
         }
+        cp_async_commit();
     };
-    auto issue = [&](int t) {  // the copies of this piece's tile t
-        if (t >= ent_base + 32) entries(t);
-        int pg[2];
-        uint32_t no = 0;
-        for (int i = 0; i < boxes; ++i) {
-            pg[i] = __shfl_sync(0xffffffffu, ent[i], t - ent_base);
-            if (pg[i] < 0 || pg[i] >= p.pages) {
-                pg[i] = p.pages;  // past the tensor: the copy fills with zeros
-                no |= 1u << i;
-            }
-        }
-        gone = (gone & ~(3u << (2 * put))) | no << (2 * put);
-        __syncwarp();  // every lane has read the slot's last tile
-        if (lane == 0) {
-            unsigned char* dst = ring + put * 2 * L::kHalf;
-            const int j = w.j0 + (w.tile0 + t * kDecWarps) * kDecTile;
-            mbar_arrive_expect_tx(wbar + put, 2u * L::kHalf);
-            for (int i = 0; i < boxes; ++i) {
-                const int slot = (j + i * box) & (page - 1);
+    // the query rows as A fragments: rows r = lane / 4 and r + 8 of i G + g
+    const int ra = lane >> 2, rb = ra + 8, ia = ra / p.G, ib = rb / p.G;
+    uint32_t qa[D / 16][4];
+    auto load_q = [&] {
+        const int R = r.n * p.G;
+        const uint32_t* qpa = reinterpret_cast<const uint32_t*>(
+            p.q + (int64_t)(r.t0 + ia) * p.q_token + (int64_t)(hk * p.G + ra - ia * p.G) * p.q_head) + (lane & 3);
+        const uint32_t* qpb = reinterpret_cast<const uint32_t*>(
+            p.q + (int64_t)(r.t0 + ib) * p.q_token + (int64_t)(hk * p.G + rb - ib * p.G) * p.q_head) + (lane & 3);
 #pragma unroll
-                for (int s = 0; s < L::kSlabs; ++s)
-                    tma_load_4d(dst + s * (kDecTile * 128) + i * box * 128, &tmap_k, 64 * s, slot, hk, pg[i],
-                                wbar + put);
-#pragma unroll
-                for (int s = 0; s < L::kSlabs; ++s)
-                    tma_load_4d(dst + L::kHalf + s * (kDecTile * 128) + i * box * 128, &tmap_v, 64 * s, slot, hk,
-                                pg[i], wbar + put);
-            }
+        for (int k = 0; k < D / 16; ++k) {
+            qa[k][0] = ra < R ? qpa[8 * k] : 0u;
+            qa[k][1] = rb < R ? qpb[8 * k] : 0u;
+            qa[k][2] = ra < R ? qpa[8 * k + 4] : 0u;
+            qa[k][3] = rb < R ? qpb[8 * k + 4] : 0u;
         }
-        put = put + 1 == L::kSlots ? 0 : put + 1;
     };
 
-    int64_t left = u1 - u0;
-    int units = dec_span(p, request_of(p, b)).units;
-    int take = (int)(left < units - off ? left : units - off);
-    open_piece(take);
-    int issued = 0;
-    for (; issued < w.tiles && issued < L::kSlots; ++issued) issue(issued);
+    open_piece();
+    load_q();
+    for (int i = 0; i < L::kSlots; ++i) issue(i, i);
 
     while (true) {
-        // ---- the query rows as A fragments -------------------------------
-        const int R = w.r.n * p.G;
-        const int ra = lane >> 2, rb = ra + 8;  // this thread's two rows
-        uint32_t qa[D / 16][4];
-        {
-            const int ia = ra / p.G, ib = rb / p.G;
-            const uint32_t* qpa = reinterpret_cast<const uint32_t*>(
-                p.q + (int64_t)(w.r.t0 + ia) * p.q_token + (int64_t)(hk * p.G + ra - ia * p.G) * p.q_head) + (lane & 3);
-            const uint32_t* qpb = reinterpret_cast<const uint32_t*>(
-                p.q + (int64_t)(w.r.t0 + ib) * p.q_token + (int64_t)(hk * p.G + rb - ib * p.G) * p.q_head) + (lane & 3);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                qa[k][0] = ra < R ? qpa[8 * k] : 0u;
-                qa[k][1] = rb < R ? qpb[8 * k] : 0u;
-                qa[k][2] = ra < R ? qpa[8 * k + 4] : 0u;
-                qa[k][3] = rb < R ? qpb[8 * k + 4] : 0u;
-            }
-        }
-        const int ea = ra < R ? last_seen(p, w.r, ra / p.G) : -1, eb = rb < R ? last_seen(p, w.r, rb / p.G) : -1;
+        const int R = r.n * p.G;
+        const int ea = ra < R ? last_seen(p, r, ia) : -1, eb = rb < R ? last_seen(p, r, ib) : -1;
         const int la = first_seen(p, ea), lb = first_seen(p, eb);
-        const int e_min = last_seen(p, w.r, 0), lo_min = first_seen(p, e_min);
-        const int lo_max = first_seen(p, w.e_last);
+        const int e_min = last_seen(p, r, 0), lo_min = first_seen(p, e_min);
+        const int lo_max = first_seen(p, e_last);
 
         float o[D / 8][4];
 #pragma unroll
@@ -247,15 +241,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
         float ma = -INFINITY, mb = -INFINITY, sa = 0.f, sb = 0.f;
 
-        bool ok = true;
-        for (int t = 0; t < issued; ++t) {
-            ok = mbar_wait_warp(wbar + get, parity, abort_flag, &g_decode_status) && ok;
-            // given up: the copies in flight still have to land, none is added
-            if (!ok) (void)mbar_wait_warp(wbar + get, parity, nullptr, &g_decode_status);
-            const uint32_t kb = smem_u32(ring + get * 2 * L::kHalf), vb = kb + L::kHalf;
-            const uint32_t no = (gone >> (2 * get)) & 3u;
-            const int j = w.j0 + (w.tile0 + t * kDecWarps) * kDecTile;
-            if (ok) {
+        int slot = 0;
+        for (int t = 0; t < tiles; ++t) {
+            cp_async_wait<L::kSlots - 1>();
+            __syncwarp();
+            const uint32_t kb = ring + slot * 2 * L::kHalf, vb = kb + L::kHalf;
+            const uint32_t no = (gone >> (2 * slot)) & 3u;
+            const int j = j0 + (tile0 + t * kDecWarps) * kDecTile;
+            {
                 // scores: two accumulators a column tile, even and odd steps
                 float s0[4] = {}, s1[4] = {}, s2[4] = {}, s3[4] = {};
                 {
@@ -289,7 +282,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     }
                     // values: a lane looks at half a key's row
                     const int key = lane >> 1, jj = j + key;
-                    const bool none = jj < lo_min || jj > w.e_last;  // seen by no row
+                    const bool none = jj < lo_min || jj > e_last;  // seen by no row
                     const bool some = !none && (jj < lo_max || jj > e_min);
                     bool odd = false;
                     if (none || some) {
@@ -300,15 +293,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
                                 } else {
                                     const uint4 v = lds_v4(a);
-                                    for (uint32_t y : {v.x, v.y, v.z, v.w})
-                                        odd |= !(fabsf(Ty::lo(y)) < INFINITY) || !(fabsf(Ty::hi(y)) < INFINITY);
+                                    odd |= ((Ty::all_ones(v.x) | Ty::all_ones(v.y) | Ty::all_ones(v.z) |
+                                             Ty::all_ones(v.w)) & 0x80008000u) != 0;
                                 }
                             }
                     }
                     const uint32_t lanes = __ballot_sync(0xffffffffu, odd);
                     for (int i = 0; i < kDecTile; ++i)
                         if ((lanes >> (2 * i)) & 3u) alone |= 1u << i;
-                    fence_proxy_async_smem();  // the slot's next copy comes after these stores
                     __syncwarp();
                 }
                 float na = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), nb = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
@@ -374,7 +366,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                                                  ((((lane & 1) * 4 + i) ^ (key & 7)) << 4)),
                                              "r"(0)
                                              : "memory");
-                    fence_proxy_async_smem();
                     __syncwarp();
                 }
                 // the weights in two parts, x = hi + lo to 2^-16 (2^-22 in fp16): a decoding row often
@@ -397,33 +388,29 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     mma_16816<Ty>(o[2 * n + 1], pb, f[2], f[3]);
                 }
             }
-            if (++get == L::kSlots) {
-                get = 0;
-                parity ^= 1;
-            }
-            if (ok && issued < w.tiles) issue(issued++);
+            __syncwarp();  // every lane has read the tile
+            issue(t + L::kSlots, slot);
+            slot = slot + 1 == L::kSlots ? 0 : slot + 1;
         }
 
-        // ---- the next piece's first copies, before this one's results meet ----
-        const Request r = w.r;
+        // ---- the next pair's first copies and rows, before this one's results meet ----
+        const Request done = r;
         const int done_hk = hk;
-        const int64_t first = u - off, end = first + units;  // the pair's units on the line
-        const bool from_start = off == 0, to_end = off + take == units;
-        left -= take;
-        u += take;
-        const bool more = left > 0;
+        const int64_t first = s0 + kDecPair, end = first + sp.units;  // the pair's units on the line
+        const bool from_start = off == 0, to_end = off + take == sp.units;
+        const bool more = u1 > end + kDecPair;
         if (more) {
-            off = 0;
+            s0 = end;
             if (++hk == p.Hkv) {
                 hk = 0;
                 do {
-                    ++b;
-                    units = dec_span(p, request_of(p, b)).units;
-                } while (units == 0);
+                    r = request_of(p, ++b);
+                    sp = dec_span(p, r);
+                } while (sp.units == 0);
             }
-            take = (int)(left < units ? left : units);
-            open_piece(take);
-            for (issued = 0; issued < w.tiles && issued < L::kSlots; ++issued) issue(issued);
+            open_piece();
+            load_q();
+            for (int i = 0; i < L::kSlots; ++i) issue(i, i);
         }
 
         // ---- the warps' results ------------------------------------------
@@ -465,97 +452,115 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
         }
         __syncthreads();
-        // thread: pairs of neighbouring columns of a row
+        // thread: pairs of neighbouring columns of one row
         const bool whole = from_start && to_end;
+        const int row = ((int)threadIdx.x & 31) / 4 + 8 * ((threadIdx.x >> 5) & 1);
+        float M = -INFINITY, S = 0.f;
+#pragma unroll
+        for (int i = 0; i < kDecWarps; ++i) M = fmaxf(M, ml[(i * 16 + row) * 2]);
+        const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int i = 0; i < kDecWarps; ++i) {
+            const float m = ml[(i * 16 + row) * 2], s = ml[(i * 16 + row) * 2 + 1];
+            if (s != 0.f) S = fmaf(s, exp2_approx(m == -INFINITY ? 0.f : m - base), S);
+        }
+        const int ti = row / p.G, th = done_hk * p.G + row - ti * p.G;  // the row's token and head
+        uint16_t* out = p.out + (int64_t)(done.t0 + ti) * p.o_token + (int64_t)th * p.o_head;
+        float* lse = p.lse ? p.lse + (int64_t)(done.t0 + ti) * p.Hq + th : nullptr;
         float* part = p.part + (int64_t)(2 * c + (from_start ? 1 : 0)) * L::kPart;
-        for (int e = threadIdx.x; e < 16 * D / 2; e += kDecThreads) {
-            const int ln = e & 31, half = (e >> 5) & 1, n = e >> 6;
-            const int row = (ln >> 2) + 8 * half, col = 8 * n + 2 * (ln & 3);
-            if (row >= R) continue;
-            float y0 = 0.f, y1 = 0.f;
+        if (row < R) {
+            const float inv = 1.f / S;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y0 += merge[i * (L::kRegs * 32) + (4 * n + 2 * half) * 32 + ln];
-                y1 += merge[i * (L::kRegs * 32) + (4 * n + 2 * half + 1) * 32 + ln];
-            }
-            float M = -INFINITY, S = 0.f;
+            for (int x = 0; x < D / 32; ++x) {
+                const int n = (threadIdx.x >> 6) + 4 * x, col = 8 * n + 2 * (lane & 3);
+                const float* at = merge + (4 * n + 2 * ((threadIdx.x >> 5) & 1)) * 32 + lane;
+                float y0 = 0.f, y1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < kDecWarps; ++i) M = fmaxf(M, ml[(i * 16 + row) * 2]);
-            const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-            for (int i = 0; i < kDecWarps; ++i) {
-                const float s = ml[(i * 16 + row) * 2 + 1];
-                const float m = ml[(i * 16 + row) * 2];
-                if (s != 0.f) S = fmaf(s, exp2_approx(m == -INFINITY ? 0.f : m - base), S);
-            }
-            if (whole) {
-                const int i = row / p.G, h = done_hk * p.G + row - i * p.G;
-                const float inv = 1.f / S;
-                *reinterpret_cast<uint32_t*>(p.out + (int64_t)(r.t0 + i) * p.o_token + (int64_t)h * p.o_head + col) =
-                    S == 0.f ? 0u : Ty::pack(y0 * inv, y1 * inv);
-                if (p.lse && col == 0)
-                    p.lse[(int64_t)(r.t0 + i) * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
-            } else {
-                *reinterpret_cast<float2*>(part + 32 + row * D + col) = make_float2(y0, y1);
-                if (col == 0) {
-                    part[2 * row] = M;
-                    part[2 * row + 1] = S;
+                for (int i = 0; i < 4; ++i) {
+                    y0 += at[i * (L::kRegs * 32)];
+                    y1 += at[i * (L::kRegs * 32) + 32];
                 }
+                if (whole)
+                    *reinterpret_cast<uint32_t*>(out + col) = S == 0.f ? 0u : Ty::pack(y0 * inv, y1 * inv);
+                else
+                    *reinterpret_cast<float2*>(part + 32 + row * D + col) = make_float2(y0, y1);
+            }
+            if ((threadIdx.x >> 6) == 0 && (lane & 3) == 0) {
+                if (!whole)
+                    *reinterpret_cast<float2*>(part + 2 * row) = make_float2(M, S);
+                else if (lse)
+                    *lse = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
             }
         }
         if (!whole) {
             // the pieces of CTAs c0 .. c1; the last to arrive joins them in CTA order
-            const int c0 = owner_of(first, U, C), c1 = owner_of(end - 1, U, C);
-            __threadfence();
+            const int c0 = owner_of(first, U, C), c1 = owner_of(end - 1, U, C), pieces = c1 - c0 + 1;
             __syncthreads();
             if (threadIdx.x == 0) {
+                __threadfence();  // the CTA's stores, ordered before by the barrier
                 const unsigned n = atomicAdd(p.counters + c0, 1u);
-                const int last = n == (unsigned)(c1 - c0);
+                const int last = n == (unsigned)(pieces - 1);
                 if (last) p.counters[c0] = 0;
-                misc[4] = last;
+                __threadfence();
+                misc[0] = last;
             }
             __syncthreads();
-            if (misc[4]) {
-                __threadfence();
+            if (misc[0]) {
+                // the pieces' maxima and sums, then weights, by row; then the columns
+                float2* pm = reinterpret_cast<float2*>(merge);  // [piece][R]
+                auto piece = [&](int i) { return p.part + (int64_t)(2 * (c0 + i) + (i == 0)) * L::kPart; };
+                constexpr int kRoom = L::kMerge / 8;
+                if (pieces * R <= kRoom) {
+                    for (int e = threadIdx.x; e < pieces * R; e += kDecThreads)
+                        pm[e] = __ldcg(reinterpret_cast<const float2*>(piece(e / R)) + e % R);
+                    __syncthreads();
+                }
                 for (int e = threadIdx.x; e < R * (D / 4); e += kDecThreads) {
-                    const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
-                    float M = -INFINITY;
-                    for (int i = c0; i <= c1; ++i)
-                        M = fmaxf(M, __ldcg(p.part + (int64_t)(2 * i + (i == c0)) * L::kPart + 2 * row));
-                    const float base = M == -INFINITY ? 0.f : M;
-                    float S = 0.f;
+                    const int jr = e / (D / 4), col = (e - jr * (D / 4)) * 4;
+                    auto at = [&](int i) {
+                        return pieces * R <= kRoom ? pm[i * R + jr] : __ldcg(reinterpret_cast<const float2*>(piece(i)) + jr);
+                    };
+                    float jm = -INFINITY, js = 0.f;
+                    for (int i = 0; i < pieces; ++i) jm = fmaxf(jm, at(i).x);
+                    const float jb = jm == -INFINITY ? 0.f : jm;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int i = c0; i <= c1; ++i) {
-                        const float* q = p.part + (int64_t)(2 * i + (i == c0)) * L::kPart;
-                        const float2 mi = __ldcg(reinterpret_cast<const float2*>(q + 2 * row));
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(q + 32 + row * D + col));
-                        if (mi.y == 0.f) continue;  // no seen key in this piece
-                        const float f = exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - base);
-                        S = fmaf(mi.y, f, S);
-                        y.x = fmaf(x.x, f, y.x);
-                        y.y = fmaf(x.y, f, y.y);
-                        y.z = fmaf(x.z, f, y.z);
-                        y.w = fmaf(x.w, f, y.w);
+                    for (int i0 = 0; i0 < pieces; i0 += 8) {
+                        float4 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i0 + i < pieces)
+                                x[i] = __ldcg(reinterpret_cast<const float4*>(piece(i0 + i) + 32 + jr * D + col));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (i0 + i >= pieces) continue;
+                            const float2 mi = at(i0 + i);
+                            if (mi.y == 0.f) continue;  // no seen key in this piece
+                            const float f = exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - jb);
+                            js = fmaf(mi.y, f, js);
+                            y.x = fmaf(x[i].x, f, y.x);
+                            y.y = fmaf(x[i].y, f, y.y);
+                            y.z = fmaf(x[i].z, f, y.z);
+                            y.w = fmaf(x[i].w, f, y.w);
+                        }
                     }
-                    const int i = row / p.G, h = done_hk * p.G + row - i * p.G;
-                    const float inv = 1.f / S;
+                    const int i = jr / p.G, h = done_hk * p.G + jr - i * p.G;
+                    const float inv = 1.f / js;
                     uint2 v = make_uint2(0u, 0u);
-                    if (S != 0.f) v = make_uint2(Ty::pack(y.x * inv, y.y * inv), Ty::pack(y.z * inv, y.w * inv));
-                    *reinterpret_cast<uint2*>(p.out + (int64_t)(r.t0 + i) * p.o_token + (int64_t)h * p.o_head + col) = v;
+                    if (js != 0.f) v = make_uint2(Ty::pack(y.x * inv, y.y * inv), Ty::pack(y.z * inv, y.w * inv));
+                    *reinterpret_cast<uint2*>(p.out + (int64_t)(done.t0 + i) * p.o_token + (int64_t)h * p.o_head + col) = v;
                     if (p.lse && col == 0)
-                        p.lse[(int64_t)(r.t0 + i) * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
+                        p.lse[(int64_t)(done.t0 + i) * p.Hq + h] = js == 0.f ? -INFINITY : kLn2 * (jm + log2f(js));
                 }
             }
         }
         if (!more) break;
         __syncthreads();  // ml and merge are free again
     }
+    cp_async_wait<0>();
 }
 
 template <typename Ty, int D>
-static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnParams& p, int ctas,
-                          cudaStream_t s, bool pdl) {
+static cudaError_t launch(const PagedAttnParams& p, int ctas, cudaStream_t s, bool pdl) {
     static bool set_for[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -566,8 +571,7 @@ static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
         if (e != cudaSuccess) return e;
         set_for[dev] = true;
     }
-    return launch_kernel(paged_decode_kernel<Ty, D>, dim3(ctas), dim3(kDecThreads), (size_t)Dec<D>::kSmem, s, pdl, tk,
-                         tv, p);
+    return launch_kernel(paged_decode_kernel<Ty, D>, dim3(ctas), dim3(kDecThreads), (size_t)Dec<D>::kSmem, s, pdl, p);
 }
 
 size_t paged_decode_part_bytes(int d, int sms) {
@@ -575,18 +579,8 @@ size_t paged_decode_part_bytes(int d, int sms) {
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl) {
-    CUtensorMap tk, tv;
-    const int box = (1 << p.shift) < kDecTile ? 1 << p.shift : kDecTile;
-    if (!paged_tmap(&tk, p, bf16, d, false, box) || !paged_tmap(&tv, p, bf16, d, true, box)) return cudaErrorInvalidValue;
-    if (bf16) return d == 128 ? launch<Bf16, 128>(tk, tv, p, sms, s, pdl) : launch<Bf16, 64>(tk, tv, p, sms, s, pdl);
-    return d == 128 ? launch<F16, 128>(tk, tv, p, sms, s, pdl) : launch<F16, 64>(tk, tv, p, sms, s, pdl);
-}
-
-int decode_read_status() {
-    int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&v, g_decode_status, sizeof(int)) != cudaSuccess) return W4A16_ECUDA;
-    if (cudaMemcpyToSymbol(g_decode_status, &zero, sizeof(int)) != cudaSuccess) return W4A16_ECUDA;
-    return v;
+    if (bf16) return d == 128 ? launch<Bf16, 128>(p, sms, s, pdl) : launch<Bf16, 64>(p, sms, s, pdl);
+    return d == 128 ? launch<F16, 128>(p, sms, s, pdl) : launch<F16, 64>(p, sms, s, pdl);
 }
 
 }  // namespace w4a16
