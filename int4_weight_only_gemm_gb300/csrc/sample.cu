@@ -36,7 +36,7 @@
 
 namespace w4a16 {
 
-constexpr int kStatThreads = 1024, kPickThreads = 512;
+constexpr int kStatThreads = 512, kPickThreads = 512;
 constexpr int kList = 2048;   // candidates that are sorted
 constexpr int kBins = 4096;   // of the histogram of a flat row
 constexpr int kMaxSplits = 8; // CTAs a row
@@ -161,6 +161,11 @@ W4A16_DEVICE float cta_before(float x, float* f) {
 }
 
 // ---- a CTA's slice of a row ----------------------------------------------------
+// Tokens that a warp has set aside: fewer than 32, and up to 256 of one load.
+struct Aside {
+    float l[288];
+    int i[288];
+};
 template <int DT, int NT>
 struct Slice {
     static constexpr int VE = DT == W4A16_F32 ? 4 : 8;  // logits of a 16-byte load
@@ -219,12 +224,65 @@ struct Slice {
         }
         if (last && tail + (int)threadIdx.x < V) one(at(tail + (int)threadIdx.x), tail + (int)threadIdx.x);
     }
+    // one(logit, index) for the tokens with a logit >= low, by the whole CTA.
+    // They are set aside per warp and handed over 32 at a time, so that `one`,
+    // which divides, counts or collects, runs with full warps however rare they
+    // are, and is there once and not for every load.
     template <typename One>
-    W4A16_DEVICE void each(One one) const {
-        each(one, [&](const float (&l)[VE], int i0) {
+    W4A16_DEVICE void from(float low, Aside* aside, One one) const {
+        constexpr int U = 4;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        Aside& own = aside[warp];
+        int count = 0;  // set aside, the same in every lane
+        auto put = [&](float l, int i) {
+            const bool hit = l >= low && l > -INFINITY;
+            const unsigned m = __ballot_sync(0xffffffffu, hit);
+            if (!m) return;
+            if (hit) {
+                const int at = count + __popc(m & ((1u << lane) - 1u));
+                own.l[at] = l;
+                own.i[at] = i;
+            }
+            count += __popc(m);
+        };
+        auto hand_over = [&](int least) {
+            while (count >= least && count > 0) {
+                __syncwarp();
+                const int n = count < 32 ? count : 32, at = count - n + lane;
+                const float l = lane < n ? own.l[at] : 0.f;
+                const int i = lane < n ? own.i[at] : 0;
+                count -= n;
+                __syncwarp();
+                if (lane < n) one(l, i);
+                __syncwarp();
+            }
+        };
+        if (first && warp == 0) put(lane < head ? at(lane) : -INFINITY, lane);
+        const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+        for (int v = v0 + warp * 32; v < v1; v += U * NT) {
+            uint4 x[U];
 #pragma unroll
-            for (int x = 0; x < VE; ++x) one(l[x], i0 + x);
-        });
+            for (int u = 0; u < U; ++u) {
+                const int y = v + u * NT + lane;
+                x[u] = y < v1 ? vec[y] : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int y = v + u * NT + lane;
+                float l[VE];
+                split(x[u], l);
+                float b = l[0];
+#pragma unroll
+                for (int z = 1; z < VE; ++z) b = fmaxf(b, l[z]);
+                if (!__any_sync(0xffffffffu, y < v1 && b >= low)) continue;
+#pragma unroll
+                for (int z = 0; z < VE; ++z) put(y < v1 ? l[z] : -INFINITY, head + y * VE + z);
+                hand_over(32);
+            }
+        }
+        if (last && warp == 0) put(tail + lane < V ? at(tail + lane) : -INFINITY, tail + lane);
+        hand_over(32);
+        hand_over(1);
     }
     W4A16_DEVICE float at(int i) const { return decode<DT>(row[i]); }
 };
@@ -263,29 +321,36 @@ W4A16_DEVICE void write_row(const w4a16_sample_args& p, int r, const Slice<DT, N
     if (p.logprob) p.logprob[r] = (z_of(row.at(token), q.T) - z_of(lmax, q.T)) - logf(sum);
 }
 
-// The slices' results as one, in slice order.
+// The slices' results as one, the sums added in slice order; by whole warps.
 struct RowStats {
     float lmax, sum, tau, best;
     int imax, ibest;
     W4A16_DEVICE RowStats(const SliceStats* s, int S, float c2) {
-        lmax = tau = best = -INFINITY;
+        const int lane = threadIdx.x & 31;
+        const bool on = lane < S;
+        const float mine = on ? __ldcg(&s[lane].lmax) : -INFINITY, part = on ? __ldcg(&s[lane].sum) : 0.f;
+        lmax = mine;
+        tau = on ? __ldcg(&s[lane].tau) : -INFINITY;
+        best = on ? __ldcg(&s[lane].best) : -INFINITY;
+        imax = on ? __ldcg(&s[lane].imax) : 0x7fffffff;
+        ibest = on ? __ldcg(&s[lane].ibest) : 0x7fffffff;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, lmax, d), y = __shfl_xor_sync(0xffffffffu, best, d);
+            const int i = __shfl_xor_sync(0xffffffffu, imax, d), j = __shfl_xor_sync(0xffffffffu, ibest, d);
+            join_best(lmax, imax, x, i);
+            join_best(best, ibest, y, j);
+            tau = fmaxf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
+        }
+        const float scaled = mine == -INFINITY ? 0.f : part * ex2((mine - lmax) * c2);
         sum = 0.f;
-        imax = ibest = 0x7fffffff;
-        for (int i = 0; i < S; ++i) {
-            join_best(lmax, imax, __ldcg(&s[i].lmax), __ldcg(&s[i].imax));
-            tau = fmaxf(tau, __ldcg(&s[i].tau));
-            join_best(best, ibest, __ldcg(&s[i].best), __ldcg(&s[i].ibest));
-        }
-        for (int i = 0; i < S; ++i) {
-            const float x = __ldcg(&s[i].lmax);
-            if (x != -INFINITY) sum += __ldcg(&s[i].sum) * ex2((x - lmax) * c2);
-        }
+        for (int i = 0; i < S; ++i) sum += __shfl_sync(0xffffffffu, scaled, i);
     }
 };
 
 // ---- 1. maximum, sum, and the race of unfiltered rows ---------------------------
 template <int DT>
-__global__ void __launch_bounds__(kStatThreads) sample_stats_kernel(const w4a16_sample_args p, const int S,
+__global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a16_sample_args p, const int S,
                                                                     const int filters) {
     constexpr int NT = kStatThreads;
     __shared__ float rf[32];
@@ -300,78 +365,140 @@ __global__ void __launch_bounds__(kStatThreads) sample_stats_kernel(const w4a16_
     const bool race = q.race;
     const float inv_t = fminf(1.f / q.T, kBig);
 
-    float mx = -kBig, sum = 0.f, best = -INFINITY;
-    int imax = V, ibest = 0x7fffffff;
+    float mx = -kBig, sum = 0.f;
+    int vmax = -1;  // the load in which mx came first: a token below V, or V + a vector's first token
+    // The race runs on approximate scores, l / T - log e, with errors below
+    // 2^-21 |z| + 2^-20 and |z| <= |score| + 104 for any finite noise: a thread
+    // keeps its two best loads, and the exact scores of the few loads that come
+    // near the CTA's best decide.
+    float top = -INFINITY, top2 = -INFINITY;
+    int vtop = -1;
+    constexpr int VE = Slice<DT, NT>::VE;
+    auto approx = [&](float l, float e) { return fmaf(l, inv_t, -0.6931471805599453f * lg2(e)); };
+    auto enter = [&](float t, int at) {
+        top2 = fmaxf(top2, fminf(top, t));
+        if (t > top) {
+            top = t;
+            vtop = at;
+        }
+    };
+    auto maximum = [&](float b, int at) {  // -kBig itself may be the first
+        if (b > mx || (vmax < 0 && b == -kBig)) {
+            sum *= ex2((mx - b) * q.c2);
+            mx = b;
+            vmax = at;
+        }
+    };
+    auto one = [&](float l, int i) {
+        maximum(l, i);
+        sum += ex2((l - mx) * q.c2);
+        if (race && l > -INFINITY) enter(approx(l, noise[i]), i);
+    };
+    auto many = [&](const float (&l)[VE], int i0) {
+        float b = l[0];
+#pragma unroll
+        for (int x = 1; x < VE; ++x) b = fmaxf(b, l[x]);
+        maximum(b, V + i0);
+        float s = 0.f;
+#pragma unroll
+        for (int x = 0; x < VE; ++x) s += ex2((l[x] - mx) * q.c2);
+        sum += s;
+    };
     const bool noise4 = (reinterpret_cast<uintptr_t>(noise + slice.head) & 15) == 0;
-    auto try_race = [&](float l, float e, int i) {
-        // the approximate score decides whether the exact one is worth computing: its error is below
-        // 2^-21 |z| + 2^-20, and |z| <= |score| + 104 for any finite noise
-        const float s = fmaf(l, inv_t, -0.6931471805599453f * lg2(e));
-        if (fmaf(fabsf(s), 4e-6f, s) + 1e-3f > best || e == 0.f) {
-            const float x = z_of(l, q.T) - logf(e);
-            if (x > best && l > -INFINITY) {
+    if (!race) {
+        slice.each(one, many);
+    } else if (noise4) {
+        // logits and their random numbers together, U vectors in flight
+        constexpr int U = 4, NE = VE / 4;
+        const uint4* vec = reinterpret_cast<const uint4*>(slice.row + slice.head);
+        const float4* nv = reinterpret_cast<const float4*>(noise + slice.head);
+        if (slice.first && (int)threadIdx.x < slice.head) one(slice.at((int)threadIdx.x), (int)threadIdx.x);
+        for (int v = slice.v0 + (int)threadIdx.x; v < slice.v1; v += U * NT) {
+            uint4 x[U];
+            float4 e[U][NE];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int y = min(v + u * NT, slice.v1 - 1);  // past the end: again, and not counted
+                x[u] = __ldcs(vec + y);
+#pragma unroll
+                for (int z = 0; z < NE; ++z) e[u][z] = __ldcs(nv + y * NE + z);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (v + u * NT >= slice.v1) break;
+                const int i0 = slice.head + (v + u * NT) * VE;
+                float l[VE], t = -INFINITY;
+                slice.split(x[u], l);
+                many(l, i0);
+#pragma unroll
+                for (int z = 0; z < NE; ++z)
+                    t = fmaxf(t, fmaxf(fmaxf(approx(l[4 * z], e[u][z].x), approx(l[4 * z + 1], e[u][z].y)),
+                                       fmaxf(approx(l[4 * z + 2], e[u][z].z), approx(l[4 * z + 3], e[u][z].w))));
+                enter(t, V + i0);
+            }
+        }
+        if (slice.last && slice.tail + (int)threadIdx.x < V)
+            one(slice.at(slice.tail + (int)threadIdx.x), slice.tail + (int)threadIdx.x);
+    } else {  // a row whose random numbers are not aligned as its logits are
+        slice.each(one, [&](const float (&l)[VE], int i0) {
+            many(l, i0);
+            float t = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < VE; ++x) t = fmaxf(t, approx(l[x], noise[i0 + x]));
+            enter(t, V + i0);
+        });
+    }
+    const float mine = vmax >= 0 ? mx : -INFINITY;  // this thread's largest logit
+    float lmax = mine;
+    int imax = vmax >= 0 ? (vmax < V ? vmax : vmax - V) : 0x7fffffff;  // the first token of its load
+    cta_best<NT>(lmax, imax, rf, ri);
+    if (lmax > -INFINITY)  // the token itself: loads rise with the threads' first tokens, so the lowest holds the lowest
+        for (int x = 0; x < VE && imax + x < V; ++x)
+            if (slice.at(imax + x) == lmax) {
+                imax += x;
+                break;
+            }
+    sum = cta_sum<NT>(mine == -INFINITY ? 0.f : sum * ex2((mine - lmax) * q.c2), rf);
+    float best = -INFINITY;
+    int ibest = 0x7fffffff;
+    if (race) {
+        float lead = top;
+        int none = 0;
+        cta_best<NT>(lead, none, rf, ri);
+        const float near = lead - 2e-3f - 8e-6f * fabsf(lead);  // (NaN where lead is infinite: all compare true below)
+        auto exact = [&](int i) {
+            const float l = slice.at(i);
+            const float x = z_of(l, q.T) - logf(noise[i]);
+            if (l > -INFINITY && (x > best || (x == best && i < ibest))) {
                 best = x;
                 ibest = i;
             }
-        }
-    };
-    auto maximum = [&](float b) {  // a new one; -kBig itself may be the first
-        if (b > mx || (imax == V && b == -kBig)) {
-            sum *= ex2((mx - b) * q.c2);
-            mx = b;
-            return true;
-        }
-        return false;
-    };
-    constexpr int VE = Slice<DT, NT>::VE;
-    slice.each(
-        [&](float l, int i) {
-            if (maximum(l)) imax = i;
-            sum += ex2((l - mx) * q.c2);
-            if (race) try_race(l, noise[i], i);
-        },
-        [&](const float (&l)[VE], int i0) {
-            float b = l[0];
-#pragma unroll
-            for (int x = 1; x < VE; ++x) b = fmaxf(b, l[x]);
-            if (maximum(b)) {
-#pragma unroll
-                for (int x = VE - 1; x >= 0; --x)
-                    if (l[x] == b) imax = i0 + x;
+        };
+        auto all_of = [&](int at) {  // a load's tokens
+            if (at < 0) return;
+#pragma unroll 1
+            for (int x = 0; x < (at < V ? 1 : VE); ++x) exact((at < V ? at : at - V) + x);
+        };
+        if (!(top < near)) {
+            if (!(top2 < near)) {
+                slice.each([&](float, int i) { all_of(i); }, [&](const float (&)[VE], int i0) { all_of(V + i0); });
+            } else {
+                all_of(vtop);
             }
-            float s = 0.f;
-#pragma unroll
-            for (int x = 0; x < VE; ++x) s += ex2((l[x] - mx) * q.c2);
-            sum += s;
-            if (race) {
-                if (noise4) {
-#pragma unroll
-                    for (int x = 0; x < VE; x += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(noise + i0 + x);
-                        try_race(l[x], e.x, i0 + x);
-                        try_race(l[x + 1], e.y, i0 + x + 1);
-                        try_race(l[x + 2], e.z, i0 + x + 2);
-                        try_race(l[x + 3], e.w, i0 + x + 3);
-                    }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < VE; ++x) try_race(l[x], noise[i0 + x], i0 + x);
-                }
-            }
-        });
-    const float mine = imax < V ? mx : -INFINITY;  // this thread's largest logit
-    float lmax = mine;
-    cta_best<NT>(lmax, imax, rf, ri);
-    sum = cta_sum<NT>(mine == -INFINITY ? 0.f : sum * ex2((mine - lmax) * q.c2), rf);
-    if (race) cta_best<NT>(best, ibest, rf, ri);
-    // k tokens of this slice at least are as large as the k-th largest of its threads' maxima
+        }
+        cta_best<NT>(best, ibest, rf, ri);
+    }
+    // m tokens of this slice at least are as large as the m-th largest of its
+    // threads' maxima: m = k for top-k; for top-p as many as the list has good
+    // room for, which most nuclei lie within
     float tau = -INFINITY;
-    if (q.by_k && q.k <= NT / 2) {
+    const int m = q.by_k ? q.k : max(kList / 2 / S, NT / 4);
+    if ((q.by_k && m <= NT / 2) || (q.by_p && !q.by_k)) {
         uint32_t lo = key_of(-INFINITY), hi = key_of(lmax);
         const uint32_t y = key_of(mine);
         for (int b = 0; b < 16 && lo < hi; ++b) {
             const uint32_t mid = lo + (hi - lo + 1) / 2;
-            if (__syncthreads_count(y >= mid) >= q.k) lo = mid; else hi = mid - 1;
+            if (__syncthreads_count(y >= mid) >= min(m, NT / 2)) lo = mid; else hi = mid - 1;
         }
         tau = value_of(lo);
     }
@@ -400,18 +527,40 @@ __global__ void __launch_bounds__(kStatThreads) sample_stats_kernel(const w4a16_
         if (last) *counter = 0;
     }
     __syncthreads();
-    if (last && threadIdx.x == 0) {
+    if (last && threadIdx.x < 32) {
         __threadfence();
         const RowStats a(space->stats, S, q.c2);
-        write_row<DT, NT>(p, r, slice, q, q.greedy ? a.imax : a.ibest, a.imax, a.lmax, a.sum);
+        if (threadIdx.x == 0) write_row<DT, NT>(p, r, slice, q, q.greedy ? a.imax : a.ibest, a.imax, a.lmax, a.sum);
     }
 }
 
-// the candidate list, by rising key and then by rising index: bitonic, n a power of two
+// The candidate list, by rising key and then by rising index: bitonic, n a
+// power of two, 32 at least.  Steps between entries less than 32 apart stay in
+// the registers of a warp.
 template <int NT>
 W4A16_DEVICE void sort_list(uint32_t* key, int* idx, int n) {
-    for (int k = 2; k <= n; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
+    auto in_warp = [&](int k0, int k1) {  // stages k0 .. k1, their steps of 16 and less
+        for (int t = threadIdx.x; t < n; t += NT) {
+            uint32_t x = key[t];
+            int u = idx[t];
+            for (int k = k0; k <= k1; k <<= 1)
+                for (int j = min(k >> 1, 16); j > 0; j >>= 1) {
+                    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+                    const int v = __shfl_xor_sync(0xffffffffu, u, j);
+                    const bool less = y < x || (y == x && v < u);
+                    if (less == (((t & k) == 0) == ((t & j) == 0))) {
+                        x = y;
+                        u = v;
+                    }
+                }
+            key[t] = x;
+            idx[t] = u;
+        }
+    };
+    __syncthreads();
+    in_warp(2, 32);
+    for (int k = 64; k <= n; k <<= 1) {
+        for (int j = k >> 1; j >= 32; j >>= 1) {
             __syncthreads();
             for (int t = threadIdx.x; t < n / 2; t += NT) {
                 const int a = 2 * t - (t & (j - 1)), b = a + j;
@@ -425,6 +574,9 @@ W4A16_DEVICE void sort_list(uint32_t* key, int* idx, int n) {
                 }
             }
         }
+        __syncthreads();
+        in_warp(k, k);
+    }
     __syncthreads();
 }
 
@@ -434,9 +586,11 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     constexpr int NT = kPickThreads;
     __shared__ float rf[32];
     __shared__ int ri[32];
-    __shared__ uint32_t list_z[kList];
-    __shared__ int list_i[kList];
-    __shared__ int hist[kBins];
+    extern __shared__ unsigned char pick_smem[];
+    uint32_t* list_z = reinterpret_cast<uint32_t*>(pick_smem);
+    int* list_i = reinterpret_cast<int*>(list_z + kList);
+    int* hist = list_i + kList;
+    Aside* aside = reinterpret_cast<Aside*>(hist + kBins);  // one a warp
     __shared__ int win[8];    // windows of bins (two), tokens above and between, list length, last arrival
     __shared__ float bound[2];
     pdl_launch_dependents();
@@ -474,19 +628,22 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     if (q.by_p && !q.by_k) R = fminf(fmaxf(logf((float)V / ((1.f - q.tp) * sum)), 0.f) + 0.02f, 80.f);
     float low = lmax - R * T * 1.0001f;
     bool listed = q.by_p && !q.by_k;  // whether the candidates may be few
+    bool all = true;                  // whether every token that may be kept is among them
+    const float wide = low;
     if (q.by_k && st.tau != -INFINITY) {
         low = st.tau;
         listed = true;
+    } else if (!q.by_k && st.tau > low) {
+        low = st.tau;
+        all = false;  // the nucleus may reach further: its weight will tell
     }
     if (V <= kList) {
         low = -kBig;
-        listed = true;
+        listed = all = true;
     }
     if (alone) {
         const float floor_l = (zmax + least) * T - fabsf(zmax * T) * 1e-5f - 1e-5f;  // no token below it passes
-        slice.each([&](float l, int i) {
-            if (l >= floor_l && l > -INFINITY) score(z_of(l, T), i);
-        });
+        slice.from(floor_l, aside, [&](float l, int i) { score(z_of(l, T), i); });
         cta_best<NT>(best, ibest, rf, ri);
         if (threadIdx.x == 0) {
             space->stats[rank].best = best;
@@ -494,8 +651,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         }
     } else if (listed) {
         bool full = false;  // a list that has overflowed takes no more from this thread
-        slice.each([&](float l, int i) {
-            if (l >= low && l > -INFINITY && !full) {
+        slice.from(low, aside, [&](float l, int i) {
+            if (!full) {
                 const int at = atomicAdd(&space->found, 1);
                 if (at < kList) {
                     space->key[at] = ~key_of(z_of(l, T));
@@ -522,12 +679,14 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         __syncthreads();
     }
     if (alone) {
+        if (threadIdx.x >= 32) return;
         const RowStats a(space->stats, S, q.c2);
         if (threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, a.ibest, a.imax, lmax, sum);
         return;
     }
     int n = listed ? __ldcg(&space->found) : kList + 1;
-    if (n <= kList) {
+    bool flat = n > kList;
+    if (!flat) {
         for (int i = threadIdx.x; i < n; i += NT) {
             list_z[i] = __ldcg(space->key + i);
             list_i[i] = __ldcg(space->index + i);
@@ -537,7 +696,10 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     int above = 0, between = 0;        // tokens above the windows around the cuts, and between them
     float mass_a = 0.f, mass_b = 0.f;  // their weights
     bool slow = false;
-    if (n > kList) {
+    while (true) {
+    if (flat) {
+        if (!all) low = wide;
+        all = true;
         // ---- 4. too many: bins of equal width in l, from the maximum down
         for (int i = threadIdx.x; i < kBins; i += NT) hist[i] = 0;
         if (threadIdx.x == 0) win[6] = 0;
@@ -549,9 +711,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
             return (int)(__float_as_uint(fminf((lmax - l) * scale, (float)(kBins - 1)) + 8388608.f) & 0x7fffffu);
         };
         __syncthreads();
-        row.each([&](float l, int) {
-            if (l >= low && l > -INFINITY) atomicAdd(&hist[bin_of(l)], 1);
-        });
+        row.from(low, aside, [&](float l, int) { atomicAdd(&hist[bin_of(l)], 1); });
         __syncthreads();
         // thread: PB bins; sums of counts, and of least and greatest weights, before them
         constexpr int PB = kBins / NT;
@@ -623,8 +783,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
             }
             above = cta_count<NT>(ca, ri);
             between = cta_count<NT>(cc, ri);
-            row.each([&](float l, int i) {
-                if (!(l >= low && l > -INFINITY)) return;
+            row.from(low, aside, [&](float l, int i) {
                 const int b = bin_of(l);
                 if (b < b1) {
                     const float z = z_of(l, T);
@@ -646,45 +805,50 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
             slow = n > kList;
         }
     }
-    if (!slow) {
-        // ---- 3. the list decides
-        int size = 1;
-        while (size < n) size <<= 1;
-        for (int i = n + (int)threadIdx.x; i < size; i += NT) {
-            list_z[i] = 0xffffffffu;
-            list_i[i] = 0x7fffffff;
-        }
-        sort_list<NT>(list_z, list_i, size);
-        constexpr int PL = kList / NT;
-        const int base = threadIdx.x * PL;
-        // entries that top-k keeps (a second window lies behind `between` tokens)
-        const int kept_k = q.by_k ? min(n, k - above - between) : n;
-        float w[PL], wt = 0.f;
+    if (slow) break;
+    // ---- 3. the list decides
+    int size = 32;
+    while (size < n) size <<= 1;
+    for (int i = n + (int)threadIdx.x; i < size; i += NT) {
+        list_z[i] = 0xffffffffu;
+        list_i[i] = 0x7fffffff;
+    }
+    sort_list<NT>(list_z, list_i, size);
+    constexpr int PL = kList / NT;
+    const int base = threadIdx.x * PL;
+    // entries that top-k keeps (a second window lies behind `between` tokens)
+    const int kept_k = q.by_k ? min(n, k - above - between) : n;
+    float w[PL], wt = 0.f;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            w[i] = base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
-            wt += w[i];
-        }
-        const float before = cta_before(wt, rf);
-        float total = sum;
-        if (q.by_k) total = mass_a + mass_b + cta_sum<NT>(wt, rf);
-        const float want = q.by_p ? q.tp * total : INFINITY;
-        float at = mass_a + before;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            if (base + i < kept_k && (!q.by_p || at < want || (above == 0 && base + i == 0)))
-                score(value_of(~list_z[base + i]), list_i[base + i]);
-            at += w[i];
-        }
-        cta_best<NT>(best, ibest, rf, ri);
-    } else {
+    for (int i = 0; i < PL; ++i) {
+        w[i] = base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
+        wt += w[i];
+    }
+    const float before = cta_before(wt, rf), listed_mass = cta_sum<NT>(wt, rf);
+    const float total = q.by_k ? mass_a + mass_b + listed_mass : sum;
+    const float want = q.by_p ? q.tp * total : INFINITY;
+    if (!all && listed_mass < want) {
+        flat = true;  // the nucleus reaches below the list
+        continue;
+    }
+    float at = mass_a + before;
+#pragma unroll 1
+    for (int i = 0; i < PL; ++i) {
+        if (base + i < kept_k && (!q.by_p || at < want || (above == 0 && base + i == 0)))
+            score(value_of(~list_z[base + i]), list_i[base + i]);
+        at += base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
+    }
+    cta_best<NT>(best, ibest, rf, ri);
+    break;
+    }
+    if (slow) {
         // ---- 5. bisection
         best = -INFINITY, ibest = 0x7fffffff;
         uint32_t cut = 0;  // keys above it are kept, and `ties` of those equal to it
         int ties = V;
         auto count = [&](uint32_t c) {
             int m = 0;
-            row.each([&](float l, int) { m += key_of(z_of(l, T)) >= c; });
+            row.from(-INFINITY, aside, [&](float l, int) { m += key_of(z_of(l, T)) >= c; });
             return cta_count<NT>(m, ri);
         };
         if (q.by_k) {
@@ -702,7 +866,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
             const int top_ties = ties;
             auto mass = [&](uint32_t c) {  // weight of the kept tokens with a key >= c
                 float s = 0.f;
-                row.each([&](float l, int) {
+                row.from(-INFINITY, aside, [&](float l, int) {
                     const float z = z_of(l, T);
                     const uint32_t y = key_of(z);
                     if (y >= c && y > top) s += weight(z);
@@ -732,10 +896,10 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
             int m = 0;
-            row.each([&](float l, int i) { m += i < mid && key_of(z_of(l, T)) == cut; });
+            row.from(-INFINITY, aside, [&](float l, int i) { m += i < mid && key_of(z_of(l, T)) == cut; });
             if (cta_count<NT>(m, ri) >= ties) hi = mid; else lo = mid + 1;
         }
-        row.each([&](float l, int i) {
+        row.from(-INFINITY, aside, [&](float l, int i) {
             const float z = z_of(l, T);
             const uint32_t y = key_of(z);
             if (l > -INFINITY && (y > cut || (y == cut && i < lo))) score(z, i);
@@ -745,10 +909,13 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     if (threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, ibest, st.imax, lmax, sum);
 }
 
-// CTAs a row: as many as keep the SMs at up to two CTAs each, slices of 4096 tokens at least
+// CTAs a row: 8 where that fills the SMs (two CTAs each) at most once, else 4,
+// with slices of 4096 tokens at least.  Four at any number of rows: their
+// threads' maxima are what the candidates are found by, and finer slices even
+// out the last wave.
 static int splits_of(int rows, int vocab, int sms) {
-    int S = kMaxSplits;
-    while (S > 1 && ((int64_t)rows * S > 2 * sms || vocab / S < 4096)) S >>= 1;
+    int S = rows * (int64_t)8 <= 2 * sms ? 8 : 4;
+    while (S > 1 && vocab / S < 4096) S >>= 1;
     return rows > kSampleSplitRows ? 1 : S;
 }
 
@@ -766,7 +933,18 @@ static cudaError_t launch(const w4a16_sample_args& a, int S, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     note_launch();
     if (!filters) return cudaSuccess;
-    e = launch_kernel(sample_pick_kernel<DT>, grid, dim3(kPickThreads), 0, s, pdl, a, S);
+    constexpr int smem = kList * 8 + kBins * 4 + kPickThreads / 32 * (int)sizeof(Aside);
+    static bool set_for[64];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set_for[dev]) {
+        e = cudaFuncSetAttribute(sample_pick_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        set_for[dev] = true;
+    }
+    e = launch_kernel(sample_pick_kernel<DT>, grid, dim3(kPickThreads), (size_t)smem, s, pdl, a, S);
     if (e == cudaSuccess) note_launch();
     return e;
 }
