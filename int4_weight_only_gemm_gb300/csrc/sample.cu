@@ -308,6 +308,11 @@ struct RowParams {
 };
 
 // The row's token and its log-probability, by one thread.
+W4A16_DEVICE void write_token(const w4a16_sample_args& p, int r, int token, float z, float zmax, float sum) {
+    p.token[r] = token;
+    if (p.logprob) p.logprob[r] = (z - zmax) - logf(sum);
+}
+// The same where the logit has to be read, or there is none.
 template <int DT, int NT>
 W4A16_DEVICE void write_row(const w4a16_sample_args& p, int r, const Slice<DT, NT>& row, const RowParams& q, int token,
                             int imax, float lmax, float sum) {
@@ -317,8 +322,7 @@ W4A16_DEVICE void write_row(const w4a16_sample_args& p, int r, const Slice<DT, N
         return;
     }
     if (token < 0 || token >= p.vocab) token = imax;  // the noise of every kept token was infinite or NaN
-    p.token[r] = token;
-    if (p.logprob) p.logprob[r] = (z_of(row.at(token), q.T) - z_of(lmax, q.T)) - logf(sum);
+    write_token(p, r, token, z_of(row.at(token), q.T), z_of(lmax, q.T), sum);
 }
 
 // The slices' results as one, the sums added in slice order; by whole warps.
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     }
     const float zmax = z_of(lmax, T);
     const float least = q.by_m ? fminf(logf(q.mp), 0.f) : -INFINITY;  // of z - zmax
-    float best = -INFINITY;
+    float best = -INFINITY, zbest = 0.f;
     int ibest = 0x7fffffff;
     auto score = [&](float z, int i) {
         if (!(z - zmax >= least)) return;
@@ -617,6 +621,16 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         if (x > best || (x == best && i < ibest)) {
             best = x;
             ibest = i;
+            zbest = z;
+        }
+    };
+    auto settle = [&] {  // the CTA's best: the thread that has it writes
+        const int mine = ibest;
+        cta_best<NT>(best, ibest, rf, ri);
+        if (ibest == 0x7fffffff) {
+            if (threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, ibest, st.imax, lmax, sum);
+        } else if (mine == ibest) {
+            write_token(p, r, ibest, zbest, zmax, sum);
         }
     };
     auto weight = [&](float z) { return ex2((z - zmax) * kLog2E); };
@@ -637,12 +651,17 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         low = st.tau;
         all = false;  // the nucleus may reach further: its weight will tell
     }
+    // what min-p drops need not be listed, but where top-p counts within what top-k left
+    const float floor_l = (zmax + least) * T - fabsf(zmax * T) * 1e-5f - 1e-5f;  // no token below it passes min-p
+    if (q.by_m && !(q.by_k && q.by_p) && floor_l >= low) {
+        low = floor_l;
+        listed = all = true;
+    }
     if (V <= kList) {
         low = -kBig;
         listed = all = true;
     }
     if (alone) {
-        const float floor_l = (zmax + least) * T - fabsf(zmax * T) * 1e-5f - 1e-5f;  // no token below it passes
         slice.from(floor_l, aside, [&](float l, int i) { score(z_of(l, T), i); });
         cta_best<NT>(best, ibest, rf, ri);
         if (threadIdx.x == 0) {
@@ -838,7 +857,6 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
             score(value_of(~list_z[base + i]), list_i[base + i]);
         at += base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
     }
-    cta_best<NT>(best, ibest, rf, ri);
     break;
     }
     if (slow) {
@@ -904,23 +922,31 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
             const uint32_t y = key_of(z);
             if (l > -INFINITY && (y > cut || (y == cut && i < lo))) score(z, i);
         });
-        cta_best<NT>(best, ibest, rf, ri);
     }
-    if (threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, ibest, st.imax, lmax, sum);
+    settle();
 }
 
-// CTAs a row: 8 where that fills the SMs (two CTAs each) at most once, else 4,
-// with slices of 4096 tokens at least.  Four at any number of rows: their
-// threads' maxima are what the candidates are found by, and finer slices even
-// out the last wave.
-static int splits_of(int rows, int vocab, int sms) {
-    int S = rows * (int64_t)8 <= 2 * sms ? 8 : 4;
-    while (S > 1 && vocab / S < 4096) S >>= 1;
-    return rows > kSampleSplitRows ? 1 : S;
+// CTAs a row, of slices of 4096 tokens at least.  Two CTAs share an SM, and a
+// CTA costs about as much as 6000 tokens beside its slice, so the fewest
+// (waves) x (slice + 6000) is taken; with filters 4 at least, whose threads'
+// maxima are what the candidates are found by.  (256 unfiltered f32 rows of
+// 151936: 4 a row 78.7 us, 1 a row 62.8.)
+static int splits_of(int rows, int vocab, bool filters, int sms) {
+    if (rows > kSampleSplitRows) return 1;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int S = 1; S <= kMaxSplits && (S == 1 || vocab / S >= 4096); S <<= 1) {
+        const int64_t waves = ((int64_t)rows * S + 2 * sms - 1) / (2 * sms), cost = waves * (vocab / S + 6000);
+        if (cost < least || (filters && S <= 4)) {
+            best = S;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 size_t sample_workspace(int rows, int vocab, bool filters, int sms) {
-    if (!filters && splits_of(rows, vocab, sms) == 1) return 0;
+    if (!filters && splits_of(rows, vocab, filters, sms) == 1) return 0;
     return kCounterBytes + (size_t)rows * sizeof(RowSpace);
 }
 
@@ -950,7 +976,7 @@ static cudaError_t launch(const w4a16_sample_args& a, int S, cudaStream_t s) {
 }
 
 cudaError_t launch_sample(const w4a16_sample_args& a, int sms, cudaStream_t s) {
-    const int S = splits_of(a.rows, a.vocab, sms);
+    const int S = splits_of(a.rows, a.vocab, a.top_k || a.top_p || a.min_p, sms);
     if (a.dtype == W4A16_F32) return launch<W4A16_F32>(a, S, s);
     if (a.dtype == W4A16_BF16) return launch<W4A16_BF16>(a, S, s);
     return launch<W4A16_F16>(a, S, s);
