@@ -49,7 +49,7 @@ static __device__ int g_chunk_status;
 constexpr int kChThreads = 352;  // two softmax warpgroups, the MMA warp, the key / value and the query copy warp
 constexpr int kChKeys = 128;
 constexpr int kChTwo = 256;  // rows that see fewer positions carry their weights in two parts
-constexpr int kChSnap = 4, kChJoin = 12;  // key tiles; see the line
+constexpr int kChSnap = 2, kChJoin = 12;  // key tiles; see the line
 constexpr int kChCounters = 1024;  // first arrival counter of this kernel (the small-row kernel's lie below)
 
 template <int D>
@@ -69,26 +69,127 @@ struct Ch {
 static_assert(Ch<128>::kSmem <= 232448 && Ch<64>::kSmem <= 232448, "shared memory");
 
 // ---- instructions ---------------------------------------------------------
+// Operand descriptors (K-major and 128-byte swizzle as smem_desc_sw128 has them;
+// for V, [128 keys][64 columns] slabs, MN-major: columns contiguous, slabs 16 KB
+// apart, 8-key groups 1 KB) differ in the start address alone, in their low
+// word.  The low words are taken from lane 0, so that the compiler knows them
+// the same in all lanes and keeps them in uniform registers, which is where the
+// instruction wants them: with descriptors built per instruction from per-lane
+// values an MMA took ~60 clocks to issue, as long as it runs.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescK = (16u >> 4) << 16, kDescV = (16384u >> 4) << 16;
+W4A16_DEVICE uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+W4A16_DEVICE uint32_t desc_low(uint32_t addr, uint32_t kind) { return uniform(((addr & 0x3FFFFu) >> 4) | kind); }
 // D[tmem] (+)= A[smem] B[smem], issued by one lane of a converged warp
-W4A16_DEVICE void mma_ss_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+W4A16_DEVICE void mma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
         : "memory");
 }
-// V tile, [128 keys][64 columns] slabs: columns contiguous (MN-major), 128-byte
-// swizzle; slabs 16 KB apart along the columns, 8-key groups 1 KB apart.
-W4A16_DEVICE uint64_t desc_v(uint32_t addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFF) >> 4);
-    d |= (uint64_t)(16384 >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// the same with A in tensor memory
+W4A16_DEVICE void mma_ts_lo(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
+        : "memory");
+}
+template <int D>
+W4A16_DEVICE void score_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    if constexpr (D == 128) asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "add.u32 y, %2, 0;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 0;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "setp.eq.u32 p, 0, 0;\n\t"
+        "add.u32 y, %2, 2;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 2;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 4;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 4;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 6;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 6;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 1024;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 1024;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 1026;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 1026;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 1028;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 1028;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 1030;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 1030;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(0), "r"(kDescHigh) : "memory");
+    else asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "add.u32 y, %2, 0;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 0;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "setp.eq.u32 p, 0, 0;\n\t"
+        "add.u32 y, %2, 2;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 2;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 4;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 4;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 y, %2, 6;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 6;\n\t"
+        "mov.b64 da, {x, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(0), "r"(kDescHigh) : "memory");
+}
+W4A16_DEVICE void pv_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "add.u32 y, %2, 0;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "setp.eq.u32 p, 0, 0;\n\t"
+        "add.u32 y, %2, 128;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 8;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 y, %2, 256;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 16;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 y, %2, 384;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 24;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 y, %2, 512;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 32;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 y, %2, 640;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 40;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 y, %2, 768;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 48;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "add.u32 y, %2, 896;\n\tmov.b64 db, {y, %5};\n\t"
+        "add.u32 x, %1, 56;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh) : "memory");
 }
 template <typename Ty>
 __device__ constexpr uint32_t idesc_ch(int N, bool v) {
@@ -507,14 +608,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 const uint32_t e = 2 * tile_of(g, k), sl = e % NS;
                 if (!mbar_wait_warp(full + sl, (e / NS) & 1, abort_flag, &g_chunk_status)) return false;
                 tc_fence_after();
-                const uint32_t qa = smem_u32(smem + (pc.duo ? g : 0) * L::kTile);
-                const uint32_t ka = smem_u32(smem + L::kRingOff + sl * L::kTile);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
-                    mma_ss_warp(tmem + L::kTS + 128 * g, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), id_s,
-                                kk > 0 ? 1u : 0u);
-                }
+                const uint32_t qa = desc_low(smem_u32(smem + (pc.duo ? g : 0) * L::kTile), kDescK);
+                const uint32_t ka = desc_low(smem_u32(smem + L::kRingOff + sl * L::kTile), kDescK);
+                const uint32_t sd = uniform(tmem + L::kTS + 128 * g);
+                score_block<D>(sd, qa, ka, id_s);
                 mma_commit_warp(s_full + g);
                 if (!pc.duo || g == 1) mma_commit_warp(empty + sl);
                 if (--scores == 0) mma_commit_warp(q_free);
@@ -534,13 +631,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     if (!ok) break;
                     ++np[g];
                     tc_fence_after();
-                    const uint32_t va = smem_u32(smem + L::kRingOff + sl * L::kTile);
-                    for (int part = 0; part < (pc.two ? 2 : 1); ++part) {
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_bf16_ts_warp(tmem + L::kTO + D * g, tmem + L::kTS + 128 * g + 64 * part + 8 * kk,
-                                             desc_v(va + kk * 2048), id_o, k > 0 || part > 0 || kk > 0 ? 1u : 0u);
-                    }
+                    const uint32_t va = desc_low(smem_u32(smem + L::kRingOff + sl * L::kTile), kDescV);
+                    const uint32_t pa = uniform(tmem + L::kTS + 128 * g), od = uniform(tmem + L::kTO + D * g);
+                    const uint32_t more = uniform(k > 0 ? 1u : 0u);
+pv_block(od, pa, va, id_o, more);
+                    if (pc.two) pv_block(od, pa + 64, va, id_o, 1u);
                     if (!pc.duo || g == 1) mma_commit_warp(empty + sl);
                     if (k + 1 < cnt[g])
                         ok = score(g, k + 1);
