@@ -70,8 +70,12 @@ W4A16_DEVICE DecSpan dec_span(const PagedAttnParams& p, const Request& r) {
     return s;
 }
 
+// x / y for 0 <= x and 0 < y: in 32 bits where both fit, a fifth of the time
+W4A16_DEVICE int64_t quotient(int64_t x, int64_t y) {
+    return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+}
 // CTA that holds place u of the line of U places cut over C CTAs
-W4A16_DEVICE int owner_of(int64_t u, int64_t U, int C) { return (int)(((u + 1) * C - 1) / U); }
+W4A16_DEVICE int owner_of(int64_t u, int64_t U, int C) { return (int)quotient((u + 1) * C - 1, U); }
 
 template <typename Ty, int D>
 __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __grid_constant__ PagedAttnParams p) {
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     before -= mine;
     const int C = (int)(U < gridDim.x ? U : gridDim.x);  // every CTA of the C has a place at least
     if (c >= C) return;
-    const int64_t u0 = (int64_t)c * U / C, u1 = (int64_t)(c + 1) * U / C;
+    const int64_t u0 = quotient(c * U, C), u1 = quotient((c + 1) * U, C);
     if (u0 >= before && u0 < before + mine) {
         int64_t at = before;
         for (int b = b0; b < b1; ++b) {
@@ -124,8 +128,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
             if (u0 < at + n) {
                 const int len = sp.units + kDecPair;
                 misc[0] = b;
-                misc[1] = (int)((u0 - at) / len);
-                misc[2] = (int)((u0 - at) % len);
+                const int head = (int)quotient(u0 - at, len);
+                misc[1] = head;
+                misc[2] = (int)(u0 - at - (int64_t)head * len);
                 misc[3] = r.t0;
                 misc[4] = r.n;
                 misc[5] = r.L;
@@ -162,22 +167,22 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         const int all = e_last < j0 ? 0 : (e_last - j0) / kDecTile + 1;  // tiles that hold a seen key
         const int end = min((off + take) * kDecWarps, all);
         tiles = tile0 < end ? (end - tile0 + kDecWarps - 1) / kDecWarps : 0;
-        ent_base = -32;
+    };
+    auto entries = [&](int t) {  // lane i: the pages of tile t + i
+        ent_base = t;
+        ent[0] = ent[1] = -1;
+        if (t + lane < tiles) {
+            const int j = j0 + (tile0 + (t + lane) * kDecWarps) * kDecTile;
+            const int* row = p.table + (int64_t)b * p.table_stride;
+            for (int i = 0; i < boxes; ++i) {
+                const int col = (j + i * box) >> p.shift;
+                if (col < p.columns) ent[i] = row[col];
+            }
+        }
     };
     auto issue = [&](int t, int slot) {  // the copies of the piece's tile t; a group of copies in any case
         if (t < tiles) {
-            if (t >= ent_base + 32) {  // lane i: the pages of tile t + i
-                ent_base = t;
-                ent[0] = ent[1] = -1;
-                if (t + lane < tiles) {
-                    const int j = j0 + (tile0 + (t + lane) * kDecWarps) * kDecTile;
-                    const int* row = p.table + (int64_t)b * p.table_stride;
-                    for (int i = 0; i < boxes; ++i) {
-                        const int col = (j + i * box) >> p.shift;
-                        if (col < p.columns) ent[i] = row[col];
-                    }
-                }
-            }
+            if (t >= ent_base + 32) entries(t);
             uint32_t no = 0;
             const int j = j0 + (tile0 + t * kDecWarps) * kDecTile;
             const uint32_t dst = ring + slot * 2 * L::kHalf + (cch >> 3) * (kDecTile * 128);
@@ -224,6 +229,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     };
 
     open_piece();
+    entries(0);
     load_q();
     for (int i = 0; i < L::kSlots; ++i) issue(i, i);
 
@@ -409,6 +415,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
                 } while (sp.units == 0);
             }
             open_piece();
+            entries(0);
             load_q();
             for (int i = 0; i < L::kSlots; ++i) issue(i, i);
         }
@@ -434,27 +441,36 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         }
         const float fa = exp2_approx(ma - (Ma == -INFINITY ? 0.f : Ma));
         const float fb = exp2_approx(mb - (Mb == -INFINITY ? 0.f : Mb));
-        if (warp >= 4) {
+        // With at most 8 rows every warp leaves its own and 8 are added below; the
+        // room is for four warps' 16 rows.
+        const bool few = R <= 8;
+        if (few) {
+            float2* at = reinterpret_cast<float2*>(merge) + warp * (L::kRegs / 4 * 32) + lane;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
+            for (int n = 0; n < D / 8; ++n) at[n * 32] = make_float2(o[n][0] * fa, o[n][1] * fa);
+        } else {
+            float2* at = reinterpret_cast<float2*>(merge) + (warp & 3) * (L::kRegs / 2 * 32) + lane;
+            if (warp >= 4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    merge[(warp - 4) * (L::kRegs * 32) + (4 * n + i) * 32 + lane] = o[n][i] * (i < 2 ? fa : fb);
-        }
-        __syncthreads();
-        if (warp < 4) {
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float* at = merge + warp * (L::kRegs * 32) + (4 * n + i) * 32 + lane;
-                    *at = fmaf(o[n][i], i < 2 ? fa : fb, *at);
+                for (int n = 0; n < D / 8; ++n) {
+                    at[2 * n * 32] = make_float2(o[n][0] * fa, o[n][1] * fa);
+                    at[(2 * n + 1) * 32] = make_float2(o[n][2] * fb, o[n][3] * fb);
                 }
+            }
+            __syncthreads();
+            if (warp < 4) {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    float2* x = at + 2 * n * 32;
+                    x[0] = make_float2(fmaf(o[n][0], fa, x[0].x), fmaf(o[n][1], fa, x[0].y));
+                    x[32] = make_float2(fmaf(o[n][2], fb, x[32].x), fmaf(o[n][3], fb, x[32].y));
+                }
+            }
         }
         __syncthreads();
         // thread: pairs of neighbouring columns of one row
         const bool whole = from_start && to_end;
-        const int row = ((int)threadIdx.x & 31) / 4 + 8 * ((threadIdx.x >> 5) & 1);
+        const int row = few ? lane / 4 : lane / 4 + 8 * (warp & 1);
         float M = -INFINITY, S = 0.f;
 #pragma unroll
         for (int i = 0; i < kDecWarps; ++i) M = fmaxf(M, ml[(i * 16 + row) * 2]);
@@ -470,22 +486,33 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         float* part = p.part + (int64_t)(2 * c + (from_start ? 1 : 0)) * L::kPart;
         if (row < R) {
             const float inv = 1.f / S;
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-                const int n = (threadIdx.x >> 6) + 4 * x, col = 8 * n + 2 * (lane & 3);
-                const float* at = merge + (4 * n + 2 * ((threadIdx.x >> 5) & 1)) * 32 + lane;
+            // column tiles n of 8: few -- warp, warp + 8; else warp / 2, warp / 2 + 4, ..
+            const int step = few ? kDecWarps : kDecWarps / 2;
+            const float2* at = reinterpret_cast<const float2*>(merge) + lane + (few ? 0 : (warp & 1) * 32);
+            for (int n = few ? warp : warp >> 1; n < D / 8; n += step) {
+                const int col = 8 * n + 2 * (lane & 3);
                 float y0 = 0.f, y1 = 0.f;
+                if (few) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y0 += at[i * (L::kRegs * 32)];
-                    y1 += at[i * (L::kRegs * 32) + 32];
+                    for (int i = 0; i < kDecWarps; ++i) {
+                        const float2 x = at[(i * (L::kRegs / 4) + n) * 32];
+                        y0 += x.x;
+                        y1 += x.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = at[(i * (L::kRegs / 2) + 2 * n) * 32];
+                        y0 += x.x;
+                        y1 += x.y;
+                    }
                 }
                 if (whole)
                     *reinterpret_cast<uint32_t*>(out + col) = S == 0.f ? 0u : Ty::pack(y0 * inv, y1 * inv);
                 else
                     *reinterpret_cast<float2*>(part + 32 + row * D + col) = make_float2(y0, y1);
             }
-            if ((threadIdx.x >> 6) == 0 && (lane & 3) == 0) {
+            if ((few ? warp : warp >> 1) == 0 && (lane & 3) == 0) {
                 if (!whole)
                     *reinterpret_cast<float2*>(part + 2 * row) = make_float2(M, S);
                 else if (lse)
@@ -497,46 +524,51 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
             const int c0 = owner_of(first, U, C), c1 = owner_of(end - 1, U, C), pieces = c1 - c0 + 1;
             __syncthreads();
             if (threadIdx.x == 0) {
-                __threadfence();  // the CTA's stores, ordered before by the barrier
-                const unsigned n = atomicAdd(p.counters + c0, 1u);
+                unsigned n;  // releases the CTA's stores, ordered before by the barrier
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                             : "=r"(n)
+                             : "l"(p.counters + c0)
+                             : "memory");
                 const int last = n == (unsigned)(pieces - 1);
                 if (last) p.counters[c0] = 0;
-                __threadfence();
                 misc[0] = last;
             }
             __syncthreads();
             if (misc[0]) {
-                // the pieces' maxima and sums, then weights, by row; then the columns
-                float2* pm = reinterpret_cast<float2*>(merge);  // [piece][R]
+                // a thread: four columns of a row, kJoin pieces at a time under a running maximum
                 auto piece = [&](int i) { return p.part + (int64_t)(2 * (c0 + i) + (i == 0)) * L::kPart; };
-                constexpr int kRoom = L::kMerge / 8;
-                if (pieces * R <= kRoom) {
-                    for (int e = threadIdx.x; e < pieces * R; e += kDecThreads)
-                        pm[e] = __ldcg(reinterpret_cast<const float2*>(piece(e / R)) + e % R);
-                    __syncthreads();
-                }
+                constexpr int kJoin = 12;
                 for (int e = threadIdx.x; e < R * (D / 4); e += kDecThreads) {
                     const int jr = e / (D / 4), col = (e - jr * (D / 4)) * 4;
-                    auto at = [&](int i) {
-                        return pieces * R <= kRoom ? pm[i * R + jr] : __ldcg(reinterpret_cast<const float2*>(piece(i)) + jr);
-                    };
                     float jm = -INFINITY, js = 0.f;
-                    for (int i = 0; i < pieces; ++i) jm = fmaxf(jm, at(i).x);
-                    const float jb = jm == -INFINITY ? 0.f : jm;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int i0 = 0; i0 < pieces; i0 += 8) {
-                        float4 x[8];
+                    for (int i0 = 0; i0 < pieces; i0 += kJoin) {
+                        float2 mi[kJoin];
+                        float4 x[kJoin];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i0 + i < pieces)
+                        for (int i = 0; i < kJoin; ++i) {
+                            mi[i] = make_float2(-INFINITY, 0.f);
+                            if (i0 + i < pieces) {
+                                mi[i] = __ldcg(reinterpret_cast<const float2*>(piece(i0 + i)) + jr);
                                 x[i] = __ldcg(reinterpret_cast<const float4*>(piece(i0 + i) + 32 + jr * D + col));
+                            }
+                        }
+                        float M = jm;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (i0 + i >= pieces) continue;
-                            const float2 mi = at(i0 + i);
-                            if (mi.y == 0.f) continue;  // no seen key in this piece
-                            const float f = exp2_approx(mi.x == -INFINITY ? 0.f : mi.x - jb);
-                            js = fmaf(mi.y, f, js);
+                        for (int i = 0; i < kJoin; ++i) M = fmaxf(M, mi[i].x);
+                        const float jb = M == -INFINITY ? 0.f : M;
+                        const float g = jm == -INFINITY ? 1.f : exp2_approx(jm - jb);
+                        js *= g;
+                        y.x *= g;
+                        y.y *= g;
+                        y.z *= g;
+                        y.w *= g;
+                        jm = M;
+#pragma unroll
+                        for (int i = 0; i < kJoin; ++i) {
+                            if (mi[i].y == 0.f) continue;  // no piece, or no seen key in it
+                            const float f = exp2_approx(mi[i].x == -INFINITY ? 0.f : mi[i].x - jb);
+                            js = fmaf(mi[i].y, f, js);
                             y.x = fmaf(x[i].x, f, y.x);
                             y.y = fmaf(x[i].y, f, y.y);
                             y.z = fmaf(x[i].z, f, y.z);
