@@ -9,11 +9,11 @@
 //      exponentials, and, where no filter is on, the race itself: one pass over
 //      logits and noise, joined by the row's last CTA;
 //   2. sample_pick_kernel, S CTAs a row, where filters may be on: what can be
-//      kept is cut down to candidates without knowing the order -- top-k by the
-//      k-th largest of the threads' own maxima (k tokens at least are that
-//      large), top-p by the weight below which all the row's tokens together
-//      are less than (1 - p) of the sum, min-p by its own bound -- and
-//      collected in a list of the row;
+//      kept is cut down to candidates without knowing the order -- top-k and
+//      top-p by the maxima of the first pass's threads, S x 512 tokens of the
+//      row: with k of them, or p of the row's weight, at and above a bound, so
+//      many of the row's tokens are; min-p by its own bound -- and collected in
+//      a list of the row;
 //   3. the row's last CTA sorts up to kList candidates and settles the cuts and
 //      the race there.  Only their random numbers are read;
 //   4. with more candidates (a flat row) it counts them in bins, which bounds
@@ -39,6 +39,7 @@ namespace w4a16 {
 constexpr int kStatThreads = 512, kPickThreads = 512;
 constexpr int kList = 2048;   // candidates that are sorted
 constexpr int kBins = 4096;   // of the histogram of a flat row
+constexpr int kTopBins = 2 * kPickThreads;  // of the histogram of the first pass's maxima
 constexpr int kMaxSplits = 8; // CTAs a row
 constexpr float kBig = 3.402823466e38f;
 constexpr float kLog2E = 1.4426950408889634f;
@@ -47,16 +48,21 @@ constexpr int kSampleCounters = 4096, kSampleSplitRows = 4096;
 
 // What a CTA leaves of its slice after the first pass, and its part of the race.
 struct SliceStats {
-    float lmax, sum, tau, best;
-    int imax, ibest, pad[2];
+    float lmax, sum, best;
+    int imax, ibest, pad[3];
 };
-// A row's part of the workspace.
+// A row's part of the workspace; behind it the maxima of the S x kStatThreads threads of the first pass.
 struct RowSpace {
     SliceStats stats[kMaxSplits];
     int found, pad[3];            // candidates collected (may exceed kList)
     uint32_t key[kList];          // candidates: keys of z, all bits turned (rising key is falling z)
     int index[kList];
+    W4A16_DEVICE float* maxima() { return reinterpret_cast<float*>(this + 1); }
 };
+__host__ __device__ constexpr size_t row_space(int S) { return sizeof(RowSpace) + (size_t)S * kStatThreads * 4; }
+W4A16_DEVICE RowSpace* space_of(void* workspace, int r, int S) {
+    return reinterpret_cast<RowSpace*>(static_cast<char*>(workspace) + kCounterBytes + r * row_space(S));
+}
 
 // order-preserving map of f32 to unsigned (no NaN): a < b <=> key(a) < key(b)
 W4A16_DEVICE uint32_t key_of(float z) {
@@ -85,6 +91,14 @@ W4A16_DEVICE float lg2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// One CTA's arrival, by one thread behind a barrier: the CTA's writes are before
+// it, the others' after it.  Their number before this one.
+W4A16_DEVICE unsigned arrive(unsigned* counter) {
+    unsigned n;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+    return n;
 }
 
 // ---- reductions over the CTA, in a fixed order --------------------------------
@@ -140,6 +154,20 @@ W4A16_DEVICE void cta_best(float& x, int& i, float* f, int* n) {
         const int j = __shfl_xor_sync(0xffffffffu, i, d);
         join_best(x, i, y, j);
     }
+}
+// sum over the threads before this one, of counts
+W4A16_DEVICE uint32_t cta_before(uint32_t x, int* n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t s = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) n[warp] = (int)s;
+    __syncthreads();
+    return s - x + __reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)n[lane] : 0u);
 }
 // sum over the threads before this one
 W4A16_DEVICE float cta_before(float x, float* f) {
@@ -327,24 +355,20 @@ W4A16_DEVICE void write_row(const w4a16_sample_args& p, int r, const Slice<DT, N
 
 // The slices' results as one, the sums added in slice order; by whole warps.
 struct RowStats {
-    float lmax, sum, tau, best;
+    float lmax, sum, best;
     int imax, ibest;
     W4A16_DEVICE RowStats(const SliceStats* s, int S, float c2) {
-        const int lane = threadIdx.x & 31;
-        const bool on = lane < S;
-        const float mine = on ? __ldcg(&s[lane].lmax) : -INFINITY, part = on ? __ldcg(&s[lane].sum) : 0.f;
+        s += threadIdx.x & (S - 1);  // (S is a power of two: the slices again and again)
+        const float mine = __ldcg(&s->lmax), part = __ldcg(&s->sum);
         lmax = mine;
-        tau = on ? __ldcg(&s[lane].tau) : -INFINITY;
-        best = on ? __ldcg(&s[lane].best) : -INFINITY;
-        imax = on ? __ldcg(&s[lane].imax) : 0x7fffffff;
-        ibest = on ? __ldcg(&s[lane].ibest) : 0x7fffffff;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
+        best = __ldcg(&s->best);
+        imax = __ldcg(&s->imax);
+        ibest = __ldcg(&s->ibest);
+        for (int d = 1; d < S; d <<= 1) {
             const float x = __shfl_xor_sync(0xffffffffu, lmax, d), y = __shfl_xor_sync(0xffffffffu, best, d);
             const int i = __shfl_xor_sync(0xffffffffu, imax, d), j = __shfl_xor_sync(0xffffffffu, ibest, d);
             join_best(lmax, imax, x, i);
             join_best(best, ibest, y, j);
-            tau = fmaxf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
         }
         const float scaled = mine == -INFINITY ? 0.f : part * ex2((mine - lmax) * c2);
         sum = 0.f;
@@ -456,12 +480,13 @@ __global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a
     float lmax = mine;
     int imax = vmax >= 0 ? (vmax < V ? vmax : vmax - V) : 0x7fffffff;  // the first token of its load
     cta_best<NT>(lmax, imax, rf, ri);
-    if (lmax > -INFINITY)  // the token itself: loads rise with the threads' first tokens, so the lowest holds the lowest
-        for (int x = 0; x < VE && imax + x < V; ++x)
-            if (slice.at(imax + x) == lmax) {
-                imax += x;
-                break;
-            }
+    if (lmax > -INFINITY) {  // the token itself: loads rise with the threads' first tokens, so the lowest holds the lowest
+        int at = 0;
+#pragma unroll
+        for (int x = VE - 1; x > 0; --x)
+            if (imax + x < V && slice.at(imax + x) == lmax) at = x;
+        if (slice.at(imax) != lmax) imax += at;
+    }
     sum = cta_sum<NT>(mine == -INFINITY ? 0.f : sum * ex2((mine - lmax) * q.c2), rf);
     float best = -INFINITY;
     int ibest = 0x7fffffff;
@@ -492,21 +517,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a
         }
         cta_best<NT>(best, ibest, rf, ri);
     }
-    // m tokens of this slice at least are as large as the m-th largest of its
-    // threads' maxima: m = k for top-k; for top-p as many as the list has good
-    // room for, which most nuclei lie within
-    float tau = -INFINITY;
-    const int m = q.by_k ? q.k : max(kList / 2 / S, NT / 4);
-    if ((q.by_k && m <= NT / 2) || (q.by_p && !q.by_k)) {
-        uint32_t lo = key_of(-INFINITY), hi = key_of(lmax);
-        const uint32_t y = key_of(mine);
-        for (int b = 0; b < 16 && lo < hi; ++b) {
-            const uint32_t mid = lo + (hi - lo + 1) / 2;
-            if (__syncthreads_count(y >= mid) >= min(m, NT / 2)) lo = mid; else hi = mid - 1;
-        }
-        tau = value_of(lo);
-    }
-    RowSpace* space = reinterpret_cast<RowSpace*>(static_cast<char*>(p.workspace) + kCounterBytes) + r;
+    RowSpace* space = space_of(p.workspace, r, S);
     const bool settled = race || q.greedy;  // nothing is left for the second kernel
     if (S == 1 && (settled || !filters)) {
         if (threadIdx.x == 0) write_row<DT, NT>(p, r, slice, q, q.greedy ? imax : ibest, imax, lmax, sum);
@@ -516,23 +527,21 @@ __global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a
         SliceStats* s = space->stats + rank;
         s->lmax = lmax;
         s->sum = sum;
-        s->tau = tau;
         s->best = best;
         s->imax = imax;
         s->ibest = ibest;
         if (rank == 0) space->found = 0;
     }
+    if (!settled) space->maxima()[rank * NT + threadIdx.x] = mine;
     if (S == 1 || !settled) return;
     // the row's last CTA joins the slices
-    __threadfence();
     if (threadIdx.x == 0) {
         unsigned* counter = static_cast<unsigned*>(p.workspace) + kSampleCounters + r;
-        last = atomicAdd(counter, 1u) == (unsigned)(S - 1);
+        last = arrive(counter) == (unsigned)(S - 1);
         if (last) *counter = 0;
     }
     __syncthreads();
     if (last && threadIdx.x < 32) {
-        __threadfence();
         const RowStats a(space->stats, S, q.c2);
         if (threadIdx.x == 0) write_row<DT, NT>(p, r, slice, q, q.greedy ? a.imax : a.ibest, a.imax, a.lmax, a.sum);
     }
@@ -584,6 +593,33 @@ W4A16_DEVICE void sort_list(uint32_t* key, int* idx, int n) {
     __syncthreads();
 }
 
+// The same for up to 256 entries by counting, for each, the entries before it:
+// NT / n threads an entry, 4 entries of the list at a time.  `rank` has room
+// for n.  (256 entries: 2.6 k clocks against 5 k.)
+template <int NT>
+W4A16_DEVICE void sort_few(uint32_t* key, int* idx, int* rank, int n) {
+    __syncthreads();
+    const int e = (int)threadIdx.x & (n - 1), part = (int)threadIdx.x / n, each = n * n / NT;
+    const uint32_t x = key[e];
+    const int u = idx[e];
+    if ((int)threadIdx.x < n) rank[e] = 0;
+    int before = 0;
+    for (int j = part * each; j < (part + 1) * each; j += 2) {
+        const uint2 y = *reinterpret_cast<const uint2*>(key + j);
+        const int2 v = *reinterpret_cast<const int2*>(idx + j);
+        before += (y.x < x || (y.x == x && v.x < u)) + (y.y < x || (y.y == x && v.y < u));
+    }
+    __syncthreads();
+    if (before) atomicAdd(rank + e, before);
+    __syncthreads();
+    if ((int)threadIdx.x < n) {
+        const int at = rank[e];
+        key[at] = x;
+        idx[at] = u;
+    }
+    __syncthreads();
+}
+
 // ---- 2. to 5. filtered rows ------------------------------------------------------
 template <int DT>
 __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a16_sample_args p, const int S) {
@@ -602,7 +638,11 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
     const RowParams q(p, r);
     if (q.race || q.greedy) return;
-    RowSpace* space = reinterpret_cast<RowSpace*>(static_cast<char*>(p.workspace) + kCounterBytes) + r;
+    RowSpace* space = space_of(p.workspace, r, S);
+    float top[kMaxSplits];  // maxima of the first pass's threads, distinct tokens of the row
+#pragma unroll
+    for (int i = 0; i < kMaxSplits; ++i)
+        top[i] = i < S && (q.by_k || q.by_p) ? __ldcg(space->maxima() + i * NT + threadIdx.x) : -INFINITY;
     const RowStats st(space->stats, S, q.c2);
     const float T = q.T, lmax = st.lmax, sum = st.sum;
     const float* noise = p.noise + r * p.noise_row;
@@ -615,15 +655,16 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     const float least = q.by_m ? fminf(logf(q.mp), 0.f) : -INFINITY;  // of z - zmax
     float best = -INFINITY, zbest = 0.f;
     int ibest = 0x7fffffff;
-    auto score = [&](float z, int i) {
+    auto score_of = [&](float z, float e, int i) {
         if (!(z - zmax >= least)) return;
-        const float x = z - logf(noise[i]);
+        const float x = z - logf(e);
         if (x > best || (x == best && i < ibest)) {
             best = x;
             ibest = i;
             zbest = z;
         }
     };
+    auto score = [&](float z, int i) { score_of(z, noise[i], i); };
     auto settle = [&] {  // the CTA's best: the thread that has it writes
         const int mine = ibest;
         cta_best<NT>(best, ibest, rf, ri);
@@ -644,12 +685,59 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     bool listed = q.by_p && !q.by_k;  // whether the candidates may be few
     bool all = true;                  // whether every token that may be kept is among them
     const float wide = low;
-    if (q.by_k && st.tau != -INFINITY) {
-        low = st.tau;
-        listed = true;
-    } else if (!q.by_k && st.tau > low) {
-        low = st.tau;
-        all = false;  // the nucleus may reach further: its weight will tell
+    const int most = min(kList / 2, S * NT / 2);  // maxima that make a good list: so many make ~20 % more tokens
+    if (V > kList && (q.by_p || (q.by_k && q.k <= most))) {
+        // bins of the maxima, their counts (top-k) or their weights' floors in 2^-31 of the sum (top-p): with
+        // `target` in the first bins, the lowest maximum in them bounds the candidates
+        float least_top = lmax;
+#pragma unroll
+        for (int i = 0; i < kMaxSplits; ++i)
+            if (top[i] > -INFINITY) least_top = fminf(least_top, top[i]);
+        least_top = value_of(__reduce_min_sync(0xffffffffu, key_of(least_top)));
+        if ((threadIdx.x & 31) == 0) rf[threadIdx.x >> 5] = least_top;
+        __syncthreads();
+        least_top = value_of(__reduce_min_sync(0xffffffffu, key_of(rf[threadIdx.x & (NT / 32 - 1)])));
+        const float scale = (kTopBins - 2) / fmaxf(fminf(lmax - least_top, 40.f * T), 1e-30f);
+        for (int turn = q.by_k ? 1 : 0; turn < 2; ++turn) {
+            const bool by_count = turn == 1;  // of top-p too, where the maxima do not weigh enough
+            uint2* bins = reinterpret_cast<uint2*>(hist);
+            const float unit = 2147483648.f / sum;
+            const uint32_t target = by_count ? (uint32_t)(q.by_k ? q.k : most)
+                                             : (uint32_t)fmaxf(fminf(q.tp * 1.00001f, 1.f) * 2147483648.f, 1.f);
+            __syncthreads();
+            bins[threadIdx.x] = make_uint2(0u, 0u);
+            if (threadIdx.x == 0) win[0] = kTopBins;
+            __syncthreads();
+            auto bin_of = [&](float l) { return (int)fminf((lmax - l) * scale, (float)(kTopBins - 1)); };
+#pragma unroll
+            for (int i = 0; i < kMaxSplits; ++i)
+                if (top[i] > -INFINITY)
+                    atomicAdd(hist + bin_of(top[i]), by_count ? 1 : (int)(uint32_t)(ex2((top[i] - lmax) * q.c2) * unit));
+            __syncthreads();
+            const uint2 mine = bins[threadIdx.x];
+            const uint32_t before = cta_before(mine.x + mine.y, ri);
+            if (before < target && before + mine.x + mine.y >= target)
+                win[0] = 2 * threadIdx.x + (before + mine.x < target);
+            __syncthreads();
+            const int cut = win[0];
+            if (cut >= kTopBins - 1) continue;  // not reached (or in the last bin, which has no end)
+            float tau = lmax;
+#pragma unroll
+            for (int i = 0; i < kMaxSplits; ++i)
+                if (top[i] > -INFINITY && bin_of(top[i]) <= cut) tau = fminf(tau, top[i]);
+            tau = value_of(__reduce_min_sync(0xffffffffu, key_of(tau)));
+            if ((threadIdx.x & 31) == 0) rf[threadIdx.x >> 5] = tau;
+            __syncthreads();
+            tau = value_of(__reduce_min_sync(0xffffffffu, key_of(rf[threadIdx.x & (NT / 32 - 1)])));
+            if (q.by_k) {
+                low = tau;
+                listed = true;
+            } else if (tau > low) {
+                low = tau;
+                all = !by_count;  // by count the nucleus may reach further: its weight will tell
+            }
+            break;
+        }
     }
     // what min-p drops need not be listed, but where top-p counts within what top-k left
     const float floor_l = (zmax + least) * T - fabsf(zmax * T) * 1e-5f - 1e-5f;  // no token below it passes min-p
@@ -684,16 +772,14 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     }
     // ---- the row's last CTA goes on
     if (S > 1) {
-        __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) {
             unsigned* counter = static_cast<unsigned*>(p.workspace) + kSampleCounters + r;
-            win[7] = atomicAdd(counter, 1u) == (unsigned)(S - 1);
+            win[7] = arrive(counter) == (unsigned)(S - 1);
             if (win[7]) *counter = 0;
         }
         __syncthreads();
         if (!win[7]) return;
-        __threadfence();
     } else {
         __syncthreads();
     }
@@ -703,10 +789,17 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         if (threadIdx.x == 0) write_row<DT, NT>(p, r, row, q, a.ibest, a.imax, lmax, sum);
         return;
     }
+    // (the first entries with their number, whether they are there or not)
+    const uint32_t key0 = __ldcg(space->key + threadIdx.x);
+    const int index0 = __ldcg(space->index + threadIdx.x);
     int n = listed ? __ldcg(&space->found) : kList + 1;
     bool flat = n > kList;
     if (!flat) {
-        for (int i = threadIdx.x; i < n; i += NT) {
+        if ((int)threadIdx.x < n) {
+            list_z[threadIdx.x] = key0;
+            list_i[threadIdx.x] = index0;
+        }
+        for (int i = NT + threadIdx.x; i < n; i += NT) {
             list_z[i] = __ldcg(space->key + i);
             list_i[i] = __ldcg(space->index + i);
         }
@@ -832,15 +925,18 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         list_z[i] = 0xffffffffu;
         list_i[i] = 0x7fffffff;
     }
-    sort_list<NT>(list_z, list_i, size);
+    if (size <= 256)
+        sort_few<NT>(list_z, list_i, hist, size);
+    else
+        sort_list<NT>(list_z, list_i, size);
     constexpr int PL = kList / NT;
-    const int base = threadIdx.x * PL;
+    const int per = max(size / NT, 1), base = (int)threadIdx.x * per;  // entries a thread, and its first
     // entries that top-k keeps (a second window lies behind `between` tokens)
     const int kept_k = q.by_k ? min(n, k - above - between) : n;
     float w[PL], wt = 0.f;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-        w[i] = base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
+        w[i] = i < per && base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
         wt += w[i];
     }
     const float before = cta_before(wt, rf), listed_mass = cta_sum<NT>(wt, rf);
@@ -850,13 +946,17 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         flat = true;  // the nucleus reaches below the list
         continue;
     }
-    float at = mass_a + before;
-#pragma unroll 1
-    for (int i = 0; i < PL; ++i) {
-        if (base + i < kept_k && (!q.by_p || at < want || (above == 0 && base + i == 0)))
-            score(value_of(~list_z[base + i]), list_i[base + i]);
-        at += base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
+    float at = mass_a + before, z[PL], e[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {  // the kept ones' random numbers, all on their way
+        const int x = base + i;
+        const bool kept = i < per && x < kept_k && (!q.by_p || at < want || (above == 0 && x == 0));
+        z[i] = kept ? value_of(~list_z[x]) : 0.f;
+        e[i] = kept ? noise[list_i[x]] : NAN;  // (takes no part)
+        at += w[i];
     }
+#pragma unroll
+    for (int i = 0; i < PL; ++i) score_of(z[i], e[i], list_i[min(base + i, kList - 1)]);
     break;
     }
     if (slow) {
@@ -947,7 +1047,7 @@ static int splits_of(int rows, int vocab, bool filters, int sms) {
 
 size_t sample_workspace(int rows, int vocab, bool filters, int sms) {
     if (!filters && splits_of(rows, vocab, filters, sms) == 1) return 0;
-    return kCounterBytes + (size_t)rows * sizeof(RowSpace);
+    return kCounterBytes + rows * row_space(splits_of(rows, vocab, filters, sms));
 }
 
 template <int DT>
