@@ -6,7 +6,7 @@
 // is ever sorted whole:
 //
 //   1. sample_stats_kernel, S CTAs a row: the row's maximum and sum of
-//      exponentials, and, where no filter is on, the race itself: one pass over
+//      exponentials, and, in a call without filters, the race itself: one pass over
 //      logits and noise, joined by the row's last CTA;
 //   2. sample_pick_kernel, S CTAs a row, where filters may be on: what can be
 //      kept is cut down to candidates without knowing the order -- top-k and
@@ -40,7 +40,7 @@ constexpr int kStatThreads = 512, kPickThreads = 512;
 constexpr int kList = 2048;   // candidates that are sorted
 constexpr int kBins = 4096;   // of the histogram of a flat row
 constexpr int kTopBins = 2 * kPickThreads;  // of the histogram of the first pass's maxima
-constexpr int kMaxSplits = 8; // CTAs a row
+constexpr int kMaxSplits = 8;  // CTAs a row, a power of two
 constexpr float kBig = 3.402823466e38f;
 constexpr float kLog2E = 1.4426950408889634f;
 // the rows' arrival counters in the workspace's counter area, behind the attention kernels'
@@ -124,36 +124,33 @@ W4A16_DEVICE int cta_count(int x, int* n) {
     __syncthreads();
     return __reduce_add_sync(0xffffffffu, lane < NT / 32 ? n[lane] : 0);
 }
-// the larger x, and of equal ones the lower index
-W4A16_DEVICE void join_best(float& x, int& i, float y, int j) {
-    if (y > x || (y == x && j < i)) {
-        x = y;
-        i = j;
-    }
+// the largest x (never -0 or NaN) and, of equal ones, the lowest index, over a warp
+W4A16_DEVICE void warp_best(float& x, int& i) {
+    const uint32_t y = key_of(x), top = __reduce_max_sync(0xffffffffu, y);
+    i = __reduce_min_sync(0xffffffffu, y == top ? i : 0x7fffffff);
+    x = value_of(top);
 }
 template <int NT>
 W4A16_DEVICE void cta_best(float& x, int& i, float* f, int* n) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, x, d);
-        const int j = __shfl_xor_sync(0xffffffffu, i, d);
-        join_best(x, i, y, j);
-    }
+    warp_best(x, i);
     __syncthreads();
     if (lane == 0) {
         f[threadIdx.x >> 5] = x;
         n[threadIdx.x >> 5] = i;
     }
     __syncthreads();
-    x = lane < NT / 32 ? f[lane] : -INFINITY;
-    i = lane < NT / 32 ? n[lane] : 0x7fffffff;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, x, d);
-        const int j = __shfl_xor_sync(0xffffffffu, i, d);
-        join_best(x, i, y, j);
-    }
+    x = f[lane & (NT / 32 - 1)];
+    i = n[lane & (NT / 32 - 1)];
+    warp_best(x, i);
+}
+template <int NT>
+W4A16_DEVICE float cta_min(float x, float* f) {
+    x = value_of(__reduce_min_sync(0xffffffffu, key_of(x)));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) f[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return value_of(__reduce_min_sync(0xffffffffu, key_of(f[threadIdx.x & (NT / 32 - 1)])));
 }
 // sum over the threads before this one, of counts
 W4A16_DEVICE uint32_t cta_before(uint32_t x, int* n) {
@@ -233,22 +230,17 @@ struct Slice {
         constexpr int U = 4;
         if (first && (int)threadIdx.x < head) one(at((int)threadIdx.x), (int)threadIdx.x);
         const uint4* vec = reinterpret_cast<const uint4*>(row + head);
-        int v = v0 + (int)threadIdx.x;
-        for (; v + (U - 1) * NT < v1; v += U * NT) {
+        for (int v = v0 + (int)threadIdx.x; v < v1; v += U * NT) {
             uint4 x[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) x[u] = vec[v + u * NT];
+            for (int u = 0; u < U; ++u) x[u] = vec[min(v + u * NT, v1 - 1)];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (v + u * NT >= v1) break;
                 float l[VE];
                 split(x[u], l);
                 many(l, head + (v + u * NT) * VE);
             }
-        }
-        for (; v < v1; v += NT) {
-            float l[VE];
-            split(vec[v], l);
-            many(l, head + v * VE);
         }
         if (last && tail + (int)threadIdx.x < V) one(at(tail + (int)threadIdx.x), tail + (int)threadIdx.x);
     }
@@ -364,12 +356,8 @@ struct RowStats {
         best = __ldcg(&s->best);
         imax = __ldcg(&s->imax);
         ibest = __ldcg(&s->ibest);
-        for (int d = 1; d < S; d <<= 1) {
-            const float x = __shfl_xor_sync(0xffffffffu, lmax, d), y = __shfl_xor_sync(0xffffffffu, best, d);
-            const int i = __shfl_xor_sync(0xffffffffu, imax, d), j = __shfl_xor_sync(0xffffffffu, ibest, d);
-            join_best(lmax, imax, x, i);
-            join_best(best, ibest, y, j);
-        }
+        warp_best(lmax, imax);
+        warp_best(best, ibest);
         const float scaled = mine == -INFINITY ? 0.f : part * ex2((mine - lmax) * c2);
         sum = 0.f;
         for (int i = 0; i < S; ++i) sum += __shfl_sync(0xffffffffu, scaled, i);
@@ -377,120 +365,116 @@ struct RowStats {
 };
 
 // ---- 1. maximum, sum, and the race of unfiltered rows ---------------------------
-template <int DT>
-__global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a16_sample_args p, const int S,
-                                                                    const int filters) {
-    constexpr int NT = kStatThreads;
-    __shared__ float rf[32];
-    __shared__ int ri[32];
-    __shared__ int last;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
-    const Slice<DT, NT> slice(p.logits, r * p.logits_row, V, rank, S);
-    const float* noise = p.noise + r * p.noise_row;
-    const RowParams q(p, r);
-    const bool race = q.race;
-    const float inv_t = fminf(1.f / q.T, kBig);
-
+// One thread's part of a pass over a slice: its largest logit and sum of
+// exponentials (STATS), and its part of the race (`race`).
+//
+// The race runs on approximate scores, l / T - log e, with errors below
+// 2^-21 |z| + 2^-20 and |z| <= |score| + 104 for any finite noise: a thread
+// keeps its two best loads, and the exact scores of the few loads that come
+// near the CTA's best decide.
+template <int DT, int NT, bool STATS>
+struct Pass {
+    using Row = Slice<DT, NT>;
+    static constexpr int VE = Row::VE;
+    const Row& slice;
+    const float* noise;
+    const RowParams& q;
     float mx = -kBig, sum = 0.f;
     int vmax = -1;  // the load in which mx came first: a token below V, or V + a vector's first token
-    // The race runs on approximate scores, l / T - log e, with errors below
-    // 2^-21 |z| + 2^-20 and |z| <= |score| + 104 for any finite noise: a thread
-    // keeps its two best loads, and the exact scores of the few loads that come
-    // near the CTA's best decide.
     float top = -INFINITY, top2 = -INFINITY;
     int vtop = -1;
-    constexpr int VE = Slice<DT, NT>::VE;
-    auto approx = [&](float l, float e) { return fmaf(l, inv_t, -0.6931471805599453f * lg2(e)); };
-    auto enter = [&](float t, int at) {
+    float inv_t;
+    bool race;
+
+    W4A16_DEVICE float approx(float l, float e) const { return fmaf(l, inv_t, -0.6931471805599453f * lg2(e)); }
+    W4A16_DEVICE void enter(float t, int at) {
         top2 = fmaxf(top2, fminf(top, t));
         if (t > top) {
             top = t;
             vtop = at;
         }
-    };
-    auto maximum = [&](float b, int at) {  // -kBig itself may be the first
+    }
+    W4A16_DEVICE void maximum(float b, int at) {  // -kBig itself may be the first
         if (b > mx || (vmax < 0 && b == -kBig)) {
             sum *= ex2((mx - b) * q.c2);
             mx = b;
             vmax = at;
         }
-    };
-    auto one = [&](float l, int i) {
-        maximum(l, i);
-        sum += ex2((l - mx) * q.c2);
-        if (race && l > -INFINITY) enter(approx(l, noise[i]), i);
-    };
-    auto many = [&](const float (&l)[VE], int i0) {
-        float b = l[0];
-#pragma unroll
-        for (int x = 1; x < VE; ++x) b = fmaxf(b, l[x]);
-        maximum(b, V + i0);
-        float s = 0.f;
-#pragma unroll
-        for (int x = 0; x < VE; ++x) s += ex2((l[x] - mx) * q.c2);
-        sum += s;
-    };
-    const bool noise4 = (reinterpret_cast<uintptr_t>(noise + slice.head) & 15) == 0;
-    if (!race) {
-        slice.each(one, many);
-    } else if (noise4) {
-        // logits and their random numbers together, U vectors in flight
-        constexpr int U = 4, NE = VE / 4;
-        const uint4* vec = reinterpret_cast<const uint4*>(slice.row + slice.head);
-        const float4* nv = reinterpret_cast<const float4*>(noise + slice.head);
-        if (slice.first && (int)threadIdx.x < slice.head) one(slice.at((int)threadIdx.x), (int)threadIdx.x);
-        for (int v = slice.v0 + (int)threadIdx.x; v < slice.v1; v += U * NT) {
-            uint4 x[U];
-            float4 e[U][NE];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int y = min(v + u * NT, slice.v1 - 1);  // past the end: again, and not counted
-                x[u] = __ldcs(vec + y);
-#pragma unroll
-                for (int z = 0; z < NE; ++z) e[u][z] = __ldcs(nv + y * NE + z);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (v + u * NT >= slice.v1) break;
-                const int i0 = slice.head + (v + u * NT) * VE;
-                float l[VE], t = -INFINITY;
-                slice.split(x[u], l);
-                many(l, i0);
-#pragma unroll
-                for (int z = 0; z < NE; ++z)
-                    t = fmaxf(t, fmaxf(fmaxf(approx(l[4 * z], e[u][z].x), approx(l[4 * z + 1], e[u][z].y)),
-                                       fmaxf(approx(l[4 * z + 2], e[u][z].z), approx(l[4 * z + 3], e[u][z].w))));
-                enter(t, V + i0);
-            }
+    }
+    W4A16_DEVICE void one(float l, int i) {
+        if constexpr (STATS) {
+            maximum(l, i);
+            sum += ex2((l - mx) * q.c2);
         }
-        if (slice.last && slice.tail + (int)threadIdx.x < V)
-            one(slice.at(slice.tail + (int)threadIdx.x), slice.tail + (int)threadIdx.x);
-    } else {  // a row whose random numbers are not aligned as its logits are
-        slice.each(one, [&](const float (&l)[VE], int i0) {
-            many(l, i0);
-            float t = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < VE; ++x) t = fmaxf(t, approx(l[x], noise[i0 + x]));
-            enter(t, V + i0);
-        });
+        if (race && l > -INFINITY) enter(approx(l, noise[i]), i);
     }
-    const float mine = vmax >= 0 ? mx : -INFINITY;  // this thread's largest logit
-    float lmax = mine;
-    int imax = vmax >= 0 ? (vmax < V ? vmax : vmax - V) : 0x7fffffff;  // the first token of its load
-    cta_best<NT>(lmax, imax, rf, ri);
-    if (lmax > -INFINITY) {  // the token itself: loads rise with the threads' first tokens, so the lowest holds the lowest
-        int at = 0;
+    W4A16_DEVICE void many(const float (&l)[VE], int i0) {
+        if constexpr (STATS) {
+            float b = l[0];
 #pragma unroll
-        for (int x = VE - 1; x > 0; --x)
-            if (imax + x < V && slice.at(imax + x) == lmax) at = x;
-        if (slice.at(imax) != lmax) imax += at;
+            for (int x = 1; x < VE; ++x) b = fmaxf(b, l[x]);
+            maximum(b, slice.V + i0);
+            float s = 0.f;
+#pragma unroll
+            for (int x = 0; x < VE; ++x) s += ex2((l[x] - mx) * q.c2);
+            sum += s;
+        }
     }
-    sum = cta_sum<NT>(mine == -INFINITY ? 0.f : sum * ex2((mine - lmax) * q.c2), rf);
-    float best = -INFINITY;
-    int ibest = 0x7fffffff;
-    if (race) {
+    W4A16_DEVICE Pass(const Row& slice_, const float* noise_, const RowParams& q_, bool race_)
+        : slice(slice_), noise(noise_), q(q_), race(race_) {
+        inv_t = fminf(1.f / q.T, kBig);
+        const int V = slice.V;
+        const bool noise4 = (reinterpret_cast<uintptr_t>(noise + slice.head) & 15) == 0;
+        if (!race) {
+            if constexpr (STATS)
+                slice.each([&](float l, int i) { one(l, i); }, [&](const float (&l)[VE], int i0) { many(l, i0); });
+        } else if (noise4) {
+            // logits and their random numbers together, U vectors in flight
+            constexpr int U = 4, NE = VE / 4;
+            const uint4* vec = reinterpret_cast<const uint4*>(slice.row + slice.head);
+            const float4* nv = reinterpret_cast<const float4*>(noise + slice.head);
+            if (slice.first && (int)threadIdx.x < slice.head) one(slice.at((int)threadIdx.x), (int)threadIdx.x);
+            for (int v = slice.v0 + (int)threadIdx.x; v < slice.v1; v += U * NT) {
+                uint4 x[U];
+                float4 e[U][NE];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int y = min(v + u * NT, slice.v1 - 1);  // past the end: again, and not counted
+                    x[u] = __ldcs(vec + y);
+#pragma unroll
+                    for (int z = 0; z < NE; ++z) e[u][z] = __ldcs(nv + y * NE + z);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (v + u * NT >= slice.v1) break;
+                    const int i0 = slice.head + (v + u * NT) * VE;
+                    float l[VE], t = -INFINITY;
+                    slice.split(x[u], l);
+                    many(l, i0);
+#pragma unroll
+                    for (int z = 0; z < NE; ++z)
+                        t = fmaxf(t, fmaxf(fmaxf(approx(l[4 * z], e[u][z].x), approx(l[4 * z + 1], e[u][z].y)),
+                                           fmaxf(approx(l[4 * z + 2], e[u][z].z), approx(l[4 * z + 3], e[u][z].w))));
+                    enter(t, V + i0);
+                }
+            }
+            if (slice.last && slice.tail + (int)threadIdx.x < V)
+                one(slice.at(slice.tail + (int)threadIdx.x), slice.tail + (int)threadIdx.x);
+        } else {  // a row whose random numbers are not aligned as its logits are
+            slice.each([&](float l, int i) { one(l, i); }, [&](const float (&l)[VE], int i0) {
+                many(l, i0);
+                float t = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < VE; ++x) t = fmaxf(t, approx(l[x], noise[i0 + x]));
+                enter(t, V + i0);
+            });
+        }
+    }
+    // the slice's winner, by the whole CTA
+    W4A16_DEVICE void winner(float& best, int& ibest, float* rf, int* ri) const {
+        const int V = slice.V;
+        best = -INFINITY;
+        ibest = 0x7fffffff;
         float lead = top;
         int none = 0;
         cta_best<NT>(lead, none, rf, ri);
@@ -517,6 +501,41 @@ __global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a
         }
         cta_best<NT>(best, ibest, rf, ri);
     }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a16_sample_args p, const int S,
+                                                                    const int filters) {
+    constexpr int NT = kStatThreads;
+    __shared__ float rf[32];
+    __shared__ int ri[32];
+    __shared__ int last;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
+    const Slice<DT, NT> slice(p.logits, r * p.logits_row, V, rank, S);
+    const RowParams q(p, r);
+    constexpr int VE = Slice<DT, NT>::VE;
+    // (with filters the second kernel runs the race of the rows that have none, beside the other rows' cuts)
+    const bool race = q.race && !filters;
+    const Pass<DT, NT, true> pass(slice, p.noise + r * p.noise_row, q, race);
+    const float mx = pass.mx;
+    const int vmax = pass.vmax;
+    const float mine = vmax >= 0 ? mx : -INFINITY;  // this thread's largest logit
+    float lmax = mine;
+    int imax = vmax >= 0 ? (vmax < V ? vmax : vmax - V) : 0x7fffffff;  // the first token of its load
+    cta_best<NT>(lmax, imax, rf, ri);
+    if (lmax > -INFINITY) {  // the token itself: loads rise with the threads' first tokens, so the lowest holds the lowest
+        int at = 0;
+#pragma unroll
+        for (int x = VE - 1; x > 0; --x)
+            if (imax + x < V && slice.at(imax + x) == lmax) at = x;
+        if (slice.at(imax) != lmax) imax += at;
+    }
+    const float sum = cta_sum<NT>(mine == -INFINITY ? 0.f : pass.sum * ex2((mine - lmax) * q.c2), rf);
+    float best = -INFINITY;
+    int ibest = 0x7fffffff;
+    if (race) pass.winner(best, ibest, rf, ri);
     RowSpace* space = space_of(p.workspace, r, S);
     const bool settled = race || q.greedy;  // nothing is left for the second kernel
     if (S == 1 && (settled || !filters)) {
@@ -532,7 +551,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a
         s->ibest = ibest;
         if (rank == 0) space->found = 0;
     }
-    if (!settled) space->maxima()[rank * NT + threadIdx.x] = mine;
+    if (!settled && !q.race) space->maxima()[rank * NT + threadIdx.x] = mine;
     if (S == 1 || !settled) return;
     // the row's last CTA joins the slices
     if (threadIdx.x == 0) {
@@ -622,7 +641,7 @@ W4A16_DEVICE void sort_few(uint32_t* key, int* idx, int* rank, int n) {
 
 // ---- 2. to 5. filtered rows ------------------------------------------------------
 template <int DT>
-__global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a16_sample_args p, const int S) {
+__global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a16_sample_args p, const int S) {
     constexpr int NT = kPickThreads;
     __shared__ float rf[32];
     __shared__ int ri[32];
@@ -637,7 +656,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
     pdl_wait();
     const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
     const RowParams q(p, r);
-    if (q.race || q.greedy) return;
+    if (q.greedy) return;
     RowSpace* space = space_of(p.workspace, r, S);
     float top[kMaxSplits];  // maxima of the first pass's threads, distinct tokens of the row
 #pragma unroll
@@ -675,7 +694,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         }
     };
     auto weight = [&](float z) { return ex2((z - zmax) * kLog2E); };
-    const bool alone = !q.by_k && !q.by_p;  // min-p alone: its bound is known
+    const bool alone = !q.by_k && !q.by_p;  // min-p alone, whose bound is known, or no filter: every CTA for itself
 
     // ---- 2. candidates: logits >= low
     // top-p: tokens with z < zmax - R weigh less than V e^-R = (1 - p) sum e^-0.02 together
@@ -693,10 +712,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
 #pragma unroll
         for (int i = 0; i < kMaxSplits; ++i)
             if (top[i] > -INFINITY) least_top = fminf(least_top, top[i]);
-        least_top = value_of(__reduce_min_sync(0xffffffffu, key_of(least_top)));
-        if ((threadIdx.x & 31) == 0) rf[threadIdx.x >> 5] = least_top;
-        __syncthreads();
-        least_top = value_of(__reduce_min_sync(0xffffffffu, key_of(rf[threadIdx.x & (NT / 32 - 1)])));
+        least_top = cta_min<NT>(least_top, rf);
         const float scale = (kTopBins - 2) / fmaxf(fminf(lmax - least_top, 40.f * T), 1e-30f);
         for (int turn = q.by_k ? 1 : 0; turn < 2; ++turn) {
             const bool by_count = turn == 1;  // of top-p too, where the maxima do not weigh enough
@@ -725,10 +741,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
 #pragma unroll
             for (int i = 0; i < kMaxSplits; ++i)
                 if (top[i] > -INFINITY && bin_of(top[i]) <= cut) tau = fminf(tau, top[i]);
-            tau = value_of(__reduce_min_sync(0xffffffffu, key_of(tau)));
-            if ((threadIdx.x & 31) == 0) rf[threadIdx.x >> 5] = tau;
-            __syncthreads();
-            tau = value_of(__reduce_min_sync(0xffffffffu, key_of(rf[threadIdx.x & (NT / 32 - 1)])));
+            tau = cta_min<NT>(tau, rf);
             if (q.by_k) {
                 low = tau;
                 listed = true;
@@ -750,8 +763,12 @@ __global__ void __launch_bounds__(kPickThreads, 1) sample_pick_kernel(const w4a1
         listed = all = true;
     }
     if (alone) {
-        slice.from(floor_l, aside, [&](float l, int i) { score(z_of(l, T), i); });
-        cta_best<NT>(best, ibest, rf, ri);
+        if (q.race) {
+            Pass<DT, NT, false>(slice, noise, q, true).winner(best, ibest, rf, ri);
+        } else {
+            slice.from(floor_l, aside, [&](float l, int i) { score(z_of(l, T), i); });
+            cta_best<NT>(best, ibest, rf, ri);
+        }
         if (threadIdx.x == 0) {
             space->stats[rank].best = best;
             space->stats[rank].ibest = ibest;
