@@ -85,6 +85,7 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cuda
     const bool even = (int64_t)a.requests * a.max_q == a.tokens;
     const bool large = (int64_t)a.max_q * p.G > kSmallRows, small = !large || !even;
     p.small_rows = small ? kSmallRows : 0;
+    p.after_small = small;
     if (small) {
         const cudaError_t e = launch_paged_decode(p, bf16, a.head_dim, sms, s, pdl);
         if (e != cudaSuccess) return e;
@@ -92,7 +93,8 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cuda
     }
     if (!large) return cudaSuccess;
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes + paged_decode_part_bytes(a.head_dim, sms));
-    const cudaError_t e = launch_paged_chunk(p, bf16, a.head_dim, sms, s, pdl);
+    // (behind the small-row kernel always as its dependent: its CTAs take the SMs as those are done)
+    const cudaError_t e = launch_paged_chunk(p, bf16, a.head_dim, sms, s, pdl || small);
     if (e == cudaSuccess) note_launch();
     return e;
 }

@@ -24,6 +24,7 @@ struct PagedAttnParams {
     int T, B, Hq, Hkv, G, pages, shift, columns;
     int window, block;
     int small_rows;  // requests with up to this many query rows a key head go to the small-row kernel
+    bool after_small;  // the kernel before in the stream is the same call's small-row kernel
     unsigned* counters;  // arrival counters, zero between calls
     float* part;         // partial results of split work
     float scale2;  // scale * log2(e): scores in the base-2 exponent

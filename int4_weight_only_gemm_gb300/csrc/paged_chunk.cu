@@ -390,7 +390,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
         prefetch_tmap(&tmap_v);
     }
     pdl_launch_dependents();
-    pdl_wait();
+    // Behind the small-row kernel of the same call there is nothing to wait for:
+    // that kernel let this one start once everything before it was done, and the
+    // two have requests, counters and workspace of their own.
+    if (!p.after_small) pdl_wait();
 
     // ---- this CTA's part of the line --------------------------------------
     // The line runs over the requests, their items, the key heads and the key
@@ -1014,6 +1017,7 @@ pv_block(od, pa, va, id_o, more);
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (p.after_small) pdl_wait();  // the call is done when both kernels are
 }
 
 template <typename Ty, int D>

@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = (int)blockIdx.x;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // in this order: the chunk kernel of the same call does not wait for this one to begin
 
     // ---- this CTA's part of the line ----------------------------------------
     // A pair (request, key head) takes kDecPair + units places of it.
