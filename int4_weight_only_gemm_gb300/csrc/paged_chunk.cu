@@ -72,36 +72,15 @@ static_assert(Ch<128>::kSmem <= 232448 && Ch<64>::kSmem <= 232448, "shared memor
 // Operand descriptors (K-major and 128-byte swizzle as smem_desc_sw128 has them;
 // for V, [128 keys][64 columns] slabs, MN-major: columns contiguous, slabs 16 KB
 // apart, 8-key groups 1 KB) differ in the start address alone, in their low
-// word.  The low words are taken from lane 0, so that the compiler knows them
-// the same in all lanes and keeps them in uniform registers, which is where the
-// instruction wants them: with descriptors built per instruction from per-lane
-// values an MMA took ~60 clocks to issue, as long as it runs.
+// word.  What they are made of goes through uniform(), so that the compiler
+// knows it the same in all lanes and keeps it in uniform registers, which is
+// where the instruction wants it: with descriptors built per instruction from
+// per-lane values an MMA took ~60 clocks to issue, as long as it runs.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescK = (16u >> 4) << 16, kDescV = (16384u >> 4) << 16;
 W4A16_DEVICE uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-W4A16_DEVICE uint32_t desc_low(uint32_t addr, uint32_t kind) { return uniform(((addr & 0x3FFFFu) >> 4) | kind); }
-// D[tmem] (+)= A[smem] B[smem], issued by one lane of a converged warp
-W4A16_DEVICE void mma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
-        : "memory");
-}
-// the same with A in tensor memory
-W4A16_DEVICE void mma_ts_lo(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 db, {%2, %5};\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-        "r"(a_tmem), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
-        : "memory");
-}
+// D[tmem] = A[smem] B[smem] over D columns, issued by one lane of a converged warp; below it D (+)= P[tmem] V[smem]
+// over 128 keys
 template <int D>
 W4A16_DEVICE void score_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
     if constexpr (D == 128) asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
@@ -600,57 +579,69 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // ------------------------------------------------------------ MMAs
         // The warpgroups in turn: P V of a tile and the scores of the next one
         // go out together.
+        // What steers the loop is made uniform, for the descriptors' sake: 206 us against
+        // 218 for a 2048-token chunk of a 8448-token request, 32 / 8 heads of 128.
         constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<Ty>(D, true);
+        const uint32_t tm = uniform(tmem), sm = uniform(smem_u32(smem));
+        auto tile_at = [&](uint32_t slot, uint32_t kind) {  // a descriptor's low word; tile 0 is Q's first
+            return ((sm + slot * (uint32_t)L::kTile) >> 4) | kind;
+        };
         uint32_t tile0 = 0, items = 0, np[2] = {0, 0};
         bool ok = true;
         while (ok && walk.next(p, span, pc)) {
-            const int cnt[2] = {pc.duo ? pc.take : (pc.take + 1) / 2, pc.duo ? pc.take : pc.take / 2};
+            const int take = (int)uniform((uint32_t)pc.take);
+            const bool duo = uniform(pc.duo) != 0, two = uniform(pc.two) != 0;
+            const int cnt[2] = {duo ? take : (take + 1) / 2, duo ? take : take / 2};
             int scores = cnt[0] + cnt[1];
-            auto tile_of = [&](int g, int k) { return tile0 + (pc.duo ? k : 2 * k + g); };
-            auto score = [&](int g, int k) {  // S_g of the warpgroup's k-th tile
-                const uint32_t e = 2 * tile_of(g, k), sl = e % NS;
-                if (!mbar_wait_warp(full + sl, (e / NS) & 1, abort_flag, &g_chunk_status)) return false;
+            auto entry_of = [&](int g, int k) { return 2 * (tile0 + (uint32_t)(duo ? k : 2 * k + g)); };  // its keys
+            auto arrived = [&](uint32_t e) {
+                return mbar_wait_warp(full + e % NS, (e / NS) & 1, abort_flag, &g_chunk_status);
+            };
+            auto score = [&](int g, int k) {  // S_g of the group's k-th tile
+                const uint32_t sl = entry_of(g, k) % NS;
                 tc_fence_after();
-                const uint32_t qa = desc_low(smem_u32(smem + (pc.duo ? g : 0) * L::kTile), kDescK);
-                const uint32_t ka = desc_low(smem_u32(smem + L::kRingOff + sl * L::kTile), kDescK);
-                const uint32_t sd = uniform(tmem + L::kTS + 128 * g);
-                score_block<D>(sd, qa, ka, id_s);
+                score_block<D>(tm + L::kTS + 128 * g, tile_at(duo ? g : 0, kDescK), tile_at(2 + sl, kDescK), id_s);
                 mma_commit_warp(s_full + g);
-                if (!pc.duo || g == 1) mma_commit_warp(empty + sl);
+                if (!duo || g == 1) mma_commit_warp(empty + sl);
                 if (--scores == 0) mma_commit_warp(q_free);
-                return true;
             };
             ok = mbar_wait_warp(q_full, items & 1, abort_flag, &g_chunk_status);
-            for (int g = 0; g < 2 && ok; ++g)
-                if (cnt[g] > 0) ok = score(g, 0);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (!ok || cnt[g] == 0) continue;
+                if (!duo || g == 0) ok = arrived(entry_of(g, 0));
+                if (ok) score(g, 0);
+            }
             for (int k = 0; k < cnt[0] && ok; ++k) {
-                for (int g = 0; g < 2 && ok; ++g) {
-                    if (k >= cnt[g]) continue;
-                    const uint32_t e = 2 * tile_of(g, k) + 1, sl = e % NS;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!ok || k >= cnt[g]) continue;
+                    const uint32_t e = entry_of(g, k) + 1, sl = e % NS;
+                    const bool next = k + 1 < cnt[g];
                     if (k == 0 && items > 0)
                         ok = mbar_wait_warp(o_free + g, (items - 1) & 1, abort_flag, &g_chunk_status);
-                    ok = ok && mbar_wait_warp(full + sl, (e / NS) & 1, abort_flag, &g_chunk_status) &&
-                         mbar_spin_warp(p_full + g, np[g] & 1, abort_flag, &g_chunk_status);
-                    if (!ok) break;
+                    ok = ok && arrived(e);
+                    ok = ok && mbar_spin_warp(p_full + g, np[g] & 1, abort_flag, &g_chunk_status);
+                    if (!ok) continue;
                     ++np[g];
                     tc_fence_after();
-                    const uint32_t va = desc_low(smem_u32(smem + L::kRingOff + sl * L::kTile), kDescV);
-                    const uint32_t pa = uniform(tmem + L::kTS + 128 * g), od = uniform(tmem + L::kTO + D * g);
-                    const uint32_t more = uniform(k > 0 ? 1u : 0u);
-pv_block(od, pa, va, id_o, more);
-                    if (pc.two) pv_block(od, pa + 64, va, id_o, 1u);
-                    if (!pc.duo || g == 1) mma_commit_warp(empty + sl);
-                    if (k + 1 < cnt[g])
-                        ok = score(g, k + 1);
-                    else
+                    const uint32_t va = tile_at(2 + sl, kDescV), pa = tm + L::kTS + 128 * g, od = tm + L::kTO + D * g;
+                    pv_block(od, pa, va, id_o, k > 0 ? 1u : 0u);
+                    if (two) pv_block(od, pa + 64, va, id_o, 1u);
+                    if (!duo || g == 1) mma_commit_warp(empty + sl);
+                    if (!next) {
                         mma_commit_warp(o_full + g);
+                    } else {
+                        ok = arrived(entry_of(g, k + 1));
+                        if (ok) score(g, k + 1);
+                    }
                 }
             }
             if (ok && cnt[1] == 0) {  // a single tile: warpgroup 1 has nothing to wait for but the count
                 if (items > 0) ok = mbar_wait_warp(o_free + 1, (items - 1) & 1, abort_flag, &g_chunk_status);
                 mma_commit_warp(o_full + 1);
             }
-            tile0 += pc.take;
+            tile0 += take;
             ++items;
         }
         mma_commit_warp(done);
