@@ -386,30 +386,60 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def _int32(t, name, n=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+    """Address of a contiguous int32 CUDA tensor, of that many entries."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
-    if n is not None and (t.dim() != 1 or t.shape[0] != n):
+    if n is not None and (t.numel() != n or t.dim() != 1):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
-    return t
+    return t.data_ptr()
 
 
 def _block_table(t, requests):
+    """Columns and row stride of a block table."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2:
         raise ValueError("block_table must be a 2-D int32 CUDA tensor")
-    if t.shape[0] != requests or (t.stride(1) != 1 and t.shape[1] > 1 and requests > 0):
+    rows, columns = t.shape
+    row, column = t.stride()
+    if rows != requests or (column != 1 and columns > 1 and requests > 0):
         raise ValueError(f"block_table must be [{requests}, columns] with contiguous rows")
-    return t
+    return columns, row if requests > 1 else columns
 
 
 def _strided(t, name, dtype, dims):
-    """A CUDA tensor of that many dimensions whose last one is contiguous."""
+    """Shape and strides of a CUDA tensor of that many dimensions whose last one is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+    shape, stride = t.shape, t.stride()
+    if len(stride) != dims or (stride[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be {dims}-D with a contiguous last dimension")
-    return t.shape
+    return shape, stride
+
+
+# Workspaces of the calls that bring none: one a stream, so that calls on two
+# streams never share counters or partial results, zeroed on that stream.  A
+# buffer that became too small stays alive: a captured graph may hold it.  (A
+# call captured on a stream that has none yet adds the zeroing of its counters
+# to the graph; give such calls a workspace.)
+_stream_workspaces: dict = {}
+_outgrown_workspaces: list = []
+
+
+def _stream_workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
+    ws = _stream_workspaces.get((index, stream))
+    if ws is not None and ws.numel() >= nbytes:
+        return ws
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)):
+        if torch.cuda.is_current_stream_capturing():  # the graph's own; every replay zeroes its counters
+            ws = torch.empty(max(nbytes, 65536), dtype=torch.uint8, device=f"cuda:{index}")
+            ws[:65536].zero_()
+            return ws
+        fresh = new_workspace(max(nbytes, 2 * ws.numel() if ws is not None else 0), f"cuda:{index}")
+    if ws is not None:
+        _outgrown_workspaces.append(ws)
+    _stream_workspaces[(index, stream)] = fresh
+    return fresh
 
 
 def w4a16_page_plan(past_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
@@ -426,35 +456,36 @@ def w4a16_page_plan(past_len: torch.Tensor, new_len: torch.Tensor, free_pages: t
     [T], slot_map [T], pages_used [1]), all int32; T is slot_map's length, or
     max_tokens where slot_map is None (entries past the new tokens are -1)."""
     B = past_len.shape[0]
-    _int32(past_len, "past_len", B)
-    _int32(new_len, "new_len", B)
-    _int32(free_pages, "free_pages")
-    _block_table(block_table, B)
-    dev = past_len.device
+    past, new, free = _int32(past_len, "past_len", B), _int32(new_len, "new_len", B), _int32(free_pages, "free_pages")
+    columns, row = _block_table(block_table, B)
     if slot_map is None:
         if max_tokens is None:
             raise ValueError("give slot_map or max_tokens")
-        slot_map = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        slot_map = torch.empty(max_tokens, dtype=torch.int32, device=past_len.device)
     T = slot_map.shape[0]
-    _int32(slot_map, "slot_map", T)
-    positions = torch.empty(T, dtype=torch.int32, device=dev) if positions is None else _int32(positions, "positions", T)
-    q_start = torch.empty(B + 1, dtype=torch.int32, device=dev) if q_start is None else _int32(q_start, "q_start", B + 1)
-    kv_len = torch.empty(B, dtype=torch.int32, device=dev) if kv_len is None else _int32(kv_len, "kv_len", B)
-    pages_used = (torch.empty(1, dtype=torch.int32, device=dev) if pages_used is None
-                  else _int32(pages_used, "pages_used", 1))
-    args = _PLAN_ARGS.pack(past_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(), block_table.data_ptr(),
-                           q_start.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), slot_map.data_ptr(),
-                           pages_used.data_ptr(), block_table.stride(0) if B > 1 else block_table.shape[1], B,
-                           free_pages.numel(), block_table.shape[1], T, page_size, flags)
-    _raise(load_library().w4a16_page_plan(args, _stream(stream, dev.index)), "w4a16_page_plan")
+    if positions is None:
+        positions = torch.empty(T, dtype=torch.int32, device=past_len.device)
+    if q_start is None:
+        q_start = torch.empty(B + 1, dtype=torch.int32, device=past_len.device)
+    if kv_len is None:
+        kv_len = torch.empty(B, dtype=torch.int32, device=past_len.device)
+    if pages_used is None:
+        pages_used = torch.empty(1, dtype=torch.int32, device=past_len.device)
+    args = _PLAN_ARGS.pack(past, new, free, block_table.data_ptr(), _int32(q_start, "q_start", B + 1),
+                           _int32(kv_len, "kv_len", B), _int32(positions, "positions", T),
+                           _int32(slot_map, "slot_map", T), _int32(pages_used, "pages_used", 1), row, B,
+                           free_pages.numel(), columns, T, page_size, flags)
+    _raise(load_library().w4a16_page_plan(args, _stream(stream, past_len.get_device())), "w4a16_page_plan")
     return q_start, kv_len, positions, slot_map, pages_used
 
 
-def _cache_shape(k_cache, v_cache, dtype):
-    shape = _strided(k_cache, "k_cache", dtype, 4)
-    if _strided(v_cache, "v_cache", dtype, 4) != shape:
-        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(shape)}")
-    return shape
+def _caches(k_cache, v_cache, dtype):
+    """Shape of both caches, and their strides."""
+    shape, ks = _strided(k_cache, "k_cache", dtype, 4)
+    vshape, vs = _strided(v_cache, "v_cache", dtype, 4)
+    if vshape != shape:
+        raise ValueError(f"v_cache has shape {tuple(vshape)}, expected {tuple(shape)}")
+    return shape, ks, vs
 
 
 def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
@@ -464,19 +495,18 @@ def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_c
     heads, page_size, head_dim] at the slots of slot_map [T] (int32; negative
     or past the cache: skipped)."""
     dtype = k.dtype
-    T, heads, d = _strided(k, "k", dtype, 3)
-    if _strided(v, "v", dtype, 3) != k.shape:
-        raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(k.shape)}")
-    pages, ch, page, cd = _cache_shape(k_cache, v_cache, dtype)
+    shape, (kt, kh, _) = _strided(k, "k", dtype, 3)
+    vshape, (vt, vh, _) = _strided(v, "v", dtype, 3)
+    if vshape != shape:
+        raise ValueError(f"v has shape {tuple(vshape)}, expected {tuple(shape)}")
+    T, heads, d = shape
+    (pages, ch, page, cd), (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, dtype)
     if ch != heads or cd != d or dtype not in _DTYPES:
         raise ValueError(f"caches of {ch} heads of {cd} do not take k of {heads} heads of {d} in {dtype}")
-    _int32(slot_map, "slot_map", T)
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    args = _WRITE_ARGS.pack(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                            kt, kh, vt, vh, *k_cache.stride()[:3], *v_cache.stride()[:3], T, heads, d, pages, page,
+    args = _WRITE_ARGS.pack(k.data_ptr(), v.data_ptr(), _int32(slot_map, "slot_map", T), k_cache.data_ptr(),
+                            v_cache.data_ptr(), kt, kh, vt, vh, kcp, kch, kcs, vcp, vch, vcs, T, heads, d, pages, page,
                             _DTYPES[dtype], flags, 0)
-    _raise(load_library().w4a16_kv_write(args, _stream(stream, k.device.index)), "w4a16_kv_write")
+    _raise(load_library().w4a16_kv_write(args, _stream(stream, k.get_device())), "w4a16_kv_write")
 
 
 def w4a16_paged_attention_workspace_bytes(tokens: int, requests: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -498,41 +528,38 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     every request's number of new tokens.  window = 0: no window.  lse: [T, Hq]
     f32, filled if given.  Returns out [T, Hq, d]."""
     dtype = q.dtype
-    T, Hq, d = _strided(q, "q", dtype, 3)
-    pages, Hkv, page, cd = _cache_shape(k_cache, v_cache, dtype)
+    shape, (qt, qh, _) = _strided(q, "q", dtype, 3)
+    T, Hq, d = shape
+    (pages, Hkv, page, cd), (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, dtype)
     if cd != d or dtype not in _DTYPES:
         raise ValueError(f"caches with heads of {cd} do not go with q with heads of {d} in {dtype}")
     B = kv_len.shape[0]
-    _int32(kv_len, "kv_len", B)
-    _int32(q_start, "q_start", B + 1)
-    _block_table(block_table, B)
+    kv, start = _int32(kv_len, "kv_len", B), _int32(q_start, "q_start", B + 1)
+    columns, row = _block_table(block_table, B)
     if out is None:
         out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
-    elif _strided(out, "out", dtype, 3) != q.shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    oshape, (ot, oh, _) = _strided(out, "out", dtype, 3)
+    if oshape != shape:
+        raise ValueError(f"out has shape {tuple(oshape)}, expected {tuple(shape)}")
     if lse is not None:
         _check(lse, "lse", torch.float32, (T, Hq))
-    lib = load_library()
+    lib, idx = load_library(), q.get_device()
+    st = _stream(stream, idx)
     if workspace is None:
-        idx = q.device.index
         key = ("paged_attention", T, B, Hq, Hkv, d, max_q, idx)
         need = _need_cache.get(key)
         if need is None:
             need = int(lib.w4a16_paged_attention_workspace_bytes(T, B, Hq, Hkv, d, max_q))
             _need_cache[key] = need
         if need:
-            workspace = _cached_workspace(need, q.device)
-    qt, qh, _ = q.stride()
-    ot, oh, _ = out.stride()
-    args = _ATTN_ARGS.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                           q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
-                           0 if lse is None else lse.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
+            workspace = _stream_workspace(need, idx, st)
+    args = _ATTN_ARGS.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), start, kv,
+                           out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                           0 if workspace is None else workspace.data_ptr(),
                            0 if workspace is None else workspace.numel() * workspace.element_size(), qt, qh, ot, oh,
-                           *k_cache.stride()[:3], *v_cache.stride()[:3],
-                           block_table.stride(0) if B > 1 else block_table.shape[1], T, B, Hq, Hkv, d, pages, page,
-                           block_table.shape[1], max_q, window, int(block), _DTYPES[dtype],
-                           0.0 if scale is None else scale, flags)
-    _raise(lib.w4a16_paged_attention(args, _stream(stream, q.device.index)), "w4a16_paged_attention")
+                           kcp, kch, kcs, vcp, vch, vcs, row, T, B, Hq, Hkv, d, pages, page, columns, max_q, window,
+                           int(block), _DTYPES[dtype], 0.0 if scale is None else scale, flags)
+    _raise(lib.w4a16_paged_attention(args, st), "w4a16_paged_attention")
     return out
 
 
@@ -541,7 +568,7 @@ def _rows_of(t, name, dtype, rows):
         return 0
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
-    if t.dim() != 1 or t.shape[0] != rows:
+    if t.numel() != rows or t.dim() != 1:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows,)}")
     return t.data_ptr()
 
@@ -564,31 +591,33 @@ def w4a16_sample(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.T
     dtype = logits.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"logits must be bf16, fp16 or f32, got {dtype}")
-    R, V = _strided(logits, "logits", dtype, 2)
-    if tuple(_strided(noise, "noise", torch.float32, 2)) != (R, V):
-        raise ValueError(f"noise has shape {tuple(noise.shape)}, expected {(R, V)}")
+    shape, (lr, _) = _strided(logits, "logits", dtype, 2)
+    nshape, (nr, _) = _strided(noise, "noise", torch.float32, 2)
+    if nshape != shape:
+        raise ValueError(f"noise has shape {tuple(nshape)}, expected {tuple(shape)}")
+    R, V = shape
     if token is None:
         token = torch.empty(R, dtype=torch.int32, device=logits.device)
     f32 = torch.float32
-    lib = load_library()
+    lib, idx = load_library(), logits.get_device()
+    st = _stream(stream, idx)
     if workspace is None:
         filters = top_k is not None or top_p is not None or min_p is not None
-        key = ("sample", R, V, filters, logits.device.index)
+        key = ("sample", R, V, filters, idx)
         need = _need_cache.get(key)
         if need is None:
             need = int(lib.w4a16_sample_workspace_bytes(R, V, int(filters)))
             _need_cache[key] = need
         if need:
-            workspace = _cached_workspace(need, logits.device)
+            workspace = _stream_workspace(need, idx, st)
     args = _SAMPLE_ARGS.pack(logits.data_ptr(), noise.data_ptr(), _rows_of(temperature, "temperature", f32, R),
                              _rows_of(top_k, "top_k", torch.int32, R), _rows_of(top_p, "top_p", f32, R),
                              _rows_of(min_p, "min_p", f32, R), _rows_of(token, "token", torch.int32, R),
                              _rows_of(logprob, "logprob", f32, R),
                              0 if workspace is None else workspace.data_ptr(),
                              0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             logits.stride(0) if R > 1 else V,
-                             noise.stride(0) if R > 1 else V, R, V, _DTYPES[dtype], flags)
-    _raise(lib.w4a16_sample(args, _stream(stream, logits.device.index)), "w4a16_sample")
+                             lr if R > 1 else V, nr if R > 1 else V, R, V, _DTYPES[dtype], flags)
+    _raise(lib.w4a16_sample(args, st), "w4a16_sample")
     return token
 
 

@@ -494,3 +494,39 @@ def test_operators_count_their_launches(w):
         n0 = w.w4a16_launch_count()
         f()
         assert w.w4a16_launch_count() >= n0 + least
+
+
+def test_workspaces_of_streams_and_graphs(w):
+    """Calls without a workspace: two streams at once, a graph captured before and kept over a larger call."""
+    def call_of(a):
+        tables = i32(a.table), i32(a.q_start), i32(a.L)
+        outs = [torch.zeros_like(a.q) for _ in range(5)]
+        return outs, lambda i, **kw: w.w4a16_paged_attention(a.q, a.kc, a.vc, *tables, int(a.n.max()), out=outs[i], **kw)
+
+    souts, small = call_of(Attn([(2000, 1), (50, 1)], 8, 2, 128, 16, "bf16", seed=21))
+    louts, large = call_of(Attn([(2500, 1)] * 6 + [(700, 200)], 16, 4, 128, 16, "bf16", seed=22))
+    small(0)
+    large(0)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for i in range(1, 5):
+        small(i, stream=s1)
+        large(i, stream=s2)
+    torch.cuda.synchronize()
+    for i in range(1, 5):
+        assert torch.equal(souts[0], souts[i]) and torch.equal(louts[0], louts[i])
+    for warm in (False, True):
+        s = torch.cuda.Stream()
+        if warm:
+            small(1, stream=s)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            small(1)
+        large(1, stream=s)  # a larger workspace on the stream of the capture
+        for _ in range(3):
+            torch.cuda.synchronize()
+            souts[1].zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(souts[0], souts[1]) and torch.equal(louts[0], louts[1])
