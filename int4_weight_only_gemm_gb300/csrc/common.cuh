@@ -140,19 +140,6 @@ W4A16_DEVICE bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
     return false;
 }
 
-// Whether the phase with the given parity is complete, without waiting.
-W4A16_DEVICE bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // As mbar_wait_warp for waits of well under a microsecond: polls instead of
 // sleeping (a sleeping thread wakes ~90 ns later); the flag and the clock are
 // looked at every 64 polls.

@@ -2,10 +2,10 @@
 //
 //     cache[slot / p][h][slot % p] = x[t][h]   for slot = slot_map[t] in range
 //
-// A thread moves one 16-byte piece of a key and the same piece of the value,
-// for kKvRun tokens (kKvStep apart) with all their loads in flight; the pieces
-// of a token are consecutive threads, so reads and writes are whole rows.
-// Bound: HBM (each byte read once and written once).
+// A thread moves one 16-byte piece of a key and the same piece of the value;
+// the pieces of a token are consecutive threads, so reads and writes are whole
+// rows; eight CTAs an SM keep enough loads in flight.  Bound: HBM, each byte
+// read once and written once.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -16,44 +16,29 @@ constexpr int kKvThreads = 256;
 struct KvWriteParams {
     w4a16_kv_write_args a;
     int shift, pieces, per_head;     // pieces of 8 elements in a token and in a head
-    uint32_t pm, hm;                 // divisions by them (FastDiv)
-    int ps, hs;
+    FastDiv by_head, by_token;
     int64_t slots;                   // num_pages * page_size
 };
 
-template <int RUN>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteParams p) {
     pdl_launch_dependents();
     pdl_wait();
     const w4a16_kv_write_args& a = p.a;
     const int64_t total = (int64_t)a.tokens * p.pieces, stride = (int64_t)gridDim.x * kKvThreads;
-    for (int64_t i0 = (int64_t)blockIdx.x * kKvThreads + threadIdx.x; i0 < total; i0 += stride * RUN) {
-        uint4 k[RUN], v[RUN];
-        int slot[RUN], h[RUN], c[RUN];
-#pragma unroll
-        for (int u = 0; u < RUN; ++u) {
-            const int64_t i = i0 + u * stride;
-            slot[u] = -1;
-            if (i < total) {
-                const int t = (int)(i / p.pieces), r = (int)(i - (int64_t)t * p.pieces);
-                h[u] = div_by(r, p.hm, p.hs);
-                c[u] = (r - h[u] * p.per_head) * 8;
-                slot[u] = a.slot_map[t];
-                k[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + t * a.k_token +
-                                                            h[u] * a.k_head + c[u]));
-                v[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + t * a.v_token +
-                                                            h[u] * a.v_head + c[u]));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < RUN; ++u) {
-            if (slot[u] < 0 || slot[u] >= p.slots) continue;
-            const int64_t pg = slot[u] >> p.shift, sl = slot[u] & ((1 << p.shift) - 1);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_cache) + pg * a.kc_page + h[u] * a.kc_head +
-                                      sl * a.kc_slot + c[u]) = k[u];
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_cache) + pg * a.vc_page + h[u] * a.vc_head +
-                                      sl * a.vc_slot + c[u]) = v[u];
-        }
+    for (int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x; i < total; i += stride) {
+        const int t = total < (1ll << 31) ? div_by((int)i, p.by_token.m, p.by_token.s) : (int)(i / p.pieces);
+        const int r = (int)(i - (int64_t)t * p.pieces), h = div_by(r, p.by_head.m, p.by_head.s);
+        const int c = (r - h * p.per_head) * 8, slot = a.slot_map[t];
+        const uint4 k = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + t * a.k_token +
+                                                             h * a.k_head + c));
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + t * a.v_token +
+                                                             h * a.v_head + c));
+        if (slot < 0 || slot >= p.slots) continue;
+        const int64_t pg = slot >> p.shift, sl = slot & ((1 << p.shift) - 1);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_cache) + pg * a.kc_page + h * a.kc_head + sl * a.kc_slot +
+                                  c) = k;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_cache) + pg * a.vc_page + h * a.vc_head + sl * a.vc_slot +
+                                  c) = v;
     }
 }
 
@@ -64,15 +49,12 @@ cudaError_t launch_kv_write(const w4a16_kv_write_args& a, int sms, cudaStream_t 
     while ((1 << p.shift) < a.page_size) ++p.shift;
     p.per_head = a.head_dim / 8;
     p.pieces = p.per_head * a.heads;
-    const FastDiv fh = fast_div(p.per_head), fp = fast_div(p.pieces);
-    p.hm = fh.m;
-    p.hs = fh.s;
-    p.pm = fp.m;
-    p.ps = fp.s;
+    p.by_head = fast_div(p.per_head);
+    p.by_token = fast_div(p.pieces);
     p.slots = (int64_t)a.num_pages * a.page_size;
     const int64_t total = (int64_t)a.tokens * p.pieces;
     const int64_t ctas = (total + kKvThreads - 1) / kKvThreads;
-    return launch_kernel(kv_write_kernel<1>, dim3((unsigned)(ctas < 65536 ? ctas : 65536)), dim3(kKvThreads), 0, s,
+    return launch_kernel(kv_write_kernel, dim3((unsigned)(ctas < 65536 ? ctas : 65536)), dim3(kKvThreads), 0, s,
                          (a.flags & W4A16_FLAG_PDL) != 0, p);
 }
 

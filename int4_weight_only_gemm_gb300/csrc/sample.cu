@@ -826,155 +826,155 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
     float mass_a = 0.f, mass_b = 0.f;  // their weights
     bool slow = false;
     while (true) {
-    if (flat) {
-        if (!all) low = wide;
-        all = true;
-        // ---- 4. too many: bins of equal width in l, from the maximum down
-        for (int i = threadIdx.x; i < kBins; i += NT) hist[i] = 0;
-        if (threadIdx.x == 0) win[6] = 0;
-        const float width = fmaxf((lmax - low) * 1.0001f, 1e-30f);
-        // no bin narrower than 4 units in the last place of a logit: equal z lie in one bin or in two neighbours
-        const float scale = fminf((kBins - 3) / width, 2097152.f / fmaxf(fmaxf(fabsf(lmax), fabsf(low)), 1e-30f));
-        // round((lmax - l) scale), by adding 2^23: never rising with l
-        auto bin_of = [&](float l) {
-            return (int)(__float_as_uint(fminf((lmax - l) * scale, (float)(kBins - 1)) + 8388608.f) & 0x7fffffu);
-        };
-        __syncthreads();
-        row.from(low, aside, [&](float l, int) { atomicAdd(&hist[bin_of(l)], 1); });
-        __syncthreads();
-        // thread: PB bins; sums of counts, and of least and greatest weights, before them
-        constexpr int PB = kBins / NT;
-        const int base = threadIdx.x * PB;
-        const float step = q.c2 / scale;  // of the exponent, base 2, a bin
-        float cnt[PB], lo[PB], up[PB], ct = 0.f, lt = 0.f, ut = 0.f;
-#pragma unroll
-        for (int i = 0; i < PB; ++i) {
-            cnt[i] = (float)hist[base + i];  // at most 2^24: exact
-            lo[i] = cnt[i] * ex2(-((float)(base + i) + 0.51f) * step);
-            up[i] = cnt[i] * ex2(fminf(-((float)(base + i) - 0.51f) * step, 0.f));
-            ct += cnt[i];
-            lt += lo[i];
-            ut += up[i];
-        }
-        const float cb = cta_before(ct, rf), lb = cta_before(lt, rf), ub = cta_before(ut, rf);
-        if (threadIdx.x == 0) {
-            win[0] = win[1] = win[2] = kBins;
-            bound[0] = bound[1] = 0.f;
-        }
-        __syncthreads();
-        if (q.by_k) {  // the bin in which the k-th token lies
-            float c = cb, a = lb, u = ub;
+        if (flat) {
+            if (!all) low = wide;
+            all = true;
+            // ---- 4. too many: bins of equal width in l, from the maximum down
+            for (int i = threadIdx.x; i < kBins; i += NT) hist[i] = 0;
+            if (threadIdx.x == 0) win[6] = 0;
+            const float width = fmaxf((lmax - low) * 1.0001f, 1e-30f);
+            // no bin narrower than 4 units in the last place of a logit: equal z lie in one bin or in two neighbours
+            const float scale = fminf((kBins - 3) / width, 2097152.f / fmaxf(fmaxf(fabsf(lmax), fabsf(low)), 1e-30f));
+            // round((lmax - l) scale), by adding 2^23: never rising with l
+            auto bin_of = [&](float l) {
+                return (int)(__float_as_uint(fminf((lmax - l) * scale, (float)(kBins - 1)) + 8388608.f) & 0x7fffffu);
+            };
+            __syncthreads();
+            row.from(low, aside, [&](float l, int) { atomicAdd(&hist[bin_of(l)], 1); });
+            __syncthreads();
+            // thread: PB bins; sums of counts, and of least and greatest weights, before them
+            constexpr int PB = kBins / NT;
+            const int base = threadIdx.x * PB;
+            const float step = q.c2 / scale;  // of the exponent, base 2, a bin
+            float cnt[PB], lo[PB], up[PB], ct = 0.f, lt = 0.f, ut = 0.f;
 #pragma unroll
             for (int i = 0; i < PB; ++i) {
-                if (c < (float)k && c + cnt[i] >= (float)k) {
-                    win[2] = base + i;
-                    bound[0] = a;          // the kept weight is at least this
-                    bound[1] = u + up[i];  // and at most this
-                }
-                c += cnt[i], a += lo[i], u += up[i];
+                cnt[i] = (float)hist[base + i];  // at most 2^24: exact
+                lo[i] = cnt[i] * ex2(-((float)(base + i) + 0.51f) * step);
+                up[i] = cnt[i] * ex2(fminf(-((float)(base + i) - 0.51f) * step, 0.f));
+                ct += cnt[i];
+                lt += lo[i];
+                ut += up[i];
             }
-        }
-        __syncthreads();
-        const int bk = win[2];
-        if (q.by_p) {
-            const float t_lo = q.tp * (q.by_k ? bound[0] : sum) * 0.9999f;
-            const float t_up = q.tp * (q.by_k ? bound[1] : sum) * 1.0001f;
-            float a = lb, u = ub;
+            const float cb = cta_before(ct, rf), lb = cta_before(lt, rf), ub = cta_before(ut, rf);
+            if (threadIdx.x == 0) {
+                win[0] = win[1] = win[2] = kBins;
+                bound[0] = bound[1] = 0.f;
+            }
+            __syncthreads();
+            if (q.by_k) {  // the bin in which the k-th token lies
+                float c = cb, a = lb, u = ub;
 #pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                u += up[i];
-                a += lo[i];
-                if (u >= t_lo) atomicMin(&win[0], base + i);  // the cut is in this bin or below
-                if (a >= t_up) atomicMin(&win[1], base + i);  // in this bin or above
-            }
-        }
-        __syncthreads();
-        int b1 = win[0], b2 = win[1];
-        slow = (q.by_k && bk >= kBins - 1) || (q.by_p && (q.by_k ? b1 : b2) >= kBins - 1);
-        // equal z may have unequal l, one bin apart at most: a bin more on each side
-        if (q.by_k && b2 > bk) b2 = bk;
-        if (!q.by_p) b1 = b2 = bk;
-        b1 = max(b1 - 1, 0);
-        b2 = min(b2 + 1, kBins - 1);
-        int bk1 = q.by_k ? max(bk - 1, 0) : kBins, bk2 = q.by_k ? min(bk + 1, kBins - 1) : kBins - 1;
-        if (q.by_k && bk1 <= b2 + 1) {  // one window
-            b2 = bk2;
-            bk1 = kBins;
-        }
-        const bool apart = bk1 < kBins;
-        if (!slow) {
-            int ca = 0, cc = 0;
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                const int b = base + i;
-                if (b < b1) ca += (int)cnt[i];
-                if (apart && b > b2 && b < bk1) cc += (int)cnt[i];
-            }
-            above = cta_count<NT>(ca, ri);
-            between = cta_count<NT>(cc, ri);
-            row.from(low, aside, [&](float l, int i) {
-                const int b = bin_of(l);
-                if (b < b1) {
-                    const float z = z_of(l, T);
-                    mass_a += weight(z);
-                    score(z, i);
-                } else if (b <= b2 || (apart && b >= bk1 && b <= bk2)) {
-                    const int at = atomicAdd(&win[6], 1);
-                    if (at < kList) {
-                        list_z[at] = ~key_of(z_of(l, T));
-                        list_i[at] = i;
+                for (int i = 0; i < PB; ++i) {
+                    if (c < (float)k && c + cnt[i] >= (float)k) {
+                        win[2] = base + i;
+                        bound[0] = a;          // the kept weight is at least this
+                        bound[1] = u + up[i];  // and at most this
                     }
-                } else if (apart && b < bk1) {
-                    mass_b += weight(z_of(l, T));
+                    c += cnt[i], a += lo[i], u += up[i];
                 }
-            });
-            mass_a = cta_sum<NT>(mass_a, rf);
-            mass_b = cta_sum<NT>(mass_b, rf);
-            n = win[6];
-            slow = n > kList;
+            }
+            __syncthreads();
+            const int bk = win[2];
+            if (q.by_p) {
+                const float t_lo = q.tp * (q.by_k ? bound[0] : sum) * 0.9999f;
+                const float t_up = q.tp * (q.by_k ? bound[1] : sum) * 1.0001f;
+                float a = lb, u = ub;
+#pragma unroll
+                for (int i = 0; i < PB; ++i) {
+                    u += up[i];
+                    a += lo[i];
+                    if (u >= t_lo) atomicMin(&win[0], base + i);  // the cut is in this bin or below
+                    if (a >= t_up) atomicMin(&win[1], base + i);  // in this bin or above
+                }
+            }
+            __syncthreads();
+            int b1 = win[0], b2 = win[1];
+            slow = (q.by_k && bk >= kBins - 1) || (q.by_p && (q.by_k ? b1 : b2) >= kBins - 1);
+            // equal z may have unequal l, one bin apart at most: a bin more on each side
+            if (q.by_k && b2 > bk) b2 = bk;
+            if (!q.by_p) b1 = b2 = bk;
+            b1 = max(b1 - 1, 0);
+            b2 = min(b2 + 1, kBins - 1);
+            int bk1 = q.by_k ? max(bk - 1, 0) : kBins, bk2 = q.by_k ? min(bk + 1, kBins - 1) : kBins - 1;
+            if (q.by_k && bk1 <= b2 + 1) {  // one window
+                b2 = bk2;
+                bk1 = kBins;
+            }
+            const bool apart = bk1 < kBins;
+            if (!slow) {
+                int ca = 0, cc = 0;
+#pragma unroll
+                for (int i = 0; i < PB; ++i) {
+                    const int b = base + i;
+                    if (b < b1) ca += (int)cnt[i];
+                    if (apart && b > b2 && b < bk1) cc += (int)cnt[i];
+                }
+                above = cta_count<NT>(ca, ri);
+                between = cta_count<NT>(cc, ri);
+                row.from(low, aside, [&](float l, int i) {
+                    const int b = bin_of(l);
+                    if (b < b1) {
+                        const float z = z_of(l, T);
+                        mass_a += weight(z);
+                        score(z, i);
+                    } else if (b <= b2 || (apart && b >= bk1 && b <= bk2)) {
+                        const int at = atomicAdd(&win[6], 1);
+                        if (at < kList) {
+                            list_z[at] = ~key_of(z_of(l, T));
+                            list_i[at] = i;
+                        }
+                    } else if (apart && b < bk1) {
+                        mass_b += weight(z_of(l, T));
+                    }
+                });
+                mass_a = cta_sum<NT>(mass_a, rf);
+                mass_b = cta_sum<NT>(mass_b, rf);
+                n = win[6];
+                slow = n > kList;
+            }
         }
-    }
-    if (slow) break;
-    // ---- 3. the list decides
-    int size = 32;
-    while (size < n) size <<= 1;
-    for (int i = n + (int)threadIdx.x; i < size; i += NT) {
-        list_z[i] = 0xffffffffu;
-        list_i[i] = 0x7fffffff;
-    }
-    if (size <= 256)
-        sort_few<NT>(list_z, list_i, hist, size);
-    else
-        sort_list<NT>(list_z, list_i, size);
-    constexpr int PL = kList / NT;
-    const int per = max(size / NT, 1), base = (int)threadIdx.x * per;  // entries a thread, and its first
-    // entries that top-k keeps (a second window lies behind `between` tokens)
-    const int kept_k = q.by_k ? min(n, k - above - between) : n;
-    float w[PL], wt = 0.f;
+        if (slow) break;
+        // ---- 3. the list decides
+        int size = 32;
+        while (size < n) size <<= 1;
+        for (int i = n + (int)threadIdx.x; i < size; i += NT) {
+            list_z[i] = 0xffffffffu;
+            list_i[i] = 0x7fffffff;
+        }
+        if (size <= 256)
+            sort_few<NT>(list_z, list_i, hist, size);
+        else
+            sort_list<NT>(list_z, list_i, size);
+        constexpr int PL = kList / NT;
+        const int per = max(size / NT, 1), base = (int)threadIdx.x * per;  // entries a thread, and its first
+        // entries that top-k keeps (a second window lies behind `between` tokens)
+        const int kept_k = q.by_k ? min(n, k - above - between) : n;
+        float w[PL], wt = 0.f;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-        w[i] = i < per && base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
-        wt += w[i];
-    }
-    const float before = cta_before(wt, rf), listed_mass = cta_sum<NT>(wt, rf);
-    const float total = q.by_k ? mass_a + mass_b + listed_mass : sum;
-    const float want = q.by_p ? q.tp * total : INFINITY;
-    if (!all && listed_mass < want) {
-        flat = true;  // the nucleus reaches below the list
-        continue;
-    }
-    float at = mass_a + before, z[PL], e[PL];
+        for (int i = 0; i < PL; ++i) {
+            w[i] = i < per && base + i < kept_k ? weight(value_of(~list_z[base + i])) : 0.f;
+            wt += w[i];
+        }
+        const float before = cta_before(wt, rf), listed_mass = cta_sum<NT>(wt, rf);
+        const float total = q.by_k ? mass_a + mass_b + listed_mass : sum;
+        const float want = q.by_p ? q.tp * total : INFINITY;
+        if (!all && listed_mass < want) {
+            flat = true;  // the nucleus reaches below the list
+            continue;
+        }
+        float at = mass_a + before, z[PL], e[PL];
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {  // the kept ones' random numbers, all on their way
-        const int x = base + i;
-        const bool kept = i < per && x < kept_k && (!q.by_p || at < want || (above == 0 && x == 0));
-        z[i] = kept ? value_of(~list_z[x]) : 0.f;
-        e[i] = kept ? noise[list_i[x]] : NAN;  // (takes no part)
-        at += w[i];
-    }
+        for (int i = 0; i < PL; ++i) {  // the kept ones' random numbers, all on their way
+            const int x = base + i;
+            const bool kept = i < per && x < kept_k && (!q.by_p || at < want || (above == 0 && x == 0));
+            z[i] = kept ? value_of(~list_z[x]) : 0.f;
+            e[i] = kept ? noise[list_i[x]] : NAN;  // (takes no part)
+            at += w[i];
+        }
 #pragma unroll
-    for (int i = 0; i < PL; ++i) score_of(z[i], e[i], list_i[min(base + i, kList - 1)]);
-    break;
+        for (int i = 0; i < PL; ++i) score_of(z[i], e[i], list_i[min(base + i, kList - 1)]);
+        break;
     }
     if (slow) {
         // ---- 5. bisection
