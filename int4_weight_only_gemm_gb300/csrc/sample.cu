@@ -230,15 +230,19 @@ struct Slice {
         constexpr int U = 4;
         if (first && (int)threadIdx.x < head) one(at((int)threadIdx.x), (int)threadIdx.x);
         const uint4* vec = reinterpret_cast<const uint4*>(row + head);
-        for (int v = v0 + (int)threadIdx.x; v < v1; v += U * NT) {
-            uint4 x[U];
+        int v = v0 + (int)threadIdx.x;
+        uint4 x[U];  // U loads in flight all the time: one is issued as one is used
+        if (v < v1) {
 #pragma unroll
             for (int u = 0; u < U; ++u) x[u] = vec[min(v + u * NT, v1 - 1)];
+        }
+        for (; v < v1; v += U * NT) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (v + u * NT >= v1) break;
                 float l[VE];
                 split(x[u], l);
+                x[u] = vec[min(v + (u + U) * NT, v1 - 1)];
                 many(l, head + (v + u * NT) * VE);
             }
         }
@@ -429,32 +433,37 @@ struct Pass {
             if constexpr (STATS)
                 slice.each([&](float l, int i) { one(l, i); }, [&](const float (&l)[VE], int i0) { many(l, i0); });
         } else if (noise4) {
-            // logits and their random numbers together, U vectors in flight
-            constexpr int U = 4, NE = VE / 4;
+            // logits and their random numbers together, U vectors in flight all the time
+            constexpr int U = VE == 4 ? 4 : 3, NE = VE / 4;
             const uint4* vec = reinterpret_cast<const uint4*>(slice.row + slice.head);
             const float4* nv = reinterpret_cast<const float4*>(noise + slice.head);
             if (slice.first && (int)threadIdx.x < slice.head) one(slice.at((int)threadIdx.x), (int)threadIdx.x);
-            for (int v = slice.v0 + (int)threadIdx.x; v < slice.v1; v += U * NT) {
-                uint4 x[U];
-                float4 e[U][NE];
+            uint4 x[U];
+            float4 e[U][NE];
+            auto load = [&](int u, int y) {
+                y = min(y, slice.v1 - 1);  // past the end: again, and not counted
+                x[u] = __ldcs(vec + y);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int y = min(v + u * NT, slice.v1 - 1);  // past the end: again, and not counted
-                    x[u] = __ldcs(vec + y);
+                for (int z = 0; z < NE; ++z) e[u][z] = __ldcs(nv + y * NE + z);
+            };
+            int v = slice.v0 + (int)threadIdx.x;
+            if (v < slice.v1) {
 #pragma unroll
-                    for (int z = 0; z < NE; ++z) e[u][z] = __ldcs(nv + y * NE + z);
-                }
+                for (int u = 0; u < U; ++u) load(u, v + u * NT);
+            }
+            for (; v < slice.v1; v += U * NT) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (v + u * NT >= slice.v1) break;
                     const int i0 = slice.head + (v + u * NT) * VE;
                     float l[VE], t = -INFINITY;
                     slice.split(x[u], l);
-                    many(l, i0);
 #pragma unroll
                     for (int z = 0; z < NE; ++z)
                         t = fmaxf(t, fmaxf(fmaxf(approx(l[4 * z], e[u][z].x), approx(l[4 * z + 1], e[u][z].y)),
                                            fmaxf(approx(l[4 * z + 2], e[u][z].z), approx(l[4 * z + 3], e[u][z].w))));
+                    load(u, v + (u + U) * NT);
+                    many(l, i0);
                     enter(t, V + i0);
                 }
             }
