@@ -21,8 +21,8 @@ struct KvWriteParams {
 };
 
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvWriteParams p) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const w4a16_kv_write_args& a = p.a;
     const int64_t total = (int64_t)a.tokens * p.pieces, stride = (int64_t)gridDim.x * kKvThreads;
     for (int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x; i < total; i += stride) {

@@ -54,8 +54,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const w4a16_pag
     int* fs = qs + B + 1;      // [B + 1] first free page of each request
     __shared__ int sa[kPlanWarps], sf[kPlanWarps];
     const int page = 1 << shift;
-    pdl_launch_dependents();
+    // In this order: with the next launch let go before the wait, several waiting
+    // kernels queue up behind one another; a host that launches about as fast as the
+    // kernel runs (2048 requests) then saw 15 us a call instead of 9.5.
     pdl_wait();
+    pdl_launch_dependents();
 
     // the two sums: thread i takes the requests [i * per, i * per + per)
     const int per = (B + kPlanThreads - 1) / kPlanThreads;

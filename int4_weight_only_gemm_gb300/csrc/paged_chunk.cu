@@ -368,11 +368,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
         prefetch_tmap(&tmap_k);
         prefetch_tmap(&tmap_v);
     }
-    pdl_launch_dependents();
     // Behind the small-row kernel of the same call there is nothing to wait for:
     // that kernel let this one start once everything before it was done, and the
     // two have requests, counters and workspace of their own.
     if (!p.after_small) pdl_wait();
+    pdl_launch_dependents();
 
     // ---- this CTA's part of the line --------------------------------------
     // The line runs over the requests, their items, the key heads and the key

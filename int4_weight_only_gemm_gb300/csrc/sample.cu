@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(kStatThreads, 2) sample_stats_kernel(const w4a
     __shared__ float rf[32];
     __shared__ int ri[32];
     __shared__ int last;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
     const Slice<DT, NT> slice(p.logits, r * p.logits_row, V, rank, S);
     const RowParams q(p, r);
@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
     Aside* aside = reinterpret_cast<Aside*>(hist + kBins);  // one a warp
     __shared__ int win[8];    // windows of bins (two), tokens above and between, list length, last arrival
     __shared__ float bound[2];
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int r = (int)blockIdx.y, rank = (int)blockIdx.x, V = p.vocab;
     const RowParams q(p, r);
     if (q.greedy) return;
