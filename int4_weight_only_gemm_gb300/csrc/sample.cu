@@ -14,8 +14,11 @@
 //      row: with k of them, or p of the row's weight, at and above a bound, so
 //      many of the row's tokens are; min-p by its own bound -- and collected in
 //      a list of the row;
-//   3. the row's last CTA sorts up to kList candidates and settles the cuts and
-//      the race there.  Only their random numbers are read;
+//   3. the row's last CTA settles the cuts and the race among up to kWide
+//      candidates: a few it sorts; of more it finds the cut's place in bins of
+//      their counts or weights and sorts what lies in that bin alone, tokens
+//      above it are kept for certain.  Only the kept ones' random numbers are
+//      read;
 //   4. with more candidates (a flat row) it counts them in bins, which bounds
 //      where the cuts fall; tokens above are kept for certain and take part in
 //      the race as they are read, their weights summed; only the tokens around
@@ -37,7 +40,9 @@
 namespace w4a16 {
 
 constexpr int kStatThreads = 512, kPickThreads = 512;
-constexpr int kList = 2048;   // candidates that are sorted
+constexpr int kWide = 8192;   // candidates of a row's list
+constexpr int kList = 2048;   // those of them, around a cut, that are sorted
+constexpr int kFew = 256;     // those that are sorted by counting
 constexpr int kBins = 4096;   // of the histogram of a flat row
 constexpr int kTopBins = 2 * kPickThreads;  // of the histogram of the first pass's maxima
 constexpr int kMaxSplits = 8;  // CTAs a row, a power of two
@@ -54,9 +59,9 @@ struct SliceStats {
 // A row's part of the workspace; behind it the maxima of the S x kStatThreads threads of the first pass.
 struct RowSpace {
     SliceStats stats[kMaxSplits];
-    int found, pad[3];            // candidates collected (may exceed kList)
-    uint32_t key[kList];          // candidates: keys of z, all bits turned (rising key is falling z)
-    int index[kList];
+    int found, pad[3];            // candidates collected (may exceed kWide)
+    uint32_t key[kWide];          // candidates: keys of z, all bits turned (rising key is falling z)
+    int index[kWide];
     W4A16_DEVICE float* maxima() { return reinterpret_cast<float*>(this + 1); }
 };
 __host__ __device__ constexpr size_t row_space(int S) { return sizeof(RowSpace) + (size_t)S * kStatThreads * 4; }
@@ -249,11 +254,18 @@ struct Slice {
         if (last && tail + (int)threadIdx.x < V) one(at(tail + (int)threadIdx.x), tail + (int)threadIdx.x);
     }
     // one(logit, index) for the tokens with a logit >= low, by the whole CTA.
-    // They are set aside per warp and handed over 32 at a time, so that `one`,
-    // which divides, counts or collects, runs with full warps however rare they
-    // are, and is there once and not for every load.
     template <typename One>
     W4A16_DEVICE void from(float low, Aside* aside, One one) const {
+        batches(low, aside, [&](int n, float l, int i) {
+            if ((int)(threadIdx.x & 31) < n) one(l, i);
+        });
+    }
+    // The same by warps: some(n, logit, index) with n tokens in the first lanes.
+    // They are set aside per warp and handed over 32 at a time, so that `some`,
+    // which divides, counts or collects, runs with full warps however rare they
+    // are, and is there once and not for every load.
+    template <typename Some>
+    W4A16_DEVICE void batches(float low, Aside* aside, Some some) const {
         constexpr int U = 4;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         Aside& own = aside[warp];
@@ -277,7 +289,7 @@ struct Slice {
                 const int i = lane < n ? own.i[at] : 0;
                 count -= n;
                 __syncwarp();
-                if (lane < n) one(l, i);
+                some(n, l, i);
                 __syncwarp();
             }
         };
@@ -712,7 +724,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
     float low = lmax - R * T * 1.0001f;
     bool listed = q.by_p && !q.by_k;  // whether the candidates may be few
     bool all = true;                  // whether every token that may be kept is among them
-    const float wide = low;
+    const float wide = low, unit = 2147483648.f / sum;
     const int most = min(kList / 2, S * NT / 2);  // maxima that make a good list: so many make ~20 % more tokens
     if (V > kList && (q.by_p || (q.by_k && q.k <= most))) {
         // bins of the maxima, their counts (top-k) or their weights' floors in 2^-31 of the sum (top-p): with
@@ -723,12 +735,13 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
             if (top[i] > -INFINITY) least_top = fminf(least_top, top[i]);
         least_top = cta_min<NT>(least_top, rf);
         const float scale = (kTopBins - 2) / fmaxf(fminf(lmax - least_top, 40.f * T), 1e-30f);
+        // (of top-p a second time by count, where all maxima do not weigh enough: most nuclei still lie
+        // within, and their weight will tell)
         for (int turn = q.by_k ? 1 : 0; turn < 2; ++turn) {
-            const bool by_count = turn == 1;  // of top-p too, where the maxima do not weigh enough
             uint2* bins = reinterpret_cast<uint2*>(hist);
-            const float unit = 2147483648.f / sum;
-            const uint32_t target = by_count ? (uint32_t)(q.by_k ? q.k : most)
-                                             : (uint32_t)fmaxf(fminf(q.tp * 1.00001f, 1.f) * 2147483648.f, 1.f);
+            const uint32_t target = q.by_k ? (uint32_t)q.k
+                                    : turn ? (uint32_t)min(S * NT * 7 / 8, kWide * 3 / 8)
+                                           : (uint32_t)fmaxf(fminf(q.tp * 1.00001f, 1.f) * 2147483648.f, 1.f);
             __syncthreads();
             bins[threadIdx.x] = make_uint2(0u, 0u);
             if (threadIdx.x == 0) win[0] = kTopBins;
@@ -737,7 +750,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
 #pragma unroll
             for (int i = 0; i < kMaxSplits; ++i)
                 if (top[i] > -INFINITY)
-                    atomicAdd(hist + bin_of(top[i]), by_count ? 1 : (int)(uint32_t)(ex2((top[i] - lmax) * q.c2) * unit));
+                    atomicAdd(hist + bin_of(top[i]), turn ? 1 : (int)(uint32_t)(ex2((top[i] - lmax) * q.c2) * unit));
             __syncthreads();
             const uint2 mine = bins[threadIdx.x];
             const uint32_t before = cta_before(mine.x + mine.y, ri);
@@ -751,13 +764,11 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
             for (int i = 0; i < kMaxSplits; ++i)
                 if (top[i] > -INFINITY && bin_of(top[i]) <= cut) tau = fminf(tau, top[i]);
             tau = cta_min<NT>(tau, rf);
-            if (q.by_k) {
+            if (q.by_k || tau > low) {
                 low = tau;
-                listed = true;
-            } else if (tau > low) {
-                low = tau;
-                all = !by_count;  // by count the nucleus may reach further: its weight will tell
+                all = q.by_k || turn == 0;
             }
+            listed = true;
             break;
         }
     }
@@ -783,16 +794,13 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
             space->stats[rank].ibest = ibest;
         }
     } else if (listed) {
-        bool full = false;  // a list that has overflowed takes no more from this thread
-        slice.from(low, aside, [&](float l, int i) {
-            if (!full) {
-                const int at = atomicAdd(&space->found, 1);
-                if (at < kList) {
-                    space->key[at] = ~key_of(z_of(l, T));
-                    space->index[at] = i;
-                } else {
-                    full = true;
-                }
+        slice.batches(low, aside, [&](int m, float l, int i) {
+            const int lane = (int)threadIdx.x & 31;
+            int at = lane == 0 ? atomicAdd(&space->found, m) : 0;
+            at = __shfl_sync(0xffffffffu, at, 0) + lane;
+            if (lane < m && at < kWide) {
+                space->key[at] = ~key_of(z_of(l, T));
+                space->index[at] = i;
             }
         });
     }
@@ -818,9 +826,11 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
     // (the first entries with their number, whether they are there or not)
     const uint32_t key0 = __ldcg(space->key + threadIdx.x);
     const int index0 = __ldcg(space->index + threadIdx.x);
-    int n = listed ? __ldcg(&space->found) : kList + 1;
-    bool flat = n > kList;
-    if (!flat) {
+    int n = listed ? __ldcg(&space->found) : kWide + 1;
+    // (both cuts on a long list: the second is one of what the first leaves)
+    const bool in_bins = n > kFew && n <= kWide && q.by_k != q.by_p;
+    bool flat = n > kWide || ((n > kList || !all) && !in_bins);
+    if (!flat && !in_bins) {
         if ((int)threadIdx.x < n) {
             list_z[threadIdx.x] = key0;
             list_i[threadIdx.x] = index0;
@@ -834,116 +844,166 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
     int above = 0, between = 0;        // tokens above the windows around the cuts, and between them
     float mass_a = 0.f, mass_b = 0.f;  // their weights
     bool slow = false;
-    while (true) {
-        if (flat) {
-            if (!all) low = wide;
-            all = true;
-            // ---- 4. too many: bins of equal width in l, from the maximum down
-            for (int i = threadIdx.x; i < kBins; i += NT) hist[i] = 0;
-            if (threadIdx.x == 0) win[6] = 0;
-            const float width = fmaxf((lmax - low) * 1.0001f, 1e-30f);
-            // no bin narrower than 4 units in the last place of a logit: equal z lie in one bin or in two neighbours
-            const float scale = fminf((kBins - 3) / width, 2097152.f / fmaxf(fmaxf(fabsf(lmax), fabsf(low)), 1e-30f));
-            // round((lmax - l) scale), by adding 2^23: never rising with l
-            auto bin_of = [&](float l) {
-                return (int)(__float_as_uint(fminf((lmax - l) * scale, (float)(kBins - 1)) + 8388608.f) & 0x7fffffu);
-            };
-            __syncthreads();
-            row.from(low, aside, [&](float l, int) { atomicAdd(&hist[bin_of(l)], 1); });
-            __syncthreads();
-            // thread: PB bins; sums of counts, and of least and greatest weights, before them
-            constexpr int PB = kBins / NT;
-            const int base = threadIdx.x * PB;
-            const float step = q.c2 / scale;  // of the exponent, base 2, a bin
-            float cnt[PB], lo[PB], up[PB], ct = 0.f, lt = 0.f, ut = 0.f;
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                cnt[i] = (float)hist[base + i];  // at most 2^24: exact
-                lo[i] = cnt[i] * ex2(-((float)(base + i) + 0.51f) * step);
-                up[i] = cnt[i] * ex2(fminf(-((float)(base + i) - 0.51f) * step, 0.f));
-                ct += cnt[i];
-                lt += lo[i];
-                ut += up[i];
-            }
-            const float cb = cta_before(ct, rf), lb = cta_before(lt, rf), ub = cta_before(ut, rf);
-            if (threadIdx.x == 0) {
-                win[0] = win[1] = win[2] = kBins;
-                bound[0] = bound[1] = 0.f;
-            }
-            __syncthreads();
-            if (q.by_k) {  // the bin in which the k-th token lies
-                float c = cb, a = lb, u = ub;
-#pragma unroll
-                for (int i = 0; i < PB; ++i) {
-                    if (c < (float)k && c + cnt[i] >= (float)k) {
-                        win[2] = base + i;
-                        bound[0] = a;          // the kept weight is at least this
-                        bound[1] = u + up[i];  // and at most this
-                    }
-                    c += cnt[i], a += lo[i], u += up[i];
+    if (in_bins) {
+        // bins of z, their counts (top-k) or weights in 2^-31 of the sum (top-p, rounded to nearest: a sum
+        // of 8192 is off by 2^-19 of it at most): the cut lies in the bin in which `target` is reached
+        const float range = fminf(zmax - z_of(fmaxf(low, -kBig), T), 80.f), scale = (kTopBins - 2) / fmaxf(range, 1e-30f);
+        auto bin_of = [&](float z) { return (int)fminf((zmax - z) * scale, (float)(kTopBins - 1)); };
+        const uint32_t target = q.by_k ? (uint32_t)k : (uint32_t)fmaxf(fminf(q.tp, 1.f) * 2147483648.f, 1.f);
+        uint2* bins = reinterpret_cast<uint2*>(hist);
+        bins[threadIdx.x] = make_uint2(0u, 0u);
+        if (threadIdx.x == 0) {
+            win[0] = kTopBins;
+            win[1] = win[6] = 0;
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += NT) {
+            const float z = value_of(~__ldcg(space->key + i));
+            atomicAdd(hist + bin_of(z), q.by_k ? 1 : (int)__float2uint_rn(weight(z) * unit));
+        }
+        __syncthreads();
+        const uint2 mine = bins[threadIdx.x];
+        const uint32_t before = cta_before(mine.x + mine.y, ri);
+        if (before < target && before + mine.x + mine.y >= target) {
+            const bool second = before + mine.x < target;
+            win[0] = 2 * threadIdx.x + second;
+            win[1] = (int)(before + (second ? mine.x : 0u));  // in the bins above
+        }
+        __syncthreads();
+        const int cut = win[0];  // kTopBins: all are kept
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += NT) {
+            const uint32_t y = __ldcg(space->key + i);
+            const int x = __ldcg(space->index + i), b = bin_of(value_of(~y));
+            if (b < cut) {
+                score(value_of(~y), x);
+            } else if (b == cut) {
+                const int at = atomicAdd(&win[6], 1);
+                if (at < kList) {
+                    list_z[at] = y;
+                    list_i[at] = x;
                 }
-            }
-            __syncthreads();
-            const int bk = win[2];
-            if (q.by_p) {
-                const float t_lo = q.tp * (q.by_k ? bound[0] : sum) * 0.9999f;
-                const float t_up = q.tp * (q.by_k ? bound[1] : sum) * 1.0001f;
-                float a = lb, u = ub;
-#pragma unroll
-                for (int i = 0; i < PB; ++i) {
-                    u += up[i];
-                    a += lo[i];
-                    if (u >= t_lo) atomicMin(&win[0], base + i);  // the cut is in this bin or below
-                    if (a >= t_up) atomicMin(&win[1], base + i);  // in this bin or above
-                }
-            }
-            __syncthreads();
-            int b1 = win[0], b2 = win[1];
-            slow = (q.by_k && bk >= kBins - 1) || (q.by_p && (q.by_k ? b1 : b2) >= kBins - 1);
-            // equal z may have unequal l, one bin apart at most: a bin more on each side
-            if (q.by_k && b2 > bk) b2 = bk;
-            if (!q.by_p) b1 = b2 = bk;
-            b1 = max(b1 - 1, 0);
-            b2 = min(b2 + 1, kBins - 1);
-            int bk1 = q.by_k ? max(bk - 1, 0) : kBins, bk2 = q.by_k ? min(bk + 1, kBins - 1) : kBins - 1;
-            if (q.by_k && bk1 <= b2 + 1) {  // one window
-                b2 = bk2;
-                bk1 = kBins;
-            }
-            const bool apart = bk1 < kBins;
-            if (!slow) {
-                int ca = 0, cc = 0;
-#pragma unroll
-                for (int i = 0; i < PB; ++i) {
-                    const int b = base + i;
-                    if (b < b1) ca += (int)cnt[i];
-                    if (apart && b > b2 && b < bk1) cc += (int)cnt[i];
-                }
-                above = cta_count<NT>(ca, ri);
-                between = cta_count<NT>(cc, ri);
-                row.from(low, aside, [&](float l, int i) {
-                    const int b = bin_of(l);
-                    if (b < b1) {
-                        const float z = z_of(l, T);
-                        mass_a += weight(z);
-                        score(z, i);
-                    } else if (b <= b2 || (apart && b >= bk1 && b <= bk2)) {
-                        const int at = atomicAdd(&win[6], 1);
-                        if (at < kList) {
-                            list_z[at] = ~key_of(z_of(l, T));
-                            list_i[at] = i;
-                        }
-                    } else if (apart && b < bk1) {
-                        mass_b += weight(z_of(l, T));
-                    }
-                });
-                mass_a = cta_sum<NT>(mass_a, rf);
-                mass_b = cta_sum<NT>(mass_b, rf);
-                n = win[6];
-                slow = n > kList;
             }
         }
-        if (slow) break;
+        __syncthreads();
+        n = win[6];
+        above = q.by_k ? win[1] : win[1] != 0;  // (of top-p only whether there are any)
+        mass_a = q.by_k ? 0.f : (float)(uint32_t)win[1] / unit;
+        flat = n > kList || (!all && cut == kTopBins);  // too many equals, or the nucleus reaches below the list
+        if (flat) {
+            above = 0, mass_a = 0.f;
+            __syncthreads();
+        }
+    }
+    if (flat) {
+        if (!all) low = wide;
+        // ---- 4. too many: bins of equal width in l, from the maximum down
+        for (int i = threadIdx.x; i < kBins; i += NT) hist[i] = 0;
+        if (threadIdx.x == 0) win[6] = 0;
+        const float width = fmaxf((lmax - low) * 1.0001f, 1e-30f);
+        // no bin narrower than 4 units in the last place of a logit: equal z lie in one bin or in two neighbours
+        const float scale = fminf((kBins - 3) / width, 2097152.f / fmaxf(fmaxf(fabsf(lmax), fabsf(low)), 1e-30f));
+        // round((lmax - l) scale), by adding 2^23: never rising with l
+        auto bin_of = [&](float l) {
+            return (int)(__float_as_uint(fminf((lmax - l) * scale, (float)(kBins - 1)) + 8388608.f) & 0x7fffffu);
+        };
+        __syncthreads();
+        row.from(low, aside, [&](float l, int) { atomicAdd(&hist[bin_of(l)], 1); });
+        __syncthreads();
+        // thread: PB bins; sums of counts, and of least and greatest weights, before them
+        constexpr int PB = kBins / NT;
+        const int base = threadIdx.x * PB;
+        const float step = q.c2 / scale;  // of the exponent, base 2, a bin
+        float cnt[PB], lo[PB], up[PB], ct = 0.f, lt = 0.f, ut = 0.f;
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            cnt[i] = (float)hist[base + i];  // at most 2^24: exact
+            lo[i] = cnt[i] * ex2(-((float)(base + i) + 0.51f) * step);
+            up[i] = cnt[i] * ex2(fminf(-((float)(base + i) - 0.51f) * step, 0.f));
+            ct += cnt[i];
+            lt += lo[i];
+            ut += up[i];
+        }
+        const float cb = cta_before(ct, rf), lb = cta_before(lt, rf), ub = cta_before(ut, rf);
+        if (threadIdx.x == 0) {
+            win[0] = win[1] = win[2] = kBins;
+            bound[0] = bound[1] = 0.f;
+        }
+        __syncthreads();
+        if (q.by_k) {  // the bin in which the k-th token lies
+            float c = cb, a = lb, u = ub;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                if (c < (float)k && c + cnt[i] >= (float)k) {
+                    win[2] = base + i;
+                    bound[0] = a;          // the kept weight is at least this
+                    bound[1] = u + up[i];  // and at most this
+                }
+                c += cnt[i], a += lo[i], u += up[i];
+            }
+        }
+        __syncthreads();
+        const int bk = win[2];
+        if (q.by_p) {
+            const float t_lo = q.tp * (q.by_k ? bound[0] : sum) * 0.9999f;
+            const float t_up = q.tp * (q.by_k ? bound[1] : sum) * 1.0001f;
+            float a = lb, u = ub;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                u += up[i];
+                a += lo[i];
+                if (u >= t_lo) atomicMin(&win[0], base + i);  // the cut is in this bin or below
+                if (a >= t_up) atomicMin(&win[1], base + i);  // in this bin or above
+            }
+        }
+        __syncthreads();
+        int b1 = win[0], b2 = win[1];
+        slow = (q.by_k && bk >= kBins - 1) || (q.by_p && (q.by_k ? b1 : b2) >= kBins - 1);
+        // equal z may have unequal l, one bin apart at most: a bin more on each side
+        if (q.by_k && b2 > bk) b2 = bk;
+        if (!q.by_p) b1 = b2 = bk;
+        b1 = max(b1 - 1, 0);
+        b2 = min(b2 + 1, kBins - 1);
+        int bk1 = q.by_k ? max(bk - 1, 0) : kBins, bk2 = q.by_k ? min(bk + 1, kBins - 1) : kBins - 1;
+        if (q.by_k && bk1 <= b2 + 1) {  // one window
+            b2 = bk2;
+            bk1 = kBins;
+        }
+        const bool apart = bk1 < kBins;
+        if (!slow) {
+            int ca = 0, cc = 0;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int b = base + i;
+                if (b < b1) ca += (int)cnt[i];
+                if (apart && b > b2 && b < bk1) cc += (int)cnt[i];
+            }
+            above = cta_count<NT>(ca, ri);
+            between = cta_count<NT>(cc, ri);
+            row.from(low, aside, [&](float l, int i) {
+                const int b = bin_of(l);
+                if (b < b1) {
+                    const float z = z_of(l, T);
+                    mass_a += weight(z);
+                    score(z, i);
+                } else if (b <= b2 || (apart && b >= bk1 && b <= bk2)) {
+                    const int at = atomicAdd(&win[6], 1);
+                    if (at < kList) {
+                        list_z[at] = ~key_of(z_of(l, T));
+                        list_i[at] = i;
+                    }
+                } else if (apart && b < bk1) {
+                    mass_b += weight(z_of(l, T));
+                }
+            });
+            mass_a = cta_sum<NT>(mass_a, rf);
+            mass_b = cta_sum<NT>(mass_b, rf);
+            n = win[6];
+            slow = n > kList;
+        }
+    }
+    if (!slow) {
         // ---- 3. the list decides
         int size = 32;
         while (size < n) size <<= 1;
@@ -951,7 +1011,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
             list_z[i] = 0xffffffffu;
             list_i[i] = 0x7fffffff;
         }
-        if (size <= 256)
+        if (size <= kFew)
             sort_few<NT>(list_z, list_i, hist, size);
         else
             sort_list<NT>(list_z, list_i, size);
@@ -968,10 +1028,6 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
         const float before = cta_before(wt, rf), listed_mass = cta_sum<NT>(wt, rf);
         const float total = q.by_k ? mass_a + mass_b + listed_mass : sum;
         const float want = q.by_p ? q.tp * total : INFINITY;
-        if (!all && listed_mass < want) {
-            flat = true;  // the nucleus reaches below the list
-            continue;
-        }
         float at = mass_a + before, z[PL], e[PL];
 #pragma unroll
         for (int i = 0; i < PL; ++i) {  // the kept ones' random numbers, all on their way
@@ -983,7 +1039,6 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
         }
 #pragma unroll
         for (int i = 0; i < PL; ++i) score_of(z[i], e[i], list_i[min(base + i, kList - 1)]);
-        break;
     }
     if (slow) {
         // ---- 5. bisection
