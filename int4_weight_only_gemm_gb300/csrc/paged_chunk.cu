@@ -35,6 +35,14 @@
 // from the definition instead (attn_row), so that a NaN stays with the rows
 // that see it.
 //
+// Bound: the chain softmax -> P -> MMAs -> scores of the two warpgroups, ~3700
+// clocks for a key tile of 256 rows, of which the tensor pipe works 2048.
+// Measured: a 2048-token chunk of a request of 8448 positions, 32 query heads over
+// 8 key heads of 128, bf16 (249 GFLOP): 206 us, 1.21 PFLOP/s (the tensor pipe
+// active 49 %); with all its pages in L2 203 us.  16 blocks of 16 draft tokens
+// over 4080 positions each (269 MB of keys and values): 54.5 us, 4.9 TB/s, 47 us
+// with the pages in L2.
+//
 // Every wait is bounded: on a timeout the kernel records W4A16_ETIMEOUT, ends
 // its copies and MMAs, frees its tensor memory and returns.
 #include <cuda.h>
@@ -579,8 +587,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // ------------------------------------------------------------ MMAs
         // The warpgroups in turn: P V of a tile and the scores of the next one
         // go out together.
-        // What steers the loop is made uniform, for the descriptors' sake: 206 us against
-        // 218 for a 2048-token chunk of a 8448-token request, 32 / 8 heads of 128.
+        // What steers the loop is made uniform, for the descriptors' sake: 206 us
+        // against 218 for the chunk above.
         constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<Ty>(D, true);
         const uint32_t tm = uniform(tmem), sm = uniform(smem_u32(smem));
         auto tile_at = [&](uint32_t slot, uint32_t kind) {  // a descriptor's low word; tile 0 is Q's first

@@ -24,6 +24,13 @@
 // copy unit of an SM for ~100 clocks, 20 bytes a clock, below what HBM delivers
 // to an SM; with them 64 requests took 248 us.
 //
+// Measured, 32 query heads over 8 key heads of 128, bf16, 16-slot pages: 64
+// requests of up to 8448 positions (1.18 GB) 182 us, 6.5 TB/s; one request of
+// 2304 positions 10.3 us, of which ~3.0 k clocks go to the cut of the line, 2.5 k
+// to the first table entries and copies, 1.9 k to the keys and values
+// themselves, 2.0 k to the warps' results and 2.4 k to the joining of the 18
+// pieces.
+//
 // Positions that a row does not see are masked in the scores; the values of
 // positions that no row of the tile sees (stale slots of the last page, slots
 // before the window) are cleared in shared memory first, and non-finite values
