@@ -94,7 +94,7 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cuda
     if (!large) return cudaSuccess;
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes + paged_decode_part_bytes(a.head_dim, sms));
     // (behind the small-row kernel always as its dependent: its CTAs take the SMs as those are done)
-    const cudaError_t e = launch_paged_chunk(p, bf16, a.head_dim, sms, s, pdl || small);
+    const cudaError_t e = launch_paged_chunk(p, bf16, a.head_dim, (int64_t)a.max_q * p.G <= 128, sms, s, pdl || small);
     if (e == cudaSuccess) note_launch();
     return e;
 }

@@ -180,6 +180,7 @@ cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int d, int 
 
 // the other requests (paged_chunk.cu)
 size_t paged_chunk_part_bytes(int d, int sms);
-cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl);
+// one: no request has more than 128 rows a key head
+cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, bool one, int sms, cudaStream_t s, bool pdl);
 
 }  // namespace w4a16

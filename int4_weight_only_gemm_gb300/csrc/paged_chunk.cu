@@ -60,12 +60,15 @@ constexpr int kChTwo = 256;  // rows that see fewer positions carry their weight
 constexpr int kChSnap = 2, kChJoin = 12;  // key tiles; see the line
 constexpr int kChCounters = 1024;  // first arrival counter of this kernel (the small-row kernel's lie below)
 
-template <int D>
+// ONE: no request has more rows a key head than one row tile (draft blocks);
+// the second tile's place then holds another slot of the ring.
+template <int D, bool ONE>
 struct Ch {
     static constexpr int kSlabs = D / 64;
     static constexpr int kTile = kSlabs * 16384;    // bytes of 128 rows of keys, values or queries
-    static constexpr int kSlots = D == 128 ? 5 : 10;
-    static constexpr int kRingOff = 2 * kTile;
+    static constexpr int kRows = ONE ? 1 : 2;       // row tiles of an item
+    static constexpr int kSlots = (D == 128 ? 7 : 12) - kRows;
+    static constexpr int kRingOff = kRows * kTile;
     static constexpr int kMlOff = kRingOff + kSlots * kTile;
     static constexpr int kBarOff = kMlOff + 2048;
     static constexpr int kMissOff = kBarOff + 384;            // [8] pages of a tile that are not there
@@ -74,7 +77,8 @@ struct Ch {
     static constexpr int kPartHalf = 128 * (D + 2);           // floats of one row tile's partial result
     static constexpr uint32_t kTS = 0, kTO = 256;             // tensor memory: S and P of both tiles, then O
 };
-static_assert(Ch<128>::kSmem <= 232448 && Ch<64>::kSmem <= 232448, "shared memory");
+static_assert(Ch<128, true>::kSmem <= 232448 && Ch<128, false>::kSmem <= 232448, "shared memory");
+static_assert(Ch<64, true>::kSmem <= 232448 && Ch<64, false>::kSmem <= 232448, "shared memory");
 
 // ---- instructions ---------------------------------------------------------
 // Operand descriptors (K-major and 128-byte swizzle as smem_desc_sw128 has them;
@@ -271,12 +275,21 @@ struct ChunkPiece {
     bool duo;                 // two row tiles (else both warpgroups share the first)
     bool two;                 // weights in two parts
 };
+// Ring entries of a piece of n tiles, from its first on.  With items of one row
+// tile (ONE) they come in the order in which the MMA warp takes them, the scores
+// of two tiles ahead: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1); else K0 V0 K1 V1 ..
+template <bool ONE>
+W4A16_DEVICE uint32_t keys_at(uint32_t t) { return !ONE ? 2 * t : t ? 2 * t - 1 : 0; }
+template <bool ONE>
+W4A16_DEVICE uint32_t values_at(uint32_t t, uint32_t n) { return !ONE || t + 1 == n ? 2 * t + 1 : 2 * t + 2; }
 // Walks a CTA's part of the line; every warp walks it for itself.
 struct ChunkWalk {
     int b, hk, q, off, items;
     int64_t at, left;
     Request r;
-    W4A16_DEVICE bool next(const PagedAttnParams& p, int span, ChunkPiece& c) {
+    template <bool ONE>
+    W4A16_DEVICE bool next(const PagedAttnParams& p, int toks, ChunkPiece& c) {
+        const int span = ONE ? toks : 2 * toks;
         if (left <= 0) return false;
         c.r = r;
         c.it = item_of(p, r, q, span);
@@ -286,7 +299,7 @@ struct ChunkWalk {
         c.off = off;
         c.take = (int)(left < c.it.tiles - off ? left : c.it.tiles - off);
         c.first = at - off;
-        c.duo = 2 * c.it.tokens > span;
+        c.duo = !ONE && c.it.tokens > toks;
         c.two = c.it.e0 - c.it.lo0 + 1 < kChTwo;
         at += c.take;
         left -= c.take;
@@ -317,11 +330,11 @@ W4A16_DEVICE void attn_rows_from_definition(const PagedAttnParams& p, int b, Req
     }
 }
 
-template <typename Ty, int D>
+template <typename Ty, int D, bool ONE>
 __global__ void __launch_bounds__(kChThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedAttnParams p) {
-    using L = Ch<D>;
+    using L = Ch<D, ONE>;
     constexpr int NS = L::kSlots;
     extern __shared__ __align__(1024) unsigned char smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
@@ -347,7 +360,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = (int)blockIdx.x;
-    const int toks = 128 / p.G, span = 2 * toks;  // tokens of a row tile and of an item
+    const int toks = 128 / p.G, span = L::kRows * toks;  // tokens of a row tile and of an item
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -527,42 +540,57 @@ __global__ void __launch_bounds__(kChThreads, 1)
     if (warp == 9) {
         // ---------------------------------------------------------- copies
         const int page = 1 << p.shift, rows = page < kChKeys ? page : kChKeys, boxes = kChKeys / rows;
-        uint32_t e = 0;     // ring entries: keys 2 i, values 2 i + 1 of this CTA's tile i
+        uint32_t e = 0, tile0 = 0;  // the next ring entry, and the piece's first tile
         bool ok = true;
-        while (ok && walk.next(p, span, pc)) {
+        while (ok && walk.next<ONE>(p, toks, pc)) {
             const int* row = p.table + (int64_t)pc.b * p.table_stride;
             auto entry = [&](int t) {  // lane's box of the piece's tile t
                 const int j = (pc.it.t0 + pc.off + t) * kChKeys + lane * rows, col = j >> p.shift;
                 // boxes that no row sees are not read: -2
-                if (lane >= boxes || j > pc.it.e1 || j + rows <= pc.it.lo0) return -2;
+                if (t >= pc.take || lane >= boxes || j > pc.it.e1 || j + rows <= pc.it.lo0) return -2;
                 return col < p.columns ? row[col] : -1;
             };
-            int ent = entry(0);
-            for (int t = 0; t < pc.take; ++t) {
-                const int j = (pc.it.t0 + pc.off + t) * kChKeys + lane * rows, slot = j & (page - 1);
+            auto load = [&](int t, int kv, int ent) {  // the next ring entry: tile t's keys or values
+                const int slot = ((pc.it.t0 + pc.off + t) * kChKeys + lane * rows) & (page - 1), sl = e % NS;
                 const bool there = ent >= 0 && ent < p.pages;
                 const int pg = there ? ent : p.pages;  // past the tensor: filled with zeros
                 const uint32_t no = __ballot_sync(0xffffffffu, !there && ent != -2);
-                if (t + 1 < pc.take) ent = entry(t + 1);
-                for (int kv = 0; kv < 2; ++kv, ++e) {
-                    const int sl = e % NS;
-                    if (e >= NS) ok = mbar_wait_warp(empty + sl, (e / NS - 1) & 1, abort_flag, &g_chunk_status);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (kv == 0) miss[(e >> 1) & 7] = no;
-                        mbar_arrive_expect_tx(full + sl, (uint32_t)L::kTile);
-                    }
-                    __syncwarp();
-                    if (lane < boxes) {
-                        unsigned char* dst = smem + L::kRingOff + sl * L::kTile + lane * rows * 128;
-#pragma unroll
-                        for (int s = 0; s < L::kSlabs; ++s)
-                            tma_load_4d(dst + s * 16384, kv ? &tmap_v : &tmap_k, 64 * s, slot, pc.hk, pg, full + sl);
-                    }
-                    __syncwarp();
+                if (e >= NS) ok = mbar_wait_warp(empty + sl, (e / NS - 1) & 1, abort_flag, &g_chunk_status);
+                if (!ok) return;
+                if (lane == 0) {
+                    if (kv == 0) miss[(tile0 + t) & 7] = no;
+                    mbar_arrive_expect_tx(full + sl, (uint32_t)L::kTile);
                 }
-                if (!ok) break;
+                __syncwarp();
+                if (lane < boxes) {
+                    unsigned char* dst = smem + L::kRingOff + sl * L::kTile + lane * rows * 128;
+#pragma unroll
+                    for (int s = 0; s < L::kSlabs; ++s)
+                        tma_load_4d(dst + s * 16384, kv ? &tmap_v : &tmap_k, 64 * s, slot, pc.hk, pg, full + sl);
+                }
+                __syncwarp();
+                ++e;
+            };
+            int ent = entry(0);  // of tile t
+            if constexpr (ONE) {
+                int next = entry(1);
+                load(0, 0, ent);
+                for (int t = 0; t < pc.take && ok; ++t) {
+                    const int after = entry(t + 2);
+                    if (t + 1 < pc.take) load(t + 1, 0, next);
+                    if (ok) load(t, 1, ent);
+                    ent = next;
+                    next = after;
+                }
+            } else {
+                for (int t = 0; t < pc.take && ok; ++t) {
+                    const int cur = ent;
+                    ent = entry(t + 1);
+                    load(t, 0, cur);
+                    if (ok) load(t, 1, cur);
+                }
             }
+            tile0 += pc.take;
         }
         // the copies in flight land before the CTA ends
         for (uint32_t i = e > NS ? e - NS : 0; i < e; ++i)
@@ -570,7 +598,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     } else if (warp == 10) {
         // --------------------------------------------------------- queries
         uint32_t items = 0;
-        while (walk.next(p, span, pc)) {
+        while (walk.next<ONE>(p, toks, pc)) {
             if (items > 0 && !mbar_wait_warp(q_free, (items - 1) & 1, abort_flag, &g_chunk_status)) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(q_full, (uint32_t)((pc.duo ? 2 : 1) * L::kSlabs * toks * p.G * 128));
@@ -596,19 +624,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
         };
         uint32_t tile0 = 0, items = 0, np[2] = {0, 0};
         bool ok = true;
-        while (ok && walk.next(p, span, pc)) {
+        while (ok && walk.next<ONE>(p, toks, pc)) {
             const int take = (int)uniform((uint32_t)pc.take);
-            const bool duo = uniform(pc.duo) != 0, two = uniform(pc.two) != 0;
+            const bool duo = !ONE && uniform(pc.duo) != 0, two = uniform(pc.two) != 0;
             const int cnt[2] = {duo ? take : (take + 1) / 2, duo ? take : take / 2};
             int scores = cnt[0] + cnt[1];
-            auto entry_of = [&](int g, int k) { return 2 * (tile0 + (uint32_t)(duo ? k : 2 * k + g)); };  // its keys
+            auto tile_of = [&](int g, int k) { return (uint32_t)(duo ? k : 2 * k + g); };
+            auto keys_of = [&](int g, int k) { return 2 * tile0 + keys_at<ONE>(tile_of(g, k)); };
             auto arrived = [&](uint32_t e) {
                 return mbar_wait_warp(full + e % NS, (e / NS) & 1, abort_flag, &g_chunk_status);
             };
             auto score = [&](int g, int k) {  // S_g of the group's k-th tile
-                const uint32_t sl = entry_of(g, k) % NS;
+                const uint32_t sl = keys_of(g, k) % NS;
                 tc_fence_after();
-                score_block<D>(tm + L::kTS + 128 * g, tile_at(duo ? g : 0, kDescK), tile_at(2 + sl, kDescK), id_s);
+                score_block<D>(tm + L::kTS + 128 * g, tile_at(duo ? g : 0, kDescK), tile_at(L::kRows + sl, kDescK), id_s);
                 mma_commit_warp(s_full + g);
                 if (!duo || g == 1) mma_commit_warp(empty + sl);
                 if (--scores == 0) mma_commit_warp(q_free);
@@ -617,14 +646,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 if (!ok || cnt[g] == 0) continue;
-                if (!duo || g == 0) ok = arrived(entry_of(g, 0));
+                if (!duo || g == 0) ok = arrived(keys_of(g, 0));
                 if (ok) score(g, 0);
             }
             for (int k = 0; k < cnt[0] && ok; ++k) {
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     if (!ok || k >= cnt[g]) continue;
-                    const uint32_t e = entry_of(g, k) + 1, sl = e % NS;
+                    const uint32_t e = 2 * tile0 + values_at<ONE>(tile_of(g, k), (uint32_t)take), sl = e % NS;
                     const bool next = k + 1 < cnt[g];
                     if (k == 0 && items > 0)
                         ok = mbar_wait_warp(o_free + g, (items - 1) & 1, abort_flag, &g_chunk_status);
@@ -633,14 +662,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     if (!ok) continue;
                     ++np[g];
                     tc_fence_after();
-                    const uint32_t va = tile_at(2 + sl, kDescV), pa = tm + L::kTS + 128 * g, od = tm + L::kTO + D * g;
+                    const uint32_t va = tile_at(L::kRows + sl, kDescV), pa = tm + L::kTS + 128 * g, od = tm + L::kTO + D * g;
                     pv_block(od, pa, va, id_o, k > 0 ? 1u : 0u);
                     if (two) pv_block(od, pa + 64, va, id_o, 1u);
                     if (!duo || g == 1) mma_commit_warp(empty + sl);
                     if (!next) {
                         mma_commit_warp(o_full + g);
                     } else {
-                        ok = arrived(entry_of(g, k + 1));
+                        ok = arrived(keys_of(g, k + 1));
                         if (ok) score(g, k + 1);
                     }
                 }
@@ -662,7 +691,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int tok = row / p.G, hh = row - tok * p.G;
         uint32_t tile0 = 0, items = 0, ns = 0, joins = 0;
         bool ok = true;
-        while (ok && walk.next(p, span, pc)) {
+        while (ok && walk.next<ONE>(p, toks, pc)) {
             const int base_tok = pc.duo ? g * toks : 0;
             const int mytok = base_tok + tok;  // of the item
             const bool valid = tok < toks && mytok < pc.it.tokens;
@@ -704,7 +733,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     const int j = j0 + row;
                     const bool none = j < pc.it.lo0 || j > pc.it.e1;  // seen by no row of the item
                     const bool some = !none && (j < pc.it.lo1 || j > pc.it.e0);
-                    const uint32_t en = 2 * (tile0 + t) + 1, sl = en % NS;
+                    const uint32_t en = 2 * tile0 + values_at<ONE>(t, pc.take), sl = en % NS;
                     ok = mbar_wait_warp(full + sl, (en / NS) & 1, abort_flag, &g_chunk_status);
                     if (!ok) break;
                     if (none || some) {
@@ -1019,7 +1048,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     if (p.after_small) pdl_wait();  // the call is done when both kernels are
 }
 
-template <typename Ty, int D>
+template <typename Ty, int D, bool ONE>
 static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnParams& p,
                           int ctas, cudaStream_t s, bool pdl) {
     static bool set_for[64];
@@ -1028,27 +1057,34 @@ static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CU
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!set_for[dev]) {
-        e = cudaFuncSetAttribute(paged_chunk_kernel<Ty, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ch<D>::kSmem);
+        e = cudaFuncSetAttribute(paged_chunk_kernel<Ty, D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ch<D, ONE>::kSmem);
         if (e != cudaSuccess) return e;
         set_for[dev] = true;
     }
-    return launch_kernel(paged_chunk_kernel<Ty, D>, dim3(ctas), dim3(kChThreads), (size_t)Ch<D>::kSmem, s, pdl, tq, tk,
+    return launch_kernel(paged_chunk_kernel<Ty, D, ONE>, dim3(ctas), dim3(kChThreads), (size_t)Ch<D, ONE>::kSmem, s, pdl, tq, tk,
                          tv, p);
 }
 
 size_t paged_chunk_part_bytes(int d, int sms) {
-    return (size_t)4 * sms * (d == 128 ? Ch<128>::kPartHalf : Ch<64>::kPartHalf) * sizeof(float);
+    return (size_t)4 * sms * (d == 128 ? Ch<128, false>::kPartHalf : Ch<64, false>::kPartHalf) * sizeof(float);
 }
 
-cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl) {
+template <typename Ty, int D>
+static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnParams& p,
+                          bool one, int ctas, cudaStream_t s, bool pdl) {
+    return one ? launch<Ty, D, true>(tq, tk, tv, p, ctas, s, pdl) : launch<Ty, D, false>(tq, tk, tv, p, ctas, s, pdl);
+}
+
+cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, bool one, int sms, cudaStream_t s, bool pdl) {
     CUtensorMap tq, tk, tv;
     const int box = (1 << p.shift) < kChKeys ? 1 << p.shift : kChKeys;
     if (!paged_tmap(&tk, p, bf16, d, false, box) || !paged_tmap(&tv, p, bf16, d, true, box) ||
         !query_tmap(&tq, p, bf16, d, 128 / p.G))
         return cudaErrorInvalidValue;
     if (bf16)
-        return d == 128 ? launch<Bf16, 128>(tq, tk, tv, p, sms, s, pdl) : launch<Bf16, 64>(tq, tk, tv, p, sms, s, pdl);
-    return d == 128 ? launch<F16, 128>(tq, tk, tv, p, sms, s, pdl) : launch<F16, 64>(tq, tk, tv, p, sms, s, pdl);
+        return d == 128 ? launch<Bf16, 128>(tq, tk, tv, p, one, sms, s, pdl)
+                        : launch<Bf16, 64>(tq, tk, tv, p, one, sms, s, pdl);
+    return d == 128 ? launch<F16, 128>(tq, tk, tv, p, one, sms, s, pdl) : launch<F16, 64>(tq, tk, tv, p, one, sms, s, pdl);
 }
 
 int chunk_read_status() {
