@@ -28,8 +28,8 @@
 //
 // Bound: HBM for many rows (every logit once; the passes after the first find
 // them in L2), launches and the chain of passes for few.  Measured, 151936
-// tokens a row: 256 f32 rows without filters 45.3 us, 6.9 TB/s; one bf16 row with
-// top-k and top-p 15.0 us (7 k clocks the first kernel, 20 k the second); 64 bf16
+// tokens a row: 256 f32 rows without filters 45.7 us, 6.8 TB/s; one bf16 row with
+// top-k and top-p 15.1 us (7 k clocks the first kernel, 20 k the second); 64 bf16
 // rows with filters of their own 26 us.  A row whose nucleus has 735 tokens takes
 // 28 us, one that step 4 has to count ~80.
 //
