@@ -530,3 +530,58 @@ def test_workspaces_of_streams_and_graphs(w):
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(souts[0], souts[1]) and torch.equal(louts[0], louts[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [9001, 60000])
+def test_sample_cuts_to_the_token(w, V, dtype):
+    """Random numbers by which the least of the kept tokens wins: the cut itself, for nuclei and k from a few to thousands."""
+    R = 24
+    r = np.random.default_rng(V)
+    x, _ = draw_rows(R, V, dtype, V + 3)
+    t = np.linspace(0.5, 1.6, R).astype(np.float32)
+    z = (x.float().cpu().numpy() / t[:, None]).astype(np.float32)
+    e = np.exp(1.5 * (z - z.max(1, keepdims=True)).astype(np.float64)).astype(np.float32)  # score: falls as z rises
+    p = r.uniform(0.5, 0.995, R).astype(np.float32)
+    k = np.unique(np.geomspace(2, min(V - 1, 6000), R).astype(int))
+    k = np.concatenate([k, np.full(R - len(k), 777)])
+    m = np.full(R, 1e-3, np.float32)
+    dev = lambda a, dt=torch.float32: torch.tensor(a, dtype=dt, device="cuda")  # noqa: E731
+    for ks, ps, ms in ((None, p, None), (k, None, None), (None, p, m), (k, p, None)):
+        tok = w.w4a16_sample(x, dev(e), dev(t), None if ks is None else dev(ks, torch.int32),
+                             None if ps is None else dev(ps), None if ms is None else dev(ms)).cpu().numpy()
+        for i in range(R):
+            order = np.lexsort((np.arange(V), -z[i].astype(np.float64)))
+            zs = z[i][order].astype(np.float64)
+            wt = np.exp(zs - zs[0])
+            n = V if ks is None else min(V, int(ks[i]))
+            ends = {n}
+            if ps is not None:
+                # a token is kept while the weight before it is below p of the total; sums in f32 and of up to
+                # 8192 weights rounded to 2^-31 of the total are off by less than 2^-17 of it
+                before, want = np.cumsum(wt[:n]) - wt[:n], float(ps[i]) * wt[:n].sum()
+                eps = 2.0 ** -17 * wt[:n].sum()
+                ends = set(range(max(1, int((before < want - eps).sum())), max(1, int((before < want + eps).sum())) + 1))
+            if ms is not None:
+                ends = {min(j, int((zs - zs[0] >= np.log(np.float64(ms[i])) - 2e-6).sum())) for j in ends} | \
+                       {min(j, int((zs - zs[0] >= np.log(np.float64(ms[i])) + 2e-6).sum())) for j in ends}
+            # of equal z the first kept one has the score of all
+            allowed = {int(order[:j][zs[:j] == zs[j - 1]][0]) for j in ends}
+            assert tok[i] in allowed, (i, float(t[i]), ks is not None and int(ks[i]), ps is not None and float(ps[i]),
+                                       int(tok[i]), sorted(allowed)[:5], min(ends), max(ends))
+
+
+def test_sample_cut_among_equals(w):
+    """Cuts that fall into thousands of equal logits, above and below other tokens."""
+    V, R = 30000, 6
+    x = torch.full((R, V), -4.0, device="cuda")
+    x[:, 100:9100] = 2.0           # 9000 equals: more than a list holds
+    x[1:, 100:4000] = 3.0          # 3900 of them above the rest
+    x[:, 20000:20040] = 6.0
+    x[5, :] = 0.0
+    e = torch.rand((R, V), generator=torch.Generator("cuda").manual_seed(1), device="cuda") + 0.5
+    for k in ([41] * R, [3000] * R, [3941] * R, [9041] * R, [1, 40, 2048, 2049, 8193, 12345]):
+        check_sample(w, x, e, k=np.array(k))
+    for p in ([0.3] * R, [0.8] * R, [0.05, 0.1, 0.2, 0.5, 0.9, 0.25]):
+        check_sample(w, x, e, p=np.array(p, np.float32))
+        check_sample(w, x, e, p=np.array(p, np.float32), k=np.array([5000] * R))
