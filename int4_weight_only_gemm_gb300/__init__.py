@@ -383,11 +383,12 @@ _WRITE_ARGS = struct.Struct("=5Q10qiiiiiiIi")
 _ATTN_ARGS = struct.Struct("=9QQ11qiiiiiiiiiiiifI")
 _SAMPLE_ARGS = struct.Struct("=9QQqqiiiI")
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_Tensor, _I32 = torch.Tensor, torch.int32  # (looked up some ten times a call)
 
 
 def _int32(t, name, n=None):
     """Address of a contiguous int32 CUDA tensor, of that many entries."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _I32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
     if n is not None and (t.numel() != n or t.dim() != 1):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
@@ -396,7 +397,7 @@ def _int32(t, name, n=None):
 
 def _block_table(t, requests):
     """Columns and row stride of a block table."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2:
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _I32 or t.dim() != 2:
         raise ValueError("block_table must be a 2-D int32 CUDA tensor")
     rows, columns = t.shape
     row, column = t.stride()
@@ -407,9 +408,9 @@ def _block_table(t, requests):
 
 def _strided(t, name, dtype, dims):
     """Shape and strides of a CUDA tensor of that many dimensions whose last one is contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     shape, stride = t.shape, t.stride()
     if len(stride) != dims or (stride[-1] != 1 and shape[-1] > 1):
@@ -566,7 +567,7 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
 def _rows_of(t, name, dtype, rows):
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
     if t.numel() != rows or t.dim() != 1:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows,)}")
