@@ -13,7 +13,7 @@
 // writes in this launch.  Bound: launch and a chain of two dependent loads.
 // Measured: 64 decoding requests 4.8 us, 2048 requests, an eighth of them with
 // up to 2048 new tokens (5.4 MB in and out), 8.2 us; called one by one from the
-// host 7.4 and 9.5 us.
+// host 7.2 and 9.5 us.
 #include "common.cuh"
 #include "kernels.h"
 
