@@ -427,16 +427,28 @@ _stream_workspaces: dict = {}
 _outgrown_workspaces: list = []
 
 
+def _stream_of(index: int, stream: int):
+    """The stream of a raw handle.  0 and 1 are the default stream, which ExternalStream cannot name: it takes 0 for
+    "none given" and hands out a stream of its pool, unordered with the default one."""
+    return torch.cuda.default_stream(index) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device=index)
+
+
+def _zeroed(nbytes: int, index: int, stream: int) -> torch.Tensor:
+    """A workspace made and its counters (all that has to be zero) zeroed on that stream."""
+    with torch.cuda.stream(_stream_of(index, stream)):
+        ws = torch.empty(max(nbytes, 65536), dtype=torch.uint8, device=f"cuda:{index}")
+        ws[:65536].zero_()
+    return ws
+
+
 def _stream_workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
     ws = _stream_workspaces.get((index, stream))
     if ws is not None and ws.numel() >= nbytes:
         return ws
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)):
+    with torch.cuda.stream(_stream_of(index, stream)):
         if torch.cuda.is_current_stream_capturing():  # the graph's own; every replay zeroes its counters
-            ws = torch.empty(max(nbytes, 65536), dtype=torch.uint8, device=f"cuda:{index}")
-            ws[:65536].zero_()
-            return ws
-        fresh = new_workspace(max(nbytes, 2 * ws.numel() if ws is not None else 0), f"cuda:{index}")
+            return _zeroed(nbytes, index, stream)
+    fresh = _zeroed(max(nbytes, 2 * ws.numel() if ws is not None else 0), index, stream)
     if ws is not None:
         _outgrown_workspaces.append(ws)
     _stream_workspaces[(index, stream)] = fresh

@@ -1,0 +1,64 @@
+"""The workspaces that the binding gives to serving calls without one: whose they are, and on which stream they are
+zeroed."""
+import pytest
+import torch
+
+import int4_weight_only_gemm_gb300 as w
+
+
+def i32(a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+@pytest.fixture
+def fresh(monkeypatch):
+    """No workspaces from calls before."""
+    monkeypatch.setattr(w, "_stream_workspaces", {})
+
+
+def attention_of(lens, heads, kv_heads, seed=0):
+    """A call without a workspace, by output: call(**more) -> out."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    page, d, columns = 16, 128, max(-(-(p + n) // 16) for p, n in lens)
+    pages = columns * len(lens)
+    q = torch.randn(sum(n for _, n in lens), heads, d, generator=g, device="cuda").to(torch.bfloat16)
+    kc, vc = torch.randn(2, pages, kv_heads, page, d, generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(len(lens), columns)
+    starts = [0]
+    for _, n in lens:
+        starts.append(starts[-1] + n)
+    args = (q, kc, vc, table, i32(starts), i32([p + n for p, n in lens]), max(n for _, n in lens))
+    need = w.w4a16_paged_attention_workspace_bytes(q.shape[0], len(lens), heads, kv_heads, d, args[-1])
+    return (lambda **more: w.w4a16_paged_attention(*args, **more)), need
+
+
+# ---------------------------------------------------------------------------
+# the default stream
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_stream_has_no_external_stream(monkeypatch, handle):
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda index: ("default", index))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: ("external", h, device))
+    assert w._stream_of(0, handle) == ("default", 0)
+    assert w._stream_of(0, 0x7f00) == ("external", 0x7f00, 0)
+
+
+@pytest.mark.gpu
+def test_first_and_growing_call_zero_on_the_default_stream(fresh, monkeypatch):
+    small, _ = attention_of([(2000, 1), (50, 1)], 8, 2)
+    large, need = attention_of([(2500, 1)] * 4 + [(700, 200)], 16, 4, seed=1)
+    ws = w.new_workspace(need)
+    want = small(workspace=ws), large(workspace=ws)
+    torch.cuda.synchronize()
+    entered, real = [], torch.cuda.stream
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: (entered.append(s.cuda_stream), real(s))[1])
+    with real(torch.cuda.default_stream()):
+        a = torch.randn(4096, 4096, device="cuda")
+        for _ in range(8):  # long work ahead of the calls
+            a = a @ a * 1e-3
+        got = [small(), large(), small(), large()]
+    torch.cuda.synchronize()
+    assert entered and set(entered) == {0}
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 2])
