@@ -535,6 +535,10 @@ int w4a16_sample(const w4a16_sample_args *args, w4a16_stream_t stream);
 /* Workspace of a call with these sizes on the current device; filters: whether top_k, top_p or min_p is given. */
 size_t w4a16_sample_workspace_bytes(int rows, int vocab, int filters);
 
+/* Number of the capture that the stream is in, 0 where it is in none.  A graph replayed beside other calls must not
+ * share a workspace with them: this tells a caller that keeps workspaces when to give one of the capture's own. */
+uint64_t w4a16_stream_capture_id(w4a16_stream_t stream);
+
 /* Number of kernel launches the library has issued in this process (every
  * entry point that launches counts its kernel; w4a16_gemm_noalloc's counter
  * memset is not a kernel launch). */

@@ -91,6 +91,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.w4a16_paged_attention_workspace_bytes.restype = sz
             lib.w4a16_sample_workspace_bytes.argtypes = [ci, ci, ci]
             lib.w4a16_sample_workspace_bytes.restype = sz
+            lib.w4a16_stream_capture_id.argtypes = [vp]
+            lib.w4a16_stream_capture_id.restype = ctypes.c_uint64
             _lib = lib
     return _lib
 
@@ -419,11 +421,12 @@ def _strided(t, name, dtype, dims):
 
 
 # Workspaces of the calls that bring none: one a stream, so that calls on two
-# streams never share counters or partial results, zeroed on that stream.  A
-# buffer that became too small stays alive: a captured graph may hold it.  (A
-# call captured on a stream that has none yet adds the zeroing of its counters
-# to the graph; give such calls a workspace.)
-_stream_workspaces: dict = {}
+# streams never share counters or partial results.  A capture never takes an
+# eager call's buffer, since its graph may be replayed beside that stream's
+# calls: it has one of its own for each of its streams, out of the graph's
+# memory, with the zeroing of its counters as a node of the graph.
+_stream_workspaces: dict = {}   # (device, stream): buffer
+_capture_workspaces: dict = {}  # (device, stream): (capture, buffer), kept for the capture's next call
 _outgrown_workspaces: list = []
 
 
@@ -441,18 +444,33 @@ def _zeroed(nbytes: int, index: int, stream: int) -> torch.Tensor:
     return ws
 
 
-def _stream_workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
-    ws = _stream_workspaces.get((index, stream))
+def _serving_workspace(nbytes: int, index: int, stream, handle: int) -> torch.Tensor:
+    """The workspace of a call that brings none; `stream` as the caller gave it, `handle` what it stands for."""
+    if stream is None:
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        capturing = load_library().w4a16_stream_capture_id(handle) != 0
+    if capturing:
+        return _capture_workspace(nbytes, index, handle)
+    if _capture_workspaces:
+        _capture_workspaces.clear()  # (their captures are over, or take new ones)
+    ws = _stream_workspaces.get((index, handle))
     if ws is not None and ws.numel() >= nbytes:
         return ws
-    with torch.cuda.stream(_stream_of(index, stream)):
-        if torch.cuda.is_current_stream_capturing():  # the graph's own; every replay zeroes its counters
-            return _zeroed(nbytes, index, stream)
-    fresh = _zeroed(max(nbytes, 2 * ws.numel() if ws is not None else 0), index, stream)
+    fresh = _zeroed(max(nbytes, 2 * ws.numel() if ws is not None else 0), index, handle)
     if ws is not None:
         _outgrown_workspaces.append(ws)
-    _stream_workspaces[(index, stream)] = fresh
+    _stream_workspaces[(index, handle)] = fresh
     return fresh
+
+
+def _capture_workspace(nbytes: int, index: int, handle: int) -> torch.Tensor:
+    capture = load_library().w4a16_stream_capture_id(handle)
+    held, ws = _capture_workspaces.get((index, handle), (0, None))
+    if held != capture or ws.numel() < nbytes:
+        ws = _zeroed(max(nbytes, 2 * ws.numel() if held == capture else 0), index, handle)
+        _capture_workspaces[(index, handle)] = capture, ws
+    return ws
 
 
 def w4a16_page_plan(past_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
@@ -565,7 +583,7 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
             need = int(lib.w4a16_paged_attention_workspace_bytes(T, B, Hq, Hkv, d, max_q))
             _need_cache[key] = need
         if need:
-            workspace = _stream_workspace(need, idx, st)
+            workspace = _serving_workspace(need, idx, stream, st)
     args = _ATTN_ARGS.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), start, kv,
                            out.data_ptr(), 0 if lse is None else lse.data_ptr(),
                            0 if workspace is None else workspace.data_ptr(),
@@ -622,7 +640,7 @@ def w4a16_sample(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.T
             need = int(lib.w4a16_sample_workspace_bytes(R, V, int(filters)))
             _need_cache[key] = need
         if need:
-            workspace = _stream_workspace(need, idx, st)
+            workspace = _serving_workspace(need, idx, stream, st)
     args = _SAMPLE_ARGS.pack(logits.data_ptr(), noise.data_ptr(), _rows_of(temperature, "temperature", f32, R),
                              _rows_of(top_k, "top_k", torch.int32, R), _rows_of(top_p, "top_p", f32, R),
                              _rows_of(min_p, "min_p", f32, R), _rows_of(token, "token", torch.int32, R),

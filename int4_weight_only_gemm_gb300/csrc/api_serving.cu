@@ -208,4 +208,14 @@ int w4a16_sample(const w4a16_sample_args* a, w4a16_stream_t stream) {
     return status_of(launch_sample(*a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+uint64_t w4a16_stream_capture_id(w4a16_stream_t stream) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+        (void)cudaGetLastError();  // (the default stream while another one captures)
+        return 0;
+    }
+    return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 }  // extern "C"

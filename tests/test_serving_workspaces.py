@@ -62,3 +62,92 @@ def test_first_and_growing_call_zero_on_the_default_stream(fresh, monkeypatch):
     assert entered and set(entered) == {0}
     for i, x in enumerate(got):
         assert torch.equal(x, want[i % 2])
+
+
+# ---------------------------------------------------------------------------
+# captures
+# ---------------------------------------------------------------------------
+
+class FakeLibrary:
+    """What the binding asks of the library to find a call's workspace."""
+    capture = 0
+
+    def w4a16_stream_capture_id(self, stream):
+        return self.capture
+
+
+@pytest.fixture
+def fake(monkeypatch, fresh):
+    lib = FakeLibrary()
+    monkeypatch.setattr(w, "_capture_workspaces", {})
+    monkeypatch.setattr(w, "load_library", lambda: lib)
+    monkeypatch.setattr(w, "_zeroed", lambda nbytes, index, handle: torch.zeros(max(nbytes, 65536), dtype=torch.uint8))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: lib.capture != 0)
+    return lib
+
+
+@pytest.mark.parametrize("stream", [None, "given"])
+def test_a_capture_takes_no_eager_buffer(fake, stream):
+    get = lambda n=100, handle=0x70: w._serving_workspace(n, 0, stream, handle)  # noqa: E731
+    eager = get()
+    assert get() is eager and get(handle=0x80) is not eager
+    fake.capture = 5
+    first = get()
+    assert first is not eager and get() is first and get(handle=0x80) is not first
+    assert get(100000).numel() >= 100000
+    fake.capture = 6
+    second = get()
+    assert second is not first and second is not eager
+    fake.capture = 0
+    assert get() is eager
+
+
+@pytest.mark.gpu
+def test_graph_of_a_warmed_stream_beside_its_calls(fresh):
+    """A graph captured on a stream with a workspace, replayed on another while the first one runs calls of its own."""
+    small, _ = attention_of([(2000, 1), (50, 1), (700, 30)], 8, 2)
+    want = small()
+    torch.cuda.synchronize()
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    out = torch.zeros_like(want)
+    with torch.cuda.stream(s):
+        small()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        small(out=out)
+        small(out=out)
+        assert len(w._capture_workspaces) == 1
+    eager = w._stream_workspaces[(0, s.cuda_stream)]
+    eager[:65536].fill_(1)  # nothing of the graph reads it
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert (eager[:65536] == 1).all()
+    eager[:65536].zero_()
+    torch.cuda.synchronize()
+    for _ in range(50):
+        with torch.cuda.stream(other):
+            graph.replay()
+        got = small(stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(out, want)
+
+
+@pytest.mark.gpu
+def test_capture_id():
+    s = torch.cuda.Stream()
+    lib = w.load_library()
+    assert lib.w4a16_stream_capture_id(s.cuda_stream) == 0 == lib.w4a16_stream_capture_id(0)
+    ids = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            ids.append(lib.w4a16_stream_capture_id(s.cuda_stream))
+            torch.zeros(4, device="cuda")
+    assert 0 not in ids and ids[0] != ids[1]
+    assert lib.w4a16_stream_capture_id(s.cuda_stream) == 0
