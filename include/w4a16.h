@@ -252,6 +252,9 @@ const char *w4a16_status_str(int status);
  * of the current device: W4A16_OK, or W4A16_ETIMEOUT when a kernel's bounded
  * wait on a barrier gave up (its output is then undefined, the context stays
  * usable).  W4A16_ECUDA if the synchronization itself failed.
+ * A kernel that gave up may leave arrival counters of its workspace above
+ * zero: after W4A16_ETIMEOUT the first 64 KB of every workspace used since the
+ * status was last read have to be zeroed before their next use.
  */
 int w4a16_last_device_status(w4a16_stream_t stream);
 
@@ -455,8 +458,9 @@ int w4a16_kv_write(const w4a16_kv_write_args *args, w4a16_stream_t stream);
  *   kv_len[b]   counted as at most columns * page_size
  *   workspace   w4a16_paged_attention_workspace_bytes bytes, 16-byte aligned,
  *               zero-filled once before its first use (its first 64 KB hold
- *               arrival counters that every call leaves at zero: the GEMM's
- *               workspace rules apply, and one buffer serves both)
+ *               arrival counters that every call leaves at zero, unless it
+ *               ends in W4A16_ETIMEOUT: the GEMM's workspace rules apply, and
+ *               one buffer serves both)
  * out and lse must not overlap the inputs.
  */
 typedef struct {

@@ -332,7 +332,10 @@ def w4a16_auto_path(M: int, N: int, K: int, group: int = 128) -> int:
 
 
 def w4a16_last_device_status(stream=None) -> int:
-    return int(load_library().w4a16_last_device_status(_stream(stream)))
+    status = int(load_library().w4a16_last_device_status(_stream(stream)))
+    if status == W4A16_ETIMEOUT:  # a kernel that gave up may have left its workspace's counters above zero
+        _stream_workspaces.clear()
+    return status
 
 
 def w4a16_launch_count() -> int:

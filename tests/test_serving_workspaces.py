@@ -1,5 +1,7 @@
 """The workspaces that the binding gives to serving calls without one: whose they are, and on which stream they are
 zeroed."""
+import ctypes
+
 import pytest
 import torch
 
@@ -151,3 +153,31 @@ def test_capture_id():
             torch.zeros(4, device="cuda")
     assert 0 not in ids and ids[0] != ids[1]
     assert lib.w4a16_stream_capture_id(s.cuda_stream) == 0
+
+
+# ---------------------------------------------------------------------------
+# after a timeout
+# ---------------------------------------------------------------------------
+
+def test_buffers_go_after_a_timeout(fake):
+    fake.w4a16_last_device_status = lambda stream: fake.status
+    get = lambda: w._serving_workspace(100, 0, None, 0x70)  # noqa: E731
+    first = get()
+    for status, kept in ((w.W4A16_OK, True), (w.W4A16_ECUDA, True), (w.W4A16_ETIMEOUT, False)):
+        fake.status = status
+        assert w.w4a16_last_device_status(0) == status
+        assert (get() is first) == kept
+
+
+@pytest.mark.gpu
+def test_attention_after_a_timeout(fresh):
+    """The wait that runs out is the self-test's; the buffer's counters stand for what a kernel that gave up leaves."""
+    small, _ = attention_of([(2000, 1), (50, 1), (700, 30)], 8, 2)
+    want = small().clone()
+    torch.cuda.synchronize()
+    (spoilt,) = w._stream_workspaces.values()
+    spoilt[:65536].fill_(1)
+    assert w.load_library().w4a16_selftest_wait_timeout(ctypes.c_longlong(20_000_000), None) == 0  # 20 ms
+    assert w.w4a16_last_device_status() == w.W4A16_ETIMEOUT
+    assert torch.equal(small(), want)
+    assert w.w4a16_last_device_status() == w.W4A16_OK
