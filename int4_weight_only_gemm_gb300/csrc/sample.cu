@@ -12,8 +12,8 @@
 //      kept is cut down to candidates without knowing the order -- top-k and
 //      top-p by the maxima of the first pass's threads, S x 512 tokens of the
 //      row: with k of them, or p of the row's weight, at and above a bound, so
-//      many of the row's tokens are; min-p by its own bound -- and collected in
-//      a list of the row;
+//      many of the row's tokens are (the bound lowered by what one quotient
+//      spans); min-p by its own bound -- and collected in a list of the row;
 //   3. the row's last CTA settles the cuts and the race among up to kWide
 //      candidates: a few it sorts; of more it finds the cut's place in bins of
 //      their counts or weights and sorts what lies in that bin alone, tokens
@@ -767,7 +767,10 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
 #pragma unroll
             for (int i = 0; i < kMaxSplits; ++i)
                 if (top[i] > -INFINITY && bin_of(top[i]) <= cut) tau = fminf(tau, top[i]);
+            // The order is that of the quotients: tokens whose z equals tau's may lie below tau by what one z spans,
+            // 2^-23 of |l| at most (2^-149 T where z is subnormal).
             tau = cta_min<NT>(tau, rf);
+            tau -= fabsf(tau) * 0x1p-21f + T * 0x1p-148f;
             if (q.by_k || tau > low) {
                 low = tau;
                 all = q.by_k || turn == 0;
@@ -963,7 +966,9 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
         }
         __syncthreads();
         int b1 = win[0], b2 = win[1];
-        slow = (q.by_k && bk >= kBins - 1) || (q.by_p && (q.by_k ? b1 : b2) >= kBins - 1);
+        // (a k-th token at the end of a range that the maxima do not bound: its equals may lie below it)
+        const int end = q.by_k && low == wide ? min(bin_of(low), kBins) - 1 : kBins - 1;
+        slow = (q.by_k && bk >= end) || (q.by_p && (q.by_k ? b1 : b2) >= kBins - 1);
         // equal z may have unequal l, one bin apart at most: a bin more on each side
         if (q.by_k && b2 > bk) b2 = bk;
         if (!q.by_p) b1 = b2 = bk;

@@ -1,0 +1,102 @@
+"""Serving operators where their definitions are exact and floats are not: equal quotients of unequal logits, filters
+wider than a masked row, lengths and windows near the ends of int32, long contexts with a NaN."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w():
+    import int4_weight_only_gemm_gb300 as w
+    return w
+
+
+def dev(a, dtype=torch.float32):
+    return None if a is None else torch.tensor(np.asarray(a), dtype=dtype, device="cuda")
+
+
+def draws(w, x, e, t=None, k=None, p=None, m=None):
+    """Tokens of the kernel and of the oracle; logits x and random numbers e are f32 arrays [R, V]."""
+    logprob = torch.empty(len(x), device="cuda")
+    token = w.w4a16_sample(dev(x), dev(e), dev(t), dev(k, torch.int32), dev(p), dev(m), logprob=logprob)
+    of = lambda a, i: None if a is None else a[i]  # noqa: E731
+    want = [serving.sample(x[i], e[i], of(t, i), of(k, i), of(p, i), of(m, i)) for i in range(len(x))]
+    for got, (_, ref) in zip(logprob.tolist(), want):
+        assert abs(got - ref) <= 2e-5 + 2e-6 * abs(ref)
+    return token.tolist(), [a for a, _ in want]
+
+
+# ---------------------------------------------------------------------------
+# sampling: equal quotients of unequal logits
+# ---------------------------------------------------------------------------
+
+def step(x, n):
+    """The f32 number n steps from x."""
+    for _ in range(abs(n)):
+        x = np.nextafter(np.float32(x), np.float32(np.inf if n > 0 else -np.inf))
+    return np.float32(x)
+
+
+def test_the_largest_quotient_at_the_lower_index(w):
+    """l / 1.5 rounds two neighbouring logits to one quotient: of equal ones the lower index is first, whichever logit
+    it has."""
+    V, T = 40000, np.float32(1.5)
+    tops = [a for a in (step(15.0, i) for i in range(64)) if np.float32(a) / T == np.float32(step(a, -1)) / T][:8]
+    assert len(tops) == 8
+    x = np.full((8, V), -4.0, np.float32)
+    for i, a in enumerate(tops):
+        x[i, 30000 + 3 * i] = a
+        x[i, 11 + 997 * i] = step(a, -1)
+    e = np.ones((8, V), np.float32)
+    t = np.full(8, T, np.float32)
+    first = [11 + 997 * i for i in range(8)]
+    for more in (dict(k=np.ones(8, int)), dict(p=np.full(8, 1e-3, np.float32)), dict(k=np.ones(8, int), p=np.full(8, 0.5, np.float32))):
+        got, want = draws(w, x, e, t, **more)
+        assert want == first and got == want
+
+
+@pytest.mark.parametrize("k", [5, 9, 13])
+def test_pairs_of_one_load_with_one_quotient(w, k):
+    """Pairs of neighbouring logits, one quotient for all: the first k of the row stay, not the larger of each pair."""
+    V, T = 40000, np.float32(1.9)
+    hi = np.float32(1.9500003)
+    lo = step(hi, -1)
+    assert lo / T == hi / T
+    x = np.full((1, V), -4.0, np.float32)
+    order = []
+    for j in range(1, 11):
+        x[0, 400 * j], x[0, 400 * j + 1] = lo, hi
+        order += [400 * j, 400 * j + 1]
+    for last in range(k):  # the one with the smallest random number is drawn if it is kept
+        e = np.ones((1, V), np.float32)
+        e[0, order[last]] = 1e-4
+        got, want = draws(w, x, e, np.array([T]), k=np.array([k]))
+        assert want == [order[last]] and got == want
+    mass = np.exp(-4 / 1.9 - 1.9500003 / 1.9) * (V - 20) + 20
+    p = np.array([(k - 0.5) / mass], np.float32)
+    for last in range(k):
+        e = np.ones((1, V), np.float32)
+        e[0, order[last]] = 1e-4
+        got, want = draws(w, x, e, np.array([T]), p=p)
+        assert want == [order[last]] and got == want
+
+
+def test_top_k_ends_where_counting_ends(w):
+    """The k-th token forty units of z below the first, where the kernel stops counting tokens of a large k."""
+    V, T, k, R = 40000, np.float32(1.9), 1500, 25
+    x = np.full((R, V), -1000.0, np.float32)
+    x[:, 1000:1000 + k - 1] = 10.0
+    e = np.ones((R, V), np.float32)
+    e[:, [3, 50]] = 1e-30
+    equal = 0
+    for i in range(R):
+        x[i, 50] = step(np.float32(10.0) - np.float32(40.0) * T * np.float32(1.0001), i - R // 2)
+        x[i, 3] = step(x[i, 50], -1)
+        equal += x[i, 50] / T == x[i, 3] / T
+    assert equal >= 5
+    got, want = draws(w, x, e, np.full(R, T), k=np.full(R, k))
+    assert got == want and want.count(3) == equal
