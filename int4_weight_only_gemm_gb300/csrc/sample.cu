@@ -1069,7 +1069,8 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
             ties = k - count(cut + 1);
         }
         if (q.by_p) {
-            const float wcut = weight(value_of(cut));
+            const bool by_k = q.by_k && cut > 0;  // (0: top-k takes all there are, and no token has that key)
+            const float wcut = by_k ? weight(value_of(cut)) : 0.f;
             const uint32_t top = cut;
             const int top_ties = ties;
             auto mass = [&](uint32_t c) {  // weight of the kept tokens with a key >= c
@@ -1079,7 +1080,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
                     const uint32_t y = key_of(z);
                     if (y >= c && y > top) s += weight(z);
                 });
-                return cta_sum<NT>(s, rf) + (q.by_k && c <= top ? (float)top_ties * wcut : 0.f);
+                return cta_sum<NT>(s, rf) + (by_k && c <= top ? (float)top_ties * wcut : 0.f);
             };
             const float want = q.tp * mass(top);
             uint32_t lo = top, hi = key_of(zmax);
@@ -1088,7 +1089,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const w4a1
                 if (mass(mid) >= want) lo = mid; else hi = mid - 1;
             }
             const float over = mass(lo + 1), wt = weight(value_of(lo));
-            const int here = q.by_k && lo == top ? top_ties : count(lo) - count(lo + 1);
+            const int here = by_k && lo == top ? top_ties : count(lo) - count(lo + 1);
             cut = lo;
             ties = 1;
             if (wt > 0.f && over + wt < want) {  // tie i stays while over + i wt < want

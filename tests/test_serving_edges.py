@@ -100,3 +100,26 @@ def test_top_k_ends_where_counting_ends(w):
     assert equal >= 5
     got, want = draws(w, x, e, np.full(R, T), k=np.full(R, k))
     assert got == want and want.count(3) == equal
+
+
+# ---------------------------------------------------------------------------
+# sampling: rows of which a mask leaves less than top-k
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("V", [1500, 3001, 40000, 151936])
+def test_top_p_of_a_row_with_fewer_tokens_than_top_k(w, V):
+    """Five tokens are left by a mask, top-k takes fifty (or 3000), top-p cuts among the five."""
+    R = 6
+    x = np.full((R, V), -np.inf, np.float32)
+    at = np.array([7, 100, 101, V // 2, V - 1])
+    x[:, at] = np.array([1.0, 3.0, 2.0, 2.5, -4.0])  # .064, .474, .174, .287 and .0004 of the probability
+    e = np.ones((R, V), np.float32)
+    for i in range(5):
+        e[i, at[i]] = 1e-6   # drawn if it is kept
+    p = np.array([0.3, 0.6, 0.6, 0.9, 0.9, 0.99], np.float32)
+    for k in (50, 3000):
+        for more in ({}, dict(m=np.full(R, 1e-6, np.float32))):
+            got, want = draws(w, x, e, k=np.full(R, k), p=p, **more)
+            assert got == want
+            got, want = draws(w, x, e, k=np.full(R, k), p=p[::-1].copy(), **more)
+            assert got == want
