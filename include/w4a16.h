@@ -385,8 +385,10 @@ typedef enum { W4A16_BF16 = 0, W4A16_F16 = 1, W4A16_F32 = 2 } w4a16_dtype;
  *     pages_used[0] = first_requests (the free pages taken; more than num_free if they did not suffice)
  *
  * A negative length counts as 0; positions past the table's last column have
- * no page.  requests <= 16384 (W4A16_EUNSUPPORTED); all arrays int32, 4-byte
- * aligned, none overlapping another.  One launch.
+ * no page, and a page whose slots are numbered past 2^31 - 1 gives slot -1.
+ * New tokens past position 2^31 - 2 do not count; q_start and pages_used stop
+ * at 2^31 - 1.  requests <= 16384 (W4A16_EUNSUPPORTED); all arrays int32,
+ * 4-byte aligned, none overlapping another.  One launch.
  */
 typedef struct {
     const int32_t *past_len;   /* [requests] tokens in the cache */

@@ -23,7 +23,21 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanRun = 4;  // tokens a lane takes per warp pass, 32 apart
 
-// exclusive sums of two ints over the CTA's threads, and their totals
+// Lengths come from memory, so no sum of them may wrap into an index: sums of
+// numbers >= 0 stop at INT_MAX (in any order of addition), which is past every
+// token and free page.
+W4A16_DEVICE int add_up(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+// a request's tokens in the cache and new ones: >= 0, together INT_MAX at most
+struct PlanLengths {
+    int past, n;
+    W4A16_DEVICE PlanLengths(const w4a16_page_plan_args& p, int b) {
+        past = max(p.past_len[b], 0);
+        n = min(max(p.new_len[b], 0), 0x7fffffff - past);
+    }
+};
+W4A16_DEVICE int pages_of(int tokens, int shift) { return (tokens >> shift) + ((tokens & ((1 << shift) - 1)) != 0); }
+
+// exclusive sums of two ints >= 0 over the CTA's threads
 W4A16_DEVICE void plan_scan(int a, int f, int* sa, int* sf, int& ea, int& ef) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int ia = a, jf = f;
@@ -31,8 +45,8 @@ W4A16_DEVICE void plan_scan(int a, int f, int* sa, int* sf, int& ea, int& ef) {
     for (int d = 1; d < 32; d <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, ia, d), y = __shfl_up_sync(0xffffffffu, jf, d);
         if (lane >= d) {
-            ia += x;
-            jf += y;
+            ia = add_up(ia, x);
+            jf = add_up(jf, y);
         }
     }
     if (lane == 31) {
@@ -40,13 +54,13 @@ W4A16_DEVICE void plan_scan(int a, int f, int* sa, int* sf, int& ea, int& ef) {
         sf[warp] = jf;
     }
     __syncthreads();
-    int ba = 0, bf = 0;
+    const int xa = __shfl_up_sync(0xffffffffu, ia, 1), xf = __shfl_up_sync(0xffffffffu, jf, 1);
+    ea = lane ? xa : 0;
+    ef = lane ? xf : 0;
     for (int w = 0; w < warp; ++w) {
-        ba += sa[w];
-        bf += sf[w];
+        ea = add_up(ea, sa[w]);
+        ef = add_up(ef, sf[w]);
     }
-    ea = ba + ia - a;
-    ef = bf + jf - f;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const w4a16_page_plan_args p, const int shift) {
@@ -65,16 +79,16 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const w4a16_pag
     // the two sums: thread i takes the requests [i * per, i * per + per)
     const int per = (B + kPlanThreads - 1) / kPlanThreads;
     for (int b = threadIdx.x; b < B; b += kPlanThreads) {
-        const int past = max(p.past_len[b], 0), n = max(p.new_len[b], 0);
-        qs[b] = n;
-        fs[b] = ((past + n + page - 1) >> shift) - ((past + page - 1) >> shift);
+        const PlanLengths l(p, b);
+        qs[b] = l.n;
+        fs[b] = pages_of(l.past + l.n, shift) - pages_of(l.past, shift);
     }
     __syncthreads();
     int a = 0, f = 0;
     const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
     for (int b = b0; b < b1; ++b) {
-        a += qs[b];
-        f += fs[b];
+        a = add_up(a, qs[b]);
+        f = add_up(f, fs[b]);
     }
     int ea, ef;
     plan_scan(a, f, sa, sf, ea, ef);
@@ -82,8 +96,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const w4a16_pag
         const int n = qs[b], m = fs[b];
         qs[b] = ea;
         fs[b] = ef;
-        ea += n;
-        ef += m;
+        ea = add_up(ea, n);
+        ef = add_up(ef, m);
     }
     if (threadIdx.x == kPlanThreads - 1) {
         qs[B] = ea;
@@ -95,15 +109,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const w4a16_pag
     // per request: lengths, and the entries past the pages held (a warp a row)
     const int gw = blockIdx.x * kPlanWarps + warp, nw = gridDim.x * kPlanWarps;
     for (int b = gw; b < B; b += nw) {
-        const int past = max(p.past_len[b], 0), n = qs[b + 1] - qs[b];
-        const int held = (past + page - 1) >> shift, need = (past + n + page - 1) >> shift;
+        const PlanLengths l(p, b);
+        const int held = pages_of(l.past, shift), need = pages_of(l.past + l.n, shift);
         if (lane == 0) {
             p.q_start[b] = qs[b];
-            p.kv_len[b] = past + n;
+            p.kv_len[b] = l.past + l.n;
         }
         int* row = p.block_table + (int64_t)b * p.table_stride;
-        for (int c = held + lane; c < p.columns; c += 32) {
-            const int at = fs[b] + c - held;
+        for (int64_t c = held + lane; c < p.columns; c += 32) {
+            const int64_t at = fs[b] + c - held;
             row[c] = c < need && at < p.num_free ? p.free_pages[at] : -1;
         }
     }
@@ -125,19 +139,20 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const w4a16_pag
                     const int mid = (lo + hi) >> 1;
                     if (qs[mid] <= (int)t) lo = mid; else hi = mid;
                 }
-                const int past = max(p.past_len[lo], 0);
-                pos = past + ((int)t - qs[lo]);
-                const int held = (past + page - 1) >> shift, c = pos >> shift;
+                const PlanLengths l(p, lo);
+                const int held = pages_of(l.past, shift);
+                pos = l.past + ((int)t - qs[lo]);  // (t is below the next request's first token: pos < past + n)
+                const int c = pos >> shift;
                 int entry = -1;
                 if (c < p.columns) {
                     if (c < held) {
                         entry = p.block_table[(int64_t)lo * p.table_stride + c];
                     } else {
-                        const int at = fs[lo] + c - held;
+                        const int64_t at = (int64_t)fs[lo] + c - held;
                         if (at < p.num_free) entry = p.free_pages[at];
                     }
                 }
-                if (entry >= 0) slot = (entry << shift) + (pos & (page - 1));
+                if (entry >= 0 && entry <= (0x7fffffff >> shift)) slot = (entry << shift) + (pos & (page - 1));
             }
             p.positions[t] = pos;
             p.slot_map[t] = slot;

@@ -123,3 +123,57 @@ def test_top_p_of_a_row_with_fewer_tokens_than_top_k(w, V):
             assert got == want
             got, want = draws(w, x, e, k=np.full(R, k), p=p[::-1].copy(), **more)
             assert got == want
+
+
+# ---------------------------------------------------------------------------
+# plan: lengths and pages near the ends of int32
+# ---------------------------------------------------------------------------
+
+MOST = 2 ** 31 - 1
+
+
+def plan(w, past, new, free, table, page, tokens):
+    """-> table, q_start, kv_len, positions, slots, used as lists."""
+    t = dev(table, torch.int32)
+    out = w.w4a16_page_plan(dev(past, torch.int32), dev(new, torch.int32), dev(free, torch.int32), t, page,
+                            max_tokens=tokens)
+    return [t.tolist()] + [x.tolist() for x in out]
+
+
+def test_plan_with_a_cache_as_long_as_int32(w):
+    table, q_start, kv_len, positions, slots, used = plan(
+        w, [MOST, 5, MOST - 4], [1, 3, 100], [40, 41], [[1, 2], [3, 4], [5, 6]], 16, 9)
+    assert table == [[1, 2], [3, -1], [5, 6]]
+    assert q_start == [0, 0, 3, 7] and kv_len == [MOST, 8, MOST]
+    assert positions == [5, 6, 7] + [MOST - 4 + i for i in range(4)] + [-1, -1]
+    assert slots == [53, 54, 55] + [-1] * 6 and used == [0]
+
+
+@pytest.mark.parametrize("page", [8, 16, 256])
+def test_plan_with_more_new_tokens_than_int32_holds(w, page):
+    T, pages = 2 * page + 3, 2 ** 31 // page
+    table, q_start, kv_len, positions, slots, used = plan(
+        w, [0, 0, 3], [MOST, MOST, 7], [40, 41, 42, 43], [[1, 2, 3]] * 3, page, T)
+    assert table == [[40, 41, 42], [-1] * 3, [1, -1, -1]]
+    assert q_start == [0, MOST, MOST, MOST] and kv_len == [MOST, MOST, 10]
+    assert positions == list(range(T))
+    assert slots == [(40 + i // page) * page + i % page for i in range(T)]
+    assert used == [2 * pages + (10 > page)]
+
+
+def test_plan_whose_pages_sum_past_int32(w):
+    B = 16384
+    past = np.zeros(B, int)
+    new = np.full(B, MOST)
+    new[-1] = 0
+    table, q_start, kv_len, positions, slots, used = plan(w, past, new, [7], np.zeros((B, 1), int), 8, 20)
+    assert table == [[7]] + [[-1]] * (B - 1) and q_start == [0] + [MOST] * B and used == [MOST]
+    assert kv_len == new.tolist() and positions == list(range(20)) and slots == list(range(56, 64)) + [-1] * 12
+
+
+def test_plan_page_past_the_last_slot(w):
+    """A page number whose slots do not fit int32 gives no slot, and none of another page."""
+    last = 2 ** 31 // 16 - 1
+    table, _, _, _, slots, _ = plan(w, [3, 3, 16], [1, 1, 1], [last + 1], [[last, 0], [2 ** 28, 0], [9, 0]], 16, 3)
+    assert slots == [last * 16 + 3, -1, -1]
+    assert table[2] == [9, last + 1]
