@@ -109,7 +109,7 @@ W4A16_DEVICE int last_seen(const PagedAttnParams& p, const Request& r, int i) {
     return p.block ? r.L - 1 : r.L - r.n + i;
 }
 W4A16_DEVICE int first_seen(const PagedAttnParams& p, int e) {
-    return p.window > 0 && e - p.window + 1 > 0 ? e - p.window + 1 : 0;
+    return p.window > 0 && e >= p.window ? e - p.window + 1 : 0;  // (e may be negative, the window as large as it gets)
 }
 
 // One query row from the definition, by one warp: every lane holds D / 32

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import serving
+from test_serving import Attn
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +178,19 @@ def test_plan_page_past_the_last_slot(w):
     table, _, _, _, slots, _ = plan(w, [3, 3, 16], [1, 1, 1], [last + 1], [[last, 0], [2 ** 28, 0], [9, 0]], 16, 3)
     assert slots == [last * 16 + 3, -1, -1]
     assert table[2] == [9, last + 1]
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+@pytest.mark.parametrize("new,L", [(4, 2), (4, 4), (20, 6), (150, 70)])
+def test_window_as_large_as_it_gets(w, window, new, L):
+    """No window in effect, also where the first tokens come before the cache's first position."""
+    a = Attn([(0, new), (40, new)], 8, 2, 128, 16, "bf16", seed=12)
+    a.L[0] = L
+    out, lse = a.run(w, window)
+    a.check(out, lse)
+    free, _ = a.run(w, 0)
+    assert torch.equal(out, free)
