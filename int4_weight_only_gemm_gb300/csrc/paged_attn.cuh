@@ -1,5 +1,5 @@
-// Shared pieces of the paged-attention kernels: their parameters, the 16-bit
-// types, and one query row computed from the definition.
+// Shared pieces of the paged-attention kernels: their parameters and the 16-bit
+// types.
 #pragma once
 
 #include <cuda.h>
@@ -110,59 +110,6 @@ W4A16_DEVICE int last_seen(const PagedAttnParams& p, const Request& r, int i) {
 }
 W4A16_DEVICE int first_seen(const PagedAttnParams& p, int e) {
     return p.window > 0 && e >= p.window ? e - p.window + 1 : 0;  // (e may be negative, the window as large as it gets)
-}
-
-// One query row from the definition, by one warp: every lane holds D / 32
-// elements, one key after the other, with the running maximum and sum of the
-// softmax.  Reads only the positions that the row sees.
-template <typename Ty, int D>
-W4A16_DEVICE void attn_row(const PagedAttnParams& p, int b, const Request& r, int i, int h) {
-    constexpr int E = D / 64;  // 32-bit words a lane
-    const int lane = threadIdx.x & 31;
-    const int hk = h / p.G, t = r.t0 + i;
-    const int e = last_seen(p, r, i), lo = first_seen(p, e);
-    uint32_t q[E];
-    const uint32_t* qp = reinterpret_cast<const uint32_t*>(p.q + t * p.q_token + h * p.q_head) + lane * E;
-#pragma unroll
-    for (int u = 0; u < E; ++u) q[u] = qp[u];
-    float m = -INFINITY, l = 0.f, acc[2 * E];
-#pragma unroll
-    for (int u = 0; u < 2 * E; ++u) acc[u] = 0.f;
-    const int* row = p.table + b * p.table_stride;
-    for (int j = lo; j <= e; ++j) {
-        const int pg = row[j >> p.shift], sl = j & ((1 << p.shift) - 1);
-        if (pg < 0 || pg >= p.pages) continue;
-        const uint32_t* kp =
-            reinterpret_cast<const uint32_t*>(p.k + pg * p.kp + hk * p.kh + sl * p.ks) + lane * E;
-        const uint32_t* vp =
-            reinterpret_cast<const uint32_t*>(p.v + pg * p.vp + hk * p.vh + sl * p.vs) + lane * E;
-        float s = 0.f;
-#pragma unroll
-        for (int u = 0; u < E; ++u) {
-            const uint32_t kk = kp[u];
-            s = fmaf(Ty::lo(q[u]), Ty::lo(kk), s);
-            s = fmaf(Ty::hi(q[u]), Ty::hi(kk), s);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= p.scale2;
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2_approx(m - base), w = exp2_approx(s - base);
-        l = l * f + w;
-#pragma unroll
-        for (int u = 0; u < E; ++u) {
-            const uint32_t vv = vp[u];
-            acc[2 * u] = acc[2 * u] * f + w * Ty::lo(vv);
-            acc[2 * u + 1] = acc[2 * u + 1] * f + w * Ty::hi(vv);
-        }
-        m = mn;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // no position seen: zero
-    uint32_t* op = reinterpret_cast<uint32_t*>(p.out + t * p.o_token + h * p.o_head) + lane * E;
-#pragma unroll
-    for (int u = 0; u < E; ++u)
-        op[u] = l == 0.f ? 0u : Ty::pack(acc[2 * u] * inv, acc[2 * u + 1] * inv);
-    if (p.lse && lane == 0) p.lse[(int64_t)t * p.Hq + h] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
 // Tensor map of the key or value cache, (column, slot, head, page), in boxes of

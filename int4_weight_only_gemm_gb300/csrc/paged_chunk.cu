@@ -30,10 +30,12 @@
 // Over hundreds of positions these roundings average out; rows that see fewer
 // than 256 positions carry them in two parts (hi + lo, two products).
 //
-// Positions that no row of an item sees are cleared in the value tile; where a
-// value that only some rows see is not finite, the item's rows are computed
-// from the definition instead (attn_row), so that a NaN stays with the rows
-// that see it.
+// Positions that no row of an item sees are cleared in the value tile.  Values
+// that only some rows see (an item's last tokens' positions, and the window's
+// first) and that are not finite are taken out of it and added to the output of
+// the rows that see them at the end of the item, so that a NaN stays with
+// those.  That costs a pass over these positions, at most 256 at either end
+// whatever the context's length, in items that have such values only.
 //
 // Bound: the chain softmax -> P -> MMAs -> scores of the two warpgroups, ~3700
 // clocks for a key tile of 256 rows, of which the tensor pipe works 2048.
@@ -222,6 +224,12 @@ W4A16_DEVICE void tmem_ld32(uint32_t taddr, uint32_t* v) {
         : "memory");
 }
 
+// the two halves of v, 0 in the place of infinities and NaN
+template <typename Ty>
+W4A16_DEVICE uint32_t finite(uint32_t v) {
+    return v & ~(((Ty::all_ones(v) >> 15) & 0x00010001u) * 0xffffu);
+}
+
 W4A16_DEVICE float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -321,13 +329,29 @@ struct ChunkWalk {
     }
 };
 
-template <typename Ty, int D>
-W4A16_DEVICE void attn_rows_from_definition(const PagedAttnParams& p, int b, Request r, int i0, int tokens,
-                                                       int hk, int warp) {
-    // a warp takes every fourth row of up to 128
-    for (int x = warp; x < tokens * p.G; x += 4) {
-        const int i = x / p.G;
-        attn_row<Ty, D>(p, b, r, i0 + i, hk * p.G + x - i * p.G);
+// Adds the values that were taken out of an item's value tiles to the columns
+// x0 .. x1 of a row that sees the positions lo .. e: those that are not finite
+// at positions that not all rows see.
+template <typename Ty>
+W4A16_DEVICE void add_taken_out(const PagedAttnParams& p, const ChunkPiece& pc, int lo, int e, uint16_t* out, int x0,
+                                int x1) {
+    const int* table = p.table + (int64_t)pc.b * p.table_stride;
+#pragma unroll 1
+    for (int j = lo; j <= e; ++j) {
+        if (j >= pc.it.lo1 && j <= pc.it.e0) {  // all rows see these
+            j = pc.it.e0;
+            continue;
+        }
+        const int pg = __ldcg(table + (j >> p.shift));
+        if (pg < 0 || pg >= p.pages) continue;
+        const uint16_t* v = p.v + pg * p.vp + pc.hk * p.vh + (int64_t)(j & ((1 << p.shift) - 1)) * p.vs;
+#pragma unroll 1
+        for (int x = x0; x < x1; x += 2) {
+            const uint32_t y = __ldcg(reinterpret_cast<const uint32_t*>(v + x)), t = Ty::all_ones(y) & 0x80008000u;
+            if (t == 0) continue;
+            uint32_t* o = reinterpret_cast<uint32_t*>(out + x);
+            *o = Ty::pack(Ty::lo(*o) + (t & 0x8000u ? Ty::lo(y) : 0.f), Ty::hi(*o) + (t >> 31 ? Ty::hi(y) : 0.f));
+        }
     }
 }
 
@@ -356,7 +380,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
     static_assert((2 * NS + 12) * 8 <= 384, "barriers");
     volatile uint32_t* miss = reinterpret_cast<volatile uint32_t*>(smem + L::kMissOff);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
-    volatile int* abort_flag = misc;  // misc: abort, request, head, item, offset, last arrival (2), -, tensor memory
+    volatile int* abort_flag = misc;  // misc: abort, request, head, item, offset, pieces with values taken out (2), -,
+                                      // tensor memory
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff) + 8;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -379,6 +404,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         mbar_init(join, 8);
         mbar_init(done, 1);
         *abort_flag = 0;
+        misc[5] = misc[6] = 0;
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -699,7 +725,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
             const int e = valid ? last_seen(p, pc.r, pc.it.i0 + mytok) : -1, lo = first_seen(p, e);
             const int cnt = pc.duo ? pc.take : (pc.take + 1 - g) / 2;
             float m = -INFINITY, l = 0.f;
-            bool odd = false;
+            // a thread that takes a value out says so here first (the warpgroups may be a piece apart)
+            volatile int* taken_out = misc + 5 + (items & 1);
             for (int k = 0; k < cnt; ++k) {
                 const int t = pc.duo ? k : 2 * k + g;
                 const int j0 = (pc.it.t0 + pc.off + t) * kChKeys;
@@ -739,18 +766,25 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     if (!ok) break;
                     if (none || some) {
                         const uint32_t va = smem_u32(smem + L::kRingOff + sl * L::kTile) + row * 128;
-                        uint32_t top = 0;  // a half's exponent is all ones: its top bit after the addition
 #pragma unroll 4
                         for (int x = 0; x < 8 * L::kSlabs; ++x) {
                             const uint32_t a = va + (x >> 3) * 16384 + (((x & 7) ^ (row & 7)) << 4);
                             if (none) {
                                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
                             } else {
+                                // (a half whose exponent is all ones has its top bit set after the addition)
                                 const uint4 v = lds_v4(a);
-                                top |= Ty::all_ones(v.x) | Ty::all_ones(v.y) | Ty::all_ones(v.z) | Ty::all_ones(v.w);
+                                if ((Ty::all_ones(v.x) | Ty::all_ones(v.y) | Ty::all_ones(v.z) | Ty::all_ones(v.w)) &
+                                    0x80008000u) {
+                                    *taken_out = (int)items + 1;
+                                    __threadfence_block();
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
+                                                 "r"(finite<Ty>(v.x)), "r"(finite<Ty>(v.y)), "r"(finite<Ty>(v.z)),
+                                                 "r"(finite<Ty>(v.w))
+                                                 : "memory");
+                                }
                             }
                         }
-                        odd |= (top & 0x80008000u) != 0;
                     }
                     fence_proxy_async_smem();
                 }
@@ -849,7 +883,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 // (the last item's are read)
                 if (items > 0) ok = ok && mbar_wait_warp(o_free + g, (items - 1) & 1, abort_flag, &g_chunk_status);
                 ml[g * 128 + row] = make_float2(m, l);
-                if (odd) ml[g * 128 + row].x = NAN;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(join);
                 ok = ok && mbar_wait_warp(join, joins & 1, abort_flag, &g_chunk_status);
@@ -862,7 +895,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
             float f0 = 1.f, f1 = 0.f;
             const bool other = !pc.duo && pc.take > 1;
             if (!pc.duo) {
-                for (int x = 0; x < 256; x += 128) odd = odd || ml[x + row].x != ml[x + row].x;
                 const float2 a = ml[row], o = ml[128 + row];
                 m = a.x;
                 l = a.y;
@@ -876,7 +908,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     m = M;
                 }
             }
-            odd = !bar_and(1 + g, 128, !odd);
+            // (where the other warpgroup took it out of a tile of both, it said so before this one found it gone)
+            const bool odd = !bar_and(1 + g, 128, *taken_out != (int)items + 1);
             const uint32_t toa = tmem + lanes + L::kTO + D * g0, tob = toa + D;
             const int x0 = pc.duo ? 0 : g * (D / 2), x1 = pc.duo ? D : x0 + D / 2;  // columns
             tc_fence_after();
@@ -892,7 +925,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 counter = p.counters + kChCounters + 2 * c0 + g;
             }
             auto piece = [&](int i) { return p.part + ((int64_t)(2 * i + (i == c0)) * 2 + g) * L::kPartHalf; };
-            const float mine_m = odd ? NAN : m * p.scale2;
+            // a piece's sums (>= 0, or NaN) carry in their sign whether values were taken out
+            const float mine_m = m * p.scale2, mine_l = __uint_as_float(__float_as_uint(l) | (odd ? 0x80000000u : 0u));
             // Where all other pieces are there already, this one need not be written:
             // it goes into the sum from tensor memory, in its place of the order.
             bool last = whole, kept = true;  // kept: this piece's output is still in tensor memory only
@@ -926,7 +960,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                             *reinterpret_cast<uint4*>(part + 256 + (((i + x) >> 2) * 128 + row) * 4) =
                                 make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
                     }
-                    reinterpret_cast<float2*>(part)[row] = make_float2(mine_m, l);
+                    reinterpret_cast<float2*>(part)[row] = make_float2(mine_m, mine_l);
                     named_bar(1 + g, 128);
                     bool is_last = true;
                     if (row == 0) {
@@ -938,17 +972,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     last = bar_and(1 + g, 128, is_last);
                 }
             }
-            bool again = odd;  // rows to compute from the definition
+            bool again = odd;  // values to add
+            float S = l;
             if (last) {
-                float M = m * p.scale2, S = l;
+                float M = m * p.scale2;
                 if (!whole) {
                     M = -INFINITY;
                     bool bad = false;
 #pragma unroll 4
                     for (int i = c0; i <= c1; ++i) {
-                        const float x = i == c && kept ? mine_m : __ldcg(piece(i) + 2 * row);
-                        bad |= x != x;
-                        M = fmaxf(M, x);
+                        const float2 mi = i == c && kept ? make_float2(mine_m, mine_l)
+                                                         : __ldcg(reinterpret_cast<const float2*>(piece(i)) + row);
+                        bad |= __float_as_uint(mi.y) >> 31;
+                        M = fmaxf(M, mi.x);
                     }
                     again = !bar_and(1 + g, 128, !bad);
                     S = 0.f;
@@ -958,71 +994,69 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 if (!whole)
 #pragma unroll 4
                     for (int i = c0; i <= c1; ++i) {
-                        const float2 mi = i == c && kept ? make_float2(mine_m, l)
+                        const float2 mi = i == c && kept ? make_float2(mine_m, mine_l)
                                                          : __ldcg(reinterpret_cast<const float2*>(piece(i)) + row);
-                        if (mi.y != 0.f) S = fmaf(mi.y, factor(mi.x), S);
+                        if (mi.y != 0.f) S = fmaf(fabsf(mi.y), factor(mi.x), S);
                     }
                 const float w = S == 0.f ? 0.f : 1.f / S;
-                if (!again) {
 #pragma unroll 1
-                    for (int x = x0; x < x1; x += 32) {
-                        float acc[32];
-                        auto own = [&](float f) {  // this piece's columns, times f, onto acc
-                            uint32_t ov[32];
-                            tmem_ld32(toa + x, ov);
+                for (int x = x0; x < x1; x += 32) {
+                    float acc[32];
+                    auto own = [&](float f) {  // this piece's columns, times f, onto acc
+                        uint32_t ov[32];
+                        tmem_ld32(toa + x, ov);
+                        tmem_wait_ld();
+                        if (other) {
+                            uint32_t ow[32];
+                            tmem_ld32(tob + x, ow);
                             tmem_wait_ld();
-                            if (other) {
-                                uint32_t ow[32];
-                                tmem_ld32(tob + x, ow);
-                                tmem_wait_ld();
 #pragma unroll
-                                for (int y = 0; y < 32; ++y)
-                                    ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
+                            for (int y = 0; y < 32; ++y)
+                                ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), f, acc[y]);
+                    };
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) acc[y] = 0.f;
+                    if (whole) {
+                        own(1.f);
+                    } else {
+                        for (int i = c0; i <= c1; ++i) {
+                            if (i == c && kept) {
+                                // (every lane: tensor-memory loads are the warp's)
+                                own(l == 0.f ? 0.f : factor(mine_m));
+                                continue;
                             }
+                            const float* q = piece(i);
+                            const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
+                            const float f = mi.y == 0.f ? 0.f : factor(mi.x);  // no seen key: zeros
+                            float4 v[8];
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), f, acc[y]);
-                        };
+                            for (int y = 0; y < 8; ++y)
+                                v[y] = __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) acc[y] = 0.f;
-                        if (whole) {
-                            own(1.f);
-                        } else {
-                            for (int i = c0; i <= c1; ++i) {
-                                if (i == c && kept) {
-                                    // (every lane: tensor-memory loads are the warp's)
-                                    own(l == 0.f ? 0.f : factor(mine_m));
-                                    continue;
-                                }
-                                const float* q = piece(i);
-                                const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
-                                const float f = mi.y == 0.f ? 0.f : factor(mi.x);  // no seen key: zeros
-                                float4 v[8];
-#pragma unroll
-                                for (int y = 0; y < 8; ++y)
-                                    v[y] = __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row);
-#pragma unroll
-                                for (int y = 0; y < 8; ++y) {
-                                    acc[4 * y] = fmaf(v[y].x, f, acc[4 * y]);
-                                    acc[4 * y + 1] = fmaf(v[y].y, f, acc[4 * y + 1]);
-                                    acc[4 * y + 2] = fmaf(v[y].z, f, acc[4 * y + 2]);
-                                    acc[4 * y + 3] = fmaf(v[y].w, f, acc[4 * y + 3]);
-                                }
+                            for (int y = 0; y < 8; ++y) {
+                                acc[4 * y] = fmaf(v[y].x, f, acc[4 * y]);
+                                acc[4 * y + 1] = fmaf(v[y].y, f, acc[4 * y + 1]);
+                                acc[4 * y + 2] = fmaf(v[y].z, f, acc[4 * y + 2]);
+                                acc[4 * y + 3] = fmaf(v[y].w, f, acc[4 * y + 3]);
                             }
                         }
-                        if (valid) {
-#pragma unroll
-                            for (int y = 0; y < 32; y += 8)
-                                *reinterpret_cast<uint4*>(out + x + y) =
-                                    S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
-                                             : make_uint4(Ty::pack(acc[y] * w, acc[y + 1] * w),
-                                                          Ty::pack(acc[y + 2] * w, acc[y + 3] * w),
-                                                          Ty::pack(acc[y + 4] * w, acc[y + 5] * w),
-                                                          Ty::pack(acc[y + 6] * w, acc[y + 7] * w));
-                        }
-                        __syncwarp();
                     }
-                    if (valid && p.lse && x0 == 0) p.lse[t * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
+                    if (valid) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+                            *reinterpret_cast<uint4*>(out + x + y) =
+                                S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                         : make_uint4(Ty::pack(acc[y] * w, acc[y + 1] * w),
+                                                      Ty::pack(acc[y + 2] * w, acc[y + 3] * w),
+                                                      Ty::pack(acc[y + 4] * w, acc[y + 5] * w),
+                                                      Ty::pack(acc[y + 6] * w, acc[y + 7] * w));
+                    }
+                    __syncwarp();
                 }
+                if (valid && p.lse && x0 == 0) p.lse[t * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
             }
             tc_fence_before();
             __syncwarp();
@@ -1030,11 +1064,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 mbar_arrive(o_free + g);
                 mbar_arrive(o_free + (pc.duo ? g : 1 - g));
             }
-            again = again && last && x0 == 0;
-            if (again) {
-                const int n = min(toks, pc.it.tokens - base_tok);
-                attn_rows_from_definition<Ty, D>(p, pc.b, pc.r, pc.it.i0 + base_tok, n, pc.hk, warp & 3);
-            }
+            if (again && last && valid && S != 0.f) add_taken_out<Ty>(p, pc, lo, e, out, x0, x1);
             tile0 += pc.take;
             ++items;
         }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import serving
-from test_serving import Attn
+from test_serving import Attn, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -194,3 +194,56 @@ def test_window_as_large_as_it_gets(w, window, new, L):
     a.check(out, lse)
     free, _ = a.run(w, 0)
     assert torch.equal(out, free)
+
+
+def spoil(a, spots):
+    """Puts values that are not finite into the value cache: (request, position, column, value)."""
+    for b, j, col, x in spots:
+        a.vc[int(a.table[b, j // a.page]), a.Hkv - 1, j % a.page, col] = x
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128, "bf16"), (4, 1, 64, "fp16"), (3, 3, 128, "fp16"), (64, 1, 64, "bf16")])
+@pytest.mark.parametrize("lens,window", [([(700, 300)], 0), ([(70, 150), (200, 19)], 0), ([(0, 600)], 64),
+                                         ([(1500, 200), (3, 1)], 5), ([(4000, 40)], 300), ([(0, 260), (900, 270)], 0)])
+def test_values_that_some_tokens_of_a_chunk_see(w, heads, lens, window):
+    """Infinities and NaN among the new tokens' own values: in the columns of the tokens that see them, nowhere else."""
+    Hq, Hkv, d, dtype = heads
+    a = Attn(lens, Hq, Hkv, d, 16, dtype, seed=13)
+    r = np.random.default_rng(5)
+    spots = []
+    for b, (past, new) in enumerate(lens):
+        for x in (np.nan, np.inf, -np.inf, np.inf, np.nan, -np.inf):
+            spots.append((b, past + int(r.integers(0, new)), int(r.integers(0, d)), x))
+        spots.append((b, past + new - 1, 0, np.inf))
+        spots.append((b, past + new - 1, 1, -np.inf))
+    spoil(a, spots)
+    out, lse = a.run(w, window)
+    assert w.w4a16_last_device_status() == 0
+    a.check(out, lse, window)
+    last = int(a.n[0]) - 1  # the newest token: its own infinities, with their signs
+    got = f64(out)[last, -1]
+    seen = {c for b, j, c, x in spots if b == 0 and c < 2 and j < lens[0][0] + lens[0][1] - 1}
+    for c, want in ((0, np.inf), (1, -np.inf)):
+        if c not in seen:
+            assert got[c] == want
+
+
+def test_a_nan_at_the_end_of_a_long_context(w):
+    """What it costs does not grow with the context, and no wait of the kernel runs out over it."""
+    past, new, page = 300000, 40, 256
+    a = Attn([(past, new)], 2, 1, 64, page, "bf16", seed=14)
+    spoil(a, [(0, past + 17, 5, np.nan), (0, past + 30, 6, np.inf)])
+    a.run(w)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    out, lse = a.run(w)
+    end.record()
+    torch.cuda.synchronize()
+    assert w.w4a16_last_device_status() == 0
+    assert start.elapsed_time(end) < 100  # ms; every row anew takes seconds
+    a.check(out, lse)
+    bad = ~np.isfinite(f64(out))
+    want = np.zeros_like(bad)
+    want[17:, :, 5] = True
+    want[30:, :, 6] = True
+    assert np.array_equal(bad, want)
