@@ -415,7 +415,8 @@ int w4a16_page_plan(const w4a16_page_plan_args *args, w4a16_stream_t stream);
  * Other tokens (padding) are skipped.  Two tokens of one call must not name
  * one slot.  16-bit elements (dtype bf16 or fp16, copied bit for bit);
  * head_dim a multiple of 8; all pointers 16-byte aligned, all strides
- * multiples of 8 elements.  The cache must not overlap k, v or slot_map.
+ * multiples of 8 elements (a dimension of one entry may have any), those of the
+ * caches not 0.  The cache must not overlap k, v or slot_map.
  */
 typedef struct {
     const void *k, *v;        /* [tokens][heads][head_dim] */
@@ -454,8 +455,9 @@ int w4a16_kv_write(const w4a16_kv_write_args *args, w4a16_stream_t stream);
  *               requests <= 16384
  *   max_q       at least every n_b (a tighter bound gives a better grid): the
  *               result is undefined for a request with more new tokens
- *   strides     elements, multiples of 8; pointers 16-byte aligned (lse and
- *               the int32 arrays 4-byte)
+ *   strides     elements, positive multiples of 8 (a dimension of one entry
+ *               may have any); pointers 16-byte aligned (lse and the int32
+ *               arrays 4-byte)
  *   lse         may be NULL
  *   kv_len[b]   counted as at most columns * page_size
  *   workspace   w4a16_paged_attention_workspace_bytes bytes, 16-byte aligned,

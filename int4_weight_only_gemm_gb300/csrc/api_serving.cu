@@ -1,6 +1,7 @@
 // C ABI of the serving operators: argument checks and launch counting.  See
 // include/w4a16.h.
 #include <cstdint>
+#include <initializer_list>
 
 #include "kernels.h"
 
@@ -37,7 +38,15 @@ int check_page_size(int p) {
     return p >= 8 && p <= 256 && (p & (p - 1)) == 0 ? W4A16_OK : W4A16_EUNSUPPORTED;
 }
 
-bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
+// Strides, in elements, of at least `least`; that of a dimension of one entry
+// is not looked at, since nothing goes by it.
+int check_strides(int64_t least, std::initializer_list<Dim> dims) {
+    for (const Dim& x : dims)
+        if (x.count > 1 && x.stride < least) return W4A16_EINVAL;
+    for (const Dim& x : dims)
+        if (x.count > 1 && x.stride % 8) return W4A16_EALIGN;
+    return W4A16_OK;
+}
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ECUDA; }
 
@@ -97,11 +106,11 @@ int w4a16_kv_write(const w4a16_kv_write_args* a, w4a16_stream_t stream) {
     if (!aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->slot_map, 4) || !aligned(a->k_cache, 16) ||
         !aligned(a->v_cache, 16))
         return W4A16_EALIGN;
-    for (int64_t x : {a->k_token, a->k_head, a->v_token, a->v_head, a->kc_page, a->kc_head, a->kc_slot, a->vc_page,
-                      a->vc_head, a->vc_slot}) {
-        if (x < 0) return W4A16_EINVAL;
-        if (!stride_ok(x)) return W4A16_EALIGN;
-    }
+    st = check_strides(0, {{a->tokens, a->k_token}, {a->heads, a->k_head}, {a->tokens, a->v_token}, {a->heads, a->v_head}});
+    if (st == W4A16_OK)
+        st = check_strides(1, {{a->num_pages, a->kc_page}, {a->heads, a->kc_head}, {a->page_size, a->kc_slot},
+                               {a->num_pages, a->vc_page}, {a->heads, a->vc_head}, {a->page_size, a->vc_slot}});
+    if (st != W4A16_OK) return st;
     const Dim d = {a->head_dim, 1};
     const Span kc = span(a->k_cache, 2, {a->num_pages, a->kc_page}, {a->heads, a->kc_head}, {a->page_size, a->kc_slot}, d);
     const Span vc = span(a->v_cache, 2, {a->num_pages, a->vc_page}, {a->heads, a->vc_head}, {a->page_size, a->vc_slot}, d);
@@ -149,11 +158,11 @@ int w4a16_paged_attention(const w4a16_paged_attention_args* a, w4a16_stream_t st
     if (!aligned(a->q, 16) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->out, 16) ||
         !aligned(a->block_table, 4) || !aligned(a->q_start, 4) || !aligned(a->kv_len, 4) || !aligned(a->lse, 4))
         return W4A16_EALIGN;
-    for (int64_t x : {a->q_token, a->q_head, a->out_token, a->out_head, a->kc_page, a->kc_head, a->kc_slot,
-                      a->vc_page, a->vc_head, a->vc_slot}) {
-        if (x < 0) return W4A16_EINVAL;
-        if (!stride_ok(x)) return W4A16_EALIGN;
-    }
+    st = check_strides(1, {{a->tokens, a->q_token}, {a->q_heads, a->q_head}, {a->tokens, a->out_token},
+                           {a->q_heads, a->out_head}, {a->num_pages, a->kc_page}, {a->kv_heads, a->kc_head},
+                           {a->page_size, a->kc_slot}, {a->num_pages, a->vc_page}, {a->kv_heads, a->vc_head},
+                           {a->page_size, a->vc_slot}});
+    if (st != W4A16_OK) return st;
     const Dim d = {a->head_dim, 1};
     const Span in[] = {
         span(a->q, 2, {a->tokens, a->q_token}, {a->q_heads, a->q_head}, d),
