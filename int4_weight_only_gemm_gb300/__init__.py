@@ -257,6 +257,14 @@ _ws_cache: dict[int, torch.Tensor] = {}
 _need_cache: dict[tuple, int] = {}
 
 
+def _remember(key: tuple, need: int) -> int:
+    """Keeps a workspace's size; all of them go where sizes keep changing."""
+    if len(_need_cache) >= 4096:
+        _need_cache.clear()
+    _need_cache[key] = int(need)
+    return int(need)
+
+
 def _workspace_need(path: int, M: int, N: int, K: int, group: int, device: torch.device) -> int:
     """Workspace bytes a problem needs, asked of the library once per problem
     and device (the answer depends only on these)."""
@@ -264,8 +272,7 @@ def _workspace_need(path: int, M: int, N: int, K: int, group: int, device: torch
     key = (path, M, N, K, group, idx)
     need = _need_cache.get(key)
     if need is None:
-        need = int(load_library().w4a16_workspace_bytes_path(path, M, N, K, group))
-        _need_cache[key] = need
+        need = _remember(key, load_library().w4a16_workspace_bytes_path(path, M, N, K, group))
     return need
 
 
@@ -430,7 +437,7 @@ def _strided(t, name, dtype, dims):
 # memory, with the zeroing of its counters as a node of the graph.
 _stream_workspaces: dict = {}   # (device, stream): buffer
 _capture_workspaces: dict = {}  # (device, stream): (capture, buffer), kept for the capture's next call
-_outgrown_workspaces: list = []
+_MOST_STREAMS = 64              # that keep a buffer; the one given longest ago goes first
 
 
 def _stream_of(index: int, stream: int):
@@ -460,9 +467,11 @@ def _serving_workspace(nbytes: int, index: int, stream, handle: int) -> torch.Te
     ws = _stream_workspaces.get((index, handle))
     if ws is not None and ws.numel() >= nbytes:
         return ws
+    # Buffers that go are the stream's own: their memory is given out again in the order of that stream, behind the
+    # kernels that still use it.
     fresh = _zeroed(max(nbytes, 2 * ws.numel() if ws is not None else 0), index, handle)
-    if ws is not None:
-        _outgrown_workspaces.append(ws)
+    if ws is None and len(_stream_workspaces) >= _MOST_STREAMS:
+        del _stream_workspaces[next(iter(_stream_workspaces))]
     _stream_workspaces[(index, handle)] = fresh
     return fresh
 
@@ -580,11 +589,11 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     lib, idx = load_library(), q.get_device()
     st = _stream(stream, idx)
     if workspace is None:
-        key = ("paged_attention", T, B, Hq, Hkv, d, max_q, idx)
+        key = ("paged_attention", Hq, Hkv, d, max_q, idx)
         need = _need_cache.get(key)
-        if need is None:
-            need = int(lib.w4a16_paged_attention_workspace_bytes(T, B, Hq, Hkv, d, max_q))
-            _need_cache[key] = need
+        if need is None:  # for as many tokens and requests as a call takes, which change from step to step
+            need = _remember(key, lib.w4a16_paged_attention_workspace_bytes(0x7fffffff // max(Hq, 1), 16384, Hq, Hkv,
+                                                                            d, max_q))
         if need:
             workspace = _serving_workspace(need, idx, stream, st)
     args = _ATTN_ARGS.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), start, kv,
@@ -640,8 +649,7 @@ def w4a16_sample(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.T
         key = ("sample", R, V, filters, idx)
         need = _need_cache.get(key)
         if need is None:
-            need = int(lib.w4a16_sample_workspace_bytes(R, V, int(filters)))
-            _need_cache[key] = need
+            need = _remember(key, lib.w4a16_sample_workspace_bytes(R, V, int(filters)))
         if need:
             workspace = _serving_workspace(need, idx, stream, st)
     args = _SAMPLE_ARGS.pack(logits.data_ptr(), noise.data_ptr(), _rows_of(temperature, "temperature", f32, R),

@@ -181,3 +181,36 @@ def test_attention_after_a_timeout(fresh):
     assert w.w4a16_last_device_status() == w.W4A16_ETIMEOUT
     assert torch.equal(small(), want)
     assert w.w4a16_last_device_status() == w.W4A16_OK
+
+
+# ---------------------------------------------------------------------------
+# what is kept
+# ---------------------------------------------------------------------------
+
+def test_what_the_binding_keeps_is_bounded(fake):
+    """A larger call takes the place of its stream's buffer, streams that come and go do not pile up."""
+    import gc
+    import weakref
+    buffers = []
+    for i in range(40):
+        buffers.append(weakref.ref(w._serving_workspace(65536 << (i % 8), 0, None, 0x70)))
+    gc.collect()
+    assert len({id(b()) for b in buffers if b() is not None}) == 1
+    for i in range(500):
+        w._serving_workspace(100, 0, None, 0x1000 + 16 * i)
+    assert len(w._stream_workspaces) == 64 and (0, 0x1000 + 16 * 499) in w._stream_workspaces
+
+
+def test_sizes_kept_are_bounded(monkeypatch):
+    monkeypatch.setattr(w, "_need_cache", {})
+    for i in range(10000):
+        assert w._remember(("gemm", i), 2 * i) == 2 * i
+        assert len(w._need_cache) <= 4096
+
+
+@pytest.mark.gpu
+def test_sizes_asked_once_for_all_steps(fresh, monkeypatch):
+    monkeypatch.setattr(w, "_need_cache", {})
+    for lens in ([(20, 1)], [(30, 1)] * 5, [(9, 1), (800, 1)]):
+        attention_of(lens, 8, 2)[0]()
+    assert len(w._need_cache) == 1
