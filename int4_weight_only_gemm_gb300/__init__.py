@@ -596,6 +596,8 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                                                                             d, max_q))
         if need:
             workspace = _serving_workspace(need, idx, stream, st)
+    elif not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     args = _ATTN_ARGS.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), start, kv,
                            out.data_ptr(), 0 if lse is None else lse.data_ptr(),
                            0 if workspace is None else workspace.data_ptr(),
@@ -652,6 +654,8 @@ def w4a16_sample(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.T
             need = _remember(key, lib.w4a16_sample_workspace_bytes(R, V, int(filters)))
         if need:
             workspace = _serving_workspace(need, idx, stream, st)
+    elif not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     args = _SAMPLE_ARGS.pack(logits.data_ptr(), noise.data_ptr(), _rows_of(temperature, "temperature", f32, R),
                              _rows_of(top_k, "top_k", torch.int32, R), _rows_of(top_p, "top_p", f32, R),
                              _rows_of(min_p, "min_p", f32, R), _rows_of(token, "token", torch.int32, R),

@@ -214,3 +214,16 @@ def test_sizes_asked_once_for_all_steps(fresh, monkeypatch):
     for lens in ([(20, 1)], [(30, 1)] * 5, [(9, 1), (800, 1)]):
         attention_of(lens, 8, 2)[0]()
     assert len(w._need_cache) == 1
+
+
+@pytest.mark.gpu
+def test_workspaces_that_are_none(fresh):
+    """Host memory, or every other byte of a buffer, is not handed to a kernel."""
+    small, need = attention_of([(20, 1)], 8, 2)
+    logits, noise = torch.randn(3, 5000, device="cuda"), torch.ones(3, 5000, device="cuda")
+    k = i32([5, 5, 5])
+    for bad in (torch.zeros(max(need, 1 << 20), dtype=torch.uint8), w.new_workspace(1 << 21)[::2], 0):
+        with pytest.raises(ValueError):
+            small(workspace=bad)
+        with pytest.raises(ValueError):
+            w.w4a16_sample(logits, noise, top_k=k, workspace=bad)
