@@ -507,8 +507,9 @@ size_t w4a16_paged_attention_workspace_bytes(int tokens, int requests, int q_hea
  * For noise drawn from the exponential distribution of rate 1 this is a draw
  * with the kept tokens' renormalised probabilities (of independent exponential
  * variables with rates p_i, variable i is the smallest with probability
- * p_i / sum p).  temperature[r] <= 0 takes the most probable token (lowest
- * index among equals) and reads no noise.
+ * p_i / sum p).  temperature[r] <= 0 (or NaN) takes the most probable token
+ * (lowest index among equals) and reads no noise; one above 0 counts as at least
+ * 1e-30 and at most 1e30.
  * logprob[r] = z_token - log sum_i exp(z_i) over the whole row, before the
  * filters (temperature 1 where temperature[r] <= 0).  NaN logits count as
  * -inf and are never taken, nor are -inf ones; a row without any other gives

@@ -88,8 +88,8 @@ W4A16_DEVICE float decode(uint32_t bits) {
     if constexpr (DT == W4A16_BF16) return clean(__uint_as_float(bits << 16));
     return clean(f16_bits_to_f32((uint16_t)bits));
 }
-// z of a cleaned logit: the f32 quotient, at most the largest finite value
-W4A16_DEVICE float z_of(float l, float t) { return fminf(__fdiv_rn(l, t), kBig) + 0.f; }
+// z of a cleaned logit above -inf: the f32 quotient, finite
+W4A16_DEVICE float z_of(float l, float t) { return fmaxf(fminf(__fdiv_rn(l, t), kBig), -kBig) + 0.f; }
 
 W4A16_DEVICE float ex2(float x) {
     float y;
@@ -335,7 +335,7 @@ struct RowParams {
     W4A16_DEVICE RowParams(const w4a16_sample_args& p, int r) {
         const float t = p.temperature ? p.temperature[r] : 1.f;
         greedy = !(t > 0.f);
-        T = greedy ? 1.f : t;
+        T = greedy ? 1.f : fminf(fmaxf(t, 1e-30f), 1e30f);  // no quotient of usual logits overflows or is subnormal
         c2 = fminf(kLog2E / T, kBig);
         k = p.top_k ? p.top_k[r] : 0;
         tp = p.top_p ? p.top_p[r] : 1.f;

@@ -247,3 +247,28 @@ def test_a_nan_at_the_end_of_a_long_context(w):
     want[17:, :, 5] = True
     want[30:, :, 6] = True
     assert np.array_equal(bad, want)
+
+
+# ---------------------------------------------------------------------------
+# sampling: temperatures near the ends of f32
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("V", [1500, 40000])
+@pytest.mark.parametrize("positive", [False, True])
+def test_temperatures_near_the_ends_of_f32(w, V, positive):
+    t = np.array([1e-45, 1e-39, 1e-38, 1e-30, 1e30, 3e38, np.inf, np.nan], np.float32)
+    R = len(t)
+    r = np.random.default_rng(V)
+    x = (r.standard_normal((R, V)) * 3 + (20 if positive else -40)).astype(np.float32)
+    x[:, 5::11] = -np.inf
+    e = r.exponential(size=(R, V)).astype(np.float32)
+    as_if = np.where(np.isnan(t), np.float32(0), np.clip(t, np.float32(1e-30), np.float32(1e30)))
+    for more in ({}, dict(k=np.full(R, 40)), dict(p=np.full(R, 0.5003, np.float32)), dict(m=np.full(R, 0.1, np.float32)),
+                 dict(k=np.full(R, 3000), p=np.full(R, 0.9, np.float32), m=np.full(R, 0.01, np.float32))):
+        want = [serving.sample(x[i], e[i], as_if[i], *(more[f][i] if f in more else None for f in "kpm")) for i in range(R)]
+        lp = torch.empty(R, device="cuda")
+        tok = w.w4a16_sample(dev(x), dev(e), dev(t), dev(more.get("k"), torch.int32), dev(more.get("p")),
+                             dev(more.get("m")), logprob=lp)
+        # (an infinite or equal draw apart: at 1e30 all quotients are below 1e-28 and the race is the noise's alone)
+        assert tok.tolist() == [a for a, _ in want], more.keys()
+        assert np.all(np.abs(lp.cpu().numpy() - [b for _, b in want]) <= 1e-4)
