@@ -96,12 +96,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct Request {
     int t0, n, L;
 };
+// (lengths and table entries are read from L2: the chunk kernel may start without a wait of its own, behind the
+// small-row kernel's, and what an SM's first-level cache holds may be older than the kernels before both)
 W4A16_DEVICE Request request_of(const PagedAttnParams& p, int b) {
     Request r;
-    r.t0 = min(max(p.q_start[b], 0), p.T);
-    r.n = min(max(p.q_start[b + 1], r.t0), p.T) - r.t0;
+    r.t0 = min(max(__ldcg(p.q_start + b), 0), p.T);
+    r.n = min(max(__ldcg(p.q_start + b + 1), r.t0), p.T) - r.t0;
     const int64_t room = (int64_t)p.columns << p.shift;
-    r.L = max(p.kv_len[b], 0);
+    r.L = max(__ldcg(p.kv_len + b), 0);
     if (r.L > room) r.L = (int)room;
     return r;
 }

@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
     }
     // Behind the small-row kernel of the same call there is nothing to wait for:
     // that kernel let this one start once everything before it was done, and the
-    // two have requests, counters and workspace of their own.
+    // two have requests, counters and workspace of their own.  What earlier kernels
+    // wrote is in L2, and is read from there (tensor copies, __ldcg).
     if (!p.after_small) pdl_wait();
     pdl_launch_dependents();
 
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 const int j = (pc.it.t0 + pc.off + t) * kChKeys + lane * rows, col = j >> p.shift;
                 // boxes that no row sees are not read: -2
                 if (t >= pc.take || lane >= boxes || j > pc.it.e1 || j + rows <= pc.it.lo0) return -2;
-                return col < p.columns ? row[col] : -1;
+                return col < p.columns ? __ldcg(row + col) : -1;
             };
             auto load = [&](int t, int kv, int ent) {  // the next ring entry: tile t's keys or values
                 const int slot = ((pc.it.t0 + pc.off + t) * kChKeys + lane * rows) & (page - 1), sl = e % NS;
