@@ -123,6 +123,8 @@ class Server:
         pages = sum(up(p + n) - up(p) for p, n in zip(self.past, new))
         if pages > len(self.free):
             raise RuntimeError("the cache is full")
+        if max(up(p + n) for p, n in zip(self.past, new)) > c.max_pages:
+            raise RuntimeError("a request is longer than its row of the block table")
         ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
         plan = w.w4a16_page_plan(ints(self.past), ints(new), ints(self.free), self.table, c.page_size,
                                  max_tokens=sum(new))
