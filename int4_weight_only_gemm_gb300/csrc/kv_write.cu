@@ -6,7 +6,7 @@
 // the pieces of a token are consecutive threads, so reads and writes are whole
 // rows; eight CTAs an SM keep enough loads in flight.  Bound: HBM, each byte
 // read once and written once.  Measured: 16301 tokens, 8 heads of 128 in bf16
-// (134 MB read and written): 22.2 us, 6.0 TB/s; 64 tokens: 2.2 us, or the 6.2 us
+// (134 MB read and written): 22.0 us, 6.0 TB/s; 64 tokens: 1.6 us, or the 5.8 us
 // that the host takes for a call.
 #include "common.cuh"
 #include "kernels.h"

@@ -11,9 +11,9 @@
 // for another: one launch, no hand-off between CTAs.  A token's page comes
 // from the lengths and the free list, never from an entry that another CTA
 // writes in this launch.  Bound: launch and a chain of two dependent loads.
-// Measured: 64 decoding requests 4.8 us, 2048 requests, an eighth of them with
-// up to 2048 new tokens (5.4 MB in and out), 8.2 us; called one by one from the
-// host 7.2 and 9.5 us.
+// Measured: 64 decoding requests 4.2 us, 2048 requests, an eighth of them with
+// up to 2048 new tokens (5.4 MB in and out), 7.8 us; called one by one from the
+// host 6.9 and 9.8 us.
 #include "common.cuh"
 #include "kernels.h"
 

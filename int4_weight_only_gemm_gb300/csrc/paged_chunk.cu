@@ -35,15 +35,16 @@
 // first) and that are not finite are taken out of it and added to the output of
 // the rows that see them at the end of the item, so that a NaN stays with
 // those.  That costs a pass over these positions, at most 256 at either end
-// whatever the context's length, in items that have such values only.
+// whatever the context's length, and only in items that have such values.
 //
 // Bound: the chain softmax -> P -> MMAs -> scores of the two warpgroups, ~3700
 // clocks for a key tile of 256 rows, of which the tensor pipe works 2048.
 // Measured: a 2048-token chunk of a request of 8448 positions, 32 query heads over
-// 8 key heads of 128, bf16 (249 GFLOP): 206 us, 1.21 PFLOP/s (the tensor pipe
-// active 49 %); with all its pages in L2 203 us.  16 blocks of 16 draft tokens
-// over 4080 positions each (269 MB of keys and values): 51.9 us, 5.2 TB/s, 47 us
-// with the pages in L2.
+// 8 key heads of 128, bf16 (249 GFLOP): 199.5 us, 1.25 PFLOP/s (the tensor pipe
+// active 50 %; pages that are in L2 already make it 1.5 % faster).  16 blocks of
+// 16 draft tokens over 4080 positions each (269 MB of keys and values): 51.8 us,
+// 5.2 TB/s, 47 us with the pages in L2.  150 tokens behind 8000 positions, 8 heads
+// over 2: 70 us, 0.97 ms with a NaN among their values.
 //
 // Every wait is bounded: on a timeout the kernel records W4A16_ETIMEOUT, ends
 // its copies and MMAs, frees its tensor memory and returns.
@@ -643,8 +644,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // ------------------------------------------------------------ MMAs
         // The warpgroups in turn: P V of a tile and the scores of the next one
         // go out together.
-        // What steers the loop is made uniform, for the descriptors' sake: 206 us
-        // against 218 for the chunk above.
+        // What steers the loop is made uniform, for the descriptors' sake: the chunk
+        // above took 206 us with it and 218 without.
         constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<Ty>(D, true);
         const uint32_t tm = uniform(tmem), sm = uniform(smem_u32(smem));
         auto tile_at = [&](uint32_t slot, uint32_t kind) {  // a descriptor's low word; tile 0 is Q's first

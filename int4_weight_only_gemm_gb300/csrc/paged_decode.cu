@@ -25,8 +25,8 @@
 // to an SM; with them 64 requests took 248 us.
 //
 // Measured, 32 query heads over 8 key heads of 128, bf16, 16-slot pages: 64
-// requests of up to 8448 positions (1.18 GB) 182 us, 6.5 TB/s; one request of
-// 2304 positions 10.3 us, of which ~3.0 k clocks go to the cut of the line, 2.5 k
+// requests of up to 8448 positions (1.18 GB) 182-185 us, 6.5 TB/s; one request of
+// 2304 positions 9.6 us, of which ~3.0 k clocks go to the cut of the line, 2.5 k
 // to the first table entries and copies, 1.9 k to the keys and values
 // themselves, 2.0 k to the warps' results and 2.4 k to the joining of the 18
 // pieces.

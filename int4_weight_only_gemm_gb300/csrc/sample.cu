@@ -19,19 +19,28 @@
 //      their counts or weights and sorts what lies in that bin alone, tokens
 //      above it are kept for certain.  Only the kept ones' random numbers are
 //      read;
-//   4. with more candidates (a flat row) it counts them in bins, which bounds
-//      where the cuts fall; tokens above are kept for certain and take part in
-//      the race as they are read, their weights summed; only the tokens around
-//      the cuts are collected and sorted;
-//   5. where even those are more than kList (thousands of equal logits), it
-//      finds the cuts by bisection over order-preserving keys.
+//   4. with more candidates (a flat row, a top-k above 1024) it counts them in
+//      bins, which bounds where the cuts fall; tokens above are kept for certain
+//      and take part in the race as they are read, their weights summed; only the
+//      tokens around the cuts are collected and sorted;
+//   5. where even those are more than kList, or the bins do not bound the cut, it
+//      finds the cuts by bisection over order-preserving keys: thousands of equal
+//      logits, but also a nucleus of many thousand tokens, and a top-k of more
+//      tokens than a mask leaves the row.
+//
+// Steps 4 and 5 are one CTA's walks over the whole row, two or three in step 4
+// and some 20 to 50 in step 5.
 //
 // Bound: HBM for many rows (every logit once; the passes after the first find
 // them in L2), launches and the chain of passes for few.  Measured, 151936
-// tokens a row: 256 f32 rows without filters 45.7 us, 6.8 TB/s; one bf16 row with
-// top-k and top-p 15.1 us (7 k clocks the first kernel, 20 k the second); 64 bf16
-// rows with filters of their own 26 us.  A row whose nucleus has 735 tokens takes
-// 28 us, one that step 4 has to count ~80.
+// tokens a row: 256 f32 rows without filters 45.4 us, 6.8 TB/s; one bf16 row with
+// top-k and top-p 14.7 us (7 k clocks the first kernel, 20 k the second); 64 bf16
+// rows with filters of their own 25-31 us, by what the filters leave.  One row,
+// and 64 of them: a nucleus of 100 to 4000 tokens 21-28 and 28-37 us (step 3; in
+// one of the 64 rows at T = 1.3 and p = 0.99 step 5, 4.5 ms), top-k 2000 to 20000
+// 140-200 and 200-300 us (step 4), a nucleus of 15000 tokens 2.9 and 4.6 ms, five
+// tokens left by a mask under top-k 50 1.2 and 2.0 ms, 105 of them (the others at
+// -1e9) under top-k 500 4.0 and 6.4 ms (step 5).
 //
 // Sums are added in an order that depends on the sizes alone, and the sort
 // makes the order of collection irrelevant, so a row's token and logprob do
