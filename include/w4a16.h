@@ -367,7 +367,10 @@ size_t w4a16_swa_workspace_bytes(int nq, int Hq, int Hkv, int head_dim, int L, i
  * W4A16_EUNSUPPORTED for a type, head width or size outside the stated set,
  * W4A16_EWORKSPACE for a missing or short workspace.
  */
-typedef enum { W4A16_BF16 = 0, W4A16_F16 = 1, W4A16_F32 = 2 } w4a16_dtype;
+typedef enum {
+    W4A16_BF16 = 0, W4A16_F16 = 1, W4A16_F32 = 2,
+    W4A16_INT8 = 3, W4A16_E4M3 = 4 /* 8-bit caches: two's complement; floating, 4 exponent and 3 mantissa bits */
+} w4a16_dtype;
 
 /*
  * Block tables, slot map and positions of a step, from the requests' lengths:
@@ -489,6 +492,159 @@ int w4a16_paged_attention(const w4a16_paged_attention_args *args, w4a16_stream_t
 /* Workspace that any call with these sizes or fewer tokens and requests needs on the current device. */
 size_t w4a16_paged_attention_workspace_bytes(int tokens, int requests, int q_heads, int kv_heads, int head_dim,
                                              int max_q);
+
+/*
+ * The same attention over an 8-bit cache, for a tree of drafted tokens, or both.
+ *
+ * 8-bit cache (cache_dtype W4A16_INT8 or W4A16_E4M3; the arguments' dtype stays
+ * that of q and out): k_cache and v_cache hold codes, and k_scale, v_scale one
+ * f32 a page, head and slot, so that
+ *
+ *     k[j][hk] = k_scale[page][hk][slot] * k_cache[page][hk][slot],  v alike
+ *
+ * The codes go into the products as they are, the scales in f32 (that of a key
+ * to its scores, that of a value to its softmax weights, which are rounded to
+ * bf16 for the product, in two parts where w4a16_paged_attention has two, and
+ * always for fp16), so that neither keys nor values are rounded.  A scale that
+ * is not finite stands for a key or a value of NaN; the e4m3 codes without a
+ * value (0x7f, 0xff) count as +-480.  Strides of k_cache and v_cache count
+ * elements, multiples of 16; those of the scales are not negative (0: one scale
+ * for all), and 4-byte alignment is all that they need.
+ *
+ * Tree (tree not NULL, block 0): the new tokens of request b are the nodes of a
+ * tree, node i in position L_b - n_b + i of the cache.  Bit k % 32 of word k / 32
+ * of row t of tree says whether token t sees node k of its own request (a path:
+ * the node itself and its ancestors; any set of bits is taken, and bits from n_b
+ * on are not looked at).  With c_t bits set among the first n_b and
+ * past = L_b - n_b,
+ *
+ *     J_t = { j < past : j >= past + c_t - window, j's page is there }   (window = 0: no lower bound)
+ *           + { past + k : bit k is set, 0 <= past + k, its page is there }
+ *
+ * so that a node's place in the window is behind the context by its depth.  A
+ * row without a bit sees the context alone; nodes past the mask's words are
+ * not seen.
+ */
+typedef struct {
+    const float *k_scale, *v_scale; /* [num_pages][kv_heads][page_size], strided; NULL with a 16-bit cache */
+    const uint32_t *tree;           /* [tokens][tree_words], rows tree_token apart, or NULL */
+    int64_t ks_page, ks_head, ks_slot, vs_page, vs_head, vs_slot; /* strides, elements */
+    int64_t tree_token;             /* stride, words */
+    int32_t cache_dtype;            /* the arguments' dtype, W4A16_INT8 or W4A16_E4M3 */
+    int32_t tree_words;             /* 1 .. 64 with a tree, else 0 */
+} w4a16_paged_attention_ext;
+/* ext may be NULL: w4a16_paged_attention.  Workspace and errors as there. */
+int w4a16_paged_attention_ex(const w4a16_paged_attention_args *args, const w4a16_paged_attention_ext *ext,
+                             w4a16_stream_t stream);
+
+/*
+ * Rotary positions.  The first rotary_dim columns of a head are r / 2 pairs,
+ * pair i the columns (i, i + r / 2), or (2 i, 2 i + 1) with interleaved = 1; at
+ * position p a pair (a, b) becomes
+ *
+ *     (a cos w - b sin w, a sin w + b cos w) * magnitude,   w = p * frequencies[i]
+ *
+ * and the other columns stay.  frequencies: radians per position in f64 (device
+ * memory), so that any scaling for long contexts can be put into them
+ * (w4a16_rope_frequencies makes the usual ones).  The angle is reduced exactly:
+ * a position times a 64-bit fraction of a turn, modulo one turn; its error, in
+ * turns, is that of the f64 frequency times p, 2^-53 p frequency / pi.  Sine, cosine
+ * and products are f32, the result is rounded once to the inputs' type.
+ *
+ * x and out: [tokens][heads][head_dim] in bf16 or fp16, out either x itself
+ * (same pointer and strides) or not overlapping it.  head_dim a multiple of 8,
+ * at most 256; rotary_dim even, 2 .. head_dim; strides (elements) and pointers
+ * as for w4a16_kv_write.  Tokens with a negative position (padding) are skipped:
+ * their rows of out stay as they are.
+ */
+typedef struct {
+    const void *x;
+    void *out;
+    const int32_t *positions;   /* [tokens] */
+    const double *frequencies;  /* [rotary_dim / 2] */
+    int64_t x_token, x_head, out_token, out_head; /* strides, elements */
+    int32_t tokens, heads, head_dim, rotary_dim, interleaved, dtype;
+    float magnitude;
+    uint32_t flags;
+} w4a16_rope_args;
+int w4a16_rope(const w4a16_rope_args *args, w4a16_stream_t stream);
+
+/*
+ * Frequencies (host memory, rotary_dim / 2 of them) and the magnitude that goes
+ * with them.  With f_i = base^(-2 i / r), and length the context that the model
+ * was trained for:
+ *
+ *     NONE        f_i
+ *     LINEAR      f_i / factor
+ *     BASE        f_i of the base base * factor^(r / (r - 2)), whose last pair is LINEAR's
+ *     RAMP        f_i for pairs of more than `high` turns in `length` positions, f_i / factor for those of less
+ *                 than `low` turns, between them blended linearly in i; magnitude 0.1 ln(factor) + 1
+ *     WAVELENGTH  the same ends, between them blended linearly in the number of turns; magnitude 1
+ *
+ * W4A16_EINVAL for a null pointer, rotary_dim not even or below 2, a base or a
+ * factor that is not above 0, and, for the last two, a length not above 0 or not
+ * low < high.
+ */
+enum { W4A16_ROPE_NONE = 0, W4A16_ROPE_LINEAR = 1, W4A16_ROPE_BASE = 2, W4A16_ROPE_RAMP = 3, W4A16_ROPE_WAVELENGTH = 4 };
+int w4a16_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double length, double low,
+                           double high, double *frequencies, float *magnitude);
+
+/*
+ * New keys and values into a cache of 16 or 8 bits, with the rotary positions of
+ * the same tokens' queries and keys on the way (frequencies not NULL) or without.
+ * Slots and skipped tokens as for w4a16_kv_write; with frequencies, tokens with a
+ * negative position are skipped altogether, and the queries of the others go,
+ * rotated, to q_out whatever their slot is.
+ *
+ * 16-bit cache (cache_dtype = dtype): keys are rotated and rounded once, values copied.
+ * 8-bit cache (W4A16_INT8, W4A16_E4M3): per token and head, in f32 operations,
+ * with amax the largest magnitude (of the rotated key) and top = 127 or 448,
+ *
+ *     scale = amax / top,  code = round(x * (top / amax))   (to nearest, ties to even, in the code's type)
+ *
+ * A row whose amax is below 2^-100 gets scale 0 and codes 0; one that holds a
+ * NaN or an infinity scale NaN and codes 0 (it reads as NaN throughout).
+ *
+ * head_dim a multiple of 8 (of 16 for an 8-bit cache), at most 256; q_heads = 0
+ * (q, q_out NULL) for no queries; without frequencies there are none.  Strides of an
+ * 8-bit cache are multiples of 16 elements, those of the scales above 0.  Neither
+ * cache nor scales overlap anything else; q_out is q itself or overlaps nothing.
+ */
+typedef struct {
+    const void *q, *k, *v;      /* [tokens][q_heads or heads][head_dim] */
+    void *q_out;
+    const int32_t *positions;   /* [tokens]; NULL without frequencies */
+    const double *frequencies;  /* [rotary_dim / 2] or NULL */
+    const int32_t *slot_map;    /* [tokens] */
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;   /* [num_pages][heads][page_size], strided; NULL with a 16-bit cache */
+    int64_t q_token, q_head, out_token, out_head, k_token, k_head, v_token, v_head; /* strides, elements */
+    int64_t kc_page, kc_head, kc_slot, vc_page, vc_head, vc_slot;
+    int64_t ks_page, ks_head, ks_slot, vs_page, vs_head, vs_slot;
+    int32_t tokens, q_heads, heads, head_dim, rotary_dim, interleaved, num_pages, page_size, dtype, cache_dtype;
+    float magnitude;
+    uint32_t flags;
+} w4a16_kv_store_args;
+int w4a16_kv_store(const w4a16_kv_store_args *args, w4a16_stream_t stream);
+
+/*
+ * Cached keys and values back as 16-bit arrays: for every token t with a slot in
+ * range, k[t][h] = k_scale * code (rounded once to dtype; a 16-bit cache: copied),
+ * v alike, by the rules of w4a16_kv_store and w4a16_paged_attention_ex.  Rows of
+ * other tokens stay as they are.  Two tokens may name one slot.
+ */
+typedef struct {
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale; /* or NULL */
+    const int32_t *slot_map;        /* [tokens] */
+    void *k, *v;                    /* [tokens][heads][head_dim] */
+    int64_t k_token, k_head, v_token, v_head;
+    int64_t kc_page, kc_head, kc_slot, vc_page, vc_head, vc_slot;
+    int64_t ks_page, ks_head, ks_slot, vs_page, vs_head, vs_slot;
+    int32_t tokens, heads, head_dim, num_pages, page_size, dtype, cache_dtype;
+    uint32_t flags;
+} w4a16_kv_read_args;
+int w4a16_kv_read(const w4a16_kv_read_args *args, w4a16_stream_t stream);
 
 /*
  * Sampling of one token a row from logits[rows][vocab], with random numbers

@@ -87,6 +87,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.w4a16_swa_workspace_bytes.restype = sz
             for name in ("w4a16_page_plan", "w4a16_kv_write", "w4a16_paged_attention", "w4a16_sample"):
                 getattr(lib, name).argtypes = [ctypes.c_char_p, vp]  # a packed argument struct, a stream
+            for name in ("w4a16_rope", "w4a16_kv_store", "w4a16_kv_read"):
+                getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
+            lib.w4a16_paged_attention_ex.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp]
+            cd = ctypes.c_double
+            lib.w4a16_rope_frequencies.argtypes = [ci, cd, ci, cd, cd, cd, cd, ctypes.POINTER(cd),
+                                                   ctypes.POINTER(ctypes.c_float)]
             lib.w4a16_paged_attention_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci]
             lib.w4a16_paged_attention_workspace_bytes.restype = sz
             lib.w4a16_sample_workspace_bytes.argtypes = [ci, ci, ci]
@@ -394,7 +400,13 @@ _PLAN_ARGS = struct.Struct("=9QqiiiiiI")
 _WRITE_ARGS = struct.Struct("=5Q10qiiiiiiIi")
 _ATTN_ARGS = struct.Struct("=9QQ11qiiiiiiiiiiiifI")
 _SAMPLE_ARGS = struct.Struct("=9QQqqiiiI")
+_EXT_ARGS = struct.Struct("=3Q7qii")
+_ROPE_ARGS = struct.Struct("=4Q4qiiiiiifI")
+_STORE_ARGS = struct.Struct("=11Q20qiiiiiiiiiifI")
+_READ_ARGS = struct.Struct("=7Q16qiiiiiiiI")
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_CODES = {torch.int8: 3, torch.float8_e4m3fn: 4}  # of 8-bit caches
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
 _Tensor, _I32 = torch.Tensor, torch.int32  # (looked up some ten times a call)
 
 
@@ -531,12 +543,90 @@ def _caches(k_cache, v_cache, dtype):
     return shape, ks, vs
 
 
+def _scale(t, name, shape):
+    """Strides of an 8-bit cache's scales [pages, heads, page_size] f32."""
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not torch.float32:
+        raise ValueError(f"{name} must be a float32 CUDA tensor")
+    if t.shape != shape[:3]:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape[:3])}")
+    return t.stride()
+
+
+def _codes(k_cache, k_scale, v_scale, dtype):
+    """The cache's element type, and its number; scales go with an 8-bit cache and with no other."""
+    if not isinstance(k_cache, _Tensor):
+        raise ValueError("k_cache must be a CUDA tensor")
+    cdtype = k_cache.dtype
+    code = _CODES.get(cdtype)
+    if dtype not in _DTYPES or dtype is torch.float32:
+        raise ValueError(f"keys, values and queries must be bf16 or fp16, got {dtype}")
+    if code is None:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError(f"a cache of {cdtype} has no scales")
+        return dtype, _DTYPES[dtype]
+    if k_scale is None or v_scale is None:
+        raise ValueError(f"a cache of {cdtype} needs k_scale and v_scale")
+    return cdtype, code
+
+
+def _frequencies(t):
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not torch.float64 or t.dim() != 1 or \
+            not t.is_contiguous():
+        raise ValueError("frequencies must be a contiguous 1-D float64 CUDA tensor")
+    return t.data_ptr()
+
+
+def w4a16_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                           length: float = 0.0, low: float = 1.0, high: float = 32.0, device=None):
+    """Radians per position of each rotary pair, f64 [rotary_dim / 2] on the GPU, and the magnitude that goes with them.
+
+    scaling "none", "linear", "base", "ramp" or "wavelength" stretches a
+    context of `length` positions by `factor` (see include/w4a16.h)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}")
+    n = max(rotary_dim // 2, 1)
+    f, magnitude = (ctypes.c_double * n)(), ctypes.c_float()
+    _raise(load_library().w4a16_rope_frequencies(rotary_dim, base, _SCALINGS[scaling], factor, length, low, high, f,
+                                                 ctypes.byref(magnitude)), "w4a16_rope_frequencies")
+    return torch.tensor(list(f), dtype=torch.float64, device=device or "cuda"), magnitude.value
+
+
+def w4a16_rope(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False,
+               magnitude: float = 1.0, out: torch.Tensor | None = None, stream=None,
+               flags: int = FLAG_PDL) -> torch.Tensor:
+    """Rotary positions of x [T, heads, d] (bf16 or fp16; strided views): the
+    first 2 * len(frequencies) columns of each head rotated by positions [T]
+    (int32; negative: the row is skipped) times frequencies (f64), as pairs
+    (i, i + r / 2), or (2 i, 2 i + 1) where interleaved.  out may be x."""
+    dtype = x.dtype
+    if dtype not in _DTYPES or dtype is torch.float32:
+        raise ValueError(f"x must be bf16 or fp16, got {dtype}")
+    shape, (xt, xh, _) = _strided(x, "x", dtype, 3)
+    T, heads, d = shape
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=dtype, device=x.device)
+    oshape, (ot, oh, _) = _strided(out, "out", dtype, 3)
+    if oshape != shape:
+        raise ValueError(f"out has shape {tuple(oshape)}, expected {tuple(shape)}")
+    f = _frequencies(frequencies)
+    args = _ROPE_ARGS.pack(x.data_ptr(), out.data_ptr(), _int32(positions, "positions", T), f, xt, xh, ot, oh, T, heads,
+                           d, 2 * frequencies.numel(), int(interleaved), _DTYPES[dtype], magnitude, flags)
+    _raise(load_library().w4a16_rope(args, _stream(stream, x.get_device())), "w4a16_rope")
+    return out
+
+
 def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
-                   v_cache: torch.Tensor, stream=None, flags: int = FLAG_PDL) -> None:
+                   v_cache: torch.Tensor, stream=None, flags: int = FLAG_PDL, k_scale: torch.Tensor | None = None,
+                   v_scale: torch.Tensor | None = None) -> None:
     """New keys and values [T, heads, head_dim] (bf16 or fp16; strided views
     such as slices of a fused projection's output) into the caches [pages,
     heads, page_size, head_dim] at the slots of slot_map [T] (int32; negative
-    or past the cache: skipped)."""
+    or past the cache: skipped).  Caches of int8 or float8_e4m3fn take them
+    quantised, with a scale for each token and head in k_scale and v_scale
+    [pages, heads, page_size] f32 (see w4a16_kv_store in include/w4a16.h)."""
+    if k_scale is not None or v_scale is not None or k_cache.dtype in _CODES:
+        _kv_store(None, k, v, None, None, slot_map, k_cache, v_cache, None, k_scale, v_scale, False, 1.0, stream, flags)
+        return
     dtype = k.dtype
     shape, (kt, kh, _) = _strided(k, "k", dtype, 3)
     vshape, (vt, vh, _) = _strided(v, "v", dtype, 3)
@@ -552,6 +642,84 @@ def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_c
     _raise(load_library().w4a16_kv_write(args, _stream(stream, k.get_device())), "w4a16_kv_write")
 
 
+def w4a16_rope_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                        frequencies: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, q_out: torch.Tensor | None = None,
+                        k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                        interleaved: bool = False, magnitude: float = 1.0, stream=None, flags: int = FLAG_PDL):
+    """w4a16_rope of q and k and w4a16_kv_write of k and v in one launch.  q
+    [T, q_heads, d] or None; q_out takes the rotated queries and may be q (a
+    new tensor where None).  The rotated keys go to the cache alone.  Tokens
+    with a negative position are skipped.  Returns q_out."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _kv_store(q, k, v, positions, frequencies, slot_map, k_cache, v_cache, q_out, k_scale, v_scale, interleaved,
+              magnitude, stream, flags)
+    return q_out
+
+
+def _kv_store(q, k, v, positions, frequencies, slot_map, k_cache, v_cache, q_out, k_scale, v_scale, interleaved,
+              magnitude, stream, flags):
+    dtype = k.dtype
+    cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
+    shape, (kt, kh, _) = _strided(k, "k", dtype, 3)
+    vshape, (vt, vh, _) = _strided(v, "v", dtype, 3)
+    if vshape != shape:
+        raise ValueError(f"v has shape {tuple(vshape)}, expected {tuple(shape)}")
+    T, heads, d = shape
+    cshape, ks, vs = _caches(k_cache, v_cache, cdtype)
+    pages, ch, page, cd = cshape
+    if ch != heads or cd != d:
+        raise ValueError(f"caches of {ch} heads of {cd} do not take k of {heads} heads of {d}")
+    Hq = qt = qh = ot = oh = 0
+    if q is not None:
+        qshape, (qt, qh, _) = _strided(q, "q", dtype, 3)
+        oshape, (ot, oh, _) = _strided(q_out, "q_out", dtype, 3)
+        Hq = qshape[1]
+        if qshape[0] != T or qshape[2] != d or oshape != qshape:
+            raise ValueError(f"q {tuple(qshape)} and q_out {tuple(oshape)} do not go with k {tuple(shape)}")
+    no = (0, 0, 0)
+    kss, vss = (no, no) if k_scale is None else (_scale(k_scale, "k_scale", cshape), _scale(v_scale, "v_scale", cshape))
+    turn = frequencies is not None
+    args = _STORE_ARGS.pack(q.data_ptr() if Hq else 0, k.data_ptr(), v.data_ptr(), q_out.data_ptr() if Hq else 0,
+                            _int32(positions, "positions", T) if turn else 0, _frequencies(frequencies) if turn else 0,
+                            _int32(slot_map, "slot_map", T), k_cache.data_ptr(), v_cache.data_ptr(),
+                            0 if k_scale is None else k_scale.data_ptr(), 0 if v_scale is None else v_scale.data_ptr(),
+                            qt, qh, ot, oh, kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, Hq, heads, d,
+                            2 * frequencies.numel() if turn else 0, int(interleaved), pages, page, _DTYPES[dtype], code,
+                            magnitude, flags)
+    _raise(load_library().w4a16_kv_store(args, _stream(stream, k.get_device())),
+           "w4a16_rope_kv_write" if turn else "w4a16_kv_write")
+
+
+def w4a16_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_map: torch.Tensor, k: torch.Tensor,
+                  v: torch.Tensor, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                  stream=None, flags: int = FLAG_PDL):
+    """Cached keys and values at the slots of slot_map [T] back into k and v
+    [T, heads, head_dim] (bf16 or fp16): copied from a 16-bit cache, scale
+    times code from an 8-bit one.  Rows of slots that are negative or past the
+    cache stay as they are.  Returns (k, v)."""
+    dtype = k.dtype
+    cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
+    shape, (kt, kh, _) = _strided(k, "k", dtype, 3)
+    vshape, (vt, vh, _) = _strided(v, "v", dtype, 3)
+    if vshape != shape:
+        raise ValueError(f"v has shape {tuple(vshape)}, expected {tuple(shape)}")
+    T, heads, d = shape
+    cshape, ks, vs = _caches(k_cache, v_cache, cdtype)
+    pages, ch, page, cd = cshape
+    if ch != heads or cd != d:
+        raise ValueError(f"caches of {ch} heads of {cd} do not go with k of {heads} heads of {d}")
+    no = (0, 0, 0)
+    kss, vss = (no, no) if k_scale is None else (_scale(k_scale, "k_scale", cshape), _scale(v_scale, "v_scale", cshape))
+    args = _READ_ARGS.pack(k_cache.data_ptr(), v_cache.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+                           0 if v_scale is None else v_scale.data_ptr(), _int32(slot_map, "slot_map", T), k.data_ptr(),
+                           v.data_ptr(), kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, heads, d, pages, page,
+                           _DTYPES[dtype], code, flags)
+    _raise(load_library().w4a16_kv_read(args, _stream(stream, k.get_device())), "w4a16_kv_read")
+    return k, v
+
+
 def w4a16_paged_attention_workspace_bytes(tokens: int, requests: int, q_heads: int, kv_heads: int, head_dim: int,
                                           max_q: int) -> int:
     return int(load_library().w4a16_paged_attention_workspace_bytes(tokens, requests, q_heads, kv_heads, head_dim,
@@ -562,18 +730,41 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                           q_start: torch.Tensor, kv_len: torch.Tensor, max_q: int, window: int = 0,
                           block: bool = False, scale: float | None = None, out: torch.Tensor | None = None,
                           lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
-                          flags: int = FLAG_PDL) -> torch.Tensor:
+                          flags: int = FLAG_PDL, k_scale: torch.Tensor | None = None,
+                          v_scale: torch.Tensor | None = None, tree: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of every request's new tokens over its paged cache (see
     include/w4a16.h): decode, draft blocks, prompt chunks and mixtures of them.
 
     q [T, Hq, d] bf16 or fp16, d 64 or 128; caches [pages, Hkv, page_size, d];
     block_table [B, columns], q_start [B+1], kv_len [B] int32; max_q at least
     every request's number of new tokens.  window = 0: no window.  lse: [T, Hq]
-    f32, filled if given.  Returns out [T, Hq, d]."""
+    f32, filled if given.  Returns out [T, Hq, d].
+
+    8-bit caches (int8, float8_e4m3fn) come with k_scale and v_scale [pages,
+    Hkv, page_size] f32.  tree [T, words] int32: the new tokens of a request are
+    the nodes of a tree, and bit k of row t says whether token t sees node k
+    (itself and its ancestors) beside the positions before the new tokens."""
     dtype = q.dtype
     shape, (qt, qh, _) = _strided(q, "q", dtype, 3)
     T, Hq, d = shape
-    (pages, Hkv, page, cd), (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, dtype)
+    ext = None
+    if k_scale is None and v_scale is None and tree is None:
+        cshape, (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, dtype)
+    else:
+        cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
+        cshape, (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, cdtype)
+        kss = vss = (0, 0, 0)
+        if k_scale is not None:
+            kss, vss = _scale(k_scale, "k_scale", cshape), _scale(v_scale, "v_scale", cshape)
+        words = node = 0
+        if tree is not None:
+            tshape, (node, _) = _strided(tree, "tree", _I32, 2)
+            words = tshape[1]
+            if tshape[0] != T or words == 0:
+                raise ValueError(f"tree has shape {tuple(tshape)}, expected ({T}, words)")
+        ext = _EXT_ARGS.pack(0 if k_scale is None else k_scale.data_ptr(), 0 if v_scale is None else v_scale.data_ptr(),
+                             0 if tree is None else tree.data_ptr(), *kss, *vss, node if T > 1 else words, code, words)
+    pages, Hkv, page, cd = cshape
     if cd != d or dtype not in _DTYPES:
         raise ValueError(f"caches with heads of {cd} do not go with q with heads of {d} in {dtype}")
     B = kv_len.shape[0]
@@ -604,7 +795,10 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                            0 if workspace is None else workspace.numel() * workspace.element_size(), qt, qh, ot, oh,
                            kcp, kch, kcs, vcp, vch, vcs, row, T, B, Hq, Hkv, d, pages, page, columns, max_q, window,
                            int(block), _DTYPES[dtype], 0.0 if scale is None else scale, flags)
-    _raise(lib.w4a16_paged_attention(args, st), "w4a16_paged_attention")
+    if ext is None:
+        _raise(lib.w4a16_paged_attention(args, st), "w4a16_paged_attention")
+    else:
+        _raise(lib.w4a16_paged_attention_ex(args, ext, st), "w4a16_paged_attention")
     return out
 
 

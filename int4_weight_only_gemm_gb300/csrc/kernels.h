@@ -138,7 +138,13 @@ constexpr int kPlanMaxRequests = 16384;
 cudaError_t launch_page_plan(const w4a16_page_plan_args& a, int sms, cudaStream_t s);
 cudaError_t launch_kv_write(const w4a16_kv_write_args& a, int sms, cudaStream_t s);
 size_t paged_attn_workspace(int tokens, int requests, int Hq, int Hkv, int d, int max_q, int sms);
-cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cudaStream_t s);
+// ext: with the defaults filled in where the caller gave none
+cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_paged_attention_ext& x, int sms, cudaStream_t s);
+cudaError_t launch_rope(const w4a16_rope_args& a, int sms, cudaStream_t s);
+void rope_frequencies(int r, double base, int scaling, double factor, double length, double low, double high, double* f,
+                      float* magnitude);
+cudaError_t launch_kv_store(const w4a16_kv_store_args& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_read(const w4a16_kv_read_args& a, cudaStream_t s);
 size_t sample_workspace(int rows, int vocab, bool filters, int sms);
 cudaError_t launch_sample(const w4a16_sample_args& a, int sms, cudaStream_t s);
 int chunk_read_status();

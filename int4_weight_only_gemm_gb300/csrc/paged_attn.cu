@@ -58,8 +58,13 @@ size_t paged_attn_workspace(int, int, int Hq, int Hkv, int d, int max_q, int sms
     return kCounterBytes + paged_decode_part_bytes(d, sms) + (large ? paged_chunk_part_bytes(d, sms) : 0);
 }
 
-cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cudaStream_t s) {
+cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_paged_attention_ext& x, int sms,
+                              cudaStream_t s) {
     PagedAttnParams p;
+    p.k_scale = x.k_scale, p.v_scale = x.v_scale;
+    p.ksp = x.ks_page, p.ksh = x.ks_head, p.kss = x.ks_slot, p.vsp = x.vs_page, p.vsh = x.vs_head, p.vss = x.vs_slot;
+    p.e4m3 = x.cache_dtype == W4A16_E4M3;
+    p.tree = x.tree, p.tree_token = x.tree_token, p.words = x.tree_words;
     p.q = static_cast<const uint16_t*>(a.q);
     p.k = static_cast<const uint16_t*>(a.k_cache);
     p.v = static_cast<const uint16_t*>(a.v_cache);
@@ -81,6 +86,11 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, int sms, cuda
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
     p.scale2 = (a.scale == 0.f ? 1.f / sqrtf((float)a.head_dim) : a.scale) * 1.4426950408889634f;
     const bool pdl = (a.flags & W4A16_FLAG_PDL) != 0, bf16 = a.dtype == W4A16_BF16;
+    if (p.k_scale || p.tree) {
+        const cudaError_t e = launch_paged_simple(p, bf16, a.head_dim, s, pdl);
+        if (e == cudaSuccess) note_launch();
+        return e;
+    }
     // Which of the two kernels can have requests: all with max_q tokens when T = B max_q.
     const bool even = (int64_t)a.requests * a.max_q == a.tokens;
     const bool large = (int64_t)a.max_q * p.G > kSmallRows, small = !large || !even;

@@ -28,6 +28,14 @@ struct PagedAttnParams {
     unsigned* counters;  // arrival counters, zero between calls
     float* part;         // partial results of split work
     float scale2;  // scale * log2(e): scores in the base-2 exponent
+    // 8-bit caches: k and v are their codes, strides count bytes
+    const float *k_scale, *v_scale;
+    int64_t ksp, ksh, kss, vsp, vsh, vss;  // strides of the scales' pages, heads, slots
+    bool e4m3;
+    // a tree of new tokens, or null
+    const uint32_t* tree;
+    int64_t tree_token;
+    int words;
 };
 
 struct Bf16 {
@@ -121,6 +129,8 @@ bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool
 // Tensor map of the queries, (column, head, token), in boxes of 64 columns by
 // the heads of a group by `tokens` tokens, 128-byte swizzle (paged_attn.cu).
 bool query_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, int tokens);
+
+cudaError_t launch_paged_simple(const PagedAttnParams& p, bool bf16, int d, cudaStream_t s, bool pdl);
 
 // requests of up to 16 query rows a key head (paged_decode.cu)
 constexpr int kSmallRows = 16;
