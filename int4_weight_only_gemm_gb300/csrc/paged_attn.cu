@@ -1,6 +1,6 @@
 // Attention of the new tokens over a paged cache: tensor maps, workspace, and
-// which kernel takes a request -- the small-row kernel (paged_decode.cu) up to
-// kSmallRows query rows a key head, the chunk kernel (paged_chunk.cu) above.
+// which kernel takes a request -- the small-row kernel (paged_decode.cuh) up to
+// kSmallRows query rows a key head, the chunk kernel (paged_chunk.cuh) above.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -86,7 +86,7 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_p
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
     p.scale2 = (a.scale == 0.f ? 1.f / sqrtf((float)a.head_dim) : a.scale) * 1.4426950408889634f;
     const bool pdl = (a.flags & W4A16_FLAG_PDL) != 0, bf16 = a.dtype == W4A16_BF16;
-    if (p.k_scale || p.tree) {
+    if (p.k_scale) {
         const cudaError_t e = launch_paged_simple(p, bf16, a.head_dim, s, pdl);
         if (e == cudaSuccess) note_launch();
         return e;
@@ -97,14 +97,17 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_p
     p.small_rows = small ? kSmallRows : 0;
     p.after_small = small;
     if (small) {
-        const cudaError_t e = launch_paged_decode(p, bf16, a.head_dim, sms, s, pdl);
+        const cudaError_t e = p.tree ? launch_paged_decode<true>(p, bf16, a.head_dim, sms, s, pdl)
+                                     : launch_paged_decode<false>(p, bf16, a.head_dim, sms, s, pdl);
         if (e != cudaSuccess) return e;
         note_launch();
     }
     if (!large) return cudaSuccess;
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes + paged_decode_part_bytes(a.head_dim, sms));
     // (behind the small-row kernel always as its dependent: its CTAs take the SMs as those are done)
-    const cudaError_t e = launch_paged_chunk(p, bf16, a.head_dim, (int64_t)a.max_q * p.G <= 128, sms, s, pdl || small);
+    const bool one = (int64_t)a.max_q * p.G <= 128;
+    const cudaError_t e = p.tree ? launch_paged_chunk<true>(p, bf16, a.head_dim, one, sms, s, pdl || small)
+                                 : launch_paged_chunk<false>(p, bf16, a.head_dim, one, sms, s, pdl || small);
     if (e == cudaSuccess) note_launch();
     return e;
 }

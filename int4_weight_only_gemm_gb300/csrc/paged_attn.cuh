@@ -122,6 +122,43 @@ W4A16_DEVICE int first_seen(const PagedAttnParams& p, int e) {
     return p.window > 0 && e >= p.window ? e - p.window + 1 : 0;  // (e may be negative, the window as large as it gets)
 }
 
+// What the tokens of a request see, of a tree's nodes or (TREE false) of the
+// positions up to their own: from `first` on, all of `lo_all` .. `e_all`, none
+// behind `last`.
+struct Seen {
+    int first, lo_all, e_all, last;
+};
+template <bool TREE>
+W4A16_DEVICE Seen seen_by(const PagedAttnParams& p, const Request& r, int i0, int i1) {  // tokens i0 .. i1
+    Seen s;
+    if constexpr (TREE) {
+        const int past = r.L - r.n;
+        s.first = p.window > 0 && past > p.window ? past - p.window : 0;  // (of a node without a bit)
+        s.lo_all = p.window > 0 && r.L > p.window ? r.L - p.window : 0;   // (of one that sees them all)
+        s.e_all = past - 1;
+        s.last = r.L - 1;
+    } else {
+        s.e_all = last_seen(p, r, i0);
+        s.last = last_seen(p, r, i1);
+        s.first = first_seen(p, s.e_all);
+        s.lo_all = first_seen(p, s.last);
+    }
+    return s;
+}
+// Word w of the nodes that token t of a request with n new tokens sees.
+W4A16_DEVICE uint32_t tree_word(const PagedAttnParams& p, int t, int n, int w) {
+    if (w < 0 || w >= p.words || 32 * w >= n) return 0u;
+    const uint32_t x = __ldcg(p.tree + (int64_t)t * p.tree_token + w);
+    return n - 32 * w >= 32 ? x : x & ((1u << (n - 32 * w)) - 1u);
+}
+// The first context position that a token of a tree sees: its place is behind the context by its depth.
+W4A16_DEVICE int tree_first(const PagedAttnParams& p, const Request& r, int t) {
+    if (p.window == 0) return 0;
+    int64_t at = (int64_t)r.L - r.n - p.window;
+    for (int w = 0; w < p.words && 32 * w < r.n; ++w) at += __popc(tree_word(p, t, r.n, w));
+    return at > 0 ? (int)at : 0;
+}
+
 // Tensor map of the key or value cache, (column, slot, head, page), in boxes of
 // 64 columns by `rows` slots, 128-byte swizzle (paged_attn.cu).
 bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool values, int rows);
@@ -132,14 +169,18 @@ bool query_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, int 
 
 cudaError_t launch_paged_simple(const PagedAttnParams& p, bool bf16, int d, cudaStream_t s, bool pdl);
 
-// requests of up to 16 query rows a key head (paged_decode.cu)
+// requests of up to 16 query rows a key head (paged_decode.cuh)
 constexpr int kSmallRows = 16;
 size_t paged_decode_part_bytes(int d, int sms);
+template <bool TREE>
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl);
 
-// the other requests (paged_chunk.cu)
+// the other requests (paged_chunk.cuh)
 size_t paged_chunk_part_bytes(int d, int sms);
 // one: no request has more than 128 rows a key head
+template <bool TREE>
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, bool one, int sms, cudaStream_t s, bool pdl);
+template <bool TREE>
+int paged_chunk_status();
 
 }  // namespace w4a16
