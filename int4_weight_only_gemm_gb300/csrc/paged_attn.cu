@@ -86,23 +86,24 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_p
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
     p.scale2 = (a.scale == 0.f ? 1.f / sqrtf((float)a.head_dim) : a.scale) * 1.4426950408889634f;
     const bool pdl = (a.flags & W4A16_FLAG_PDL) != 0, bf16 = a.dtype == W4A16_BF16;
-    if (p.k_scale) {
-        const cudaError_t e = launch_paged_simple(p, bf16, a.head_dim, s, pdl);
-        if (e == cudaSuccess) note_launch();
-        return e;
-    }
     // Which of the two kernels can have requests: all with max_q tokens when T = B max_q.
     const bool even = (int64_t)a.requests * a.max_q == a.tokens;
     const bool large = (int64_t)a.max_q * p.G > kSmallRows, small = !large || !even;
     p.small_rows = small ? kSmallRows : 0;
     p.after_small = small;
     if (small) {
-        const cudaError_t e = p.tree ? launch_paged_decode<true>(p, bf16, a.head_dim, sms, s, pdl)
-                                     : launch_paged_decode<false>(p, bf16, a.head_dim, sms, s, pdl);
+        auto* launch = p.k_scale ? (p.tree ? launch_paged_decode8<true> : launch_paged_decode8<false>)
+                                 : (p.tree ? launch_paged_decode<true> : launch_paged_decode<false>);
+        const cudaError_t e = launch(p, bf16, a.head_dim, sms, s, pdl);
         if (e != cudaSuccess) return e;
         note_launch();
     }
     if (!large) return cudaSuccess;
+    if (p.k_scale) {
+        const cudaError_t e = launch_paged_simple(p, bf16, a.head_dim, s, pdl);
+        if (e == cudaSuccess) note_launch();
+        return e;
+    }
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes + paged_decode_part_bytes(a.head_dim, sms));
     // (behind the small-row kernel always as its dependent: its CTAs take the SMs as those are done)
     const bool one = (int64_t)a.max_q * p.G <= 128;

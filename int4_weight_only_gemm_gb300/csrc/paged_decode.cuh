@@ -38,14 +38,9 @@
 // a NaN from a position outside its own.
 #pragma once
 
-#include "paged_attn.cuh"
+#include "paged_line.cuh"
 
 namespace w4a16 {
-
-constexpr int kDecWarps = 8;
-constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecTile = 16;                      // keys of a warp's tile
-constexpr int kDecUnit = kDecTile * kDecWarps;    // keys of a unit
 
 template <int D>
 struct Dec {
@@ -59,34 +54,8 @@ struct Dec {
     static constexpr int kMlOff = kMergeOff + kMerge;        // [warp][16][2]
     static constexpr int kMiscOff = kMlOff + kDecWarps * 16 * 2 * 4;
     static constexpr int kSmem = kMiscOff + 128;
-    static constexpr int kPart = 16 * (D + 2);               // floats of a partial result
 };
 static_assert(Dec<128>::kSmem <= 232448 && Dec<64>::kSmem <= 232448, "shared memory");
-// What a pair costs beside its units, in units: the rows' first load, the
-// warps' meeting and the output, of which the copies ahead hide a part.
-constexpr int kDecPair = 2;
-
-// Units of a request for one key head, and its first key (a multiple of 16).
-struct DecSpan {
-    int units, j0;
-};
-template <bool TREE>
-W4A16_DEVICE DecSpan dec_span(const PagedAttnParams& p, const Request& r) {
-    DecSpan s{0, 0};
-    if (r.n == 0 || r.n * p.G > p.small_rows) return s;
-    const Seen see = seen_by<TREE>(p, r, 0, r.n - 1);
-    s.j0 = see.first & ~(kDecTile - 1);
-    const int keys = see.last + 1 - s.j0;
-    s.units = keys > 0 ? (keys + kDecUnit - 1) / kDecUnit : 1;  // no key: one unit that writes zeros
-    return s;
-}
-
-// x / y for 0 <= x and 0 < y: in 32 bits where both fit, a fifth of the time
-W4A16_DEVICE int64_t quotient(int64_t x, int64_t y) {
-    return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
-}
-// CTA that holds place u of the line of U places cut over C CTAs
-W4A16_DEVICE int owner_of(int64_t u, int64_t U, int C) { return (int)quotient((u + 1) * C - 1, U); }
 
 template <typename Ty, int D, bool TREE>
 __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __grid_constant__ PagedAttnParams p) {
@@ -100,64 +69,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     pdl_wait();
     pdl_launch_dependents();  // in this order: the chunk kernel of the same call does not wait for this one to begin
 
-    // ---- this CTA's part of the line ----------------------------------------
-    // A pair (request, key head) takes kDecPair + units places of it.
-    int64_t* warp_sum = reinterpret_cast<int64_t*>(ml);
-    const int per = (p.B + kDecThreads - 1) / kDecThreads;
-    const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
-    Request r{0, 0, 0};
-    DecSpan sp{0, 0};
-    int64_t mine = 0;
-    auto places = [&](int b) {  // of a request, r and sp on the way
-        r = request_of(p, b);
-        sp = dec_span<TREE>(p, r);
-        return sp.units ? (int64_t)(sp.units + kDecPair) * p.Hkv : (int64_t)0;
-    };
-    for (int b = b0; b < b1; ++b) mine += places(b);
-    int64_t before = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += x;
-    }
-    if (lane == 31) warp_sum[warp] = before;
-    __syncthreads();
-    int64_t U = 0;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-        if (w < warp) before += warp_sum[w];
-        U += warp_sum[w];
-    }
-    before -= mine;
-    const int C = (int)(U < gridDim.x ? U : gridDim.x);  // every CTA of the C has a place at least
-    if (c >= C) return;
-    const int64_t u0 = quotient(c * U, C), u1 = quotient((c + 1) * U, C);
-    if (u0 >= before && u0 < before + mine) {
-        int64_t at = before;
-        for (int b = b0; b < b1; ++b) {
-            const int64_t n = per == 1 ? mine : places(b);
-            if (u0 < at + n) {
-                const int len = sp.units + kDecPair;
-                misc[0] = b;
-                const int head = (int)quotient(u0 - at, len);
-                misc[1] = head;
-                misc[2] = (int)(u0 - at - (int64_t)head * len);
-                misc[3] = r.t0;
-                misc[4] = r.n;
-                misc[5] = r.L;
-                misc[6] = sp.units;
-                misc[7] = sp.j0;
-                break;
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
-    int b = misc[0], hk = misc[1];
-    int64_t s0 = u0 - misc[2];  // the pair's first place
-    r = Request{misc[3], misc[4], misc[5]};
-    sp = DecSpan{misc[6], misc[7]};
-    if (u1 <= s0 + kDecPair) return;  // a place before the pair's first unit
+    DecCut cut;
+    if (!dec_cut<TREE>(p, reinterpret_cast<int64_t*>(ml), misc, cut)) return;
+    const int64_t U = cut.U, u0 = cut.u0, u1 = cut.u1;
+    const int C = cut.C;
+    int b = cut.b, hk = cut.hk;
+    int64_t s0 = cut.s0;  // the pair's first place
+    Request r = cut.r;
+    DecSpan sp = cut.sp;
 
     // ---- the warp's ring -------------------------------------------------
     const uint32_t ring = smem_u32(smem) + warp * (L::kSlots * 2 * L::kHalf);
@@ -508,7 +427,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         const int ti = row / p.G, th = done_hk * p.G + row - ti * p.G;  // the row's token and head
         uint16_t* out = p.out + (int64_t)(done.t0 + ti) * p.o_token + (int64_t)th * p.o_head;
         float* lse = p.lse ? p.lse + (int64_t)(done.t0 + ti) * p.Hq + th : nullptr;
-        float* part = p.part + (int64_t)(2 * c + (from_start ? 1 : 0)) * L::kPart;
+        float* part = p.part + (int64_t)(2 * c + (from_start ? 1 : 0)) * kDecPart<D>;
         if (row < R) {
             const float inv = 1.f / S;
             // column tiles n of 8: few -- warp, warp + 8; else warp / 2, warp / 2 + 4, ..
@@ -544,72 +463,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
                     *lse = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
             }
         }
-        if (!whole) {
-            // the pieces of CTAs c0 .. c1; the last to arrive joins them in CTA order
-            const int c0 = owner_of(first, U, C), c1 = owner_of(end - 1, U, C), pieces = c1 - c0 + 1;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                unsigned n;  // releases the CTA's stores, ordered before by the barrier
-                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                             : "=r"(n)
-                             : "l"(p.counters + c0)
-                             : "memory");
-                const int last = n == (unsigned)(pieces - 1);
-                if (last) p.counters[c0] = 0;
-                misc[0] = last;
-            }
-            __syncthreads();
-            if (misc[0]) {
-                // a thread: four columns of a row, kJoin pieces at a time under a running maximum
-                auto piece = [&](int i) { return p.part + (int64_t)(2 * (c0 + i) + (i == 0)) * L::kPart; };
-                constexpr int kJoin = 12;
-                for (int e = threadIdx.x; e < R * (D / 4); e += kDecThreads) {
-                    const int jr = e / (D / 4), col = (e - jr * (D / 4)) * 4;
-                    float jm = -INFINITY, js = 0.f;
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int i0 = 0; i0 < pieces; i0 += kJoin) {
-                        float2 mi[kJoin];
-                        float4 x[kJoin];
-#pragma unroll
-                        for (int i = 0; i < kJoin; ++i) {
-                            mi[i] = make_float2(-INFINITY, 0.f);
-                            if (i0 + i < pieces) {
-                                mi[i] = __ldcg(reinterpret_cast<const float2*>(piece(i0 + i)) + jr);
-                                x[i] = __ldcg(reinterpret_cast<const float4*>(piece(i0 + i) + 32 + jr * D + col));
-                            }
-                        }
-                        float M = jm;
-#pragma unroll
-                        for (int i = 0; i < kJoin; ++i) M = fmaxf(M, mi[i].x);
-                        const float jb = M == -INFINITY ? 0.f : M;
-                        const float g = jm == -INFINITY ? 1.f : exp2_approx(jm - jb);
-                        js *= g;
-                        y.x *= g;
-                        y.y *= g;
-                        y.z *= g;
-                        y.w *= g;
-                        jm = M;
-#pragma unroll
-                        for (int i = 0; i < kJoin; ++i) {
-                            if (mi[i].y == 0.f) continue;  // no piece, or no seen key in it
-                            const float f = exp2_approx(mi[i].x == -INFINITY ? 0.f : mi[i].x - jb);
-                            js = fmaf(mi[i].y, f, js);
-                            y.x = fmaf(x[i].x, f, y.x);
-                            y.y = fmaf(x[i].y, f, y.y);
-                            y.z = fmaf(x[i].z, f, y.z);
-                            y.w = fmaf(x[i].w, f, y.w);
-                        }
-                    }
-                    const int i = jr / p.G, h = done_hk * p.G + jr - i * p.G;
-                    const float inv = 1.f / js;
-                    uint2 v = make_uint2(0u, 0u);
-                    if (js != 0.f) v = make_uint2(Ty::pack(y.x * inv, y.y * inv), Ty::pack(y.z * inv, y.w * inv));
-                    *reinterpret_cast<uint2*>(p.out + (int64_t)(done.t0 + i) * p.o_token + (int64_t)h * p.o_head + col) = v;
-                    if (p.lse && col == 0)
-                        p.lse[(int64_t)(done.t0 + i) * p.Hq + h] = js == 0.f ? -INFINITY : kLn2 * (jm + log2f(js));
-                }
-            }
-        }
+        if (!whole) dec_join<Ty, D>(p, done, done_hk, owner_of(first, U, C), owner_of(end - 1, U, C), misc);
         if (!more) break;
         __syncthreads();  // ml and merge are free again
     }

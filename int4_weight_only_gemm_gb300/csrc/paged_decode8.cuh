@@ -1,0 +1,479 @@
+// Paged attention over an 8-bit cache for few query rows (at most 16 a key head).
+//
+//     s_j = scale log2(e) ks_j (q . kcode_j),  out = sum_j 2^(s_j - m) vs_j vcode_j / sum_j 2^(s_j - m)
+//
+// Bound: HBM, at half the bytes of a 16-bit cache, with the unpacking of the
+// codes close behind: a 16-key tile of 4.2 KB takes ~130 instructions a lane for
+// it.  The line of units and the joining of pieces are paged_line.cuh's.
+//
+// Eight warps work without meeting, each with a ring of its own filled by 16-byte
+// asynchronous copies: codes, and 4 bytes a key and value for their scales.  The
+// products have the keys (and then the columns) as the 16 rows of an MMA and 8
+// query rows as its columns, so that one code in a register is used for all query
+// rows at once; more than 8 query rows take a second column block.
+//
+//   * S^T = K Q^T.  Which columns of a head a step of 16 takes is free as long as
+//     both operands agree: lane q of four takes the 16 codes that one 16-byte
+//     load gives it, four at a step.
+//   * O^T = V^T P^T.  The two keys of an operand register sit in two rows of the
+//     tile; a byte of either row makes a pair without a transposing load, and
+//     which output column a row of the MMA stands for is free again: lane l / 4
+//     owns D / 8 columns that follow each other.
+//
+// A key's scale multiplies its score in f32, a value's its weight, which goes to
+// the product in two bf16 parts (16 bits): codes are exact in bf16 and fp16, and
+// neither a weight nor a scale leaves bf16's range.  A row's maximum moves only
+// when a score passes it by 2^8, so that most tiles need no exchange between lanes.
+#pragma once
+
+#include <type_traits>
+
+#include "codes.cuh"
+#include "paged_line.cuh"
+
+namespace w4a16 {
+
+template <int D>
+struct Dec8 {
+    static constexpr int kHalf = kDecTile * D;                 // bytes of a tile's key codes (and of its value codes)
+    static constexpr int kSlot = 2 * kHalf + 2 * kDecTile * 4;  // and both scales
+    static constexpr int kSlots = D == 128 ? 5 : 10;           // ring slots a warp
+    static constexpr int kRing = kDecWarps * kSlots * kSlot;
+    static constexpr int kStride = D + 4;                      // floats of a row of results
+    static constexpr int kMergeOff = kRing;
+    static constexpr int kMerge = kDecWarps * 8 * kStride * 4;
+    static constexpr int kMlOff = kMergeOff + kMerge;          // [warp][16][2]
+    static constexpr int kMiscOff = kMlOff + kDecWarps * 16 * 2 * 4;
+    static constexpr int kSmem = kMiscOff + 128;
+};
+static_assert(Dec8<128>::kSmem <= 232448 && Dec8<64>::kSmem <= 232448, "shared memory");
+
+// Where a tile's 16-byte piece `chunk` of key `row` lies, so that neither product's loads meet in a bank: four
+// lanes on a row and its neighbour (keys), eight on every other row (values).
+template <int D>
+W4A16_DEVICE uint32_t piece_at(int row, int chunk) {
+    if constexpr (D == 128) return row * 128 + ((chunk ^ (((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) << 4);
+    return (row >> 1) * 128 + (((row ^ (row >> 2)) & 1) << 6) + ((chunk ^ (((row >> 1) & 1) << 1)) << 4);
+}
+W4A16_DEVICE uint32_t transposed(uint32_t x) {  // an 8 x 8 block of 16-bit numbers, two a lane
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+W4A16_DEVICE void cp_async_4_or_zero(uint32_t smem_dst, const void* gsrc, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(there ? 4 : 0) : "memory");
+}
+
+template <typename Ty, int D, bool E4M3, bool TREE>
+__global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __grid_constant__ PagedAttnParams p) {
+    using L = Dec8<D>;
+    constexpr bool BF = Ty::idesc_type == 1;
+    extern __shared__ __align__(128) unsigned char smem[];
+    float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
+    float* ml = reinterpret_cast<float*>(smem + L::kMlOff);
+    volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = (int)blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();  // in this order: the chunk kernel of the same call does not wait for this one to begin
+
+    DecCut cut;
+    if (!dec_cut<TREE>(p, reinterpret_cast<int64_t*>(ml), misc, cut)) return;
+    const int64_t U = cut.U, u0 = cut.u0, u1 = cut.u1;
+    const int C = cut.C;
+    int b = cut.b, hk = cut.hk;
+    int64_t s0 = cut.s0;  // the pair's first place
+    Request r = cut.r;
+    DecSpan sp = cut.sp;
+
+    // ---- the warp's ring -------------------------------------------------
+    const uint32_t ring = smem_u32(smem) + warp * (L::kSlots * L::kSlot);
+    uint32_t gone = 0;             // 2 bits a slot: pages of the tile that are not there
+    const int page = 1 << p.shift, box = page < kDecTile ? page : kDecTile;
+    const int boxes = kDecTile / box;  // 1, or 2 for 8-slot pages
+    constexpr int kRow = D / 16;       // lanes a row
+    const int crow = lane / kRow, cch = lane % kRow;  // this lane's row and 16-byte piece of a copy step
+    int j0, e_last, tile0, tiles;      // of the piece: first key, last key seen, this warp's first tile and their number
+    int off, take;                     // units of the pair before the piece, and in it
+    int ent[2], ent_base;              // table entries of the tiles ent_base + lane
+    auto open_piece = [&] {
+        off = (int)(u0 > s0 + kDecPair ? u0 - s0 - kDecPair : 0);
+        take = (int)(u1 - s0 - kDecPair < sp.units ? u1 - s0 - kDecPair : sp.units) - off;
+        j0 = sp.j0;
+        e_last = seen_by<TREE>(p, r, 0, r.n - 1).last;
+        tile0 = off * kDecWarps + warp;
+        const int all = e_last < j0 ? 0 : (e_last - j0) / kDecTile + 1;  // tiles that hold a seen key
+        const int end = min((off + take) * kDecWarps, all);
+        tiles = tile0 < end ? (end - tile0 + kDecWarps - 1) / kDecWarps : 0;
+    };
+    auto entries = [&](int t) {  // lane i: the pages of tile t + i
+        ent_base = t;
+        ent[0] = ent[1] = -1;
+        if (t + lane < tiles) {
+            const int j = j0 + (tile0 + (t + lane) * kDecWarps) * kDecTile;
+            const int* row = p.table + (int64_t)b * p.table_stride;
+            for (int i = 0; i < boxes; ++i) {
+                const int col = (j + i * box) >> p.shift;
+                if (col < p.columns) ent[i] = row[col];
+            }
+        }
+    };
+    const uint8_t *kcodes = reinterpret_cast<const uint8_t*>(p.k), *vcodes = reinterpret_cast<const uint8_t*>(p.v);
+    auto issue = [&](int t, int slot) {  // the copies of the piece's tile t; a group of copies in any case
+        if (t < tiles) {
+            if (t >= ent_base + 32) entries(t);
+            uint32_t no = 0;
+            const int j = j0 + (tile0 + t * kDecWarps) * kDecTile;
+            const uint32_t dst = ring + slot * L::kSlot;
+            const int skey = lane & 15;  // the key whose scale this lane copies: a key's, or (upper lanes) a value's
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // rows 0 .. 7 and 8 .. 15
+                const int i = boxes == 2 ? h : 0;
+                int pg = __shfl_sync(0xffffffffu, ent[i], t - ent_base);
+                const bool there = pg >= 0 && pg < p.pages;
+                if (!there) {
+                    no |= 1u << i;
+                    pg = 0;
+                }
+                const int slot0 = (j + 8 * h) & (page - 1);
+                const uint8_t* kp = kcodes + pg * p.kp + hk * p.kh + (int64_t)(slot0 + crow) * p.ks + cch * 16;
+                const uint8_t* vp = vcodes + pg * p.vp + hk * p.vh + (int64_t)(slot0 + crow) * p.vs + cch * 16;
+#pragma unroll
+                for (int x = 0; x < 8 * kRow / 32; ++x) {
+                    const uint32_t a = dst + piece_at<D>(8 * h + x * (32 / kRow) + crow, cch);
+                    cp_async_16_or_zero(a, kp + (int64_t)(x * (32 / kRow)) * p.ks, there);
+                    cp_async_16_or_zero(a + L::kHalf, vp + (int64_t)(x * (32 / kRow)) * p.vs, there);
+                }
+                if ((skey >> 3) == h) {
+                    const int64_t sl = slot0 + (skey & 7);
+                    const float* s = lane < 16 ? p.k_scale + pg * p.ksp + hk * p.ksh + sl * p.kss
+                                               : p.v_scale + pg * p.vsp + hk * p.vsh + sl * p.vss;
+                    cp_async_4_or_zero(dst + 2 * L::kHalf + lane * 4, s, there);
+                }
+            }
+            gone = (gone & ~(3u << (2 * slot))) | no << (2 * slot);
+        }
+        cp_async_commit();
+    };
+    // the query rows 8 g + lane / 4 as B fragments: lane q of four has the columns 16 (q + 4 c) .. + 15
+    const int q = lane & 3, n = lane >> 2;
+    uint2 qf[2][D / 16];
+    auto load_q = [&] {
+        const int R = r.n * p.G;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int row = 8 * g + n, i = row / p.G;
+            const uint16_t* at = p.q + (int64_t)(r.t0 + i) * p.q_token + (int64_t)(hk * p.G + row - i * p.G) * p.q_head + 16 * q;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                qf[g][k] = row < R ? *reinterpret_cast<const uint2*>(at + 64 * (k >> 2) + 4 * (k & 3)) : make_uint2(0u, 0u);
+        }
+    };
+
+    open_piece();
+    entries(0);
+    load_q();
+    for (int i = 0; i < L::kSlots; ++i) issue(i, i);
+
+    while (true) {
+        const int R = r.n * p.G;
+        const bool more_rows = R > 8;
+        const Seen see = seen_by<TREE>(p, r, 0, r.n - 1);
+        const int e_min = see.e_all, lo_max = see.lo_all;
+
+        float o[2][D / 16][4];  // [rows 8 g ..][columns 2 t, 2 t + 1 of the lane's][row 2 q, 2 q + 1 of either column]
+        float m[2][2], l[2][2];  // of rows 8 g + 2 q, + 1
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[g][t][i] = 0.f;
+            m[g][0] = m[g][1] = -INFINITY;
+            l[g][0] = l[g][1] = 0.f;
+        }
+
+        int slot = 0;
+        for (int t = 0; t < tiles; ++t) {
+            cp_async_wait<L::kSlots - 1>();
+            __syncwarp();
+            const uint32_t kb = ring + slot * L::kSlot, vb = kb + L::kHalf, sb = vb + L::kHalf;
+            const uint32_t no = (gone >> (2 * slot)) & 3u;
+            const int j = j0 + (tile0 + t * kDecWarps) * kDecTile;
+            // scores: keys n and n + 8 by rows 2 q, 2 q + 1
+            float s[2][4] = {};
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                const uint4 ka = lds_v4(kb + piece_at<D>(n, q + 4 * x)), kc = lds_v4(kb + piece_at<D>(n + 8, q + 4 * x));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a[4] = {code_pair<E4M3, BF, 0, 1>(wa[k], 0u), code_pair<E4M3, BF, 0, 1>(wc[k], 0u),
+                                           code_pair<E4M3, BF, 2, 3>(wa[k], 0u), code_pair<E4M3, BF, 2, 3>(wc[k], 0u)};
+                    mma_16816<Ty>(s[0], a, qf[0][4 * x + k].x, qf[0][4 * x + k].y);
+                    if (more_rows) mma_16816<Ty>(s[1], a, qf[1][4 * x + k].x, qf[1][4 * x + k].y);
+                }
+            }
+            const float ks0 = finite_or_nan(__uint_as_float(lds_u32(sb + 4 * n))) * p.scale2;
+            const float ks1 = finite_or_nan(__uint_as_float(lds_u32(sb + 4 * n + 32))) * p.scale2;
+            const float vs0 = finite_or_nan(__uint_as_float(lds_u32(sb + 4 * n + 64)));
+            const float vs1 = finite_or_nan(__uint_as_float(lds_u32(sb + 4 * n + 96)));
+            const bool edge = j < lo_max || j + kDecTile - 1 > e_min || no;
+            uint32_t hidden = 0;  // bit 4 g + i: s[g][i] is of a position that the row does not see
+            if (edge) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int row = 8 * g + 2 * q + y, tok = row / p.G;
+                        int e = -1, lo = 0;
+                        uint32_t bits = 0u;
+                        if (row < R) {
+                            if constexpr (TREE) {
+                                e = e_min;
+                                lo = tree_first(p, r, r.t0 + tok);
+                                bits = tree_word(p, r.t0 + tok, r.n, 0);
+                            } else {
+                                e = last_seen(p, r, tok);
+                                lo = first_seen(p, e);
+                            }
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int key = n + 8 * x, jj = j + key;
+                            bool sees = jj >= lo && jj <= e;
+                            if constexpr (TREE) {
+                                const uint32_t node = (uint32_t)(jj - e - 1);
+                                if (jj > e) sees = node < 32u && ((bits >> (node & 31u)) & 1u);
+                            }
+                            if (!sees || ((no >> (boxes == 2 ? x : 0)) & 1u)) hidden |= 1u << (4 * g + 2 * x + y);
+                        }
+                    }
+            }
+            bool grew = false;
+            float top[2][2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (g && !more_rows) break;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    s[g][y] = (hidden >> (4 * g + y)) & 1u ? -INFINITY : s[g][y] * ks0;
+                    s[g][2 + y] = (hidden >> (4 * g + 2 + y)) & 1u ? -INFINITY : s[g][2 + y] * ks1;
+                    top[g][y] = fmaxf(s[g][y], s[g][2 + y]);
+                    grew |= top[g][y] > m[g][y] + 8.f;
+                }
+            }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g && !more_rows) break;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float x = top[g][y];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        x = fmaxf(x, m[g][y]);
+                        const float f = x == -INFINITY ? 1.f : exp2_approx(m[g][y] - x);
+                        m[g][y] = x;
+                        l[g][y] *= f;
+#pragma unroll
+                        for (int t2 = 0; t2 < D / 16; ++t2) {
+                            o[g][t2][y] *= f;
+                            o[g][t2][2 + y] *= f;
+                        }
+                    }
+                }
+            }
+            // weights in two bf16 parts, turned into the second product's operand
+            uint32_t ph[2][2], pl[2][2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (g && !more_rows) break;
+                float w[4];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float base = m[g][y] == -INFINITY ? 0.f : m[g][y];
+                    const float a = exp2_approx(s[g][y] - base), d = exp2_approx(s[g][2 + y] - base);
+                    l[g][y] += a + d;
+                    w[y] = (hidden >> (4 * g + y)) & 1u ? 0.f : a * vs0;
+                    w[2 + y] = (hidden >> (4 * g + 2 + y)) & 1u ? 0.f : d * vs1;
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t hi = Bf16::pack(w[2 * x], w[2 * x + 1]);
+                    ph[g][x] = transposed(hi);
+                    pl[g][x] = transposed(Bf16::pack(w[2 * x] - Bf16::lo(hi), w[2 * x + 1] - Bf16::hi(hi)));
+                }
+            }
+            // values: keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9, the lane's D / 8 columns of each
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 2 * q + (i & 1) + 8 * (i >> 1);
+                if constexpr (D == 128) {
+                    const uint4 x = lds_v4(vb + piece_at<D>(row, n));
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                } else {
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                 : "=r"(v[i][0]), "=r"(v[i][1])
+                                 : "r"(vb + piece_at<D>(row, n >> 1) + (n & 1) * 8));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {  // four columns: two tiles of two
+                const uint32_t a0[4] = {code_pair<E4M3, true, 0, 4>(v[0][i], v[1][i]), code_pair<E4M3, true, 1, 5>(v[0][i], v[1][i]),
+                                        code_pair<E4M3, true, 0, 4>(v[2][i], v[3][i]), code_pair<E4M3, true, 1, 5>(v[2][i], v[3][i])};
+                const uint32_t a1[4] = {code_pair<E4M3, true, 2, 6>(v[0][i], v[1][i]), code_pair<E4M3, true, 3, 7>(v[0][i], v[1][i]),
+                                        code_pair<E4M3, true, 2, 6>(v[2][i], v[3][i]), code_pair<E4M3, true, 3, 7>(v[2][i], v[3][i])};
+                mma_16816<Bf16>(o[0][2 * i], a0, ph[0][0], ph[0][1]);
+                mma_16816<Bf16>(o[0][2 * i + 1], a1, ph[0][0], ph[0][1]);
+                mma_16816<Bf16>(o[0][2 * i], a0, pl[0][0], pl[0][1]);
+                mma_16816<Bf16>(o[0][2 * i + 1], a1, pl[0][0], pl[0][1]);
+                if (more_rows) {
+                    mma_16816<Bf16>(o[1][2 * i], a0, ph[1][0], ph[1][1]);
+                    mma_16816<Bf16>(o[1][2 * i + 1], a1, ph[1][0], ph[1][1]);
+                    mma_16816<Bf16>(o[1][2 * i], a0, pl[1][0], pl[1][1]);
+                    mma_16816<Bf16>(o[1][2 * i + 1], a1, pl[1][0], pl[1][1]);
+                }
+            }
+            __syncwarp();  // every lane has read the tile
+            issue(t + L::kSlots, slot);
+            slot = slot + 1 == L::kSlots ? 0 : slot + 1;
+        }
+
+        // ---- the next pair's first copies and rows, before this one's results meet ----
+        const Request done = r;
+        const int done_hk = hk;
+        const int64_t first = s0 + kDecPair, end = first + sp.units;  // the pair's units on the line
+        const bool from_start = off == 0, to_end = off + take == sp.units;
+        const bool more = u1 > end + kDecPair;
+        if (more) {
+            s0 = end;
+            if (++hk == p.Hkv) {
+                hk = 0;
+                do {
+                    r = request_of(p, ++b);
+                    sp = dec_span<TREE>(p, r);
+                } while (sp.units == 0);
+            }
+            open_piece();
+            entries(0);
+            load_q();
+            for (int i = 0; i < L::kSlots; ++i) issue(i, i);
+        }
+
+        // ---- the warps' results ------------------------------------------
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[g][y] += __shfl_xor_sync(0xffffffffu, l[g][y], d);
+                if (n == 0) {
+                    ml[(warp * 16 + 8 * g + 2 * q + y) * 2] = m[g][y];
+                    ml[(warp * 16 + 8 * g + 2 * q + y) * 2 + 1] = l[g][y];
+                }
+            }
+        __syncthreads();
+        // Every warp leaves its rows 0 .. 7 and eight are added; with more rows, warps 4 .. 7 leave all 16 of theirs
+        // and warps 0 .. 3 add to them first.  A row's place: even rows first, so that the lanes' stores do not meet.
+        auto place = [&](int w, int g, int y) {
+            return merge + ((more_rows ? 2 * w + g : w) * 8 + 4 * y + q) * L::kStride + n * (D / 8);
+        };
+        auto leave = [&](int g, int w, bool add) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int row = 8 * g + 2 * q + y;
+                float M = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kDecWarps; ++i) M = fmaxf(M, ml[(i * 16 + row) * 2]);
+                const float f = exp2_approx(m[g][y] - (M == -INFINITY ? 0.f : M));
+                float4* at = reinterpret_cast<float4*>(place(w, g, y));
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    float4 x = make_float4(o[g][2 * i][y], o[g][2 * i][2 + y], o[g][2 * i + 1][y], o[g][2 * i + 1][2 + y]);
+                    const float4 z = add ? at[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x = make_float4(fmaf(x.x, f, z.x), fmaf(x.y, f, z.y), fmaf(x.z, f, z.z), fmaf(x.w, f, z.w));
+                    at[i] = x;
+                }
+            }
+        };
+        if (!more_rows) {
+            leave(0, warp, false);
+        } else {
+            if (warp >= 4) leave(0, warp - 4, false), leave(1, warp - 4, false);
+            __syncthreads();
+            if (warp < 4) leave(0, warp, true), leave(1, warp, true);
+        }
+        __syncthreads();
+        // thread: four columns of a row
+        const bool whole = from_start && to_end;
+        float* part = p.part + (int64_t)(2 * c + (from_start ? 1 : 0)) * kDecPart<D>;
+        for (int e = threadIdx.x; e < R * (D / 4); e += kDecThreads) {
+            const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
+            float M = -INFINITY, S = 0.f;
+#pragma unroll
+            for (int i = 0; i < kDecWarps; ++i) M = fmaxf(M, ml[(i * 16 + row) * 2]);
+            const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int i = 0; i < kDecWarps; ++i) {
+                const float mi = ml[(i * 16 + row) * 2], si = ml[(i * 16 + row) * 2 + 1];
+                if (si != 0.f) S = fmaf(si, exp2_approx(mi == -INFINITY ? 0.f : mi - base), S);
+            }
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int blocks = more_rows ? kDecWarps / 2 : kDecWarps;
+            for (int i = 0; i < blocks; ++i) {
+                const float4 y = *reinterpret_cast<const float4*>(
+                    merge + ((more_rows ? 2 * i + (row >> 3) : i) * 8 + 4 * (row & 1) + ((row & 7) >> 1)) * L::kStride + col);
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+            }
+            const int ti = row / p.G, th = done_hk * p.G + row - ti * p.G;  // the row's token and head
+            if (whole) {
+                const float inv = 1.f / S;
+                *reinterpret_cast<uint2*>(p.out + (int64_t)(done.t0 + ti) * p.o_token + (int64_t)th * p.o_head + col) =
+                    S == 0.f ? make_uint2(0u, 0u) : make_uint2(Ty::pack(x.x * inv, x.y * inv), Ty::pack(x.z * inv, x.w * inv));
+                if (p.lse && col == 0)
+                    p.lse[(int64_t)(done.t0 + ti) * p.Hq + th] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
+            } else {
+                *reinterpret_cast<float4*>(part + 32 + row * D + col) = x;
+                if (col == 0) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(M, S);
+            }
+        }
+        if (!whole) dec_join<Ty, D>(p, done, done_hk, owner_of(first, U, C), owner_of(end - 1, U, C), misc);
+        if (!more) break;
+        __syncthreads();  // ml and merge are free again
+    }
+    cp_async_wait<0>();
+}
+
+template <typename Ty, int D, bool E4M3, bool TREE>
+static cudaError_t launch(const PagedAttnParams& p, int ctas, cudaStream_t s, bool pdl) {
+    static bool set_for[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    auto kernel = paged_decode8_kernel<Ty, D, E4M3, TREE>;
+    if (!set_for[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Dec8<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        set_for[dev] = true;
+    }
+    return launch_kernel(kernel, dim3(ctas), dim3(kDecThreads), (size_t)Dec8<D>::kSmem, s, pdl, p);
+}
+
+template <bool TREE>
+cudaError_t launch_paged_decode8(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl) {
+    auto of = [&](auto ty, auto e4m3) {
+        using Ty = decltype(ty);
+        return d == 128 ? launch<Ty, 128, decltype(e4m3)::value, TREE>(p, sms, s, pdl)
+                        : launch<Ty, 64, decltype(e4m3)::value, TREE>(p, sms, s, pdl);
+    };
+    if (bf16) return p.e4m3 ? of(Bf16{}, std::true_type{}) : of(Bf16{}, std::false_type{});
+    return p.e4m3 ? of(F16{}, std::true_type{}) : of(F16{}, std::false_type{});
+}
+
+}  // namespace w4a16

@@ -18,6 +18,7 @@ __global__ void __launch_bounds__(256) paged_simple_kernel(const __grid_constant
         if (p.q_start[mid] <= t) lo = mid; else hi = mid;
     }
     const Request r = request_of(p, lo);
+    if (r.n * p.G <= p.small_rows) return;
     constexpr int N = D / 32;
     float q[N], o[N] = {};
     const uint16_t* qp = p.q + t * p.q_token + h * p.q_head + lane * N;
