@@ -1,10 +1,10 @@
 // Codes of the 8-bit caches: what a code stands for, in the 16-bit operand types
 // of the tensor cores and in f32.
 //
-// int8: two's complement.  Spread to the low bytes of 16-bit halves, a code's
-// low seven bits over the exponent of 128 are the bf16 number 128 + low, its top
-// bit over the same exponent gives 128 or 256: the difference is the code,
-// exact.  In fp16 a byte over the exponent of 1024 is 1024 + (code + 128).
+// int8: two's complement.  In the low byte of a 16-bit half, a code's low seven
+// bits over the exponent of 128 are the bf16 number 128 + low, its top bit over
+// the same exponent gives 128 or 256: the difference is the code, exact.  In fp16
+// a byte over the exponent of 1024 is 1024 + (code + 128).
 // e4m3: sign and magnitude moved to where the 16-bit type has them, times two to
 // the difference of the exponents' biases; subnormal codes come out right since
 // the product of a subnormal and a power of two is exact.  0x7f and 0xff, which
@@ -26,19 +26,26 @@ W4A16_DEVICE uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Codes LO and HI of the eight of x (0 .. 3) and y (4 .. 7) as a pair, LO in the low half.
-template <bool E4M3, bool BF, int LO, int HI>
-W4A16_DEVICE uint32_t code_pair(uint32_t x, uint32_t y) {
+// The number that int8 codes are laid over, kept in a register: an instruction takes one constant operand, and with
+// both as constants the compiler makes two of each of the ones below (64 more for a 16-key tile).
+template <bool BF>
+W4A16_DEVICE uint32_t code_base() {
+    uint32_t x;
+    if constexpr (BF) asm volatile("mov.b32 %0, 0x43004300;" : "=r"(x));
+    else asm volatile("mov.b32 %0, 0x64806480;" : "=r"(x));
+    return x;
+}
+// The codes in bytes 0 and 2 of w (ODD: 1 and 3) as a pair, the lower byte's in the low half; base: code_base<BF>().
+template <bool E4M3, bool BF, bool ODD>
+W4A16_DEVICE uint32_t code_pair(uint32_t w, uint32_t base) {
     if constexpr (E4M3) {
-        const uint32_t v = __byte_perm(x, y, (LO << 4) | LO | (HI << 12) | (HI << 8));  // each code in both bytes of its half
-        if constexpr (BF) return bf16x2_mul(((v >> 4) & 0x07f007f0u) | (v & 0x80008000u), 0x7b807b80u);  // 2^120
-        return f16x2_mul(((v >> 1) & 0x3f803f80u) | (v & 0x80008000u), 0x5c005c00u);                     // 2^8
-    } else if constexpr (BF) {
-        const uint32_t v = __byte_perm(x, y, (LO << 4) | LO | (HI << 12) | (HI << 8));
-        return bf16x2_sub((v & 0x007f007fu) | 0x43004300u, (v & 0x00800080u) | 0x43004300u);
+        const uint32_t sign = (ODD ? w : w << 8) & 0x80008000u;
+        if constexpr (BF) return bf16x2_mul(((ODD ? w >> 4 : w << 4) & 0x07f007f0u) | sign, 0x7b807b80u);  // 2^120
+        return f16x2_mul(((ODD ? w >> 1 : w << 7) & 0x3f803f80u) | sign, 0x5c005c00u);                     // 2^8
     } else {
-        const uint32_t v = __byte_perm(x, y, (LO << 4) | LO | (HI << 12) | (HI << 8));
-        return f16x2_sub(((v & 0x00ff00ffu) ^ 0x00800080u) | 0x64006400u, 0x64806480u);  // 1024 + 128
+        const uint32_t v = ODD ? w >> 8 : w;
+        if constexpr (BF) return bf16x2_sub((v & 0x007f007fu) | base, (v & 0x00800080u) | base);
+        return f16x2_sub((v & 0x00ff00ffu) ^ base, base);  // (the top bit flipped: + 128)
     }
 }
 
@@ -51,9 +58,7 @@ W4A16_DEVICE float code_value(uint32_t c) {
         return (float)(int8_t)c;
 }
 
-// A scale that is not finite stands for NaN.
-W4A16_DEVICE float finite_or_nan(float s) {
-    return (__float_as_uint(s) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : s;
-}
+// A scale that is not finite stands for NaN (infinity times 0 is one).
+W4A16_DEVICE float finite_or_nan(float s) { return __fmaf_rn(s, 0.f, s); }
 
 }  // namespace w4a16

@@ -92,9 +92,11 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_p
     p.small_rows = small ? kSmallRows : 0;
     p.after_small = small;
     if (small) {
-        auto* launch = p.k_scale ? (p.tree ? launch_paged_decode8<true> : launch_paged_decode8<false>)
-                                 : (p.tree ? launch_paged_decode<true> : launch_paged_decode<false>);
-        const cudaError_t e = launch(p, bf16, a.head_dim, sms, s, pdl);
+        // the most query rows that a request of this kernel can have
+        const int rows = p.G * (a.max_q < kSmallRows / p.G ? a.max_q : kSmallRows / p.G);
+        const cudaError_t e =
+            p.k_scale ? (p.tree ? launch_paged_decode8<true> : launch_paged_decode8<false>)(p, bf16, a.head_dim, rows <= 8, sms, s, pdl)
+                      : (p.tree ? launch_paged_decode<true> : launch_paged_decode<false>)(p, bf16, a.head_dim, sms, s, pdl);
         if (e != cudaSuccess) return e;
         note_launch();
     }

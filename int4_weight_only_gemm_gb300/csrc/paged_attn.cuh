@@ -175,9 +175,9 @@ size_t paged_decode_part_bytes(int d, int sms);
 template <bool TREE>
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl);
 
-// and over an 8-bit cache (paged_decode8.cuh); partial results as there
+// and over an 8-bit cache (paged_decode8.cuh); few: none of these has more than 8; no more partial results than there
 template <bool TREE>
-cudaError_t launch_paged_decode8(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl);
+cudaError_t launch_paged_decode8(const PagedAttnParams& p, bool bf16, int d, bool few, int sms, cudaStream_t s, bool pdl);
 
 // the other requests (paged_chunk.cuh)
 size_t paged_chunk_part_bytes(int d, int sms);

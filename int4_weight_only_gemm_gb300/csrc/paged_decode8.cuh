@@ -33,20 +33,24 @@
 
 namespace w4a16 {
 
-template <int D>
+// NG: 8-row blocks of query rows, 1 or 2.  With one, a thread needs few enough
+// registers for two CTAs an SM.
+template <int D, int NG>
 struct Dec8 {
     static constexpr int kHalf = kDecTile * D;                 // bytes of a tile's key codes (and of its value codes)
     static constexpr int kSlot = 2 * kHalf + 2 * kDecTile * 4;  // and both scales
-    static constexpr int kSlots = D == 128 ? 5 : 10;           // ring slots a warp
+    static constexpr int kSlots = (D == 128 ? 5 : 10) / (3 - NG);  // ring slots a warp
     static constexpr int kRing = kDecWarps * kSlots * kSlot;
     static constexpr int kStride = D + 4;                      // floats of a row of results
     static constexpr int kMergeOff = kRing;
     static constexpr int kMerge = kDecWarps * 8 * kStride * 4;
     static constexpr int kMlOff = kMergeOff + kMerge;          // [warp][16][2]
     static constexpr int kMiscOff = kMlOff + kDecWarps * 16 * 2 * 4;
+    static constexpr int kLineOff = kMiscOff + 64;
     static constexpr int kSmem = kMiscOff + 128;
 };
-static_assert(Dec8<128>::kSmem <= 232448 && Dec8<64>::kSmem <= 232448, "shared memory");
+static_assert(Dec8<128, 2>::kSmem <= 232448 && Dec8<64, 2>::kSmem <= 232448, "shared memory");
+static_assert(2 * (Dec8<128, 1>::kSmem + 1024) <= 233472 && 2 * (Dec8<64, 1>::kSmem + 1024) <= 233472, "two CTAs an SM");
 
 // Where a tile's 16-byte piece `chunk` of key `row` lies, so that neither product's loads meet in a bank: four
 // lanes on a row and its neighbour (keys), eight on every other row (values).
@@ -60,14 +64,18 @@ W4A16_DEVICE uint32_t transposed(uint32_t x) {  // an 8 x 8 block of 16-bit numb
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-W4A16_DEVICE void cp_async_4_or_zero(uint32_t smem_dst, const void* gsrc, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(there ? 4 : 0) : "memory");
+W4A16_DEVICE void copy_16(uint32_t smem_dst, const void* gsrc) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
+}
+W4A16_DEVICE void copy_4(uint32_t smem_dst, const void* gsrc) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_dst), "l"(gsrc) : "memory");
 }
 
-template <typename Ty, int D, bool E4M3, bool TREE>
-__global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __grid_constant__ PagedAttnParams p) {
-    using L = Dec8<D>;
+template <typename Ty, int D, int NG, bool E4M3, bool TREE>
+__global__ void __launch_bounds__(kDecThreads, 3 - NG) paged_decode8_kernel(const __grid_constant__ PagedAttnParams p) {
+    using L = Dec8<D, NG>;
     constexpr bool BF = Ty::idesc_type == 1;
+    const uint32_t vbase = code_base<true>(), kbase = BF ? vbase : code_base<BF>();
     extern __shared__ __align__(128) unsigned char smem[];
     float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
     float* ml = reinterpret_cast<float*>(smem + L::kMlOff);
@@ -79,8 +87,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
 
     DecCut cut;
     if (!dec_cut<TREE>(p, reinterpret_cast<int64_t*>(ml), misc, cut)) return;
-    const int64_t U = cut.U, u0 = cut.u0, u1 = cut.u1;
-    const int C = cut.C;
+    // (the line's numbers wait in shared memory: a piece needs them at its ends alone)
+    volatile int64_t* line = reinterpret_cast<volatile int64_t*>(smem + L::kLineOff);
+    if (threadIdx.x == 0) line[0] = cut.U, line[1] = cut.u0, line[2] = cut.u1, line[3] = cut.C;
+    __syncthreads();
     int b = cut.b, hk = cut.hk;
     int64_t s0 = cut.s0;  // the pair's first place
     Request r = cut.r;
@@ -96,7 +106,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
     int j0, e_last, tile0, tiles;      // of the piece: first key, last key seen, this warp's first tile and their number
     int off, take;                     // units of the pair before the piece, and in it
     int ent[2], ent_base;              // table entries of the tiles ent_base + lane
+    const uint8_t *kmine, *vmine;      // this lane's part of a copy: 16 bytes of rows crow, crow + kStep, ..
+    const float* smine;                // and a scale of key lane % 16: of the key, in the upper lanes of its value
     auto open_piece = [&] {
+        const int64_t u0 = line[1], u1 = line[2];
+        kmine = reinterpret_cast<const uint8_t*>(p.k) + hk * p.kh + crow * p.ks + cch * 16;
+        vmine = reinterpret_cast<const uint8_t*>(p.v) + hk * p.vh + crow * p.vs + cch * 16;
+        const int key = lane & (box - 1);
+        smine = lane < 16 ? p.k_scale + hk * p.ksh + key * p.kss : p.v_scale + hk * p.vsh + key * p.vss;
         off = (int)(u0 > s0 + kDecPair ? u0 - s0 - kDecPair : 0);
         take = (int)(u1 - s0 - kDecPair < sp.units ? u1 - s0 - kDecPair : sp.units) - off;
         j0 = sp.j0;
@@ -118,38 +135,46 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
             }
         }
     };
-    const uint8_t *kcodes = reinterpret_cast<const uint8_t*>(p.k), *vcodes = reinterpret_cast<const uint8_t*>(p.v);
+    constexpr int kStep = 32 / kRow;   // rows of a copy step
+    const uint32_t mine = piece_at<D>(crow, cch);
+    const bool dense = p.ks == D && p.vs == D;
+    const int64_t spage = lane < 16 ? p.ksp : p.vsp, sslot = lane < 16 ? p.kss : p.vss;
     auto issue = [&](int t, int slot) {  // the copies of the piece's tile t; a group of copies in any case
         if (t < tiles) {
             if (t >= ent_base + 32) entries(t);
-            uint32_t no = 0;
-            const int j = j0 + (tile0 + t * kDecWarps) * kDecTile;
+            const int slot0 = (j0 + (tile0 + t * kDecWarps) * kDecTile) & (page - 1);
             const uint32_t dst = ring + slot * L::kSlot;
-            const int skey = lane & 15;  // the key whose scale this lane copies: a key's, or (upper lanes) a value's
+            uint32_t no = 0;
+            // rows 8 h .., all of one page; with the slots of a head behind each other (`dense`) the steps' distance is
+            // a constant.  Of a page that is not there nothing is copied: any codes stand for numbers, and their
+            // weights are zero whatever scales the slot holds.
+            auto rows = [&](int h, int steps, auto dense) {
+                const int pg = __shfl_sync(0xffffffffu, ent[h], t - ent_base);
+                if (pg < 0 || pg >= p.pages) {
+                    no |= 1u << h;
+                    return;
+                }
+                const uint8_t* kp = kmine + (pg * p.kp + slot0 * p.ks);
+                const uint8_t* vp = vmine + (pg * p.vp + slot0 * p.vs);
+                const int64_t kstep = decltype(dense)::value ? kStep * D : kStep * p.ks;
+                const int64_t vstep = decltype(dense)::value ? kStep * D : kStep * p.vs;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // rows 0 .. 7 and 8 .. 15
-                const int i = boxes == 2 ? h : 0;
-                int pg = __shfl_sync(0xffffffffu, ent[i], t - ent_base);
-                const bool there = pg >= 0 && pg < p.pages;
-                if (!there) {
-                    no |= 1u << i;
-                    pg = 0;
+                for (int x = 0; x < 16 / kStep; ++x) {
+                    if (x == steps) break;
+                    // (piece_at of row x kStep on: 512 bytes behind it, and for D = 128 in the other half of its 128)
+                    const uint32_t a = dst + 8 * D * h + x * kStep * D + (D == 128 && (x & 1) ? mine ^ 64u : mine);
+                    copy_16(a, kp + x * kstep);
+                    copy_16(a + L::kHalf, vp + x * vstep);
                 }
-                const int slot0 = (j + 8 * h) & (page - 1);
-                const uint8_t* kp = kcodes + pg * p.kp + hk * p.kh + (int64_t)(slot0 + crow) * p.ks + cch * 16;
-                const uint8_t* vp = vcodes + pg * p.vp + hk * p.vh + (int64_t)(slot0 + crow) * p.vs + cch * 16;
-#pragma unroll
-                for (int x = 0; x < 8 * kRow / 32; ++x) {
-                    const uint32_t a = dst + piece_at<D>(8 * h + x * (32 / kRow) + crow, cch);
-                    cp_async_16_or_zero(a, kp + (int64_t)(x * (32 / kRow)) * p.ks, there);
-                    cp_async_16_or_zero(a + L::kHalf, vp + (int64_t)(x * (32 / kRow)) * p.vs, there);
-                }
-                if ((skey >> 3) == h) {
-                    const int64_t sl = slot0 + (skey & 7);
-                    const float* s = lane < 16 ? p.k_scale + pg * p.ksp + hk * p.ksh + sl * p.kss
-                                               : p.v_scale + pg * p.vsp + hk * p.vsh + sl * p.vss;
-                    cp_async_4_or_zero(dst + 2 * L::kHalf + lane * 4, s, there);
-                }
+                if (steps == 16 / kStep || ((lane >> 3) & 1) == h)
+                    copy_4(dst + 2 * L::kHalf + lane * 4, smine + (pg * spage + slot0 * sslot));
+            };
+            if (boxes == 1) {
+                if (dense) rows(0, 16 / kStep, std::true_type{});
+                else rows(0, 16 / kStep, std::false_type{});
+            } else {  // pages of 8 slots: from slot 0 each
+                rows(0, 8 / kStep, std::false_type{});
+                rows(1, 8 / kStep, std::false_type{});
             }
             gone = (gone & ~(3u << (2 * slot))) | no << (2 * slot);
         }
@@ -157,16 +182,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
     };
     // the query rows 8 g + lane / 4 as B fragments: lane q of four has the columns 16 (q + 4 c) .. + 15
     const int q = lane & 3, n = lane >> 2;
-    uint2 qf[2][D / 16];
+    uint2 qf[NG][D / 16];  // of four columns, the first and the third, then the others: as codes come in pairs
     auto load_q = [&] {
         const int R = r.n * p.G;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < NG; ++g) {
             const int row = 8 * g + n, i = row / p.G;
             const uint16_t* at = p.q + (int64_t)(r.t0 + i) * p.q_token + (int64_t)(hk * p.G + row - i * p.G) * p.q_head + 16 * q;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                qf[g][k] = row < R ? *reinterpret_cast<const uint2*>(at + 64 * (k >> 2) + 4 * (k & 3)) : make_uint2(0u, 0u);
+            for (int k = 0; k < D / 16; ++k) {
+                uint2 x = make_uint2(0u, 0u);
+                if (row < R) x = *reinterpret_cast<const uint2*>(at + 64 * (k >> 2) + 4 * (k & 3));
+                qf[g][k] = make_uint2(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632));
+            }
         }
     };
 
@@ -177,14 +205,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
 
     while (true) {
         const int R = r.n * p.G;
-        const bool more_rows = R > 8;
+        const bool more_rows = NG == 2 && R > 8;
         const Seen see = seen_by<TREE>(p, r, 0, r.n - 1);
         const int e_min = see.e_all, lo_max = see.lo_all;
 
-        float o[2][D / 16][4];  // [rows 8 g ..][columns 2 t, 2 t + 1 of the lane's][row 2 q, 2 q + 1 of either column]
-        float m[2][2], l[2][2];  // of rows 8 g + 2 q, + 1
+        float o[NG][D / 16][4];  // [rows 8 g ..][columns 2 t, 2 t + 1 of the lane's][row 2 q, 2 q + 1 of either column]
+        float m[NG][2], l[NG][2];  // of rows 8 g + 2 q, + 1
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < NG; ++g) {
 #pragma unroll
             for (int t = 0; t < D / 16; ++t)
 #pragma unroll
@@ -201,17 +229,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
             const uint32_t no = (gone >> (2 * slot)) & 3u;
             const int j = j0 + (tile0 + t * kDecWarps) * kDecTile;
             // scores: keys n and n + 8 by rows 2 q, 2 q + 1
-            float s[2][4] = {};
+            float s[NG][4] = {};
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
                 const uint4 ka = lds_v4(kb + piece_at<D>(n, q + 4 * x)), kc = lds_v4(kb + piece_at<D>(n + 8, q + 4 * x));
                 const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t a[4] = {code_pair<E4M3, BF, 0, 1>(wa[k], 0u), code_pair<E4M3, BF, 0, 1>(wc[k], 0u),
-                                           code_pair<E4M3, BF, 2, 3>(wa[k], 0u), code_pair<E4M3, BF, 2, 3>(wc[k], 0u)};
+                    const uint32_t a[4] = {code_pair<E4M3, BF, false>(wa[k], kbase), code_pair<E4M3, BF, false>(wc[k], kbase),
+                                           code_pair<E4M3, BF, true>(wa[k], kbase), code_pair<E4M3, BF, true>(wc[k], kbase)};
                     mma_16816<Ty>(s[0], a, qf[0][4 * x + k].x, qf[0][4 * x + k].y);
-                    if (more_rows) mma_16816<Ty>(s[1], a, qf[1][4 * x + k].x, qf[1][4 * x + k].y);
+                    if (more_rows) mma_16816<Ty>(s[NG - 1], a, qf[NG - 1][4 * x + k].x, qf[NG - 1][4 * x + k].y);
                 }
             }
             const float ks0 = finite_or_nan(__uint_as_float(lds_u32(sb + 4 * n))) * p.scale2;
@@ -219,10 +247,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
             const float vs0 = finite_or_nan(__uint_as_float(lds_u32(sb + 4 * n + 64)));
             const float vs1 = finite_or_nan(__uint_as_float(lds_u32(sb + 4 * n + 96)));
             const bool edge = j < lo_max || j + kDecTile - 1 > e_min || no;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    s[g][y] *= ks0;
+                    s[g][2 + y] *= ks1;
+                }
             uint32_t hidden = 0;  // bit 4 g + i: s[g][i] is of a position that the row does not see
             if (edge) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int row = 8 * g + 2 * q + y, tok = row / p.G;
@@ -246,30 +281,24 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
                                 const uint32_t node = (uint32_t)(jj - e - 1);
                                 if (jj > e) sees = node < 32u && ((bits >> (node & 31u)) & 1u);
                             }
-                            if (!sees || ((no >> (boxes == 2 ? x : 0)) & 1u)) hidden |= 1u << (4 * g + 2 * x + y);
+                            if (!sees || ((no >> (boxes == 2 ? x : 0)) & 1u)) {
+                                hidden |= 1u << (4 * g + 2 * x + y);
+                                s[g][2 * x + y] = -INFINITY;
+                            }
                         }
                     }
             }
             bool grew = false;
-            float top[2][2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (g && !more_rows) break;
+            for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    s[g][y] = (hidden >> (4 * g + y)) & 1u ? -INFINITY : s[g][y] * ks0;
-                    s[g][2 + y] = (hidden >> (4 * g + 2 + y)) & 1u ? -INFINITY : s[g][2 + y] * ks1;
-                    top[g][y] = fmaxf(s[g][y], s[g][2 + y]);
-                    grew |= top[g][y] > m[g][y] + 8.f;
-                }
-            }
+                for (int y = 0; y < 2; ++y) grew |= fmaxf(s[g][y], s[g][2 + y]) > m[g][y] + 8.f;
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (g && !more_rows) break;
+                for (int g = 0; g < NG; ++g) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float x = top[g][y];
+                        float x = fmaxf(s[g][y], s[g][2 + y]);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
                         x = fmaxf(x, m[g][y]);
@@ -285,19 +314,22 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
                 }
             }
             // weights in two bf16 parts, turned into the second product's operand
-            uint32_t ph[2][2], pl[2][2];
+            uint32_t ph[NG][2], pl[NG][2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (g && !more_rows) break;
+            for (int g = 0; g < NG; ++g) {
                 float w[4];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const float base = m[g][y] == -INFINITY ? 0.f : m[g][y];
                     const float a = exp2_approx(s[g][y] - base), d = exp2_approx(s[g][2 + y] - base);
                     l[g][y] += a + d;
-                    w[y] = (hidden >> (4 * g + y)) & 1u ? 0.f : a * vs0;
-                    w[2 + y] = (hidden >> (4 * g + 2 + y)) & 1u ? 0.f : d * vs1;
+                    w[y] = a * vs0;
+                    w[2 + y] = d * vs1;
                 }
+                if (edge)  // (the scale of a position that is not seen may be anything)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((hidden >> (4 * g + i)) & 1u) w[i] = 0.f;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t hi = Bf16::pack(w[2 * x], w[2 * x + 1]);
@@ -321,19 +353,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
             }
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {  // four columns: two tiles of two
-                const uint32_t a0[4] = {code_pair<E4M3, true, 0, 4>(v[0][i], v[1][i]), code_pair<E4M3, true, 1, 5>(v[0][i], v[1][i]),
-                                        code_pair<E4M3, true, 0, 4>(v[2][i], v[3][i]), code_pair<E4M3, true, 1, 5>(v[2][i], v[3][i])};
-                const uint32_t a1[4] = {code_pair<E4M3, true, 2, 6>(v[0][i], v[1][i]), code_pair<E4M3, true, 3, 7>(v[0][i], v[1][i]),
-                                        code_pair<E4M3, true, 2, 6>(v[2][i], v[3][i]), code_pair<E4M3, true, 3, 7>(v[2][i], v[3][i])};
-                mma_16816<Bf16>(o[0][2 * i], a0, ph[0][0], ph[0][1]);
-                mma_16816<Bf16>(o[0][2 * i + 1], a1, ph[0][0], ph[0][1]);
-                mma_16816<Bf16>(o[0][2 * i], a0, pl[0][0], pl[0][1]);
-                mma_16816<Bf16>(o[0][2 * i + 1], a1, pl[0][0], pl[0][1]);
-                if (more_rows) {
-                    mma_16816<Bf16>(o[1][2 * i], a0, ph[1][0], ph[1][1]);
-                    mma_16816<Bf16>(o[1][2 * i + 1], a1, ph[1][0], ph[1][1]);
-                    mma_16816<Bf16>(o[1][2 * i], a0, pl[1][0], pl[1][1]);
-                    mma_16816<Bf16>(o[1][2 * i + 1], a1, pl[1][0], pl[1][1]);
+                uint32_t a[2][4];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t lo = __byte_perm(v[0][i], v[1][i], x ? 0x7632 : 0x5410);
+                    const uint32_t hi = __byte_perm(v[2][i], v[3][i], x ? 0x7632 : 0x5410);
+                    a[x][0] = code_pair<E4M3, true, false>(lo, vbase);
+                    a[x][1] = code_pair<E4M3, true, true>(lo, vbase);
+                    a[x][2] = code_pair<E4M3, true, false>(hi, vbase);
+                    a[x][3] = code_pair<E4M3, true, true>(hi, vbase);
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    if (g && !more_rows) break;
+                    mma_16816<Bf16>(o[g][2 * i], a[0], ph[g][0], ph[g][1]);
+                    mma_16816<Bf16>(o[g][2 * i + 1], a[1], ph[g][0], ph[g][1]);
+                    mma_16816<Bf16>(o[g][2 * i], a[0], pl[g][0], pl[g][1]);
+                    mma_16816<Bf16>(o[g][2 * i + 1], a[1], pl[g][0], pl[g][1]);
                 }
             }
             __syncwarp();  // every lane has read the tile
@@ -346,7 +382,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
         const int done_hk = hk;
         const int64_t first = s0 + kDecPair, end = first + sp.units;  // the pair's units on the line
         const bool from_start = off == 0, to_end = off + take == sp.units;
-        const bool more = u1 > end + kDecPair;
+        const bool more = line[2] > end + kDecPair;
         if (more) {
             s0 = end;
             if (++hk == p.Hkv) {
@@ -364,7 +400,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
 
         // ---- the warps' results ------------------------------------------
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
 #pragma unroll
@@ -401,14 +437,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
         if (!more_rows) {
             leave(0, warp, false);
         } else {
-            if (warp >= 4) leave(0, warp - 4, false), leave(1, warp - 4, false);
+            if (warp >= 4) leave(0, warp - 4, false), leave(NG - 1, warp - 4, false);
             __syncthreads();
-            if (warp < 4) leave(0, warp, true), leave(1, warp, true);
+            if (warp < 4) leave(0, warp, true), leave(NG - 1, warp, true);
         }
         __syncthreads();
         // thread: four columns of a row
         const bool whole = from_start && to_end;
-        float* part = p.part + (int64_t)(2 * c + (from_start ? 1 : 0)) * kDecPart<D>;
+        float* part = p.part + (int64_t)(2 * c + (from_start ? 1 : 0)) * kDecPart<D, 8 * NG>;
         for (int e = threadIdx.x; e < R * (D / 4); e += kDecThreads) {
             const int row = e / (D / 4), col = (e - row * (D / 4)) * 4;
             float M = -INFINITY, S = 0.f;
@@ -438,39 +474,41 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode8_kernel(const __g
                 if (p.lse && col == 0)
                     p.lse[(int64_t)(done.t0 + ti) * p.Hq + th] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
             } else {
-                *reinterpret_cast<float4*>(part + 32 + row * D + col) = x;
+                *reinterpret_cast<float4*>(part + 16 * NG + row * D + col) = x;
                 if (col == 0) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(M, S);
             }
         }
-        if (!whole) dec_join<Ty, D>(p, done, done_hk, owner_of(first, U, C), owner_of(end - 1, U, C), misc);
+        if (!whole) dec_join<Ty, D, 8 * NG>(p, done, done_hk, owner_of(first, line[0], (int)line[3]),
+                                             owner_of(end - 1, line[0], (int)line[3]), misc);
         if (!more) break;
         __syncthreads();  // ml and merge are free again
     }
     cp_async_wait<0>();
 }
 
-template <typename Ty, int D, bool E4M3, bool TREE>
-static cudaError_t launch(const PagedAttnParams& p, int ctas, cudaStream_t s, bool pdl) {
+template <typename Ty, int D, int NG, bool E4M3, bool TREE>
+static cudaError_t launch(const PagedAttnParams& p, int sms, cudaStream_t s, bool pdl) {
     static bool set_for[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = paged_decode8_kernel<Ty, D, E4M3, TREE>;
+    auto kernel = paged_decode8_kernel<Ty, D, NG, E4M3, TREE>;
     if (!set_for[dev]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Dec8<D>::kSmem);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Dec8<D, NG>::kSmem);
         if (e != cudaSuccess) return e;
         set_for[dev] = true;
     }
-    return launch_kernel(kernel, dim3(ctas), dim3(kDecThreads), (size_t)Dec8<D>::kSmem, s, pdl, p);
+    return launch_kernel(kernel, dim3((3 - NG) * sms), dim3(kDecThreads), (size_t)Dec8<D, NG>::kSmem, s, pdl, p);
 }
 
 template <bool TREE>
-cudaError_t launch_paged_decode8(const PagedAttnParams& p, bool bf16, int d, int sms, cudaStream_t s, bool pdl) {
+cudaError_t launch_paged_decode8(const PagedAttnParams& p, bool bf16, int d, bool few, int sms, cudaStream_t s, bool pdl) {
     auto of = [&](auto ty, auto e4m3) {
         using Ty = decltype(ty);
-        return d == 128 ? launch<Ty, 128, decltype(e4m3)::value, TREE>(p, sms, s, pdl)
-                        : launch<Ty, 64, decltype(e4m3)::value, TREE>(p, sms, s, pdl);
+        constexpr bool E = decltype(e4m3)::value;
+        if (few) return d == 128 ? launch<Ty, 128, 1, E, TREE>(p, sms, s, pdl) : launch<Ty, 64, 1, E, TREE>(p, sms, s, pdl);
+        return d == 128 ? launch<Ty, 128, 2, E, TREE>(p, sms, s, pdl) : launch<Ty, 64, 2, E, TREE>(p, sms, s, pdl);
     };
     if (bf16) return p.e4m3 ? of(Bf16{}, std::true_type{}) : of(Bf16{}, std::false_type{});
     return p.e4m3 ? of(F16{}, std::true_type{}) : of(F16{}, std::false_type{});

@@ -3,6 +3,6 @@
 
 namespace w4a16 {
 
-template cudaError_t launch_paged_decode8<true>(const PagedAttnParams&, bool, int, int, cudaStream_t, bool);
+template cudaError_t launch_paged_decode8<true>(const PagedAttnParams&, bool, int, bool, int, cudaStream_t, bool);
 
 }  // namespace w4a16

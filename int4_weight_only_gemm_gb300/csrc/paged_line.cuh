@@ -19,8 +19,8 @@ constexpr int kDecUnit = kDecTile * kDecWarps;    // keys of a unit
 // What a pair costs beside its units, in units: the rows' first load, the
 // warps' meeting and the output, of which the copies ahead hide a part.
 constexpr int kDecPair = 2;
-template <int D>
-constexpr int kDecPart = 16 * (D + 2);            // floats of a partial result: (maximum, sum) of 16 rows, the rows
+template <int D, int ROWS = 16>
+constexpr int kDecPart = ROWS * (D + 2);          // floats of a partial result: (maximum, sum) of its rows, the rows
 
 // Units of a request for one key head, and its first key (a multiple of 16).
 struct DecSpan {
@@ -121,7 +121,7 @@ W4A16_DEVICE bool dec_cut(const PagedAttnParams& p, int64_t* warp_sum, volatile 
 
 // The pieces of a pair that CTAs c0 .. c1 hold; the last to arrive joins them in
 // CTA order.  Every thread of the CTA calls it behind its stores of the piece.
-template <typename Ty, int D>
+template <typename Ty, int D, int ROWS = 16>
 W4A16_DEVICE void dec_join(const PagedAttnParams& p, const Request& done, int done_hk, int c0, int c1, volatile int* misc) {
     const int R = done.n * p.G, pieces = c1 - c0 + 1;
     __syncthreads();
@@ -135,8 +135,8 @@ W4A16_DEVICE void dec_join(const PagedAttnParams& p, const Request& done, int do
     __syncthreads();
     if (!misc[0]) return;
     // a thread: four columns of a row, kJoin pieces at a time under a running maximum
-    auto piece = [&](int i) { return p.part + (int64_t)(2 * (c0 + i) + (i == 0)) * kDecPart<D>; };
-    constexpr int kJoin = 12;
+    auto piece = [&](int i) { return p.part + (int64_t)(2 * (c0 + i) + (i == 0)) * kDecPart<D, ROWS>; };
+    constexpr int kJoin = ROWS == 16 ? 12 : 4;
     for (int e = threadIdx.x; e < R * (D / 4); e += kDecThreads) {
         const int jr = e / (D / 4), col = (e - jr * (D / 4)) * 4;
         float jm = -INFINITY, js = 0.f;
@@ -149,7 +149,7 @@ W4A16_DEVICE void dec_join(const PagedAttnParams& p, const Request& done, int do
                 mi[i] = make_float2(-INFINITY, 0.f);
                 if (i0 + i < pieces) {
                     mi[i] = __ldcg(reinterpret_cast<const float2*>(piece(i0 + i)) + jr);
-                    x[i] = __ldcg(reinterpret_cast<const float4*>(piece(i0 + i) + 32 + jr * D + col));
+                    x[i] = __ldcg(reinterpret_cast<const float4*>(piece(i0 + i) + 2 * ROWS + jr * D + col));
                 }
             }
             float M = jm;
