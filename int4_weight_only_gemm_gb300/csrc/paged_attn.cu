@@ -101,16 +101,12 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_p
         note_launch();
     }
     if (!large) return cudaSuccess;
-    if (p.k_scale) {
-        const cudaError_t e = launch_paged_simple(p, bf16, a.head_dim, s, pdl);
-        if (e == cudaSuccess) note_launch();
-        return e;
-    }
     p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes + paged_decode_part_bytes(a.head_dim, sms));
     // (behind the small-row kernel always as its dependent: its CTAs take the SMs as those are done)
     const bool one = (int64_t)a.max_q * p.G <= 128;
-    const cudaError_t e = p.tree ? launch_paged_chunk<true>(p, bf16, a.head_dim, one, sms, s, pdl || small)
-                                 : launch_paged_chunk<false>(p, bf16, a.head_dim, one, sms, s, pdl || small);
+    auto* launch = p.k_scale ? (p.tree ? launch_paged_chunk<true, true> : launch_paged_chunk<false, true>)
+                             : (p.tree ? launch_paged_chunk<true, false> : launch_paged_chunk<false, false>);
+    const cudaError_t e = launch(p, bf16, a.head_dim, one, sms, s, pdl || small);
     if (e == cudaSuccess) note_launch();
     return e;
 }

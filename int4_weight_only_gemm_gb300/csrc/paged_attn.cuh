@@ -167,8 +167,6 @@ bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool
 // the heads of a group by `tokens` tokens, 128-byte swizzle (paged_attn.cu).
 bool query_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, int tokens);
 
-cudaError_t launch_paged_simple(const PagedAttnParams& p, bool bf16, int d, cudaStream_t s, bool pdl);
-
 // requests of up to 16 query rows a key head (paged_decode.cuh)
 constexpr int kSmallRows = 16;
 size_t paged_decode_part_bytes(int d, int sms);
@@ -182,9 +180,9 @@ cudaError_t launch_paged_decode8(const PagedAttnParams& p, bool bf16, int d, boo
 // the other requests (paged_chunk.cuh)
 size_t paged_chunk_part_bytes(int d, int sms);
 // one: no request has more than 128 rows a key head
-template <bool TREE>
+template <bool TREE, bool Q8>
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, bool one, int sms, cudaStream_t s, bool pdl);
-template <bool TREE>
+template <bool TREE, bool Q8>
 int paged_chunk_status();
 
 }  // namespace w4a16

@@ -53,13 +53,19 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
+#include "codes.cuh"
 #include "paged_attn.cuh"
 
 namespace w4a16 {
 
 static __device__ int g_chunk_status;
 
-constexpr int kChThreads = 352;  // two softmax warpgroups, the MMA warp, the key / value and the query copy warp
+// two softmax warpgroups, the MMA warp, the key / value and the query copy warp; over an 8-bit cache the MMA and the
+// query copy warp have a warpgroup, and four warps bring keys and values
+template <bool Q8>
+constexpr int kChThreads = Q8 ? 512 : 352;
 constexpr int kChKeys = 128;
 constexpr int kChTwo = 256;  // rows that see fewer positions carry their weights in two parts
 constexpr int kChSnap = 2, kChJoin = 12;  // key tiles; see the line
@@ -68,23 +74,36 @@ constexpr int kChCounters = 1024;  // first arrival counter of this kernel (the 
 // ONE: no request has more rows a key head than one row tile (draft blocks);
 // the second tile's place then holds another slot of the ring, and keys come two
 // tiles ahead (16 blocks of 16: 55.3 -> 51.9 us).
-template <int D, bool ONE>
+template <int D, bool ONE, bool Q8 = false>
 struct Ch {
     static constexpr int kSlabs = D / 64;
     static constexpr int kTile = kSlabs * 16384;    // bytes of 128 rows of keys, values or queries
     static constexpr int kRows = ONE ? 1 : 2;       // row tiles of an item
-    static constexpr int kSlots = (D == 128 ? 7 : 12) - kRows;
+    static constexpr int kSlots = (D == 128 ? 7 : 12) - kRows - (Q8 ? 1 : 0);
     static constexpr int kRingOff = kRows * kTile;
     static constexpr int kMlOff = kRingOff + kSlots * kTile;
     static constexpr int kBarOff = kMlOff + 2048;
     static constexpr int kMissOff = kBarOff + 384;            // [8] pages of a tile that are not there
     static constexpr int kMiscOff = kMissOff + 64;
-    static constexpr int kSmem = kMiscOff + 128;               // no static shared memory: the base is 1024-aligned
+    // Q8: scales of eight tiles [tile][keys', values', values' with 0 for what is not finite][128], and 128 ones
+    static constexpr int kScaleOff = kMiscOff + 128;
+    static constexpr int kSmem = kScaleOff + (Q8 ? (8 * 3 + 1) * 512 : 0);  // no static shared memory: the base is 1024-aligned
     static constexpr int kPartHalf = 128 * (D + 2);           // floats of one row tile's partial result
     static constexpr uint32_t kTS = 0, kTO = 256;             // tensor memory: S and P of both tiles, then O
 };
 static_assert(Ch<128, true>::kSmem <= 232448 && Ch<128, false>::kSmem <= 232448, "shared memory");
 static_assert(Ch<64, true>::kSmem <= 232448 && Ch<64, false>::kSmem <= 232448, "shared memory");
+static_assert(Ch<128, true, true>::kSmem <= 232448 && Ch<128, false, true>::kSmem <= 232448, "shared memory");
+static_assert(Ch<64, true, true>::kSmem <= 232448 && Ch<64, false, true>::kSmem <= 232448, "shared memory");
+
+// Over an 8-bit cache the block is launched with 128 registers a thread, 65536 in all; the warpgroups of the copies
+// and MMAs give some to the softmax ones: 2 x 168 + 64 + 112 = 4 x 128.
+constexpr int kChSoftmaxRegs = 168, kChMmaRegs = 64, kChCopyRegs = 112;
+static_assert(2 * kChSoftmaxRegs + kChMmaRegs + kChCopyRegs <= 4 * 128, "registers of the launch");
+template <int N>
+W4A16_DEVICE void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+W4A16_DEVICE void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // ---- instructions ---------------------------------------------------------
 // Operand descriptors (K-major and 128-byte swizzle as smem_desc_sw128 has them;
@@ -158,6 +177,8 @@ W4A16_DEVICE void score_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
         "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(0), "r"(kDescHigh) : "memory");
 }
+// (SPREAD: the weights of 32 keys lie in the 16 first of the columns that their scores had)
+template <bool SPREAD>
 W4A16_DEVICE void pv_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
         "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -166,27 +187,29 @@ W4A16_DEVICE void pv_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, u
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
         "setp.eq.u32 p, 0, 0;\n\t"
         "add.u32 y, %2, 128;\n\tmov.b64 db, {y, %5};\n\t"
-        "add.u32 x, %1, 8;\n\t"
+        "add.u32 x, %1, %6;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
         "add.u32 y, %2, 256;\n\tmov.b64 db, {y, %5};\n\t"
-        "add.u32 x, %1, 16;\n\t"
+        "add.u32 x, %1, %7;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
         "add.u32 y, %2, 384;\n\tmov.b64 db, {y, %5};\n\t"
-        "add.u32 x, %1, 24;\n\t"
+        "add.u32 x, %1, %8;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
         "add.u32 y, %2, 512;\n\tmov.b64 db, {y, %5};\n\t"
-        "add.u32 x, %1, 32;\n\t"
+        "add.u32 x, %1, %9;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
         "add.u32 y, %2, 640;\n\tmov.b64 db, {y, %5};\n\t"
-        "add.u32 x, %1, 40;\n\t"
+        "add.u32 x, %1, %10;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
         "add.u32 y, %2, 768;\n\tmov.b64 db, {y, %5};\n\t"
-        "add.u32 x, %1, 48;\n\t"
+        "add.u32 x, %1, %11;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
         "add.u32 y, %2, 896;\n\tmov.b64 db, {y, %5};\n\t"
-        "add.u32 x, %1, 56;\n\t"
+        "add.u32 x, %1, %12;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t"
-        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh) : "memory");
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh), "n"(8), "n"(SPREAD ? 32 : 16),
+        "n"(SPREAD ? 40 : 24), "n"(SPREAD ? 64 : 32), "n"(SPREAD ? 72 : 40), "n"(SPREAD ? 96 : 48), "n"(SPREAD ? 104 : 56)
+        : "memory");
 }
 template <typename Ty>
 __device__ constexpr uint32_t idesc_ch(int N, bool v) {
@@ -245,6 +268,14 @@ W4A16_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
         "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+W4A16_DEVICE float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
 W4A16_DEVICE float2 add2(float2 a, float2 b) {
@@ -369,11 +400,155 @@ W4A16_DEVICE void add_taken_out(const PagedAttnParams& p, const ChunkPiece& pc, 
     }
 }
 
-template <typename Ty, int D, bool ONE, bool TREE>
-__global__ void __launch_bounds__(kChThreads, 1)
+// ---- keys and values of an 8-bit cache --------------------------------------
+// the type of the product with the values: their codes and weights in bf16, which has f32's range
+template <typename Ty, bool Q8>
+struct PvType {
+    using type = Ty;
+};
+template <typename Ty>
+struct PvType<Ty, true> {
+    using type = Bf16;
+};
+
+// The four copy warps: a thread takes the same 16-code column of every 16th row of
+// a tile (32nd for D = 64) from memory to registers, two ring entries ahead, and
+// puts them into the ring as 16-bit numbers in the layout that tensor copies
+// would give.  Thread i brings the scale of key i.
+template <typename Ty, int D, bool ONE, bool TREE, bool E4M3>
+W4A16_DEVICE void copy_codes(const PagedAttnParams& p, ChunkWalk walk, int toks, unsigned char* smem, uint64_t* full,
+                             uint64_t* empty, volatile uint32_t* miss, float* scales, volatile int* abort_flag,
+                             uint32_t vbase) {
+    using L = Ch<D, ONE, true>;
+    constexpr int NS = L::kSlots, kPieces = D / 16, kStep = 128 / kPieces, N = 128 / kStep;  // threads and steps of a tile
+    constexpr bool BF = Ty::idesc_type == 1;
+    const uint32_t kbase = BF ? vbase : code_base<BF>();
+    const int tid = threadIdx.x & 127, lane = tid & 31, prow = tid / kPieces, pcol = tid % kPieces;
+    const int page = 1 << p.shift, rows = page < kChKeys ? page : kChKeys, sh = p.shift < 7 ? p.shift : 7;
+    const int boxes = kChKeys >> sh;
+    struct Entry {
+        uint4 v[N];
+        float scale[2];     // (of keys and values, with the keys: the softmax needs both before it needs the values)
+        uint32_t no, tile;  // pages that are not there; the CTA's tile number
+        int kv;             // 0 keys, 1 values, -1 nothing
+    };
+    // the next entry to fetch: number i of the piece's 2 take, and the table entries of tile `at` and the one behind
+    ChunkPiece pc;
+    uint32_t i = 0, tile0 = 0, at = 0;
+    int ent[2] = {-2, -2};
+    bool more = true;
+    pc.take = 0;
+    auto entry = [&](int t) {  // lane's box of the piece's tile t (-2: no row sees it)
+        const int j = (pc.it.t0 + pc.off + t) * kChKeys + (lane << sh), col = j >> p.shift;
+        if (t >= pc.take || lane >= boxes || j > pc.it.e1 || j + rows <= pc.it.lo0) return -2;
+        return col < p.columns ? __ldcg(p.table + (int64_t)pc.b * p.table_stride + col) : -1;
+    };
+    auto fetch = [&](Entry& x) {
+        if (i == 2 * (uint32_t)pc.take) {
+            tile0 += pc.take;
+            more = more && walk.next<ONE, TREE>(p, toks, pc);
+            x.kv = -1;
+            if (!more) return;
+            i = at = 0;
+            ent[0] = entry(0);
+            ent[1] = entry(1);
+        }
+        // the order of the ring's entries (keys_at, values_at)
+        const uint32_t n = pc.take;
+        uint32_t t;
+        if (!ONE) t = i >> 1, x.kv = i & 1;
+        else if (i == 0) t = 0, x.kv = 0;
+        else if (i == 2 * n - 1) t = n - 1, x.kv = 1;
+        else if (i & 1) t = (i + 1) >> 1, x.kv = 0;
+        else t = (i >> 1) - 1, x.kv = 1;
+        ++i;
+        const int en = t == at ? ent[0] : ent[1];
+        const bool there = en >= 0 && en < p.pages;
+        x.no = __ballot_sync(0xffffffffu, !there && en != -2);
+        x.tile = tile0 + t;
+        const int j0 = (pc.it.t0 + pc.off + t) * kChKeys, pg = there ? en : -1;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(x.kv ? p.v : p.k) + pc.hk * (x.kv ? p.vh : p.kh) + pcol * 16;
+        const int64_t ps = x.kv ? p.vp : p.kp, ss = x.kv ? p.vs : p.ks;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int row = k * kStep + prow, j = j0 + row;
+            const int g = __shfl_sync(0xffffffffu, pg, row >> sh);
+            x.v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (g >= 0 && j >= pc.it.lo0 && j <= pc.it.e1)
+                x.v[k] = __ldcg(reinterpret_cast<const uint4*>(src + (g * ps + (j & (page - 1)) * ss)));
+        }
+        const int g = __shfl_sync(0xffffffffu, pg, tid >> sh), j = j0 + tid;
+        x.scale[0] = x.scale[1] = 0.f;
+        if (!x.kv && g >= 0 && j >= pc.it.lo0 && j <= pc.it.e1) {
+            const int64_t sl = j & (page - 1);
+            x.scale[0] = __ldcg(p.k_scale + g * p.ksp + pc.hk * p.ksh + sl * p.kss);
+            x.scale[1] = __ldcg(p.v_scale + g * p.vsp + pc.hk * p.vsh + sl * p.vss);
+        }
+        if (x.kv) {  // its table entry is done with
+            at = t + 1;
+            ent[0] = ent[1];
+            ent[1] = entry(t + 2);
+        }
+    };
+    uint32_t e = 0;  // the next ring entry
+    auto store = [&](const Entry& x) {
+        const uint32_t sl = e % NS;
+        if (e >= NS && !mbar_wait_warp(empty + sl, (e / NS - 1) & 1, abort_flag, &g_chunk_status)) return false;
+        const uint32_t dst = smem_u32(smem) + L::kRingOff + sl * L::kTile + (pcol >> 2) * 16384;
+        auto put = [&](auto values) {
+            constexpr bool V = decltype(values)::value, B = V || BF;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int row = k * kStep + prow;
+                const uint32_t w[4] = {x.v[k].x, x.v[k].y, x.v[k].z, x.v[k].w};
+                uint32_t y[8];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)  // bytes 2 h, 2 h + 1 to where code_pair has them
+                        y[2 * c + h] = code_pair<E4M3, B, E4M3>(
+                            __byte_perm(w[c], 0u, E4M3 ? (h ? 0x3424 : 0x1404) : (h ? 0x4342 : 0x4140)), V ? vbase : kbase);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a = dst + row * 128 + ((((pcol & 3) * 2 + h) ^ (row & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[4 * h]), "r"(y[4 * h + 1]),
+                                 "r"(y[4 * h + 2]), "r"(y[4 * h + 3])
+                                 : "memory");
+                }
+            }
+        };
+        if (x.kv) {
+            put(std::true_type{});
+        } else {
+            put(std::false_type{});
+            float* sc = scales + (x.tile & 7) * 384 + tid;
+            const float f = finite_or_nan(x.scale[1]);
+            sc[0] = finite_or_nan(x.scale[0]) * p.scale2;
+            sc[128] = f;
+            sc[256] = fabsf(f) < INFINITY ? f : 0.f;
+            if (tid == 0) miss[x.tile & 7] = x.no;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + sl);
+        ++e;
+        return true;
+    };
+    Entry a, b;
+    fetch(a);
+    fetch(b);
+    while (a.kv >= 0 && store(a)) {
+        fetch(a);
+        if (b.kv < 0 || !store(b)) break;
+        fetch(b);
+    }
+}
+
+template <typename Ty, int D, bool ONE, bool TREE, bool Q8>
+__global__ void __launch_bounds__(kChThreads<Q8>, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedAttnParams p) {
-    using L = Ch<D, ONE>;
+    using L = Ch<D, ONE, Q8>;
     constexpr int NS = L::kSlots;
     extern __shared__ __align__(1024) unsigned char smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
@@ -404,7 +579,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, 1);
+            mbar_init(full + i, Q8 ? 4 : 1);  // (Q8: a lane of each copy warp arrives)
             mbar_init(empty + i, 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -427,9 +602,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
     }
     if (warp == 9 && lane == 0) {
         prefetch_tmap(&tmap_q);
-        prefetch_tmap(&tmap_k);
-        prefetch_tmap(&tmap_v);
+        if constexpr (!Q8) {
+            prefetch_tmap(&tmap_k);
+            prefetch_tmap(&tmap_v);
+        }
     }
+    float* scales = reinterpret_cast<float*>(smem + L::kScaleOff);
+    if constexpr (Q8)
+        if (threadIdx.x < 128) scales[8 * 3 * 128 + threadIdx.x] = 1.f;
     // Behind the small-row kernel of the same call there is nothing to wait for:
     // that kernel let this one start once everything before it was done, and the
     // two have requests, counters and workspace of their own.  What earlier kernels
@@ -443,7 +623,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     // the ring's memory, not yet in use); a thread takes a pair at a time.
     int* warp_sum = reinterpret_cast<int*>(ml);                        // (not in use before the first item's end)
     int64_t* cut = reinterpret_cast<int64_t*>(warp_sum + 16);
-    constexpr int NT = kChThreads;
+    constexpr int NT = kChThreads<Q8>;
     int* start = reinterpret_cast<int*>(smem);
     auto scan = [&](int x, int& total) {  // exclusive sum over the threads
         int y = x;
@@ -579,7 +759,17 @@ __global__ void __launch_bounds__(kChThreads, 1)
     };
 
     ChunkPiece pc;
-    if (warp == 9) {
+    if (Q8 && warp >= 12) {
+        // ------------------------------------------- copies of an 8-bit cache
+        if constexpr (Q8) {
+            fewer_registers<kChCopyRegs>();
+            const uint32_t vbase = code_base<true>();
+            if (p.e4m3) copy_codes<Ty, D, ONE, TREE, true>(p, walk, toks, smem, full, empty, miss, scales, abort_flag, vbase);
+            else copy_codes<Ty, D, ONE, TREE, false>(p, walk, toks, smem, full, empty, miss, scales, abort_flag, vbase);
+        }
+    } else if (warp >= 8) {
+      if constexpr (Q8) fewer_registers<kChMmaRegs>();
+      if (!Q8 && warp == 9) {
         // ---------------------------------------------------------- copies
         const int page = 1 << p.shift, rows = page < kChKeys ? page : kChKeys, boxes = kChKeys / rows;
         uint32_t e = 0, tile0 = 0;  // the next ring entry, and the piece's first tile
@@ -637,7 +827,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // the copies in flight land before the CTA ends
         for (uint32_t i = e > NS ? e - NS : 0; i < e; ++i)
             (void)mbar_wait_warp(full + i % NS, (i / NS) & 1, nullptr, &g_chunk_status);
-    } else if (warp == 10) {
+      } else if (warp == (Q8 ? 9 : 10)) {
         // --------------------------------------------------------- queries
         uint32_t items = 0;
         while (walk.next<ONE, TREE>(p, toks, pc)) {
@@ -653,13 +843,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
             ++items;
         }
         if (items > 0) (void)mbar_wait_warp(q_full, (items - 1) & 1, nullptr, &g_chunk_status);
-    } else if (warp == 8) {
+      } else if (warp == 8) {
         // ------------------------------------------------------------ MMAs
         // The warpgroups in turn: P V of a tile and the scores of the next one
         // go out together.
         // What steers the loop is made uniform, for the descriptors' sake: the chunk
         // above took 206 us with it and 218 without.
-        constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<Ty>(D, true);
+        constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<typename PvType<Ty, Q8>::type>(D, true);
         const uint32_t tm = uniform(tmem), sm = uniform(smem_u32(smem));
         auto tile_at = [&](uint32_t slot, uint32_t kind) {  // a descriptor's low word; tile 0 is Q's first
             return ((sm + slot * (uint32_t)L::kTile) >> 4) | kind;
@@ -668,7 +858,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         bool ok = true;
         while (ok && walk.next<ONE, TREE>(p, toks, pc)) {
             const int take = (int)uniform((uint32_t)pc.take);
-            const bool duo = !ONE && uniform(pc.duo) != 0, two = uniform(pc.two) != 0;
+            const bool duo = !ONE && uniform(pc.duo) != 0, two = uniform(pc.two || (Q8 && Ty::idesc_type == 0)) != 0;
             const int cnt[2] = {duo ? take : (take + 1) / 2, duo ? take : take / 2};
             int scores = cnt[0] + cnt[1];
             auto tile_of = [&](int g, int k) { return (uint32_t)(duo ? k : 2 * k + g); };
@@ -705,8 +895,17 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     ++np[g];
                     tc_fence_after();
                     const uint32_t va = tile_at(L::kRows + sl, kDescV), pa = tm + L::kTS + 128 * g, od = tm + L::kTO + D * g;
-                    pv_block(od, pa, va, id_o, k > 0 ? 1u : 0u);
-                    if (two) pv_block(od, pa + 64, va, id_o, 1u);
+                    if constexpr (Q8) {
+                        if (two) {
+                            pv_block<true>(od, pa, va, id_o, k > 0 ? 1u : 0u);
+                            pv_block<true>(od, pa + 16, va, id_o, 1u);
+                        } else {
+                            pv_block<false>(od, pa, va, id_o, k > 0 ? 1u : 0u);
+                        }
+                    } else {
+                        pv_block<false>(od, pa, va, id_o, k > 0 ? 1u : 0u);
+                        if (two) pv_block<false>(od, pa + 64, va, id_o, 1u);
+                    }
                     if (!duo || g == 1) mma_commit_warp(empty + sl);
                     if (!next) {
                         mma_commit_warp(o_full + g);
@@ -725,15 +924,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         mma_commit_warp(done);
         (void)mbar_wait_warp(done, 0, nullptr, &g_chunk_status);
+      }
     } else {
         // --------------------------------------------------------- softmax
+        if constexpr (Q8) more_registers<kChSoftmaxRegs>();
         const int g = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + L::kTS + 128 * g, to = tmem + lanes + L::kTO + D * g;
         const int tok = row / p.G, hh = row - tok * p.G;
         uint32_t tile0 = 0, items = 0, ns = 0, joins = 0;
         bool ok = true;
+        const float scale2 = Q8 ? 1.f : p.scale2;  // of the scores as they are read (Q8: the keys' scales have it)
         while (ok && walk.next<ONE, TREE>(p, toks, pc)) {
+            const bool two = pc.two || (Q8 && Ty::idesc_type == 0);
             const int base_tok = pc.duo ? g * toks : 0;
             const int mytok = base_tok + tok;  // of the item
             const bool valid = tok < toks && mytok < pc.it.tokens;
@@ -757,9 +960,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t no = miss[(tile0 + t) & 7];
+                // Q8: the tile's scales -- of the scores, and of the weights
+                const float* kc = scales + ((tile0 + t) & 7) * 384;
+                const float* vc = kc + 128;
                 if (j0 < pc.it.lo1 || j0 + kChKeys - 1 > pc.it.e0 || no) {
                     // an edge: scores outside the row's positions become -inf, 32 at a time
                     const int rl = lo - j0, re = e - j0;
+                    bool bad = false;
 #pragma unroll 1
                     for (int x = 0; x < 128; x += 32) {
                         uint32_t seen = re >= x + 31 ? ~0u : re < x ? 0u : (2u << (re - x)) - 1u;
@@ -775,46 +982,59 @@ __global__ void __launch_bounds__(kChThreads, 1)
                             for (int i = 0; i < 32; i += 8)
                                 if ((no >> ((x + i) >> sh)) & 1u) seen &= ~(0xffu << i);
                         }
-                        if (__all_sync(0xffffffffu, seen == ~0u)) continue;
+                        if constexpr (Q8) {
+                            // a row that sees a value without a finite scale takes all scales as they are, and
+                            // becomes NaN; the others take 0 for such scales
+                            if (__ballot_sync(0xffffffffu, !(fabsf(kc[128 + x + lane]) < INFINITY)) & seen) bad = true;
+                        } else if (__all_sync(0xffffffffu, seen == ~0u)) {
+                            continue;
+                        }
                         uint32_t sv[32];
                         tmem_ld32(ts + x, sv);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 32; ++i) {
+                            if constexpr (Q8) sv[i] = __float_as_uint(__uint_as_float(sv[i]) * kc[x + i]);
                             if (!((seen >> i) & 1u)) sv[i] = 0xff800000u;
+                        }
                         tmem_st32(ts + x, sv);
                     }
                     tmem_wait_st();
-                    // values: a thread looks at one key's
-                    const int j = j0 + row;
-                    const bool none = j < pc.it.lo0 || j > pc.it.e1;  // seen by no row of the item
-                    const bool some = !none && (j < pc.it.lo1 || j > pc.it.e0);
-                    const uint32_t en = 2 * tile0 + values_at<ONE>(t, pc.take), sl = en % NS;
-                    ok = mbar_wait_warp(full + sl, (en / NS) & 1, abort_flag, &g_chunk_status);
-                    if (!ok) break;
-                    if (none || some) {
-                        const uint32_t va = smem_u32(smem + L::kRingOff + sl * L::kTile) + row * 128;
+                    if constexpr (Q8) {
+                        kc = scales + 8 * 384;  // (scaled by now)
+                        if (!bad) vc += 128;
+                    } else {
+                        // values: a thread looks at one key's
+                        const int j = j0 + row;
+                        const bool none = j < pc.it.lo0 || j > pc.it.e1;  // seen by no row of the item
+                        const bool some = !none && (j < pc.it.lo1 || j > pc.it.e0);
+                        const uint32_t en = 2 * tile0 + values_at<ONE>(t, pc.take), sl = en % NS;
+                        ok = mbar_wait_warp(full + sl, (en / NS) & 1, abort_flag, &g_chunk_status);
+                        if (!ok) break;
+                        if (none || some) {
+                            const uint32_t va = smem_u32(smem + L::kRingOff + sl * L::kTile) + row * 128;
 #pragma unroll 4
-                        for (int x = 0; x < 8 * L::kSlabs; ++x) {
-                            const uint32_t a = va + (x >> 3) * 16384 + (((x & 7) ^ (row & 7)) << 4);
-                            if (none) {
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
-                            } else {
-                                // (a half whose exponent is all ones has its top bit set after the addition)
-                                const uint4 v = lds_v4(a);
-                                if ((Ty::all_ones(v.x) | Ty::all_ones(v.y) | Ty::all_ones(v.z) | Ty::all_ones(v.w)) &
-                                    0x80008000u) {
-                                    *taken_out = (int)items + 1;
-                                    __threadfence_block();
-                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
-                                                 "r"(finite<Ty>(v.x)), "r"(finite<Ty>(v.y)), "r"(finite<Ty>(v.z)),
-                                                 "r"(finite<Ty>(v.w))
-                                                 : "memory");
+                            for (int x = 0; x < 8 * L::kSlabs; ++x) {
+                                const uint32_t a = va + (x >> 3) * 16384 + (((x & 7) ^ (row & 7)) << 4);
+                                if (none) {
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+                                } else {
+                                    // (a half whose exponent is all ones has its top bit set after the addition)
+                                    const uint4 v = lds_v4(a);
+                                    if ((Ty::all_ones(v.x) | Ty::all_ones(v.y) | Ty::all_ones(v.z) | Ty::all_ones(v.w)) &
+                                        0x80008000u) {
+                                        *taken_out = (int)items + 1;
+                                        __threadfence_block();
+                                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
+                                                     "r"(finite<Ty>(v.x)), "r"(finite<Ty>(v.y)), "r"(finite<Ty>(v.z)),
+                                                     "r"(finite<Ty>(v.w))
+                                                     : "memory");
+                                    }
                                 }
                             }
                         }
-                    }
                     fence_proxy_async_smem();
+                    }
                 }
                 // the row's maximum, 32 scores at a time and the next 32 on their way
                 uint32_t sv[2][32];
@@ -826,14 +1046,21 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        mx = max3(mx, __uint_as_float(sv[x & 1][i]), __uint_as_float(sv[x & 1][i + 1]));
-                        mo = max3(mo, __uint_as_float(sv[x & 1][i + 2]), __uint_as_float(sv[x & 1][i + 3]));
+                        float2 a = make_float2(__uint_as_float(sv[x & 1][i]), __uint_as_float(sv[x & 1][i + 1]));
+                        float2 b = make_float2(__uint_as_float(sv[x & 1][i + 2]), __uint_as_float(sv[x & 1][i + 3]));
+                        if constexpr (Q8) {
+                            const float4 c = *reinterpret_cast<const float4*>(kc + 32 * x + i);
+                            a = mul2(a, make_float2(c.x, c.y));
+                            b = mul2(b, make_float2(c.z, c.w));
+                        }
+                        mx = max3(mx, a.x, a.y);
+                        mo = max3(mo, b.x, b.y);
                     }
                 }
                 mx = fmaxf(mx, mo);
-                const bool grew = (mx - m) * p.scale2 > 8.f;  // also from -inf
+                const bool grew = (mx - m) * scale2 > 8.f;  // also from -inf
                 if (__any_sync(0xffffffffu, grew)) {
-                    const float f = mx == -INFINITY ? 1.f : exp2_approx((m - mx) * p.scale2);
+                    const float f = mx == -INFINITY ? 1.f : exp2_approx((m - mx) * scale2);
                     l *= f;
                     m = mx;
                     if (k > 0) {
@@ -850,10 +1077,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : m * p.scale2;
+                const float base = m == -INFINITY ? 0.f : m * scale2;
                 // weights: scores 32 x .. become the 16 columns 16 x .., over scores read before
                 float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-                const float2 sc = make_float2(p.scale2, p.scale2), nb = make_float2(-base, -base);
+                const float2 sc = make_float2(scale2, scale2), nb = make_float2(-base, -base);
                 auto weights = [&](const uint32_t* v, uint32_t* pk) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -866,8 +1093,57 @@ __global__ void __launch_bounds__(kChThreads, 1)
                         pk[i] = Ty::pack(a.x, a.y);
                     }
                 };
+                if constexpr (Q8) {
+                    // weights times their values' scales, in bf16 (one or two parts over the columns of their scores)
+                    auto scaled = [&](const uint32_t* v, int x, uint32_t* hi, uint32_t* lo) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float4 c = *reinterpret_cast<const float4*>(kc + 32 * x + 2 * i);
+                            const float4 d = *reinterpret_cast<const float4*>(vc + 32 * x + 2 * i);
+                            float2 a = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                            float2 b = make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3]));
+                            a = fma2(a, make_float2(c.x, c.y), nb);
+                            b = fma2(b, make_float2(c.z, c.w), nb);
+                            a.x = exp2_approx(a.x);
+                            a.y = exp2_approx(a.y);
+                            b.x = exp2_approx(b.x);
+                            b.y = exp2_approx(b.y);
+                            l0 = add2(l0, a);
+                            l1 = add2(l1, b);
+                            a = mul2(a, make_float2(d.x, d.y));
+                            b = mul2(b, make_float2(d.z, d.w));
+                            hi[i] = Bf16::pack(a.x, a.y);
+                            hi[i + 1] = Bf16::pack(b.x, b.y);
+                            if (lo) {
+                                lo[i] = Bf16::pack(a.x - Bf16::lo(hi[i]), a.y - Bf16::hi(hi[i]));
+                                lo[i + 1] = Bf16::pack(b.x - Bf16::lo(hi[i + 1]), b.y - Bf16::hi(hi[i + 1]));
+                            }
+                        }
+                    };
+                    tmem_ld32(ts, sv[0]);
+                    if (!two) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            tmem_wait_ld();
+                            if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
+                            uint32_t hi[16];
+                            scaled(sv[x & 1], x, hi, nullptr);
+                            tmem_st16(ts + 16 * x, hi);
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            tmem_wait_ld();
+                            if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
+                            uint32_t hi[16], lo[16];
+                            scaled(sv[x & 1], x, hi, lo);
+                            tmem_st16(ts + 32 * x, hi);
+                            tmem_st16(ts + 32 * x + 16, lo);
+                        }
+                    }
+                } else {
                 tmem_ld32(ts, sv[0]);
-                if (!pc.two) {
+                if (!two) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         tmem_wait_ld();
@@ -885,8 +1161,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
                         weights(sv[x & 1], pk[x]);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float a = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i]), p.scale2, -base));
-                            const float b = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i + 1]), p.scale2, -base));
+                            const float a = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i]), scale2, -base));
+                            const float b = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i + 1]), scale2, -base));
                             pl[x][i] = Ty::pack(a - Ty::lo(pk[x][i]), b - Ty::hi(pk[x][i]));
                         }
                         if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
@@ -896,6 +1172,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                         tmem_st16(ts + 16 * x, pk[x]);
                         tmem_st16(ts + 64 + 16 * x, pl[x]);
                     }
+                }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -928,8 +1205,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 l = a.y;
                 if (other) {
                     const float M = fmaxf(m, o.x), b = M == -INFINITY ? 0.f : M;
-                    f0 = exp2_approx((m - b) * p.scale2);
-                    f1 = exp2_approx((o.x - b) * p.scale2);
+                    f0 = exp2_approx((m - b) * scale2);
+                    f1 = exp2_approx((o.x - b) * scale2);
                     // a sum that is not a number stays one
                     l = (l == 0.f ? 0.f : l * (m == -INFINITY ? 1.f : f0)) +
                         (o.y == 0.f ? 0.f : o.y * (o.x == -INFINITY ? 1.f : f1));
@@ -954,7 +1231,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             }
             auto piece = [&](int i) { return p.part + ((int64_t)(2 * i + (i == c0)) * 2 + g) * L::kPartHalf; };
             // a piece's sums (>= 0, or NaN) carry in their sign whether values were taken out
-            const float mine_m = m * p.scale2, mine_l = __uint_as_float(__float_as_uint(l) | (odd ? 0x80000000u : 0u));
+            const float mine_m = m * scale2, mine_l = __uint_as_float(__float_as_uint(l) | (odd ? 0x80000000u : 0u));
             // Where all other pieces are there already, this one need not be written:
             // it goes into the sum from tensor memory, in its place of the order.
             bool last = whole, kept = true;  // kept: this piece's output is still in tensor memory only
@@ -1003,7 +1280,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             bool again = odd;  // values to add
             float S = l;
             if (last) {
-                float M = m * p.scale2;
+                float M = m * scale2;
                 if (!whole) {
                     M = -INFINITY;
                     bool bad = false;
@@ -1092,7 +1369,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 mbar_arrive(o_free + g);
                 mbar_arrive(o_free + (pc.duo ? g : 1 - g));
             }
-            if (again && last && valid && S != 0.f) add_taken_out<Ty, TREE>(p, pc, my_t, lo, e, out, x0, x1);
+            if constexpr (!Q8)
+                if (again && last && valid && S != 0.f) add_taken_out<Ty, TREE>(p, pc, my_t, lo, e, out, x0, x1);
             tile0 += pc.take;
             ++items;
         }
@@ -1107,7 +1385,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     if (p.after_small) pdl_wait();  // the call is done when both kernels are
 }
 
-template <typename Ty, int D, bool ONE, bool TREE>
+template <typename Ty, int D, bool ONE, bool TREE, bool Q8>
 static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnParams& p,
                           int ctas, cudaStream_t s, bool pdl) {
     static bool set_for[64];
@@ -1115,36 +1393,38 @@ static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CU
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    auto kernel = paged_chunk_kernel<Ty, D, ONE, TREE>;
+    auto kernel = paged_chunk_kernel<Ty, D, ONE, TREE, Q8>;
+    constexpr int smem = Ch<D, ONE, Q8>::kSmem;
     if (!set_for[dev]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ch<D, ONE>::kSmem);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         set_for[dev] = true;
     }
-    return launch_kernel(kernel, dim3(ctas), dim3(kChThreads), (size_t)Ch<D, ONE>::kSmem, s, pdl, tq, tk, tv, p);
+    return launch_kernel(kernel, dim3(ctas), dim3(kChThreads<Q8>), (size_t)smem, s, pdl, tq, tk, tv, p);
 }
 
-template <typename Ty, int D, bool TREE>
+template <typename Ty, int D, bool TREE, bool Q8>
 static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnParams& p,
                           bool one, int ctas, cudaStream_t s, bool pdl) {
-    return one ? launch<Ty, D, true, TREE>(tq, tk, tv, p, ctas, s, pdl) : launch<Ty, D, false, TREE>(tq, tk, tv, p, ctas, s, pdl);
+    return one ? launch<Ty, D, true, TREE, Q8>(tq, tk, tv, p, ctas, s, pdl)
+               : launch<Ty, D, false, TREE, Q8>(tq, tk, tv, p, ctas, s, pdl);
 }
 
-template <bool TREE>
+template <bool TREE, bool Q8>
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, bool one, int sms, cudaStream_t s, bool pdl) {
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk = {}, tv = {};
     const int box = (1 << p.shift) < kChKeys ? 1 << p.shift : kChKeys;
-    if (!paged_tmap(&tk, p, bf16, d, false, box) || !paged_tmap(&tv, p, bf16, d, true, box) ||
-        !query_tmap(&tq, p, bf16, d, 128 / p.G))
+    if (!Q8 && (!paged_tmap(&tk, p, bf16, d, false, box) || !paged_tmap(&tv, p, bf16, d, true, box)))
         return cudaErrorInvalidValue;
+    if (!query_tmap(&tq, p, bf16, d, 128 / p.G)) return cudaErrorInvalidValue;
     if (bf16)
-        return d == 128 ? launch<Bf16, 128, TREE>(tq, tk, tv, p, one, sms, s, pdl)
-                        : launch<Bf16, 64, TREE>(tq, tk, tv, p, one, sms, s, pdl);
-    return d == 128 ? launch<F16, 128, TREE>(tq, tk, tv, p, one, sms, s, pdl)
-                    : launch<F16, 64, TREE>(tq, tk, tv, p, one, sms, s, pdl);
+        return d == 128 ? launch<Bf16, 128, TREE, Q8>(tq, tk, tv, p, one, sms, s, pdl)
+                        : launch<Bf16, 64, TREE, Q8>(tq, tk, tv, p, one, sms, s, pdl);
+    return d == 128 ? launch<F16, 128, TREE, Q8>(tq, tk, tv, p, one, sms, s, pdl)
+                    : launch<F16, 64, TREE, Q8>(tq, tk, tv, p, one, sms, s, pdl);
 }
 
-template <bool TREE>
+template <bool TREE, bool Q8>
 int paged_chunk_status() {
     int v = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&v, g_chunk_status, sizeof(int)) != cudaSuccess) return W4A16_ECUDA;

@@ -3,7 +3,7 @@
 
 namespace w4a16 {
 
-template cudaError_t launch_paged_chunk<true>(const PagedAttnParams&, bool, int, bool, int, cudaStream_t, bool);
-template int paged_chunk_status<true>();
+template cudaError_t launch_paged_chunk<true, false>(const PagedAttnParams&, bool, int, bool, int, cudaStream_t, bool);
+template int paged_chunk_status<true, false>();
 
 }  // namespace w4a16
