@@ -21,20 +21,24 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool values, int rows) {
+bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, bool codes, int d, bool values, int rows) {
     auto encode = encoder();
     if (!encode) return false;
     const uint64_t page = 1ull << p.shift;
     // a dimension of one entry takes any stride: the row's, so that it is a valid one
-    const uint64_t ss = (uint64_t)(values ? p.vs : p.ks) * 2;
-    const uint64_t hs = p.Hkv == 1 ? ss : (uint64_t)(values ? p.vh : p.kh) * 2;
-    const uint64_t ps = p.pages == 1 ? ss : (uint64_t)(values ? p.vp : p.kp) * 2;
+    const int size = codes ? 1 : 2;
+    const uint64_t ss = (uint64_t)(values ? p.vs : p.ks) * size;
+    const uint64_t hs = p.Hkv == 1 ? ss : (uint64_t)(values ? p.vh : p.kh) * size;
+    const uint64_t ps = p.pages == 1 ? ss : (uint64_t)(values ? p.vp : p.kp) * size;
     const cuuint64_t dims[4] = {(cuuint64_t)d, page, (cuuint64_t)p.Hkv, (cuuint64_t)p.pages};
     const cuuint64_t strides[3] = {ss, hs, ps};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
-    return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  const_cast<uint16_t*>(values ? p.v : p.k), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint32_t box[4] = {(cuuint32_t)(codes ? d : 64), (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return encode(m,
+                  codes  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                  : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  4, const_cast<uint16_t*>(values ? p.v : p.k), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

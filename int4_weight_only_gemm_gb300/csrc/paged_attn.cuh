@@ -160,8 +160,9 @@ W4A16_DEVICE int tree_first(const PagedAttnParams& p, const Request& r, int t) {
 }
 
 // Tensor map of the key or value cache, (column, slot, head, page), in boxes of
-// 64 columns by `rows` slots, 128-byte swizzle (paged_attn.cu).
-bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, int d, bool values, int rows);
+// 64 columns by `rows` slots, 128-byte swizzle; of 8-bit codes in boxes of d
+// columns without one (paged_attn.cu).
+bool paged_tmap(CUtensorMap* m, const PagedAttnParams& p, bool bf16, bool codes, int d, bool values, int rows);
 
 // Tensor map of the queries, (column, head, token), in boxes of 64 columns by
 // the heads of a group by `tokens` tokens, 128-byte swizzle (paged_attn.cu).

@@ -62,8 +62,8 @@ namespace w4a16 {
 
 static __device__ int g_chunk_status;
 
-// two softmax warpgroups, the MMA warp, the key / value and the query copy warp; over an 8-bit cache the MMA and the
-// query copy warp have a warpgroup, and four warps bring keys and values
+// two softmax warpgroups, the MMA warp, the key / value and the query copy warp; over an 8-bit cache these three have a
+// warpgroup (and a warp that idles), and four more warps unpack codes
 template <bool Q8>
 constexpr int kChThreads = Q8 ? 512 : 352;
 constexpr int kChKeys = 128;
@@ -96,10 +96,10 @@ static_assert(Ch<64, true>::kSmem <= 232448 && Ch<64, false>::kSmem <= 232448, "
 static_assert(Ch<128, true, true>::kSmem <= 232448 && Ch<128, false, true>::kSmem <= 232448, "shared memory");
 static_assert(Ch<64, true, true>::kSmem <= 232448 && Ch<64, false, true>::kSmem <= 232448, "shared memory");
 
-// Over an 8-bit cache the block is launched with 128 registers a thread, 65536 in all; the warpgroups of the copies
-// and MMAs give some to the softmax ones: 2 x 168 + 64 + 112 = 4 x 128.
-constexpr int kChSoftmaxRegs = 168, kChMmaRegs = 64, kChCopyRegs = 112;
-static_assert(2 * kChSoftmaxRegs + kChMmaRegs + kChCopyRegs <= 4 * 128, "registers of the launch");
+// Over an 8-bit cache the block is launched with 128 registers a thread, 65536 in all; the two other warpgroups give
+// some to the softmax ones: 2 x 168 + 64 + 112 = 4 x 128.
+constexpr int kChSoftmaxRegs = 168, kChMmaRegs = 64, kChUnpackRegs = 112;
+static_assert(2 * kChSoftmaxRegs + kChMmaRegs + kChUnpackRegs <= 4 * 128, "registers of the launch");
 template <int N>
 W4A16_DEVICE void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -400,6 +400,11 @@ W4A16_DEVICE void add_taken_out(const PagedAttnParams& p, const ChunkPiece& pc, 
     }
 }
 
+// One of the barrier's arrivals, once this thread's asynchronous copies are done.
+W4A16_DEVICE void arrive_behind_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // ---- keys and values of an 8-bit cache --------------------------------------
 // the type of the product with the values: their codes and weights in bf16, which has f32's range
 template <typename Ty, bool Q8>
@@ -411,136 +416,70 @@ struct PvType<Ty, true> {
     using type = Bf16;
 };
 
-// The four copy warps: a thread takes the same 16-code column of every 16th row of
-// a tile (32nd for D = 64) from memory to registers, two ring entries ahead, and
-// puts them into the ring as 16-bit numbers in the layout that tensor copies
-// would give.  Thread i brings the scale of key i.
+// The four unpacking warps.  A tile's codes lie in the upper half of its ring slot:
+// a thread takes the same 16-code column of every 16th row (32nd for D = 64) into
+// registers and, once all have, puts them back over the whole slot as 16-bit
+// numbers in the layout that tensor copies of such would give.  Thread i turns the
+// scales of key i into what the softmax takes.
 template <typename Ty, int D, bool ONE, bool TREE, bool E4M3>
-W4A16_DEVICE void copy_codes(const PagedAttnParams& p, ChunkWalk walk, int toks, unsigned char* smem, uint64_t* full,
-                             uint64_t* empty, volatile uint32_t* miss, float* scales, volatile int* abort_flag,
-                             uint32_t vbase) {
+W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int toks, unsigned char* smem, uint64_t* full,
+                               uint64_t* raw, float* scales, volatile int* abort_flag) {
     using L = Ch<D, ONE, true>;
     constexpr int NS = L::kSlots, kPieces = D / 16, kStep = 128 / kPieces, N = 128 / kStep;  // threads and steps of a tile
     constexpr bool BF = Ty::idesc_type == 1;
-    const uint32_t kbase = BF ? vbase : code_base<BF>();
+    const uint32_t vbase = code_base<true>(), kbase = BF ? vbase : code_base<BF>();
     const int tid = threadIdx.x & 127, lane = tid & 31, prow = tid / kPieces, pcol = tid % kPieces;
-    const int page = 1 << p.shift, rows = page < kChKeys ? page : kChKeys, sh = p.shift < 7 ? p.shift : 7;
-    const int boxes = kChKeys >> sh;
-    struct Entry {
-        uint4 v[N];
-        float scale[2];     // (of keys and values, with the keys: the softmax needs both before it needs the values)
-        uint32_t no, tile;  // pages that are not there; the CTA's tile number
-        int kv;             // 0 keys, 1 values, -1 nothing
-    };
-    // the next entry to fetch: number i of the piece's 2 take, and the table entries of tile `at` and the one behind
+    // (row & 7 is prow & 7 in every step)
+    const uint32_t ring = smem_u32(smem) + L::kRingOff, from = ring + L::kTile / 2 + prow * D + pcol * 16;
+    const uint32_t to = ring + (pcol >> 2) * 16384 + prow * 128 + ((((pcol & 3) * 2) ^ (prow & 7)) << 4);
     ChunkPiece pc;
-    uint32_t i = 0, tile0 = 0, at = 0;
-    int ent[2] = {-2, -2};
-    bool more = true;
-    pc.take = 0;
-    auto entry = [&](int t) {  // lane's box of the piece's tile t (-2: no row sees it)
-        const int j = (pc.it.t0 + pc.off + t) * kChKeys + (lane << sh), col = j >> p.shift;
-        if (t >= pc.take || lane >= boxes || j > pc.it.e1 || j + rows <= pc.it.lo0) return -2;
-        return col < p.columns ? __ldcg(p.table + (int64_t)pc.b * p.table_stride + col) : -1;
-    };
-    auto fetch = [&](Entry& x) {
-        if (i == 2 * (uint32_t)pc.take) {
-            tile0 += pc.take;
-            more = more && walk.next<ONE, TREE>(p, toks, pc);
-            x.kv = -1;
-            if (!more) return;
-            i = at = 0;
-            ent[0] = entry(0);
-            ent[1] = entry(1);
-        }
-        // the order of the ring's entries (keys_at, values_at)
+    uint32_t e = 0, tile0 = 0;
+    while (walk.next<ONE, TREE>(p, toks, pc)) {
         const uint32_t n = pc.take;
-        uint32_t t;
-        if (!ONE) t = i >> 1, x.kv = i & 1;
-        else if (i == 0) t = 0, x.kv = 0;
-        else if (i == 2 * n - 1) t = n - 1, x.kv = 1;
-        else if (i & 1) t = (i + 1) >> 1, x.kv = 0;
-        else t = (i >> 1) - 1, x.kv = 1;
-        ++i;
-        const int en = t == at ? ent[0] : ent[1];
-        const bool there = en >= 0 && en < p.pages;
-        x.no = __ballot_sync(0xffffffffu, !there && en != -2);
-        x.tile = tile0 + t;
-        const int j0 = (pc.it.t0 + pc.off + t) * kChKeys, pg = there ? en : -1;
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(x.kv ? p.v : p.k) + pc.hk * (x.kv ? p.vh : p.kh) + pcol * 16;
-        const int64_t ps = x.kv ? p.vp : p.kp, ss = x.kv ? p.vs : p.ks;
+#pragma unroll 1
+        for (uint32_t i = 0; i < 2 * n; ++i, ++e) {
+            // entry i is tile t's keys (values_at and keys_at of ChunkWalk's order), or values
+            const bool keys = !ONE ? !(i & 1) : i == 0 || ((i & 1) && i + 1 < 2 * n);
+            const uint32_t sl = e % NS, off = sl * L::kTile;
+            const bool ok = mbar_wait_warp(raw + sl, (e / NS) & 1, abort_flag, &g_chunk_status);
+            uint4 v[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int row = k * kStep + prow, j = j0 + row;
-            const int g = __shfl_sync(0xffffffffu, pg, row >> sh);
-            x.v[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (g >= 0 && j >= pc.it.lo0 && j <= pc.it.e1)
-                x.v[k] = __ldcg(reinterpret_cast<const uint4*>(src + (g * ps + (j & (page - 1)) * ss)));
-        }
-        const int g = __shfl_sync(0xffffffffu, pg, tid >> sh), j = j0 + tid;
-        x.scale[0] = x.scale[1] = 0.f;
-        if (!x.kv && g >= 0 && j >= pc.it.lo0 && j <= pc.it.e1) {
-            const int64_t sl = j & (page - 1);
-            x.scale[0] = __ldcg(p.k_scale + g * p.ksp + pc.hk * p.ksh + sl * p.kss);
-            x.scale[1] = __ldcg(p.v_scale + g * p.vsp + pc.hk * p.vsh + sl * p.vss);
-        }
-        if (x.kv) {  // its table entry is done with
-            at = t + 1;
-            ent[0] = ent[1];
-            ent[1] = entry(t + 2);
-        }
-    };
-    uint32_t e = 0;  // the next ring entry
-    auto store = [&](const Entry& x) {
-        const uint32_t sl = e % NS;
-        if (e >= NS && !mbar_wait_warp(empty + sl, (e / NS - 1) & 1, abort_flag, &g_chunk_status)) return false;
-        const uint32_t dst = smem_u32(smem) + L::kRingOff + sl * L::kTile + (pcol >> 2) * 16384;
-        auto put = [&](auto values) {
-            constexpr bool V = decltype(values)::value, B = V || BF;
+            for (int k = 0; k < N; ++k) v[k] = lds_v4(from + off + k * kStep * D);
+            if (keys) {
+                const uint32_t t = !ONE ? i >> 1 : (i + 1) >> 1;
+                float* sc = scales + ((tile0 + t) & 7) * 384 + tid;
+                const float f = finite_or_nan(sc[128]);
+                sc[0] = finite_or_nan(sc[0]) * p.scale2;
+                sc[128] = f;
+                sc[256] = fabsf(f) < INFINITY ? f : 0.f;
+            }
+            if (!bar_and(3, 128, ok)) return;  // all have read the slot (or one gave up, and all do)
+            auto put = [&](auto values) {
+                constexpr bool B = decltype(values)::value || BF;
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int row = k * kStep + prow;
-                const uint32_t w[4] = {x.v[k].x, x.v[k].y, x.v[k].z, x.v[k].w};
-                uint32_t y[8];
+                for (int k = 0; k < N; ++k) {
+                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                    uint32_t y[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)  // bytes 2 h, 2 h + 1 to where code_pair has them
-                        y[2 * c + h] = code_pair<E4M3, B, E4M3>(
-                            __byte_perm(w[c], 0u, E4M3 ? (h ? 0x3424 : 0x1404) : (h ? 0x4342 : 0x4140)), V ? vbase : kbase);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a = dst + row * 128 + ((((pcol & 3) * 2 + h) ^ (row & 7)) << 4);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[4 * h]), "r"(y[4 * h + 1]),
-                                 "r"(y[4 * h + 2]), "r"(y[4 * h + 3])
+                        for (int h = 0; h < 2; ++h)  // bytes 2 h, 2 h + 1 to where code_pair has them
+                            y[2 * c + h] = code_pair<E4M3, B, E4M3>(
+                                __byte_perm(w[c], 0u, E4M3 ? (h ? 0x3424 : 0x1404) : (h ? 0x4342 : 0x4140)), B ? vbase : kbase);
+                    const uint32_t a = to + off + k * kStep * 128;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a ^ 16u), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
                                  : "memory");
                 }
-            }
-        };
-        if (x.kv) {
-            put(std::true_type{});
-        } else {
-            put(std::false_type{});
-            float* sc = scales + (x.tile & 7) * 384 + tid;
-            const float f = finite_or_nan(x.scale[1]);
-            sc[0] = finite_or_nan(x.scale[0]) * p.scale2;
-            sc[128] = f;
-            sc[256] = fabsf(f) < INFINITY ? f : 0.f;
-            if (tid == 0) miss[x.tile & 7] = x.no;
+            };
+            if (BF || !keys) put(std::true_type{});
+            else put(std::false_type{});
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + sl);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + sl);
-        ++e;
-        return true;
-    };
-    Entry a, b;
-    fetch(a);
-    fetch(b);
-    while (a.kv >= 0 && store(a)) {
-        fetch(a);
-        if (b.kv < 0 || !store(b)) break;
-        fetch(b);
+        tile0 += n;
     }
 }
 
@@ -566,7 +505,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     uint64_t* q_free = q_full + 1;
     uint64_t* join = q_free + 1;     // both warpgroups' maxima and sums are in ml
     uint64_t* done = join + 1;       // every MMA of the CTA is done
-    static_assert((2 * NS + 12) * 8 <= 384, "barriers");
+    uint64_t* raw = done + 1;        // Q8: [NS] a slot's codes, and with keys both scales, are there
+    static_assert(((Q8 ? 3 : 2) * NS + 12) * 8 <= 384, "barriers");
     volatile uint32_t* miss = reinterpret_cast<volatile uint32_t*>(smem + L::kMissOff);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
     volatile int* abort_flag = misc;  // misc: abort, request, head, item, offset, pieces with values taken out (2), -,
@@ -579,7 +519,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, Q8 ? 4 : 1);  // (Q8: a lane of each copy warp arrives)
+            mbar_init(full + i, Q8 ? 4 : 1);  // (Q8: a lane of each unpacking warp arrives)
+            if constexpr (Q8) mbar_init(raw + i, 33);  // the tensor copies, and every lane's scales
             mbar_init(empty + i, 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -602,10 +543,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     }
     if (warp == 9 && lane == 0) {
         prefetch_tmap(&tmap_q);
-        if constexpr (!Q8) {
-            prefetch_tmap(&tmap_k);
-            prefetch_tmap(&tmap_v);
-        }
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
     }
     float* scales = reinterpret_cast<float*>(smem + L::kScaleOff);
     if constexpr (Q8)
@@ -760,16 +699,15 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
 
     ChunkPiece pc;
     if (Q8 && warp >= 12) {
-        // ------------------------------------------- copies of an 8-bit cache
+        // ---------------------------------------- codes of an 8-bit cache to numbers
         if constexpr (Q8) {
-            fewer_registers<kChCopyRegs>();
-            const uint32_t vbase = code_base<true>();
-            if (p.e4m3) copy_codes<Ty, D, ONE, TREE, true>(p, walk, toks, smem, full, empty, miss, scales, abort_flag, vbase);
-            else copy_codes<Ty, D, ONE, TREE, false>(p, walk, toks, smem, full, empty, miss, scales, abort_flag, vbase);
+            fewer_registers<kChUnpackRegs>();
+            if (p.e4m3) unpack_codes<Ty, D, ONE, TREE, true>(p, walk, toks, smem, full, raw, scales, abort_flag);
+            else unpack_codes<Ty, D, ONE, TREE, false>(p, walk, toks, smem, full, raw, scales, abort_flag);
         }
     } else if (warp >= 8) {
       if constexpr (Q8) fewer_registers<kChMmaRegs>();
-      if (!Q8 && warp == 9) {
+      if (warp == 9) {
         // ---------------------------------------------------------- copies
         const int page = 1 << p.shift, rows = page < kChKeys ? page : kChKeys, boxes = kChKeys / rows;
         uint32_t e = 0, tile0 = 0;  // the next ring entry, and the piece's first tile
@@ -791,10 +729,27 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 if (!ok) return;
                 if (lane == 0) {
                     if (kv == 0) miss[(tile0 + t) & 7] = no;
-                    mbar_arrive_expect_tx(full + sl, (uint32_t)L::kTile);
+                    mbar_arrive_expect_tx((Q8 ? raw : full) + sl, (uint32_t)(Q8 ? L::kTile / 2 : L::kTile));
                 }
                 __syncwarp();
-                if (lane < boxes) {
+                if constexpr (Q8) {
+                    if (lane < boxes)
+                        tma_load_4d(smem + L::kRingOff + sl * L::kTile + L::kTile / 2 + lane * rows * D, kv ? &tmap_v : &tmap_k, 0,
+                                    slot, pc.hk, pg, raw + sl);
+                    if (kv == 0) {  // the scales of keys 32 x + lane; what no row sees keeps any number
+                        const int sh = p.shift < 7 ? p.shift : 7, j0 = (pc.it.t0 + pc.off + t) * kChKeys;
+                        float* sc = scales + ((tile0 + t) & 7) * 384;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int row = 32 * x + lane, g = __shfl_sync(0xffffffffu, pg, row >> sh);
+                            if (g >= p.pages) continue;
+                            const int64_t at = (j0 + row) & (page - 1);
+                            cp_async_4(sc + row, p.k_scale + g * p.ksp + pc.hk * p.ksh + at * p.kss);
+                            cp_async_4(sc + 128 + row, p.v_scale + g * p.vsp + pc.hk * p.vsh + at * p.vss);
+                        }
+                    }
+                    arrive_behind_copies(raw + sl);
+                } else if (lane < boxes) {
                     unsigned char* dst = smem + L::kRingOff + sl * L::kTile + lane * rows * 128;
 #pragma unroll
                     for (int s = 0; s < L::kSlabs; ++s)
@@ -826,8 +781,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
         }
         // the copies in flight land before the CTA ends
         for (uint32_t i = e > NS ? e - NS : 0; i < e; ++i)
-            (void)mbar_wait_warp(full + i % NS, (i / NS) & 1, nullptr, &g_chunk_status);
-      } else if (warp == (Q8 ? 9 : 10)) {
+            (void)mbar_wait_warp((Q8 ? raw : full) + i % NS, (i / NS) & 1, nullptr, &g_chunk_status);
+      } else if (warp == 10) {
         // --------------------------------------------------------- queries
         uint32_t items = 0;
         while (walk.next<ONE, TREE>(p, toks, pc)) {
@@ -1412,11 +1367,11 @@ static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CU
 
 template <bool TREE, bool Q8>
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, bool bf16, int d, bool one, int sms, cudaStream_t s, bool pdl) {
-    CUtensorMap tq, tk = {}, tv = {};
+    CUtensorMap tq, tk, tv;
     const int box = (1 << p.shift) < kChKeys ? 1 << p.shift : kChKeys;
-    if (!Q8 && (!paged_tmap(&tk, p, bf16, d, false, box) || !paged_tmap(&tv, p, bf16, d, true, box)))
+    if (!paged_tmap(&tk, p, bf16, Q8, d, false, box) || !paged_tmap(&tv, p, bf16, Q8, d, true, box) ||
+        !query_tmap(&tq, p, bf16, d, 128 / p.G))
         return cudaErrorInvalidValue;
-    if (!query_tmap(&tq, p, bf16, d, 128 / p.G)) return cudaErrorInvalidValue;
     if (bf16)
         return d == 128 ? launch<Bf16, 128, TREE, Q8>(tq, tk, tv, p, one, sms, s, pdl)
                         : launch<Bf16, 64, TREE, Q8>(tq, tk, tv, p, one, sms, s, pdl);
