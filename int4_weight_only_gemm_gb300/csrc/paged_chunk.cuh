@@ -97,8 +97,8 @@ static_assert(Ch<128, true, true>::kSmem <= 232448 && Ch<128, false, true>::kSme
 static_assert(Ch<64, true, true>::kSmem <= 232448 && Ch<64, false, true>::kSmem <= 232448, "shared memory");
 
 // Over an 8-bit cache the block is launched with 128 registers a thread, 65536 in all; the two other warpgroups give
-// some to the softmax ones: 2 x 168 + 64 + 112 = 4 x 128.
-constexpr int kChSoftmaxRegs = 168, kChMmaRegs = 64, kChUnpackRegs = 112;
+// some to the softmax ones: 2 x 184 + 64 + 80 = 4 x 128.
+constexpr int kChSoftmaxRegs = 184, kChMmaRegs = 64, kChUnpackRegs = 80;
 static_assert(2 * kChSoftmaxRegs + kChMmaRegs + kChUnpackRegs <= 4 * 128, "registers of the launch");
 template <int N>
 W4A16_DEVICE void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -416,22 +416,65 @@ struct PvType<Ty, true> {
     using type = Bf16;
 };
 
-// The four unpacking warps.  A tile's codes lie in the upper half of its ring slot:
-// a thread takes the same 16-code column of every 16th row (32nd for D = 64) into
-// registers and, once all have, puts them back over the whole slot as 16-bit
-// numbers in the layout that tensor copies of such would give.  Thread i turns the
-// scales of key i into what the softmax takes.
+// Weights of 32 scores, times their values' scales, in bf16: hi, and with TWO what hi lacks; the sums l0 and l1 are of
+// the weights alone.
+template <bool TWO>
+W4A16_DEVICE void scaled_weights(const uint32_t (&v)[32], const float* kc, const float* vc, float2 nb, float2& l0, float2& l1,
+                                 uint32_t (&hi)[16], uint32_t* lo) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const float4 c = *reinterpret_cast<const float4*>(kc + 2 * i);
+        const float4 d = *reinterpret_cast<const float4*>(vc + 2 * i);
+        float2 a = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        float2 b = make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3]));
+        a = fma2(a, make_float2(c.x, c.y), nb);
+        b = fma2(b, make_float2(c.z, c.w), nb);
+        a.x = exp2_approx(a.x);
+        a.y = exp2_approx(a.y);
+        b.x = exp2_approx(b.x);
+        b.y = exp2_approx(b.y);
+        l0 = add2(l0, a);
+        l1 = add2(l1, b);
+        a = mul2(a, make_float2(d.x, d.y));
+        b = mul2(b, make_float2(d.z, d.w));
+        hi[i] = Bf16::pack(a.x, a.y);
+        hi[i + 1] = Bf16::pack(b.x, b.y);
+        if constexpr (TWO) {
+            lo[i] = Bf16::pack(a.x - Bf16::lo(hi[i]), a.y - Bf16::hi(hi[i]));
+            lo[i + 1] = Bf16::pack(b.x - Bf16::lo(hi[i + 1]), b.y - Bf16::hi(hi[i + 1]));
+        }
+    }
+}
+// Those of a row's 128 scores in two parts, for the rows of few positions: out of line, so that the loop of the long
+// ones fits the instruction caches (346 us with it, 387 without, for the chunk below).
+static __device__ __noinline__ float2 weights_in_two_parts(uint32_t ts, const float* kc, const float* vc, float base) {
+    float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {
+        uint32_t v[32], hi[16], lo[16];
+        tmem_ld32(ts + 32 * x, v);
+        tmem_wait_ld();
+        scaled_weights<true>(v, kc + 32 * x, vc + 32 * x, make_float2(-base, -base), l0, l1, hi, lo);
+        tmem_st16(ts + 32 * x, hi);
+        tmem_st16(ts + 32 * x + 16, lo);
+    }
+    return add2(l0, l1);
+}
+
+// The four unpacking warps.  A tile's codes lie in the upper half of its ring slot
+// and become 16-bit numbers over the whole slot, in the layout that tensor copies
+// of such would give: a thread takes the same 16 columns of 64 of every 32nd row.
+// Thread i turns the scales of key i into what the softmax takes.
 template <typename Ty, int D, bool ONE, bool TREE, bool E4M3>
 W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int toks, unsigned char* smem, uint64_t* full,
                                uint64_t* raw, float* scales, volatile int* abort_flag) {
     using L = Ch<D, ONE, true>;
-    constexpr int NS = L::kSlots, kPieces = D / 16, kStep = 128 / kPieces, N = 128 / kStep;  // threads and steps of a tile
+    constexpr int NS = L::kSlots;
     constexpr bool BF = Ty::idesc_type == 1;
     const uint32_t vbase = code_base<true>(), kbase = BF ? vbase : code_base<BF>();
-    const int tid = threadIdx.x & 127, lane = tid & 31, prow = tid / kPieces, pcol = tid % kPieces;
-    // (row & 7 is prow & 7 in every step)
+    const int tid = threadIdx.x & 127, lane = tid & 31, prow = tid >> 2, pcol = tid & 3;
     const uint32_t ring = smem_u32(smem) + L::kRingOff, from = ring + L::kTile / 2 + prow * D + pcol * 16;
-    const uint32_t to = ring + (pcol >> 2) * 16384 + prow * 128 + ((((pcol & 3) * 2) ^ (prow & 7)) << 4);
+    const uint32_t to = ring + prow * 128 + (((pcol * 2) ^ (prow & 7)) << 4);  // (row & 7 is prow & 7 in every step)
     ChunkPiece pc;
     uint32_t e = 0, tile0 = 0;
     while (walk.next<ONE, TREE>(p, toks, pc)) {
@@ -442,9 +485,43 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
             const bool keys = !ONE ? !(i & 1) : i == 0 || ((i & 1) && i + 1 < 2 * n);
             const uint32_t sl = e % NS, off = sl * L::kTile;
             const bool ok = mbar_wait_warp(raw + sl, (e / NS) & 1, abort_flag, &g_chunk_status);
-            uint4 v[N];
+            auto put = [&](uint32_t a, const uint4& v, auto values) {
+                constexpr bool B = decltype(values)::value;
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t y[8];
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = lds_v4(from + off + k * kStep * D);
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)  // bytes 2 h, 2 h + 1 to where code_pair has them
+                        y[2 * c + h] = code_pair<E4M3, B, E4M3>(
+                            __byte_perm(w[c], 0u, E4M3 ? (h ? 0x3424 : 0x1404) : (h ? 0x4342 : 0x4140)), B ? vbase : kbase);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a ^ 16u), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                             : "memory");
+            };
+            auto unpack = [&](auto values) {
+                if constexpr (D == 128) {
+                    // a row's 128 codes lie where the last 64 of its numbers go: four lanes read and write them
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 x = lds_v4(from + off + k * 32 * 128), y = lds_v4(from + off + k * 32 * 128 + 64);
+                        __syncwarp();
+                        put(to + off + k * 32 * 128, x, values);
+                        put(to + off + k * 32 * 128 + 16384, y, values);
+                    }
+                    return ok;
+                } else {
+                    // a row of numbers lies over two rows of codes: all are in registers first
+                    uint4 v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = lds_v4(from + off + k * 32 * 64);
+                    if (!bar_and(3, 128, ok)) return false;  // all have read theirs (or one gave up, and all do)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) put(to + off + k * 32 * 128, v[k], values);
+                    return true;
+                }
+            };
             if (keys) {
                 const uint32_t t = !ONE ? i >> 1 : (i + 1) >> 1;
                 float* sc = scales + ((tile0 + t) & 7) * 384 + tid;
@@ -453,28 +530,7 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
                 sc[128] = f;
                 sc[256] = fabsf(f) < INFINITY ? f : 0.f;
             }
-            if (!bar_and(3, 128, ok)) return;  // all have read the slot (or one gave up, and all do)
-            auto put = [&](auto values) {
-                constexpr bool B = decltype(values)::value || BF;
-#pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                    uint32_t y[8];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)  // bytes 2 h, 2 h + 1 to where code_pair has them
-                            y[2 * c + h] = code_pair<E4M3, B, E4M3>(
-                                __byte_perm(w[c], 0u, E4M3 ? (h ? 0x3424 : 0x1404) : (h ? 0x4342 : 0x4140)), B ? vbase : kbase);
-                    const uint32_t a = to + off + k * kStep * 128;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a ^ 16u), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                                 : "memory");
-                }
-            };
-            if (BF || !keys) put(std::true_type{});
-            else put(std::false_type{});
+            if (!(BF || !keys ? unpack(std::true_type{}) : unpack(std::false_type{}))) return;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(full + sl);
@@ -995,14 +1051,19 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 uint32_t sv[2][32];
                 tmem_ld32(ts, sv[0]);
                 float mx = m, mo = m;
+                // (Q8: 64 scores a round, since with all 128 written out the code of the CTA's roles no longer fits
+                // the instruction caches: 416 us for the chunk below)
+#pragma unroll(Q8 ? 1 : 2)
+                for (int x0 = 0; x0 < 4; x0 += 2)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int y = 0; y < 2; ++y) {
+                    const int x = x0 + y;
                     tmem_wait_ld();
-                    if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
+                    if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[1 - y]);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        float2 a = make_float2(__uint_as_float(sv[x & 1][i]), __uint_as_float(sv[x & 1][i + 1]));
-                        float2 b = make_float2(__uint_as_float(sv[x & 1][i + 2]), __uint_as_float(sv[x & 1][i + 3]));
+                        float2 a = make_float2(__uint_as_float(sv[y][i]), __uint_as_float(sv[y][i + 1]));
+                        float2 b = make_float2(__uint_as_float(sv[y][i + 2]), __uint_as_float(sv[y][i + 3]));
                         if constexpr (Q8) {
                             const float4 c = *reinterpret_cast<const float4*>(kc + 32 * x + i);
                             a = mul2(a, make_float2(c.x, c.y));
@@ -1049,52 +1110,35 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     }
                 };
                 if constexpr (Q8) {
-                    // weights times their values' scales, in bf16 (one or two parts over the columns of their scores)
-                    auto scaled = [&](const uint32_t* v, int x, uint32_t* hi, uint32_t* lo) {
+                    if (Ty::idesc_type == 1 && two) {
+                        l0 = weights_in_two_parts(ts, kc, vc, base);
+                    } else if (Ty::idesc_type == 1) {
+                        tmem_ld32(ts, sv[0]);
+#pragma unroll 1
+                        for (int x0 = 0; x0 < 4; x0 += 2)
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float4 c = *reinterpret_cast<const float4*>(kc + 32 * x + 2 * i);
-                            const float4 d = *reinterpret_cast<const float4*>(vc + 32 * x + 2 * i);
-                            float2 a = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                            float2 b = make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3]));
-                            a = fma2(a, make_float2(c.x, c.y), nb);
-                            b = fma2(b, make_float2(c.z, c.w), nb);
-                            a.x = exp2_approx(a.x);
-                            a.y = exp2_approx(a.y);
-                            b.x = exp2_approx(b.x);
-                            b.y = exp2_approx(b.y);
-                            l0 = add2(l0, a);
-                            l1 = add2(l1, b);
-                            a = mul2(a, make_float2(d.x, d.y));
-                            b = mul2(b, make_float2(d.z, d.w));
-                            hi[i] = Bf16::pack(a.x, a.y);
-                            hi[i + 1] = Bf16::pack(b.x, b.y);
-                            if (lo) {
-                                lo[i] = Bf16::pack(a.x - Bf16::lo(hi[i]), a.y - Bf16::hi(hi[i]));
-                                lo[i + 1] = Bf16::pack(b.x - Bf16::lo(hi[i + 1]), b.y - Bf16::hi(hi[i + 1]));
+                            for (int y = 0; y < 2; ++y) {
+                                const int x = x0 + y;
+                                tmem_wait_ld();
+                                if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[1 - y]);
+                                uint32_t hi[16];
+                                scaled_weights<false>(sv[y], kc + 32 * x, vc + 32 * x, nb, l0, l1, hi, nullptr);
+                                tmem_st16(ts + 16 * x, hi);
                             }
-                        }
-                    };
-                    tmem_ld32(ts, sv[0]);
-                    if (!two) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            tmem_wait_ld();
-                            if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
-                            uint32_t hi[16];
-                            scaled(sv[x & 1], x, hi, nullptr);
-                            tmem_st16(ts + 16 * x, hi);
-                        }
                     } else {
+                        tmem_ld32(ts, sv[0]);
+#pragma unroll 1
+                        for (int x0 = 0; x0 < 4; x0 += 2)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            tmem_wait_ld();
-                            if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
-                            uint32_t hi[16], lo[16];
-                            scaled(sv[x & 1], x, hi, lo);
-                            tmem_st16(ts + 32 * x, hi);
-                            tmem_st16(ts + 32 * x + 16, lo);
-                        }
+                            for (int y = 0; y < 2; ++y) {
+                                const int x = x0 + y;
+                                tmem_wait_ld();
+                                if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[1 - y]);
+                                uint32_t hi[16], lo[16];
+                                scaled_weights<true>(sv[y], kc + 32 * x, vc + 32 * x, nb, l0, l1, hi, lo);
+                                tmem_st16(ts + 32 * x, hi);
+                                tmem_st16(ts + 32 * x + 16, lo);
+                            }
                     }
                 } else {
                 tmem_ld32(ts, sv[0]);
