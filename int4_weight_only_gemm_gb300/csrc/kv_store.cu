@@ -55,6 +55,36 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const __grid_cons
     pdl_wait();
     pdl_launch_dependents();
     const int t0 = (int)blockIdx.x * p.per_cta, nt = min(p.per_cta, p.tokens - t0);
+    const int r0 = (int)blockIdx.y * p.row0s, nr = min(p.row0s, p.rows - r0);
+    constexpr int GROUPS = kRowThreads / LANES;
+    const int lane = threadIdx.x % LANES, col = 8 * lane;
+    const bool on = col < p.d;
+    // (all lanes of a warp go round together: shuffles)
+    const int items = nt * nr, rounds = (items + GROUPS - 1) / GROUPS;
+    struct Row {
+        int tt, kind, h, slot;  // token of the CTA; 0 query, 1 key, 2 value; head
+        bool live;
+        const uint16_t* src;
+        uint4 raw;
+    };
+    auto load = [&](int n) {  // the row of round n, on its way
+        Row r;
+        const int item = n * GROUPS + threadIdx.x / LANES;
+        const bool have = item < items;
+        r.tt = !have ? 0 : nr == p.rows ? div_by(item, p.by_rows.m, p.by_rows.s) : item / nr;
+        const int row = r0 + (have ? item - r.tt * nr : 0), t = t0 + r.tt;
+        r.kind = row < p.q_heads ? 0 : row < p.q_heads + p.heads ? 1 : 2;
+        r.h = row - (r.kind == 0 ? 0 : r.kind == 1 ? p.q_heads : p.q_heads + p.heads);
+        r.slot = r.kind ? p.slots[t] : 0;
+        r.live = have && on && (!p.freq || p.positions[t] >= 0) && (r.kind == 0 || (r.slot >= 0 && r.slot < p.total_slots));
+        r.src = r.kind == 0   ? p.q + t * p.q_token + r.h * p.q_head
+                : r.kind == 1 ? p.k + t * p.k_token + r.h * p.k_head
+                              : p.v + t * p.v_token + r.h * p.v_head;
+        r.raw = make_uint4(0u, 0u, 0u, 0u);
+        if (have && on) r.raw = *reinterpret_cast<const uint4*>(r.src + col);
+        return r;
+    };
+    Row next = load(0);
     if (p.freq) {
         for (int e = threadIdx.x; e < nt * p.half; e += kRowThreads) {
             const int tt = div_by(e, p.by_half.m, p.by_half.s), i = e - tt * p.half;
@@ -67,27 +97,13 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const __grid_cons
         }
         __syncthreads();
     }
-    const int r0 = (int)blockIdx.y * p.row0s, nr = min(p.row0s, p.rows - r0);
-    constexpr int GROUPS = kRowThreads / LANES;
-    const int lane = threadIdx.x % LANES, col = 8 * lane;
-    const bool on = col < p.d;
-    // (all lanes of a warp go round together: shuffles)
-    const int items = nt * nr, rounds = (items + GROUPS - 1) / GROUPS;
     for (int n = 0; n < rounds; ++n) {
-        const int item = n * GROUPS + threadIdx.x / LANES;
-        const bool have = item < items;
-        const int tt = !have ? 0 : nr == p.rows ? div_by(item, p.by_rows.m, p.by_rows.s) : item / nr;
-        const int row = r0 + (have ? item - tt * nr : 0), t = t0 + tt;
-        const int kind = row < p.q_heads ? 0 : row < p.q_heads + p.heads ? 1 : 2;
-        const int h = row - (kind == 0 ? 0 : kind == 1 ? p.q_heads : p.q_heads + p.heads);
-        const int slot = kind ? p.slots[t] : 0;
-        const bool live = have && on && (!p.freq || p.positions[t] >= 0) &&
-                          (kind == 0 || (slot >= 0 && slot < p.total_slots));
-        const uint16_t* src = kind == 0   ? p.q + t * p.q_token + h * p.q_head
-                              : kind == 1 ? p.k + t * p.k_token + h * p.k_head
-                                          : p.v + t * p.v_token + h * p.v_head;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (live) raw = *reinterpret_cast<const uint4*>(src + col);
+        const Row cur = next;
+        if (n + 1 < rounds) next = load(n + 1);
+        const int tt = cur.tt, kind = cur.kind, h = cur.h, slot = cur.slot, t = t0 + tt;
+        const bool live = cur.live;
+        const uint4 raw = cur.raw;
+        const uint16_t* src = cur.src;
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = half_of<Ty>(raw, i);
@@ -189,10 +205,11 @@ static cudaError_t launch(RowParams& p, bool bf16, int code, int rot, int sms, c
     p.by_lane = p.half % 8 == 0;
     p.rows = p.q_heads + 2 * p.heads;
     const int groups = kRowThreads / (p.d <= 128 ? 16 : 32);
-    // Tokens of a CTA: as many as its groups of lanes have rows for; a token's rows
-    // over several CTAs where there are too few tokens to fill the GPU.
+    // Tokens of a CTA: as many as its groups of lanes have rows for, up to eight rounds of them while the GPU stays
+    // full (cosines for all threads, loads a round ahead); a token's rows over several CTAs where tokens are too few.
     int per = groups / p.rows;
     per = per < 1 ? 1 : per > kRowTokens ? kRowTokens : per;
+    while (per * 2 <= kRowTokens && (int64_t)per * 2 * p.rows <= 8 * groups && p.tokens / (per * 2) >= 16 * sms) per *= 2;
     const int ctas = (p.tokens + per - 1) / per;
     int split = 1;
     while (ctas * split * 2 <= 4 * sms && (p.rows + split * 2 - 1) / (split * 2) >= groups) split *= 2;

@@ -1113,18 +1113,14 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     if (Ty::idesc_type == 1 && two) {
                         l0 = weights_in_two_parts(ts, kc, vc, base);
                     } else if (Ty::idesc_type == 1) {
-                        tmem_ld32(ts, sv[0]);
 #pragma unroll 1
-                        for (int x0 = 0; x0 < 4; x0 += 2)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int x = x0 + y;
-                                tmem_wait_ld();
-                                if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[1 - y]);
-                                uint32_t hi[16];
-                                scaled_weights<false>(sv[y], kc + 32 * x, vc + 32 * x, nb, l0, l1, hi, nullptr);
-                                tmem_st16(ts + 16 * x, hi);
-                            }
+                        for (int x = 0; x < 4; ++x) {  // (the next 32 ahead cost more code than they save time: 301 us)
+                            uint32_t hi[16];
+                            tmem_ld32(ts + 32 * x, sv[0]);
+                            tmem_wait_ld();
+                            scaled_weights<false>(sv[0], kc + 32 * x, vc + 32 * x, nb, l0, l1, hi, nullptr);
+                            tmem_st16(ts + 16 * x, hi);
+                        }
                     } else {
                         tmem_ld32(ts, sv[0]);
 #pragma unroll 1
