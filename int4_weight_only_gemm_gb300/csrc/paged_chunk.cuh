@@ -1255,6 +1255,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                             for (int x = 0; x < 32; ++x)
                                 ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f0 + __uint_as_float(ow[x]) * f1);
                         }
+                        if (valid)
 #pragma unroll
                         for (int x = 0; x < 32; x += 4)  // [column / 4][row]: neighbours write neighbours
                             *reinterpret_cast<uint4*>(part + 256 + (((i + x) >> 2) * 128 + row) * 4) =
@@ -1299,11 +1300,17 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                         if (mi.y != 0.f) S = fmaf(fabsf(mi.y), factor(mi.x), S);
                     }
                 const float w = S == 0.f ? 0.f : 1.f / S;
+                auto put = [&](int x, const float* acc) {  // 8 columns
+                    *reinterpret_cast<uint4*>(out + x) =
+                        S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                 : make_uint4(Ty::pack(acc[0] * w, acc[1] * w), Ty::pack(acc[2] * w, acc[3] * w),
+                                              Ty::pack(acc[4] * w, acc[5] * w), Ty::pack(acc[6] * w, acc[7] * w));
+                };
+                if (whole) {
 #pragma unroll 1
-                for (int x = x0; x < x1; x += 32) {
-                    float acc[32];
-                    auto own = [&](float f) {  // this piece's columns, times f, onto acc
+                    for (int x = x0; x < x1; x += 32) {
                         uint32_t ov[32];
+                        float acc[32];
                         tmem_ld32(toa + x, ov);
                         tmem_wait_ld();
                         if (other) {
@@ -1315,46 +1322,72 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                                 ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
                         }
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), f, acc[y]);
-                    };
+                        for (int y = 0; y < 32; ++y) acc[y] = __uint_as_float(ov[y]) + 0.f;  // (-0 becomes 0)
+                        if (valid)
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) acc[y] = 0.f;
-                    if (whole) {
-                        own(1.f);
-                    } else {
-                        for (int i = c0; i <= c1; ++i) {
-                            if (i == c && kept) {
-                                // (every lane: tensor-memory loads are the warp's)
-                                own(l == 0.f ? 0.f : factor(mine_m));
-                                continue;
+                            for (int y = 0; y < 32; y += 8) put(x + y, acc + y);
+                        __syncwarp();
+                    }
+                } else {
+                    // 16 columns at a time, of four pieces in flight (32 of one piece: 34 us for 13 tokens over 2303
+                    // positions, whose 19 pieces come one after the other then)
+#pragma unroll 1
+                    for (int x = x0; x < x1; x += 16) {
+                        float acc[16];
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) acc[y] = 0.f;
+#pragma unroll 1
+                        for (int i0 = c0; i0 <= c1; i0 += 4) {
+                            float4 v[4][4];
+                            float fs[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int i = i0 + u;
+                                fs[u] = 0.f;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) v[u][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (i > c1 || (i == c && kept) || !valid) continue;
+                                const float* q = piece(i);
+                                const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
+                                fs[u] = mi.y == 0.f ? 0.f : factor(mi.x);  // no seen key: zeros
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    v[u][y] = __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row);
                             }
-                            const float* q = piece(i);
-                            const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
-                            const float f = mi.y == 0.f ? 0.f : factor(mi.x);  // no seen key: zeros
-                            float4 v[8];
 #pragma unroll
-                            for (int y = 0; y < 8; ++y)
-                                v[y] = __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row);
+                            for (int u = 0; u < 4; ++u) {
+                                if (i0 + u == c && kept) {  // this piece's, by every lane: tensor-memory loads are the warp's
+                                    uint32_t ov[16];
+                                    tmem_ld_x16(toa + x, ov);
+                                    tmem_wait_ld();
+                                    if (other) {
+                                        uint32_t ow[16];
+                                        tmem_ld_x16(tob + x, ow);
+                                        tmem_wait_ld();
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) {
-                                acc[4 * y] = fmaf(v[y].x, f, acc[4 * y]);
-                                acc[4 * y + 1] = fmaf(v[y].y, f, acc[4 * y + 1]);
-                                acc[4 * y + 2] = fmaf(v[y].z, f, acc[4 * y + 2]);
-                                acc[4 * y + 3] = fmaf(v[y].w, f, acc[4 * y + 3]);
+                                        for (int y = 0; y < 16; ++y)
+                                            ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
+                                    }
+                                    const float f = l == 0.f ? 0.f : factor(mine_m);
+#pragma unroll
+                                    for (int y = 0; y < 16; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), f, acc[y]);
+                                } else {
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        acc[4 * y] = fmaf(v[u][y].x, fs[u], acc[4 * y]);
+                                        acc[4 * y + 1] = fmaf(v[u][y].y, fs[u], acc[4 * y + 1]);
+                                        acc[4 * y + 2] = fmaf(v[u][y].z, fs[u], acc[4 * y + 2]);
+                                        acc[4 * y + 3] = fmaf(v[u][y].w, fs[u], acc[4 * y + 3]);
+                                    }
+                                }
                             }
                         }
+                        if (valid) {
+                            put(x, acc);
+                            put(x + 8, acc + 8);
+                        }
+                        __syncwarp();
                     }
-                    if (valid) {
-#pragma unroll
-                        for (int y = 0; y < 32; y += 8)
-                            *reinterpret_cast<uint4*>(out + x + y) =
-                                S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
-                                         : make_uint4(Ty::pack(acc[y] * w, acc[y + 1] * w),
-                                                      Ty::pack(acc[y + 2] * w, acc[y + 3] * w),
-                                                      Ty::pack(acc[y + 4] * w, acc[y + 5] * w),
-                                                      Ty::pack(acc[y + 6] * w, acc[y + 7] * w));
-                    }
-                    __syncwarp();
                 }
                 if (valid && p.lse && x0 == 0) p.lse[t * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
             }
