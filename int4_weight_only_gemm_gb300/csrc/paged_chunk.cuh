@@ -685,7 +685,14 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     // to the end.
     const int64_t n_items = (int64_t)pairs * p.Hkv;
     const bool single = n_items <= gridDim.x && (int64_t)(most - kChJoin) * gridDim.x <= U;
-    const int C = single ? (int)n_items : (int)(U < gridDim.x ? U : gridDim.x);
+    int C = single ? (int)n_items : (int)(U < gridDim.x ? U : gridDim.x);
+    // A piece more costs the joining CTA about two fifths of a tile's time, so that few items are not cut below
+    // sqrt(2 / 5 tiles) tiles a piece: 13 nodes over 2303 positions, 8 items of 19 tiles, 36 us in 152 pieces.
+    if ((TREE || Q8) && !single) {
+        int least = 1;
+        while (5 * least * least < 2 * most) ++least;
+        C = (int)min((int64_t)C, (U + least - 1) / least);
+    }
     ChunkWalk walk;
     walk.left = 0;
     if (c < C) {
@@ -978,15 +985,18 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     // an edge: scores outside the row's positions become -inf, 32 at a time
                     const int rl = lo - j0, re = e - j0;
                     bool bad = false;
+                    uint32_t nodes[5];  // the words with the nodes at the tile's positions
+                    if constexpr (TREE)
+#pragma unroll
+                        for (int i = 0; i < 5; ++i) nodes[i] = valid ? tree_word(p, my_t, pc.r.n, ((j0 - past) >> 5) + i) : 0u;
 #pragma unroll 1
                     for (int x = 0; x < 128; x += 32) {
                         uint32_t seen = re >= x + 31 ? ~0u : re < x ? 0u : (2u << (re - x)) - 1u;
                         seen &= rl <= x ? ~0u : rl > x + 31 ? 0u : ~0u << (rl - x);
                         if constexpr (TREE) {  // node k is position past + k
-                            const int k = j0 + x - past;
-                            if (valid && k > -32 && k < pc.r.n)
-                                seen |= __funnelshift_r(tree_word(p, my_t, pc.r.n, k >> 5),
-                                                        tree_word(p, my_t, pc.r.n, (k >> 5) + 1), k & 31);
+                            seen |= __funnelshift_r(nodes[0], nodes[1], (j0 - past) & 31);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) nodes[i] = nodes[i + 1];
                         }
                         if (no) {  // pages that are not there: 2^sh keys a bit
                             const int sh = p.shift < 7 ? p.shift : 7;
@@ -1339,21 +1349,21 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
 #pragma unroll 1
                         for (int i0 = c0; i0 <= c1; i0 += 4) {
                             float4 v[4][4];
+                            float2 mi[4];
                             float fs[4];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
+                            for (int u = 0; u < 4; ++u) {  // (all on their way before any is waited for)
                                 const int i = i0 + u;
-                                fs[u] = 0.f;
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) v[u][y] = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (i > c1 || (i == c && kept) || !valid) continue;
-                                const float* q = piece(i);
-                                const float2 mi = __ldcg(reinterpret_cast<const float2*>(q) + row);
-                                fs[u] = mi.y == 0.f ? 0.f : factor(mi.x);  // no seen key: zeros
+                                const bool there = i <= c1 && !(i == c && kept) && valid;
+                                const float* q = piece(there ? i : c0);
+                                mi[u] = there ? __ldcg(reinterpret_cast<const float2*>(q) + row) : make_float2(0.f, 0.f);
 #pragma unroll
                                 for (int y = 0; y < 4; ++y)
-                                    v[u][y] = __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row);
+                                    v[u][y] = there ? __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row)
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
                             }
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) fs[u] = mi[u].y == 0.f ? 0.f : factor(mi[u].x);  // no seen key: zeros
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
                                 if (i0 + u == c && kept) {  // this piece's, by every lane: tensor-memory loads are the warp's
