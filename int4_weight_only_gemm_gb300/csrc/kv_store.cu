@@ -6,7 +6,8 @@
 //
 // A CTA takes a few tokens.  Its threads first make the cosines and sines of the
 // tokens' pairs, in shared memory for all heads, then 16 lanes (32 for heads over
-// 128 wide) take a head's row at a time, 8 elements a lane.  Angles: a frequency
+// 128 wide) take a token's rows one after the other, 8 elements a lane, with the
+// cosines and sines of their columns in registers.  Angles: a frequency
 // is a 64-bit fraction F of a turn a position, so position * F modulo 2^64 is the
 // fraction of a turn, without rounding; its top 32 bits go to sincospi.
 //
@@ -20,7 +21,6 @@
 namespace w4a16 {
 
 constexpr int kRowThreads = 256;
-constexpr int kRowTokens = 16;  // most tokens of a CTA
 
 struct RowParams {
     const uint16_t *q, *k, *v;
@@ -34,11 +34,11 @@ struct RowParams {
     int64_t kcp, kch, kcs, vcp, vch, vcs, ksp, ksh, kss, vsp, vsh, vss;
     int64_t total_slots;
     int tokens, q_heads, heads, d, half, interleaved, shift;
-    int per_cta;    // tokens of a CTA
-    int rows, row0s;  // rows (q heads, k heads, v heads) of a token, and those of one CTA
+    int per_shift;  // log2 of the tokens of a CTA
+    int rows, cta_rows;  // rows (q heads, k heads, v heads) of a token, and those of one CTA
     bool by_lane;   // a pair's partner is in the same lane, or in the lane `half / 8` on
     float magnitude;
-    FastDiv by_rows, by_half;
+    FastDiv by_half;
 };
 
 enum { kCode16 = 0, kCodeInt8 = 1, kCodeE4m3 = 2 };
@@ -49,116 +49,127 @@ W4A16_DEVICE float half_of(const uint4& v, int i) {
     return i & 1 ? Ty::hi(x) : Ty::lo(x);
 }
 
-template <typename Ty, int CODE, int LANES>
-__global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const __grid_constant__ RowParams p) {
+// KV: keys and values too, else queries alone
+template <typename Ty, int CODE, int LANES, bool KV>
+__global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_constant__ RowParams p) {
     extern __shared__ float2 turn[];  // [token][pair] cosine and sine
     pdl_wait();
     pdl_launch_dependents();
-    const int t0 = (int)blockIdx.x * p.per_cta, nt = min(p.per_cta, p.tokens - t0);
-    const int r0 = (int)blockIdx.y * p.row0s, nr = min(p.row0s, p.rows - r0);
     constexpr int GROUPS = kRowThreads / LANES;
-    const int lane = threadIdx.x % LANES, col = 8 * lane;
-    const bool on = col < p.d;
-    // (all lanes of a warp go round together: shuffles)
-    const int items = nt * nr, rounds = (items + GROUPS - 1) / GROUPS;
+    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, col = 8 * lane;
+    // a group of lanes has one token, and every step-th of its rows from `sub` on
+    const int tt = group & ((1 << p.per_shift) - 1), sub = group >> p.per_shift, step = GROUPS >> p.per_shift;
+    const int t0 = (int)blockIdx.x << p.per_shift, t = t0 + tt, nt = min(1 << p.per_shift, p.tokens - t0);
+    const int r0 = (int)blockIdx.y * p.cta_rows, r1 = min(r0 + p.cta_rows, p.rows);
+    const bool on = t < p.tokens && col < p.d;
+    const bool here = on && (!p.freq || p.positions[t] >= 0);
+    const int slot = KV && t < p.tokens ? p.slots[t] : -1;
+    const bool stored = here && slot >= 0 && slot < p.total_slots;
+    const int64_t pg = slot >> p.shift, sl = slot & ((1 << p.shift) - 1);
+
     struct Row {
-        int tt, kind, h, slot;  // token of the CTA; 0 query, 1 key, 2 value; head
+        int kind, h;  // 0 query, 1 key, 2 value; head
         bool live;
         const uint16_t* src;
         uint4 raw;
     };
-    auto load = [&](int n) {  // the row of round n, on its way
+    auto load = [&](int row) {  // on its way
         Row r;
-        const int item = n * GROUPS + threadIdx.x / LANES;
-        const bool have = item < items;
-        r.tt = !have ? 0 : nr == p.rows ? div_by(item, p.by_rows.m, p.by_rows.s) : item / nr;
-        const int row = r0 + (have ? item - r.tt * nr : 0), t = t0 + r.tt;
-        r.kind = row < p.q_heads ? 0 : row < p.q_heads + p.heads ? 1 : 2;
-        r.h = row - (r.kind == 0 ? 0 : r.kind == 1 ? p.q_heads : p.q_heads + p.heads);
-        r.slot = r.kind ? p.slots[t] : 0;
-        r.live = have && on && (!p.freq || p.positions[t] >= 0) && (r.kind == 0 || (r.slot >= 0 && r.slot < p.total_slots));
-        r.src = r.kind == 0   ? p.q + t * p.q_token + r.h * p.q_head
-                : r.kind == 1 ? p.k + t * p.k_token + r.h * p.k_head
-                              : p.v + t * p.v_token + r.h * p.v_head;
+        r.kind = 0;
+        r.h = row;
+        r.live = here && row < r1;
+        if (KV && row >= p.q_heads) {
+            r.kind = row < p.q_heads + p.heads ? 1 : 2;
+            r.h = row - p.q_heads - (r.kind == 2 ? p.heads : 0);
+            r.live = stored && row < r1;
+            r.src = r.kind == 1 ? p.k + t * p.k_token + r.h * p.k_head : p.v + t * p.v_token + r.h * p.v_head;
+        } else {
+            r.src = p.q + t * p.q_token + r.h * p.q_head;
+        }
         r.raw = make_uint4(0u, 0u, 0u, 0u);
-        if (have && on) r.raw = *reinterpret_cast<const uint4*>(r.src + col);
+        if (r.live) r.raw = *reinterpret_cast<const uint4*>(r.src + col);
         return r;
     };
-    Row next = load(0);
+    Row next = load(r0 + sub);
+
+    float2 w[8];  // of the lane's columns (of its pairs, the first four, where these lie together)
+    uint32_t turned = 0;  // bit i: w[i] is of a column (of a pair) that turns
     if (p.freq) {
         for (int e = threadIdx.x; e < nt * p.half; e += kRowThreads) {
-            const int tt = div_by(e, p.by_half.m, p.by_half.s), i = e - tt * p.half;
+            const int et = div_by(e, p.by_half.m, p.by_half.s), i = e - et * p.half;
             const double turns = p.freq[i] * 0.15915494309189533577;  // of 2 pi
             const int64_t f = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-            const uint64_t w = (uint64_t)(int64_t)p.positions[t0 + tt] * (uint64_t)f;
+            const uint64_t phase = (uint64_t)(int64_t)p.positions[t0 + et] * (uint64_t)f;
             float s, c;
-            sincospif((float)(int32_t)(w >> 32) * 4.656612873077393e-10f, &s, &c);  // 2 / 2^32
+            sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);  // 2 / 2^32
             turn[e] = make_float2(c * p.magnitude, s * p.magnitude);
         }
         __syncthreads();
+        const float2* cs = turn + tt * p.half;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = col + (p.interleaved ? 2 * i : i);
+            const bool does = on && at < 2 * p.half && (!p.interleaved || i < 4);
+            turned |= does ? 1u << i : 0u;
+            w[i] = does ? cs[p.interleaved ? at >> 1 : at < p.half ? at : at - p.half] : make_float2(1.f, 0.f);
+        }
     }
-    for (int n = 0; n < rounds; ++n) {
+    const int gap = p.half >> 3;
+    const int partner = (threadIdx.x & 31 & ~(LANES - 1)) + (lane < gap ? lane + gap : lane < 2 * gap ? lane - gap : lane);
+    if (p.freq && !p.interleaved && lane < gap && p.by_lane)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i].y = -w[i].y;
+
+    // (all lanes of a warp go round together: shuffles)
+    for (int row = r0; row < r1; row += step) {
         const Row cur = next;
-        if (n + 1 < rounds) next = load(n + 1);
-        const int tt = cur.tt, kind = cur.kind, h = cur.h, slot = cur.slot, t = t0 + tt;
+        if (row + step < r1) next = load(row + step + sub);
+        const int kind = cur.kind, h = cur.h;
         const bool live = cur.live;
         const uint4 raw = cur.raw;
-        const uint16_t* src = cur.src;
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = half_of<Ty>(raw, i);
         if (p.freq) {
-            const bool turns = kind < 2 && live;
-            const float2* cs = turn + tt * p.half;
+            const bool turns = !KV || kind < 2;
             if (p.interleaved) {
-                if (turns)
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2)
-                        if (col + i < 2 * p.half) {
-                            const float2 w = cs[(col + i) >> 1];
-                            const float a = x[i], b = x[i + 1];
-                            x[i] = a * w.x - b * w.y;
-                            x[i + 1] = a * w.y + b * w.x;
-                        }
-            } else if (p.by_lane) {
-                const int gap = p.half >> 3;
-                const int from = (threadIdx.x & 31 & ~(LANES - 1)) + (lane < gap ? lane + gap : lane < 2 * gap ? lane - gap : lane);
-                const uint4 o = make_uint4(__shfl_sync(0xffffffffu, raw.x, from), __shfl_sync(0xffffffffu, raw.y, from),
-                                           __shfl_sync(0xffffffffu, raw.z, from), __shfl_sync(0xffffffffu, raw.w, from));
-                if (turns && lane < 2 * gap)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 w = cs[lane < gap ? col + i : col + i - p.half];
-                        const float y = half_of<Ty>(o, i);
-                        x[i] = lane < gap ? x[i] * w.x - y * w.y : y * w.y + x[i] * w.x;
+                for (int i = 0; i < 4; ++i)
+                    if (turns && ((turned >> i) & 1u)) {
+                        const float a = x[2 * i], b = x[2 * i + 1];
+                        x[2 * i] = a * w[i].x - b * w[i].y;
+                        x[2 * i + 1] = a * w[i].y + b * w[i].x;
                     }
+            } else if (p.by_lane) {
+                const uint4 o = make_uint4(__shfl_sync(0xffffffffu, raw.x, partner), __shfl_sync(0xffffffffu, raw.y, partner),
+                                           __shfl_sync(0xffffffffu, raw.z, partner), __shfl_sync(0xffffffffu, raw.w, partner));
+                if (turns && turned)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = x[i] * w[i].x + half_of<Ty>(o, i) * w[i].y;
             } else {
                 // (partners by element, all read before any lane of the row writes: out may be x)
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int at = col + i < p.half ? col + i + p.half : col + i - p.half;
-                    y[i] = turns && col + i < 2 * p.half ? Ty::lo(src[at]) : 0.f;
+                    y[i] = turns && live && ((turned >> i) & 1u) ? Ty::lo(cur.src[at]) : 0.f;
                 }
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (turns && col + i < 2 * p.half) {
-                        const bool first = col + i < p.half;
-                        const float2 w = cs[first ? col + i : col + i - p.half];
-                        x[i] = first ? x[i] * w.x - y[i] * w.y : y[i] * w.y + x[i] * w.x;
-                    }
+                    if (turns && ((turned >> i) & 1u))
+                        x[i] = col + i < p.half ? x[i] * w[i].x - y[i] * w[i].y : x[i] * w[i].x + y[i] * w[i].y;
             }
         }
         const uint4 packed = make_uint4(Ty::pack(x[0], x[1]), Ty::pack(x[2], x[3]), Ty::pack(x[4], x[5]), Ty::pack(x[6], x[7]));
-        if (kind == 0) {
+        if (!KV || kind == 0) {
             if (live) *reinterpret_cast<uint4*>(p.q_out + t * p.o_token + h * p.o_head + col) = packed;
+            if (!KV || CODE == kCode16) continue;
         }
-        const int64_t pg = slot >> p.shift, sl = slot & ((1 << p.shift) - 1);
         const int64_t at = kind == 1 ? pg * p.kcp + h * p.kch + sl * p.kcs : pg * p.vcp + h * p.vch + sl * p.vcs;
         if constexpr (CODE == kCode16) {
             // (what is not rotated is copied bit for bit)
-            if (live && kind) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kind == 1 ? p.kc : p.vc) + at + col) =
+            if (live) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kind == 1 ? p.kc : p.vc) + at + col) =
                 p.freq && kind == 1 && col < 2 * p.half ? packed : raw;
         } else {
             uint32_t most = 0;  // magnitudes as integers: NaN and infinities are the largest
@@ -173,11 +184,12 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const __grid_cons
             uint32_t w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float a = x[4 * i] * inv, b = x[4 * i + 1] * inv, c = x[4 * i + 2] * inv, e = x[4 * i + 3] * inv;
+                const float a = __fmul_rn(x[4 * i], inv), b = __fmul_rn(x[4 * i + 1], inv);
+                const float c = __fmul_rn(x[4 * i + 2], inv), e = __fmul_rn(x[4 * i + 3], inv);
                 if constexpr (CODE == kCodeInt8) {
-                    w[i] = bad ? 0u
-                               : __byte_perm(__byte_perm(__float2int_rn(a), __float2int_rn(b), 0x0040),
-                                             __byte_perm(__float2int_rn(c), __float2int_rn(e), 0x0040), 0x5410);
+                    // the sum with 1.5 * 2^23 is rounded to a whole number, which is its low bits
+                    auto bits = [](float y) { return __float_as_uint(__fadd_rn(y, 12582912.f)); };
+                    w[i] = bad ? 0u : __byte_perm(__byte_perm(bits(a), bits(b), 0x0040), __byte_perm(bits(c), bits(e), 0x0040), 0x5410);
                 } else {
                     uint16_t lo, hi;
                     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -196,8 +208,12 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const __grid_cons
 
 template <typename Ty, int CODE>
 static cudaError_t launch_rows(const RowParams& p, dim3 grid, size_t smem, cudaStream_t s, bool pdl) {
-    return p.d <= 128 ? launch_kernel(kv_store_kernel<Ty, CODE, 16>, grid, dim3(kRowThreads), smem, s, pdl, p)
-                      : launch_kernel(kv_store_kernel<Ty, CODE, 32>, grid, dim3(kRowThreads), smem, s, pdl, p);
+    if constexpr (CODE == kCode16)
+        if (p.heads == 0)
+            return p.d <= 128 ? launch_kernel(kv_store_kernel<Ty, CODE, 16, false>, grid, dim3(kRowThreads), smem, s, pdl, p)
+                              : launch_kernel(kv_store_kernel<Ty, CODE, 32, false>, grid, dim3(kRowThreads), smem, s, pdl, p);
+    return p.d <= 128 ? launch_kernel(kv_store_kernel<Ty, CODE, 16, true>, grid, dim3(kRowThreads), smem, s, pdl, p)
+                      : launch_kernel(kv_store_kernel<Ty, CODE, 32, true>, grid, dim3(kRowThreads), smem, s, pdl, p);
 }
 
 static cudaError_t launch(RowParams& p, bool bf16, int code, int rot, int sms, cudaStream_t s, bool pdl) {
@@ -205,19 +221,19 @@ static cudaError_t launch(RowParams& p, bool bf16, int code, int rot, int sms, c
     p.by_lane = p.half % 8 == 0;
     p.rows = p.q_heads + 2 * p.heads;
     const int groups = kRowThreads / (p.d <= 128 ? 16 : 32);
-    // Tokens of a CTA: as many as its groups of lanes have rows for, up to eight rounds of them while the GPU stays
-    // full (cosines for all threads, loads a round ahead); a token's rows over several CTAs where tokens are too few.
-    int per = groups / p.rows;
-    per = per < 1 ? 1 : per > kRowTokens ? kRowTokens : per;
-    while (per * 2 <= kRowTokens && (int64_t)per * 2 * p.rows <= 8 * groups && p.tokens / (per * 2) >= 16 * sms) per *= 2;
-    const int ctas = (p.tokens + per - 1) / per;
+    // Tokens of a CTA, a power of two: as many as its groups of lanes have rows for, up to 24 rounds of them while
+    // the GPU stays full (a lane's cosines are read once, loads are a round ahead); a token's rows over several CTAs
+    // where tokens are too few.
+    while ((2 << p.per_shift) <= groups && (p.rows << p.per_shift) * 2 <= groups) ++p.per_shift;
+    while ((2 << p.per_shift) <= groups && (p.rows << p.per_shift) * 2 <= 24 * groups &&
+           (p.tokens >> (p.per_shift + 1)) >= 12 * sms)
+        ++p.per_shift;
+    const int per = 1 << p.per_shift, ctas = (p.tokens + per - 1) / per;
     int split = 1;
     while (ctas * split * 2 <= 4 * sms && (p.rows + split * 2 - 1) / (split * 2) >= groups) split *= 2;
-    p.per_cta = per;
-    p.row0s = (p.rows + split - 1) / split;
-    p.by_rows = fast_div(p.rows);
+    p.cta_rows = (p.rows + split - 1) / split;
     p.by_half = fast_div(p.half);
-    const dim3 grid((unsigned)ctas, (unsigned)((p.rows + p.row0s - 1) / p.row0s));
+    const dim3 grid((unsigned)ctas, (unsigned)((p.rows + p.cta_rows - 1) / p.cta_rows));
     const size_t smem = p.freq ? (size_t)per * p.half * sizeof(float2) : 0;
     if (bf16)
         return code == kCode16     ? launch_rows<Bf16, kCode16>(p, grid, smem, s, pdl)
