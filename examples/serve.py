@@ -1,21 +1,24 @@
 """Continuous batching on the GPU kernels: a small decoder with 4-bit weights
 answers prompts of different lengths from a paged cache.
 
-    python examples/serve.py [--requests 6] [--new 24] [--seed 0]
+    python examples/serve.py [--requests 6] [--new 24] [--seed 0] [--cache bf16|int8|e4m3]
 
 Each step takes any mixture of prompts, prompt chunks and single tokens:
 
     w4a16_page_plan         pages, slots and positions of the step's tokens
     per layer
         w4a16_gemm          the fused q / k / v projection
-        w4a16_kv_write      the new keys and values into the cache
+        w4a16_rope_kv_write rotary positions, the new keys and values into the cache
         w4a16_paged_attention
         w4a16_gemm          output projection
         w4a16_gemm_gate_up_silu, w4a16_gemm    the MLP
     w4a16_gemm              the vocabulary head, for every request's last token
     w4a16_sample            temperature, top-k, top-p and min-p per request
 
-Norms and the rotary embedding are plain PyTorch, the weights random.
+`Server.verify` takes a tree of drafted tokens a request instead: one step gives
+the logits behind every node, the longest path that the model agrees with is
+kept, and its keys and values move to the places behind each other
+(w4a16_kv_read, w4a16_kv_write).  Norms are plain PyTorch, the weights random.
 """
 from __future__ import annotations
 
@@ -43,6 +46,7 @@ class Config:
     pages: int = 512
     max_pages: int = 64      # of a request
     window: int = 0
+    cache: str = "bf16"      # or "int8", "e4m3"
 
 
 class Linear:
@@ -65,13 +69,23 @@ def norm(x):
     return (x.float() * torch.rsqrt(x.float().pow(2).mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
 
 
-def rotate(x, positions):
-    """Rotary embedding of [T, heads, head_dim], in place."""
-    half = x.shape[-1] // 2
-    angle = positions.float()[:, None] * 10000.0 ** (-torch.arange(half, device=x.device).float() / half)
-    cos, sin = angle.cos()[:, None], angle.sin()[:, None]
-    a, b = x[..., :half].float(), x[..., half:].float()
-    x[..., :half], x[..., half:] = (a * cos - b * sin).to(x.dtype), (a * sin + b * cos).to(x.dtype)
+class Cache:
+    """Keys and values of a layer."""
+
+    def __init__(self, cfg: Config):
+        shape = (cfg.pages, cfg.kv_heads, cfg.page_size, cfg.head_dim)
+        dtype = {"bf16": torch.bfloat16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}[cfg.cache]
+        self.pages = [torch.zeros(shape, dtype=torch.int8 if dtype.itemsize == 1 else dtype, device="cuda").view(dtype)
+                      for _ in range(2)]
+        self.scales = {} if cfg.cache == "bf16" else {
+            n: torch.zeros(shape[:3], device="cuda") for n in ("k_scale", "v_scale")}
+
+    def move(self, source, target):
+        """Keys and values from the slots `source` to the slots `target`."""
+        _, heads, _, d = self.pages[0].shape
+        k, v = torch.empty(2, source.numel(), heads, d, dtype=torch.bfloat16, device="cuda")
+        w.w4a16_kv_read(*self.pages, source, k, v, **self.scales)
+        w.w4a16_kv_write(k, v, target, *self.pages, **self.scales)
 
 
 class Model:
@@ -84,25 +98,31 @@ class Model:
                         Linear(c.hidden, 2 * c.mlp, g, gate_up=True), Linear(c.mlp, c.hidden, g))
                        for _ in range(c.layers)]
         self.head = Linear(c.hidden, c.vocab, g)
-        shape = (c.pages, c.kv_heads, c.page_size, c.head_dim)
-        self.caches = [(torch.zeros(shape, dtype=torch.bfloat16, device="cuda"),
-                        torch.zeros(shape, dtype=torch.bfloat16, device="cuda")) for _ in range(c.layers)]
+        self.caches = [Cache(c) for _ in range(c.layers)]
+        self.frequencies, _ = w.w4a16_rope_frequencies(c.head_dim)
 
-    def __call__(self, tokens, plan, table, max_q):
-        """Logits [B, vocab] behind every request's last token; tokens [T] in request order."""
+    def __call__(self, tokens, plan, table, max_q, tree=None):
+        """Logits [B, vocab] behind every request's last token; tokens [T] in request order.  With a tree, (mask [T,
+        words], positions [T]) of the tokens as its nodes: logits [T, vocab] behind every node."""
         c = self.cfg
         q_start, kv_len, positions, slots, _ = plan
+        mask = None
+        if tree is not None:
+            mask, positions = tree
         x = self.embed[tokens.long()]
         T = x.shape[0]
-        for (qkv, o_proj, gate_up, down), (k_cache, v_cache) in zip(self.blocks, self.caches):
-            y = qkv(norm(x)).view(T, c.heads + 2 * c.kv_heads, c.head_dim)
-            rotate(y[:, :c.heads + c.kv_heads], positions)
-            q, k, v = y.split([c.heads, c.kv_heads, c.kv_heads], dim=1)
-            w.w4a16_kv_write(k, v, slots, k_cache, v_cache)
-            a = w.w4a16_paged_attention(q, k_cache, v_cache, table, q_start, kv_len, max_q, window=c.window)
+        for (qkv, o_proj, gate_up, down), cache in zip(self.blocks, self.caches):
+            q, k, v = qkv(norm(x)).view(T, -1, c.head_dim).split([c.heads, c.kv_heads, c.kv_heads], dim=1)
+            w.w4a16_rope_kv_write(q, k, v, positions, self.frequencies, slots, *cache.pages, q_out=q, **cache.scales)
+            a = w.w4a16_paged_attention(q, *cache.pages, table, q_start, kv_len, max_q, window=c.window, tree=mask,
+                                        **cache.scales)
             x = x + o_proj(a.view(T, -1))
             x = x + down(gate_up(norm(x)))
-        return self.head(norm(x[q_start[1:].long() - 1]))
+        return self.head(norm(x if tree is not None else x[q_start[1:].long() - 1]))
+
+
+def _starts(counts):
+    return [sum(counts[:i]) for i in range(len(counts))]
 
 
 class Server:
@@ -115,10 +135,9 @@ class Server:
         self.free = list(range(c.pages))
         self.past = [0] * requests
 
-    def step(self, tokens):
-        """Takes each request's new tokens (lists, none empty) and gives the logits behind them."""
+    def _plan(self, new):
+        """Pages, slots and positions of so many new tokens a request; what it needs of `free` is gone then."""
         c = self.cfg
-        new = [len(t) for t in tokens]
         up = lambda n: -(-n // c.page_size)
         pages = sum(up(p + n) - up(p) for p, n in zip(self.past, new))
         if pages > len(self.free):
@@ -129,8 +148,54 @@ class Server:
         plan = w.w4a16_page_plan(ints(self.past), ints(new), ints(self.free), self.table, c.page_size,
                                  max_tokens=sum(new))
         del self.free[:pages]
+        return plan
+
+    def step(self, tokens):
+        """Takes each request's new tokens (lists, none empty) and gives the logits behind them."""
+        new = [len(t) for t in tokens]
+        plan = self._plan(new)
         self.past = [p + n for p, n in zip(self.past, new)]
-        return self.model(ints([t for row in tokens for t in row]), plan, self.table, max(new))
+        tokens = torch.tensor([t for row in tokens for t in row], dtype=torch.int32, device="cuda")
+        return self.model(tokens, plan, self.table, max(new))
+
+    def verify(self, trees):
+        """Takes a tree a request, a list of (parent, token) with parents before children; node 0, parent -1, is the
+        request's last token, which is not in the cache yet, the others are drafts.  Gives each request's next tokens
+        (the drafts on the longest path that the model's likeliest tokens follow, and its token behind them)."""
+        new = [len(t) for t in trees]
+        seen = torch.zeros((sum(new), -(-max(new) // 32) * 32), dtype=torch.bool)
+        depth, at = [], 0
+        for n, nodes in zip(new, trees):
+            for i, (parent, _) in enumerate(nodes):
+                if parent >= 0:
+                    seen[at + i] = seen[at + parent]
+                seen[at + i, i] = True
+                depth.append(depth[at + parent] + 1 if parent >= 0 else 0)
+            at += n
+        mask = (seen.view(at, -1, 32).long() << torch.arange(32)).sum(-1).to(torch.int32).cuda()
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        positions = ints([p + d for p, n, s in zip(self.past, new, _starts(new)) for d in depth[s:s + n]])
+        plan = self._plan(new)
+        logits = self.model(ints([t for nodes in trees for _, t in nodes]), plan, self.table, max(new), (mask, positions))
+        best, out, source, target = logits.argmax(-1).tolist(), [], [], []
+        for r, (nodes, s) in enumerate(zip(trees, _starts(new))):
+            path = [0]
+            while (child := next((i for i, (p, t) in enumerate(nodes) if p == path[-1] and t == best[s + path[-1]]), None)):
+                path.append(child)
+            out.append([nodes[i][1] for i in path[1:]] + [best[s + path[-1]]])
+            source += [s + i for i in path]
+            target += range(s, s + len(path))
+            # pages behind the path's last position go back
+            up = lambda n: -(-n // self.cfg.page_size)
+            held = up(self.past[r] + len(path))
+            self.free += self.table[r, held:up(self.past[r] + new[r])].tolist()
+            self.table[r, held:] = -1
+            self.past[r] += len(path)
+        slots = plan[3]
+        if source != target:
+            for cache in self.model.caches:
+                cache.move(slots[ints(source).long()], slots[ints(target).long()])
+        return out
 
     def drop(self, keep):
         """Keeps the requests of these indices."""
@@ -166,8 +231,9 @@ def main():
     p.add_argument("--requests", type=int, default=6)
     p.add_argument("--new", type=int, default=24)
     p.add_argument("--seed", type=int, default=0)
+    p.add_argument("--cache", choices=["bf16", "int8", "e4m3"], default="bf16")
     a = p.parse_args()
-    model, g = Model(Config(), a.seed), torch.Generator().manual_seed(a.seed)
+    model, g = Model(Config(cache=a.cache), a.seed), torch.Generator().manual_seed(a.seed)
     prompts = [torch.randint(0, model.cfg.vocab, (n,), generator=g).tolist()
                for n in torch.randint(1, 300, (a.requests,), generator=g).tolist()]
     new = [a.new - i % 3 for i in range(a.requests)]

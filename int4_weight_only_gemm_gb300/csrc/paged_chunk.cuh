@@ -400,11 +400,6 @@ W4A16_DEVICE void add_taken_out(const PagedAttnParams& p, const ChunkPiece& pc, 
     }
 }
 
-// One of the barrier's arrivals, once this thread's asynchronous copies are done.
-W4A16_DEVICE void arrive_behind_copies(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // ---- keys and values of an 8-bit cache --------------------------------------
 // the type of the product with the values: their codes and weights in bf16, which has f32's range
 template <typename Ty, bool Q8>
@@ -464,7 +459,8 @@ static __device__ __noinline__ float2 weights_in_two_parts(uint32_t ts, const fl
 // The four unpacking warps.  A tile's codes lie in the upper half of its ring slot
 // and become 16-bit numbers over the whole slot, in the layout that tensor copies
 // of such would give: a thread takes the same 16 columns of 64 of every 32nd row.
-// Thread i turns the scales of key i into what the softmax takes.
+// Thread i brings the scales of key i, a tile ahead, and leaves them as the softmax
+// takes them.
 template <typename Ty, int D, bool ONE, bool TREE, bool E4M3>
 W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int toks, unsigned char* smem, uint64_t* full,
                                uint64_t* raw, float* scales, volatile int* abort_flag) {
@@ -479,6 +475,22 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
     uint32_t e = 0, tile0 = 0;
     while (walk.next<ONE, TREE>(p, toks, pc)) {
         const uint32_t n = pc.take;
+        // of tile t: the page of key tid (-1: not there, or no row sees it), and the key's scales from that
+        const int* table = p.table + (int64_t)pc.b * p.table_stride;
+        const int first = (pc.it.t0 + pc.off) * kChKeys + tid;
+        auto page_of = [&](uint32_t t) {
+            const int j = first + (int)t * kChKeys, col = j >> p.shift;
+            return t < n && j >= pc.it.lo0 && j <= pc.it.e1 && col < p.columns ? __ldcg(table + col) : -1;
+        };
+        float ks, vs;
+        auto scales_of = [&](uint32_t t, int pg) {
+            const int64_t at = (first + (int)t * kChKeys) & ((1 << p.shift) - 1);
+            const bool there = pg >= 0 && pg < p.pages;
+            ks = there ? __ldcg(p.k_scale + pg * p.ksp + pc.hk * p.ksh + at * p.kss) : 0.f;
+            vs = there ? __ldcg(p.v_scale + pg * p.vsp + pc.hk * p.vsh + at * p.vss) : 0.f;
+        };
+        int pg = page_of(0);
+        uint32_t t = ~0u;  // scales of tile t + 1 are on their way, or t + 1 is 0
 #pragma unroll 1
         for (uint32_t i = 0; i < 2 * n; ++i, ++e) {
             // entry i is tile t's keys (values_at and keys_at of ChunkWalk's order), or values
@@ -523,12 +535,18 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
                 }
             };
             if (keys) {
-                const uint32_t t = !ONE ? i >> 1 : (i + 1) >> 1;
+                if (t == ~0u) {
+                    scales_of(0, pg);
+                    pg = page_of(1);
+                }
+                ++t;
                 float* sc = scales + ((tile0 + t) & 7) * 384 + tid;
-                const float f = finite_or_nan(sc[128]);
-                sc[0] = finite_or_nan(sc[0]) * p.scale2;
+                const float f = finite_or_nan(vs);
+                sc[0] = finite_or_nan(ks) * p.scale2;
                 sc[128] = f;
                 sc[256] = fabsf(f) < INFINITY ? f : 0.f;
+                scales_of(t + 1, pg);
+                pg = page_of(t + 2);
             }
             if (!(BF || !keys ? unpack(std::true_type{}) : unpack(std::false_type{}))) return;
             fence_proxy_async_smem();
@@ -561,7 +579,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     uint64_t* q_free = q_full + 1;
     uint64_t* join = q_free + 1;     // both warpgroups' maxima and sums are in ml
     uint64_t* done = join + 1;       // every MMA of the CTA is done
-    uint64_t* raw = done + 1;        // Q8: [NS] a slot's codes, and with keys both scales, are there
+    uint64_t* raw = done + 1;        // Q8: [NS] a slot's codes are there
     static_assert(((Q8 ? 3 : 2) * NS + 12) * 8 <= 384, "barriers");
     volatile uint32_t* miss = reinterpret_cast<volatile uint32_t*>(smem + L::kMissOff);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
@@ -576,7 +594,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(full + i, Q8 ? 4 : 1);  // (Q8: a lane of each unpacking warp arrives)
-            if constexpr (Q8) mbar_init(raw + i, 33);  // the tensor copies, and every lane's scales
+            if constexpr (Q8) mbar_init(raw + i, 1);
             mbar_init(empty + i, 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -799,19 +817,6 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     if (lane < boxes)
                         tma_load_4d(smem + L::kRingOff + sl * L::kTile + L::kTile / 2 + lane * rows * D, kv ? &tmap_v : &tmap_k, 0,
                                     slot, pc.hk, pg, raw + sl);
-                    if (kv == 0) {  // the scales of keys 32 x + lane; what no row sees keeps any number
-                        const int sh = p.shift < 7 ? p.shift : 7, j0 = (pc.it.t0 + pc.off + t) * kChKeys;
-                        float* sc = scales + ((tile0 + t) & 7) * 384;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int row = 32 * x + lane, g = __shfl_sync(0xffffffffu, pg, row >> sh);
-                            if (g >= p.pages) continue;
-                            const int64_t at = (j0 + row) & (page - 1);
-                            cp_async_4(sc + row, p.k_scale + g * p.ksp + pc.hk * p.ksh + at * p.kss);
-                            cp_async_4(sc + 128 + row, p.v_scale + g * p.vsp + pc.hk * p.vsh + at * p.vss);
-                        }
-                    }
-                    arrive_behind_copies(raw + sl);
                 } else if (lane < boxes) {
                     unsigned char* dst = smem + L::kRingOff + sl * L::kTile + lane * rows * 128;
 #pragma unroll
