@@ -1,0 +1,167 @@
+"""Rotary positions, the 8-bit cache and drafted trees where calls meet: captures and replays, streams side by side,
+offsets past 32 bits, many requests, lengths at their ends.  Tolerances as in test_drafts.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import drafts
+from test_drafts import Draft, partner_sum
+from test_serving import f64, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w():
+    import int4_weight_only_gemm_gb300 as w
+    return w
+
+
+def step_of(w, a, seed, new):
+    """Queries, keys and values of new tokens behind the requests' context, and the call that rotates, stores and attends."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    T, d, Hkv = int(sum(new)), a.d, a.Hkv
+    qkv = torch.randn(T, a.Hq + 2 * Hkv, d, generator=g, device="cuda").to(a.dt)
+    positions = torch.cat([torch.arange(L - n, L) for L, n in zip(a.L.tolist(), new)])
+    slots = torch.cat([torch.from_numpy(a.table[b])[torch.arange(L - n, L) // a.page] * a.page + torch.arange(L - n, L) % a.page
+                       for b, (L, n) in enumerate(zip(a.L.tolist(), new))])
+    f, _ = w.w4a16_rope_frequencies(d)
+    st = dict(qkv=qkv, pos=i32(positions), slots=i32(slots), q=torch.empty_like(qkv[:, :a.Hq]).contiguous(),
+              table=i32(a.table), start=i32(a.q_start), L=i32(a.L), out=torch.zeros(T, a.Hq, d, dtype=a.dt, device="cuda"))
+
+    st["tree"] = None if a.tree is None else i32(a.tree)
+
+    def call():
+        q, k, v = st["qkv"].split([a.Hq, Hkv, Hkv], dim=1)
+        scales = dict(k_scale=a.ks, v_scale=a.vs) if a.code else {}
+        w.w4a16_rope_kv_write(q, k, v, st["pos"], f, st["slots"], a.kc, a.vc, q_out=st["q"], **scales)
+        w.w4a16_paged_attention(st["q"], a.kc, a.vc, st["table"], st["start"], st["L"], int(max(new)), out=st["out"],
+                                tree=st["tree"], **scales)
+        return st["out"]
+
+    return st, call
+
+
+@pytest.mark.parametrize("code", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("lens,tree", [([(300, 1), (40, 1)], None), ([(200, 40), (9, 3)], None), ([(500, 3), (20, 2)], "tree"),
+                                       ([(300, 70), (30, 40)], "tree")])
+def test_captured_and_replayed_beside_eager_calls(w, code, lens, tree):
+    a = Draft(lens, 8, 2, 128, 16, "bf16", code, tree, seed=1)
+    st, call = step_of(w, a, 5, a.n)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed in (6, 7):
+        st["qkv"].copy_(torch.randn(st["qkv"].shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda"))
+        want = call().clone()
+        state = [x.clone() for x in (a.kc.view(torch.uint8), a.vc.view(torch.uint8))]
+        st["out"].zero_()
+        graph.replay()
+        assert torch.equal(st["out"], want)
+        assert all(torch.equal(x, y.view(torch.uint8)) for x, y in zip(state, (a.kc, a.vc)))
+    # replays beside calls of the same kind on another stream
+    other = Draft(lens, 8, 2, 128, 16, "bf16", code, tree, seed=2)
+    so, oc = step_of(w, other, 8, other.n)
+    ref = oc().clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        graph.replay()
+        with torch.cuda.stream(s):
+            oc()
+    torch.cuda.synchronize()
+    assert torch.equal(so["out"], ref) and torch.equal(st["out"], want)
+    assert w.w4a16_last_device_status() == 0
+
+
+@pytest.mark.parametrize("lens,tree", [([(300, 1)], None), ([(250, 70)], None), ([(250, 3)], "tree"), ([(250, 70)], "tree")])
+def test_offsets_past_32_bits(w, lens, tree):
+    """A cache whose last pages lie more than 2^31 elements behind its first."""
+    a = Draft(lens, 4, 2, 128, 128, "bf16", "int8", tree, seed=3)
+    held = a.kc.shape[0]
+    pages = 66000
+    assert pages * 2 * 128 * 128 > 2 ** 31
+    small = [a.kc, a.vc, a.ks, a.vs]
+    big = [torch.zeros((pages,) + x.shape[1:], dtype=x.dtype, device="cuda") for x in small]
+    for x, y in zip(big, small):
+        x[-held:] = y
+    kc, vc, ks, vs = big
+    out, lse = a.run(w)
+    a.kc, a.vc, a.ks, a.vs = big
+    a.table = np.where(a.table >= 0, a.table + pages - held, -1)
+    again, lse2 = a.run(w)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    # writing and reading there
+    k = torch.randn(2, 5, 2, 128, device="cuda").to(torch.bfloat16)
+    slots = torch.tensor([pages * 128 - 1 - i for i in range(5)], dtype=torch.int32, device="cuda")
+    w.w4a16_kv_write(k[0], k[1], slots, kc, vc, k_scale=ks, v_scale=vs)
+    back = torch.zeros_like(k)
+    w.w4a16_kv_read(kc, vc, slots, back[0], back[1], k_scale=ks, v_scale=vs)
+    codes, scale = drafts.quantise(k.float().cpu().numpy(), "int8")
+    ref = drafts.values(codes, scale, "int8")
+    assert np.all(np.abs(f64(back) - ref) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(ref))
+    assert not kc[0].any() and not vc[0].any() and not ks[0].any()
+
+
+@pytest.mark.parametrize("code,tree", [("int8", None), ("e4m3", "tree"), (None, "tree"), ("int8", "any")])
+def test_many_requests(w, code, tree):
+    """More requests than a CTA has threads, most of them short, some without a token."""
+    r = np.random.default_rng(4)
+    lens = [(int(p), int(n)) for p, n in zip(r.integers(0, 40, 700), r.integers(0, 4, 700))]
+    lens[350] = (900, 2)
+    if tree is None:
+        lens[20], lens[699] = (100, 40), (10, 60)
+    a = Draft(lens, 4, 2, 64, 16, "bf16", code, tree, seed=5)
+    a.check(*a.run(w))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("heads,kv_heads,lens", [(64, 1, [(33, 1), (200, 2)]), (9, 1, [(65, 1)]), (12, 12, [(10, 16), (7, 8)]),
+                                                 (24, 3, [(129, 1), (128, 2)]), (16, 1, [(500, 1), (3, 1)])])
+def test_rows_at_the_kernels_limits(w, code, heads, kv_heads, lens):
+    """8, 9, 16 and more query rows a key head, in one call and alone."""
+    for d, dtype in ((64, "fp16"), (128, "bf16")):
+        a = Draft(lens, heads, kv_heads, d, 16, dtype, code, seed=6)
+        a.check(*a.run(w))
+        a.check(*a.run(w, 30), 30)
+
+
+def test_all_zero_and_equal_scales(w):
+    """Rows of zeros (scale 0) are values of zero, not of nothing."""
+    for lens in ([(50, 1)], [(50, 40)]):
+        a = Draft(lens, 8, 2, 128, 16, "bf16", "int8", seed=7)
+        a.vs[:] = 0
+        out, lse = a.run(w)
+        a.check(out, lse)
+        assert (out == 0).all() and torch.isfinite(lse).all()
+        a.ks[:] = 0    # every score 0: the mean of the values
+        a.vs[:] = 0.01
+        a.check(*a.run(w))
+
+
+def test_more_nodes_than_a_row_tile_and_the_widest_mask(w):
+    """2048 nodes, the most that a mask has words for, as chains of chains; and masks wider than the tree."""
+    n = 2048
+    a = Draft([(20, n)], 1, 1, 64, 64, "bf16", None, "chain", seed=8)
+    assert a.words == 64
+    out, lse = a.run(w)
+    b = Draft([(20, n)], 1, 1, 64, 64, "bf16", seed=8)
+    b.check(out, lse)
+    c = Draft([(40, 5), (3, 30)], 4, 2, 128, 16, "bf16", "int8", "tree", words=64, seed=9)
+    c.check(*c.run(w))
+
+
+def test_rope_in_place_on_a_side_stream(w):
+    x = torch.randn(500, 12, 128, device="cuda").to(torch.bfloat16)
+    kept = f64(x)
+    pos = np.arange(500) * 37
+    f, m = w.w4a16_rope_frequencies(128, scaling="ramp", factor=8.0, length=4096)
+    positions = i32(pos)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    w.w4a16_rope(x, positions, f, magnitude=m, out=x, stream=s)
+    s.synchronize()
+    ref = drafts.rotate(kept, pos, f64(f), False, m)
+    assert np.all(np.abs(f64(x) - ref) <= m * 2.0 ** -21 * partner_sum(kept, 64, False) + 2.0 ** -8 * np.abs(ref))
