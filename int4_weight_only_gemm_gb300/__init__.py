@@ -407,7 +407,7 @@ _READ_ARGS = struct.Struct("=7Q16qiiiiiiiI")
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _CODES = {torch.int8: 3, torch.float8_e4m3fn: 4}  # of 8-bit caches
 _SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
-_Tensor, _I32 = torch.Tensor, torch.int32  # (looked up some ten times a call)
+_Tensor, _I32, _F32 = torch.Tensor, torch.int32, torch.float32  # (looked up some ten times a call)
 
 
 def _int32(t, name, n=None):
@@ -543,12 +543,13 @@ def _caches(k_cache, v_cache, dtype):
     return shape, ks, vs
 
 
-def _scale(t, name, shape):
+def _scale(t, name, pages, heads, page):
     """Strides of an 8-bit cache's scales [pages, heads, page_size] f32."""
-    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not torch.float32:
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _F32:
         raise ValueError(f"{name} must be a float32 CUDA tensor")
-    if t.shape != shape[:3]:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape[:3])}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != pages or shape[1] != heads or shape[2] != page:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(pages, heads, page)}")
     return t.stride()
 
 
@@ -558,12 +559,13 @@ def _codes(k_cache, k_scale, v_scale, dtype):
         raise ValueError("k_cache must be a CUDA tensor")
     cdtype = k_cache.dtype
     code = _CODES.get(cdtype)
-    if dtype not in _DTYPES or dtype is torch.float32:
+    number = _DTYPES.get(dtype)
+    if number is None or number == 2:
         raise ValueError(f"keys, values and queries must be bf16 or fp16, got {dtype}")
     if code is None:
         if k_scale is not None or v_scale is not None:
             raise ValueError(f"a cache of {cdtype} has no scales")
-        return dtype, _DTYPES[dtype]
+        return dtype, number
     if k_scale is None or v_scale is None:
         raise ValueError(f"a cache of {cdtype} needs k_scale and v_scale")
     return cdtype, code
@@ -678,14 +680,16 @@ def _kv_store(q, k, v, positions, frequencies, slot_map, k_cache, v_cache, q_out
         Hq = qshape[1]
         if qshape[0] != T or qshape[2] != d or oshape != qshape:
             raise ValueError(f"q {tuple(qshape)} and q_out {tuple(oshape)} do not go with k {tuple(shape)}")
-    no = (0, 0, 0)
-    kss, vss = (no, no) if k_scale is None else (_scale(k_scale, "k_scale", cshape), _scale(v_scale, "v_scale", cshape))
+    kss = vss = (0, 0, 0)
+    ksp = vsp = 0
+    if k_scale is not None:
+        kss, vss = _scale(k_scale, "k_scale", pages, heads, page), _scale(v_scale, "v_scale", pages, heads, page)
+        ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
     turn = frequencies is not None
     args = _STORE_ARGS.pack(q.data_ptr() if Hq else 0, k.data_ptr(), v.data_ptr(), q_out.data_ptr() if Hq else 0,
                             _int32(positions, "positions", T) if turn else 0, _frequencies(frequencies) if turn else 0,
                             _int32(slot_map, "slot_map", T), k_cache.data_ptr(), v_cache.data_ptr(),
-                            0 if k_scale is None else k_scale.data_ptr(), 0 if v_scale is None else v_scale.data_ptr(),
-                            qt, qh, ot, oh, kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, Hq, heads, d,
+                            ksp, vsp, qt, qh, ot, oh, kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, Hq, heads, d,
                             2 * frequencies.numel() if turn else 0, int(interleaved), pages, page, _DTYPES[dtype], code,
                             magnitude, flags)
     _raise(load_library().w4a16_kv_store(args, _stream(stream, k.get_device())),
@@ -710,11 +714,13 @@ def w4a16_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_map: torch.
     pages, ch, page, cd = cshape
     if ch != heads or cd != d:
         raise ValueError(f"caches of {ch} heads of {cd} do not go with k of {heads} heads of {d}")
-    no = (0, 0, 0)
-    kss, vss = (no, no) if k_scale is None else (_scale(k_scale, "k_scale", cshape), _scale(v_scale, "v_scale", cshape))
-    args = _READ_ARGS.pack(k_cache.data_ptr(), v_cache.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
-                           0 if v_scale is None else v_scale.data_ptr(), _int32(slot_map, "slot_map", T), k.data_ptr(),
-                           v.data_ptr(), kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, heads, d, pages, page,
+    kss = vss = (0, 0, 0)
+    ksp = vsp = 0
+    if k_scale is not None:
+        kss, vss = _scale(k_scale, "k_scale", pages, heads, page), _scale(v_scale, "v_scale", pages, heads, page)
+        ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
+    args = _READ_ARGS.pack(k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, _int32(slot_map, "slot_map", T),
+                           k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, heads, d, pages, page,
                            _DTYPES[dtype], code, flags)
     _raise(load_library().w4a16_kv_read(args, _stream(stream, k.get_device())), "w4a16_kv_read")
     return k, v
@@ -754,16 +760,18 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
         cshape, (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, cdtype)
         kss = vss = (0, 0, 0)
+        ksp = vsp = words = node = 0
         if k_scale is not None:
-            kss, vss = _scale(k_scale, "k_scale", cshape), _scale(v_scale, "v_scale", cshape)
-        words = node = 0
+            pages, Hkv, page, _ = cshape
+            kss, vss = _scale(k_scale, "k_scale", pages, Hkv, page), _scale(v_scale, "v_scale", pages, Hkv, page)
+            ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
         if tree is not None:
             tshape, (node, _) = _strided(tree, "tree", _I32, 2)
             words = tshape[1]
             if tshape[0] != T or words == 0:
                 raise ValueError(f"tree has shape {tuple(tshape)}, expected ({T}, words)")
-        ext = _EXT_ARGS.pack(0 if k_scale is None else k_scale.data_ptr(), 0 if v_scale is None else v_scale.data_ptr(),
-                             0 if tree is None else tree.data_ptr(), *kss, *vss, node if T > 1 else words, code, words)
+        ext = _EXT_ARGS.pack(ksp, vsp, 0 if tree is None else tree.data_ptr(), *kss, *vss, node if T > 1 else words, code,
+                             words)
     pages, Hkv, page, cd = cshape
     if cd != d or dtype not in _DTYPES:
         raise ValueError(f"caches with heads of {cd} do not go with q with heads of {d} in {dtype}")

@@ -96,10 +96,12 @@ cudaError_t launch_paged_attn(const w4a16_paged_attention_args& a, const w4a16_p
     p.small_rows = small ? kSmallRows : 0;
     p.after_small = small;
     if (small) {
-        // the most query rows that a request of this kernel can have
-        const int rows = p.G * (a.max_q < kSmallRows / p.G ? a.max_q : kSmallRows / p.G);
+        // Over an 8-bit cache, the form for up to 8 rows where no request of this kernel has more (and none with more
+        // than max_q says gets there: partial results are of 8 rows).
+        const bool few = p.k_scale && p.G * (a.max_q < kSmallRows / p.G ? a.max_q : kSmallRows / p.G) <= 8;
+        if (few) p.small_rows = 8;
         const cudaError_t e =
-            p.k_scale ? (p.tree ? launch_paged_decode8<true> : launch_paged_decode8<false>)(p, bf16, a.head_dim, rows <= 8, sms, s, pdl)
+            p.k_scale ? (p.tree ? launch_paged_decode8<true> : launch_paged_decode8<false>)(p, bf16, a.head_dim, few, sms, s, pdl)
                       : (p.tree ? launch_paged_decode<true> : launch_paged_decode<false>)(p, bf16, a.head_dim, sms, s, pdl);
         if (e != cudaSuccess) return e;
         note_launch();

@@ -563,6 +563,10 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedAttnParams p) {
     using L = Ch<D, ONE, Q8>;
     constexpr int NS = L::kSlots;
+    // The loops over a row's scores are rolled, and weights in two parts lie over their own scores' columns: for an
+    // 8-bit cache since the code of the CTA's roles has to fit the instruction caches (a 2048-token chunk: 416 us with
+    // the loops written out, 283 so), for trees since their short calls run every line once (WRITTEN).
+    constexpr bool SPREAD = Q8 || TREE;
     extern __shared__ __align__(1024) unsigned char smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
         if (threadIdx.x == 0) atomicExch(&g_chunk_status, (int)W4A16_ECUDA);
@@ -918,7 +922,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     ++np[g];
                     tc_fence_after();
                     const uint32_t va = tile_at(L::kRows + sl, kDescV), pa = tm + L::kTS + 128 * g, od = tm + L::kTO + D * g;
-                    if constexpr (Q8) {
+                    if constexpr (SPREAD) {
                         if (two) {
                             pv_block<true>(od, pa, va, id_o, k > 0 ? 1u : 0u);
                             pv_block<true>(od, pa + 16, va, id_o, 1u);
@@ -1066,9 +1070,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 uint32_t sv[2][32];
                 tmem_ld32(ts, sv[0]);
                 float mx = m, mo = m;
-                // (Q8: 64 scores a round, since with all 128 written out the code of the CTA's roles no longer fits
-                // the instruction caches: 416 us for the chunk below)
-#pragma unroll(Q8 ? 1 : 2)
+#pragma unroll(SPREAD ? 1 : 2)
                 for (int x0 = 0; x0 < 4; x0 += 2)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
@@ -1124,6 +1126,14 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                         pk[i] = Ty::pack(a.x, a.y);
                     }
                 };
+                auto second = [&](const uint32_t* v, const uint32_t* pk, uint32_t* pl) {  // what the first parts lack
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = exp2_approx(fmaf(__uint_as_float(v[2 * i]), scale2, -base));
+                        const float b = exp2_approx(fmaf(__uint_as_float(v[2 * i + 1]), scale2, -base));
+                        pl[i] = Ty::pack(a - Ty::lo(pk[i]), b - Ty::hi(pk[i]));
+                    }
+                };
                 if constexpr (Q8) {
                     if (Ty::idesc_type == 1 && two) {
                         l0 = weights_in_two_parts(ts, kc, vc, base);
@@ -1151,6 +1161,21 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                                 tmem_st16(ts + 32 * x + 16, lo);
                             }
                     }
+                } else if constexpr (SPREAD) {
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t pk[16], pl[16];
+                        tmem_ld32(ts + 32 * x, sv[0]);
+                        tmem_wait_ld();
+                        weights(sv[0], pk);
+                        if (!two) {
+                            tmem_st16(ts + 16 * x, pk);
+                        } else {
+                            second(sv[0], pk, pl);
+                            tmem_st16(ts + 32 * x, pk);
+                            tmem_st16(ts + 32 * x + 16, pl);
+                        }
+                    }
                 } else {
                 tmem_ld32(ts, sv[0]);
                 if (!two) {
@@ -1169,12 +1194,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     for (int x = 0; x < 4; ++x) {
                         tmem_wait_ld();
                         weights(sv[x & 1], pk[x]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float a = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i]), scale2, -base));
-                            const float b = exp2_approx(fmaf(__uint_as_float(sv[x & 1][2 * i + 1]), scale2, -base));
-                            pl[x][i] = Ty::pack(a - Ty::lo(pk[x][i]), b - Ty::hi(pk[x][i]));
-                        }
+                        second(sv[x & 1], pk[x], pl[x]);
                         if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[(x + 1) & 1]);
                     }
 #pragma unroll
