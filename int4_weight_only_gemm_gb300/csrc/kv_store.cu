@@ -11,7 +11,13 @@
 // is a 64-bit fraction F of a turn a position, so position * F modulo 2^64 is the
 // fraction of a turn, without rounding; its top 32 bits go to sincospi.
 //
-// Bound: HBM, each row read and written once.
+// Bound: HBM, each row read and written once; what is left to it is the latency of a
+// round (loads are one ahead; two ahead cost more registers than they gain) and, in
+// 8 bits, issue slots (196 instructions a warp for two rows, 62 % of the slots).
+// Measured: 16301 tokens of 40 heads of 128 in bf16 (334 MB), half of each head
+// turned: 67-70 us, 4.9 TB/s, the whole head in halves 68; keys and values of 16301
+// tokens, 8 heads of 128, to e4m3: 34 us (101 MB), with the read-back of the cache
+// 53; 64 tokens of 32 + 8 heads, turned and to int8: 6.7 us alone, 9.7 us a call.
 #include <cmath>
 
 #include "codes.cuh"
@@ -49,9 +55,11 @@ W4A16_DEVICE float half_of(const uint4& v, int i) {
     return i & 1 ? Ty::hi(x) : Ty::lo(x);
 }
 
-// KV: keys and values too, else queries alone
-template <typename Ty, int CODE, int LANES, bool KV>
-__global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_constant__ RowParams p) {
+// KV: keys and values too, else queries alone; TURN: with rotary positions.  CTAs an SM as the registers allow.  Without
+// turns, five of 48 registers: 16301 tokens stored in 8 bits and read back 53 us, with six 57, with the three that the
+// kernel with turns has 57.
+template <typename Ty, int CODE, int LANES, bool KV, bool TURN>
+__global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : KV ? 3 : 4) kv_store_kernel(const __grid_constant__ RowParams p) {
     extern __shared__ float2 turn[];  // [token][pair] cosine and sine
     pdl_wait();
     pdl_launch_dependents();
@@ -62,10 +70,25 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
     const int t0 = (int)blockIdx.x << p.per_shift, t = t0 + tt, nt = min(1 << p.per_shift, p.tokens - t0);
     const int r0 = (int)blockIdx.y * p.cta_rows, r1 = min(r0 + p.cta_rows, p.rows);
     const bool on = t < p.tokens && col < p.d;
-    const bool here = on && (!p.freq || p.positions[t] >= 0);
+    const bool here = on && (!TURN || p.positions[t] >= 0);
     const int slot = KV && t < p.tokens ? p.slots[t] : -1;
     const bool stored = here && slot >= 0 && slot < p.total_slots;
+    // what of an address goes by the token
     const int64_t pg = slot >> p.shift, sl = slot & ((1 << p.shift) - 1);
+    const uint16_t *qs = p.q + t * p.q_token + col, *ks = nullptr, *vs = nullptr;
+    int64_t kat = 0, vat = 0;
+    float *kscale = nullptr, *vscale = nullptr;
+    if constexpr (KV) {
+        ks = p.k + t * p.k_token + col;
+        vs = p.v + t * p.v_token + col;
+        kat = pg * p.kcp + sl * p.kcs + col;
+        vat = pg * p.vcp + sl * p.vcs + col;
+        if constexpr (CODE != kCode16) {
+            kscale = p.ks + pg * p.ksp + sl * p.kss;
+            vscale = p.vs + pg * p.vsp + sl * p.vss;
+        }
+    }
+    uint16_t* const qo = p.q_out + t * p.o_token + col;
 
     struct Row {
         int kind, h;  // 0 query, 1 key, 2 value; head
@@ -82,19 +105,19 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
             r.kind = row < p.q_heads + p.heads ? 1 : 2;
             r.h = row - p.q_heads - (r.kind == 2 ? p.heads : 0);
             r.live = stored && row < r1;
-            r.src = r.kind == 1 ? p.k + t * p.k_token + r.h * p.k_head : p.v + t * p.v_token + r.h * p.v_head;
+            r.src = (r.kind == 1 ? ks : vs) + r.h * (r.kind == 1 ? p.k_head : p.v_head);
         } else {
-            r.src = p.q + t * p.q_token + r.h * p.q_head;
+            r.src = qs + r.h * p.q_head;
         }
         r.raw = make_uint4(0u, 0u, 0u, 0u);
-        if (r.live) r.raw = *reinterpret_cast<const uint4*>(r.src + col);
+        if (r.live) r.raw = *reinterpret_cast<const uint4*>(r.src);
         return r;
     };
     Row next = load(r0 + sub);
 
     float2 w[8];  // of the lane's columns (of its pairs, the first four, where these lie together)
     uint32_t turned = 0;  // bit i: w[i] is of a column (of a pair) that turns
-    if (p.freq) {
+    if constexpr (TURN) {
         for (int e = threadIdx.x; e < nt * p.half; e += kRowThreads) {
             const int et = div_by(e, p.by_half.m, p.by_half.s), i = e - et * p.half;
             const double turns = p.freq[i] * 0.15915494309189533577;  // of 2 pi
@@ -116,7 +139,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
     }
     const int gap = p.half >> 3;
     const int partner = (threadIdx.x & 31 & ~(LANES - 1)) + (lane < gap ? lane + gap : lane < 2 * gap ? lane - gap : lane);
-    if (p.freq && !p.interleaved && lane < gap && p.by_lane)
+    if (TURN && !p.interleaved && lane < gap && p.by_lane)
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i].y = -w[i].y;
 
@@ -130,7 +153,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = half_of<Ty>(raw, i);
-        if (p.freq) {
+        if constexpr (TURN) {
             const bool turns = !KV || kind < 2;
             if (p.interleaved) {
 #pragma unroll
@@ -152,7 +175,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int at = col + i < p.half ? col + i + p.half : col + i - p.half;
-                    y[i] = turns && live && ((turned >> i) & 1u) ? Ty::lo(cur.src[at]) : 0.f;
+                    y[i] = turns && live && ((turned >> i) & 1u) ? Ty::lo(cur.src[at - col]) : 0.f;
                 }
                 __syncwarp();
 #pragma unroll
@@ -163,14 +186,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
         }
         const uint4 packed = make_uint4(Ty::pack(x[0], x[1]), Ty::pack(x[2], x[3]), Ty::pack(x[4], x[5]), Ty::pack(x[6], x[7]));
         if (!KV || kind == 0) {
-            if (live) *reinterpret_cast<uint4*>(p.q_out + t * p.o_token + h * p.o_head + col) = packed;
+            if (live) *reinterpret_cast<uint4*>(qo + h * p.o_head) = packed;
             if (!KV || CODE == kCode16) continue;
         }
-        const int64_t at = kind == 1 ? pg * p.kcp + h * p.kch + sl * p.kcs : pg * p.vcp + h * p.vch + sl * p.vcs;
+        const int64_t at = (kind == 1 ? kat : vat) + h * (kind == 1 ? p.kch : p.vch);
         if constexpr (CODE == kCode16) {
             // (what is not rotated is copied bit for bit)
-            if (live) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kind == 1 ? p.kc : p.vc) + at + col) =
-                p.freq && kind == 1 && col < 2 * p.half ? packed : raw;
+            if (live) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kind == 1 ? p.kc : p.vc) + at) =
+                TURN && kind == 1 && col < 2 * p.half ? packed : raw;
         } else {
             uint32_t most = 0;  // magnitudes as integers: NaN and infinities are the largest
 #pragma unroll
@@ -179,9 +202,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
             for (int i = 1; i < LANES; i <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, i));
             const float top = CODE == kCodeInt8 ? 127.f : 448.f, amax = __uint_as_float(most);
             const bool none = most < (27u << 23), bad = most >= 0x7f800000u;  // below 2^-100
-            const float scale = bad ? __uint_as_float(0x7fffffffu) : none ? 0.f : __fdiv_rn(amax, top);
+            // amax / top: a quotient by a constant, put right by what it leaves (correct in the last place: Markstein, "Computation
+            // of elementary functions on the IBM RISC System/6000 processor", 1990; tried for every mantissa)
+            const float rcp = CODE == kCodeInt8 ? 1.f / 127.f : 1.f / 448.f, about = amax * rcp;
+            const float quotient = __fmaf_rn(__fmaf_rn(-about, top, amax), rcp, about);
+            const float scale = bad ? __uint_as_float(0x7fffffffu) : none ? 0.f : quotient;
             const float inv = bad || none ? 0.f : __fdiv_rn(top, amax);
-            uint32_t w[2];
+            uint32_t codes[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float a = __fmul_rn(x[4 * i], inv), b = __fmul_rn(x[4 * i + 1], inv);
@@ -189,18 +216,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
                 if constexpr (CODE == kCodeInt8) {
                     // the sum with 1.5 * 2^23 is rounded to a whole number, which is its low bits
                     auto bits = [](float y) { return __float_as_uint(__fadd_rn(y, 12582912.f)); };
-                    w[i] = bad ? 0u : __byte_perm(__byte_perm(bits(a), bits(b), 0x0040), __byte_perm(bits(c), bits(e), 0x0040), 0x5410);
+                    codes[i] = bad ? 0u : __byte_perm(__byte_perm(bits(a), bits(b), 0x0040), __byte_perm(bits(c), bits(e), 0x0040), 0x5410);
                 } else {
                     uint16_t lo, hi;
                     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
                     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(e), "f"(c));
-                    w[i] = bad ? 0u : (uint32_t)lo | (uint32_t)hi << 16;
+                    codes[i] = bad ? 0u : (uint32_t)lo | (uint32_t)hi << 16;
                 }
             }
             if (live && kind) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(kind == 1 ? p.kc : p.vc) + at + col) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(kind == 1 ? p.kc : p.vc) + at) = make_uint2(codes[0], codes[1]);
                 if (lane == 0)
-                    *(kind == 1 ? p.ks + pg * p.ksp + h * p.ksh + sl * p.kss : p.vs + pg * p.vsp + h * p.vsh + sl * p.vss) = scale;
+                    *((kind == 1 ? kscale : vscale) + h * (kind == 1 ? p.ksh : p.vsh)) = scale;
             }
         }
     }
@@ -208,12 +235,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_store_kernel(const __grid_c
 
 template <typename Ty, int CODE>
 static cudaError_t launch_rows(const RowParams& p, dim3 grid, size_t smem, cudaStream_t s, bool pdl) {
+    auto run = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kRowThreads), smem, s, pdl, p); };
+    const bool narrow = p.d <= 128;
     if constexpr (CODE == kCode16)
-        if (p.heads == 0)
-            return p.d <= 128 ? launch_kernel(kv_store_kernel<Ty, CODE, 16, false>, grid, dim3(kRowThreads), smem, s, pdl, p)
-                              : launch_kernel(kv_store_kernel<Ty, CODE, 32, false>, grid, dim3(kRowThreads), smem, s, pdl, p);
-    return p.d <= 128 ? launch_kernel(kv_store_kernel<Ty, CODE, 16, true>, grid, dim3(kRowThreads), smem, s, pdl, p)
-                      : launch_kernel(kv_store_kernel<Ty, CODE, 32, true>, grid, dim3(kRowThreads), smem, s, pdl, p);
+        if (p.heads == 0) return narrow ? run(kv_store_kernel<Ty, CODE, 16, false, true>) : run(kv_store_kernel<Ty, CODE, 32, false, true>);
+    if (!p.freq) return narrow ? run(kv_store_kernel<Ty, CODE, 16, true, false>) : run(kv_store_kernel<Ty, CODE, 32, true, false>);
+    return narrow ? run(kv_store_kernel<Ty, CODE, 16, true, true>) : run(kv_store_kernel<Ty, CODE, 32, true, true>);
 }
 
 static cudaError_t launch(RowParams& p, bool bf16, int code, int rot, int sms, cudaStream_t s, bool pdl) {

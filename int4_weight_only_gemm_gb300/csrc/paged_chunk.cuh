@@ -46,6 +46,21 @@
 // 5.2 TB/s, 47 us with the pages in L2.  150 tokens behind 8000 positions, 8 heads
 // over 2: 70 us, 0.97 ms with a NaN among their values.
 //
+// Over an 8-bit cache (Q8) tensor copies bring a tile's codes into the upper half
+// of its slot, and four more warps turn them into 16-bit numbers over the whole
+// slot: exact ones, keys in the queries' type, values in bf16.  A key's scale
+// multiplies its score in f32, a value's its weight (bf16, which has f32's range; in
+// two parts for rows of fewer than 256 positions, and always for fp16, whose 11 bits
+// one part of 8 would lose).  Bound: as above, with twice the instructions in a
+// softmax warp's turn, and with the unpacking of 32768 codes a key tile.  Measured:
+// the chunk above 280-287 us with int8 or e4m3, 408 in fp16; the 16 blocks 78 us.
+//
+// For a tree of drafted tokens (TREE) a row sees the positions before the new tokens
+// and the nodes that its bits say; the words with a tile's nodes are read at once.
+// Measured: 16 trees of 64 nodes over 4080 positions 76 us (285 MB, 68 GFLOP); one of
+// 13 over 2303 positions 22.4 us, of which ~2.6 go to the cut of the line, 1.8 to the
+// first keys, 8 to the five tiles of the longest piece and 7 to the join.
+//
 // Every wait is bounded: on a timeout the kernel records W4A16_ETIMEOUT, ends
 // its copies and MMAs, frees its tensor memory and returns.
 #pragma once
@@ -441,7 +456,7 @@ W4A16_DEVICE void scaled_weights(const uint32_t (&v)[32], const float* kc, const
     }
 }
 // Those of a row's 128 scores in two parts, for the rows of few positions: out of line, so that the loop of the long
-// ones fits the instruction caches (346 us with it, 387 without, for the chunk below).
+// ones fits the instruction caches (350 us instead of 379 for the chunk above, before the next steps).
 static __device__ __noinline__ float2 weights_in_two_parts(uint32_t ts, const float* kc, const float* vc, float base) {
     float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll 1
@@ -565,7 +580,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     constexpr int NS = L::kSlots;
     // The loops over a row's scores are rolled, and weights in two parts lie over their own scores' columns: for an
     // 8-bit cache since the code of the CTA's roles has to fit the instruction caches (a 2048-token chunk: 416 us with
-    // the loops written out, 283 so), for trees since their short calls run every line once (WRITTEN).
+    // the loops written out, 283 so), for trees since their short calls run most lines once (13 nodes: 24.5 us written
+    // out, 22.4 so; 16 trees of 64 nodes alike).
     constexpr bool SPREAD = Q8 || TREE;
     extern __shared__ __align__(1024) unsigned char smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
@@ -1139,7 +1155,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                         l0 = weights_in_two_parts(ts, kc, vc, base);
                     } else if (Ty::idesc_type == 1) {
 #pragma unroll 1
-                        for (int x = 0; x < 4; ++x) {  // (the next 32 ahead cost more code than they save time: 301 us)
+                        for (int x = 0; x < 4; ++x) {  // (the next 32 ahead cost more code than they save time: 301 us, 290 so)
                             uint32_t hi[16];
                             tmem_ld32(ts + 32 * x, sv[0]);
                             tmem_wait_ld();

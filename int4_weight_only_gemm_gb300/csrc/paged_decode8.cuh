@@ -2,9 +2,15 @@
 //
 //     s_j = scale log2(e) ks_j (q . kcode_j),  out = sum_j 2^(s_j - m) vs_j vcode_j / sum_j 2^(s_j - m)
 //
-// Bound: HBM, at half the bytes of a 16-bit cache, with the unpacking of the
-// codes close behind: a 16-key tile of 4.2 KB takes ~130 instructions a lane for
-// it.  The line of units and the joining of pieces are paged_line.cuh's.
+// Bound: HBM, at half the bytes of a 16-bit cache, with the instructions close
+// behind: a 16-key tile of 4.2 KB takes ~540, 240 of them to unpack the codes.  The
+// line of units and the joining of pieces are paged_line.cuh's.
+//
+// Measured, 32 query heads over 8 key heads of 128, bf16, 16-slot pages: 64 requests of
+// up to 8448 positions (612 MB) 117 us with int8, 5.2 TB/s (DRAM 67 %, the ALU pipe
+// 58 %, issue slots 59 %), 121 with e4m3, 113 in fp16; one request of 2304 positions
+// 11.4 us, which is what the host takes for a call.  With one CTA of 252 registers an
+// SM it was 226 us, with copies that compute their addresses one by one 146.
 //
 // Eight warps work without meeting, each with a ring of its own filled by 16-byte
 // asynchronous copies: codes, and 4 bytes a key and value for their scales.  The
