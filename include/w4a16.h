@@ -503,11 +503,14 @@ size_t w4a16_paged_attention_workspace_bytes(int tokens, int requests, int q_hea
  *     k[j][hk] = k_scale[page][hk][slot] * k_cache[page][hk][slot],  v alike
  *
  * The codes go into the products as they are, the scales in f32 (that of a key
- * to its scores, that of a value to its softmax weights, which are rounded to
- * bf16 for the product, in two parts where w4a16_paged_attention has two, and
- * always for fp16), so that neither keys nor values are rounded.  A scale that
- * is not finite stands for a key or a value of NaN; the e4m3 codes without a
- * value (0x7f, 0xff) count as +-480.  Strides of k_cache and v_cache count
+ * to its scores, that of a value to its softmax weights, which are rounded as
+ * w4a16_paged_attention rounds them), so that neither keys nor values are
+ * rounded.  In fp16 with more than 16 query rows a key head a weight is rounded, where
+ * that is more, by 2^-31 of what the token's largest score and the largest of its
+ * values' scales would make together, which shows where the token rests on values
+ * whose scales are 2^20 below the largest; scales above 2^100 overflow there.  A scale that is not finite stands
+ * for a key or a value of NaN; the e4m3 codes without a value (0x7f, 0xff) count
+ * as +-480.  Strides of k_cache and v_cache count
  * elements, multiples of 16; those of the scales are not negative (0: one scale
  * for all), and 4-byte alignment is all that they need.
  *

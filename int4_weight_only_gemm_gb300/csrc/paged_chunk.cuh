@@ -48,12 +48,11 @@
 //
 // Over an 8-bit cache (Q8) tensor copies bring a tile's codes into the upper half
 // of its slot, and four more warps turn them into 16-bit numbers over the whole
-// slot: exact ones, keys in the queries' type, values in bf16.  A key's scale
-// multiplies its score in f32, a value's its weight (bf16, which has f32's range; in
-// two parts for rows of fewer than 256 positions, and always for fp16, whose 11 bits
-// one part of 8 would lose).  Bound: as above, with twice the instructions in a
+// slot, exact ones of the queries' type.  A key's scale
+// multiplies its score in f32, a value's its weight, which is of the queries' type as
+// the codes are (in two parts for rows of fewer than 256 positions).  Bound: as above, with twice the instructions in a
 // softmax warp's turn, and with the unpacking of 32768 codes a key tile.  Measured:
-// the chunk above 280-287 us with int8 or e4m3, 408 in fp16; the 16 blocks 78 us.
+// the chunk above 280-287 us with int8 or e4m3, 299 in fp16; the 16 blocks 78 us.
 //
 // For a tree of drafted tokens (TREE) a row sees the positions before the new tokens
 // and the nodes that its bits say; the words with a tile's nodes are read at once.
@@ -100,9 +99,10 @@ struct Ch {
     static constexpr int kBarOff = kMlOff + 2048;
     static constexpr int kMissOff = kBarOff + 384;            // [8] pages of a tile that are not there
     static constexpr int kMiscOff = kMissOff + 64;
-    // Q8: scales of eight tiles [tile][keys', values', values' with 0 for what is not finite][128], and 128 ones
+    // Q8: scales of eight tiles [tile][keys', values', values' with 0 for what is not finite][128], 128 ones, and the
+    // largest of the values' scales [tile][unpacking warp]
     static constexpr int kScaleOff = kMiscOff + 128;
-    static constexpr int kSmem = kScaleOff + (Q8 ? (8 * 3 + 1) * 512 : 0);  // no static shared memory: the base is 1024-aligned
+    static constexpr int kSmem = kScaleOff + (Q8 ? (8 * 3 + 1) * 512 + 128 : 0);  // no static shared memory: the base is 1024-aligned
     static constexpr int kPartHalf = 128 * (D + 2);           // floats of one row tile's partial result
     static constexpr uint32_t kTS = 0, kTO = 256;             // tensor memory: S and P of both tiles, then O
 };
@@ -416,19 +416,21 @@ W4A16_DEVICE void add_taken_out(const PagedAttnParams& p, const ChunkPiece& pc, 
 }
 
 // ---- keys and values of an 8-bit cache --------------------------------------
-// the type of the product with the values: their codes and weights in bf16, which has f32's range
-template <typename Ty, bool Q8>
-struct PvType {
-    using type = Ty;
-};
-template <typename Ty>
-struct PvType<Ty, true> {
-    using type = Bf16;
-};
+// Weights carry their values' scales.  In bf16 these have f32's range.  In fp16 (for
+// fp16 queries, whose outputs a weight of 8 bits would spoil) the base that scores
+// are taken against goes by the sum of the largest score and the logarithm of the
+// largest scale (a power of two, out of 2^-96 .. 2^100) that the row has seen: a
+// weight is at most 2^14, what the largest score and the largest scale would make
+// at least 2^5, and a weight is rounded by 2^-11 of itself or by 2^-25.  (Two bf16
+// parts did it before: the chunk above 408 us.)
+constexpr float kChShift = 6.f;  // of the base: weights are up to 2^(8 + 6)
+W4A16_DEVICE float scale_log(float largest) {  // an exponent that the scale is not above
+    return fminf(fmaxf((float)((int)(__float_as_uint(largest) >> 23) - 126), -96.f), 100.f);
+}
 
-// Weights of 32 scores, times their values' scales, in bf16: hi, and with TWO what hi lacks; the sums l0 and l1 are of
-// the weights alone.
-template <bool TWO>
+// Weights of 32 scores, times their values' scales: hi, and with TWO what hi lacks; the sums l0 and l1 are of the weights
+// alone.
+template <typename Ty, bool TWO>
 W4A16_DEVICE void scaled_weights(const uint32_t (&v)[32], const float* kc, const float* vc, float2 nb, float2& l0, float2& l1,
                                  uint32_t (&hi)[16], uint32_t* lo) {
 #pragma unroll
@@ -447,24 +449,25 @@ W4A16_DEVICE void scaled_weights(const uint32_t (&v)[32], const float* kc, const
         l1 = add2(l1, b);
         a = mul2(a, make_float2(d.x, d.y));
         b = mul2(b, make_float2(d.z, d.w));
-        hi[i] = Bf16::pack(a.x, a.y);
-        hi[i + 1] = Bf16::pack(b.x, b.y);
+        hi[i] = Ty::pack(a.x, a.y);
+        hi[i + 1] = Ty::pack(b.x, b.y);
         if constexpr (TWO) {
-            lo[i] = Bf16::pack(a.x - Bf16::lo(hi[i]), a.y - Bf16::hi(hi[i]));
-            lo[i + 1] = Bf16::pack(b.x - Bf16::lo(hi[i + 1]), b.y - Bf16::hi(hi[i + 1]));
+            lo[i] = Ty::pack(a.x - Ty::lo(hi[i]), a.y - Ty::hi(hi[i]));
+            lo[i + 1] = Ty::pack(b.x - Ty::lo(hi[i + 1]), b.y - Ty::hi(hi[i + 1]));
         }
     }
 }
 // Those of a row's 128 scores in two parts, for the rows of few positions: out of line, so that the loop of the long
 // ones fits the instruction caches (350 us instead of 379 for the chunk above, before the next steps).
-static __device__ __noinline__ float2 weights_in_two_parts(uint32_t ts, const float* kc, const float* vc, float base) {
+template <typename Ty>
+__device__ __noinline__ float2 weights_in_two_parts(uint32_t ts, const float* kc, const float* vc, float base) {
     float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll 1
     for (int x = 0; x < 4; ++x) {
         uint32_t v[32], hi[16], lo[16];
         tmem_ld32(ts + 32 * x, v);
         tmem_wait_ld();
-        scaled_weights<true>(v, kc + 32 * x, vc + 32 * x, make_float2(-base, -base), l0, l1, hi, lo);
+        scaled_weights<Ty, true>(v, kc + 32 * x, vc + 32 * x, make_float2(-base, -base), l0, l1, hi, lo);
         tmem_st16(ts + 32 * x, hi);
         tmem_st16(ts + 32 * x + 16, lo);
     }
@@ -482,7 +485,7 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
     using L = Ch<D, ONE, true>;
     constexpr int NS = L::kSlots;
     constexpr bool BF = Ty::idesc_type == 1;
-    const uint32_t vbase = code_base<true>(), kbase = BF ? vbase : code_base<BF>();
+    const uint32_t base = code_base<BF>();
     const int tid = threadIdx.x & 127, lane = tid & 31, prow = tid >> 2, pcol = tid & 3;
     const uint32_t ring = smem_u32(smem) + L::kRingOff, from = ring + L::kTile / 2 + prow * D + pcol * 16;
     const uint32_t to = ring + prow * 128 + (((pcol * 2) ^ (prow & 7)) << 4);  // (row & 7 is prow & 7 in every step)
@@ -512,30 +515,29 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
             const bool keys = !ONE ? !(i & 1) : i == 0 || ((i & 1) && i + 1 < 2 * n);
             const uint32_t sl = e % NS, off = sl * L::kTile;
             const bool ok = mbar_wait_warp(raw + sl, (e / NS) & 1, abort_flag, &g_chunk_status);
-            auto put = [&](uint32_t a, const uint4& v, auto values) {
-                constexpr bool B = decltype(values)::value;
+            auto put = [&](uint32_t a, const uint4& v) {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t y[8];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)  // bytes 2 h, 2 h + 1 to where code_pair has them
-                        y[2 * c + h] = code_pair<E4M3, B, E4M3>(
-                            __byte_perm(w[c], 0u, E4M3 ? (h ? 0x3424 : 0x1404) : (h ? 0x4342 : 0x4140)), B ? vbase : kbase);
+                        y[2 * c + h] = code_pair<E4M3, BF, E4M3>(
+                            __byte_perm(w[c], 0u, E4M3 ? (h ? 0x3424 : 0x1404) : (h ? 0x4342 : 0x4140)), base);
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                              : "memory");
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a ^ 16u), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
                              : "memory");
             };
-            auto unpack = [&](auto values) {
+            auto unpack = [&] {
                 if constexpr (D == 128) {
                     // a row's 128 codes lie where the last 64 of its numbers go: four lanes read and write them
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         const uint4 x = lds_v4(from + off + k * 32 * 128), y = lds_v4(from + off + k * 32 * 128 + 64);
                         __syncwarp();
-                        put(to + off + k * 32 * 128, x, values);
-                        put(to + off + k * 32 * 128 + 16384, y, values);
+                        put(to + off + k * 32 * 128, x);
+                        put(to + off + k * 32 * 128 + 16384, y);
                     }
                     return ok;
                 } else {
@@ -545,7 +547,7 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
                     for (int k = 0; k < 4; ++k) v[k] = lds_v4(from + off + k * 32 * 64);
                     if (!bar_and(3, 128, ok)) return false;  // all have read theirs (or one gave up, and all do)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) put(to + off + k * 32 * 128, v[k], values);
+                    for (int k = 0; k < 4; ++k) put(to + off + k * 32 * 128, v[k]);
                     return true;
                 }
             };
@@ -559,11 +561,16 @@ W4A16_DEVICE void unpack_codes(const PagedAttnParams& p, ChunkWalk walk, int tok
                 const float f = finite_or_nan(vs);
                 sc[0] = finite_or_nan(ks) * p.scale2;
                 sc[128] = f;
-                sc[256] = fabsf(f) < INFINITY ? f : 0.f;
+                const float g = fabsf(f) < INFINITY ? f : 0.f;
+                sc[256] = g;
+                if constexpr (!BF) {  // (0 where no row sees the key)
+                    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(g)));
+                    if (lane == 0) scales[25 * 128 + ((tile0 + t) & 7) * 4 + (tid >> 5)] = __uint_as_float(most);
+                }
                 scales_of(t + 1, pg);
                 pg = page_of(t + 2);
             }
-            if (!(BF || !keys ? unpack(std::true_type{}) : unpack(std::false_type{}))) return;
+            if (!unpack()) return;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(full + sl);
@@ -583,6 +590,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     // the loops written out, 283 so), for trees since their short calls run most lines once (13 nodes: 24.5 us written
     // out, 22.4 so; 16 trees of 64 nodes alike).
     constexpr bool SPREAD = Q8 || TREE;
+    constexpr bool BASED = Q8 && Ty::idesc_type == 0;  // scores against a base that the values' scales are part of
     extern __shared__ __align__(1024) unsigned char smem[];
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
         if (threadIdx.x == 0) atomicExch(&g_chunk_status, (int)W4A16_ECUDA);
@@ -892,7 +900,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
         // go out together.
         // What steers the loop is made uniform, for the descriptors' sake: the chunk
         // above took 206 us with it and 218 without.
-        constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<typename PvType<Ty, Q8>::type>(D, true);
+        constexpr uint32_t id_s = idesc_ch<Ty>(kChKeys, false), id_o = idesc_ch<Ty>(D, true);
         const uint32_t tm = uniform(tmem), sm = uniform(smem_u32(smem));
         auto tile_at = [&](uint32_t slot, uint32_t kind) {  // a descriptor's low word; tile 0 is Q's first
             return ((sm + slot * (uint32_t)L::kTile) >> 4) | kind;
@@ -901,7 +909,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
         bool ok = true;
         while (ok && walk.next<ONE, TREE>(p, toks, pc)) {
             const int take = (int)uniform((uint32_t)pc.take);
-            const bool duo = !ONE && uniform(pc.duo) != 0, two = uniform(pc.two || (Q8 && Ty::idesc_type == 0)) != 0;
+            const bool duo = !ONE && uniform(pc.duo) != 0, two = uniform(pc.two) != 0;
             const int cnt[2] = {duo ? take : (take + 1) / 2, duo ? take : take / 2};
             int scores = cnt[0] + cnt[1];
             auto tile_of = [&](int g, int k) { return (uint32_t)(duo ? k : 2 * k + g); };
@@ -979,7 +987,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
         bool ok = true;
         const float scale2 = Q8 ? 1.f : p.scale2;  // of the scores as they are read (Q8: the keys' scales have it)
         while (ok && walk.next<ONE, TREE>(p, toks, pc)) {
-            const bool two = pc.two || (Q8 && Ty::idesc_type == 0);
+            const bool two = pc.two;
             const int base_tok = pc.duo ? g * toks : 0;
             const int mytok = base_tok + tok;  // of the item
             const bool valid = tok < toks && mytok < pc.it.tokens;
@@ -1006,10 +1014,16 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 // Q8: the tile's scales -- of the scores, and of the weights
                 const float* kc = scales + ((tile0 + t) & 7) * 384;
                 const float* vc = kc + 128;
+                float largest = 0.f;  // of the values' scales that the row sees
+                if constexpr (BASED) {
+                    const float4 x = *reinterpret_cast<const float4*>(scales + 25 * 128 + ((tile0 + t) & 7) * 4);
+                    largest = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+                }
                 if (j0 < pc.it.lo1 || j0 + kChKeys - 1 > pc.it.e0 || no) {
                     // an edge: scores outside the row's positions become -inf, 32 at a time
                     const int rl = lo - j0, re = e - j0;
                     bool bad = false;
+                    if constexpr (BASED) largest = 0.f;
                     uint32_t nodes[5];  // the words with the nodes at the tile's positions
                     if constexpr (TREE)
 #pragma unroll
@@ -1041,6 +1055,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             if constexpr (Q8) sv[i] = __float_as_uint(__uint_as_float(sv[i]) * kc[x + i]);
+                            if constexpr (BASED)
+                                if ((seen >> i) & 1u) largest = fmaxf(largest, fabsf(kc[256 + x + i]));
                             if (!((seen >> i) & 1u)) sv[i] = 0xff800000u;
                         }
                         tmem_st32(ts + x, sv);
@@ -1085,7 +1101,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 // the row's maximum, 32 scores at a time and the next 32 on their way
                 uint32_t sv[2][32];
                 tmem_ld32(ts, sv[0]);
-                float mx = m, mo = m;
+                float mx = BASED ? -INFINITY : m, mo = mx;
 #pragma unroll(SPREAD ? 1 : 2)
                 for (int x0 = 0; x0 < 4; x0 += 2)
 #pragma unroll
@@ -1107,6 +1123,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     }
                 }
                 mx = fmaxf(mx, mo);
+                if constexpr (BASED) mx = fmaxf(m, mx + (scale_log(largest) - kChShift));
                 const bool grew = (mx - m) * scale2 > 8.f;  // also from -inf
                 if (__any_sync(0xffffffffu, grew)) {
                     const float f = mx == -INFINITY ? 1.f : exp2_approx((m - mx) * scale2);
@@ -1151,31 +1168,17 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     }
                 };
                 if constexpr (Q8) {
-                    if (Ty::idesc_type == 1 && two) {
-                        l0 = weights_in_two_parts(ts, kc, vc, base);
-                    } else if (Ty::idesc_type == 1) {
+                    if (two) {
+                        l0 = weights_in_two_parts<Ty>(ts, kc, vc, base);
+                    } else {
 #pragma unroll 1
                         for (int x = 0; x < 4; ++x) {  // (the next 32 ahead cost more code than they save time: 301 us, 290 so)
                             uint32_t hi[16];
                             tmem_ld32(ts + 32 * x, sv[0]);
                             tmem_wait_ld();
-                            scaled_weights<false>(sv[0], kc + 32 * x, vc + 32 * x, nb, l0, l1, hi, nullptr);
+                            scaled_weights<Ty, false>(sv[0], kc + 32 * x, vc + 32 * x, nb, l0, l1, hi, nullptr);
                             tmem_st16(ts + 16 * x, hi);
                         }
-                    } else {
-                        tmem_ld32(ts, sv[0]);
-#pragma unroll 1
-                        for (int x0 = 0; x0 < 4; x0 += 2)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int x = x0 + y;
-                                tmem_wait_ld();
-                                if (x < 3) tmem_ld32(ts + 32 * (x + 1), sv[1 - y]);
-                                uint32_t hi[16], lo[16];
-                                scaled_weights<true>(sv[y], kc + 32 * x, vc + 32 * x, nb, l0, l1, hi, lo);
-                                tmem_st16(ts + 32 * x, hi);
-                                tmem_st16(ts + 32 * x + 16, lo);
-                            }
                     }
                 } else if constexpr (SPREAD) {
 #pragma unroll 1

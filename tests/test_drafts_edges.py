@@ -165,3 +165,38 @@ def test_rope_in_place_on_a_side_stream(w):
     s.synchronize()
     ref = drafts.rotate(kept, pos, f64(f), False, m)
     assert np.all(np.abs(f64(x) - ref) <= m * 2.0 ** -21 * partner_sum(kept, 64, False) + 2.0 ** -8 * np.abs(ref))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("far", [0, 12, 20])
+@pytest.mark.parametrize("lens,tree", [([(900, 130), (300, 70)], None), ([(700, 60), (280, 90)], "tree")])
+def test_fp16_weights_of_long_rows(w, code, far, lens, tree):
+    """Rows of 256 positions and more have weights of one part, 11 bits: rounded by 2^-11 of themselves or by 2^-25.  The base
+    is at most the largest score + log2 (the largest scale, rounded up to a power of two) - 6, so that the key of the largest
+    score has a weight of 2^5 / (largest scale) at least before its value's scale, and the row's sum is no less.  So
+    |out - ref| <= (2^-11 + 2e-4) sum p|v| + 2^-11 |ref| + 2^-25 + n 2^-30 largest scale * 127 (or 480) with n positions.
+    Some values are 2^far times larger."""
+    a = Draft(lens, 8, 2, 128, 16, "fp16", code, tree, seed=11)
+    a.vs *= 2.0 ** -10
+    a.vs[torch.rand(a.vs.shape, generator=torch.Generator("cuda").manual_seed(1), device="cuda") < 0.02] *= 2.0 ** far
+    out, lse = a.run(w)
+    ref, rl, spread, _ = a.reference()
+    most = float(a.vs.max()) * (127 if code == "int8" else 480)
+    bound = (2.0 ** -11 + 2e-4) * spread + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + a.L.max() * 2.0 ** -30 * most
+    assert np.all(np.abs(f64(out) - ref) <= bound)
+    assert np.all(np.abs(f64(lse) - rl) <= 1e-4 + 1e-6 * np.abs(rl))
+
+
+@pytest.mark.parametrize("lens", [[(900, 130)], [(40, 50), (5, 9)], [(100, 1)]])
+def test_fp16_rows_of_zeros_and_mixed_with_them(w, lens):
+    a = Draft(lens, 8, 2, 128, 16, "fp16", "int8", seed=12)
+    keep = a.vs.clone()
+    a.vs[:] = 0
+    out, lse = a.run(w)
+    a.check(out, lse)
+    assert (out == 0).all() and torch.isfinite(lse).all()
+    a.vs[:] = torch.where(torch.rand(keep.shape, device="cuda") < 0.5, keep, torch.zeros_like(keep))
+    ref, rl, spread, _ = a.reference()
+    out, lse = a.run(w)
+    assert np.all(np.abs(f64(out) - ref) <= (2.0 ** -11 + 2e-4) * spread + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25)
+    assert np.all(np.abs(f64(lse) - rl) <= 1e-4 + 1e-6 * np.abs(rl))
