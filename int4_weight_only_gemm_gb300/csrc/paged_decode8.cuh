@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kDecThreads, 3 - NG) paged_decode8_kernel(cons
             }
         }
         if (!whole) dec_join<Ty, D, 8 * NG>(p, done, done_hk, owner_of(first, line[0], (int)line[3]),
-                                             owner_of(end - 1, line[0], (int)line[3]), misc);
+                                             owner_of(end - 1, line[0], (int)line[3]), misc, merge);
         if (!more) break;
         __syncthreads();  // ml and merge are free again
     }
