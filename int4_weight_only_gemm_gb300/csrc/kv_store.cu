@@ -12,12 +12,14 @@
 // fraction of a turn, without rounding; its top 32 bits go to sincospi.
 //
 // Bound: HBM, each row read and written once; what is left to it is the latency of a
-// round (loads are one ahead; two ahead cost more registers than they gain) and, in
-// 8 bits, issue slots (196 instructions a warp for two rows, 62 % of the slots).
+// round and, in 8 bits, issue slots (196 instructions a warp for two rows, 62 % of the
+// slots).  Queries alone have the loads of three rows on their way (one 73 us, two 61-65,
+// three 58.6, four 58.4), a store one (16301 tokens turned and to int8, 48 heads: 129 us,
+// two ahead 156; without turns, stored and read back, 49 and 52).
 // Measured: 16301 tokens of 40 heads of 128 in bf16 (334 MB), half of each head
-// turned: 67-70 us, 4.9 TB/s, the whole head in halves 68; keys and values of 16301
-// tokens, 8 heads of 128, to e4m3: 34 us (101 MB), with the read-back of the cache
-// 53; 64 tokens of 32 + 8 heads, turned and to int8: 6.7 us alone, 9.7 us a call.
+// turned: 58.6 us, 5.7 TB/s, the whole head in pairs 59.4; keys and values of 16301
+// tokens, 8 heads of 128, to e4m3 (101 MB), with the read-back of the cache
+// 49; 64 tokens of 32 + 8 heads, turned and to int8: 6.7 us alone, 9.7 us a call.
 #include <cmath>
 
 #include "codes.cuh"
@@ -56,10 +58,9 @@ W4A16_DEVICE float half_of(const uint4& v, int i) {
 }
 
 // KV: keys and values too, else queries alone; TURN: with rotary positions.  CTAs an SM as the registers allow.  Without
-// turns, five of 48 registers: 16301 tokens stored in 8 bits and read back 53 us, with six 57, with the three that the
-// kernel with turns has 57.
+// turns, five of 48 registers: 16301 tokens stored in 8 bits and read back 49 us, with four 52, with six 55.
 template <typename Ty, int CODE, int LANES, bool KV, bool TURN>
-__global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : KV ? 3 : 4) kv_store_kernel(const __grid_constant__ RowParams p) {
+__global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : 3) kv_store_kernel(const __grid_constant__ RowParams p) {
     extern __shared__ float2 turn[];  // [token][pair] cosine and sine
     pdl_wait();
     pdl_launch_dependents();
@@ -94,9 +95,8 @@ __global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : KV ? 3 : 4) kv_store_
         int kind, h;  // 0 query, 1 key, 2 value; head
         bool live;
         const uint16_t* src;
-        uint4 raw;
     };
-    auto load = [&](int row) {  // on its way
+    auto where = [&](int row) {
         Row r;
         r.kind = 0;
         r.h = row;
@@ -109,11 +109,16 @@ __global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : KV ? 3 : 4) kv_store_
         } else {
             r.src = qs + r.h * p.q_head;
         }
-        r.raw = make_uint4(0u, 0u, 0u, 0u);
-        if (r.live) r.raw = *reinterpret_cast<const uint4*>(r.src);
         return r;
     };
-    Row next = load(r0 + sub);
+    auto load = [&](int row) {  // on its way
+        const Row r = where(row);
+        return r.live ? *reinterpret_cast<const uint4*>(r.src) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    constexpr int AHEAD = KV ? 1 : 3;  // rows whose loads are on their way
+    uint4 ahead[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) ahead[i] = load(r0 + i * step + sub);
 
     float2 w[8];  // of the lane's columns (of its pairs, the first four, where these lie together)
     uint32_t turned = 0;  // bit i: w[i] is of a column (of a pair) that turns
@@ -143,13 +148,12 @@ __global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : KV ? 3 : 4) kv_store_
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i].y = -w[i].y;
 
-    // (all lanes of a warp go round together: shuffles)
-    for (int row = r0; row < r1; row += step) {
-        const Row cur = next;
-        if (row + step < r1) next = load(row + step + sub);
+    auto turn_and_store = [&](int row, uint4& buffer) {
+        const Row cur = where(row);
         const int kind = cur.kind, h = cur.h;
         const bool live = cur.live;
-        const uint4 raw = cur.raw;
+        const uint4 raw = buffer;
+        buffer = load(row + AHEAD * step);
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = half_of<Ty>(raw, i);
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : KV ? 3 : 4) kv_store_
         const uint4 packed = make_uint4(Ty::pack(x[0], x[1]), Ty::pack(x[2], x[3]), Ty::pack(x[4], x[5]), Ty::pack(x[6], x[7]));
         if (!KV || kind == 0) {
             if (live) *reinterpret_cast<uint4*>(qo + h * p.o_head) = packed;
-            if (!KV || CODE == kCode16) continue;
+            if (!KV || CODE == kCode16) return;
         }
         const int64_t at = (kind == 1 ? kat : vat) + h * (kind == 1 ? p.kch : p.vch);
         if constexpr (CODE == kCode16) {
@@ -230,7 +234,13 @@ __global__ void __launch_bounds__(kRowThreads, !TURN ? 5 : KV ? 3 : 4) kv_store_
                     *((kind == 1 ? kscale : vscale) + h * (kind == 1 ? p.ksh : p.vsh)) = scale;
             }
         }
-    }
+    };
+    // (all lanes of a warp go round together: shuffles)
+#pragma unroll 1
+    for (int row = r0; row < r1; row += AHEAD * step)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (i == 0 || row + i * step < r1) turn_and_store(row + i * step + sub, ahead[i]);
 }
 
 template <typename Ty, int CODE>

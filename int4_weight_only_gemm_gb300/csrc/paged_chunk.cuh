@@ -67,7 +67,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <type_traits>
 
 #include "codes.cuh"
 #include "paged_attn.cuh"

@@ -18,7 +18,8 @@ Attention: softmax weights rounded once to the 16-bit type of the product with v
 f32 scores, exponentials and sums within 2e-4 of exact for the sizes here (128 products in f32, scores below 64):
     |out - ref| <= (u_w + 2e-4) sum_j p_j |v_j| + u |ref|     (fp16: + n 2^-25 max|v| over a 16-bit cache, + 2^-25)
     |lse - ref| <= 1e-4 + 1e-6 |ref|
-with u_w = 2^-8 for bf16, 2^-11 for fp16 over a 16-bit cache, 2^-15 for fp16 over an 8-bit one (two bf16 parts).
+with u_w = 2^-8 for bf16, 2^-11 for fp16 over a 16-bit cache, 2^-15 for fp16 over an 8-bit one, whose weights go in two
+parts (the long rows of the largest calls have one: test_drafts_edges.py).
 """
 import numpy as np
 import pytest
