@@ -106,6 +106,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 # the current stream's handle without building a Stream object (a few
 # microseconds a call); the public route where this torch lacks it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream, device_index: int | None = None) -> int:
@@ -553,6 +554,14 @@ def _scale(t, name, pages, heads, page):
     return t.stride()
 
 
+def _here(t, other):
+    """Index of the current device, on which the call is launched and its tensors have to lie."""
+    index = _current()
+    if t.get_device() != index or other.get_device() != index:
+        raise ValueError(f"tensors of one call must all lie on the current device, cuda:{index}")
+    return index
+
+
 def _codes(k_cache, k_scale, v_scale, dtype):
     """The cache's element type, and its number; scales go with an 8-bit cache and with no other."""
     if not isinstance(k_cache, _Tensor):
@@ -611,9 +620,10 @@ def w4a16_rope(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tens
     if oshape != shape:
         raise ValueError(f"out has shape {tuple(oshape)}, expected {tuple(shape)}")
     f = _frequencies(frequencies)
+    idx = _here(x, out)
     args = _ROPE_ARGS.pack(x.data_ptr(), out.data_ptr(), _int32(positions, "positions", T), f, xt, xh, ot, oh, T, heads,
                            d, 2 * frequencies.numel(), int(interleaved), _DTYPES[dtype], magnitude, flags)
-    _raise(load_library().w4a16_rope(args, _stream(stream, x.get_device())), "w4a16_rope")
+    _raise(load_library().w4a16_rope(args, _stream(stream, idx)), "w4a16_rope")
     return out
 
 
@@ -626,7 +636,7 @@ def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_c
     or past the cache: skipped).  Caches of int8 or float8_e4m3fn take them
     quantised, with a scale for each token and head in k_scale and v_scale
     [pages, heads, page_size] f32 (see w4a16_kv_store in include/w4a16.h)."""
-    if k_scale is not None or v_scale is not None or k_cache.dtype in _CODES:
+    if k_scale is not None or v_scale is not None or getattr(k_cache, "dtype", None) in _CODES:
         _kv_store(None, k, v, None, None, slot_map, k_cache, v_cache, None, k_scale, v_scale, False, 1.0, stream, flags)
         return
     dtype = k.dtype
@@ -686,13 +696,14 @@ def _kv_store(q, k, v, positions, frequencies, slot_map, k_cache, v_cache, q_out
         kss, vss = _scale(k_scale, "k_scale", pages, heads, page), _scale(v_scale, "v_scale", pages, heads, page)
         ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
     turn = frequencies is not None
+    idx = _here(k, k_cache)
     args = _STORE_ARGS.pack(q.data_ptr() if Hq else 0, k.data_ptr(), v.data_ptr(), q_out.data_ptr() if Hq else 0,
                             _int32(positions, "positions", T) if turn else 0, _frequencies(frequencies) if turn else 0,
                             _int32(slot_map, "slot_map", T), k_cache.data_ptr(), v_cache.data_ptr(),
                             ksp, vsp, qt, qh, ot, oh, kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, Hq, heads, d,
                             2 * frequencies.numel() if turn else 0, int(interleaved), pages, page, _DTYPES[dtype], code,
                             magnitude, flags)
-    _raise(load_library().w4a16_kv_store(args, _stream(stream, k.get_device())),
+    _raise(load_library().w4a16_kv_store(args, _stream(stream, idx)),
            "w4a16_rope_kv_write" if turn else "w4a16_kv_write")
 
 
@@ -719,10 +730,11 @@ def w4a16_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_map: torch.
     if k_scale is not None:
         kss, vss = _scale(k_scale, "k_scale", pages, heads, page), _scale(v_scale, "v_scale", pages, heads, page)
         ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
+    idx = _here(k, k_cache)
     args = _READ_ARGS.pack(k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, _int32(slot_map, "slot_map", T),
                            k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, heads, d, pages, page,
                            _DTYPES[dtype], code, flags)
-    _raise(load_library().w4a16_kv_read(args, _stream(stream, k.get_device())), "w4a16_kv_read")
+    _raise(load_library().w4a16_kv_read(args, _stream(stream, idx)), "w4a16_kv_read")
     return k, v
 
 
@@ -770,6 +782,7 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
             words = tshape[1]
             if tshape[0] != T or words == 0:
                 raise ValueError(f"tree has shape {tuple(tshape)}, expected ({T}, words)")
+        _here(q, k_cache)
         ext = _EXT_ARGS.pack(ksp, vsp, 0 if tree is None else tree.data_ptr(), *kss, *vss, node if T > 1 else words, code,
                              words)
     pages, Hkv, page, cd = cshape

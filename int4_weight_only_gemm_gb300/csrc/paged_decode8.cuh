@@ -56,6 +56,7 @@ struct Dec8 {
     static constexpr int kSmem = kMiscOff + 128;
 };
 static_assert(Dec8<128, 2>::kSmem <= 232448 && Dec8<64, 2>::kSmem <= 232448, "shared memory");
+static_assert(Dec8<64, 2>::kMerge >= 6 * kDecThreads * 4, "dec_join's room");
 static_assert(2 * (Dec8<128, 1>::kSmem + 1024) <= 233472 && 2 * (Dec8<64, 1>::kSmem + 1024) <= 233472, "two CTAs an SM");
 
 // Where a tile's 16-byte piece `chunk` of key `row` lies, so that neither product's loads meet in a bank: four

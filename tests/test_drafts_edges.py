@@ -200,3 +200,36 @@ def test_fp16_rows_of_zeros_and_mixed_with_them(w, lens):
     out, lse = a.run(w)
     assert np.all(np.abs(f64(out) - ref) <= (2.0 ** -11 + 2e-4) * spread + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25)
     assert np.all(np.abs(f64(lse) - rl) <= 1e-4 + 1e-6 * np.abs(rl))
+
+
+@pytest.mark.parametrize("code,tree", [("int8", None), ("e4m3", "tree"), ("e4m3", None)])
+def test_few_rows_cut_over_many_ctas(w, code, tree):
+    """Requests whose keys fall to many CTAs, next to requests of one CTA: a CTA that joins goes on with the next request."""
+    for heads, kv_heads, d in ((4, 1, 128), (8, 2, 64), (6, 2, 128), (2, 2, 128)):
+        lens = [(9000, 1), (40, 1), (3001, 1), (0, 1), (500, 1), (7011, 1), (130, 1)]
+        a = Draft(lens, heads, kv_heads, d, 16, "bf16", code, tree, seed=31)
+        a.check(*a.run(w))
+        a.check(*a.run(w, 2000), 2000)
+        b = Draft([(2303, 1)], heads, kv_heads, d, 64, "fp16", code, tree, seed=32)
+        b.check(*b.run(w))
+
+
+def test_tensors_of_another_device_are_refused(w, monkeypatch):
+    a = Draft([(20, 2)], 4, 2, 64, 16, "bf16", "int8", seed=33)
+    f, _ = w.w4a16_rope_frequencies(64)
+    T = a.q.shape[0]
+    at, k = i32(np.zeros(T)), torch.zeros(T, 2, 64, dtype=a.dt, device="cuda")
+    before = a.kc.clone()
+    calls = [lambda: w.w4a16_rope(a.q, at, f), lambda: a.run(w),
+             lambda: w.w4a16_kv_write(k, k, at, a.kc, a.vc, k_scale=a.ks, v_scale=a.vs),
+             lambda: w.w4a16_rope_kv_write(None, k, k, at, f, at, a.kc, a.vc, k_scale=a.ks, v_scale=a.vs),
+             lambda: w.w4a16_kv_read(a.kc, a.vc, at, k, k.clone(), a.ks, a.vs)]
+    for call in calls:
+        with monkeypatch.context() as m:
+            m.setattr(w, "_current", lambda: 1)   # as with torch.cuda.device(1) around the call
+            with pytest.raises(ValueError, match="device"):
+                call()
+    with pytest.raises(ValueError):
+        w.w4a16_kv_write(k, k, at, None, None)
+    torch.cuda.synchronize()
+    assert torch.equal(a.kc, before)
