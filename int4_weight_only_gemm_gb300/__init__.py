@@ -408,7 +408,7 @@ _READ_ARGS = struct.Struct("=7Q16qiiiiiiiI")
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _CODES = {torch.int8: 3, torch.float8_e4m3fn: 4}  # of 8-bit caches
 _SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
-_Tensor, _I32, _F32 = torch.Tensor, torch.int32, torch.float32  # (looked up some ten times a call)
+_Tensor, _I32, _F32, _F64 = torch.Tensor, torch.int32, torch.float32, torch.float64  # (looked up some ten times a call)
 
 
 def _int32(t, name, n=None):
@@ -544,22 +544,51 @@ def _caches(k_cache, v_cache, dtype):
     return shape, ks, vs
 
 
-def _scale(t, name, pages, heads, page):
-    """Strides of an 8-bit cache's scales [pages, heads, page_size] f32."""
-    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _F32:
-        raise ValueError(f"{name} must be a float32 CUDA tensor")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != pages or shape[1] != heads or shape[2] != page:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(pages, heads, page)}")
-    return t.stride()
+def _at(t, name, dtype, dims, idx):
+    """_strided of a tensor on the current device, idx: the call is launched there."""
+    if not isinstance(t, _Tensor) or t.get_device() != idx:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, cuda:{idx}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    stride = t.stride()
+    if len(stride) != dims or (stride[-1] != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be {dims}-D with a contiguous last dimension")
+    return t.shape, stride
 
 
-def _here(t, other):
-    """Index of the current device, on which the call is launched and its tensors have to lie."""
-    index = _current()
-    if t.get_device() != index or other.get_device() != index:
-        raise ValueError(f"tensors of one call must all lie on the current device, cuda:{index}")
-    return index
+def _alike(t, name, dtype, shape, idx):
+    """Strides of a tensor of that shape on the current device, idx, with a contiguous last dimension."""
+    if not isinstance(t, _Tensor) or t.get_device() != idx:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, cuda:{idx}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return stride
+
+
+def _list(t, name, dtype, n, idx):
+    """Address of a contiguous 1-D tensor of n entries (None: any number) on the current device, idx."""
+    if not isinstance(t, _Tensor) or t.get_device() != idx or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor on the current device, cuda:{idx}")
+    if t.dim() != 1 or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected 1-D" + (f" of {n}" if n is not None else ""))
+    return t.data_ptr()
+
+
+def _scale(t, name, shape, idx):
+    """Address and strides of an 8-bit cache's scales [pages, heads, page_size] f32."""
+    if not isinstance(t, _Tensor) or t.get_device() != idx or t.dtype is not _F32:
+        raise ValueError(f"{name} must be a float32 CUDA tensor on the current device, cuda:{idx}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return t.data_ptr(), t.stride()
+
+
+_NO_SCALE = 0, (0, 0, 0)
 
 
 def _codes(k_cache, k_scale, v_scale, dtype):
@@ -578,13 +607,6 @@ def _codes(k_cache, k_scale, v_scale, dtype):
     if k_scale is None or v_scale is None:
         raise ValueError(f"a cache of {cdtype} needs k_scale and v_scale")
     return cdtype, code
-
-
-def _frequencies(t):
-    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not torch.float64 or t.dim() != 1 or \
-            not t.is_contiguous():
-        raise ValueError("frequencies must be a contiguous 1-D float64 CUDA tensor")
-    return t.data_ptr()
 
 
 def w4a16_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -612,16 +634,14 @@ def w4a16_rope(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tens
     dtype = x.dtype
     if dtype not in _DTYPES or dtype is torch.float32:
         raise ValueError(f"x must be bf16 or fp16, got {dtype}")
-    shape, (xt, xh, _) = _strided(x, "x", dtype, 3)
+    idx = _current()
+    shape, (xt, xh, _) = _at(x, "x", dtype, 3, idx)
     T, heads, d = shape
     if out is None:
         out = torch.empty((T, heads, d), dtype=dtype, device=x.device)
-    oshape, (ot, oh, _) = _strided(out, "out", dtype, 3)
-    if oshape != shape:
-        raise ValueError(f"out has shape {tuple(oshape)}, expected {tuple(shape)}")
-    f = _frequencies(frequencies)
-    idx = _here(x, out)
-    args = _ROPE_ARGS.pack(x.data_ptr(), out.data_ptr(), _int32(positions, "positions", T), f, xt, xh, ot, oh, T, heads,
+    ot, oh, _ = _alike(out, "out", dtype, shape, idx)
+    args = _ROPE_ARGS.pack(x.data_ptr(), out.data_ptr(), _list(positions, "positions", _I32, T, idx),
+                           _list(frequencies, "frequencies", _F64, None, idx), xt, xh, ot, oh, T, heads,
                            d, 2 * frequencies.numel(), int(interleaved), _DTYPES[dtype], magnitude, flags)
     _raise(load_library().w4a16_rope(args, _stream(stream, idx)), "w4a16_rope")
     return out
@@ -672,34 +692,32 @@ def w4a16_rope_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor
 
 def _kv_store(q, k, v, positions, frequencies, slot_map, k_cache, v_cache, q_out, k_scale, v_scale, interleaved,
               magnitude, stream, flags):
-    dtype = k.dtype
+    dtype, idx = k.dtype, _current()
     cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
-    shape, (kt, kh, _) = _strided(k, "k", dtype, 3)
-    vshape, (vt, vh, _) = _strided(v, "v", dtype, 3)
-    if vshape != shape:
-        raise ValueError(f"v has shape {tuple(vshape)}, expected {tuple(shape)}")
+    shape, (kt, kh, _) = _at(k, "k", dtype, 3, idx)
+    vt, vh, _ = _alike(v, "v", dtype, shape, idx)
     T, heads, d = shape
-    cshape, ks, vs = _caches(k_cache, v_cache, cdtype)
+    cshape, ks = _at(k_cache, "k_cache", cdtype, 4, idx)
+    vs = _alike(v_cache, "v_cache", cdtype, cshape, idx)
     pages, ch, page, cd = cshape
     if ch != heads or cd != d:
         raise ValueError(f"caches of {ch} heads of {cd} do not take k of {heads} heads of {d}")
     Hq = qt = qh = ot = oh = 0
     if q is not None:
-        qshape, (qt, qh, _) = _strided(q, "q", dtype, 3)
-        oshape, (ot, oh, _) = _strided(q_out, "q_out", dtype, 3)
+        qshape, (qt, qh, _) = _at(q, "q", dtype, 3, idx)
         Hq = qshape[1]
-        if qshape[0] != T or qshape[2] != d or oshape != qshape:
-            raise ValueError(f"q {tuple(qshape)} and q_out {tuple(oshape)} do not go with k {tuple(shape)}")
-    kss = vss = (0, 0, 0)
-    ksp = vsp = 0
+        if qshape[0] != T or qshape[2] != d:
+            raise ValueError(f"q {tuple(qshape)} does not go with k {tuple(shape)}")
+        ot, oh, _ = _alike(q_out, "q_out", dtype, qshape, idx)
+    (ksp, kss), (vsp, vss) = _NO_SCALE, _NO_SCALE
     if k_scale is not None:
-        kss, vss = _scale(k_scale, "k_scale", pages, heads, page), _scale(v_scale, "v_scale", pages, heads, page)
-        ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
+        scales = (pages, heads, page)
+        (ksp, kss), (vsp, vss) = _scale(k_scale, "k_scale", scales, idx), _scale(v_scale, "v_scale", scales, idx)
     turn = frequencies is not None
-    idx = _here(k, k_cache)
     args = _STORE_ARGS.pack(q.data_ptr() if Hq else 0, k.data_ptr(), v.data_ptr(), q_out.data_ptr() if Hq else 0,
-                            _int32(positions, "positions", T) if turn else 0, _frequencies(frequencies) if turn else 0,
-                            _int32(slot_map, "slot_map", T), k_cache.data_ptr(), v_cache.data_ptr(),
+                            _list(positions, "positions", _I32, T, idx) if turn else 0,
+                            _list(frequencies, "frequencies", _F64, None, idx) if turn else 0,
+                            _list(slot_map, "slot_map", _I32, T, idx), k_cache.data_ptr(), v_cache.data_ptr(),
                             ksp, vsp, qt, qh, ot, oh, kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, Hq, heads, d,
                             2 * frequencies.numel() if turn else 0, int(interleaved), pages, page, _DTYPES[dtype], code,
                             magnitude, flags)
@@ -714,26 +732,23 @@ def w4a16_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_map: torch.
     [T, heads, head_dim] (bf16 or fp16): copied from a 16-bit cache, scale
     times code from an 8-bit one.  Rows of slots that are negative or past the
     cache stay as they are.  Returns (k, v)."""
-    dtype = k.dtype
+    dtype, idx = k.dtype, _current()
     cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
-    shape, (kt, kh, _) = _strided(k, "k", dtype, 3)
-    vshape, (vt, vh, _) = _strided(v, "v", dtype, 3)
-    if vshape != shape:
-        raise ValueError(f"v has shape {tuple(vshape)}, expected {tuple(shape)}")
+    shape, (kt, kh, _) = _at(k, "k", dtype, 3, idx)
+    vt, vh, _ = _alike(v, "v", dtype, shape, idx)
     T, heads, d = shape
-    cshape, ks, vs = _caches(k_cache, v_cache, cdtype)
+    cshape, ks = _at(k_cache, "k_cache", cdtype, 4, idx)
+    vs = _alike(v_cache, "v_cache", cdtype, cshape, idx)
     pages, ch, page, cd = cshape
     if ch != heads or cd != d:
         raise ValueError(f"caches of {ch} heads of {cd} do not go with k of {heads} heads of {d}")
-    kss = vss = (0, 0, 0)
-    ksp = vsp = 0
+    (ksp, kss), (vsp, vss) = _NO_SCALE, _NO_SCALE
     if k_scale is not None:
-        kss, vss = _scale(k_scale, "k_scale", pages, heads, page), _scale(v_scale, "v_scale", pages, heads, page)
-        ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
-    idx = _here(k, k_cache)
-    args = _READ_ARGS.pack(k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, _int32(slot_map, "slot_map", T),
-                           k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, heads, d, pages, page,
-                           _DTYPES[dtype], code, flags)
+        scales = (pages, heads, page)
+        (ksp, kss), (vsp, vss) = _scale(k_scale, "k_scale", scales, idx), _scale(v_scale, "v_scale", scales, idx)
+    args = _READ_ARGS.pack(k_cache.data_ptr(), v_cache.data_ptr(), ksp, vsp, _list(slot_map, "slot_map", _I32, T, idx),
+                           k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, *ks[:3], *vs[:3], *kss, *vss, T, heads, d,
+                           pages, page, _DTYPES[dtype], code, flags)
     _raise(load_library().w4a16_kv_read(args, _stream(stream, idx)), "w4a16_kv_read")
     return k, v
 
@@ -769,22 +784,24 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     if k_scale is None and v_scale is None and tree is None:
         cshape, (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, dtype)
     else:
+        here = _current()
+        if q.get_device() != here:
+            raise ValueError(f"q must be a CUDA tensor on the current device, cuda:{here}")
         cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
-        cshape, (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, cdtype)
-        kss = vss = (0, 0, 0)
-        ksp = vsp = words = node = 0
+        cshape, (kcp, kch, kcs, _) = _at(k_cache, "k_cache", cdtype, 4, here)
+        vcp, vch, vcs, _ = _alike(v_cache, "v_cache", cdtype, cshape, here)
+        (ksp, kss), (vsp, vss), words, node = _NO_SCALE, _NO_SCALE, 0, 0
         if k_scale is not None:
             pages, Hkv, page, _ = cshape
-            kss, vss = _scale(k_scale, "k_scale", pages, Hkv, page), _scale(v_scale, "v_scale", pages, Hkv, page)
-            ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
+            scales = (pages, Hkv, page)
+            (ksp, kss), (vsp, vss) = _scale(k_scale, "k_scale", scales, here), _scale(v_scale, "v_scale", scales, here)
         if tree is not None:
-            tshape, (node, _) = _strided(tree, "tree", _I32, 2)
+            tshape, (node, _) = _at(tree, "tree", _I32, 2, here)
             words = tshape[1]
             if tshape[0] != T or words == 0:
                 raise ValueError(f"tree has shape {tuple(tshape)}, expected ({T}, words)")
-        _here(q, k_cache)
-        ext = _EXT_ARGS.pack(ksp, vsp, 0 if tree is None else tree.data_ptr(), *kss, *vss, node if T > 1 else words, code,
-                             words)
+        ext = _EXT_ARGS.pack(ksp, vsp, 0 if tree is None else tree.data_ptr(), *kss, *vss, node if T > 1 else words,
+                             code, words)
     pages, Hkv, page, cd = cshape
     if cd != d or dtype not in _DTYPES:
         raise ValueError(f"caches with heads of {cd} do not go with q with heads of {d} in {dtype}")
