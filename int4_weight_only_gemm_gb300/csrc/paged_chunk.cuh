@@ -1330,30 +1330,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
             float S = l;
             if (last) {
                 float M = m * scale2;
-                if (!whole) {
-                    M = -INFINITY;
-                    bool bad = false;
-#pragma unroll 4
-                    for (int i = c0; i <= c1; ++i) {
-                        const float2 mi = i == c && kept ? make_float2(mine_m, mine_l)
-                                                         : __ldcg(reinterpret_cast<const float2*>(piece(i)) + row);
-                        bad |= __float_as_uint(mi.y) >> 31;
-                        M = fmaxf(M, mi.x);
-                    }
-                    again = !bar_and(1 + g, 128, !bad);
-                    S = 0.f;
-                }
-                const float b = M == -INFINITY ? 0.f : M;
-                auto factor = [&](float mi) { return exp2_approx(mi == -INFINITY ? 0.f : mi - b); };
-                if (!whole)
-#pragma unroll 4
-                    for (int i = c0; i <= c1; ++i) {
-                        const float2 mi = i == c && kept ? make_float2(mine_m, mine_l)
-                                                         : __ldcg(reinterpret_cast<const float2*>(piece(i)) + row);
-                        if (mi.y != 0.f) S = fmaf(fabsf(mi.y), factor(mi.x), S);
-                    }
-                const float w = S == 0.f ? 0.f : 1.f / S;
                 auto put = [&](int x, const float* acc) {  // 8 columns
+                    const float w = S == 0.f ? 0.f : 1.f / S;
                     *reinterpret_cast<uint4*>(out + x) =
                         S == 0.f ? make_uint4(0u, 0u, 0u, 0u)
                                  : make_uint4(Ty::pack(acc[0] * w, acc[1] * w), Ty::pack(acc[2] * w, acc[3] * w),
@@ -1383,12 +1361,16 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                     }
                 } else {
                     // 16 columns at a time, of four pieces in flight (32 of one piece: 34 us for 13 tokens over 2303
-                    // positions, whose 19 pieces come one after the other then)
+                    // positions, whose 19 pieces come one after the other then), under a running maximum, so that
+                    // nothing waits for the maxima of all (a microsecond more with a pass over these before)
+                    bool bad = false;
 #pragma unroll 1
                     for (int x = x0; x < x1; x += 16) {
                         float acc[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y) acc[y] = 0.f;
+                        M = -INFINITY;
+                        S = 0.f;
 #pragma unroll 1
                         for (int i0 = c0; i0 <= c1; i0 += 4) {
                             float4 v[4][4];
@@ -1399,14 +1381,32 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                                 const int i = i0 + u;
                                 const bool there = i <= c1 && !(i == c && kept) && valid;
                                 const float* q = piece(there ? i : c0);
-                                mi[u] = there ? __ldcg(reinterpret_cast<const float2*>(q) + row) : make_float2(0.f, 0.f);
+                                mi[u] = there                 ? __ldcg(reinterpret_cast<const float2*>(q) + row)
+                                        : i == c && kept ? make_float2(mine_m, mine_l)
+                                                         : make_float2(-INFINITY, 0.f);
 #pragma unroll
                                 for (int y = 0; y < 4; ++y)
                                     v[u][y] = there ? __ldcg(reinterpret_cast<const float4*>(q + 256) + ((x >> 2) + y) * 128 + row)
                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
                             }
+                            const float before = M;
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) fs[u] = mi[u].y == 0.f ? 0.f : factor(mi[u].x);  // no seen key: zeros
+                            for (int u = 0; u < 4; ++u) {
+                                bad |= __float_as_uint(mi[u].y) >> 31;
+                                M = fmaxf(M, mi[u].x);
+                            }
+                            const float b = M == -INFINITY ? 0.f : M;
+                            if (i0 != c0) {
+                                const float f = exp2_approx(before == -INFINITY ? 0.f : before - b);
+                                S *= f;
+#pragma unroll
+                                for (int y = 0; y < 16; ++y) acc[y] *= f;
+                            }
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {  // no seen key: zeros
+                                fs[u] = mi[u].y == 0.f ? 0.f : exp2_approx(mi[u].x == -INFINITY ? 0.f : mi[u].x - b);
+                                if (mi[u].y != 0.f) S = fmaf(fabsf(mi[u].y), fs[u], S);
+                            }
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
                                 if (i0 + u == c && kept) {  // this piece's, by every lane: tensor-memory loads are the warp's
@@ -1421,9 +1421,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                                         for (int y = 0; y < 16; ++y)
                                             ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
                                     }
-                                    const float f = l == 0.f ? 0.f : factor(mine_m);
 #pragma unroll
-                                    for (int y = 0; y < 16; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), f, acc[y]);
+                                    for (int y = 0; y < 16; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), fs[u], acc[y]);
                                 } else {
 #pragma unroll
                                     for (int y = 0; y < 4; ++y) {
@@ -1441,6 +1440,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                         }
                         __syncwarp();
                     }
+                    again = !bar_and(1 + g, 128, !bad);
                 }
                 if (valid && p.lse && x0 == 0) p.lse[t * p.Hq + h] = S == 0.f ? -INFINITY : kLn2 * (M + log2f(S));
             }
