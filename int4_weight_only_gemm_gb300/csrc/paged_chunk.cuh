@@ -52,13 +52,13 @@
 // multiplies its score in f32, a value's its weight, which is of the queries' type as
 // the codes are (in two parts for rows of fewer than 256 positions).  Bound: as above, with twice the instructions in a
 // softmax warp's turn, and with the unpacking of 32768 codes a key tile.  Measured:
-// the chunk above 280-287 us with int8 or e4m3, 299 in fp16; the 16 blocks 78 us.
+// the chunk above 276-283 us with int8 or e4m3, 299 in fp16; the 16 blocks 78 us.
 //
 // For a tree of drafted tokens (TREE) a row sees the positions before the new tokens
 // and the nodes that its bits say; the words with a tile's nodes are read at once.
-// Measured: 16 trees of 64 nodes over 4080 positions 76 us (285 MB, 68 GFLOP); one of
-// 13 over 2303 positions 22.4 us, of which ~2.6 go to the cut of the line, 1.8 to the
-// first keys, 8 to the five tiles of the longest piece and 7 to the join.
+// Measured: 16 trees of 64 nodes over 4080 positions 74.4 us (285 MB, 68 GFLOP); one of
+// 13 over 2303 positions 21.7 us, of which ~2.6 go to the cut of the line, 1.8 to the
+// first keys, 8 to the five tiles of the longest piece and 6 to the join.
 //
 // Every wait is bounded: on a timeout the kernel records W4A16_ETIMEOUT, ends
 // its copies and MMAs, frees its tensor memory and returns.
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     // The loops over a row's scores are rolled, and weights in two parts lie over their own scores' columns: for an
     // 8-bit cache since the code of the CTA's roles has to fit the instruction caches (a 2048-token chunk: 416 us with
     // the loops written out, 283 so), for trees since their short calls run most lines once (13 nodes: 24.5 us written
-    // out, 22.4 so; 16 trees of 64 nodes alike).
+    // out, 22.4 so, before the join's present form; 16 trees of 64 nodes alike).
     constexpr bool SPREAD = Q8 || TREE;
     constexpr bool BASED = Q8 && Ty::idesc_type == 0;  // scores against a base that the values' scales are part of
     extern __shared__ __align__(1024) unsigned char smem[];
