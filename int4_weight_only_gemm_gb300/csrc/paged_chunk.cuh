@@ -422,10 +422,20 @@ W4A16_DEVICE void add_taken_out(const PagedAttnParams& p, const ChunkPiece& pc, 
 // weight is at most 2^14, what the largest score and the largest scale would make
 // at least 2^5, and a weight is rounded by 2^-11 of itself or by 2^-25.  (Two bf16
 // parts did it before: the chunk above 408 us.)
+// As the scales run, a base may move by more than the 126 binades that an f32 factor
+// has, with a sum of weights (before their scales) that lies in range on both sides of
+// the move: such factors are taken as their square root, twice.
 constexpr float kChShift = 6.f;  // of the base: weights are up to 2^(8 + 6)
 W4A16_DEVICE float scale_log(float largest) {  // an exponent that the scale is not above
     return fminf(fmaxf((float)((int)(__float_as_uint(largest) >> 23) - 126), -96.f), 100.f);
 }
+// 2^x as a factor, and products with it; TWICE: kept as its root
+template <bool TWICE>
+W4A16_DEVICE float power_of_2(float x) { return exp2_approx(TWICE ? 0.5f * x : x); }
+template <bool TWICE>
+W4A16_DEVICE float times(float x, float f) { return TWICE ? x * f * f : x * f; }
+template <bool TWICE>
+W4A16_DEVICE float add_times(float x, float f, float sum) { return fmaf(TWICE ? x * f : x, f, sum); }
 
 // Weights of 32 scores, times their values' scales: hi, and with TWO what hi lacks; the sums l0 and l1 are of the weights
 // alone.
@@ -1125,8 +1135,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 if constexpr (BASED) mx = fmaxf(m, mx + (scale_log(largest) - kChShift));
                 const bool grew = (mx - m) * scale2 > 8.f;  // also from -inf
                 if (__any_sync(0xffffffffu, grew)) {
-                    const float f = mx == -INFINITY ? 1.f : exp2_approx((m - mx) * scale2);
-                    l *= f;
+                    const float f = mx == -INFINITY ? 1.f : power_of_2<BASED>((m - mx) * scale2);
+                    l = times<BASED>(l, f);
                     m = mx;
                     if (k > 0) {
                         // all MMAs before this tile's scores are done: nothing adds to O now
@@ -1136,7 +1146,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                             tmem_ld_x16(to + i, ov);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f);
+                            for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(times<BASED>(__uint_as_float(ov[x]), f));
                             tmem_st_x8(to + i, *reinterpret_cast<const uint32_t(*)[8]>(ov));
                             tmem_st_x8(to + i + 8, *reinterpret_cast<const uint32_t(*)[8]>(ov + 8));
                         }
@@ -1253,14 +1263,17 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 l = a.y;
                 if (other) {
                     const float M = fmaxf(m, o.x), b = M == -INFINITY ? 0.f : M;
-                    f0 = exp2_approx((m - b) * scale2);
-                    f1 = exp2_approx((o.x - b) * scale2);
+                    f0 = power_of_2<BASED>((m - b) * scale2);
+                    f1 = power_of_2<BASED>((o.x - b) * scale2);
                     // a sum that is not a number stays one
-                    l = (l == 0.f ? 0.f : l * (m == -INFINITY ? 1.f : f0)) +
-                        (o.y == 0.f ? 0.f : o.y * (o.x == -INFINITY ? 1.f : f1));
+                    l = (l == 0.f ? 0.f : times<BASED>(l, m == -INFINITY ? 1.f : f0)) +
+                        (o.y == 0.f ? 0.f : times<BASED>(o.y, o.x == -INFINITY ? 1.f : f1));
                     m = M;
                 }
             }
+            auto both = [&](uint32_t x, uint32_t y) {  // both warpgroups' outputs
+                return times<BASED>(__uint_as_float(x), f0) + times<BASED>(__uint_as_float(y), f1);
+            };
             // (where the other warpgroup took it out of a tile of both, it said so before this one found it gone)
             const bool odd = !bar_and(1 + g, 128, *taken_out != (int)items + 1);
             const uint32_t toa = tmem + lanes + L::kTO + D * g0, tob = toa + D;
@@ -1306,7 +1319,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                             tmem_wait_ld();
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
-                                ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f0 + __uint_as_float(ow[x]) * f1);
+                                ov[x] = __float_as_uint(both(ov[x], ow[x]));
                         }
                         if (valid)
 #pragma unroll
@@ -1350,7 +1363,7 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                             tmem_wait_ld();
 #pragma unroll
                             for (int y = 0; y < 32; ++y)
-                                ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
+                                ov[y] = __float_as_uint(both(ov[y], ow[y]));
                         }
 #pragma unroll
                         for (int y = 0; y < 32; ++y) acc[y] = __uint_as_float(ov[y]) + 0.f;  // (-0 becomes 0)
@@ -1397,15 +1410,15 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                             }
                             const float b = M == -INFINITY ? 0.f : M;
                             if (i0 != c0) {
-                                const float f = exp2_approx(before == -INFINITY ? 0.f : before - b);
-                                S *= f;
+                                const float f = power_of_2<BASED>(before == -INFINITY ? 0.f : before - b);
+                                S = times<BASED>(S, f);
 #pragma unroll
-                                for (int y = 0; y < 16; ++y) acc[y] *= f;
+                                for (int y = 0; y < 16; ++y) acc[y] = times<BASED>(acc[y], f);
                             }
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {  // no seen key: zeros
-                                fs[u] = mi[u].y == 0.f ? 0.f : exp2_approx(mi[u].x == -INFINITY ? 0.f : mi[u].x - b);
-                                if (mi[u].y != 0.f) S = fmaf(fabsf(mi[u].y), fs[u], S);
+                                fs[u] = mi[u].y == 0.f ? 0.f : power_of_2<BASED>(mi[u].x == -INFINITY ? 0.f : mi[u].x - b);
+                                if (mi[u].y != 0.f) S = add_times<BASED>(fabsf(mi[u].y), fs[u], S);
                             }
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
@@ -1419,17 +1432,17 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                                         tmem_wait_ld();
 #pragma unroll
                                         for (int y = 0; y < 16; ++y)
-                                            ov[y] = __float_as_uint(__uint_as_float(ov[y]) * f0 + __uint_as_float(ow[y]) * f1);
+                                            ov[y] = __float_as_uint(both(ov[y], ow[y]));
                                     }
 #pragma unroll
-                                    for (int y = 0; y < 16; ++y) acc[y] = fmaf(__uint_as_float(ov[y]), fs[u], acc[y]);
+                                    for (int y = 0; y < 16; ++y) acc[y] = add_times<BASED>(__uint_as_float(ov[y]), fs[u], acc[y]);
                                 } else {
 #pragma unroll
                                     for (int y = 0; y < 4; ++y) {
-                                        acc[4 * y] = fmaf(v[u][y].x, fs[u], acc[4 * y]);
-                                        acc[4 * y + 1] = fmaf(v[u][y].y, fs[u], acc[4 * y + 1]);
-                                        acc[4 * y + 2] = fmaf(v[u][y].z, fs[u], acc[4 * y + 2]);
-                                        acc[4 * y + 3] = fmaf(v[u][y].w, fs[u], acc[4 * y + 3]);
+                                        acc[4 * y] = add_times<BASED>(v[u][y].x, fs[u], acc[4 * y]);
+                                        acc[4 * y + 1] = add_times<BASED>(v[u][y].y, fs[u], acc[4 * y + 1]);
+                                        acc[4 * y + 2] = add_times<BASED>(v[u][y].z, fs[u], acc[4 * y + 2]);
+                                        acc[4 * y + 3] = add_times<BASED>(v[u][y].w, fs[u], acc[4 * y + 3]);
                                     }
                                 }
                             }
