@@ -418,16 +418,19 @@ W4A16_DEVICE void add_taken_out(const PagedAttnParams& p, const ChunkPiece& pc, 
 // Weights carry their values' scales.  In bf16 these have f32's range.  In fp16 (for
 // fp16 queries, whose outputs a weight of 8 bits would spoil) the base that scores
 // are taken against goes by the sum of the largest score and the logarithm of the
-// largest scale (a power of two, out of 2^-96 .. 2^100) that the row has seen: a
+// largest scale (a power of two, out of 2^-60 .. 2^100) that the row has seen: a
 // weight is at most 2^14, what the largest score and the largest scale would make
 // at least 2^5, and a weight is rounded by 2^-11 of itself or by 2^-25.  (Two bf16
 // parts did it before: the chunk above 408 us.)
+// The base lies 66 binades below the row's largest score to 94 above it, so that
+// the sum of the weights before their scales is 2^-94 at least and, with the lag of
+// 2^8 of a maximum, 2^74 a position at most; scales below 2^-60 make outputs of 0.
 // As the scales run, a base may move by more than the 126 binades that an f32 factor
-// has, with a sum of weights (before their scales) that lies in range on both sides of
-// the move: such factors are taken as their square root, twice.
+// has, with a sum that lies in range on both sides of the move: such factors are
+// taken as their square root, twice.
 constexpr float kChShift = 6.f;  // of the base: weights are up to 2^(8 + 6)
 W4A16_DEVICE float scale_log(float largest) {  // an exponent that the scale is not above
-    return fminf(fmaxf((float)((int)(__float_as_uint(largest) >> 23) - 126), -96.f), 100.f);
+    return fminf(fmaxf((float)((int)(__float_as_uint(largest) >> 23) - 126), -60.f), 100.f);
 }
 // 2^x as a factor, and products with it; TWICE: kept as its root
 template <bool TWICE>

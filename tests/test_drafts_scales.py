@@ -1,11 +1,13 @@
 """Attention over an 8-bit cache in fp16 with more than 16 query rows a key head: its weights are taken against a base that
 the values' scales are part of, and neither the softmax's sum nor the outputs may depend on how these scales run."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from test_drafts import Draft
-from test_serving import f64
+from test_serving import f64, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,19 @@ def test_a_later_scale_leaves_the_sum_of_earlier_positions(w, code, small, large
     ref, rl, spread, _ = a.reference()
     assert np.all(np.abs(f64(lse) - rl) <= 1e-4 + 1e-6 * np.abs(rl))
     assert np.all(np.abs(f64(out) - ref) <= (2.0 ** -11 + 2e-4) * spread + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25)
+
+
+def test_the_sum_of_a_long_context_of_zero_scales_stays_finite(w):
+    """160 requests over the same 2^20 positions, every value's scale 0: the first 128 scores are 5.4 below the others, which is
+    less than what moves a row's base.  (A tile's sum is added to the row's with one rounding of 2^-24.)"""
+    L, n, d, page = 1 << 20, 17, 64, 256
+    kc = torch.ones(L // page, 1, page, d, dtype=torch.int8, device="cuda")
+    kc[0, :, :128] = -1
+    ks = torch.full((L // page, 1, page), 2.7 * 8 / 64, device="cuda")   # scores of 2.7 and -2.7
+    q = torch.ones(160 * n, 1, d, dtype=torch.float16, device="cuda")
+    table = torch.arange(L // page, dtype=torch.int32, device="cuda").repeat(160, 1)
+    lse = torch.zeros(160 * n, 1, device="cuda")
+    out = w.w4a16_paged_attention(q, kc, torch.ones_like(kc), table, i32(np.arange(161) * n), i32([L] * 160), n, block=True,
+                                  lse=lse, k_scale=ks, v_scale=torch.zeros_like(ks))
+    want = 2.7 + math.log(L - 128 + 128 * math.exp(-5.4))
+    assert (out == 0).all() and (lse - want).abs().max() <= 1e-4 + 1e-6 * want + L / 128 * 2.0 ** -24
