@@ -53,3 +53,47 @@ def test_the_sum_of_a_long_context_of_zero_scales_stays_finite(w):
                                   lse=lse, k_scale=ks, v_scale=torch.zeros_like(ks))
     want = 2.7 + math.log(L - 128 + 128 * math.exp(-5.4))
     assert (out == 0).all() and (lse - want).abs().max() <= 1e-4 + 1e-6 * want + L / 128 * 2.0 ** -24
+
+
+# Slots that no token sees, and scales that are no numbers, in fp16: the rows' base must not take them up.
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("fill", [3e38, float("nan"), float("-inf")])
+@pytest.mark.parametrize("lens,window,tree", [([(40, 150), (3, 60)], 0, None), ([(500, 130)], 64, None), ([(700, 30)], 0, None),
+                                              ([(90, 70)], 20, "tree"), ([(500, 70)], 300, "tree"), ([(99, 1), (300, 4)], 40, None)])
+def test_scales_of_unseen_slots_have_no_part(w, fill, lens, window, tree, code):
+    """Rows of 256 positions and more have weights of one part: bound as in test_fp16_weights_of_long_rows, with the largest
+    scale that any row may see."""
+    a = Draft(lens, 8, 2, 128, 16, "fp16", code, tree, seed=22)
+    used = torch.zeros(a.ks.shape[0], 16, dtype=torch.bool)
+    for b, L in enumerate(a.L):
+        for j in range(int(L)):
+            used[a.table[b, j // 16], j % 16] = True
+    free = ~used[:, None].expand(-1, 2, -1).cuda()
+    most = float(a.vs[~free].max()) * (127 if code == "int8" else 480)
+    for c, s in ((a.kc, a.ks), (a.vc, a.vs)):
+        c.view(torch.uint8)[free] = 0xff
+        s[free] = fill
+    out, lse = a.run(w, window)
+    a.vs[free] = a.ks[free] = 0   # (the oracle does not look at them)
+    ref, rl, spread, _ = a.reference(window)
+    bound = (2.0 ** -11 + 2e-4) * spread + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + a.L.max() * 2.0 ** -30 * most
+    assert np.all(np.abs(f64(out) - ref) <= bound)
+    assert np.all(np.abs(f64(lse) - rl) <= 1e-4 + 1e-6 * np.abs(rl))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens,pos,window,tree", [([(30, 150)], 100, 0, None), ([(300, 140)], 290, 64, None), ([(700, 40)], 600, 0, None),
+                                                  ([(200, 300)], 255, 0, None), ([(100, 60)], 120, 0, "tree"), ([(300, 60)], 320, 0, "tree"),
+                                                  ([(300, 60)], 20, 0, "tree")])
+def test_a_bad_scale_of_a_value_leaves_other_rows_alone(w, bad, lens, pos, window, tree, code):
+    a = Draft(lens, 8, 2, 128, 16, "fp16", code, tree, seed=23)
+    most = float(a.vs.max()) * (127 if code == "int8" else 480)
+    a.vs[int(a.table[0, pos // 16]), 1, pos % 16] = bad
+    out, lse = a.run(w, window)
+    ref, rl, spread, _ = a.reference(window)
+    got, hit = f64(out), np.isnan(ref)
+    assert hit.any() and np.array_equal(np.isnan(got), hit)
+    bound = (2.0 ** -11 + 2e-4) * spread + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + a.L.max() * 2.0 ** -30 * most
+    assert np.all((np.abs(got - ref) <= bound)[~hit])
+    assert np.all(np.abs(f64(lse) - rl) <= 1e-4 + 1e-6 * np.abs(rl))
