@@ -581,7 +581,8 @@ int w4a16_rope(const w4a16_rope_args *args, w4a16_stream_t stream);
  *     LINEAR      f_i / factor
  *     BASE        f_i of the base base * factor^(r / (r - 2)), whose last pair is LINEAR's
  *     RAMP        f_i for pairs of more than `high` turns in `length` positions, f_i / factor for those of less
- *                 than `low` turns, between them blended linearly in i; magnitude 0.1 ln(factor) + 1
+ *                 than `low` turns, between them blended linearly in i, from the whole pair before the first
+ *                 place (0 at least) to the one behind the second (r - 1 at most); magnitude 0.1 ln(factor) + 1
  *     WAVELENGTH  the same ends, between them blended linearly in the number of turns; magnitude 1
  *
  * W4A16_EINVAL for a null pointer, rotary_dim not even or below 2, a base or a

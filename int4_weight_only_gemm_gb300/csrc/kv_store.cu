@@ -313,18 +313,18 @@ void rope_frequencies(int r, double base, int scaling, double factor, double len
                       float* magnitude) {
     const double two_pi = 6.283185307179586476925;
     const double b = scaling == W4A16_ROPE_BASE && r > 2 ? base * std::pow(factor, (double)r / (r - 2)) : base;
-    // the pair (not a whole number) that turns `turns` times in `length` positions
+    // the pair (not a whole number, and it may lie outside the head's) that turns `turns` times in `length` positions
     auto pair_of = [&](double turns) { return r * std::log(length / (turns * two_pi)) / (2 * std::log(base)); };
     double lo = 0, hi = 0;
     if (scaling == W4A16_ROPE_RAMP) {
         lo = std::fmax(std::floor(pair_of(high)), 0.0);
-        hi = std::fmin(std::ceil(pair_of(low)), r / 2 - 1.0);
+        hi = std::fmin(std::ceil(pair_of(low)), r - 1.0);  // (behind the last pair where that turns more than `low` times)
     }
     *magnitude = scaling == W4A16_ROPE_RAMP ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
     for (int i = 0; i < r / 2; ++i) {
         f[i] = std::pow(b, -2.0 * i / r);
         double stretched = scaling == W4A16_ROPE_LINEAR ? 1.0 : 0.0;
-        if (scaling == W4A16_ROPE_RAMP) stretched = (i - lo) / std::fmax(hi - lo, 0.001);
+        if (scaling == W4A16_ROPE_RAMP) stretched = i >= hi ? 1.0 : (i - lo) / std::fmax(hi - lo, 1.0);
         if (scaling == W4A16_ROPE_WAVELENGTH) stretched = (high - length * f[i] / two_pi) / (high - low);
         stretched = std::fmin(std::fmax(stretched, 0.0), 1.0);
         f[i] = f[i] * (1.0 - stretched) + f[i] / factor * stretched;

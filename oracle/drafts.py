@@ -52,8 +52,9 @@ def frequencies(r, base=10000.0, scaling="none", factor=1.0, length=0.0, low=1.0
         return np.array([wide ** (-2.0 * i / r) for i in range(r // 2)]), 1.0
     if scaling == "ramp":
         pair = lambda turns: r * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base))
-        first, last = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), r // 2 - 1)
-        share = [min(max((i - first) / max(last - first, 0.001), 0.0), 1.0) for i in range(r // 2)]
+        # the line's ends are whole pairs, the last of which may lie behind the head's (there are r // 2)
+        first, last = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), r - 1)
+        share = [1.0 if i >= last else max((i - first) / max(last - first, 1), 0.0) for i in range(r // 2)]
         return np.array([f * (1 - s) + f / factor * s for f, s in zip(plain, share)]), 0.1 * math.log(factor) + 1.0
     out = []
     for f in plain:
