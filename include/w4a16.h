@@ -586,8 +586,8 @@ int w4a16_rope(const w4a16_rope_args *args, w4a16_stream_t stream);
  *     WAVELENGTH  the same ends, between them blended linearly in the number of turns; magnitude 1
  *
  * W4A16_EINVAL for a null pointer, rotary_dim not even or below 2, a base or a
- * factor that is not above 0, and, for the last two, a length not above 0 or not
- * low < high.
+ * factor that is not above 0, for the last two a length not above 0 or not
+ * 0 < low < high, and for RAMP a base not above 1.
  */
 enum { W4A16_ROPE_NONE = 0, W4A16_ROPE_LINEAR = 1, W4A16_ROPE_BASE = 2, W4A16_ROPE_RAMP = 3, W4A16_ROPE_WAVELENGTH = 4 };
 int w4a16_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double length, double low,

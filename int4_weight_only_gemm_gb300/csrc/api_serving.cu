@@ -181,6 +181,7 @@ int w4a16_rope_frequencies(int rotary_dim, double base, int scaling, double fact
     if (!frequencies || !magnitude || rotary_dim < 2 || rotary_dim % 2 || scaling < W4A16_ROPE_NONE ||
         scaling > W4A16_ROPE_WAVELENGTH || !(base > 0 && base < most) || !(factor > 0 && factor < most))
         return W4A16_EINVAL;
+    if (scaling == W4A16_ROPE_RAMP && !(base > 1)) return W4A16_EINVAL;  // (pairs have to turn less one after the other)
     if (scaling >= W4A16_ROPE_RAMP && (!(length > 0 && length < most) || !(low > 0 && low < high && high < most)))
         return W4A16_EINVAL;
     rope_frequencies(rotary_dim, base, scaling, factor, length, low, high, frequencies, magnitude);

@@ -45,6 +45,17 @@ def test_pairs_are_kept_or_stretched_by_their_turns(scaling, r, base, factor, le
             assert 1 / (span + 2) - 1e-12 <= between[1] - between[0] <= 1 / span + 1e-12
 
 
+@pytest.mark.parametrize("base", [1.0, 0.5, 1e-4])
+def test_a_ramp_needs_pairs_that_turn_less_one_after_the_other(base):
+    """At a base of 1 or below pairs turn ever more, or all alike: no pair lies between `high` and `low` turns."""
+    with pytest.raises(w.W4A16Error) as e:
+        w.w4a16_rope_frequencies(64, base, "ramp", 8.0, 4096.0, device="cpu")
+    assert e.value.status == w.W4A16_EINVAL
+    f = both(64, base, "wavelength", 8.0, 4096.0, 1.0, 32.0)   # by a pair's own turns
+    plain = base ** (-2.0 * np.arange(32) / 64)
+    assert np.all(f <= plain * (1 + 1e-12)) and np.all(f >= plain / 8 * (1 - 1e-12))
+
+
 def test_a_line_that_ends_behind_the_last_pair():
     """128 columns, base 10000, 131072 positions: the last pair turns 2.4 times, pair 69 (there is none) once."""
     f = both(128, 10000.0, "ramp", 8.0, 131072.0, 1.0, 32.0)
