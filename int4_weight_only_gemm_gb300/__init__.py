@@ -420,10 +420,12 @@ def _int32(t, name, n=None):
     return t.data_ptr()
 
 
-def _block_table(t, requests):
-    """Columns and row stride of a block table."""
+def _block_table(t, requests, idx=None):
+    """Columns and row stride of a block table (on the device idx, where given)."""
     if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _I32 or t.dim() != 2:
         raise ValueError("block_table must be a 2-D int32 CUDA tensor")
+    if idx is not None and t.get_device() != idx:
+        raise ValueError(f"block_table must be a CUDA tensor on the current device, cuda:{idx}")
     rows, columns = t.shape
     row, column = t.stride()
     if rows != requests or (column != 1 and columns > 1 and requests > 0):
@@ -542,6 +544,13 @@ def _caches(k_cache, v_cache, dtype):
     if vshape != shape:
         raise ValueError(f"v_cache has shape {tuple(vshape)}, expected {tuple(shape)}")
     return shape, ks, vs
+
+
+def _here(t, name):
+    """The current device, where a call with the CUDA tensor t is launched."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return _current()
 
 
 def _at(t, name, dtype, dims, idx):
@@ -777,19 +786,15 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     Hkv, page_size] f32.  tree [T, words] int32: the new tokens of a request are
     the nodes of a tree, and bit k of row t says whether token t sees node k
     (itself and its ancestors) beside the positions before the new tokens."""
-    dtype = q.dtype
-    shape, (qt, qh, _) = _strided(q, "q", dtype, 3)
+    here, dtype = _here(q, "q"), q.dtype
+    shape, (qt, qh, _) = _at(q, "q", dtype, 3, here)
     T, Hq, d = shape
+    plain = k_scale is None and v_scale is None and tree is None
+    cdtype, code = (dtype, 0) if plain else _codes(k_cache, k_scale, v_scale, dtype)
+    cshape, (kcp, kch, kcs, _) = _at(k_cache, "k_cache", cdtype, 4, here)
+    vcp, vch, vcs, _ = _alike(v_cache, "v_cache", cdtype, cshape, here)
     ext = None
-    if k_scale is None and v_scale is None and tree is None:
-        cshape, (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, dtype)
-    else:
-        here = _current()
-        if q.get_device() != here:
-            raise ValueError(f"q must be a CUDA tensor on the current device, cuda:{here}")
-        cdtype, code = _codes(k_cache, k_scale, v_scale, dtype)
-        cshape, (kcp, kch, kcs, _) = _at(k_cache, "k_cache", cdtype, 4, here)
-        vcp, vch, vcs, _ = _alike(v_cache, "v_cache", cdtype, cshape, here)
+    if not plain:
         (ksp, kss), (vsp, vss), words, node = _NO_SCALE, _NO_SCALE, 0, 0
         if k_scale is not None:
             pages, Hkv, page, _ = cshape
@@ -806,27 +811,27 @@ def w4a16_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     if cd != d or dtype not in _DTYPES:
         raise ValueError(f"caches with heads of {cd} do not go with q with heads of {d} in {dtype}")
     B = kv_len.shape[0]
-    kv, start = _int32(kv_len, "kv_len", B), _int32(q_start, "q_start", B + 1)
-    columns, row = _block_table(block_table, B)
+    kv, start = _list(kv_len, "kv_len", _I32, B, here), _list(q_start, "q_start", _I32, B + 1, here)
+    columns, row = _block_table(block_table, B, here)
     if out is None:
         out = torch.empty((T, Hq, d), dtype=dtype, device=q.device)
-    oshape, (ot, oh, _) = _strided(out, "out", dtype, 3)
-    if oshape != shape:
-        raise ValueError(f"out has shape {tuple(oshape)}, expected {tuple(shape)}")
+    ot, oh, _ = _alike(out, "out", dtype, shape, here)
     if lse is not None:
-        _check(lse, "lse", torch.float32, (T, Hq))
-    lib, idx = load_library(), q.get_device()
-    st = _stream(stream, idx)
+        _alike(lse, "lse", _F32, (T, Hq), here)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    lib = load_library()
+    st = _stream(stream, here)
     if workspace is None:
-        key = ("paged_attention", Hq, Hkv, d, max_q, idx)
+        key = ("paged_attention", Hq, Hkv, d, max_q, here)
         need = _need_cache.get(key)
         if need is None:  # for as many tokens and requests as a call takes, which change from step to step
             need = _remember(key, lib.w4a16_paged_attention_workspace_bytes(0x7fffffff // max(Hq, 1), 16384, Hq, Hkv,
                                                                             d, max_q))
         if need:
-            workspace = _serving_workspace(need, idx, stream, st)
-    elif not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+            workspace = _serving_workspace(need, here, stream, st)
+    elif not isinstance(workspace, _Tensor) or workspace.get_device() != here or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on the current device, cuda:{here}")
     args = _ATTN_ARGS.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), start, kv,
                            out.data_ptr(), 0 if lse is None else lse.data_ptr(),
                            0 if workspace is None else workspace.data_ptr(),
