@@ -537,15 +537,6 @@ def w4a16_page_plan(past_len: torch.Tensor, new_len: torch.Tensor, free_pages: t
     return q_start, kv_len, positions, slot_map, pages_used
 
 
-def _caches(k_cache, v_cache, dtype):
-    """Shape of both caches, and their strides."""
-    shape, ks = _strided(k_cache, "k_cache", dtype, 4)
-    vshape, vs = _strided(v_cache, "v_cache", dtype, 4)
-    if vshape != shape:
-        raise ValueError(f"v_cache has shape {tuple(vshape)}, expected {tuple(shape)}")
-    return shape, ks, vs
-
-
 def _here(t, name):
     """The current device, where a call with the CUDA tensor t is launched."""
     if not isinstance(t, _Tensor) or not t.is_cuda:
@@ -668,19 +659,19 @@ def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_c
     if k_scale is not None or v_scale is not None or getattr(k_cache, "dtype", None) in _CODES:
         _kv_store(None, k, v, None, None, slot_map, k_cache, v_cache, None, k_scale, v_scale, False, 1.0, stream, flags)
         return
-    dtype = k.dtype
-    shape, (kt, kh, _) = _strided(k, "k", dtype, 3)
-    vshape, (vt, vh, _) = _strided(v, "v", dtype, 3)
-    if vshape != shape:
-        raise ValueError(f"v has shape {tuple(vshape)}, expected {tuple(shape)}")
+    here, dtype = _here(k, "k"), k.dtype
+    shape, (kt, kh, _) = _at(k, "k", dtype, 3, here)
+    vt, vh, _ = _alike(v, "v", dtype, shape, here)
     T, heads, d = shape
-    (pages, ch, page, cd), (kcp, kch, kcs, _), (vcp, vch, vcs, _) = _caches(k_cache, v_cache, dtype)
+    cshape, (kcp, kch, kcs, _) = _at(k_cache, "k_cache", dtype, 4, here)
+    vcp, vch, vcs, _ = _alike(v_cache, "v_cache", dtype, cshape, here)
+    pages, ch, page, cd = cshape
     if ch != heads or cd != d or dtype not in _DTYPES:
         raise ValueError(f"caches of {ch} heads of {cd} do not take k of {heads} heads of {d} in {dtype}")
-    args = _WRITE_ARGS.pack(k.data_ptr(), v.data_ptr(), _int32(slot_map, "slot_map", T), k_cache.data_ptr(),
+    args = _WRITE_ARGS.pack(k.data_ptr(), v.data_ptr(), _list(slot_map, "slot_map", _I32, T, here), k_cache.data_ptr(),
                             v_cache.data_ptr(), kt, kh, vt, vh, kcp, kch, kcs, vcp, vch, vcs, T, heads, d, pages, page,
                             _DTYPES[dtype], flags, 0)
-    _raise(load_library().w4a16_kv_write(args, _stream(stream, k.get_device())), "w4a16_kv_write")
+    _raise(load_library().w4a16_kv_write(args, _stream(stream, here)), "w4a16_kv_write")
 
 
 def w4a16_rope_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,

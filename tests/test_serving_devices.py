@@ -71,3 +71,33 @@ def test_attention_refuses_each_tensor_of_another_device(launched, kind):
     with pytest.raises(ValueError, match="CUDA"):   # or on the host
         call(tensors)
     assert len(launched) == 1
+
+
+def rows(kind):
+    bf, i32 = torch.bfloat16, torch.int32
+    code = torch.int8 if kind.endswith("int8") else bf
+    a = dict(k=torch.zeros(T, H, D, dtype=bf), v=torch.zeros(T, H, D, dtype=bf), slot_map=torch.zeros(T, dtype=i32),
+             k_cache=torch.zeros(PAGES, H, PAGE, D, dtype=code), v_cache=torch.zeros(PAGES, H, PAGE, D, dtype=code))
+    if kind.endswith("int8"):
+        a.update(k_scale=torch.zeros(PAGES, H, PAGE), v_scale=torch.zeros(PAGES, H, PAGE))
+    if kind.startswith("rope"):
+        a.update(q=torch.zeros(T, HQ, D, dtype=bf), q_out=torch.zeros(T, HQ, D, dtype=bf), positions=torch.zeros(T, dtype=i32),
+                 frequencies=torch.zeros(D // 2, dtype=torch.float64))
+    return a
+
+
+@pytest.mark.parametrize("kind", ["write", "write int8", "rope", "rope int8", "read", "read int8"])
+def test_cache_calls_refuse_each_tensor_of_another_device(launched, kind):
+    tensors = rows(kind)
+    function = {"write": w.w4a16_kv_write, "rope": w.w4a16_rope_kv_write, "read": w.w4a16_kv_read}[kind.split()[0]]
+    call = lambda a: function(**a, stream=0)  # noqa: E731
+    call({n: on(t) for n, t in tensors.items()})
+    assert len(launched) == 1
+    for name in tensors:
+        with pytest.raises(ValueError, match=name):
+            call({n: on(t, Other if n == name else Placed) for n, t in tensors.items()})
+    with pytest.raises(ValueError):
+        call({n: on(t, Other) for n, t in tensors.items()})
+    with pytest.raises(ValueError, match="CUDA"):
+        call(tensors)
+    assert len(launched) == 1
