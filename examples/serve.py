@@ -81,11 +81,16 @@ class Cache:
             n: torch.zeros(shape[:3], device="cuda") for n in ("k_scale", "v_scale")}
 
     def move(self, source, target):
-        """Keys and values from the slots `source` to the slots `target`."""
-        _, heads, _, d = self.pages[0].shape
+        """Keys and values from the slots `source` to the slots `target`, as they are: of an 8-bit cache two codes at a time,
+        as 16-bit numbers that are copied bit for bit, and the scales."""
+        pages = [c.view(torch.bfloat16) for c in self.pages]
+        _, heads, size, d = pages[0].shape
         k, v = torch.empty(2, source.numel(), heads, d, dtype=torch.bfloat16, device="cuda")
-        w.w4a16_kv_read(*self.pages, source, k, v, **self.scales)
-        w.w4a16_kv_write(k, v, target, *self.pages, **self.scales)
+        w.w4a16_kv_read(*pages, source, k, v)
+        w.w4a16_kv_write(k, v, target, *pages)
+        source, target = source.long(), target.long()
+        for s in self.scales.values():
+            s[target // size, :, target % size] = s[source // size, :, source % size]
 
 
 class Model:
@@ -183,8 +188,8 @@ class Server:
             while (child := next((i for i, (p, t) in enumerate(nodes) if p == path[-1] and t == best[s + path[-1]]), None)):
                 path.append(child)
             out.append([nodes[i][1] for i in path[1:]] + [best[s + path[-1]]])
-            source += [s + i for i in path]
-            target += range(s, s + len(path))
+            source += [s + i for at, i in enumerate(path) if i != at]   # (the others lie in place)
+            target += [s + at for at, i in enumerate(path) if i != at]
             # pages behind the path's last position go back
             up = lambda n: -(-n // self.cfg.page_size)
             held = up(self.past[r] + len(path))
@@ -192,7 +197,7 @@ class Server:
             self.table[r, held:] = -1
             self.past[r] += len(path)
         slots = plan[3]
-        if source != target:
+        if source:
             for cache in self.model.caches:
                 cache.move(slots[ints(source).long()], slots[ints(target).long()])
         return out
