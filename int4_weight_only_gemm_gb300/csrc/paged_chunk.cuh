@@ -1136,7 +1136,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
                 }
                 mx = fmaxf(mx, mo);
                 if constexpr (BASED) mx = fmaxf(m, mx + (scale_log(largest) - kChShift));
-                const bool grew = (mx - m) * scale2 > 8.f;  // also from -inf
+                // (rows behind the item's take what shared memory held for queries: they move no neighbour's maximum)
+                const bool grew = valid && (mx - m) * scale2 > 8.f;  // also from -inf
                 if (__any_sync(0xffffffffu, grew)) {
                     const float f = mx == -INFINITY ? 1.f : power_of_2<BASED>((m - mx) * scale2);
                     l = times<BASED>(l, f);
