@@ -506,11 +506,13 @@ size_t w4a16_paged_attention_workspace_bytes(int tokens, int requests, int q_hea
  * to its scores, that of a value to its softmax weights, which are rounded as
  * w4a16_paged_attention rounds them), so that neither keys nor values are
  * rounded.  In fp16 with more than 16 query rows a key head a weight is rounded, where
- * that is more, by 2^-31 of what the token's largest score and the largest of its
- * values' scales would make together, which shows where the token rests on values
- * whose scales are 2^20 below the largest; scales above 2^100 overflow there.  A scale that is not finite stands
- * for a key or a value of NaN; the e4m3 codes without a value (0x7f, 0xff) count
- * as +-480.  Strides of k_cache and v_cache count
+ * that is more, by 2^-30 of what the token's largest score and the largest of its
+ * values' scales would make together (a scale below 2^-60 counts as 2^-60), which
+ * shows where the token rests on values whose scales are 2^19 below the largest; lse
+ * has no part in that.  Weights times scales are summed in f32 before the division by
+ * the softmax's sum: scales of values above 2^100 may overflow.  A scale that is not
+ * finite stands for a key or a value of NaN; the e4m3 codes without a value (0x7f,
+ * 0xff) count as +-480.  Strides of k_cache and v_cache count
  * elements, multiples of 16; those of the scales are not negative (0: one scale
  * for all), and 4-byte alignment is all that they need.
  *

@@ -14,12 +14,16 @@
 // Bound: HBM, each row read and written once; what is left to it is the latency of a
 // round and, in 8 bits, issue slots (196 instructions a warp for two rows, 62 % of the
 // slots).  Queries alone have the loads of three rows on their way (one 73 us, two 61-65,
-// three 58.6, four 58.4), a store one (16301 tokens turned and to int8, 48 heads: 129 us,
-// two ahead 156; without turns, stored and read back, 49 and 52).
+// three 58.6, four 58.4), a store one (two ahead: a fifth more time with turns, 52 us for 49
+// without, stored and read back).
 // Measured: 16301 tokens of 40 heads of 128 in bf16 (334 MB), half of each head
 // turned: 58.6 us, 5.7 TB/s, the whole head in pairs 59.4; keys and values of 16301
 // tokens, 8 heads of 128, to e4m3 (101 MB), with the read-back of the cache
 // 49; 64 tokens of 32 + 8 heads, turned and to int8: 6.7 us alone, 9.7 us a call.
+// 16301 tokens of 32 + 8 heads and their values, turned and stored: 110 us to int8 (109 to
+// e4m3, 107 to 16 bits) for a floor of 54 (59), half the rate of either of its parts: the
+// query rows, two in three, take the one load ahead of the others and, in 8 bits, their
+// shuffles and products too.  (w4a16_rope over both and w4a16_kv_write: 96, in 16 bits 89.)
 #include <cmath>
 
 #include "codes.cuh"

@@ -52,11 +52,13 @@
 // multiplies its score in f32, a value's its weight, which is of the queries' type as
 // the codes are (in two parts for rows of fewer than 256 positions).  Bound: as above, with twice the instructions in a
 // softmax warp's turn, and with the unpacking of 32768 codes a key tile.  Measured:
-// the chunk above 276-283 us with int8 or e4m3, 299 in fp16; the 16 blocks 78 us.
+// the chunk above 276-283 us with int8 or e4m3, 291-300 in fp16; the 16 blocks 64-73
+// (a tile's codes are unpacked for 64 rows, half of what a tile has room for).
 //
 // For a tree of drafted tokens (TREE) a row sees the positions before the new tokens
 // and the nodes that its bits say; the words with a tile's nodes are read at once.
-// Measured: 16 trees of 64 nodes over 4080 positions 74.4 us (285 MB, 68 GFLOP); one of
+// Measured: 16 trees of 64 nodes over 4080 positions 74.9 us (285 MB, 68 GFLOP; 128
+// items on as many of the 152 CTAs, since a cut costs more than it brings by kChJoin); one of
 // 13 over 2303 positions 21.7 us, of which ~2.6 go to the cut of the line, 1.8 to the
 // first keys, 8 to the five tiles of the longest piece and 6 to the join.
 //
@@ -745,7 +747,8 @@ __global__ void __launch_bounds__(kChThreads<Q8>, 1)
     const bool single = n_items <= gridDim.x && (int64_t)(most - kChJoin) * gridDim.x <= U;
     int C = single ? (int)n_items : (int)(U < gridDim.x ? U : gridDim.x);
     // A piece more costs the joining CTA about two fifths of a tile's time, so that few items are not cut below
-    // sqrt(2 / 5 tiles) tiles a piece: 13 nodes over 2303 positions, 8 items of 19 tiles, 36 us in 152 pieces.
+    // sqrt(2 / 5 tiles) tiles a piece: 13 nodes over 2303 positions, 8 items of 19 tiles, 36 us in 152 pieces.  (kChJoin
+    // was fitted to an earlier and slower join, and so was the causal form over 16 bits, which has no such least share.)
     if ((TREE || Q8) && !single) {
         int least = 1;
         while (5 * least * least < 2 * most) ++least;
